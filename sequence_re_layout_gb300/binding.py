@@ -1,4 +1,5 @@
-"""ctypes binding of ``libbasp.so`` (declared in ``include/basp.h``).
+"""ctypes binding of ``libbasp.so`` (declared in ``include/basp.h`` and
+``include/basp_fp8.h``).
 
 Argument marshalling only: every function here takes Python ints or torch
 tensors, turns them into the C-ABI's pointers and sizes, calls the library and
@@ -36,6 +37,13 @@ EXPORTS = ("basp_layout_create", "basp_layout_create_ex", "basp_layout_query",
            "basp_seq2head_qkv", "basp_head2seq_qkv", "basp_seq2head_host",
            "basp_head2seq_host", "basp_seq2head_noalloc", "basp_status_string")
 
+# every symbol include/basp_fp8.h declares
+FP8_EXPORTS = ("basp_rmsnorm", "basp_rmsnorm_backward", "basp_rmsnorm_backward_workspace",
+               "basp_quantize_fp8", "basp_matmul_fp8", "basp_matmul_fp8_timeouts")
+
+# values that share a scale along a row of an 8-bit matrix
+BASP_FP8_BLOCK = 128
+
 # size of the library's built-in scratch for basp_seq2head_noalloc
 BASP_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -55,6 +63,11 @@ class basp_info(ctypes.Structure):
 class basp_layout_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("B", "S", "Hq", "Hkv", "d", "N", "K")] + \
         [("dtype", ctypes.c_int), ("order", ctypes.c_int)]
+
+
+class basp_fp8_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int64) for n in ("rows", "cols", "pitch", "scale_pitch", "block_rows")]
 
 
 class BaspError(RuntimeError):
@@ -101,6 +114,21 @@ def load_library():
     lib.basp_head2seq_qkv.restype = ctypes.c_int
     lib.basp_seq2head_noalloc.argtypes = [vp] + [vp] * 6 + [vp]
     lib.basp_seq2head_noalloc.restype = ctypes.c_int
+    ci, mp = ctypes.c_int, ctypes.POINTER(basp_fp8_matrix)
+    lib.basp_rmsnorm.argtypes = [ci, i64, i64, vp, i64, vp, i64, vp, ci, ctypes.c_float,
+                                 vp, i64, vp, i64, mp, vp, vp]
+    lib.basp_rmsnorm.restype = ci
+    lib.basp_rmsnorm_backward.argtypes = [ci, i64, i64, vp, i64, vp, i64, vp, vp, ci, vp, i64,
+                                          vp, i64, vp, vp, sz, vp]
+    lib.basp_rmsnorm_backward.restype = ci
+    lib.basp_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    lib.basp_rmsnorm_backward_workspace.restype = i64
+    lib.basp_quantize_fp8.argtypes = [ci, i64, i64, vp, i64, mp, mp, vp]
+    lib.basp_quantize_fp8.restype = ci
+    lib.basp_matmul_fp8.argtypes = [mp, mp, vp, ci, ci, vp, i64, vp]
+    lib.basp_matmul_fp8.restype = ci
+    lib.basp_matmul_fp8_timeouts.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
+    lib.basp_matmul_fp8_timeouts.restype = ci
     if hasattr(lib, "basp_debug_bounds_violations"):
         lib.basp_debug_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
         lib.basp_debug_bounds_violations.restype = ctypes.c_int
@@ -336,6 +364,128 @@ def basp_seq2head_noalloc(layout, q, k, v, q_out, k_out, v_out, stream=None):
     a = _triple(layout, w, ("q", "k", "v"), (q, k, v), "device")
     b = _triple(layout, w, ("q_out", "k_out", "v_out"), (q_out, k_out, v_out), "device")
     _check(load_library().basp_seq2head_noalloc(layout, *a, *b, _stream(stream)), w)
+
+
+# ---- the 8-bit projections (include/basp_fp8.h) ----------------------------
+
+_FP8_DTYPES = {}
+
+
+def fp8_dtype_code(dtype) -> int:
+    """basp_dtype of a torch element type that the 8-bit operators take or
+    give (bfloat16, float16, float32)."""
+    if not _FP8_DTYPES:
+        import torch
+        _FP8_DTYPES.update({torch.bfloat16: BASP_DTYPE_BF16, torch.float16: BASP_DTYPE_FP16,
+                            torch.float32: BASP_DTYPE_FP32})
+    try:
+        return _FP8_DTYPES[dtype]
+    except KeyError:
+        raise ValueError("element type must be bfloat16, float16 or float32, got %s" % (dtype,)) from None
+
+
+def _rows(x, where, name, rows, cols, dtype, cur):
+    """(address, row stride) of a [rows, cols] CUDA matrix with unit column
+    stride and the given element type; (None, 0) for None."""
+    if x is None:
+        return None, 0
+    if not x.is_cuda or x.device.index != cur:
+        raise ValueError("%s: %s must be on the current device cuda:%d, it is on %s"
+                         % (where, name, cur, x.device))
+    if x.dtype != dtype:
+        raise ValueError("%s: %s must be %s, got %s" % (where, name, dtype, x.dtype))
+    if tuple(x.shape) != (rows, cols):
+        raise ValueError("%s: %s must have shape %s, got %s"
+                         % (where, name, (rows, cols), tuple(x.shape)))
+    s0, s1 = x.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("%s: the columns of %s must be next to each other" % (where, name))
+    return x.data_ptr() or None, s0 if rows > 1 else cols
+
+
+def _vector(x, where, name, n, dtype, cur):
+    """Address of a contiguous CUDA vector of n elements, or None."""
+    if x is None:
+        return None
+    if not x.is_cuda or x.device.index != cur:
+        raise ValueError("%s: %s must be on the current device cuda:%d, it is on %s"
+                         % (where, name, cur, x.device))
+    if x.dtype != dtype:
+        raise ValueError("%s: %s must be %s, got %s" % (where, name, dtype, x.dtype))
+    if x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
+        raise ValueError("%s: %s must be a contiguous vector of %d" % (where, name, n))
+    return x.data_ptr() or None
+
+
+def _2d(x, where, name):
+    if x.dim() != 2:
+        raise ValueError("%s: %s must have two dimensions, got shape %s" % (where, name, tuple(x.shape)))
+    return x.shape
+
+
+def basp_rmsnorm(x, residual, weight, eps, h=None, y=None, q=None, rstd=None, stream=None):
+    """Residual addition + root-mean-square norm; see ``basp_fp8.h``.  ``q`` is
+    a :class:`basp_fp8_matrix`, everything else a tensor or None."""
+    import torch
+    w = "basp_rmsnorm"
+    rows, cols = _2d(x, w, "x")
+    code, cur = fp8_dtype_code(x.dtype), _current_device()
+    wcode = fp8_dtype_code(weight.dtype)
+    _check(load_library().basp_rmsnorm(
+        code, rows, cols, *_rows(x, w, "x", rows, cols, x.dtype, cur),
+        *_rows(residual, w, "residual", rows, cols, x.dtype, cur),
+        _vector(weight, w, "weight", cols, weight.dtype, cur), wcode, eps,
+        *_rows(h, w, "h", rows, cols, x.dtype, cur), *_rows(y, w, "y", rows, cols, x.dtype, cur),
+        q, _vector(rstd, w, "rstd", rows, torch.float32, cur), _stream(stream)), w)
+
+
+def basp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
+    return load_library().basp_rmsnorm_backward_workspace(rows, cols)
+
+
+def basp_rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight=None, workspace=None, stream=None):
+    """Gradient of :func:`basp_rmsnorm`; see ``basp_fp8.h``."""
+    import torch
+    w = "basp_rmsnorm_backward"
+    rows, cols = _2d(dy, w, "dy")
+    code, cur = fp8_dtype_code(dy.dtype), _current_device()
+    wcode = fp8_dtype_code(weight.dtype)
+    _check(load_library().basp_rmsnorm_backward(
+        code, rows, cols, *_rows(dy, w, "dy", rows, cols, dy.dtype, cur),
+        *_rows(h, w, "h", rows, cols, dy.dtype, cur), _vector(rstd, w, "rstd", rows, torch.float32, cur),
+        _vector(weight, w, "weight", cols, weight.dtype, cur), wcode,
+        *_rows(dh, w, "dh", rows, cols, dy.dtype, cur), *_rows(dx, w, "dx", rows, cols, dy.dtype, cur),
+        _vector(dweight, w, "dweight", cols, torch.float32, cur),
+        _tptr(workspace, None, w, "workspace", "device", cur), _nbytes(workspace), _stream(stream)), w)
+
+
+def basp_quantize_fp8(x, q=None, qt=None, stream=None):
+    """A matrix, and its transpose, to 8 bits; see ``basp_fp8.h``.  ``q`` and
+    ``qt`` are :class:`basp_fp8_matrix` or None."""
+    w = "basp_quantize_fp8"
+    rows, cols = _2d(x, w, "x")
+    _check(load_library().basp_quantize_fp8(
+        fp8_dtype_code(x.dtype), rows, cols, *_rows(x, w, "x", rows, cols, x.dtype, _current_device()),
+        q, qt, _stream(stream)), w)
+
+
+def basp_matmul_fp8(a, b, bias, c, accumulate=False, stream=None):
+    """C = A B^T (+ bias) (+ C); see ``basp_fp8.h``.  ``a`` and ``b`` are
+    :class:`basp_fp8_matrix`."""
+    w = "basp_matmul_fp8"
+    cur = _current_device()
+    cp, cs = _rows(c, w, "c", a.rows, b.rows, c.dtype, cur)
+    _check(load_library().basp_matmul_fp8(
+        a, b, _vector(bias, w, "bias", b.rows, c.dtype, cur), int(accumulate), fp8_dtype_code(c.dtype),
+        cp, cs, _stream(stream)), w)
+
+
+def basp_matmul_fp8_timeouts() -> int:
+    """Read and clear the count of waits that ran out in the product's kernel
+    on the current device (synchronises it)."""
+    n = ctypes.c_ulonglong()
+    _check(load_library().basp_matmul_fp8_timeouts(ctypes.byref(n)), "basp_matmul_fp8_timeouts")
+    return n.value
 
 
 class Layout:

@@ -11,10 +11,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libbasp.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "libbasp_debug.so")
-SOURCES = ["layout.cpp", "relayout.cu"]
-HEADERS = [os.path.join(INCLUDE, "basp.h"), os.path.join(INCLUDE, "basp_debug.h"),
-           os.path.join(CSRC, "layout_internal.h"), os.path.join(CSRC, "relayout_kernel.cuh"),
-           os.path.join(CSRC, "scratch_cache.h")]
+SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "quantize.cu", "matmul.cu"]
+HEADERS = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h")] + \
+    [os.path.join(CSRC, h) for h in ("layout_internal.h", "relayout_kernel.cuh", "scratch_cache.h",
+                                     "fp8_common.cuh", "tcgen05.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -22,6 +22,7 @@ NVCC_FLAGS = [
     "-lineinfo",
     "-Xcompiler", "-fPIC",
     "-shared",
+    "--threads", "8",       # the sources side by side
 ]
 
 

@@ -1,0 +1,526 @@
+// matmul.cu -- C = A B^T of two e4m3 matrices with a power-of-two scale for
+// each 128 values along K (basp_matmul_fp8).
+//
+//     C[m][n] = sum over k of 2^(ea[m][k/128] + eb[n][k/128]) * A[m][k] * B[n][k]
+//
+// The tensor cores of sm_103a take such scales as they are (tcgen05.mma,
+// kind::mxf8f6f4: one e8m0 byte for each row and 32 values of K, read from
+// tensor memory), so a block of 128 is four instructions that name the same
+// byte, and the scales cost no arithmetic.  Their 32-bit words hold four
+// bytes: the scales of 512 values of K, loaded once for four blocks.
+//
+// Orientation.  The instruction's 128-row side is B (a weight's output
+// features) and its N side, 16 to 256 wide, is A (the tokens).  The
+// accumulator then has n along tensor-memory lanes and m along columns, so
+// for each m a warp's 32 lanes store 32 neighbouring elements of C's row:
+// coalesced whatever the row stride, the bias is one value a thread, and one
+// token costs a 16-wide instruction instead of a padded 128-row one.
+//
+// A CTA is eight warps: one issues TMA loads (128 bytes of K a stage, in the
+// 128-byte swizzle), one issues the products, one brings scales, four drain
+// accumulators.  Large products run a persistent CTA per SM whose accumulator
+// is double-buffered, so a tile's stores overlap the next tile's products.
+// With few tiles, a cluster of CTAs splits K; the parts meet in shared memory
+// and are added in rank order, so results do not depend on timing.
+//
+// Waits.  Every wait on an mbarrier has a time limit.  When one runs out the
+// CTA's roles leave their loops, wait (with the limit again) for copies and
+// products in flight, write NaN where results would have gone, and count it.
+#include <atomic>
+
+#include "fp8_common.cuh"
+#include "tcgen05.cuh"
+
+namespace basp_fp8 {
+namespace {
+
+__device__ unsigned long long g_timeouts;
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+constexpr int kTileP = 128;              // rows of B a tile: the instruction's M
+constexpr int kStageK = kBlock;          // K of a stage, one scale
+constexpr int kScaleSlots = 2;
+
+__host__ __device__ constexpr int stage_bytes(int BN) { return (kTileP + BN) * kStageK; }
+// scales of 128 rows x 4 blocks are 512 bytes; B's 128 rows, then A's BN
+__host__ __device__ constexpr int scale_bytes(int BN) { return 512 + (BN > 128 ? 1024 : 512); }
+__host__ __device__ constexpr int scale_columns(int BN) { return scale_bytes(BN) / 128; }
+
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kBarrierBytes = 512;
+__host__ __device__ constexpr int stages(int BN) {
+    const int n = (kSmemLimit - 1024 - kBarrierBytes - kScaleSlots * scale_bytes(BN)) / stage_bytes(BN);
+    return n < 8 ? n : 8;
+}
+__host__ __device__ constexpr int smem_bytes(int BN) {
+    return 1024 + stages(BN) * stage_bytes(BN) + kScaleSlots * scale_bytes(BN) + kBarrierBytes;
+}
+
+// Tensor-memory columns: two accumulators and two scale slots.  Two of 256
+// columns leave no room for the scales in 512, so there the accumulators
+// overlap by 32 columns, which the drain reads first.
+constexpr int kOverlap = 32;
+__host__ __device__ constexpr int acc_offset(int BN) { return BN == 256 ? BN - kOverlap : BN; }
+__host__ __device__ constexpr int scale_base(int BN) { return acc_offset(BN) + BN; }
+__host__ __device__ constexpr int tmem_columns(int BN) {
+    const int need = scale_base(BN) + kScaleSlots * scale_columns(BN);
+    return need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
+static_assert(scale_base(256) + kScaleSlots * scale_columns(256) <= 512, "tensor memory");
+
+struct MatmulArgs {
+    const uint8_t *sp, *sq;              // scales of B (P side) and A (Q side)
+    int64_t sp_pitch, sq_pitch;
+    int sp_shift, sq_shift;              // row -> scale row: 0 or 7
+    void *c;
+    const void *bias;
+    int64_t c_stride;
+    int M, N, nk;                        // nk: blocks of 128 along K
+    int tiles_m, tiles_n, tiles;
+    int split;                           // CTAs of a cluster that share a tile
+    int accumulate;
+};
+
+// Tiles of one group of 16 tile rows of B run side by side over all of A, so
+// what the CTAs in flight read of B stays in L2.
+constexpr int kGroupN = 16;
+__device__ __forceinline__ void tile_at(const MatmulArgs &a, int t, int *tm, int *tn) {
+    const int per_group = kGroupN * a.tiles_m;
+    const int g = t / per_group, r = t % per_group;
+    const int width = min(kGroupN, a.tiles_n - g * kGroupN);
+    *tn = g * kGroupN + r % width;
+    *tm = r / width;
+}
+
+struct Waiter {
+    volatile int *abort;                 // shared by the CTA
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, bool give_up_early = true) const {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(bar, parity)) {
+            if (give_up_early && *abort) return false;
+            if (global_ns() - t0 > kWaitLimitNs) {
+                if (!*abort) atomicAdd(&g_timeouts, 1ull);
+                *abort = 1;
+                return false;
+            }
+        }
+        return true;
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void put(const MatmulArgs &a, T *c, float v) {
+    if (a.accumulate) v += Elem<T>::to_float(*c);
+    *c = Elem<T>::from_float(v);
+}
+
+template <int BN, class T>
+__global__ void __launch_bounds__(256, 1)
+matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_p,
+              const __grid_constant__ CUtensorMap map_q) {
+    constexpr int ST = stages(BN);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    uint8_t *scale_smem = smem + ST * stage_bytes(BN);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scale_smem + kScaleSlots * scale_bytes(BN));
+    const uint32_t stage0 = smem_addr(smem), scale0 = smem_addr(scale_smem), bar0 = smem_addr(bars);
+    const uint32_t full = bar0, empty = full + 8 * ST, sfull = empty + 8 * ST, sempty = sfull + 8 * kScaleSlots;
+    const uint32_t acc_full = sempty + 8 * kScaleSlots, acc_free = acc_full + 16, drained = acc_free + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * ST + 2 * kScaleSlots + 4);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert(8 * (2 * ST + 2 * kScaleSlots + 4) + 8 <= kBarrierBytes, "barrier space");
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = a.split > 1 ? int(blockIdx.x) % a.split : 0;
+    const int first = int(blockIdx.x) / a.split, step = int(gridDim.x) / a.split;
+    const int kb0 = int(int64_t(a.nk) * rank / a.split), kb1 = int(int64_t(a.nk) * (rank + 1) / a.split);
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&map_p);
+        tma_prefetch_map(&map_q);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(sfull + 8 * s, 1);
+            mbar_init(sempty + 8 * s, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_full + 8, 1);
+        mbar_init(acc_free, 4);
+        mbar_init(drained, 1);
+        *abort = 0;
+        fence_mbar_init();
+        fence_async_shared();
+    }
+    if (warp == 3) tmem_alloc(smem_addr(tmem_slot), tmem_columns(BN));
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+    const Waiter wait{abort};
+
+    if (warp == 0) {
+        if (lane == 0) {                                  // loads
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; t < a.tiles && ok; t += step) {
+                int tm, tn;
+                tile_at(a, t, &tm, &tn);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % ST, use = it / ST;
+                    ok = wait(empty + 8 * s, (use & 1) ^ 1);
+                    if (!ok) break;
+                    mbar_expect_tx(full + 8 * s, stage_bytes(BN));
+                    tma_load_2d(stage0 + s * stage_bytes(BN), &map_p, kb * kStageK, tn * kTileP, full + 8 * s);
+                    tma_load_2d(stage0 + s * stage_bytes(BN) + kTileP * kStageK, &map_q, kb * kStageK, tm * BN,
+                                full + 8 * s);
+                }
+            }
+            if (!ok)                                      // copies in flight end before the CTA does
+                for (uint32_t j = it < uint32_t(ST) ? 0 : it - ST; j < it; ++j)
+                    wait(full + 8 * (j % ST), (j / ST) & 1, false);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {                                  // products
+            uint32_t it = 0, group = 0, count = 0;
+            bool ok = true;
+            for (int t = first; t < a.tiles && ok; t += step, ++count) {
+                const uint32_t acc = tmem + (count & 1) * acc_offset(BN);
+                if (count > 0) ok = wait(acc_free, (count - 1) & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                uint32_t slot = 0;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    if (kb == kb0 || kb % 4 == 0) {       // scales of the next four blocks
+                        slot = group % kScaleSlots;
+                        ok = wait(sfull + 8 * slot, (group / kScaleSlots) & 1);
+                        if (!ok) break;
+                        tcgen05_after_sync();
+                        const uint32_t src = scale0 + slot * scale_bytes(BN);
+                        const uint32_t dst = tmem + scale_base(BN) + slot * scale_columns(BN);
+#pragma unroll
+                        for (int i = 0; i < scale_bytes(BN) / 512; ++i)
+                            tmem_copy_scales(dst + 4 * i, scale_desc(src + 512 * i));
+                        ++group;
+                    }
+                    const uint32_t s = it % ST;
+                    ok = wait(full + 8 * s, (it / ST) & 1);
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    const uint64_t dp = operand_desc(stage0 + s * stage_bytes(BN));
+                    const uint64_t dq = operand_desc(stage0 + s * stage_bytes(BN) + kTileP * kStageK);
+                    const uint32_t sf = tmem + scale_base(BN) + slot * scale_columns(BN);
+                    const uint32_t idesc = mma_desc(kTileP, BN) | mma_scale_ids(kb & 3);
+#pragma unroll
+                    for (int k = 0; k < kStageK / 32; ++k)
+                        mma_mxf8(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, kb > kb0 || k > 0);
+                    mma_commit(empty + 8 * s);
+                    if (kb + 1 == kb1 || kb % 4 == 3) mma_commit(sempty + 8 * slot);
+                }
+                if (ok) mma_commit(acc_full + 8 * (count & 1));
+            }
+            if (!ok) {                                    // products in flight end before the CTA does
+                mma_commit(drained);
+                wait(drained, 0, false);
+            }
+        }
+    } else if (warp == 2) {                               // scales
+        uint32_t group = 0;
+        bool ok = true;
+        for (int t = first; t < a.tiles && ok; t += step) {
+            int tm, tn;
+            tile_at(a, t, &tm, &tn);
+            for (int g = kb0 / 4; 4 * g < kb1; ++g, ++group) {
+                uint4 w[scale_bytes(BN) / 512];
+#pragma unroll
+                for (int i = 0; i < scale_bytes(BN) / 512; ++i) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int in_tile = (i > 0 ? (i - 1) * 128 : 0) + 32 * j + lane;
+                        const int64_t row = i == 0 ? int64_t(tn) * kTileP + in_tile : int64_t(tm) * BN + in_tile;
+                        r[j] = 0x7f7f7f7fu;               // rows that do not exist: values are 0
+                        if (i == 0) {
+                            if (row < a.N)
+                                r[j] = __ldg(reinterpret_cast<const uint32_t *>(
+                                    a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g)));
+                        } else if (in_tile < BN && row < a.M) {
+                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
+                                a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g)));
+                        }
+                    }
+                    w[i] = make_uint4(r[0], r[1], r[2], r[3]);
+                }
+                const uint32_t slot = group % kScaleSlots;
+                ok = wait(sempty + 8 * slot, ((group / kScaleSlots) & 1) ^ 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < scale_bytes(BN) / 512; ++i)
+                    reinterpret_cast<uint4 *>(scale_smem + slot * scale_bytes(BN) + 512 * i)[lane] = w[i];
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull + 8 * slot);
+            }
+        }
+    } else if (warp >= 4) {                               // drain
+        const int quarter = warp % 4, row = quarter * 32 + lane;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        uint32_t count = 0;
+        bool ok = true;
+        for (int t = first; t < a.tiles; t += step, ++count) {
+            int tm, tn;
+            tile_at(a, t, &tm, &tn);
+            const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
+            const bool mine = n < a.N;
+            const float bias = mine && a.bias != nullptr && a.split == 1
+                                   ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
+            T *c = static_cast<T *>(a.c) + m0 * a.c_stride + n;
+            float *part = reinterpret_cast<float *>(smem);     // [BN][128], split only
+            const bool arrived = ok && wait(acc_full + 8 * (count & 1), (count >> 1) & 1);
+            ok = __all_sync(0xffffffffu, arrived);
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + lanes + (count & 1) * acc_offset(BN);
+            if (BN < 256 && ok) {
+                // no columns shared: what this warp read of the other accumulator is behind it
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_free);
+            }
+            for (int i = 0; i < BN / 16; ++i) {
+                // the first accumulator shares its last columns, the second its first
+                const int j0 = 16 * (BN == 256 && (count & 1) == 0 ? BN / 16 - 1 - i : i);
+                uint32_t v[16];
+                if (ok) {
+                    tmem_load16(acc + j0, v);
+                    tmem_load_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+                }
+                if (BN == 256 && i == kOverlap / 16 - 1 && ok) {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_free);
+                }
+                if (a.split > 1) {
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
+                } else if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (m0 + j0 + j < a.M) put<T>(a, c + (j0 + j) * a.c_stride, __uint_as_float(v[j]) + bias);
+                }
+            }
+        }
+    }
+
+    if (a.split > 1) {                                    // one tile: join the cluster's parts
+        __syncthreads();
+        if (*abort)                                       // nothing is in flight any more
+            for (int i = threadIdx.x; i < BN * kTileP; i += blockDim.x)
+                reinterpret_cast<uint32_t *>(smem)[i] = 0x7fffffffu;
+        __syncwarp();
+        cluster_sync();
+        int tm, tn;
+        tile_at(a, first, &tm, &tn);
+        const int row = threadIdx.x % kTileP, half = threadIdx.x / kTileP;
+        const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
+        if (n < a.N) {
+            const float bias = a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
+            const int j1 = min(BN * (rank + 1) / a.split, int(min(int64_t(BN), a.M - m0)));
+            for (int j = BN * rank / a.split + half; j < j1; j += 2) {
+                float v = 0.f;
+                for (int r = 0; r < a.split; ++r)
+                    v += cluster_load(cluster_addr(stage0 + uint32_t(j * kTileP + row) * 4, r));
+                put<T>(a, static_cast<T *>(a.c) + (m0 + j) * a.c_stride + n, v + bias);
+            }
+        }
+        cluster_sync();                                   // the others may still read this CTA's part
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 3) tmem_free(tmem, tmem_columns(BN));
+}
+
+// C = bias, zero, or itself where there is nothing to sum over.
+template <class T>
+__global__ void bias_kernel(const __grid_constant__ MatmulArgs a) {
+    grid_dependency();
+    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= int64_t(a.M) * a.N) return;
+    const int64_t m = i / a.N, n = i % a.N;
+    put<T>(a, static_cast<T *>(a.c) + m * a.c_stride + n,
+           a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f);
+}
+
+// ---- host ---------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) !=
+                cudaSuccess || qr != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return EncodeFn(nullptr);
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Boxes of 128 bytes of K x `box_rows`; past the matrix' end they read zero.
+bool encode(const basp_fp8_matrix *m, int box_rows, CUtensorMap *out) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(m->cols), cuuint64_t(m->rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(m->pitch)};
+    const cuuint32_t box[2] = {kStageK, cuuint32_t(box_rows)};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m->data, dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Shape {
+    int bn, split;
+};
+
+// The tile width (along A's rows) and the number of CTAs that split K with
+// the least estimated time, in SM cycles: rounds of CTAs over the SMs, each
+// paying for its stages (tensor cores or loads, whichever takes longer) and
+// for a start and a drain that no stage hides.
+Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
+    Shape best = {256, 1};
+    double best_cost = 1e300;
+    for (int bn = 16; bn <= 256; bn *= 2) {
+        if (bn > 16 && bn / 2 >= M) break;
+        const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP);
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (split > nk || tiles * split > sms)) break;
+            const double stage = std::max(2.0 * bn, stage_bytes(bn) / 64.0);
+            const double k = double(ceil_div(nk, split)) * stage;
+            const double drain = 6.0 * bn / split + (split > 1 ? 2000 : 0);
+            const double rounds = double(ceil_div(tiles * split, sms));
+            const double cost = 3000 + rounds * k + (rounds - 1) * 300 + drain;
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bn, split};
+            }
+        }
+    }
+    return best;
+}
+
+template <int BN, class T>
+basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q, int sms,
+                          cudaStream_t stream) {
+    CUtensorMap map_p, map_q;
+    if (!encode(p, kTileP, &map_p) || !encode(q, BN, &map_q)) return BASP_ERR_CUDA;
+    static std::atomic<bool> ready[64];   // per device; a benign race
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BASP_ERR_CUDA;
+    if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(matmul_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem_bytes(BN)) != cudaSuccess) {
+            cudaGetLastError();
+            return BASP_ERR_CUDA;
+        }
+        if (dev < 64) ready[dev].store(true, std::memory_order_release);
+    }
+    const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, sms);
+    return launch(matmul_kernel<BN, T>, dim3(unsigned(ctas)), dim3(256), smem_bytes(BN), a.split, stream, a,
+                  map_p, map_q);
+}
+
+template <class T>
+basp_status run(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q, cudaStream_t stream) {
+    if (a.nk == 0) {
+        if (a.accumulate && a.bias == nullptr) return BASP_OK;
+        const int64_t ctas = ceil_div(int64_t(a.M) * a.N, 256);
+        if (ctas > kMaxSide) return BASP_ERR_TOO_LARGE;
+        return launch(bias_kernel<T>, dim3(unsigned(ctas)), dim3(256), 0, 1, stream, a);
+    }
+    const int sms = sm_count();
+    const Shape s = pick_shape(a.M, a.N, a.nk, sms);
+    const int64_t tiles = ceil_div(a.M, s.bn) * ceil_div(a.N, kTileP);
+    if (tiles > (int64_t(1) << 30)) return BASP_ERR_TOO_LARGE;
+    a.tiles_m = int(ceil_div(a.M, s.bn));
+    a.tiles_n = int(ceil_div(a.N, kTileP));
+    a.tiles = int(tiles);
+    a.split = s.split;
+    switch (s.bn) {
+        case 16: return launch_matmul<16, T>(a, p, q, sms, stream);
+        case 32: return launch_matmul<32, T>(a, p, q, sms, stream);
+        case 64: return launch_matmul<64, T>(a, p, q, sms, stream);
+        case 128: return launch_matmul<128, T>(a, p, q, sms, stream);
+        default: return launch_matmul<256, T>(a, p, q, sms, stream);
+    }
+}
+
+}  // namespace
+}  // namespace basp_fp8
+
+using namespace basp_fp8;
+
+extern "C" basp_status basp_matmul_fp8(const basp_fp8_matrix *a, const basp_fp8_matrix *b, const void *bias,
+                                       int accumulate, basp_dtype dtype, void *c, int64_t c_stride,
+                                       cudaStream_t stream) {
+    NvtxRange range("basp_matmul_fp8");
+    const int64_t esz = elem_size(dtype);
+    if (esz == 0 || a == nullptr || b == nullptr || a->cols != b->cols) return BASP_ERR_INVALID_ARG;
+    basp_status st = BASP_OK;
+    if (!sides_ok(a->rows, a->cols, &st) || !sides_ok(b->rows, b->cols, &st)) return st;
+    Args args;
+    args.fp8(a, a->rows, a->cols, false);
+    args.fp8(b, b->rows, b->cols, false);
+    args.matrix(bias, 1, b->rows, b->rows, esz, false, false);
+    args.matrix(c, a->rows, b->rows, c_stride, esz, true);
+    st = args.status();
+    if (st != BASP_OK || a->rows == 0 || b->rows == 0) return st;
+
+    MatmulArgs m = {};
+    m.sp = static_cast<const uint8_t *>(b->scales);
+    m.sq = static_cast<const uint8_t *>(a->scales);
+    m.sp_pitch = b->scale_pitch;
+    m.sq_pitch = a->scale_pitch;
+    m.sp_shift = b->block_rows == 1 ? 0 : 7;
+    m.sq_shift = a->block_rows == 1 ? 0 : 7;
+    m.c = c;
+    m.bias = bias;
+    m.c_stride = c_stride;
+    m.M = int(a->rows);
+    m.N = int(b->rows);
+    m.nk = int(ceil_div(a->cols, kBlock));
+    m.accumulate = accumulate != 0;
+    switch (dtype) {
+        case BASP_DTYPE_BF16: return run<__nv_bfloat16>(m, b, a, stream);
+        case BASP_DTYPE_FP16: return run<__half>(m, b, a, stream);
+        default: return run<float>(m, b, a, stream);
+    }
+}
+
+extern "C" basp_status basp_matmul_fp8_timeouts(unsigned long long *count) {
+    if (count == nullptr) return BASP_ERR_INVALID_ARG;
+    const unsigned long long zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpyFromSymbol(count, g_timeouts, sizeof(*count)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_timeouts, &zero, sizeof(zero)) != cudaSuccess) {
+        cudaGetLastError();
+        return BASP_ERR_CUDA;
+    }
+    return BASP_OK;
+}

@@ -1,0 +1,342 @@
+"""The 8-bit operators on the GPU against their plain 64-bit forms
+(tests/fp8_reference.py).
+
+Tolerances.  u(t) = finfo(t).eps / 2 is one rounding to t.  Everything before
+the last rounding is in 32 bits: a row's sum of n squares is off by at most
+n * 2^-24 of itself, its root by half of that, so a normed value by
+(n / 2 + 8) * 2^-24 of itself before it is rounded.  An e4m3 value is off by
+half a step: 2^-4 of a normal value, 2^-10 of the scale below.  A product's sum
+over K has at most one rounding or truncation, 2^-23, for each 32 terms and
+each part of a split, of at most the sum of magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_reference as ref
+import sequence_re_layout_gb300 as basp
+from sequence_re_layout_gb300 import fp8
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+F32 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sequence_re_layout_gb300.build import build_library
+    build_library()
+
+
+def u(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().float().double().numpy() if t.dtype != torch.float64 else t.cpu().numpy()
+
+
+def values_and_exps(q):
+    """A Quantized as the plain form has it."""
+    return f64(q.data), q.scales.cpu().view(torch.uint8).numpy().astype(np.int64) - 127
+
+
+def random(rows, cols, dtype, seed, spread=2.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(spread * torch.randn(1, cols, generator=g))
+    return x.to(dtype).cuda()
+
+
+def strided(x, pad):
+    """The same matrix with `pad` more elements in each row of its storage."""
+    big = torch.full((x.shape[0], x.shape[1] + pad), float("nan"), dtype=x.dtype, device=x.device)
+    big[:, :x.shape[1]] = x
+    return big[:, :x.shape[1]]
+
+
+SHAPES = [(1, 1), (1, 64), (1, 2048), (3, 127), (2, 128), (5, 129), (33, 260), (700, 256), (401, 1000), (9, 4099),
+          (2, 16385), (400, 2048), (310, 5120)]
+
+
+# ---- quantisation -------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 300), (2, 128), (127, 129), (128, 128), (130, 257), (300, 1000),
+                                       (1, 4096), (517, 36)])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize(rows, cols, dtype, block_rows):
+    """Bit for bit: the input is exact and a power-of-two scale rounds nothing."""
+    x = random(rows, cols, DTYPES[dtype], rows * cols)
+    q, qt = fp8.quantize(x, block_rows=block_rows, transposed=True)
+    for got, want in ((q, f64(x)), (qt, f64(x).T)):
+        v, e = values_and_exps(got)
+        rv, re = ref.quantize(want, block_rows)
+        assert np.array_equal(e, re)
+        assert np.array_equal(v, rv)
+    alone, alone_t = fp8.quantize(x, block_rows=block_rows), fp8.quantize(x, block_rows=block_rows, rows=False,
+                                                                          transposed=True)
+    for a, b in ((alone, q), (alone_t, qt)):
+        assert torch.equal(a.data.view(torch.uint8), b.data.view(torch.uint8))
+        assert torch.equal(a.scales.view(torch.uint8), b.scales.view(torch.uint8))
+
+
+@pytest.mark.parametrize("pad", [1, 4, 8])
+def test_quantize_strided_input(pad):
+    x = random(140, 200, torch.bfloat16, 7)
+    want, got = fp8.quantize(x, transposed=True), fp8.quantize(strided(x, pad), transposed=True)
+    for a, b in zip(want, got):
+        assert torch.equal(a.data.view(torch.uint8), b.data.view(torch.uint8))
+        assert torch.equal(a.scales.view(torch.uint8), b.scales.view(torch.uint8))
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_extreme_values(block_rows):
+    """Zeros, the type's largest and smallest magnitudes, infinities and NaN."""
+    x = torch.zeros(130, 384)
+    x[0, :128] = torch.finfo(torch.float32).max
+    x[1, :128] = -torch.finfo(torch.float32).tiny
+    x[2, :128] = 1e-45
+    x[129, 5] = float("inf")
+    x[129, 6] = float("-inf")
+    x[129, 130] = float("nan")
+    x[129, 131] = 3.0
+    x[4, 256:] = torch.arange(128) * 0.25
+    q, qt = fp8.quantize(x.cuda(), block_rows=block_rows, transposed=True)
+    for got, want in ((q, f64(x)), (qt, f64(x).T)):
+        v, e = values_and_exps(got)
+        rv, re = ref.quantize(want, block_rows)
+        assert np.array_equal(e, re)
+        assert np.array_equal(v, rv, equal_nan=True)
+
+
+def test_quantize_writes_nothing_past_its_rows():
+    x = random(130, 200, torch.bfloat16, 9)
+    stores = [torch.full((r, c), 0x55, dtype=torch.uint8, device="cuda")
+              for r, c in ((130, 224), (130, 8), (200, 160), (200, 8))]
+    q, s, qt, st = stores
+    mats = [fp8.Quantized(d.view(torch.float8_e4m3fn)[:, :c], z.view(torch.float8_e8m0fnu)[:, :2])
+            for d, z, c in ((q, s, 200), (qt, st, 130))]
+    basp.basp_quantize_fp8(x, mats[0]._c, mats[1]._c, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for store, cols in zip(stores, (200, 2, 130, 2)):
+        assert bool((store[:, cols:] == 0x55).all())
+    assert np.array_equal(values_and_exps(mats[1])[0], ref.quantize(f64(x).T, 1)[0])
+
+
+# ---- norm -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm(rows, cols, dtype, residual):
+    t = DTYPES[dtype]
+    x, r = random(rows, cols, t, 1, 1.0), random(rows, cols, t, 2, 1.0) if residual else None
+    w = random(1, cols, torch.float32 if rows % 2 else t, 3, 0.5)[0]
+    q, h, rstd = fp8.rmsnorm(x, w, residual=r, eps=1e-5)
+    y, h2, rstd2 = fp8.rmsnorm(x, w, residual=r, eps=1e-5, quantized=False)
+    assert torch.equal(rstd, rstd2) and torch.equal(h, h2)
+    want_h = x if r is None else (x.double() + r.double()).float().to(t)     # the sum, rounded to 32 bits and to t
+    assert torch.equal(h, want_h)
+    ry, rr = ref.norm(f64(h), f64(w), 1e-5)
+    slack = (cols / 2 + 8) * F32
+    assert (np.abs(f64(rstd) - rr) <= slack * rr).all()
+    assert (np.abs(f64(y) - ry) <= (u(t) + slack) * np.abs(ry) + 2.0 ** -25).all()
+    v, e = values_and_exps(q)
+    rv, re = ref.quantize(ry, 1)
+    scale = ref.dequantize(np.ones_like(v), e, 1)
+    assert (np.abs(e - re) <= 1).all() and (e != re).mean() < 0.01           # next to a border, either will do
+    assert (np.abs(v * scale - ry) <= np.maximum(np.abs(ry) * (2.0 ** -4 + slack), scale * 2.0 ** -10) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("cols", [200, 201, 2048])
+def test_rmsnorm_in_place_and_strided(cols):
+    x, r = random(70, cols, torch.bfloat16, 1), random(70, cols, torch.bfloat16, 2)
+    w = random(1, cols, torch.bfloat16, 3)[0]
+    want, want_h, _ = fp8.rmsnorm(x, w, residual=r)
+    for pad in (0, 4, 3):
+        xs, rs = strided(x, pad), strided(r, pad)
+        got, h, _ = fp8.rmsnorm(xs, w, residual=rs, h=rs)
+        assert h is rs and torch.equal(rs, want_h)
+        assert torch.equal(got.data.view(torch.uint8), want.data.view(torch.uint8))
+    xs = x.clone()
+    assert torch.equal(fp8.rmsnorm(xs, w, residual=r, h=xs)[1], want_h) and torch.equal(xs, want_h)
+
+
+def test_rmsnorm_leading_dimensions():
+    x = random(6, 256, torch.bfloat16, 1).view(2, 3, 256)
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    y, h, rstd = fp8.rmsnorm(x, w, quantized=False)
+    assert y.shape == x.shape and h is x and rstd.shape == (6,)
+
+
+def test_rmsnorm_rows_of_zeros_infinities_and_nan():
+    x = torch.zeros(4, 256)
+    x[1, 3], x[2, 200], x[3] = float("inf"), float("nan"), 1.0
+    y, _, rstd = fp8.rmsnorm(x.cuda(), torch.ones(256, device="cuda"), eps=1e-6, quantized=True)
+    d = y.dequantize().cpu()
+    assert bool((d[0] == 0).all())
+    assert torch.isnan(d[1, 3]) and bool((d[1, :3] == 0).all())         # inf * 0 and 0 * 0
+    assert bool(torch.isnan(d[2]).all()) and bool((d[3] == 1).all())
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES + [(1300, 384), (3, 8193)])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("more", [False, True])
+def test_rmsnorm_backward(rows, cols, dtype, more):
+    t = DTYPES[dtype]
+    h, dy = random(rows, cols, t, 1, 1.0), random(rows, cols, t, 2, 0.5)
+    w = random(1, cols, torch.float32 if rows % 2 else t, 3, 0.5)[0]
+    dh = random(rows, cols, t, 4, 0.5) if more else None
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+    dx, dw = fp8.rmsnorm_backward(dy, h, rstd, w, dh=dh)
+    rx, rw = ref.norm_backward(f64(dy), f64(h), f64(rstd), f64(w), None if dh is None else f64(dh))
+    # dx is a sum of three terms, one of them with a mean over the row
+    g, n = np.abs(f64(dy) * f64(w)), np.abs(f64(h) * f64(rstd)[:, None])
+    size = f64(rstd)[:, None] * (g + n * (g * n).mean(1, keepdims=True)) + (0 if dh is None else np.abs(f64(dh)))
+    assert (np.abs(f64(dx) - rx) <= u(t) * np.abs(rx) + (cols + 8) * F32 * size + 2.0 ** -25).all()
+    assert (np.abs(f64(dw) - rw) <= (rows + 8) * F32 * (np.abs(f64(dy)) * n).sum(0) + 1e-30).all()
+    again = fp8.rmsnorm_backward(dy, h, rstd, w, dh=dh)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    alone, none = fp8.rmsnorm_backward(dy, h, rstd, w, dh=dh, need_dweight=False)
+    assert none is None and torch.equal(alone, dx)
+
+
+def test_rmsnorm_backward_of_no_rows():
+    e = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    dx, dw = fp8.rmsnorm_backward(e, e, torch.empty(0, device="cuda"), torch.ones(256, device="cuda"))
+    assert dx.shape == (0, 256) and bool((dw == 0).all())
+
+
+# ---- product ----------------------------------------------------------------------
+
+def quantized(rows, cols, block_rows, seed):
+    """An 8-bit matrix with exponents of its own, and its 64-bit values."""
+    g = torch.Generator().manual_seed(seed)
+    data = (torch.randn(rows, cols, generator=g) * 40).clamp(-448, 448).to(torch.float8_e4m3fn)
+    srows, blocks = -(-rows // block_rows), -(-cols // 128)
+    exps = torch.randint(-9, 10, (srows, blocks), generator=g)
+    q = fp8.Quantized.empty(rows, cols, block_rows)
+    q.data.view(torch.uint8).copy_(data.view(torch.uint8))
+    q.scales.view(torch.uint8).copy_((exps + 127).to(torch.uint8))
+    return q, ref.dequantize(data.double().numpy(), exps.numpy(), block_rows)
+
+
+def check_product(c, a64, b64, K, bias=None, base=None):
+    want, size = a64 @ b64.T, np.abs(a64) @ np.abs(b64).T
+    for extra in (bias, base):
+        if extra is not None:
+            want, size = want + extra, size + np.abs(extra)
+    tol = u(c.dtype) * np.abs(want) + (-(-K // 32) + 16) * 2.0 ** -23 * size
+    assert (np.abs(f64(c) - want) <= tol + 2.0 ** -25).all(), np.abs((f64(c) - want) / size).max()
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 128, 128), (1, 128, 32), (1, 1, 1), (1, 130, 513), (16, 128, 512), (17, 256, 640), (31, 300, 1000),
+    (33, 128, 128), (64, 512, 2048), (65, 129, 127), (127, 257, 129), (128, 128, 4096), (129, 640, 384),
+    (255, 1000, 260), (257, 999, 1543), (1000, 77, 128), (2048, 2048, 256), (4099, 1100, 300)])
+@pytest.mark.parametrize("out", sorted(DTYPES))
+def test_matmul(M, N, K, out):
+    a, a64 = quantized(M, K, 1, 1)
+    b, b64 = quantized(N, K, 128 if N % 2 else 1, 2)
+    scale = 1.0 if out != "fp16" else 2.0 ** -12               # fp16 ends at 65504
+    if out == "fp16":
+        a64 = a64 * scale
+        a.scales.view(torch.uint8).sub_(12)
+        b64 = b64 * 2.0 ** -8
+        b.scales.view(torch.uint8).sub_(8)
+    check_product(fp8.matmul(a, b, out_dtype=DTYPES[out]), a64, b64, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 700), (40, 129, 2000), (300, 140, 260)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_matmul_bias_accumulate_and_stride(M, N, K, out):
+    t = DTYPES[out]
+    a, a64 = quantized(M, K, 1, 1)
+    b, b64 = quantized(N, K, 128, 2)
+    bias, base = random(1, N, t, 5)[0] * 1000, random(M, N, t, 6) * 1000
+    store = torch.full((M, N + 3), 7.0, dtype=t, device="cuda")
+    c = store[:, :N]
+    c.copy_(base)
+    got = fp8.matmul(a, b, bias=bias, out=c, accumulate=True)
+    assert got is c and bool((store[:, N:] == 7).all())
+    check_product(c, a64, b64, K, f64(bias), f64(base))
+    check_product(fp8.matmul(a, b, bias=bias, out_dtype=t), a64, b64, K, f64(bias))
+
+
+def test_matmul_of_128_row_blocks_on_both_sides():
+    a, a64 = quantized(300, 400, 128, 1)
+    b, b64 = quantized(200, 400, 128, 2)
+    check_product(fp8.matmul(a, b, out_dtype=torch.float32), a64, b64, 400)
+
+
+def test_matmul_repeats_bit_for_bit():
+    a, _ = quantized(24, 4000, 1, 1)
+    b, _ = quantized(500, 4000, 1, 2)
+    first = fp8.matmul(a, b, out_dtype=torch.float32)
+    for _ in range(5):
+        assert torch.equal(fp8.matmul(a, b, out_dtype=torch.float32), first)
+
+
+def test_matmul_of_nothing():
+    a, b = fp8.Quantized.empty(5, 0), fp8.Quantized.empty(7, 0)
+    bias = torch.arange(7, dtype=torch.bfloat16, device="cuda")
+    assert bool((fp8.matmul(a, b) == 0).all())
+    assert torch.equal(fp8.matmul(a, b, bias=bias), bias.expand(5, 7))
+    c = torch.ones(5, 7, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(fp8.matmul(a, b, bias=bias, out=c, accumulate=True), bias.expand(5, 7) + 1)
+    assert fp8.matmul(fp8.Quantized.empty(0, 128), fp8.Quantized.empty(7, 128)).shape == (0, 7)
+
+
+def test_matmul_nan_stays_in_its_row_and_column():
+    a, a64 = quantized(40, 300, 1, 1)
+    b, b64 = quantized(140, 300, 1, 2)
+    a.data.view(torch.uint8)[3, 299] = 0x7F
+    b.data.view(torch.uint8)[131, 0] = 0xFF
+    c = fp8.matmul(a, b, out_dtype=torch.float32).cpu()
+    bad = torch.isnan(c)
+    assert bool(bad[3].all()) and bool(bad[:, 131].all()) and int(bad.sum()) == 140 + 40 - 1
+
+
+def test_matmul_scales_at_their_ends():
+    """Scale bytes 0 and 254 (2^-127 and 2^127) against each other."""
+    a, _ = quantized(20, 128, 1, 1)
+    b, _ = quantized(130, 128, 1, 2)
+    plain = fp8.matmul(a, b, out_dtype=torch.float32)
+    a.scales.view(torch.uint8).copy_(torch.full((20, 1), 0, dtype=torch.uint8))
+    b.scales.view(torch.uint8).copy_(torch.full((130, 1), 254, dtype=torch.uint8))
+    extreme = fp8.matmul(a, b, out_dtype=torch.float32)
+    a.scales.view(torch.uint8).fill_(127)
+    b.scales.view(torch.uint8).fill_(127)
+    assert torch.equal(extreme, fp8.matmul(a, b, out_dtype=torch.float32))
+    assert bool(torch.isfinite(plain).all())
+
+
+def test_other_stream_and_graph():
+    """The calls follow the current stream, and a captured chain replays."""
+    x, r = random(64, 2048, torch.bfloat16, 1), random(64, 2048, torch.bfloat16, 2)
+    w = torch.ones(2048, dtype=torch.bfloat16, device="cuda")
+    wq, _ = quantized(512, 2048, 128, 3)
+
+    def chain():
+        q, h, _ = fp8.rmsnorm(x, w, residual=r)
+        return h, fp8.matmul(q, wq)
+
+    want = chain()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = chain()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    x.copy_(random(64, 2048, torch.bfloat16, 9))
+    g.replay()
+    want = chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_zz_no_wait_ran_out():
+    assert basp.basp_matmul_fp8_timeouts() == 0
