@@ -33,14 +33,88 @@ template <> struct Elem<__half> {
 
 template <class T> struct alignas(4 * sizeof(T)) Vec4 { T v[4]; };
 
+// 16 bytes of a row as they lie in memory: eight 16-bit values or four of 32
+// bits.  max_abs is elementwise, and a NaN does not count; two 16-bit values
+// take one instruction.
+template <class T> struct Pack;
+template <> struct Pack<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 x, float (&v)[4]) {
+        v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+    }
+    static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
+        return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(x))));
+    }
+};
+template <> struct Pack<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 x, float (&v)[8]) {
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
+        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&m),
+                                         __habs2(*reinterpret_cast<__nv_bfloat162 *>(&x)));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    // the float bits of the low and the high value
+    static __device__ __forceinline__ uint32_t low(uint32_t x) { return x << 16; }
+    static __device__ __forceinline__ uint32_t high(uint32_t x) { return x & 0xffff0000u; }
+};
+template <> struct Pack<__half> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 x, float (&v)[8]) {
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
+        const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&m), __habs2(*reinterpret_cast<__half2 *>(&x)));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ uint32_t low(uint32_t x) {
+        return __float_as_uint(__half2float(__ushort_as_half(uint16_t(x))));
+    }
+    static __device__ __forceinline__ uint32_t high(uint32_t x) {
+        return __float_as_uint(__half2float(__ushort_as_half(uint16_t(x >> 16))));
+    }
+};
+
 // Four values of a 128-block for one lane.  VEC: columns 4*lane .. 4*lane+3 in
 // one access (the row is aligned to four elements).  Otherwise columns lane,
 // lane+32, lane+64, lane+96, so that a warp's accesses still fall next to
 // each other, whatever the row's alignment.
-template <bool VEC> __device__ __forceinline__ int lane_col(int lane, int j) {
-    return VEC ? 4 * lane + j : lane + 32 * j;
-}
-
 // `row` points to the block's first element; `left` columns of the block
 // exist.  Values past the end read as zero.
 template <class T, bool VEC>
@@ -59,6 +133,22 @@ __device__ __forceinline__ void load4(const T *row, int lane, int left, float (&
         for (int j = 0; j < 4; ++j)
             v[j] = lane + 32 * j < left ? Elem<T>::to_float(row[lane + 32 * j]) : 0.f;
     }
+}
+
+// ---- loads ahead of their use -----------------------------------------------
+
+// A thread copies the 16 bytes that it will read itself into shared memory
+// (cp.async: no register holds them on the way, and no barrier is needed to
+// read one's own copies).  `have` false: zeros, and nothing is read.
+__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src, bool have) {
+    const uint32_t to = uint32_t(__cvta_generic_to_shared(dst));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(have ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest N groups of this thread have arrived
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <class T, bool VEC>
@@ -81,11 +171,20 @@ __device__ __forceinline__ void store4(T *row, int lane, int left, const float (
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// The magnitude's bits where x is finite, else 0: magnitudes order as their
-// bits do, so a block's largest finite magnitude is an integer maximum.
+// The largest magnitude's bits, NaN aside: magnitudes order as their bits do,
+// so maxima of several lanes are integer maxima.  Infinities count; a block
+// where this says kInfBits takes the forms below that look at each value.
+__device__ __forceinline__ uint32_t max_bits4(const float (&v)[4]) {
+    return __float_as_uint(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+}
+
+// The magnitude's bits where x is finite, else 0.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     return b < kInfBits ? b : 0u;
+}
+__device__ __forceinline__ uint32_t max_finite_bits4(const float (&v)[4]) {
+    return max(max(finite_bits(v[0]), finite_bits(v[1])), max(finite_bits(v[2]), finite_bits(v[3])));
 }
 
 // The biased exponent e + 127 of the least scale 2^e with amax <= 448 * 2^e:
@@ -105,21 +204,41 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
     return __uint_as_float((254u - byte) << 23);
 }
 
-// Infinities become NaN, which e4m3 can hold; finite values pass.
-__device__ __forceinline__ float nan_if_infinite(float x) {
-    return (__float_as_uint(x) & 0x7fffffffu) == kInfBits ? __uint_as_float(0x7fffffffu) : x;
+// Four values times the inverse scale, rounded to nearest even: e4m3 bytes,
+// the first in the low byte.  NaN gives NaN; an infinity would saturate.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, float inv) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+    return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+__device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4], float inv) {
+    return to_e4m3x4(v[0], v[1], v[2], v[3], inv);
+}
+// the bytes of N = 4 or 8 values to memory
+template <int N> __device__ __forceinline__ void store_e4m3(uint8_t *out, const float (&v)[N], float inv) {
+    const uint32_t lo = to_e4m3x4(v[0], v[1], v[2], v[3], inv);
+    if constexpr (N == 8)
+        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, to_e4m3x4(v[4], v[5], v[6], v[7], inv));
+    else
+        *reinterpret_cast<uint32_t *>(out) = lo;
 }
 
-// Four values times the inverse scale, rounded to nearest even: e4m3 bytes,
-// the first in the low byte.
-__device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4], float inv) {
-    float s[4];
+// Infinities as NaN, which e4m3 can hold; other values as they are.
+template <int N> __device__ __forceinline__ void infinite_to_nan(float (&v)[N]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = nan_if_infinite(v[j]) * inv;
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(s[1]), "f"(s[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(s[3]), "f"(s[2]));
-    return uint32_t(lo) | (uint32_t(hi) << 16);
+    for (int j = 0; j < N; ++j)
+        if ((__float_as_uint(v[j]) & 0x7fffffffu) == kInfBits) v[j] = __uint_as_float(0x7fffffffu);
+}
+
+// The scale byte of a 1 x 128 block that a warp holds; infinities become NaN.
+__device__ __forceinline__ uint32_t row_scale(float (&v)[4]) {
+    uint32_t m = __reduce_max_sync(0xffffffffu, max_bits4(v));
+    if (m >= kInfBits) {
+        m = __reduce_max_sync(0xffffffffu, max_finite_bits4(v));
+        infinite_to_nan(v);
+    }
+    return scale_byte(m);
 }
 
 template <bool VEC>
@@ -131,10 +250,6 @@ __device__ __forceinline__ void store4_e4m3(uint8_t *row, int lane, int left, ui
         for (int j = 0; j < 4; ++j)
             if (lane + 32 * j < left) row[lane + 32 * j] = uint8_t(q >> (8 * j));
     }
-}
-
-__device__ __forceinline__ uint32_t max_bits4(const float (&v)[4]) {
-    return max(max(finite_bits(v[0]), finite_bits(v[1])), max(finite_bits(v[2]), finite_bits(v[3])));
 }
 
 // ---- launch ---------------------------------------------------------------
@@ -179,6 +294,20 @@ struct NvtxRange {
 
 // SMs of the current device (152 on GB300); 1 if it cannot be read.
 int sm_count();
+
+// CTAs of `kernel` that fit on the current device at once; also lets the
+// kernel have `smem` bytes of dynamic shared memory.
+template <class K>
+int64_t resident_ctas(K kernel, int threads, size_t smem) {
+    int per_sm = 0;
+    if ((smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  int(smem)) != cudaSuccess) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    return int64_t(sm_count()) * (per_sm > 0 ? per_sm : 1);
+}
 
 // ---- argument checks (host) -----------------------------------------------
 
@@ -272,7 +401,12 @@ inline bool sides_ok(int64_t rows, int64_t cols, basp_status *st) {
 }
 
 // Whether rows of `stride` elements of `esz` bytes at p (NULL counts) and
-// `cols` allow accesses of four elements.
+// `cols` allow accesses of 16 bytes.
+inline bool vec16_ok(const void *p, int64_t stride, int64_t cols, int64_t esz) {
+    return p == nullptr || (uintptr_t(p) % 16 == 0 && stride * esz % 16 == 0 && cols * esz % 16 == 0);
+}
+
+// Whether they allow accesses of four elements.
 inline bool vec4_ok(const void *p, int64_t stride, int64_t cols, int64_t esz) {
     return p == nullptr || (uintptr_t(p) % uintptr_t(4 * esz) == 0 && stride % 4 == 0 && cols % 4 == 0);
 }

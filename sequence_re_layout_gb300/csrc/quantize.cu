@@ -3,14 +3,15 @@
 // (basp_quantize_fp8).
 //
 // Each value is read once whatever is asked for: the bound is memory (3 bytes
-// a value for a 16-bit matrix, 4 with the transpose).  Rows alone need no
-// tile: a warp owns 128-blocks, four values a lane.  The transpose and
-// 128 x 128 scales work on a 128 x 128 tile a CTA: warp w holds rows 16w to
-// 16w+15 in registers (64 values a lane), so a row's maximum is one warp
-// reduction, a column's maximum is a maximum over the lane's own 16 values
-// joined across the eight warps in shared memory, and the 16 values that a
-// lane holds of a column are 16 consecutive bytes of the transpose, which go
-// through shared memory to leave as 128-byte rows.
+// a value for a 16-bit matrix, 4 with the transpose), if the instructions stay
+// few.  Rows alone need no tile: a warp owns 128-blocks, four values a lane.
+// The transpose and 128 x 128 scales work on 128 x 128 tiles: a lane holds a
+// few columns of a few rows, so that row maxima join lanes of one warp, column
+// maxima join warps in shared memory, and four rows of a column are four
+// consecutive bytes of the transpose, which go through shared memory to leave
+// as 128-byte rows.
+#include <algorithm>
+
 #include "fp8_common.cuh"
 
 namespace basp_fp8 {
@@ -50,7 +51,7 @@ quantize_rows_kernel(const __grid_constant__ QuantArgs a, int groups) {
     for (int i = 0; i < kRowBlocks; ++i) {
         const int64_t c = int64_t(b0 + i) * kBlock;
         if (c >= a.cols) break;
-        const uint32_t sb = scale_byte(__reduce_max_sync(0xffffffffu, max_bits4(v[i])));
+        const uint32_t sb = row_scale(v[i]);
         store4_e4m3<VEC>(a.q + row * a.qs + c, lane, int(a.cols - c), to_e4m3x4(v[i], inverse_scale(sb)));
         if (lane == 0) a.scales[row * a.ss + b0 + i] = uint8_t(sb);
     }
@@ -58,18 +59,225 @@ quantize_rows_kernel(const __grid_constant__ QuantArgs a, int groups) {
 
 // ---- tiles ----------------------------------------------------------------
 
-constexpr int kTileWarps = 8;
+constexpr int kTileWarps = 16;
+constexpr int kTileThreads = kTileWarps * 32;
 constexpr int kTileRows = kBlock / kTileWarps;      // rows a warp
+constexpr int kTileAhead = 1;                       // tiles whose loads are on their way
 
-// Where 16-byte piece `w` of transposed row n sits in its 128 bytes of shared
-// memory: eight neighbouring lanes, whose n differ by 1 or by 4, hit eight
-// different pieces, so the 16-byte stores and loads are free of conflicts.
-__device__ __forceinline__ int piece(int n, int w) { return w ^ ((n ^ (n >> 2)) & 7); }
+// Where 4-byte piece p (of 32) of transposed row n sits in its 128 bytes of
+// shared memory: neighbouring lanes, whose n differ by 1, 4 or 8, store to the
+// eight 16-byte groups in turn, and a group's four pieces stay together for
+// the loads.
+__device__ __forceinline__ int piece(int n, int p) { return p ^ ((((n >> 3) ^ n) & 7) << 2); }
 
+// The transpose's tile from shared memory: 16 bytes a thread, eight threads a
+// row.
+__device__ __forceinline__ void store_transposed(const QuantArgs &a, const uint8_t *t, int64_t m0, int64_t n0,
+                                                 int left_m, int left_n) {
+#pragma unroll
+    for (int k = 0; k < kBlock * kBlock / (16 * kTileThreads); ++k) {
+        const int n = k * (kTileThreads / 8) + int(threadIdx.x) / 8, w = threadIdx.x % 8;
+        if (n >= left_n || 16 * w >= left_m) continue;
+        const uint4 p = *reinterpret_cast<const uint4 *>(t + n * kBlock + 4 * piece(n, 4 * w));
+        uint8_t *out = a.qt + (n0 + n) * a.qts + m0 + 16 * w;
+        if (16 * w + 16 <= left_m) {
+            *reinterpret_cast<uint4 *>(out) = p;
+        } else {                           // bytes past the row's end are not ours
+            const uint32_t b[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (16 * w + i < left_m) out[i] = uint8_t(b[i / 4] >> (8 * (i % 4)));
+        }
+    }
+}
+
+// Rows that allow accesses of 16 bytes: a CTA walks tiles with the grid's
+// stride, and the next tile's loads are on their way to shared memory while
+// one is worked on.  A lane has N neighbouring columns (8 of 16 bits, 4 of
+// 32) of R neighbouring rows, 32 values; it copies them itself and reads them
+// from shared memory each time it needs them (maxima, rows, transpose).  The
+// maxima of 16-bit values are taken two at a time.
 // PER_ROW: 1 x 128 scales; otherwise one scale for the tile.
-template <class T, bool VEC, bool PER_ROW>
-__global__ void __launch_bounds__(kTileWarps * 32)
-quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n) {
+template <class T, bool PER_ROW>
+__global__ void __launch_bounds__(kTileThreads, 2)
+quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n, int tiles) {
+    constexpr int ST = kTileAhead + 1, N = Pack<T>::N, G = kBlock / N, R = 32 / N;
+    extern __shared__ __align__(16) uint8_t smem[];     // [ST][R][threads] of 16 bytes
+    __shared__ uint32_t col_max[kTileWarps][kBlock];
+    __shared__ float col_inv[kBlock];
+    __shared__ __align__(16) uint8_t t[kBlock * kBlock];
+    grid_dependency();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int r0 = warp * kTileRows + lane / G * R, c0 = lane % G * N;
+    const T *const x = static_cast<const T *>(a.x);
+    uint4 *const all = reinterpret_cast<uint4 *>(smem);
+    auto fetch = [&](int64_t tile, int stage) {
+        if (tile < tiles) {
+            const int64_t m = tile / tiles_n * kBlock + r0, n = tile % tiles_n * kBlock + c0;
+            const T *from = x + m * a.xs + n;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool have = m + i < a.rows && n < a.cols;
+                copy16_async(all + (stage * R + i) * kTileThreads + threadIdx.x, have ? from + i * a.xs : x, have);
+            }
+        }
+        copy_commit();
+    };
+    for (int i = 0; i < kTileAhead; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+    int stage = ST - 1;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t tm = tile / tiles_n;
+        const int tn = int(tile % tiles_n);
+        const int64_t m0 = tm * kBlock, n0 = int64_t(tn) * kBlock;
+        const int left_n = int(min(int64_t(kBlock), a.cols - n0));
+        const int left_m = int(min(int64_t(kBlock), a.rows - m0));
+        fetch(tile + int64_t(kTileAhead) * gridDim.x, stage);
+        copy_wait<kTileAhead>();
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        const uint4 *mine = all + stage * R * kTileThreads + threadIdx.x;
+
+        // Maxima: of the lane's columns over its rows, joined over the warp's
+        // other rows where it holds two; of its rows over its columns.
+        uint32_t col[4] = {0, 0, 0, 0};          // packed as the values are
+        uint32_t row[R];                          // float bits
+        {
+            uint32_t two[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const uint4 v = mine[i * kTileThreads];
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                two[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    col[j] = Pack<T>::max_abs(col[j], u[j]);
+                    two[i] = Pack<T>::max_abs(two[i], u[j]);
+                }
+            }
+            if constexpr (N == 8) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    col[j] = Pack<T>::max_abs(col[j], __shfl_xor_sync(0xffffffffu, col[j], 16));
+#pragma unroll
+                for (int i = 0; i < R; i += 2) {  // rows i and i + 1 in one word
+                    uint32_t m = Pack<T>::max_abs(__byte_perm(two[i], two[i + 1], 0x5410),
+                                                  __byte_perm(two[i], two[i + 1], 0x7632));
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1)
+                        m = Pack<T>::max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    row[i] = Pack<T>::low(m);
+                    row[i + 1] = Pack<T>::high(m);
+                }
+                if (lane < 16) *reinterpret_cast<uint4 *>(&col_max[warp][lane * 4]) =
+                    make_uint4(col[0], col[1], col[2], col[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; ++i) row[i] = __reduce_max_sync(0xffffffffu, two[i]);
+                *reinterpret_cast<uint4 *>(&col_max[warp][lane * 4]) = make_uint4(col[0], col[1], col[2], col[3]);
+            }
+        }
+        // whether the tile holds an infinity: then each value is looked at
+        bool inf_here = false;
+#pragma unroll
+        for (int i = 0; i < R; ++i) inf_here |= row[i] >= kInfBits;
+        const bool infinite = __syncthreads_or(inf_here);
+        uint32_t tile_sb = 127;
+        if (!PER_ROW || a.qt != nullptr) {
+            // column threadIdx.x of the tile (PER_ROW); all of them otherwise
+            uint32_t m = 0;
+            if (threadIdx.x < kBlock) {
+                const int n = threadIdx.x;
+                if (infinite) {
+                    for (int r = 0; r < kBlock; ++r) {
+                        const int i = r % kTileRows, th = r / kTileRows * 32 + i / R * G + n / N;
+                        const T *v = reinterpret_cast<const T *>(all + (stage * R + i % R) * kTileThreads + th);
+                        m = max(m, finite_bits(Elem<T>::to_float(v[n % N])));
+                    }
+                } else if constexpr (N == 8) {
+                    uint32_t p = 0;
+#pragma unroll
+                    for (int w = 0; w < kTileWarps; ++w) p = Pack<T>::max_abs(p, col_max[w][n / 2]);
+                    m = n % 2 ? Pack<T>::high(p) : Pack<T>::low(p);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < kTileWarps; ++w) m = max(m, col_max[w][n]);
+                }
+                if (PER_ROW) {
+                    const uint32_t sb = scale_byte(m);
+                    col_inv[n] = inverse_scale(sb);
+                    if (n < left_n) a.scales_t[(n0 + n) * a.sts + tm] = uint8_t(sb);
+                } else {
+                    m = __reduce_max_sync(0xffffffffu, m);
+                    if (lane == 0) col_inv[warp] = __uint_as_float(m);
+                }
+            }
+            __syncthreads();
+            if (!PER_ROW) {
+                m = 0;
+#pragma unroll
+                for (int w = 0; w < kBlock / 32; ++w) m = max(m, __float_as_uint(col_inv[w]));
+                tile_sb = scale_byte(m);
+                if (threadIdx.x == 0) {
+                    if (a.q != nullptr) a.scales[tm * a.ss + tn] = uint8_t(tile_sb);
+                    if (a.qt != nullptr) a.scales_t[tn * a.sts + tm] = uint8_t(tile_sb);
+                }
+            }
+        }
+
+        if (a.q != nullptr) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float v[N];
+                Pack<T>::unpack(mine[i * kTileThreads], v);
+                uint32_t sb = tile_sb;
+                if (infinite) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) m = max(m, finite_bits(v[j]));
+#pragma unroll
+                    for (int o = G / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    row[i] = m;
+                    infinite_to_nan(v);
+                }
+                if (r0 + i < left_m) {
+                    const int64_t m = m0 + r0 + i;
+                    if (PER_ROW) {
+                        sb = scale_byte(row[i]);
+                        if (lane % G == 0) a.scales[m * a.ss + tn] = uint8_t(sb);
+                    }
+                    if (c0 < left_n) store_e4m3<N>(a.q + m * a.qs + n0 + c0, v, inverse_scale(sb));
+                }
+            }
+        }
+
+        if (a.qt != nullptr) {
+            float inv[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) inv[j] = PER_ROW ? col_inv[c0 + j] : inverse_scale(tile_sb);
+#pragma unroll
+            for (int k = 0; k < R; k += 4) {
+                float v[4][N];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Pack<T>::unpack(mine[(k + i) * kTileThreads], v[i]);
+                    if (infinite) infinite_to_nan(v[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    *reinterpret_cast<uint32_t *>(t + (c0 + j) * kBlock + 4 * piece(c0 + j, (r0 + k) / 4)) =
+                        to_e4m3x4(v[0][j], v[1][j], v[2][j], v[3][j], inv[j]);
+            }
+            __syncthreads();
+            store_transposed(a, t, m0, n0, left_m, left_n);
+        }
+        __syncthreads();                   // t, col_max and col_inv are used again
+    }
+}
+
+// Rows of any alignment: a tile a CTA, its values in registers, columns lane,
+// lane + 32, ... of a row to a lane.
+template <class T, bool PER_ROW>
+__global__ void __launch_bounds__(kTileThreads, 2)
+quantize_any_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n) {
     __shared__ uint32_t col_max[kTileWarps][kBlock];
     __shared__ __align__(16) uint8_t t[kBlock * kBlock];
     grid_dependency();
@@ -84,113 +292,89 @@ quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n) {
     float v[kTileRows][4];
     const T *x = static_cast<const T *>(a.x) + (m0 + r0) * a.xs + n0;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        if (r0 + i < left_m) {
-            load4<T, VEC>(x + i * a.xs, lane, left_n, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
-        }
-    }
+    for (int i = 0; i < kTileRows; ++i) load4<T, false>(x + i * a.xs, lane, r0 + i < left_m ? left_n : 0, v[i]);
 
+    uint32_t col[4] = {0, 0, 0, 0}, most = 0;
+#pragma unroll
+    for (int i = 0; i < kTileRows; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) col[j] = max(col[j], finite_bits(v[i][j]));
+    most = max(max(col[0], col[1]), max(col[2], col[3]));
     uint32_t tile_sb = 127;
-    if (!PER_ROW) {
-        uint32_t m = 0;
+    if (PER_ROW) {
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) m = max(m, max_bits4(v[i]));
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) col_max[warp][0] = m;
+        for (int j = 0; j < 4; ++j) col_max[warp][lane + 32 * j] = col[j];
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kTileWarps; ++w) m = max(m, col_max[w][0]);
-        tile_sb = scale_byte(m);
+    } else {
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) col_max[0][warp] = most;
+        __syncthreads();
+        tile_sb = scale_byte(__reduce_max_sync(0xffffffffu, lane < kTileWarps ? col_max[0][lane] : 0u));
         if (threadIdx.x == 0) {
             if (a.q != nullptr) a.scales[tm * a.ss + tn] = uint8_t(tile_sb);
             if (a.qt != nullptr) a.scales_t[tn * a.sts + tm] = uint8_t(tile_sb);
         }
     }
-
-    if (a.q != nullptr) {
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) {
-            if (r0 + i >= left_m) break;
-            const int64_t m = m0 + r0 + i;
-            uint32_t sb = tile_sb;
-            if (PER_ROW) {
-                sb = scale_byte(__reduce_max_sync(0xffffffffu, max_bits4(v[i])));
-                if (lane == 0) a.scales[m * a.ss + tn] = uint8_t(sb);
-            }
-            store4_e4m3<VEC>(a.q + m * a.qs + n0, lane, left_n, to_e4m3x4(v[i], inverse_scale(sb)));
-        }
+    for (int i = 0; i < kTileRows; ++i) {
+        const uint32_t sb = PER_ROW ? row_scale(v[i]) : tile_sb;
+        infinite_to_nan(v[i]);
+        if (a.q == nullptr || r0 + i >= left_m) continue;
+        const int64_t m = m0 + r0 + i;
+        if (PER_ROW && lane == 0) a.scales[m * a.ss + tn] = uint8_t(sb);
+        store4_e4m3<false>(a.q + m * a.qs + n0, lane, left_n, to_e4m3x4(v[i], inverse_scale(sb)));
     }
     if (a.qt == nullptr) return;
-
-    uint32_t sb[4] = {tile_sb, tile_sb, tile_sb, tile_sb};
-    if (PER_ROW) {
-        uint32_t m[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < kTileRows; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m[j] = max(m[j], finite_bits(v[i][j]));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) col_max[warp][lane_col<VEC>(lane, j)] = m[j];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = lane_col<VEC>(lane, j);
-#pragma unroll
-            for (int w = 0; w < kTileWarps; ++w) m[j] = max(m[j], col_max[w][n]);
-            sb[j] = scale_byte(m[j]);
-            if (warp == 0 && n < left_n) a.scales_t[(n0 + n) * a.sts + tm] = uint8_t(sb[j]);
-        }
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int n = lane_col<VEC>(lane, j);
-        const float inv = inverse_scale(sb[j]);
-        uint32_t p[kTileRows / 4];
+        const int n = lane + 32 * j;
+        uint32_t sb = tile_sb;
+        if (PER_ROW) {
+            uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kTileRows / 4; ++k) {
-            const float c[4] = {v[4 * k][j], v[4 * k + 1][j], v[4 * k + 2][j], v[4 * k + 3][j]};
-            p[k] = to_e4m3x4(c, inv);
+            for (int w = 0; w < kTileWarps; ++w) m = max(m, col_max[w][n]);
+            sb = scale_byte(m);
+            if (warp == 0 && n < left_n) a.scales_t[(n0 + n) * a.sts + tm] = uint8_t(sb);
         }
-        *reinterpret_cast<uint4 *>(t + n * kBlock + 16 * piece(n, warp)) = make_uint4(p[0], p[1], p[2], p[3]);
+        const float inv = inverse_scale(sb);
+#pragma unroll
+        for (int k = 0; k < kTileRows; k += 4)
+            *reinterpret_cast<uint32_t *>(t + n * kBlock + 4 * piece(n, (r0 + k) / 4)) =
+                to_e4m3x4(v[k][j], v[k + 1][j], v[k + 2][j], v[k + 3][j], inv);
     }
     __syncthreads();
-    // 16 bytes a thread, eight threads a transposed row, four rounds
-#pragma unroll
-    for (int k = 0; k < kBlock * kBlock / (16 * kTileWarps * 32); ++k) {
-        const int n = k * (kTileWarps * 4) + int(threadIdx.x) / 8, w = threadIdx.x % 8;
-        if (n >= left_n || 16 * w >= left_m) continue;
-        const uint4 p = *reinterpret_cast<const uint4 *>(t + n * kBlock + 16 * piece(n, w));
-        uint8_t *out = a.qt + (n0 + n) * a.qts + m0 + 16 * w;
-        if (16 * w + 16 <= left_m) {
-            *reinterpret_cast<uint4 *>(out) = p;
-        } else {                           // bytes past the row's end are not ours
-            const uint32_t b[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (16 * w + i < left_m) out[i] = uint8_t(b[i / 4] >> (8 * (i % 4)));
-        }
+    store_transposed(a, t, m0, n0, left_m, left_n);
+}
+
+template <class T>
+basp_status launch_tiles(const QuantArgs &a, bool per_row, bool vec16, cudaStream_t stream) {
+    const int64_t blocks = ceil_div(a.cols, kBlock), tiles = ceil_div(a.rows, kBlock) * blocks;
+    if (tiles > kMaxSide) return BASP_ERR_TOO_LARGE;
+    if (!vec16) {
+        auto kernel = per_row ? quantize_any_tile_kernel<T, true> : quantize_any_tile_kernel<T, false>;
+        return launch(kernel, dim3(unsigned(tiles)), dim3(kTileThreads), 0, 1, stream, a, int(blocks));
     }
+    auto kernel = per_row ? quantize_tile_kernel<T, true> : quantize_tile_kernel<T, false>;
+    const size_t smem = size_t(kTileAhead + 1) * kBlock * kBlock * sizeof(T);
+    const int64_t ctas = std::min(tiles, resident_ctas(kernel, kTileThreads, smem));
+    return launch(kernel, dim3(unsigned(ctas)), dim3(kTileThreads), smem, 1, stream, a, int(blocks), int(tiles));
 }
 
 template <class T, bool VEC>
+basp_status launch_rows(const QuantArgs &a, cudaStream_t stream) {
+    const int64_t groups = ceil_div(ceil_div(a.cols, kBlock), kRowBlocks);
+    const int64_t ctas = ceil_div(a.rows * groups, kRowWarps);
+    if (ctas > kMaxSide) return BASP_ERR_TOO_LARGE;
+    return launch(quantize_rows_kernel<T, VEC>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a,
+                  int(groups));
+}
+
+template <class T>
 basp_status launch_quantize(const QuantArgs &a, bool per_row, cudaStream_t stream) {
-    const int64_t blocks = ceil_div(a.cols, kBlock);
-    if (per_row && a.qt == nullptr) {
-        const int64_t groups = ceil_div(blocks, kRowBlocks);
-        const int64_t ctas = ceil_div(a.rows * groups, kRowWarps);
-        if (ctas > kMaxSide) return BASP_ERR_TOO_LARGE;
-        return launch(quantize_rows_kernel<T, VEC>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream,
-                      a, int(groups));
-    }
-    const int64_t tiles = ceil_div(a.rows, kBlock) * blocks;
-    if (tiles > kMaxSide) return BASP_ERR_TOO_LARGE;
-    const dim3 grid(static_cast<unsigned>(tiles)), block(kTileWarps * 32);
-    if (per_row)
-        return launch(quantize_tile_kernel<T, VEC, true>, grid, block, 0, 1, stream, a, int(blocks));
-    return launch(quantize_tile_kernel<T, VEC, false>, grid, block, 0, 1, stream, a, int(blocks));
+    if (!per_row || a.qt != nullptr)
+        return launch_tiles<T>(a, per_row, vec16_ok(a.x, a.xs, a.cols, sizeof(T)), stream);
+    return vec4_ok(a.x, a.xs, a.cols, sizeof(T)) ? launch_rows<T, true>(a, stream)
+                                                 : launch_rows<T, false>(a, stream);
 }
 
 }  // namespace
@@ -229,16 +413,9 @@ extern "C" basp_status basp_quantize_fp8(basp_dtype dtype, int64_t rows, int64_t
         a.sts = qt->scale_pitch;
     }
     const bool per_row = (q != nullptr ? q : qt)->block_rows == 1;
-    const bool vec = vec4_ok(x, x_stride, cols, esz);
     switch (dtype) {
-        case BASP_DTYPE_BF16:
-            return vec ? launch_quantize<__nv_bfloat16, true>(a, per_row, stream)
-                       : launch_quantize<__nv_bfloat16, false>(a, per_row, stream);
-        case BASP_DTYPE_FP16:
-            return vec ? launch_quantize<__half, true>(a, per_row, stream)
-                       : launch_quantize<__half, false>(a, per_row, stream);
-        default:
-            return vec ? launch_quantize<float, true>(a, per_row, stream)
-                       : launch_quantize<float, false>(a, per_row, stream);
+        case BASP_DTYPE_BF16: return launch_quantize<__nv_bfloat16>(a, per_row, stream);
+        case BASP_DTYPE_FP16: return launch_quantize<__half>(a, per_row, stream);
+        default: return launch_quantize<float>(a, per_row, stream);
     }
 }

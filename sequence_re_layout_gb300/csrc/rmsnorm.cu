@@ -42,6 +42,7 @@ struct NormArgs {
     int64_t xs, rs, hs, ys, qs, ss;
     int64_t rows;
     int cols;
+    bool vec16;
     float eps, inv_cols;
 };
 
@@ -75,7 +76,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int64_t row, int b
     if (a.y != nullptr)
         store4<T, VEC>(static_cast<T *>(a.y) + row * a.ys + b * kBlock, lane, left, y);
     if (a.q != nullptr) {
-        const uint32_t sb = scale_byte(__reduce_max_sync(0xffffffffu, max_bits4(y)));
+        const uint32_t sb = row_scale(y);
         store4_e4m3<VEC>(a.q + row * a.qs + b * kBlock, lane, left, to_e4m3x4(y, inverse_scale(sb)));
         if (lane == 0) a.scales[row * a.ss + b] = uint8_t(sb);
     }
@@ -84,7 +85,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int64_t row, int b
 // NB > 0: warp w of a row's warps holds blocks w, w + warps, ... (NB of them)
 // in registers.  NB = 0: rows too long for that; the row is walked twice.
 template <class T, class W, int NB, bool VEC>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(NB == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float part[32];
     grid_dependency();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -166,6 +167,151 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     }
 }
 
+// The same for many rows that allow accesses of 16 bytes: the CTA walks rows
+// with the grid's stride, and the loads of the next kAhead rows are on their
+// way to shared memory while one is worked on, each thread copying what it
+// will read itself.  A thread has NV vectors of 16 bytes, 8 or 4 values each;
+// 16 or 32 neighbouring threads hold a 128-block.  The instructions count
+// here: a value takes about 15, and 28 would be the bound instead of memory.
+constexpr int kAhead = 2;
+constexpr int kWalkThreads = 512;
+
+// As row_sum, for whole rows a CTA and with fewer instructions: every thread
+// adds the warps' parts itself.  `part` has room for 16 and is zero past the
+// CTA's warps.
+__device__ __forceinline__ float walk_sum(float v, float *part, int warps) {
+    v = warp_sum(v);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < warps; i += 4) {
+        const float4 p = *reinterpret_cast<const float4 *>(part + i);
+        v += (p.x + p.y) + (p.z + p.w);
+    }
+    return v;
+}
+
+// Largest over the threads of a 128-block (16 or 32 of a warp).
+template <int THREADS> __device__ __forceinline__ uint32_t block_max(uint32_t m) {
+    if constexpr (THREADS == 32) return __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+    for (int o = THREADS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+template <class T, class W, int NV>
+__global__ void __launch_bounds__(kWalkThreads) norm_walk_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int ST = kAhead + 1, N = Pack<T>::N, G = kBlock / N;
+    extern __shared__ __align__(16) uint8_t smem[];     // [stage][x, residual][vector][thread]
+    __shared__ __align__(16) float part[2][16];
+    const int threads = blockDim.x, warps = threads / 32;
+    if (threadIdx.x < 32) part[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+    uint4 *mine = reinterpret_cast<uint4 *>(smem) + threadIdx.x;
+    grid_dependency();
+
+    const T *x = static_cast<const T *>(a.x), *r = static_cast<const T *>(a.residual);
+    int col[NV];
+    bool have[NV];
+    float wv[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        col[i] = (i * threads + int(threadIdx.x)) * N;
+        have[i] = col[i] < a.cols;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            wv[i][j] = have[i] ? Elem<W>::to_float(static_cast<const W *>(a.weight)[col[i] + j]) : 0.f;
+    }
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            const T *xr = x + row * a.xs, *rr = r + row * a.rs;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                copy16_async(mine + (stage * 2 * NV + i) * threads, have[i] ? xr + col[i] : x, have[i]);
+                if (r != nullptr)
+                    copy16_async(mine + (stage * 2 * NV + NV + i) * threads, have[i] ? rr + col[i] : r, have[i]);
+            }
+        }
+        copy_commit();                    // an empty group past the end keeps the count
+    };
+    const int64_t step = gridDim.x;
+    for (int i = 0; i < kAhead; ++i) fetch(blockIdx.x + i * step, i);
+    __syncthreads();                      // part is zero
+
+    int stage = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += step, turn ^= 1) {
+        fetch(row + kAhead * step, stage >= 1 ? stage - 1 : ST - 1);
+        copy_wait<kAhead>();
+        float hv[NV][N], sq = 0.f, top[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint4 raw = mine[(stage * 2 * NV + i) * threads];
+            Pack<T>::unpack(raw, hv[i]);
+            if (r != nullptr) {
+                float f[N];
+                Pack<T>::unpack(mine[(stage * 2 * NV + NV + i) * threads], f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) hv[i][j] += f[j];
+                raw = Pack<T>::pack(hv[i]);
+                Pack<T>::unpack(raw, hv[i]);
+            }
+            if (a.h != nullptr && have[i])
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + row * a.hs + col[i]) = raw;
+            // times the weight before the root is known: y is this times rstd
+            top[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                sq += hv[i][j] * hv[i][j];
+                hv[i][j] *= wv[i][j];
+                top[i] = fmaxf(top[i], fabsf(hv[i][j]));
+            }
+        }
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        // two buffers in turn: a warp can be one row ahead of another
+        const float rstd = rsqrtf(walk_sum(sq, part[turn], warps) * a.inv_cols + a.eps);
+        if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+        if (a.y != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float y[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) y[j] = hv[i][j] * rstd;
+                if (have[i])
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ys + col[i]) = Pack<T>::pack(y);
+            }
+        }
+        if (a.q != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                // rounding is monotonic: the largest y is the largest product's
+                uint32_t m = block_max<G>(__float_as_uint(top[i] * rstd));
+                float inv = rstd;
+                // An infinity, 0 * inf, or so far out that rstd times the
+                // inverse scale might be too: look at each value.
+                const bool odd = m != 0 && m - 0x20000000u >= 0x3f000000u;
+                if (__any_sync(0xffffffffu, odd)) {
+                    uint32_t f = 0;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) f = max(f, finite_bits(hv[i][j] * rstd));
+                    f = block_max<G>(f);
+                    if (odd) {
+                        m = f;
+                        inv = 1.f;
+#pragma unroll
+                        for (int j = 0; j < N; ++j) hv[i][j] *= rstd;
+                        infinite_to_nan(hv[i]);
+                    }
+                }
+                const uint32_t sb = scale_byte(m);
+                if (have[i]) {
+                    // a power of two times rstd rounds nothing
+                    store_e4m3<N>(a.q + row * a.qs + col[i], hv[i], inv * inverse_scale(sb));
+                    if (threadIdx.x % G == 0) a.scales[row * a.ss + col[i] / kBlock] = uint8_t(sb);
+                }
+            }
+        }
+    }
+}
+
 template <class T, class W, bool VEC>
 basp_status launch_norm(const NormArgs &a, cudaStream_t stream) {
     const int blocks = int(ceil_div(a.cols, kBlock));
@@ -173,6 +319,18 @@ basp_status launch_norm(const NormArgs &a, cudaStream_t stream) {
     // four blocks a warp, which keeps 8 loads a thread in flight and the
     // cross-warp step small.
     const bool few = a.rows <= 2 * sm_count();
+    if (a.vec16 && !few) {
+        const int vectors = int(a.cols / Pack<T>::N);
+        auto walk = [&](auto kernel, int nv) {
+            const int threads = int(ceil_div(vectors, nv * 32)) * 32;
+            const size_t smem = size_t(kAhead + 1) * 2 * nv * threads * 16;
+            const int64_t ctas = std::min(a.rows, resident_ctas(kernel, threads, smem));
+            return launch(kernel, dim3(unsigned(ctas)), dim3(threads), smem, 1, stream, a);
+        };
+        if (vectors <= kWalkThreads) return walk(norm_walk_kernel<T, W, 1>, 1);
+        if (vectors <= 2 * kWalkThreads) return walk(norm_walk_kernel<T, W, 2>, 2);
+        if (vectors <= 4 * kWalkThreads) return walk(norm_walk_kernel<T, W, 4>, 4);
+    }
     if (blocks <= 4 && !few) {            // one warp a row, four rows a CTA
         return launch(norm_kernel<T, W, 4, VEC>, dim3(unsigned(ceil_div(a.rows, 4))), dim3(32, 4), 0, 1,
                       stream, a);
@@ -180,10 +338,10 @@ basp_status launch_norm(const NormArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(a.rows));
     if (few && blocks <= 32)
         return launch(norm_kernel<T, W, 1, VEC>, grid, dim3(unsigned(blocks) * 32), 0, 1, stream, a);
-    if (blocks <= 4 * 32)
+    if (blocks <= 4 * 16)
         return launch(norm_kernel<T, W, 4, VEC>, grid, dim3(unsigned(ceil_div(blocks, 4)) * 32), 0, 1,
                       stream, a);
-    return launch(norm_kernel<T, W, 0, VEC>, grid, dim3(1024), 0, 1, stream, a);
+    return launch(norm_kernel<T, W, 0, VEC>, grid, dim3(512), 0, 1, stream, a);
 }
 
 struct NormBackArgs {
@@ -194,12 +352,13 @@ struct NormBackArgs {
     int64_t dys, hs, dhs, dxs;
     int64_t rows;
     int cols;
+    bool vec16;
     float inv_cols;
 };
 
 // NB blocks a warp, as above; the CTA walks rows blockIdx.x, + gridDim.x, ...
 template <class T, class W, int NB, bool VEC>
-__global__ void __launch_bounds__(NB > 0 ? 512 : 1024) norm_back_kernel(const __grid_constant__ NormBackArgs a) {
+__global__ void __launch_bounds__(512) norm_back_kernel(const __grid_constant__ NormBackArgs a) {
     __shared__ float part[2][32];
     grid_dependency();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -301,6 +460,95 @@ __global__ void __launch_bounds__(NB > 0 ? 512 : 1024) norm_back_kernel(const __
     }
 }
 
+// The same for rows that allow accesses of 16 bytes, with the loads of the
+// next kAhead rows on their way to shared memory.
+template <class T, class W, int NV>
+__global__ void __launch_bounds__(kWalkThreads) norm_back_walk_kernel(const __grid_constant__ NormBackArgs a) {
+    constexpr int ST = kAhead + 1, N = Pack<T>::N;
+    extern __shared__ __align__(16) uint8_t smem[];     // [stage][dy, h, dh][vector][thread]
+    __shared__ __align__(16) float part[2][16];
+    const int threads = blockDim.x, warps = threads / 32;
+    if (threadIdx.x < 32) part[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+    uint4 *mine = reinterpret_cast<uint4 *>(smem) + threadIdx.x;
+    grid_dependency();
+
+    const T *dy = static_cast<const T *>(a.dy), *h = static_cast<const T *>(a.h);
+    const T *dh = static_cast<const T *>(a.dh);
+    int col[NV];
+    bool have[NV];
+    float wv[NV][N], dw[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        col[i] = (i * threads + int(threadIdx.x)) * N;
+        have[i] = col[i] < a.cols;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            wv[i][j] = have[i] ? Elem<W>::to_float(static_cast<const W *>(a.weight)[col[i] + j]) : 0.f;
+            dw[i][j] = 0.f;
+        }
+    }
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.rows) {
+            const T *d = dy + row * a.dys, *n = h + row * a.hs, *m = dh + row * a.dhs;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                uint4 *to = mine + (stage * 3 * NV + i) * threads;
+                copy16_async(to, have[i] ? d + col[i] : dy, have[i]);
+                copy16_async(to + NV * threads, have[i] ? n + col[i] : h, have[i]);
+                if (dh != nullptr) copy16_async(to + 2 * NV * threads, have[i] ? m + col[i] : dh, have[i]);
+            }
+        }
+        copy_commit();                    // an empty group past the end keeps the count
+    };
+    const int64_t step = gridDim.x;
+    for (int i = 0; i < kAhead; ++i) fetch(blockIdx.x + i * step, i);
+    __syncthreads();                      // part is zero
+
+    int stage = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += step, turn ^= 1) {
+        fetch(row + kAhead * step, stage >= 1 ? stage - 1 : ST - 1);
+        const float rstd = a.rstd[row];
+        copy_wait<kAhead>();
+        const uint4 *at = mine + stage * 3 * NV * threads;
+        float g[NV][N], n[NV][N], dot = 0.f;
+        uint4 rest[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Pack<T>::unpack(at[i * threads], g[i]);
+            Pack<T>::unpack(at[(NV + i) * threads], n[i]);
+            rest[i] = dh != nullptr ? at[(2 * NV + i) * threads] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                n[i][j] *= rstd;
+                dw[i][j] += g[i][j] * n[i][j];
+                g[i][j] *= wv[i][j];
+                dot += g[i][j] * n[i][j];
+            }
+        }
+        stage = stage + 1 < ST ? stage + 1 : 0;
+        const float mean = walk_sum(dot, part[turn], warps) * a.inv_cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float d[N];
+            Pack<T>::unpack(rest[i], d);
+#pragma unroll
+            for (int j = 0; j < N; ++j) d[j] += rstd * (g[i][j] - n[i][j] * mean);
+            if (have[i])
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.dxs + col[i]) = Pack<T>::pack(d);
+        }
+    }
+    if (a.part != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (have[i]) {
+                float4 *out = reinterpret_cast<float4 *>(a.part + int64_t(blockIdx.x) * a.cols + col[i]);
+#pragma unroll
+                for (int j = 0; j < N / 4; ++j)
+                    out[j] = make_float4(dw[i][4 * j], dw[i][4 * j + 1], dw[i][4 * j + 2], dw[i][4 * j + 3]);
+            }
+    }
+}
+
 // dweight[c] = sum over the parts' rows, in their order: 32 columns a CTA,
 // 32 warps that each add every 32nd row, then one warp adds their sums.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int parts, int cols, float *out) {
@@ -329,13 +577,24 @@ template <class T, class W, bool VEC>
 basp_status launch_norm_back(const NormBackArgs &a, cudaStream_t stream) {
     const int blocks = int(ceil_div(a.cols, kBlock));
     const dim3 grid(static_cast<unsigned>(back_parts(a.rows)));
+    if (a.vec16) {
+        const int vectors = int(a.cols / Pack<T>::N);
+        auto walk = [&](auto kernel, int nv) {
+            const int threads = int(ceil_div(vectors, nv * 32)) * 32;
+            const size_t smem = size_t(kAhead + 1) * 3 * nv * threads * 16;
+            resident_ctas(kernel, threads, smem);
+            return launch(kernel, grid, dim3(threads), smem, 1, stream, a);
+        };
+        if (vectors <= kWalkThreads) return walk(norm_back_walk_kernel<T, W, 1>, 1);
+        if (vectors <= 2 * kWalkThreads) return walk(norm_back_walk_kernel<T, W, 2>, 2);
+    }
     if (blocks <= 32)
         return launch(norm_back_kernel<T, W, 2, VEC>, grid, dim3(unsigned(ceil_div(blocks, 2)) * 32), 0, 1,
                       stream, a);
     if (blocks <= 64)
         return launch(norm_back_kernel<T, W, 4, VEC>, grid, dim3(unsigned(ceil_div(blocks, 4)) * 32), 0, 1,
                       stream, a);
-    return launch(norm_back_kernel<T, W, 0, VEC>, grid, dim3(1024), 0, 1, stream, a);
+    return launch(norm_back_kernel<T, W, 0, VEC>, grid, dim3(512), 0, 1, stream, a);
 }
 
 // Calls f<T, W, VEC>() for the run-time types.
@@ -396,6 +655,8 @@ extern "C" basp_status basp_rmsnorm(basp_dtype dtype, int64_t rows, int64_t cols
     const bool vec = vec4_ok(x, x_stride, cols, esz) && vec4_ok(residual, residual_stride, cols, esz) &&
                      vec4_ok(weight, 0, cols, wsz) && vec4_ok(h, h_stride, cols, esz) &&
                      vec4_ok(y, y_stride, cols, esz);
+    a.vec16 = vec16_ok(x, x_stride, cols, esz) && vec16_ok(residual, residual_stride, cols, esz) &&
+              vec16_ok(h, h_stride, cols, esz) && vec16_ok(y, y_stride, cols, esz);
     return dispatch(dtype, weight_dtype, vec, [&](auto t, auto w, auto v) {
         return launch_norm<decltype(t), decltype(w), decltype(v)::value>(a, stream);
     });
@@ -454,6 +715,8 @@ extern "C" basp_status basp_rmsnorm_backward(basp_dtype dtype, int64_t rows, int
     const bool vec = vec4_ok(dy, dy_stride, cols, esz) && vec4_ok(h, h_stride, cols, esz) &&
                      vec4_ok(weight, 0, cols, wsz) && vec4_ok(dh, dh_stride, cols, esz) &&
                      vec4_ok(dx, dx_stride, cols, esz);
+    a.vec16 = vec16_ok(dy, dy_stride, cols, esz) && vec16_ok(h, h_stride, cols, esz) &&
+              vec16_ok(dh, dh_stride, cols, esz) && vec16_ok(dx, dx_stride, cols, esz);
     st = dispatch(dtype, weight_dtype, vec, [&](auto t, auto w, auto v) {
         return launch_norm_back<decltype(t), decltype(w), decltype(v)::value>(a, stream);
     });
