@@ -16,12 +16,26 @@
 // coalesced whatever the row stride, the bias is one value a thread, and one
 // token costs a 16-wide instruction instead of a padded 128-row one.
 //
-// A CTA is eight warps: one issues TMA loads (128 bytes of K a stage, in the
-// 128-byte swizzle), one issues the products, one brings scales, four drain
-// accumulators.  Large products run a persistent CTA per SM whose accumulator
-// is double-buffered, so a tile's stores overlap the next tile's products.
-// With few tiles, a cluster of CTAs splits K; the parts meet in shared memory
-// and are added in rank order, so results do not depend on timing.
+// A CTA has a warp that issues TMA loads (128 bytes of K a stage, in the
+// 128-byte swizzle), one that issues the products, one that brings scales,
+// and four or eight that drain accumulators.  Large products run a persistent
+// CTA per SM whose accumulator is double-buffered, so a tile's drain overlaps
+// the next tile's products.  With few tiles, a cluster of CTAs splits K; the
+// parts meet in shared memory and are added in rank order, so results do not
+// depend on timing.
+//
+// Drain.  16-bit results leave tensor memory as matrix fragments, which
+// stmatrix transposes into 64-byte rows of C in shared memory, and TMA stores
+// them: about two instructions a value, where one store a value kept the
+// products waiting (2.2 PFLOP/s at 32768 x 6144 x 2048).  Rows of C that TMA
+// cannot address, and accumulation into C, take one store a value.
+//
+// Long sums.  The tensor cores' 32-bit accumulator truncates: after 1024
+// instructions (K = 32768) a sum is off by 8e-6 of its size, systematically.
+// For 32-bit results the accumulator therefore starts afresh every 2048
+// values of K, and the drain adds the segments in registers, rounding to
+// nearest; a 16-bit result's own rounding is a hundred times larger, so
+// there one accumulator takes all of K.
 //
 // Waits.  Every wait on an mbarrier has a time limit.  When one runs out the
 // CTA's roles leave their loops, wait (with the limit again) for copies and
@@ -47,14 +61,24 @@ __host__ __device__ constexpr int stage_bytes(int BN) { return (kTileP + BN) * k
 __host__ __device__ constexpr int scale_bytes(int BN) { return 512 + (BN > 128 ? 1024 : 512); }
 __host__ __device__ constexpr int scale_columns(int BN) { return scale_bytes(BN) / 128; }
 
+// K blocks of a segment of a 32-bit result.
+constexpr int kSegment = 16;
+
+// Drain warps: 32-bit results keep a tile's sums in registers (128 a thread).
+template <class T> __host__ __device__ constexpr int drain_warps() { return sizeof(T) == 4 ? 8 : 4; }
+template <class T> __host__ __device__ constexpr int cta_threads() { return 128 + 32 * drain_warps<T>(); }
+// 32 rows of 32 16-bit results, two a drain warp
+constexpr int kOutBytes = 32 * 64, kOutBuffers = 2;
+constexpr int kOutTotal = 4 * kOutBuffers * kOutBytes;
+
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarrierBytes = 512;
 __host__ __device__ constexpr int stages(int BN) {
-    const int n = (kSmemLimit - 1024 - kBarrierBytes - kScaleSlots * scale_bytes(BN)) / stage_bytes(BN);
+    const int n = (kSmemLimit - 1024 - kBarrierBytes - kOutTotal - kScaleSlots * scale_bytes(BN)) / stage_bytes(BN);
     return n < 8 ? n : 8;
 }
 __host__ __device__ constexpr int smem_bytes(int BN) {
-    return 1024 + stages(BN) * stage_bytes(BN) + kScaleSlots * scale_bytes(BN) + kBarrierBytes;
+    return 1024 + stages(BN) * stage_bytes(BN) + kScaleSlots * scale_bytes(BN) + kOutTotal + kBarrierBytes;
 }
 
 // Tensor-memory columns: two accumulators and two scale slots.  Two of 256
@@ -80,6 +104,7 @@ struct MatmulArgs {
     int tiles_m, tiles_n, tiles;
     int split;                           // CTAs of a cluster that share a tile
     int accumulate;
+    int tma_out;                         // C's rows can be stored by TMA
 };
 
 // Tiles of one group of 16 tile rows of B run side by side over all of A, so
@@ -117,14 +142,46 @@ __device__ __forceinline__ void put(const MatmulArgs &a, T *c, float v) {
     *c = Elem<T>::from_float(v);
 }
 
+template <class T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Adds a tile's parts of all CTAs of the cluster, in rank order; each CTA
+// stores a share of the columns.  `part0`: [BN][128] floats in every CTA.
 template <int BN, class T>
-__global__ void __launch_bounds__(256, 1)
+__device__ __forceinline__ void join_parts(const MatmulArgs &a, uint32_t part0, int rank, int tm, int tn) {
+    const int row = threadIdx.x % kTileP, half = threadIdx.x / kTileP, halves = blockDim.x / kTileP;
+    const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
+    if (n >= a.N) return;
+    const float bias = a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
+    const int j1 = min(BN * (rank + 1) / a.split, int(min(int64_t(BN), a.M - m0)));
+    for (int j = BN * rank / a.split + half; j < j1; j += halves) {
+        float p[8], v = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < a.split) p[r] = cluster_load(cluster_addr(part0 + uint32_t(j * kTileP + row) * 4, r));
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < a.split) v += p[r];
+        put<T>(a, static_cast<T *>(a.c) + (m0 + j) * a.c_stride + n, v + bias);
+    }
+}
+
+template <int BN, class T>
+__global__ void __launch_bounds__(cta_threads<T>(), 1)
 matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_p,
-              const __grid_constant__ CUtensorMap map_q) {
-    constexpr int ST = stages(BN);
+              const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c) {
+    constexpr int ST = stages(BN), DW = drain_warps<T>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    uint8_t *scale_smem = smem + ST * stage_bytes(BN);
+    uint8_t *out_smem = smem + ST * stage_bytes(BN);
+    uint8_t *scale_smem = out_smem + kOutTotal;
     uint64_t *bars = reinterpret_cast<uint64_t *>(scale_smem + kScaleSlots * scale_bytes(BN));
     const uint32_t stage0 = smem_addr(smem), scale0 = smem_addr(scale_smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * ST, sfull = empty + 8 * ST, sempty = sfull + 8 * kScaleSlots;
@@ -137,6 +194,9 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     const int rank = a.split > 1 ? int(blockIdx.x) % a.split : 0;
     const int first = int(blockIdx.x) / a.split, step = int(gridDim.x) / a.split;
     const int kb0 = int(int64_t(a.nk) * rank / a.split), kb1 = int(int64_t(a.nk) * (rank + 1) / a.split);
+    // one accumulator takes `segment` blocks of K; a tile has `segments`
+    const int segment = sizeof(T) == 4 ? kSegment : a.nk;
+    const int segments = (kb1 - kb0 + segment - 1) / segment;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&map_p);
@@ -151,7 +211,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_full + 8, 1);
-        mbar_init(acc_free, 4);
+        mbar_init(acc_free, DW);
         mbar_init(drained, 1);
         *abort = 0;
         fence_mbar_init();
@@ -190,13 +250,18 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         if (lane == 0) {                                  // products
             uint32_t it = 0, group = 0, count = 0;
             bool ok = true;
-            for (int t = first; t < a.tiles && ok; t += step, ++count) {
-                const uint32_t acc = tmem + (count & 1) * acc_offset(BN);
-                if (count > 0) ok = wait(acc_free, (count - 1) & 1);
-                if (!ok) break;
-                tcgen05_after_sync();
-                uint32_t slot = 0;
+            for (int t = first; t < a.tiles && ok; t += step) {
+                uint32_t slot = 0, acc = 0;
+                int left = 0;                             // blocks left of the segment
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const bool fresh = left == 0;
+                    if (fresh) {
+                        left = segment;
+                        acc = tmem + (count & 1) * acc_offset(BN);
+                        if (count > 0) ok = wait(acc_free, (count - 1) & 1);
+                        if (!ok) break;
+                        tcgen05_after_sync();
+                    }
                     if (kb == kb0 || kb % 4 == 0) {       // scales of the next four blocks
                         slot = group % kScaleSlots;
                         ok = wait(sfull + 8 * slot, (group / kScaleSlots) & 1);
@@ -219,11 +284,14 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     const uint32_t idesc = mma_desc(kTileP, BN) | mma_scale_ids(kb & 3);
 #pragma unroll
                     for (int k = 0; k < kStageK / 32; ++k)
-                        mma_mxf8(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, kb > kb0 || k > 0);
+                        mma_mxf8(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
                     mma_commit(empty + 8 * s);
                     if (kb + 1 == kb1 || kb % 4 == 3) mma_commit(sempty + 8 * slot);
+                    if (--left == 0 || kb + 1 == kb1) {
+                        mma_commit(acc_full + 8 * (count & 1));
+                        ++count;
+                    }
                 }
-                if (ok) mma_commit(acc_full + 8 * (count & 1));
             }
             if (!ok) {                                    // products in flight end before the CTA does
                 mma_commit(drained);
@@ -272,54 +340,166 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     } else if (warp >= 4) {                               // drain
         const int quarter = warp % 4, row = quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        float *part = reinterpret_cast<float *>(smem);     // [BN][128], split only
         uint32_t count = 0;
         bool ok = true;
-        for (int t = first; t < a.tiles; t += step, ++count) {
+        auto next_accumulator = [&]() {
+            const bool arrived = ok && wait(acc_full + 8 * (count & 1), (count >> 1) & 1);
+            ok = __all_sync(0xffffffffu, arrived);
+            tcgen05_after_sync();
+            return tmem + lanes + (count & 1) * acc_offset(BN);
+        };
+        // The next products may write the other accumulator: what this warp
+        // reads of it, or of the columns it shares, is behind it.
+        auto release = [&]() {
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free);
+        };
+        for (int t = first; t < a.tiles; t += step) {
             int tm, tn;
             tile_at(a, t, &tm, &tn);
             const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
             const bool mine = n < a.N;
+            T *c = static_cast<T *>(a.c) + m0 * a.c_stride + n;
             const float bias = mine && a.bias != nullptr && a.split == 1
                                    ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
-            T *c = static_cast<T *>(a.c) + m0 * a.c_stride + n;
-            float *part = reinterpret_cast<float *>(smem);     // [BN][128], split only
-            const bool arrived = ok && wait(acc_full + 8 * (count & 1), (count >> 1) & 1);
-            ok = __all_sync(0xffffffffu, arrived);
-            tcgen05_after_sync();
-            const uint32_t acc = tmem + lanes + (count & 1) * acc_offset(BN);
-            if (BN < 256 && ok) {
-                // no columns shared: what this warp read of the other accumulator is behind it
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_free);
-            }
-            for (int i = 0; i < BN / 16; ++i) {
-                // the first accumulator shares its last columns, the second its first
-                const int j0 = 16 * (BN == 256 && (count & 1) == 0 ? BN / 16 - 1 - i : i);
-                uint32_t v[16];
-                if (ok) {
-                    tmem_load16(acc + j0, v);
-                    tmem_load_wait();
-                } else {
+            if constexpr (sizeof(T) == 4) {
+                // Two warps a quarter, half of the columns each: the first
+                // upwards, the second downwards, so that shared columns come first.
+                constexpr int NC = BN < 32 ? 1 : BN / 32; // chunks of 16 columns
+                const int half = (warp - 4) / 4;
+                const bool active = BN >= 32 || half == 0;
+                float sum[NC][16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
-                }
-                if (BN == 256 && i == kOverlap / 16 - 1 && ok) {
-                    tcgen05_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_free);
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
+                auto column = [&](int i) { return half == 0 ? 16 * i : BN - 16 - 16 * i; };
+                for (int s = 0; s < segments; ++s, ++count) {
+                    const uint32_t acc = next_accumulator();
+                    if (ok && (BN < 256 || half != int((count & 1) ^ 1))) release();
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        uint32_t v[16];
+                        if (ok) {
+                            tmem_load16(acc + (active ? column(i) : 0), v);
+                            tmem_load_wait();
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+                        }
+                        if (BN == 256 && i == kOverlap / 16 - 1 && ok && half == int((count & 1) ^ 1)) release();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[i][j] += __uint_as_float(v[j]);
+                    }
                 }
                 if (a.split > 1) {
-                    if (!ok) break;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
-                } else if (mine) {
+                    for (int i = 0; i < NC; ++i)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (m0 + j0 + j < a.M) put<T>(a, c + (j0 + j) * a.c_stride, __uint_as_float(v[j]) + bias);
+                        for (int j = 0; j < 16; ++j)
+                            if (ok && active) part[(column(i) + j) * kTileP + row] = sum[i][j];
+                } else if (mine && active) {
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        T *to = c + column(i) * a.c_stride;
+                        const int left = int(a.M - m0) - column(i);
+                        if (a.accumulate) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, to += a.c_stride)
+                                if (j < left) sum[i][j] += *to;
+                            to = c + column(i) * a.c_stride;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, to += a.c_stride)
+                            if (j < left) *to = sum[i][j] + bias;
+                    }
                 }
+            } else if (a.tma_out) {
+                // Fragments hold lanes t / 4 and t / 4 + 8 of each 16.
+                float fb[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int64_t k = int64_t(tn) * kTileP + quarter * 32 + 16 * h + 8 * q + lane / 4;
+                        fb[h][q] = k < a.N && a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[k])
+                                                                : 0.f;
+                    }
+                const uint32_t acc = next_accumulator();
+                if (BN < 256 && ok) release();
+                constexpr int CH = BN < 32 ? 1 : BN / 32;  // chunks of 32 columns (a narrow tile: 16 used)
+                const uint32_t out0 = smem_addr(out_smem) + quarter * kOutBuffers * kOutBytes;
+                // row lane % 8 of matrix lane / 8: 16 bytes in the 64-byte swizzle
+                const int r8 = lane % 8, piece = lane / 8;
+                for (int i = 0; i < CH; ++i) {
+                    // the first accumulator shares its last columns, the second its first
+                    const int ch = BN == 256 && (count & 1) == 0 ? CH - 1 - i : i;
+                    uint32_t v[2][16];
+                    if (ok) {
+                        tmem_load_fragments(acc + 32 * ch, v[0]);
+                        tmem_load_fragments(acc + 32 * ch + (16u << 16), v[1]);
+                        tmem_load_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0x7fffffffu;
+                    }
+                    if (BN == 256 && i == 0 && ok) release();
+                    const uint32_t buf = out0 + (i % kOutBuffers) * kOutBytes;
+                    if (lane == 0) tma_store_wait_read<kOutBuffers - 1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t p[2][2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                p[h][q] = pack2<T>(__uint_as_float(v[h][4 * g + 2 * q]) + fb[h][q],
+                                                   __uint_as_float(v[h][4 * g + 2 * q + 1]) + fb[h][q]);
+                        const int r = 8 * g + r8;
+                        store_matrix_transposed(buf + r * 64 + 16 * (piece ^ ((r >> 1) & 3)), p[0][0], p[0][1],
+                                                p[1][0], p[1][1]);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&map_c, buf, tn * kTileP + quarter * 32, int(m0) + 32 * ch);
+                        tma_store_commit();
+                    }
+                }
+                ++count;
+            } else {
+                const uint32_t acc = next_accumulator();
+                if (BN < 256 && ok) release();
+                for (int i = 0; i < BN / 16; ++i) {
+                    const int j0 = 16 * (BN == 256 && (count & 1) == 0 ? BN / 16 - 1 - i : i);
+                    uint32_t v[16];
+                    if (ok) {
+                        tmem_load16(acc + j0, v);
+                        tmem_load_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+                    }
+                    if (BN == 256 && i == kOverlap / 16 - 1 && ok) release();
+                    if (a.split > 1) {
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (m0 + j0 + j < a.M)
+                                put<T>(a, c + (j0 + j) * a.c_stride, __uint_as_float(v[j]) + bias);
+                    }
+                }
+                ++count;
             }
         }
+        if (a.tma_out && lane == 0) tma_store_wait_read<0>();   // shared memory stays until it is read
     }
 
     if (a.split > 1) {                                    // one tile: join the cluster's parts
@@ -331,18 +511,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         cluster_sync();
         int tm, tn;
         tile_at(a, first, &tm, &tn);
-        const int row = threadIdx.x % kTileP, half = threadIdx.x / kTileP;
-        const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
-        if (n < a.N) {
-            const float bias = a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
-            const int j1 = min(BN * (rank + 1) / a.split, int(min(int64_t(BN), a.M - m0)));
-            for (int j = BN * rank / a.split + half; j < j1; j += 2) {
-                float v = 0.f;
-                for (int r = 0; r < a.split; ++r)
-                    v += cluster_load(cluster_addr(stage0 + uint32_t(j * kTileP + row) * 4, r));
-                put<T>(a, static_cast<T *>(a.c) + (m0 + j) * a.c_stride + n, v + bias);
-            }
-        }
+        join_parts<BN, T>(a, stage0, rank, tm, tn);
+        __syncwarp();
         cluster_sync();                                   // the others may still read this CTA's part
     }
     tcgen05_before_sync();
@@ -395,6 +565,19 @@ bool encode(const basp_fp8_matrix *m, int box_rows, CUtensorMap *out) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of 32 x 32 16-bit results of C (16 rows where tiles are that narrow).
+bool encode_out(const MatmulArgs &a, int box_rows, CUtensorMap *out) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(a.N), cuuint64_t(a.M)};
+    const cuuint64_t strides[1] = {cuuint64_t(a.c_stride) * 2};
+    const cuuint32_t box[2] = {32, cuuint32_t(box_rows)};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.c, dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Shape {
     int bn, split;
 };
@@ -428,8 +611,13 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
 template <int BN, class T>
 basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q, int sms,
                           cudaStream_t stream) {
-    CUtensorMap map_p, map_q;
-    if (!encode(p, kTileP, &map_p) || !encode(q, BN, &map_q)) return BASP_ERR_CUDA;
+    CUtensorMap map_p, map_q, map_c = {};
+    // one row of C: its stride is free
+    if (a.M == 1) a.c_stride = ceil_div(a.N, 8) * 8;
+    a.tma_out = sizeof(T) == 2 && a.split == 1 && !a.accumulate && uintptr_t(a.c) % 16 == 0 && a.c_stride % 8 == 0;
+    if (!encode(p, kTileP, &map_p) || !encode(q, BN, &map_q) ||
+        (a.tma_out && !encode_out(a, BN < 32 ? BN : 32, &map_c)))
+        return BASP_ERR_CUDA;
     static std::atomic<bool> ready[64];   // per device; a benign race
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return BASP_ERR_CUDA;
@@ -442,8 +630,8 @@ basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8
         if (dev < 64) ready[dev].store(true, std::memory_order_release);
     }
     const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, sms);
-    return launch(matmul_kernel<BN, T>, dim3(unsigned(ctas)), dim3(256), smem_bytes(BN), a.split, stream, a,
-                  map_p, map_q);
+    return launch(matmul_kernel<BN, T>, dim3(unsigned(ctas)), dim3(cta_threads<T>()), smem_bytes(BN), a.split, stream,
+                  a, map_p, map_q, map_c);
 }
 
 template <class T>
