@@ -53,16 +53,11 @@ __device__ unsigned long long g_timeouts;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 constexpr int kTileP = 128;              // rows of B a tile: the instruction's M
-constexpr int kStageK = kBlock;          // K of a stage, one scale
-constexpr int kScaleSlots = 2;
+constexpr int kStageBlocks = 2;          // blocks of 128 along K of a stage
+constexpr int kScaleSlots = 4;           // scale words on their way, of four blocks each
 
-__host__ __device__ constexpr int stage_bytes(int BN) { return (kTileP + BN) * kStageK; }
-// scales of 128 rows x 4 blocks are 512 bytes; B's 128 rows, then A's BN
-__host__ __device__ constexpr int scale_bytes(int BN) { return 512 + (BN > 128 ? 1024 : 512); }
-__host__ __device__ constexpr int scale_columns(int BN) { return scale_bytes(BN) / 128; }
-
-// K blocks of a segment of a 32-bit result.
-constexpr int kSegment = 16;
+// Stages of a segment of a 32-bit result.
+constexpr int kSegment = 8;
 
 // Drain warps: 32-bit results keep a tile's sums in registers (128 a thread).
 template <class T> __host__ __device__ constexpr int drain_warps() { return sizeof(T) == 4 ? 8 : 4; }
@@ -73,25 +68,29 @@ constexpr int kOutTotal = 4 * kOutBuffers * kOutBytes;
 
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarrierBytes = 512;
-__host__ __device__ constexpr int stages(int BN) {
-    const int n = (kSmemLimit - 1024 - kBarrierBytes - kOutTotal - kScaleSlots * scale_bytes(BN)) / stage_bytes(BN);
-    return n < 8 ? n : 8;
-}
-__host__ __device__ constexpr int smem_bytes(int BN) {
-    return 1024 + stages(BN) * stage_bytes(BN) + kScaleSlots * scale_bytes(BN) + kOutTotal + kBarrierBytes;
-}
 
-// Tensor-memory columns: two accumulators and two scale slots.  Two of 256
-// columns leave no room for the scales in 512, so there the accumulators
-// overlap by 32 columns, which the drain reads first.
-constexpr int kOverlap = 32;
-__host__ __device__ constexpr int acc_offset(int BN) { return BN == 256 ? BN - kOverlap : BN; }
-__host__ __device__ constexpr int scale_base(int BN) { return acc_offset(BN) + BN; }
-__host__ __device__ constexpr int tmem_columns(int BN) {
-    const int need = scale_base(BN) + kScaleSlots * scale_columns(BN);
-    return need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
-}
-static_assert(scale_base(256) + kScaleSlots * scale_columns(256) <= 512, "tensor memory");
+// Sizes of a CTA whose tile is BN rows of A wide; CG = 2: of each CTA of a
+// pair, which loads half of those rows.
+template <int BN, int CG> struct Sizes {
+    static constexpr int kRowsQ = BN / CG;
+    static constexpr int kBlockP = kTileP * kBlock;            // bytes of one block of a stage
+    static constexpr int kBlockQ = kRowsQ * kBlock;
+    static constexpr int kStage = kStageBlocks * (kBlockP + kBlockQ);
+    // scales of 128 rows x 4 blocks are 512 bytes; B's 128 rows, then A's BN
+    static constexpr int kScale = 512 + (BN > 128 ? 1024 : 512);
+    static constexpr int kScaleColumns = kScale / 128;
+    static constexpr int kFixed = 1024 + kOutTotal + kScaleSlots * kScale + kBarrierBytes;
+    static constexpr int kStages = (kSmemLimit - kFixed) / kStage;
+    static constexpr int kSmem = kFixed + kStages * kStage;
+    // Tensor-memory columns: two accumulators and the scale slots.
+    static constexpr int kScaleBase = 2 * BN;
+    static constexpr int kNeed = kScaleBase + kScaleSlots * kScaleColumns;
+    static constexpr int kColumns = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr int kBarriers = 2 * kStages + 3 * kScaleSlots + 5;
+    static_assert(kNeed <= 512, "tensor memory");
+    static_assert(8 * kBarriers + 8 <= kBarrierBytes, "barriers");
+    static_assert(kBlockQ % 1024 == 0, "swizzle");
+};
 
 struct MatmulArgs {
     const uint8_t *sp, *sq;              // scales of B (P side) and A (Q side)
@@ -101,6 +100,7 @@ struct MatmulArgs {
     const void *bias;
     int64_t c_stride;
     int M, N, nk;                        // nk: blocks of 128 along K
+    int ns;                              // stages along K
     int tiles_m, tiles_n, tiles;
     int split;                           // CTAs of a cluster that share a tile
     int accumulate;
@@ -120,11 +120,12 @@ __device__ __forceinline__ void tile_at(const MatmulArgs &a, int t, int *tm, int
 
 struct Waiter {
     volatile int *abort;                 // shared by the CTA
+    template <bool CLUSTER = false>
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, bool give_up_early = true) const {
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
         const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(bar, parity)) {
+        while (!mbar_try_wait<CLUSTER>(bar, parity)) {
             if (give_up_early && *abort) return false;
             if (global_ns() - t0 > kWaitLimitNs) {
                 if (!*abort) atomicAdd(&g_timeouts, 1ull);
@@ -133,6 +134,21 @@ struct Waiter {
             }
         }
         return true;
+    }
+    // for an arrival from another CTA's threads
+    __device__ __forceinline__ bool cluster(uint32_t bar, uint32_t parity) const {
+        return operator()<true>(bar, parity);
+    }
+};
+
+// A ring's place and the parity of its turn, counted instead of divided.
+template <int N> struct Ring {
+    uint32_t at = 0, turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            turn ^= 1;
+        }
     }
 };
 
@@ -173,30 +189,35 @@ __device__ __forceinline__ void join_parts(const MatmulArgs &a, uint32_t part0, 
     }
 }
 
-template <int BN, class T>
+template <int BN, int CG, class T>
 __global__ void __launch_bounds__(cta_threads<T>(), 1)
 matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_p,
               const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c) {
-    constexpr int ST = stages(BN), DW = drain_warps<T>();
+    using S = Sizes<BN, CG>;
+    constexpr int ST = S::kStages, DW = drain_warps<T>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    uint8_t *out_smem = smem + ST * stage_bytes(BN);
+    uint8_t *out_smem = smem + ST * S::kStage;
     uint8_t *scale_smem = out_smem + kOutTotal;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scale_smem + kScaleSlots * scale_bytes(BN));
-    const uint32_t stage0 = smem_addr(smem), scale0 = smem_addr(scale_smem), bar0 = smem_addr(bars);
-    const uint32_t full = bar0, empty = full + 8 * ST, sfull = empty + 8 * ST, sempty = sfull + 8 * kScaleSlots;
-    const uint32_t acc_full = sempty + 8 * kScaleSlots, acc_free = acc_full + 16, drained = acc_free + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * ST + 2 * kScaleSlots + 4);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scale_smem + kScaleSlots * S::kScale);
+    const uint32_t stage0 = smem_addr(smem), scale0 = smem_addr(scale_smem);
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST;
+    const uint32_t sfull = empty + 8 * ST, sempty = sfull + 8 * kScaleSlots;
+    const uint32_t swritten = sempty + 8 * kScaleSlots;
+    const uint32_t acc_full = swritten + 8 * kScaleSlots, acc_free = acc_full + 16, drained = acc_free + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::kBarriers);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(8 * (2 * ST + 2 * kScaleSlots + 4) + 8 <= kBarrierBytes, "barrier space");
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = a.split > 1 ? int(blockIdx.x) % a.split : 0;
-    const int first = int(blockIdx.x) / a.split, step = int(gridDim.x) / a.split;
-    const int kb0 = int(int64_t(a.nk) * rank / a.split), kb1 = int(int64_t(a.nk) * (rank + 1) / a.split);
-    // one accumulator takes `segment` blocks of K; a tile has `segments`
-    const int segment = sizeof(T) == 4 ? kSegment : a.nk;
-    const int segments = (kb1 - kb0 + segment - 1) / segment;
+    // CTAs that share a tile: a pair, or the parts of a split K
+    const int sharing = CG == 2 ? 2 : a.split;
+    const int peer = CG == 2 ? int(blockIdx.x) % 2 : 0;    // 0 leads the pair
+    const int rank = CG == 1 && a.split > 1 ? int(blockIdx.x) % a.split : 0;
+    const int first = int(blockIdx.x) / sharing, step = int(gridDim.x) / sharing;
+    const int s0 = int(int64_t(a.ns) * rank / a.split), s1 = int(int64_t(a.ns) * (rank + 1) / a.split);
+    // one accumulator takes `segment` stages; a tile has `segments`
+    const int segment = sizeof(T) == 4 ? kSegment : a.ns;
+    const int segments = (s1 - s0 + segment - 1) / segment;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&map_p);
@@ -206,211 +227,296 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            mbar_init(sfull + 8 * s, 1);
+            mbar_init(sfull + 8 * s, CG);
             mbar_init(sempty + 8 * s, 1);
+            mbar_init(swritten + 8 * s, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_full + 8, 1);
-        mbar_init(acc_free, DW);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + 8 * s, 1);
+            mbar_init(acc_free + 8 * s, CG * DW);
+        }
         mbar_init(drained, 1);
         *abort = 0;
         fence_mbar_init();
         fence_async_shared();
     }
-    if (warp == 3) tmem_alloc(smem_addr(tmem_slot), tmem_columns(BN));
+    if (warp == 3) tmem_alloc<CG>(smem_addr(tmem_slot), S::kColumns);
     tcgen05_before_sync();
     __syncthreads();
+    if (CG == 2) cluster_sync();                          // the other CTA's barriers are there
     tcgen05_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dependency();
+    // the leader's barriers that the other CTA's loads, scales and drains reach
+    const uint32_t lead_full = CG == 2 ? cluster_addr(full, 0) : full;
+    const uint32_t lead_sfull = CG == 2 ? cluster_addr(sfull, 0) : sfull;
+    const uint32_t lead_acc_free = CG == 2 ? cluster_addr(acc_free, 0) : acc_free;
+    auto arrive = [](uint32_t bar) {
+        if constexpr (CG == 2) mbar_arrive_cluster(bar);
+        else mbar_arrive(bar);
+    };
     const Waiter wait{abort};
 
-    if (warp == 0) {
-        if (lane == 0) {                                  // loads
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = first; t < a.tiles && ok; t += step) {
-                int tm, tn;
-                tile_at(a, t, &tm, &tn);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % ST, use = it / ST;
-                    ok = wait(empty + 8 * s, (use & 1) ^ 1);
-                    if (!ok) break;
-                    mbar_expect_tx(full + 8 * s, stage_bytes(BN));
-                    tma_load_2d(stage0 + s * stage_bytes(BN), &map_p, kb * kStageK, tn * kTileP, full + 8 * s);
-                    tma_load_2d(stage0 + s * stage_bytes(BN) + kTileP * kStageK, &map_q, kb * kStageK, tm * BN,
-                                full + 8 * s);
-                }
-            }
-            if (!ok)                                      // copies in flight end before the CTA does
-                for (uint32_t j = it < uint32_t(ST) ? 0 : it - ST; j < it; ++j)
-                    wait(full + 8 * (j % ST), (j / ST) & 1, false);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {                                  // products
-            uint32_t it = 0, group = 0, count = 0;
-            bool ok = true;
-            for (int t = first; t < a.tiles && ok; t += step) {
-                uint32_t slot = 0, acc = 0;
-                int left = 0;                             // blocks left of the segment
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const bool fresh = left == 0;
-                    if (fresh) {
-                        left = segment;
-                        acc = tmem + (count & 1) * acc_offset(BN);
-                        if (count > 0) ok = wait(acc_free, (count - 1) & 1);
-                        if (!ok) break;
-                        tcgen05_after_sync();
-                    }
-                    if (kb == kb0 || kb % 4 == 0) {       // scales of the next four blocks
-                        slot = group % kScaleSlots;
-                        ok = wait(sfull + 8 * slot, (group / kScaleSlots) & 1);
-                        if (!ok) break;
-                        tcgen05_after_sync();
-                        const uint32_t src = scale0 + slot * scale_bytes(BN);
-                        const uint32_t dst = tmem + scale_base(BN) + slot * scale_columns(BN);
-#pragma unroll
-                        for (int i = 0; i < scale_bytes(BN) / 512; ++i)
-                            tmem_copy_scales(dst + 4 * i, scale_desc(src + 512 * i));
-                        ++group;
-                    }
-                    const uint32_t s = it % ST;
-                    ok = wait(full + 8 * s, (it / ST) & 1);
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    const uint64_t dp = operand_desc(stage0 + s * stage_bytes(BN));
-                    const uint64_t dq = operand_desc(stage0 + s * stage_bytes(BN) + kTileP * kStageK);
-                    const uint32_t sf = tmem + scale_base(BN) + slot * scale_columns(BN);
-                    const uint32_t idesc = mma_desc(kTileP, BN) | mma_scale_ids(kb & 3);
-#pragma unroll
-                    for (int k = 0; k < kStageK / 32; ++k)
-                        mma_mxf8(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
-                    mma_commit(empty + 8 * s);
-                    if (kb + 1 == kb1 || kb % 4 == 3) mma_commit(sempty + 8 * slot);
-                    if (--left == 0 || kb + 1 == kb1) {
-                        mma_commit(acc_full + 8 * (count & 1));
-                        ++count;
-                    }
-                }
-            }
-            if (!ok) {                                    // products in flight end before the CTA does
-                mma_commit(drained);
-                wait(drained, 0, false);
-            }
-        }
-    } else if (warp == 2) {                               // scales
-        uint32_t group = 0;
+    if (warp == 0) {                                      // loads
+        Ring<ST> ring;
+        uint32_t issued = 0;
         bool ok = true;
         for (int t = first; t < a.tiles && ok; t += step) {
             int tm, tn;
             tile_at(a, t, &tm, &tn);
-            for (int g = kb0 / 4; 4 * g < kb1; ++g, ++group) {
-                uint4 w[scale_bytes(BN) / 512];
+            const int p = (tn * CG + peer) * kTileP, q = tm * BN + peer * S::kRowsQ;
+            for (int s = s0; s < s1; ++s, ring.next(), ++issued) {
+                ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t to = stage0 + ring.at * S::kStage, bar = full + 8 * ring.at;
+                    const int kb = s * kStageBlocks, blocks = min(kStageBlocks, a.nk - kb);
+                    // the leader's barrier counts both CTAs' bytes
+                    if (peer == 0) mbar_expect_tx(bar, CG * blocks * (S::kBlockP + S::kBlockQ));
 #pragma unroll
-                for (int i = 0; i < scale_bytes(BN) / 512; ++i) {
-                    uint32_t r[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int in_tile = (i > 0 ? (i - 1) * 128 : 0) + 32 * j + lane;
-                        const int64_t row = i == 0 ? int64_t(tn) * kTileP + in_tile : int64_t(tm) * BN + in_tile;
-                        r[j] = 0x7f7f7f7fu;               // rows that do not exist: values are 0
-                        if (i == 0) {
-                            if (row < a.N)
-                                r[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                                    a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g)));
-                        } else if (in_tile < BN && row < a.M) {
-                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                                a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g)));
+                    for (int i = 0; i < kStageBlocks; ++i) {
+                        if (i >= blocks) break;
+                        const uint32_t to_p = to + i * S::kBlockP;
+                        const uint32_t to_q = to + kStageBlocks * S::kBlockP + i * S::kBlockQ;
+                        const int x = (kb + i) * kBlock;
+                        if constexpr (CG == 2) {
+                            tma_load_2d_pair(to_p, &map_p, x, p, lead_full + 8 * ring.at);
+                            tma_load_2d_pair(to_q, &map_q, x, q, lead_full + 8 * ring.at);
+                        } else {
+                            tma_load_2d(to_p, &map_p, x, p, bar);
+                            tma_load_2d(to_q, &map_q, x, q, bar);
                         }
                     }
-                    w[i] = make_uint4(r[0], r[1], r[2], r[3]);
                 }
-                const uint32_t slot = group % kScaleSlots;
-                ok = wait(sempty + 8 * slot, ((group / kScaleSlots) & 1) ^ 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < scale_bytes(BN) / 512; ++i)
-                    reinterpret_cast<uint4 *>(scale_smem + slot * scale_bytes(BN) + 512 * i)[lane] = w[i];
-                fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sfull + 8 * slot);
             }
         }
+        // A CTA ends after the last arrival at its barriers, and after its
+        // copies in flight (a pair's count at the leader).
+        const uint32_t open = issued < uint32_t(ST) ? issued : ST;
+        for (uint32_t j = issued - open; j < issued; ++j) {
+            if (CG == 2 && ok) wait(empty + 8 * (j % ST), (j / ST) & 1);
+            if (!ok && peer == 0) wait(full + 8 * (j % ST), (j / ST) & 1, false);
+        }
+    } else if (warp == 1) {
+        if (peer == 0) {                                  // products
+            Ring<ST> ring;
+            Ring<kScaleSlots> words;
+            Ring<2> accs;
+            uint32_t count = 0;
+            bool ok = true, ready = false;
+            for (int t = first; t < a.tiles && ok; t += step) {
+                int left = 0;                             // stages left of the segment
+                for (int s = s0; s < s1; ++s) {
+                    const bool fresh = left == 0;
+                    const bool scales = s == s0 || s % 2 == 0;   // a new word: four blocks
+                    if (fresh) {
+                        left = segment;
+                        // drained of the sum before the last
+                        if (count >= 2) ok = wait.cluster(acc_free + 8 * accs.at, accs.turn ^ 1);
+                    }
+                    if (scales) ok = ok && wait.cluster(sfull + 8 * words.at, words.turn);
+                    if (!ready) ok = ok && wait(full + 8 * ring.at, ring.turn);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    --left;
+                    const bool last = left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % 2 == 1;
+                    if (elect_one()) {
+                        const uint32_t sf = tmem + S::kScaleBase + words.at * S::kScaleColumns;
+                        if (scales) {
+                            const uint32_t src = scale0 + words.at * S::kScale;
+#pragma unroll
+                            for (int i = 0; i < S::kScale / 512; ++i)
+                                tmem_copy_scales<CG>(sf + 4 * i, scale_desc(src + 512 * i));
+                        }
+                        const uint32_t acc = tmem + accs.at * BN;
+                        const uint32_t at = stage0 + ring.at * S::kStage;
+                        const int blocks = min(kStageBlocks, a.nk - s * kStageBlocks);
+#pragma unroll
+                        for (int i = 0; i < kStageBlocks; ++i) {
+                            if (i >= blocks) break;
+                            const uint64_t dp = operand_desc(at + i * S::kBlockP);
+                            const uint64_t dq = operand_desc(at + kStageBlocks * S::kBlockP + i * S::kBlockQ);
+                            const uint32_t idesc =
+                                mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks + i);
+#pragma unroll
+                            for (int k = 0; k < kBlock / 32; ++k)
+                                mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4,
+                                             !fresh || i > 0 || k > 0);
+                        }
+                        mma_commit<CG>(empty + 8 * ring.at);
+                        if (word_done) mma_commit<CG>(sempty + 8 * words.at);
+                        if (last) mma_commit<CG>(acc_full + 8 * accs.at);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    ready = mbar_try_wait<false>(full + 8 * ring.at, ring.turn);   // known by the time it is asked
+                    if (word_done) words.next();
+                    if (last) {
+                        left = 0;
+                        ++count;
+                        accs.next();
+                    }
+                }
+            }
+            if (!ok) {                                    // products in flight end before the CTA does
+                __syncwarp();
+                if (elect_one()) mma_commit<CG>(drained);
+                __syncwarp();
+                wait(drained, 0, false);
+            }
+        }
+    } else if (warp == 2) {                               // scales
+        constexpr int A = S::kScale / 512;                // groups of 128 rows
+        Ring<kScaleSlots> words;
+        uint32_t issued = 0;
+        bool ok = true;
+        // A lane's words of rows lane, lane + 32, ... of B's 128 and of A's.
+        auto load = [&](int tm, int tn, int g, uint4 (&w)[A]) {
+#pragma unroll
+            for (int i = 0; i < A; ++i) {
+                uint32_t r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int in_tile = (i > 0 ? (i - 1) * 128 : 0) + 32 * j + lane;
+                    r[j] = 0x7f7f7f7fu;                   // rows that do not exist: values are 0
+                    if (i == 0) {
+                        const int64_t row = (int64_t(tn) * CG + peer) * kTileP + in_tile;
+                        if (row < a.N)
+                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
+                                a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g)));
+                    } else {
+                        const int64_t row = int64_t(tm) * BN + in_tile;
+                        if (in_tile < BN && row < a.M)
+                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
+                                a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g)));
+                    }
+                }
+                w[i] = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+        };
+        // Words in order: those of one tile, then of the CTA's next.  kAhead of
+        // them are on their way in registers: beside the tiles' traffic a load
+        // takes longer than the products of four blocks.
+        constexpr int kAhead = 4;
+        const int g0 = s0 / 2, g1 = (s1 + 1) / 2;
+        int t = first, g = g0, tm = 0, tn = 0;
+        if (t < a.tiles) tile_at(a, t, &tm, &tn);
+        uint4 w[kAhead][A];
+        bool have[kAhead];
+        auto fetch = [&](uint4 (&to)[A]) {
+            if (t >= a.tiles) return false;
+            load(tm, tn, g, to);
+            if (++g == g1) {
+                g = g0;
+                t += step;
+                if (t < a.tiles) tile_at(a, t, &tm, &tn);
+            }
+            return true;
+        };
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) have[d] = fetch(w[d]);
+        while (have[0] && ok) {
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+                if (!have[d] || !ok) break;
+                ok = __all_sync(0xffffffffu, wait(sempty + 8 * words.at, words.turn ^ 1));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < A; ++i)
+                    reinterpret_cast<uint4 *>(scale_smem + words.at * S::kScale + 512 * i)[lane] = w[d][i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(swritten + 8 * words.at);
+                words.next();
+                ++issued;
+                have[d] = fetch(w[d]);
+            }
+        }
+        if (CG == 2 && ok)                                // the last arrivals, as above
+            for (uint32_t j = issued < kScaleSlots ? 0 : issued - kScaleSlots; j < issued; ++j)
+                wait(sempty + 8 * (j % kScaleSlots), (j / kScaleSlots) & 1);
+    } else if (warp == 3) {                               // scales, on to the products
+        // A warp of its own: a fence waits for the loads that its warp has in
+        // flight, and the scales' are four words ahead.
+        Ring<kScaleSlots> words;
+        bool ok = true;
+        for (int t = first; t < a.tiles && ok; t += step)
+            for (int g = s0 / 2; g < (s1 + 1) / 2; ++g, words.next()) {
+                ok = __all_sync(0xffffffffu, wait(swritten + 8 * words.at, words.turn));
+                if (!ok) break;
+                fence_async_shared();
+                if (lane == 0) arrive(lead_sfull + 8 * words.at);
+            }
     } else if (warp >= 4) {                               // drain
         const int quarter = warp % 4, row = quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         float *part = reinterpret_cast<float *>(smem);     // [BN][128], split only
-        uint32_t count = 0;
+        Ring<2> accs;
         bool ok = true;
         auto next_accumulator = [&]() {
-            const bool arrived = ok && wait(acc_full + 8 * (count & 1), (count >> 1) & 1);
-            ok = __all_sync(0xffffffffu, arrived);
+            ok = __all_sync(0xffffffffu, ok && wait(acc_full + 8 * accs.at, accs.turn));
             tcgen05_after_sync();
-            return tmem + lanes + (count & 1) * acc_offset(BN);
+            return tmem + lanes + accs.at * BN;
         };
-        // The next products may write the other accumulator: what this warp
-        // reads of it, or of the columns it shares, is behind it.
+        // what this warp reads of the accumulator is behind it
         auto release = [&]() {
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_free);
+            if (ok && lane == 0) arrive(lead_acc_free + 8 * accs.at);
+            accs.next();
         };
         for (int t = first; t < a.tiles; t += step) {
             int tm, tn;
             tile_at(a, t, &tm, &tn);
-            const int64_t n = int64_t(tn) * kTileP + row, m0 = int64_t(tm) * BN;
+            const int64_t n0 = (int64_t(tn) * CG + peer) * kTileP, n = n0 + row, m0 = int64_t(tm) * BN;
             const bool mine = n < a.N;
             T *c = static_cast<T *>(a.c) + m0 * a.c_stride + n;
             const float bias = mine && a.bias != nullptr && a.split == 1
                                    ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
             if constexpr (sizeof(T) == 4) {
-                // Two warps a quarter, half of the columns each: the first
-                // upwards, the second downwards, so that shared columns come first.
+                // Two warps a quarter, half of the columns each.
                 constexpr int NC = BN < 32 ? 1 : BN / 32; // chunks of 16 columns
-                const int half = (warp - 4) / 4;
+                const int half = (warp - 4) / 4, j0 = BN < 32 ? 0 : half * (BN / 2);
                 const bool active = BN >= 32 || half == 0;
                 float sum[NC][16];
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
-                auto column = [&](int i) { return half == 0 ? 16 * i : BN - 16 - 16 * i; };
-                for (int s = 0; s < segments; ++s, ++count) {
+                for (int s = 0; s < segments; ++s) {
                     const uint32_t acc = next_accumulator();
-                    if (ok && (BN < 256 || half != int((count & 1) ^ 1))) release();
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
                         uint32_t v[16];
                         if (ok) {
-                            tmem_load16(acc + (active ? column(i) : 0), v);
+                            tmem_load16(acc + j0 + 16 * i, v);
                             tmem_load_wait();
                         } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
                         }
-                        if (BN == 256 && i == kOverlap / 16 - 1 && ok && half == int((count & 1) ^ 1)) release();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            sum[i][j] += __uint_as_float(v[j]);
+                        for (int j = 0; j < 16; ++j) sum[i][j] += __uint_as_float(v[j]);
                     }
+                    release();
                 }
                 if (a.split > 1) {
 #pragma unroll
                     for (int i = 0; i < NC; ++i)
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (ok && active) part[(column(i) + j) * kTileP + row] = sum[i][j];
+                            if (ok && active) part[(j0 + 16 * i + j) * kTileP + row] = sum[i][j];
                 } else if (mine && active) {
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        T *to = c + column(i) * a.c_stride;
-                        const int left = int(a.M - m0) - column(i);
+                        T *to = c + (j0 + 16 * i) * a.c_stride;
+                        const int left = int(a.M - m0) - j0 - 16 * i;
                         if (a.accumulate) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j, to += a.c_stride)
                                 if (j < left) sum[i][j] += *to;
-                            to = c + column(i) * a.c_stride;
+                            to = c + (j0 + 16 * i) * a.c_stride;
                         }
 #pragma unroll
                         for (int j = 0; j < 16; ++j, to += a.c_stride)
@@ -424,19 +530,16 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int64_t k = int64_t(tn) * kTileP + quarter * 32 + 16 * h + 8 * q + lane / 4;
+                        const int64_t k = n0 + quarter * 32 + 16 * h + 8 * q + lane / 4;
                         fb[h][q] = k < a.N && a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[k])
                                                                 : 0.f;
                     }
                 const uint32_t acc = next_accumulator();
-                if (BN < 256 && ok) release();
                 constexpr int CH = BN < 32 ? 1 : BN / 32;  // chunks of 32 columns (a narrow tile: 16 used)
                 const uint32_t out0 = smem_addr(out_smem) + quarter * kOutBuffers * kOutBytes;
                 // row lane % 8 of matrix lane / 8: 16 bytes in the 64-byte swizzle
                 const int r8 = lane % 8, piece = lane / 8;
-                for (int i = 0; i < CH; ++i) {
-                    // the first accumulator shares its last columns, the second its first
-                    const int ch = BN == 256 && (count & 1) == 0 ? CH - 1 - i : i;
+                for (int ch = 0; ch < CH; ++ch) {
                     uint32_t v[2][16];
                     if (ok) {
                         tmem_load_fragments(acc + 32 * ch, v[0]);
@@ -446,8 +549,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0x7fffffffu;
                     }
-                    if (BN == 256 && i == 0 && ok) release();
-                    const uint32_t buf = out0 + (i % kOutBuffers) * kOutBytes;
+                    if (ch + 1 == CH) release();
+                    const uint32_t buf = out0 + (ch % kOutBuffers) * kOutBytes;
                     if (lane == 0) tma_store_wait_read<kOutBuffers - 1>();
                     __syncwarp();
 #pragma unroll
@@ -466,16 +569,14 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&map_c, buf, tn * kTileP + quarter * 32, int(m0) + 32 * ch);
-                        tma_store_commit();
+                        if (n0 + quarter * 32 < a.N && m0 + 32 * ch < a.M)
+                            tma_store_2d(&map_c, buf, int(n0) + quarter * 32, int(m0) + 32 * ch);
+                        tma_store_commit();               // also of nothing: buffers are counted in groups
                     }
                 }
-                ++count;
             } else {
                 const uint32_t acc = next_accumulator();
-                if (BN < 256 && ok) release();
-                for (int i = 0; i < BN / 16; ++i) {
-                    const int j0 = 16 * (BN == 256 && (count & 1) == 0 ? BN / 16 - 1 - i : i);
+                for (int j0 = 0; j0 < BN; j0 += 16) {
                     uint32_t v[16];
                     if (ok) {
                         tmem_load16(acc + j0, v);
@@ -484,11 +585,11 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
                     }
-                    if (BN == 256 && i == kOverlap / 16 - 1 && ok) release();
+                    if (j0 + 16 == BN) release();
                     if (a.split > 1) {
-                        if (!ok) break;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
+                        for (int j = 0; j < 16; ++j)
+                            if (ok) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
                     } else if (mine) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -496,13 +597,12 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                                 put<T>(a, c + (j0 + j) * a.c_stride, __uint_as_float(v[j]) + bias);
                     }
                 }
-                ++count;
             }
         }
         if (a.tma_out && lane == 0) tma_store_wait_read<0>();   // shared memory stays until it is read
     }
 
-    if (a.split > 1) {                                    // one tile: join the cluster's parts
+    if (CG == 1 && a.split > 1) {                         // one tile: join the cluster's parts
         __syncthreads();
         if (*abort)                                       // nothing is in flight any more
             for (int i = threadIdx.x; i < BN * kTileP; i += blockDim.x)
@@ -517,8 +617,9 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     }
     tcgen05_before_sync();
     __syncthreads();
+    if (CG == 2) cluster_sync();                          // nothing of the pair's reaches the other any more
     tcgen05_after_sync();
-    if (warp == 3) tmem_free(tmem, tmem_columns(BN));
+    if (warp == 3) tmem_free<CG>(tmem, S::kColumns);
 }
 
 // C = bias, zero, or itself where there is nothing to sum over.
@@ -558,7 +659,7 @@ bool encode(const basp_fp8_matrix *m, int box_rows, CUtensorMap *out) {
     if (fn == nullptr) return false;
     const cuuint64_t dims[2] = {cuuint64_t(m->cols), cuuint64_t(m->rows)};
     const cuuint64_t strides[1] = {cuuint64_t(m->pitch)};
-    const cuuint32_t box[2] = {kStageK, cuuint32_t(box_rows)};
+    const cuuint32_t box[2] = {kBlock, cuuint32_t(box_rows)};
     const cuuint32_t elem[2] = {1, 1};
     return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m->data, dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -579,59 +680,64 @@ bool encode_out(const MatmulArgs &a, int box_rows, CUtensorMap *out) {
 }
 
 struct Shape {
-    int bn, split;
+    int bn, pair, split;
 };
 
-// The tile width (along A's rows) and the number of CTAs that split K with
-// the least estimated time, in SM cycles: rounds of CTAs over the SMs, each
-// paying for its stages (tensor cores or loads, whichever takes longer) and
-// for a start and a drain that no stage hides.
+// The tile (its width along A's rows, one CTA or a pair) and the number of
+// CTAs that split K with the least estimated time, in SM cycles: rounds of
+// tiles over the SMs, each paying for its stages (tensor cores, or loads at
+// what an SM gets from L2, 64 bytes a cycle) and for a start and a drain that
+// no stage hides.
 Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
-    Shape best = {256, 1};
+    Shape best = {128, 0, 1};
     double best_cost = 1e300;
-    for (int bn = 16; bn <= 256; bn *= 2) {
-        if (bn > 16 && bn / 2 >= M) break;
-        const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP);
-        for (int split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (split > nk || tiles * split > sms)) break;
-            const double stage = std::max(2.0 * bn, stage_bytes(bn) / 64.0);
-            const double k = double(ceil_div(nk, split)) * stage;
-            const double drain = 6.0 * bn / split + (split > 1 ? 2000 : 0);
-            const double rounds = double(ceil_div(tiles * split, sms));
-            const double cost = 3000 + rounds * k + (rounds - 1) * 300 + drain;
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = {bn, split};
-            }
+    auto consider = [&](int bn, int pair, int split) {
+        const int cg = 1 + pair;
+        const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP * cg);
+        if (split > 1 && (split > ceil_div(nk, kStageBlocks) || tiles * split > sms)) return;
+        const double block = std::max(2.0 * bn, (kTileP + bn / cg) * kBlock / 64.0);
+        const double k = double(ceil_div(nk, split)) * block;
+        const double drain = 6.0 * bn / split + (split > 1 ? 2000 : 0);
+        const double rounds = double(ceil_div(tiles * split * cg, sms));
+        const double cost = 3000 + rounds * k + (rounds - 1) * 300 + drain;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = {bn, pair, split};
         }
+    };
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        if (bn > 16 && bn / 2 >= M) break;
+        for (int split = 1; split <= 8; split *= 2) consider(bn, 0, split);
     }
+    if (M > 128)
+        for (int bn : {224, 192}) consider(bn, 1, 1);
     return best;
 }
 
-template <int BN, class T>
+template <int BN, int CG, class T>
 basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q, int sms,
                           cudaStream_t stream) {
     CUtensorMap map_p, map_q, map_c = {};
     // one row of C: its stride is free
     if (a.M == 1) a.c_stride = ceil_div(a.N, 8) * 8;
     a.tma_out = sizeof(T) == 2 && a.split == 1 && !a.accumulate && uintptr_t(a.c) % 16 == 0 && a.c_stride % 8 == 0;
-    if (!encode(p, kTileP, &map_p) || !encode(q, BN, &map_q) ||
+    if (!encode(p, kTileP, &map_p) || !encode(q, BN / CG, &map_q) ||
         (a.tma_out && !encode_out(a, BN < 32 ? BN : 32, &map_c)))
         return BASP_ERR_CUDA;
     static std::atomic<bool> ready[64];   // per device; a benign race
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return BASP_ERR_CUDA;
     if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(matmul_kernel<BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem_bytes(BN)) != cudaSuccess) {
+        if (cudaFuncSetAttribute(matmul_kernel<BN, CG, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Sizes<BN, CG>::kSmem) != cudaSuccess) {
             cudaGetLastError();
             return BASP_ERR_CUDA;
         }
         if (dev < 64) ready[dev].store(true, std::memory_order_release);
     }
-    const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, sms);
-    return launch(matmul_kernel<BN, T>, dim3(unsigned(ctas)), dim3(cta_threads<T>()), smem_bytes(BN), a.split, stream,
-                  a, map_p, map_q, map_c);
+    const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles * CG, sms / CG * CG);
+    return launch(matmul_kernel<BN, CG, T>, dim3(unsigned(ctas)), dim3(cta_threads<T>()), Sizes<BN, CG>::kSmem,
+                  a.split * CG, stream, a, map_p, map_q, map_c);
 }
 
 template <class T>
@@ -644,18 +750,20 @@ basp_status run(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q
     }
     const int sms = sm_count();
     const Shape s = pick_shape(a.M, a.N, a.nk, sms);
-    const int64_t tiles = ceil_div(a.M, s.bn) * ceil_div(a.N, kTileP);
-    if (tiles > (int64_t(1) << 30)) return BASP_ERR_TOO_LARGE;
     a.tiles_m = int(ceil_div(a.M, s.bn));
-    a.tiles_n = int(ceil_div(a.N, kTileP));
+    a.tiles_n = int(ceil_div(a.N, kTileP * (1 + s.pair)));
+    const int64_t tiles = int64_t(a.tiles_m) * a.tiles_n;
+    if (tiles > (int64_t(1) << 30)) return BASP_ERR_TOO_LARGE;
     a.tiles = int(tiles);
     a.split = s.split;
+    a.ns = int(ceil_div(a.nk, kStageBlocks));
     switch (s.bn) {
-        case 16: return launch_matmul<16, T>(a, p, q, sms, stream);
-        case 32: return launch_matmul<32, T>(a, p, q, sms, stream);
-        case 64: return launch_matmul<64, T>(a, p, q, sms, stream);
-        case 128: return launch_matmul<128, T>(a, p, q, sms, stream);
-        default: return launch_matmul<256, T>(a, p, q, sms, stream);
+        case 16: return launch_matmul<16, 1, T>(a, p, q, sms, stream);
+        case 32: return launch_matmul<32, 1, T>(a, p, q, sms, stream);
+        case 64: return launch_matmul<64, 1, T>(a, p, q, sms, stream);
+        case 128: return launch_matmul<128, 1, T>(a, p, q, sms, stream);
+        case 192: return launch_matmul<192, 2, T>(a, p, q, sms, stream);
+        default: return launch_matmul<224, 2, T>(a, p, q, sms, stream);
     }
 }
 
