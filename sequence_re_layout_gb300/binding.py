@@ -368,75 +368,88 @@ def basp_seq2head_noalloc(layout, q, k, v, q_out, k_out, v_out, stream=None):
 
 # ---- the 8-bit projections (include/basp_fp8.h) ----------------------------
 
-_FP8_DTYPES = {}
+# Calls here take microseconds on the GPU, so the checks are kept to a few
+# attribute reads a tensor; each refuses with ValueError before the C call.
+
+_FP8_DTYPES = {}       # torch element type -> basp_dtype
+_F32 = None            # torch.float32
+
+
+def _fp8_types():
+    global _F32
+    import torch
+    _FP8_DTYPES.update({torch.bfloat16: BASP_DTYPE_BF16, torch.float16: BASP_DTYPE_FP16,
+                        torch.float32: BASP_DTYPE_FP32})
+    _F32 = torch.float32
 
 
 def fp8_dtype_code(dtype) -> int:
     """basp_dtype of a torch element type that the 8-bit operators take or
     give (bfloat16, float16, float32)."""
     if not _FP8_DTYPES:
-        import torch
-        _FP8_DTYPES.update({torch.bfloat16: BASP_DTYPE_BF16, torch.float16: BASP_DTYPE_FP16,
-                            torch.float32: BASP_DTYPE_FP32})
-    try:
-        return _FP8_DTYPES[dtype]
-    except KeyError:
-        raise ValueError("element type must be bfloat16, float16 or float32, got %s" % (dtype,)) from None
+        _fp8_types()
+    code = _FP8_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("element type must be bfloat16, float16 or float32, got %s" % (dtype,))
+    return code
 
 
-def _rows(x, where, name, rows, cols, dtype, cur):
-    """(address, row stride) of a [rows, cols] CUDA matrix with unit column
-    stride and the given element type; (None, 0) for None."""
+def _wrong(x, where, name, shape, dtype, cur):
+    if x.get_device() != cur:
+        what = "must be on the current device cuda:%d, it is on %s" % (cur, x.device)
+    elif x.dtype != dtype:
+        what = "must be %s, got %s" % (dtype, x.dtype)
+    elif tuple(x.shape) != shape:
+        what = "must have shape %s, got %s" % (shape, tuple(x.shape))
+    else:
+        what = "must have its columns next to each other, got strides %s" % (tuple(x.stride()),)
+    raise ValueError("%s: %s %s" % (where, name, what))
+
+
+def _rows(x, where, name, shape, dtype, cur):
+    """(address, row stride) of a CUDA matrix of this (rows, cols) with unit
+    column stride and the given element type; (None, 0) for None."""
     if x is None:
         return None, 0
-    if not x.is_cuda or x.device.index != cur:
-        raise ValueError("%s: %s must be on the current device cuda:%d, it is on %s"
-                         % (where, name, cur, x.device))
-    if x.dtype != dtype:
-        raise ValueError("%s: %s must be %s, got %s" % (where, name, dtype, x.dtype))
-    if tuple(x.shape) != (rows, cols):
-        raise ValueError("%s: %s must have shape %s, got %s"
-                         % (where, name, (rows, cols), tuple(x.shape)))
+    if x.get_device() != cur or x.dtype != dtype or x.shape != shape:
+        _wrong(x, where, name, shape, dtype, cur)
     s0, s1 = x.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError("%s: the columns of %s must be next to each other" % (where, name))
-    return x.data_ptr() or None, s0 if rows > 1 else cols
+    if s1 != 1 and shape[1] > 1:
+        _wrong(x, where, name, shape, dtype, cur)
+    # the stride of a single row says nothing
+    return x.data_ptr() or None, s0 if shape[0] > 1 else shape[1]
 
 
 def _vector(x, where, name, n, dtype, cur):
     """Address of a contiguous CUDA vector of n elements, or None."""
     if x is None:
         return None
-    if not x.is_cuda or x.device.index != cur:
-        raise ValueError("%s: %s must be on the current device cuda:%d, it is on %s"
-                         % (where, name, cur, x.device))
-    if x.dtype != dtype:
-        raise ValueError("%s: %s must be %s, got %s" % (where, name, dtype, x.dtype))
-    if x.dim() != 1 or x.shape[0] != n or not x.is_contiguous():
-        raise ValueError("%s: %s must be a contiguous vector of %d" % (where, name, n))
+    if x.get_device() != cur or x.dtype != dtype or x.shape != (n,) or (n > 1 and x.stride() != (1,)):
+        _wrong(x, where, name, (n,), dtype, cur)
     return x.data_ptr() or None
 
 
 def _2d(x, where, name):
     if x.dim() != 2:
         raise ValueError("%s: %s must have two dimensions, got shape %s" % (where, name, tuple(x.shape)))
-    return x.shape
+    return tuple(x.shape)
 
 
 def basp_rmsnorm(x, residual, weight, eps, h=None, y=None, q=None, rstd=None, stream=None):
     """Residual addition + root-mean-square norm; see ``basp_fp8.h``.  ``q`` is
     a :class:`basp_fp8_matrix`, everything else a tensor or None."""
-    import torch
     w = "basp_rmsnorm"
-    rows, cols = _2d(x, w, "x")
-    code, cur = fp8_dtype_code(x.dtype), _current_device()
-    wcode = fp8_dtype_code(weight.dtype)
-    _check(load_library().basp_rmsnorm(
-        code, rows, cols, *_rows(x, w, "x", rows, cols, x.dtype, cur),
-        *_rows(residual, w, "residual", rows, cols, x.dtype, cur),
-        _vector(weight, w, "weight", cols, weight.dtype, cur), wcode, eps,
-        *_rows(h, w, "h", rows, cols, x.dtype, cur), *_rows(y, w, "y", rows, cols, x.dtype, cur),
-        q, _vector(rstd, w, "rstd", rows, torch.float32, cur), _stream(stream)), w)
+    shape, t = _2d(x, w, "x"), x.dtype
+    code, wcode, cur = fp8_dtype_code(t), fp8_dtype_code(weight.dtype), _current_device()
+    xp, xs = _rows(x, w, "x", shape, t, cur)
+    rp, rs = _rows(residual, w, "residual", shape, t, cur)
+    hp, hs = _rows(h, w, "h", shape, t, cur)
+    yp, ys = _rows(y, w, "y", shape, t, cur)
+    st = load_library().basp_rmsnorm(
+        code, shape[0], shape[1], xp, xs, rp, rs, _vector(weight, w, "weight", shape[1], weight.dtype, cur),
+        wcode, eps, hp, hs, yp, ys, q, _vector(rstd, w, "rstd", shape[0], _F32, cur), _stream(stream))
+    if st:
+        _check(st, w)
 
 
 def basp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
@@ -445,39 +458,52 @@ def basp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
 
 def basp_rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight=None, workspace=None, stream=None):
     """Gradient of :func:`basp_rmsnorm`; see ``basp_fp8.h``."""
-    import torch
     w = "basp_rmsnorm_backward"
-    rows, cols = _2d(dy, w, "dy")
-    code, cur = fp8_dtype_code(dy.dtype), _current_device()
-    wcode = fp8_dtype_code(weight.dtype)
-    _check(load_library().basp_rmsnorm_backward(
-        code, rows, cols, *_rows(dy, w, "dy", rows, cols, dy.dtype, cur),
-        *_rows(h, w, "h", rows, cols, dy.dtype, cur), _vector(rstd, w, "rstd", rows, torch.float32, cur),
-        _vector(weight, w, "weight", cols, weight.dtype, cur), wcode,
-        *_rows(dh, w, "dh", rows, cols, dy.dtype, cur), *_rows(dx, w, "dx", rows, cols, dy.dtype, cur),
-        _vector(dweight, w, "dweight", cols, torch.float32, cur),
-        _tptr(workspace, None, w, "workspace", "device", cur), _nbytes(workspace), _stream(stream)), w)
+    shape, t = _2d(dy, w, "dy"), dy.dtype
+    code, wcode, cur = fp8_dtype_code(t), fp8_dtype_code(weight.dtype), _current_device()
+    yp, ys = _rows(dy, w, "dy", shape, t, cur)
+    hp, hs = _rows(h, w, "h", shape, t, cur)
+    dp, ds = _rows(dh, w, "dh", shape, t, cur)
+    xp, xs = _rows(dx, w, "dx", shape, t, cur)
+    st = load_library().basp_rmsnorm_backward(
+        code, shape[0], shape[1], yp, ys, hp, hs, _vector(rstd, w, "rstd", shape[0], _F32, cur),
+        _vector(weight, w, "weight", shape[1], weight.dtype, cur), wcode, dp, ds, xp, xs,
+        _vector(dweight, w, "dweight", shape[1], _F32, cur),
+        _tptr(workspace, None, w, "workspace", "device", cur), _nbytes(workspace), _stream(stream))
+    if st:
+        _check(st, w)
 
 
 def basp_quantize_fp8(x, q=None, qt=None, stream=None):
     """A matrix, and its transpose, to 8 bits; see ``basp_fp8.h``.  ``q`` and
     ``qt`` are :class:`basp_fp8_matrix` or None."""
     w = "basp_quantize_fp8"
-    rows, cols = _2d(x, w, "x")
-    _check(load_library().basp_quantize_fp8(
-        fp8_dtype_code(x.dtype), rows, cols, *_rows(x, w, "x", rows, cols, x.dtype, _current_device()),
-        q, qt, _stream(stream)), w)
+    shape = _2d(x, w, "x")
+    code = fp8_dtype_code(x.dtype)
+    xp, xs = _rows(x, w, "x", shape, x.dtype, _current_device())
+    st = load_library().basp_quantize_fp8(code, shape[0], shape[1], xp, xs, q, qt, _stream(stream))
+    if st:
+        _check(st, w)
 
 
 def basp_matmul_fp8(a, b, bias, c, accumulate=False, stream=None):
     """C = A B^T (+ bias) (+ C); see ``basp_fp8.h``.  ``a`` and ``b`` are
     :class:`basp_fp8_matrix`."""
     w = "basp_matmul_fp8"
-    cur = _current_device()
-    cp, cs = _rows(c, w, "c", a.rows, b.rows, c.dtype, cur)
-    _check(load_library().basp_matmul_fp8(
-        a, b, _vector(bias, w, "bias", b.rows, c.dtype, cur), int(accumulate), fp8_dtype_code(c.dtype),
-        cp, cs, _stream(stream)), w)
+    t, n, cur = c.dtype, b.rows, _current_device()
+    code = fp8_dtype_code(t)
+    cp, cs = _rows(c, w, "c", (a.rows, n), t, cur)
+    st = load_library().basp_matmul_fp8(a, b, _vector(bias, w, "bias", n, t, cur), int(accumulate), code, cp, cs,
+                                        _stream(stream))
+    if st:
+        _check(st, w)
+
+
+def fp8_entry_points():
+    """Addresses of the loaded library's 8-bit entry points, in the order in
+    which the torch module (``csrc/torch_ops.cpp``) takes them."""
+    lib = load_library()
+    return tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in FP8_EXPORTS[:5])
 
 
 def basp_matmul_fp8_timeouts() -> int:

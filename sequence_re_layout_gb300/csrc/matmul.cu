@@ -40,6 +40,7 @@
 // Waits.  Every wait on an mbarrier has a time limit.  When one runs out the
 // CTA's roles leave their loops, wait (with the limit again) for copies and
 // products in flight, write NaN where results would have gone, and count it.
+#include <algorithm>
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -90,7 +91,10 @@ template <int BN, int CG> struct Sizes {
     static_assert(kNeed <= 512, "tensor memory");
     static_assert(8 * kBarriers + 8 <= kBarrierBytes, "barriers");
     static_assert(kBlockQ % 1024 == 0, "swizzle");
+    static_assert(kStageBlocks == 2, "the products' loop");
 };
+
+constexpr int kMaxSplit = 4;             // CTAs that share K: eight rarely fit a GPC at once
 
 struct MatmulArgs {
     const uint8_t *sp, *sq;              // scales of B (P side) and A (Q side)
@@ -177,15 +181,23 @@ __device__ __forceinline__ void join_parts(const MatmulArgs &a, uint32_t part0, 
     if (n >= a.N) return;
     const float bias = a.bias != nullptr ? Elem<T>::to_float(static_cast<const T *>(a.bias)[n]) : 0.f;
     const int j1 = min(BN * (rank + 1) / a.split, int(min(int64_t(BN), a.M - m0)));
-    for (int j = BN * rank / a.split + half; j < j1; j += halves) {
-        float p[8], v = 0.f;
+    constexpr int U = 4;                                  // columns at once: a load takes a microsecond
+    for (int j = BN * rank / a.split + half; j < j1; j += U * halves) {
+        float v[U];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < a.split) p[r] = cluster_load(cluster_addr(part0 + uint32_t(j * kTileP + row) * 4, r));
+        for (int u = 0; u < U; ++u) v[u] = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < a.split) v += p[r];
-        put<T>(a, static_cast<T *>(a.c) + (m0 + j) * a.c_stride + n, v + bias);
+        for (int r = 0; r < kMaxSplit; ++r) {
+            if (r >= a.split) break;
+            const uint32_t part = cluster_addr(part0 + uint32_t(j * kTileP + row) * 4, r);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j + u * halves < j1) v[u] += cluster_load(part + uint32_t(u * halves * kTileP) * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u * halves < j1)
+                put<T>(a, static_cast<T *>(a.c) + (m0 + j + u * halves) * a.c_stride + n, v[u] + bias);
     }
 }
 
@@ -320,38 +332,35 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tcgen05_after_sync();
-                    --left;
-                    const bool last = left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % 2 == 1;
+                    const uint32_t at = ring.at;
+                    ring.next();
+                    ready = mbar_test(full + 8 * ring.at, ring.turn);   // known by the time it is asked
+                    const bool last = --left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % 2 == 1;
                     if (elect_one()) {
                         const uint32_t sf = tmem + S::kScaleBase + words.at * S::kScaleColumns;
                         if (scales) {
-                            const uint32_t src = scale0 + words.at * S::kScale;
+                            const uint64_t src = scale_desc(scale0 + words.at * S::kScale);
 #pragma unroll
-                            for (int i = 0; i < S::kScale / 512; ++i)
-                                tmem_copy_scales<CG>(sf + 4 * i, scale_desc(src + 512 * i));
+                            for (int i = 0; i < S::kScale / 512; ++i) tmem_copy_scales<CG>(sf + 4 * i, src + 32 * i);
                         }
                         const uint32_t acc = tmem + accs.at * BN;
-                        const uint32_t at = stage0 + ring.at * S::kStage;
-                        const int blocks = min(kStageBlocks, a.nk - s * kStageBlocks);
+                        const uint64_t dp = operand_desc(stage0 + at * S::kStage);
+                        const uint64_t dq = operand_desc(stage0 + at * S::kStage + kStageBlocks * S::kBlockP);
+                        const uint32_t idesc = mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks);
 #pragma unroll
-                        for (int i = 0; i < kStageBlocks; ++i) {
-                            if (i >= blocks) break;
-                            const uint64_t dp = operand_desc(at + i * S::kBlockP);
-                            const uint64_t dq = operand_desc(at + kStageBlocks * S::kBlockP + i * S::kBlockQ);
-                            const uint32_t idesc =
-                                mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks + i);
+                        for (int k = 0; k < kBlock / 32; ++k)
+                            mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
+                        if (s * kStageBlocks + 1 < a.nk) {
 #pragma unroll
                             for (int k = 0; k < kBlock / 32; ++k)
-                                mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4,
-                                             !fresh || i > 0 || k > 0);
+                                mma_mxf8<CG>(acc, dp + S::kBlockP / 16 + 2 * k, dq + S::kBlockQ / 16 + 2 * k,
+                                             idesc + mma_scale_ids(1), sf, sf + 4, true);
                         }
-                        mma_commit<CG>(empty + 8 * ring.at);
+                        mma_commit<CG>(empty + 8 * at);
                         if (word_done) mma_commit<CG>(sempty + 8 * words.at);
                         if (last) mma_commit<CG>(acc_full + 8 * accs.at);
                     }
                     __syncwarp();
-                    ring.next();
-                    ready = mbar_try_wait<false>(full + 8 * ring.at, ring.turn);   // known by the time it is asked
                     if (word_done) words.next();
                     if (last) {
                         left = 0;
@@ -372,29 +381,47 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         Ring<kScaleSlots> words;
         uint32_t issued = 0;
         bool ok = true;
-        // A lane's words of rows lane, lane + 32, ... of B's 128 and of A's.
+        // A lane's words (blocks 4 g .. 4 g + 3) of rows lane, lane + 32, ... of
+        // B's 128 and of A's.
         auto load = [&](int tm, int tn, int g, uint4 (&w)[A]) {
+            const uint8_t *at[A][4];
 #pragma unroll
-            for (int i = 0; i < A; ++i) {
-                uint32_t r[4];
+            for (int i = 0; i < A; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int in_tile = (i > 0 ? (i - 1) * 128 : 0) + 32 * j + lane;
-                    r[j] = 0x7f7f7f7fu;                   // rows that do not exist: values are 0
-                    if (i == 0) {
-                        const int64_t row = (int64_t(tn) * CG + peer) * kTileP + in_tile;
-                        if (row < a.N)
-                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                                a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g)));
-                    } else {
-                        const int64_t row = int64_t(tm) * BN + in_tile;
-                        if (in_tile < BN && row < a.M)
-                            r[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                                a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g)));
-                    }
+                    const int64_t row = i == 0 ? (int64_t(tn) * CG + peer) * kTileP + in_tile
+                                               : int64_t(tm) * BN + in_tile;
+                    at[i][j] = nullptr;                   // rows that do not exist: values are 0
+                    if (i == 0 && row < a.N) at[i][j] = a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g);
+                    if (i > 0 && in_tile < BN && row < a.M)
+                        at[i][j] = a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g);
                 }
-                w[i] = make_uint4(r[0], r[1], r[2], r[3]);
+            uint32_t r[A][4];
+            const int bytes = min(4, a.nk - 4 * g);
+            if (bytes == 4) {
+#pragma unroll
+                for (int i = 0; i < A; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        r[i][j] = 0x7f7f7f7fu;
+                        if (at[i][j] != nullptr) r[i][j] = __ldg(reinterpret_cast<const uint32_t *>(at[i][j]));
+                    }
+            } else {                                      // a row's last bytes: what follows is not its
+#pragma unroll
+                for (int i = 0; i < A; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        r[i][j] = 0x7f7f7f7fu;
+                        if (at[i][j] != nullptr) {
+                            r[i][j] = __ldg(at[i][j]);
+                            if (bytes > 1) r[i][j] |= uint32_t(__ldg(at[i][j] + 1)) << 8;
+                            if (bytes > 2) r[i][j] |= uint32_t(__ldg(at[i][j] + 2)) << 16;
+                        }
+                    }
             }
+#pragma unroll
+            for (int i = 0; i < A; ++i) w[i] = make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
         };
         // Words in order: those of one tile, then of the CTA's next.  kAhead of
         // them are on their way in registers: beside the tiles' traffic a load
@@ -591,10 +618,16 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         for (int j = 0; j < 16; ++j)
                             if (ok) part[(j0 + j) * kTileP + row] = __uint_as_float(v[j]);
                     } else if (mine) {
+                        T *to = c + j0 * a.c_stride;
+                        if (!a.accumulate && m0 + j0 + 16 <= a.M) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (m0 + j0 + j < a.M)
-                                put<T>(a, c + (j0 + j) * a.c_stride, __uint_as_float(v[j]) + bias);
+                            for (int j = 0; j < 16; ++j, to += a.c_stride)
+                                *to = Elem<T>::from_float(__uint_as_float(v[j]) + bias);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, to += a.c_stride)
+                                if (m0 + j0 + j < a.M) put<T>(a, to, __uint_as_float(v[j]) + bias);
+                        }
                     }
                 }
             }
@@ -695,11 +728,12 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
         const int cg = 1 + pair;
         const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP * cg);
         if (split > 1 && (split > ceil_div(nk, kStageBlocks) || tiles * split > sms)) return;
-        const double block = std::max(2.0 * bn, (kTileP + bn / cg) * kBlock / 64.0);
-        const double k = double(ceil_div(nk, split)) * block;
-        const double drain = 6.0 * bn / split + (split > 1 ? 2000 : 0);
+        // a block's products, its loads, or what issuing them takes
+        const double block = std::max({2.0 * bn, (kTileP + bn / cg) * kBlock / 55.0, 350.0});
         const double rounds = double(ceil_div(tiles * split * cg, sms));
-        const double cost = 3000 + rounds * k + (rounds - 1) * 300 + drain;
+        const double start = pair ? 9000 : 5500, drain = (pair ? 8.0 : 20.0) * bn;
+        const double cost = start + rounds * double(ceil_div(nk, split)) * block + drain +
+                            (split > 1 ? 2500 + 10.0 * bn : 0);
         if (cost < best_cost) {
             best_cost = cost;
             best = {bn, pair, split};
@@ -707,7 +741,7 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
     };
     for (int bn = 16; bn <= 128; bn *= 2) {
         if (bn > 16 && bn / 2 >= M) break;
-        for (int split = 1; split <= 8; split *= 2) consider(bn, 0, split);
+        for (int split = 1; split <= kMaxSplit; split *= 2) consider(bn, 0, split);
     }
     if (M > 128)
         for (int bn : {224, 192}) consider(bn, 1, 1);

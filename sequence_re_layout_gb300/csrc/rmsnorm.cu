@@ -193,10 +193,13 @@ __device__ __forceinline__ float walk_sum(float v, float *part, int warps) {
 
 // Largest over the threads of a 128-block (16 or 32 of a warp).
 template <int THREADS> __device__ __forceinline__ uint32_t block_max(uint32_t m) {
-    if constexpr (THREADS == 32) return __reduce_max_sync(0xffffffffu, m);
+    if constexpr (THREADS == 32) {
+        return __reduce_max_sync(0xffffffffu, m);
+    } else {
 #pragma unroll
-    for (int o = THREADS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+        for (int o = THREADS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
 }
 
 template <class T, class W, int NV>

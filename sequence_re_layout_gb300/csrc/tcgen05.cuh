@@ -58,6 +58,17 @@ template <bool CLUSTER> __device__ __forceinline__ bool mbar_try_wait(uint32_t b
             : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+// Whether it is complete now: try_wait may suspend the thread for a while,
+// this does not.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // mbarrier initialisation and generic writes to shared memory, made visible
 // to the asynchronous proxy (TMA, tcgen05)
 __device__ __forceinline__ void fence_mbar_init() {

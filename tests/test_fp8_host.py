@@ -1,6 +1,5 @@
 """CPU checks of the 8-bit operators' C ABI (include/basp_fp8.h): exported
 symbols, and refusals, which all happen before anything reaches a GPU."""
-import ctypes
 import os
 import re
 
@@ -146,12 +145,21 @@ def test_status_pointer(lib):
 
 
 def test_python_refusals():
-    d = torch.zeros(4, 16).to(torch.float8_e4m3fn)
-    s = torch.ones(4, 1).to(torch.float8_e8m0fnu)
-    for args in ((d, s, 2), (d.float(), s), (d, s.float()), (d[0], s), (d, s[:3]), (d, s)):
-        with pytest.raises(ValueError):        # the last one: not on a GPU
-            fp8.Quantized(*args)
+    """What the tensors' calls refuse before they look for a GPU."""
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.ones(16, dtype=torch.bfloat16)
+    q = fp8.Quantized(torch.zeros(4, 16).to(torch.float8_e4m3fn), torch.ones(4, 1).to(torch.float8_e8m0fnu))
+    for call in (lambda: fp8.rmsnorm(x, w), lambda: fp8.rmsnorm(x.double(), w), lambda: fp8.rmsnorm(x, None),
+                 lambda: fp8.rmsnorm_backward(x, x, torch.ones(4), w), lambda: fp8.quantize(x),
+                 lambda: fp8.quantize(x, block_rows=64), lambda: fp8.quantize(x, rows=False),
+                 lambda: fp8.quantize(torch.zeros(())), lambda: fp8.matmul(q, q),
+                 lambda: fp8.Quantized.empty(4, 16, 2, "cpu")):
+        with pytest.raises(ValueError):
+            call()
     with pytest.raises(ValueError):
         basp.binding.fp8_dtype_code(torch.float64)
-    with pytest.raises(ValueError):
-        fp8.matmul(None, None, accumulate=True)
+
+
+def test_torch_module_calls_the_loaded_library(lib):
+    import ctypes
+    want = [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in basp.FP8_EXPORTS[:5]]
+    assert list(basp.binding.fp8_entry_points()) == want

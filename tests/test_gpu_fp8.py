@@ -114,13 +114,13 @@ def test_quantize_writes_nothing_past_its_rows():
     stores = [torch.full((r, c), 0x55, dtype=torch.uint8, device="cuda")
               for r, c in ((130, 224), (130, 8), (200, 160), (200, 8))]
     q, s, qt, st = stores
-    mats = [fp8.Quantized(d.view(torch.float8_e4m3fn)[:, :c], z.view(torch.float8_e8m0fnu)[:, :2])
-            for d, z, c in ((q, s, 200), (qt, st, 130))]
-    basp.basp_quantize_fp8(x, mats[0]._c, mats[1]._c, torch.cuda.current_stream())
+    mats = [basp.basp_fp8_matrix(d.data_ptr(), z.data_ptr(), r, c, d.stride(0), 8, 1)
+            for d, z, r, c in ((q, s, 130, 200), (qt, st, 200, 130))]
+    basp.basp_quantize_fp8(x, mats[0], mats[1], torch.cuda.current_stream())
     torch.cuda.synchronize()
     for store, cols in zip(stores, (200, 2, 130, 2)):
         assert bool((store[:, cols:] == 0x55).all())
-    assert np.array_equal(values_and_exps(mats[1])[0], ref.quantize(f64(x).T, 1)[0])
+    assert np.array_equal(f64(qt.view(torch.float8_e4m3fn)[:, :130]), ref.quantize(f64(x).T, 1)[0])
 
 
 # ---- norm -----------------------------------------------------------------------
@@ -309,6 +309,70 @@ def test_matmul_scales_at_their_ends():
     b.scales.view(torch.uint8).fill_(127)
     assert torch.equal(extreme, fp8.matmul(a, b, out_dtype=torch.float32))
     assert bool(torch.isfinite(plain).all())
+
+
+def c_matrix(q):
+    """A Quantized for the ctypes binding."""
+    d, s = q.data, q.scales
+    return basp.basp_fp8_matrix(d.data_ptr(), s.data_ptr(), *d.shape, d.stride(0), s.stride(0), q.block_rows)
+
+
+def test_binding_and_tensors_give_the_same():
+    """The ctypes binding's calls, with outputs of the caller's."""
+    x, r, w = (random(n, 512, torch.bfloat16, i) for i, n in enumerate((40, 40, 1)))
+    w, stream = w[0], torch.cuda.current_stream()
+    y, h, rstd = fp8.rmsnorm(x, w, residual=r)
+    q, h2, rstd2 = fp8.Quantized.empty(40, 512), torch.empty_like(x), torch.empty_like(rstd)
+    basp.basp_rmsnorm(x, r, w, 1e-6, h=h2, q=c_matrix(q), rstd=rstd2, stream=stream)
+    assert torch.equal(h, h2) and torch.equal(rstd, rstd2)
+    assert torch.equal(q.data.view(torch.uint8), y.data.view(torch.uint8))
+    wq = fp8.quantize(random(96, 512, torch.float32, 5), block_rows=128)
+    c = torch.empty(40, 96, dtype=torch.bfloat16, device="cuda")
+    basp.basp_matmul_fp8(c_matrix(q), c_matrix(wq), None, c, stream=stream)
+    assert torch.equal(c, fp8.matmul(y, wq))
+    dx, dw = torch.empty_like(x), torch.empty(512, device="cuda")
+    ws = torch.empty(basp.basp_rmsnorm_backward_workspace(40, 512), dtype=torch.uint8, device="cuda")
+    basp.basp_rmsnorm_backward(x, h, rstd, w, None, dx, dw, ws, stream=stream)
+    want = fp8.rmsnorm_backward(x, h, rstd, w)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("how", ["dtype", "shape", "columns", "cpu", "bias", "scales", "out", "block_rows", "rows"])
+def test_refusals(how):
+    x, w = random(4, 256, torch.bfloat16, 1), torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    q, _ = quantized(4, 256, 1, 1)
+    call = {
+        "dtype": lambda: fp8.rmsnorm(x, w, residual=x.half()),
+        "shape": lambda: fp8.rmsnorm(x, w[:255]),
+        "columns": lambda: fp8.quantize(x.t()),
+        "cpu": lambda: fp8.rmsnorm(x, w, residual=x.cpu()),
+        "bias": lambda: fp8.matmul(q, q, bias=torch.zeros(4, device="cuda")),
+        "scales": lambda: fp8.matmul(fp8.Quantized(q.data, q.scales[:, :1]), q),
+        "out": lambda: fp8.matmul(q, q, out=torch.zeros(4, 5, dtype=torch.bfloat16, device="cuda")),
+        "block_rows": lambda: fp8.matmul(fp8.Quantized(q.data, q.scales, 2), q),
+        "rows": lambda: fp8.rmsnorm(torch.zeros(8, 4, 256, device="cuda")[::2, ::2], torch.ones(256, device="cuda"),
+                                    residual=torch.zeros(4, 2, 256, device="cuda").transpose(0, 1).reshape(2, 4, 256)
+                                    .transpose(0, 1)),
+    }[how]
+    with pytest.raises(ValueError):
+        call()
+
+
+def test_overlapping_output_is_refused():
+    x = random(4, 256, torch.bfloat16, 1)
+    with pytest.raises(basp.BaspError) as e:
+        fp8.rmsnorm(x[:3], torch.ones(256, dtype=torch.bfloat16, device="cuda"), residual=x[:3].clone(), h=x[1:])
+    assert e.value.status == basp.BASP_ERR_ALIASING
+
+
+def test_scales_end_with_their_storage():
+    """A last row of scales without the bytes up to a multiple of four."""
+    q, q64 = quantized(5, 700, 1, 3)
+    scales = torch.empty_strided((5, 6), (8, 1), dtype=torch.float8_e8m0fnu, device="cuda")
+    scales.view(torch.uint8).copy_(q.scales.view(torch.uint8))
+    assert scales.untyped_storage().nbytes() == 4 * 8 + 6
+    b, b64 = quantized(9, 700, 128, 4)
+    check_product(fp8.matmul(fp8.Quantized(q.data, scales), b, out_dtype=torch.float32), q64, b64, 700)
 
 
 def test_other_stream_and_graph():
