@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n, int tiles) {
     constexpr int ST = kTileAhead + 1, N = Pack<T>::N, G = kBlock / N, R = 32 / N;
     extern __shared__ __align__(16) uint8_t smem[];     // [ST][R][threads] of 16 bytes
-    __shared__ uint32_t col_max[kTileWarps][kBlock];
+    __shared__ __align__(16) uint32_t col_max[kTileWarps][kBlock];
     __shared__ float col_inv[kBlock];
     __shared__ __align__(16) uint8_t t[kBlock * kBlock];
     grid_dependency();
@@ -278,7 +278,7 @@ quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n, int tiles
 template <class T, bool PER_ROW>
 __global__ void __launch_bounds__(kTileThreads, 2)
 quantize_any_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n) {
-    __shared__ uint32_t col_max[kTileWarps][kBlock];
+    __shared__ __align__(16) uint32_t col_max[kTileWarps][kBlock];
     __shared__ __align__(16) uint8_t t[kBlock * kBlock];
     grid_dependency();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;

@@ -46,6 +46,24 @@ struct NormArgs {
     float eps, inv_cols;
 };
 
+// 1 / sqrt(x) to half a unit in the last place: the hardware's estimate and
+// one Newton step on the residual 1 - x r^2, taken exactly.  (A value next to
+// a border of two 8-bit values is decided by this last bit.)
+__device__ __forceinline__ float inverse_root(float x) {
+    const float r = rsqrtf(x);
+    const float t = x * r;
+    const float e = fmaf(-t, r, 1.f) - fmaf(x, r, -t) * r;
+    const float better = fmaf(0.5f * r, e, r);
+    return better == better ? better : r;                // x = 0 or infinite: the estimate says it
+}
+
+// sum / n to half a unit in the last place, given 1 / n.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv_n) {
+    const float q = sum * inv_n;
+    const float better = fmaf(fmaf(-q, n, sum), inv_n, q);
+    return better == better ? better : q;                // an infinite sum
+}
+
 // Sum over the warps of one row: warps of a row are blockDim.x / 32, rows of
 // a CTA blockDim.y (more than one only with one warp a row).
 __device__ __forceinline__ float warp_sum(float v) {
@@ -124,7 +142,7 @@ __global__ void __launch_bounds__(NB == 1 ? 1024 : 512) norm_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 4; ++j) sq += hv[i][j] * hv[i][j];
         }
-        const float rstd = rsqrtf(row_sum(sq, part, warps) * a.inv_cols + a.eps);
+        const float rstd = inverse_root(mean_of(row_sum(sq, part, warps), float(a.cols), a.inv_cols) + a.eps);
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -153,7 +171,7 @@ __global__ void __launch_bounds__(NB == 1 ? 1024 : 512) norm_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 4; ++j) sq += hv[j] * hv[j];
         }
-        const float rstd = rsqrtf(row_sum(sq, part, warps) * a.inv_cols + a.eps);
+        const float rstd = inverse_root(mean_of(row_sum(sq, part, warps), float(a.cols), a.inv_cols) + a.eps);
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
         for (int64_t c = int64_t(warp) * kBlock; c < a.cols; c += int64_t(warps) * kBlock) {
             float hv[4], wv[4];
@@ -270,7 +288,7 @@ __global__ void __launch_bounds__(kWalkThreads) norm_walk_kernel(const __grid_co
         }
         stage = stage + 1 < ST ? stage + 1 : 0;
         // two buffers in turn: a warp can be one row ahead of another
-        const float rstd = rsqrtf(walk_sum(sq, part[turn], warps) * a.inv_cols + a.eps);
+        const float rstd = inverse_root(mean_of(walk_sum(sq, part[turn], warps), float(a.cols), a.inv_cols) + a.eps);
         if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
         if (a.y != nullptr) {
 #pragma unroll

@@ -55,7 +55,10 @@ def strided(x, pad):
 
 
 SHAPES = [(1, 1), (1, 64), (1, 2048), (3, 127), (2, 128), (5, 129), (33, 260), (700, 256), (401, 1000), (9, 4099),
-          (2, 16385), (400, 2048), (310, 5120)]
+          (2, 16385), (400, 2048), (310, 5120),
+          # many rows that start anywhere: from one column to the longest that stay in registers, and past it
+          (1201, 1), (700, 7), (333, 129), (320, 130), (1300, 257), (309, 4099), (310, 9001), (305, 16001),
+          (306, 16389), (320, 20000)]
 
 
 # ---- quantisation -------------------------------------------------------------
@@ -160,6 +163,63 @@ def test_rmsnorm_in_place_and_strided(cols):
         assert torch.equal(got.data.view(torch.uint8), want.data.view(torch.uint8))
     xs = x.clone()
     assert torch.equal(fp8.rmsnorm(xs, w, residual=r, h=xs)[1], want_h) and torch.equal(xs, want_h)
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("cols,pad", [(203, 0), (200, 1), (203, 5), (16, 3), (1000, 1), (5, 0), (1, 1)])
+@pytest.mark.parametrize("offset", [0, 1, 3])
+def test_rmsnorm_of_many_rows_that_start_anywhere(cols, pad, dtype, offset):
+    """Rows, first elements and strides off the 16-byte grid, all matrices alike
+    and then one of them differently, forward and backward, next to memory that
+    must stay as it is and must not be used (NaN)."""
+    t, rows = DTYPES[dtype], 620
+    x, r = random(rows, cols, t, 1, 1.0), random(rows, cols, t, 2, 1.0)
+    w = random(1, cols, t, 3, 0.5)[0]
+    want, want_h, want_rstd = fp8.rmsnorm(x, w, residual=r)
+    want_dx, want_dw = fp8.rmsnorm_backward(x, want_h, want_rstd, w, dh=r)
+    rv, re = ref.quantize(ref.norm(f64(want_h), f64(w), 1e-6)[0], 1)
+
+    def placed(m, offset):
+        store = torch.full((rows * (cols + pad) + 64,), float("nan"), dtype=t, device="cuda")
+        view = store[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+        view.copy_(m)
+        return store, view
+
+    for other in (offset, offset + 1):                     # alike, or the residual one element further
+        (_, xs), (_, rs), (hstore, hs) = placed(x, offset), placed(r, other), placed(r, offset)
+        got, h, rstd = fp8.rmsnorm(xs, w, residual=rs, h=hs)
+        assert torch.equal(hs, want_h)
+        hs.fill_(float("nan"))
+        assert bool(torch.isnan(hstore).all())
+        v, e = values_and_exps(got)
+        assert (e != re).mean() < 0.01 and (v != rv).mean() < 0.01
+        # the same bits as the aligned call, but for the order of a row's sum
+        assert float((rstd / want_rstd - 1).abs().max()) < 2.0 ** -20
+        (_, dys), (_, hs), (_, dhs) = placed(x, offset), placed(want_h, offset), placed(r, other)
+        dx, dw = fp8.rmsnorm_backward(dys, hs, want_rstd, w, dh=dhs)
+        size = f64(want_rstd)[:, None] * 4 * np.abs(f64(x) * f64(w)).max() + np.abs(f64(r))
+        assert (np.abs(f64(dx) - f64(want_dx)) <= 2 * u(t) * np.abs(f64(want_dx)) + (cols + 8) * F32 * size).all()
+        scale = (np.abs(f64(x)) * np.abs(f64(want_h)) * f64(want_rstd)[:, None]).sum(0)
+        assert (np.abs(f64(dw) - f64(want_dw)) <= 2 * (rows + 8) * F32 * scale + 1e-30).all()
+
+
+def test_rmsnorm_of_many_ragged_rows_with_infinities():
+    """The looked-at values of rows that start anywhere: one infinity makes its
+    row's root zero; one NaN its whole row."""
+    x = torch.ones(400, 391)
+    x[7, 130], x[9, 388], x[11, 0] = float("inf"), float("nan"), float("-inf")
+    y, _, _ = fp8.rmsnorm(x.cuda(), torch.ones(391, device="cuda"), quantized=True)
+    d = y.dequantize().cpu()
+    for row, bad in ((7, 130), (11, 0)):
+        assert torch.isnan(d[row, bad]) and int(torch.isnan(d[row]).sum()) == 1
+        assert float(d[row].nan_to_num().abs().max()) == 0
+    assert bool(torch.isnan(d[9]).all())
+    rest = torch.ones(400, dtype=torch.bool)
+    rest[[7, 9, 11]] = False
+    assert bool((d[rest] == 1).all())
+    tiny = torch.full((400, 391), 1e-30, device="cuda")     # 0.03 of the root of eps, times a tiny weight
+    y, _, _ = fp8.rmsnorm(tiny, torch.full((391,), 1e-38, device="cuda"), eps=1e-37)
+    assert bool(torch.isfinite(y.dequantize()).all())
 
 
 def test_rmsnorm_leading_dimensions():
