@@ -34,8 +34,9 @@ template <> struct Elem<__half> {
 template <class T> struct alignas(4 * sizeof(T)) Vec4 { T v[4]; };
 
 // 16 bytes of a row as they lie in memory: eight 16-bit values or four of 32
-// bits.  max_abs is elementwise, and a NaN does not count; two 16-bit values
-// take one instruction.
+// bits.  max_abs is elementwise: the larger magnitude, a NaN not counted, in
+// one instruction for two 16-bit values; the result's signs mean nothing
+// (`magnitude` takes them off).
 template <class T> struct Pack;
 template <> struct Pack<float> {
     static constexpr int N = 4;
@@ -48,8 +49,9 @@ template <> struct Pack<float> {
                           __float_as_uint(v[3]));
     }
     static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
-        return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(x))));
+        return __float_as_uint(fmaxf(fabsf(__uint_as_float(m)), fabsf(__uint_as_float(x))));
     }
+    static __device__ __forceinline__ uint32_t magnitude(uint32_t x) { return x & 0x7fffffffu; }
 };
 template <> struct Pack<__nv_bfloat16> {
     static constexpr int N = 8;
@@ -71,10 +73,11 @@ template <> struct Pack<__nv_bfloat16> {
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
     static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
-        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&m),
-                                         __habs2(*reinterpret_cast<__nv_bfloat162 *>(&x)));
-        return *reinterpret_cast<const uint32_t *>(&r);
+        uint32_t r;
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+        return r;
     }
+    static __device__ __forceinline__ uint32_t magnitude(uint32_t x) { return x & 0x7fff7fffu; }
     // the float bits of the low and the high value
     static __device__ __forceinline__ uint32_t low(uint32_t x) { return x << 16; }
     static __device__ __forceinline__ uint32_t high(uint32_t x) { return x & 0xffff0000u; }
@@ -100,9 +103,11 @@ template <> struct Pack<__half> {
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
     static __device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t x) {
-        const __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&m), __habs2(*reinterpret_cast<__half2 *>(&x)));
-        return *reinterpret_cast<const uint32_t *>(&r);
+        uint32_t r;
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+        return r;
     }
+    static __device__ __forceinline__ uint32_t magnitude(uint32_t x) { return x & 0x7fff7fffu; }
     static __device__ __forceinline__ uint32_t low(uint32_t x) {
         return __float_as_uint(__half2float(__ushort_as_half(uint16_t(x))));
     }
@@ -296,11 +301,12 @@ struct NvtxRange {
 int sm_count();
 
 // CTAs of `kernel` that fit on the current device at once; also lets the
-// kernel have `smem` bytes of dynamic shared memory.
+// kernel have `smem` bytes of dynamic shared memory (48 KB less its static
+// ones come unasked).
 template <class K>
 int64_t resident_ctas(K kernel, int threads, size_t smem) {
     int per_sm = 0;
-    if ((smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((smem > 16 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   int(smem)) != cudaSuccess) ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
         cudaGetLastError();
