@@ -126,8 +126,7 @@ struct Waiter {
     volatile int *abort;                 // shared by the CTA
     template <bool CLUSTER = false>
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, bool give_up_early = true) const {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+        if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait<CLUSTER>(bar, parity)) {
             if (give_up_early && *abort) return false;
@@ -139,9 +138,9 @@ struct Waiter {
         }
         return true;
     }
-    // for an arrival from another CTA's threads
-    __device__ __forceinline__ bool cluster(uint32_t bar, uint32_t parity) const {
-        return operator()<true>(bar, parity);
+    // for an arrival that may come from the other CTA's threads of a pair
+    template <int CG> __device__ __forceinline__ bool pair(uint32_t bar, uint32_t parity) const {
+        return operator()<CG == 2>(bar, parity);
     }
 };
 
@@ -311,7 +310,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             if (!ok && peer == 0) wait(full + 8 * (j % ST), (j / ST) & 1, false);
         }
     } else if (warp == 1) {
-        if (peer == 0) {                                  // products
+        if (peer == 0 && elect_one()) {                   // products
             Ring<ST> ring;
             Ring<kScaleSlots> words;
             Ring<2> accs;
@@ -325,42 +324,38 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     if (fresh) {
                         left = segment;
                         // drained of the sum before the last
-                        if (count >= 2) ok = wait.cluster(acc_free + 8 * accs.at, accs.turn ^ 1);
+                        if (count >= 2) ok = wait.template pair<CG>(acc_free + 8 * accs.at, accs.turn ^ 1);
                     }
-                    if (scales) ok = ok && wait.cluster(sfull + 8 * words.at, words.turn);
+                    if (scales) ok = ok && wait.template pair<CG>(sfull + 8 * words.at, words.turn);
                     if (!ready) ok = ok && wait(full + 8 * ring.at, ring.turn);
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tcgen05_after_sync();
                     const uint32_t at = ring.at;
                     ring.next();
                     ready = mbar_test(full + 8 * ring.at, ring.turn);   // known by the time it is asked
                     const bool last = --left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % 2 == 1;
-                    if (elect_one()) {
-                        const uint32_t sf = tmem + S::kScaleBase + words.at * S::kScaleColumns;
-                        if (scales) {
-                            const uint64_t src = scale_desc(scale0 + words.at * S::kScale);
+                    const uint32_t sf = tmem + S::kScaleBase + words.at * S::kScaleColumns;
+                    if (scales) {
+                        const uint64_t src = scale_desc(scale0 + words.at * S::kScale);
 #pragma unroll
-                            for (int i = 0; i < S::kScale / 512; ++i) tmem_copy_scales<CG>(sf + 4 * i, src + 32 * i);
-                        }
-                        const uint32_t acc = tmem + accs.at * BN;
-                        const uint64_t dp = operand_desc(stage0 + at * S::kStage);
-                        const uint64_t dq = operand_desc(stage0 + at * S::kStage + kStageBlocks * S::kBlockP);
-                        const uint32_t idesc = mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks);
+                        for (int i = 0; i < S::kScale / 512; ++i) tmem_copy_scales<CG>(sf + 4 * i, src + 32 * i);
+                    }
+                    const uint32_t acc = tmem + accs.at * BN;
+                    const uint32_t dp = operand_desc_low(stage0) + at * (S::kStage / 16);
+                    const uint32_t dq = dp + kStageBlocks * S::kBlockP / 16;
+                    const uint32_t idesc = mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks);
+#pragma unroll
+                    for (int k = 0; k < kBlock / 32; ++k)
+                        mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
+                    if (s * kStageBlocks + 1 < a.nk) {
 #pragma unroll
                         for (int k = 0; k < kBlock / 32; ++k)
-                            mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
-                        if (s * kStageBlocks + 1 < a.nk) {
-#pragma unroll
-                            for (int k = 0; k < kBlock / 32; ++k)
-                                mma_mxf8<CG>(acc, dp + S::kBlockP / 16 + 2 * k, dq + S::kBlockQ / 16 + 2 * k,
-                                             idesc + mma_scale_ids(1), sf, sf + 4, true);
-                        }
-                        mma_commit<CG>(empty + 8 * at);
-                        if (word_done) mma_commit<CG>(sempty + 8 * words.at);
-                        if (last) mma_commit<CG>(acc_full + 8 * accs.at);
+                            mma_mxf8<CG>(acc, dp + S::kBlockP / 16 + 2 * k, dq + S::kBlockQ / 16 + 2 * k,
+                                         idesc + mma_scale_ids(1), sf, sf + 4, true);
                     }
-                    __syncwarp();
+                    mma_commit<CG>(empty + 8 * at);
+                    if (word_done) mma_commit<CG>(sempty + 8 * words.at);
+                    if (last) mma_commit<CG>(acc_full + 8 * accs.at);
                     if (word_done) words.next();
                     if (last) {
                         left = 0;
@@ -370,20 +365,29 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 }
             }
             if (!ok) {                                    // products in flight end before the CTA does
-                __syncwarp();
-                if (elect_one()) mma_commit<CG>(drained);
-                __syncwarp();
+                mma_commit<CG>(drained);
                 wait(drained, 0, false);
             }
         }
     } else if (warp == 2) {                               // scales
-        constexpr int A = S::kScale / 512;                // groups of 128 rows
-        Ring<kScaleSlots> words;
+        // Each lane copies the words (four blocks' bytes) of rows lane, lane + 32,
+        // ... of B's 128 and of A's to where the products' copy expects them.
+        // kAhead words are on their way beside the one that is passed on: next
+        // to the tiles' traffic a load takes longer than four blocks' products.
+        constexpr int A = S::kScale / 512, kAhead = 1;    // A: groups of 128 rows
+        static_assert(kAhead < kScaleSlots, "a slot each");
+        Ring<kScaleSlots> words, passed;
         uint32_t issued = 0;
         bool ok = true;
-        // A lane's words (blocks 4 g .. 4 g + 3) of rows lane, lane + 32, ... of
-        // B's 128 and of A's.
-        auto load = [&](int tm, int tn, int g, uint4 (&w)[A]) {
+        const int g0 = s0 / 2, g1 = (s1 + 1) / 2;
+        auto pass_on = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(swritten + 8 * passed.at);
+            passed.next();
+        };
+        for (int t = first; t < a.tiles && ok; t += step) {
+            int tm, tn;
+            tile_at(a, t, &tm, &tn);
             const uint8_t *at[A][4];
 #pragma unroll
             for (int i = 0; i < A; ++i)
@@ -392,80 +396,38 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     const int in_tile = (i > 0 ? (i - 1) * 128 : 0) + 32 * j + lane;
                     const int64_t row = i == 0 ? (int64_t(tn) * CG + peer) * kTileP + in_tile
                                                : int64_t(tm) * BN + in_tile;
-                    at[i][j] = nullptr;                   // rows that do not exist: values are 0
-                    if (i == 0 && row < a.N) at[i][j] = a.sp + (row >> a.sp_shift) * a.sp_pitch + 4 * int64_t(g);
-                    if (i > 0 && in_tile < BN && row < a.M)
-                        at[i][j] = a.sq + (row >> a.sq_shift) * a.sq_pitch + 4 * int64_t(g);
+                    at[i][j] = nullptr;                   // rows that do not exist: their values are 0
+                    if (i == 0 && row < a.N) at[i][j] = a.sp + (row >> a.sp_shift) * a.sp_pitch;
+                    if (i > 0 && in_tile < BN && row < a.M) at[i][j] = a.sq + (row >> a.sq_shift) * a.sq_pitch;
                 }
-            uint32_t r[A][4];
-            const int bytes = min(4, a.nk - 4 * g);
-            if (bytes == 4) {
-#pragma unroll
-                for (int i = 0; i < A; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        r[i][j] = 0x7f7f7f7fu;
-                        if (at[i][j] != nullptr) r[i][j] = __ldg(reinterpret_cast<const uint32_t *>(at[i][j]));
-                    }
-            } else {                                      // a row's last bytes: what follows is not its
-#pragma unroll
-                for (int i = 0; i < A; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        r[i][j] = 0x7f7f7f7fu;
-                        if (at[i][j] != nullptr) {
-                            r[i][j] = __ldg(at[i][j]);
-                            if (bytes > 1) r[i][j] |= uint32_t(__ldg(at[i][j] + 1)) << 8;
-                            if (bytes > 2) r[i][j] |= uint32_t(__ldg(at[i][j] + 2)) << 16;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < A; ++i) w[i] = make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
-        };
-        // Words in order: those of one tile, then of the CTA's next.  kAhead of
-        // them are on their way in registers: beside the tiles' traffic a load
-        // takes longer than the products of four blocks.
-        constexpr int kAhead = 4;
-        const int g0 = s0 / 2, g1 = (s1 + 1) / 2;
-        int t = first, g = g0, tm = 0, tn = 0;
-        if (t < a.tiles) tile_at(a, t, &tm, &tn);
-        uint4 w[kAhead][A];
-        bool have[kAhead];
-        auto fetch = [&](uint4 (&to)[A]) {
-            if (t >= a.tiles) return false;
-            load(tm, tn, g, to);
-            if (++g == g1) {
-                g = g0;
-                t += step;
-                if (t < a.tiles) tile_at(a, t, &tm, &tn);
-            }
-            return true;
-        };
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) have[d] = fetch(w[d]);
-        while (have[0] && ok) {
-#pragma unroll
-            for (int d = 0; d < kAhead; ++d) {
-                if (!have[d] || !ok) break;
+            for (int g = g0; g < g1; ++g) {
                 ok = __all_sync(0xffffffffu, wait(sempty + 8 * words.at, words.turn ^ 1));
                 if (!ok) break;
+                const uint32_t to = scale0 + words.at * S::kScale + 16 * lane;
+                const int bytes = min(4, a.nk - 4 * g);   // what follows a row's last is not its
 #pragma unroll
                 for (int i = 0; i < A; ++i)
-                    reinterpret_cast<uint4 *>(scale_smem + words.at * S::kScale + 512 * i)[lane] = w[d][i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(swritten + 8 * words.at);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool have = at[i][j] != nullptr;
+                        copy4_async(to + 512 * i + 4 * j, have ? at[i][j] + 4 * g : a.sp, have ? bytes : 0);
+                    }
+                copy_commit();
                 words.next();
-                ++issued;
-                have[d] = fetch(w[d]);
+                if (++issued > kAhead) {
+                    copy_wait<kAhead>();
+                    pass_on();
+                }
             }
         }
+        copy_wait<0>();
+        for (uint32_t j = issued < kAhead ? 0 : issued - kAhead; j < issued; ++j) pass_on();
         if (CG == 2 && ok)                                // the last arrivals, as above
             for (uint32_t j = issued < kScaleSlots ? 0 : issued - kScaleSlots; j < issued; ++j)
                 wait(sempty + 8 * (j % kScaleSlots), (j / kScaleSlots) & 1);
     } else if (warp == 3) {                               // scales, on to the products
-        // A warp of its own: a fence waits for the loads that its warp has in
-        // flight, and the scales' are four words ahead.
+        // A warp of its own: a fence waits for the copies that its warp has in
+        // flight (3000 cycles for four blocks, when one warp did both).
         Ring<kScaleSlots> words;
         bool ok = true;
         for (int t = first; t < a.tiles && ok; t += step)
@@ -718,9 +680,12 @@ struct Shape {
 
 // The tile (its width along A's rows, one CTA or a pair) and the number of
 // CTAs that split K with the least estimated time, in SM cycles: rounds of
-// tiles over the SMs, each paying for its stages (tensor cores, or loads at
-// what an SM gets from L2, 64 bytes a cycle) and for a start and a drain that
-// no stage hides.
+// tiles over the SMs, each paying for its blocks of K, and what no round
+// hides.  The figures are fits to GPU times on 152 SMs: one tile of K = 2048
+// takes 5.0 us at 16 wide, 6.8 at 128, 8.7 in a pair 192 wide, and 0.15, 0.19
+// and 0.20 us for each further block; beside other CTAs an SM gets 57 to 68
+// bytes a cycle from L2; a split into 4 saves 5.5 us at one token and K =
+// 8192 (6.6 instead of 12.1) and loses 1.2 at K = 2048.
 Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
     Shape best = {128, 0, 1};
     double best_cost = 1e300;
@@ -729,11 +694,11 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
         const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP * cg);
         if (split > 1 && (split > ceil_div(nk, kStageBlocks) || tiles * split > sms)) return;
         // a block's products, its loads, or what issuing them takes
-        const double block = std::max({2.0 * bn, (kTileP + bn / cg) * kBlock / 55.0, 350.0});
+        const double block = std::max({2.0 * bn, (kTileP + bn / cg) * kBlock / (pair ? 57.0 : 68.0), 280.0});
         const double rounds = double(ceil_div(tiles * split * cg, sms));
-        const double start = pair ? 9000 : 5500, drain = (pair ? 8.0 : 20.0) * bn;
-        const double cost = start + rounds * double(ceil_div(nk, split)) * block + drain +
-                            (split > 1 ? 2500 + 10.0 * bn : 0);
+        const double start = pair ? 9000 + 8.0 * bn : 5000 + 15.0 * bn;
+        const double cost = start + rounds * double(ceil_div(nk, split)) * block +
+                            (split > 1 ? 2000 + 70.0 * bn : 0);
         if (cost < best_cost) {
             best_cost = cost;
             best = {bn, pair, split};

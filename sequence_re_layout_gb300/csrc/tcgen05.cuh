@@ -119,6 +119,12 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// A thread's 4 bytes of global memory to shared memory, the first `bytes` of
+// them; the others become zero.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // ---- tensor memory ------------------------------------------------------------
 
 // Both by one whole warp (of each CTA of a pair, CG = 2).  `slot` is a
@@ -173,11 +179,12 @@ __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::l
 
 // Shared-memory descriptor of a K-major operand of 128-byte rows in the
 // 128-byte swizzle that TMA writes: groups of 8 rows are 1024 bytes apart.
-// Adding 2 to it moves 32 bytes (one instruction's K) along the row.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Only its low word depends on the address; adding 2 to it moves 32 bytes (one
+// instruction's K) along the row.
+__device__ __forceinline__ uint32_t operand_desc_low(uint32_t addr) {
+    return ((addr & 0x3ffff) >> 4) | (1u << 16);
 }
+constexpr uint32_t kOperandDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // Descriptor of 32 rows x 16 bytes without swizzle, 8 rows every 128 bytes.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
     return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
@@ -202,20 +209,26 @@ __device__ __forceinline__ uint32_t mma_scale_ids(uint32_t id) { return (id << 4
 // CG = 2: one product over a pair of CTAs, issued by the first: each holds 128
 // of the 256 rows of A and of the result, and half of B's rows.
 template <int CG>
-__device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+__device__ __forceinline__ void mma_mxf8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa,
                                          uint32_t sb, bool accumulate) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %7};\n\t"
+            "mov.b64 b, {%2, %7};\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(accumulate)) : "memory");
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], a, b, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(accumulate)),
+              "n"(kOperandDescHigh) : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %7};\n\t"
+            "mov.b64 b, {%2, %7};\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(accumulate)) : "memory");
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], a, b, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(accumulate)),
+              "n"(kOperandDescHigh) : "memory");
 }
 // The barrier (in a pair: of both CTAs, at the same place) gets one arrival
 // when everything this thread issued so far is done.
