@@ -54,33 +54,38 @@ __device__ unsigned long long g_timeouts;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 constexpr int kTileP = 128;              // rows of B a tile: the instruction's M
-constexpr int kStageBlocks = 2;          // blocks of 128 along K of a stage
+// Blocks of 128 along K of a stage.  A pair, which waits for loads more than
+// for anything else, has as many stages on their way as fit; a CTA alone
+// spends more on a stage's bookkeeping.
+template <int CG> __host__ __device__ constexpr int stage_blocks() { return CG == 2 ? 1 : 2; }
 constexpr int kScaleSlots = 4;           // scale words on their way, of four blocks each
 
-// Stages of a segment of a 32-bit result.
-constexpr int kSegment = 8;
+// Blocks of K of a segment of a 32-bit result.
+constexpr int kSegment = 16;
 
 // Drain warps: 32-bit results keep a tile's sums in registers (128 a thread).
 template <class T> __host__ __device__ constexpr int drain_warps() { return sizeof(T) == 4 ? 8 : 4; }
 template <class T> __host__ __device__ constexpr int cta_threads() { return 128 + 32 * drain_warps<T>(); }
-// 32 rows of 32 16-bit results, two a drain warp
-constexpr int kOutBytes = 32 * 64, kOutBuffers = 2;
-constexpr int kOutTotal = 4 * kOutBuffers * kOutBytes;
+constexpr int kOutBytes = 32 * 64;       // 32 rows of 32 16-bit results
 
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarrierBytes = 512;
 
 // Sizes of a CTA whose tile is BN rows of A wide; CG = 2: of each CTA of a
 // pair, which loads half of those rows.
-template <int BN, int CG> struct Sizes {
+template <int BN, int CG, class T> struct Sizes {
+    static constexpr int kBlocks = stage_blocks<CG>();
     static constexpr int kRowsQ = BN / CG;
     static constexpr int kBlockP = kTileP * kBlock;            // bytes of one block of a stage
     static constexpr int kBlockQ = kRowsQ * kBlock;
-    static constexpr int kStage = kStageBlocks * (kBlockP + kBlockQ);
+    static constexpr int kStage = kBlocks * (kBlockP + kBlockQ);
     // scales of 128 rows x 4 blocks are 512 bytes; B's 128 rows, then A's BN
     static constexpr int kScale = 512 + (BN > 128 ? 1024 : 512);
     static constexpr int kScaleColumns = kScale / 128;
-    static constexpr int kFixed = 1024 + kOutTotal + kScaleSlots * kScale + kBarrierBytes;
+    // results on their way out, one or two buffers for each of four drain warps
+    static constexpr int kOutBuffers = CG == 2 ? 1 : 2;
+    static constexpr int kOut = sizeof(T) == 4 ? 0 : 4 * kOutBuffers * kOutBytes;
+    static constexpr int kFixed = 1024 + kOut + kScaleSlots * kScale + kBarrierBytes;
     static constexpr int kStages = (kSmemLimit - kFixed) / kStage;
     static constexpr int kSmem = kFixed + kStages * kStage;
     // Tensor-memory columns: two accumulators and the scale slots.
@@ -91,7 +96,6 @@ template <int BN, int CG> struct Sizes {
     static_assert(kNeed <= 512, "tensor memory");
     static_assert(8 * kBarriers + 8 <= kBarrierBytes, "barriers");
     static_assert(kBlockQ % 1024 == 0, "swizzle");
-    static_assert(kStageBlocks == 2, "the products' loop");
 };
 
 constexpr int kMaxSplit = 4;             // CTAs that share K: eight rarely fit a GPC at once
@@ -204,12 +208,13 @@ template <int BN, int CG, class T>
 __global__ void __launch_bounds__(cta_threads<T>(), 1)
 matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_p,
               const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_c) {
-    using S = Sizes<BN, CG>;
-    constexpr int ST = S::kStages, DW = drain_warps<T>();
+    using S = Sizes<BN, CG, T>;
+    constexpr int ST = S::kStages, DW = drain_warps<T>(), SB = S::kBlocks;
+    constexpr int WS = 4 / SB;                            // stages of a word of scales
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     uint8_t *out_smem = smem + ST * S::kStage;
-    uint8_t *scale_smem = out_smem + kOutTotal;
+    uint8_t *scale_smem = out_smem + S::kOut;
     uint64_t *bars = reinterpret_cast<uint64_t *>(scale_smem + kScaleSlots * S::kScale);
     const uint32_t stage0 = smem_addr(smem), scale0 = smem_addr(scale_smem);
     const uint32_t full = smem_addr(bars), empty = full + 8 * ST;
@@ -227,7 +232,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     const int first = int(blockIdx.x) / sharing, step = int(gridDim.x) / sharing;
     const int s0 = int(int64_t(a.ns) * rank / a.split), s1 = int(int64_t(a.ns) * (rank + 1) / a.split);
     // one accumulator takes `segment` stages; a tile has `segments`
-    const int segment = sizeof(T) == 4 ? kSegment : a.ns;
+    const int segment = sizeof(T) == 4 ? kSegment / SB : a.ns;
     const int segments = (s1 - s0 + segment - 1) / segment;
 
     if (warp == 0 && lane == 0) {
@@ -281,14 +286,14 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t to = stage0 + ring.at * S::kStage, bar = full + 8 * ring.at;
-                    const int kb = s * kStageBlocks, blocks = min(kStageBlocks, a.nk - kb);
+                    const int kb = s * SB, blocks = min(SB, a.nk - kb);
                     // the leader's barrier counts both CTAs' bytes
                     if (peer == 0) mbar_expect_tx(bar, CG * blocks * (S::kBlockP + S::kBlockQ));
 #pragma unroll
-                    for (int i = 0; i < kStageBlocks; ++i) {
+                    for (int i = 0; i < SB; ++i) {
                         if (i >= blocks) break;
                         const uint32_t to_p = to + i * S::kBlockP;
-                        const uint32_t to_q = to + kStageBlocks * S::kBlockP + i * S::kBlockQ;
+                        const uint32_t to_q = to + SB * S::kBlockP + i * S::kBlockQ;
                         const int x = (kb + i) * kBlock;
                         if constexpr (CG == 2) {
                             tma_load_2d_pair(to_p, &map_p, x, p, lead_full + 8 * ring.at);
@@ -320,7 +325,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 int left = 0;                             // stages left of the segment
                 for (int s = s0; s < s1; ++s) {
                     const bool fresh = left == 0;
-                    const bool scales = s == s0 || s % 2 == 0;   // a new word: four blocks
+                    const bool scales = s == s0 || s % WS == 0;  // a new word: four blocks
                     if (fresh) {
                         left = segment;
                         // drained of the sum before the last
@@ -333,7 +338,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     const uint32_t at = ring.at;
                     ring.next();
                     ready = mbar_test(full + 8 * ring.at, ring.turn);   // known by the time it is asked
-                    const bool last = --left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % 2 == 1;
+                    const bool last = --left == 0 || s + 1 == s1, word_done = s + 1 == s1 || s % WS == WS - 1;
                     const uint32_t sf = tmem + S::kScaleBase + words.at * S::kScaleColumns;
                     if (scales) {
                         const uint64_t src = scale_desc(scale0 + words.at * S::kScale);
@@ -342,16 +347,15 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     }
                     const uint32_t acc = tmem + accs.at * BN;
                     const uint32_t dp = operand_desc_low(stage0) + at * (S::kStage / 16);
-                    const uint32_t dq = dp + kStageBlocks * S::kBlockP / 16;
-                    const uint32_t idesc = mma_desc(CG * kTileP, BN) | mma_scale_ids((s & 1) * kStageBlocks);
+                    const uint32_t dq = dp + SB * S::kBlockP / 16;
+                    const uint32_t idesc = mma_desc(CG * kTileP, BN) | mma_scale_ids(s % WS * SB);
 #pragma unroll
-                    for (int k = 0; k < kBlock / 32; ++k)
-                        mma_mxf8<CG>(acc, dp + 2 * k, dq + 2 * k, idesc, sf, sf + 4, !fresh || k > 0);
-                    if (s * kStageBlocks + 1 < a.nk) {
+                    for (int i = 0; i < SB; ++i) {
+                        if (i > 0 && s * SB + i >= a.nk) break;
 #pragma unroll
                         for (int k = 0; k < kBlock / 32; ++k)
-                            mma_mxf8<CG>(acc, dp + S::kBlockP / 16 + 2 * k, dq + S::kBlockQ / 16 + 2 * k,
-                                         idesc + mma_scale_ids(1), sf, sf + 4, true);
+                            mma_mxf8<CG>(acc, dp + i * (S::kBlockP / 16) + 2 * k, dq + i * (S::kBlockQ / 16) + 2 * k,
+                                         idesc + mma_scale_ids(i), sf, sf + 4, !fresh || i > 0 || k > 0);
                     }
                     mma_commit<CG>(empty + 8 * at);
                     if (word_done) mma_commit<CG>(sempty + 8 * words.at);
@@ -379,7 +383,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         Ring<kScaleSlots> words, passed;
         uint32_t issued = 0;
         bool ok = true;
-        const int g0 = s0 / 2, g1 = (s1 + 1) / 2;
+        const int g0 = s0 / WS, g1 = (s1 + WS - 1) / WS;
         auto pass_on = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(swritten + 8 * passed.at);
@@ -431,7 +435,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         Ring<kScaleSlots> words;
         bool ok = true;
         for (int t = first; t < a.tiles && ok; t += step)
-            for (int g = s0 / 2; g < (s1 + 1) / 2; ++g, words.next()) {
+            for (int g = s0 / WS; g < (s1 + WS - 1) / WS; ++g, words.next()) {
                 ok = __all_sync(0xffffffffu, wait(swritten + 8 * words.at, words.turn));
                 if (!ok) break;
                 fence_async_shared();
@@ -525,7 +529,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     }
                 const uint32_t acc = next_accumulator();
                 constexpr int CH = BN < 32 ? 1 : BN / 32;  // chunks of 32 columns (a narrow tile: 16 used)
-                const uint32_t out0 = smem_addr(out_smem) + quarter * kOutBuffers * kOutBytes;
+                const uint32_t out0 = smem_addr(out_smem) + quarter * S::kOutBuffers * kOutBytes;
                 // row lane % 8 of matrix lane / 8: 16 bytes in the 64-byte swizzle
                 const int r8 = lane % 8, piece = lane / 8;
                 for (int ch = 0; ch < CH; ++ch) {
@@ -539,8 +543,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0x7fffffffu;
                     }
                     if (ch + 1 == CH) release();
-                    const uint32_t buf = out0 + (ch % kOutBuffers) * kOutBytes;
-                    if (lane == 0) tma_store_wait_read<kOutBuffers - 1>();
+                    const uint32_t buf = out0 + (ch % S::kOutBuffers) * kOutBytes;
+                    if (lane == 0) tma_store_wait_read<S::kOutBuffers - 1>();
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -692,7 +696,7 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
     auto consider = [&](int bn, int pair, int split) {
         const int cg = 1 + pair;
         const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP * cg);
-        if (split > 1 && (split > ceil_div(nk, kStageBlocks) || tiles * split > sms)) return;
+        if (split > 1 && (split > ceil_div(nk, stage_blocks<1>()) || tiles * split > sms)) return;
         // a block's products, its loads, or what issuing them takes
         const double block = std::max({2.0 * bn, (kTileP + bn / cg) * kBlock / (pair ? 57.0 : 68.0), 280.0});
         const double rounds = double(ceil_div(tiles * split * cg, sms));
@@ -728,14 +732,14 @@ basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8
     if (cudaGetDevice(&dev) != cudaSuccess) return BASP_ERR_CUDA;
     if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(matmul_kernel<BN, CG, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Sizes<BN, CG>::kSmem) != cudaSuccess) {
+                                 Sizes<BN, CG, T>::kSmem) != cudaSuccess) {
             cudaGetLastError();
             return BASP_ERR_CUDA;
         }
         if (dev < 64) ready[dev].store(true, std::memory_order_release);
     }
     const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles * CG, sms / CG * CG);
-    return launch(matmul_kernel<BN, CG, T>, dim3(unsigned(ctas)), dim3(cta_threads<T>()), Sizes<BN, CG>::kSmem,
+    return launch(matmul_kernel<BN, CG, T>, dim3(unsigned(ctas)), dim3(cta_threads<T>()), Sizes<BN, CG, T>::kSmem,
                   a.split * CG, stream, a, map_p, map_q, map_c);
 }
 
@@ -755,7 +759,7 @@ basp_status run(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8_matrix *q
     if (tiles > (int64_t(1) << 30)) return BASP_ERR_TOO_LARGE;
     a.tiles = int(tiles);
     a.split = s.split;
-    a.ns = int(ceil_div(a.nk, kStageBlocks));
+    a.ns = int(ceil_div(a.nk, s.pair ? stage_blocks<2>() : stage_blocks<1>()));
     switch (s.bn) {
         case 16: return launch_matmul<16, 1, T>(a, p, q, sms, stream);
         case 32: return launch_matmul<32, 1, T>(a, p, q, sms, stream);
