@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "basp.h"
+#include "basp_fp8.h"
 
 namespace basp {
 
@@ -102,6 +103,34 @@ private:
     basp_layout *handle_ = nullptr;
     basp_info info_{};
 };
+
+// ---- the 8-bit projections (basp_fp8.h): the same calls, throwing ------------
+
+inline void rmsnorm(basp_dtype dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                    const void *residual, int64_t residual_stride, const void *weight,
+                    basp_dtype weight_dtype, float eps, void *h, int64_t h_stride, void *y,
+                    int64_t y_stride, const basp_fp8_matrix *q, float *rstd, cudaStream_t stream) {
+    check(basp_rmsnorm(dtype, rows, cols, x, x_stride, residual, residual_stride, weight, weight_dtype,
+                       eps, h, h_stride, y, y_stride, q, rstd, stream), "basp_rmsnorm");
+}
+inline void rmsnorm_backward(basp_dtype dtype, int64_t rows, int64_t cols, const void *dy,
+                             int64_t dy_stride, const void *h, int64_t h_stride, const float *rstd,
+                             const void *weight, basp_dtype weight_dtype, const void *dh,
+                             int64_t dh_stride, void *dx, int64_t dx_stride, float *dweight,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    check(basp_rmsnorm_backward(dtype, rows, cols, dy, dy_stride, h, h_stride, rstd, weight,
+                                weight_dtype, dh, dh_stride, dx, dx_stride, dweight, workspace,
+                                workspace_bytes, stream), "basp_rmsnorm_backward");
+}
+inline void quantize_fp8(basp_dtype dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                         const basp_fp8_matrix *q, const basp_fp8_matrix *qt, cudaStream_t stream) {
+    check(basp_quantize_fp8(dtype, rows, cols, x, x_stride, q, qt, stream), "basp_quantize_fp8");
+}
+inline void matmul_fp8(const basp_fp8_matrix &a, const basp_fp8_matrix &b, const void *bias,
+                       bool accumulate, basp_dtype dtype, void *c, int64_t c_stride,
+                       cudaStream_t stream) {
+    check(basp_matmul_fp8(&a, &b, bias, accumulate, dtype, c, c_stride, stream), "basp_matmul_fp8");
+}
 
 }  // namespace basp
 
