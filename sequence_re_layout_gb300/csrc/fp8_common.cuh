@@ -8,6 +8,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "basp_fp8.h"
 
@@ -116,16 +117,22 @@ template <> struct Pack<__half> {
     }
 };
 
-// Four values of a 128-block for one lane.  VEC: columns 4*lane .. 4*lane+3 in
-// one access (the row is aligned to four elements).  Otherwise columns lane,
-// lane+32, lane+64, lane+96, so that a warp's accesses still fall next to
-// each other, whatever the row's alignment.
+// How a warp's lanes touch a 128-block, four values each.
+//   kVector: columns 4*lane .. 4*lane+3 in one access (rows aligned to four
+//            elements, and their number a multiple of four)
+//   kStrided: columns lane, lane+32, lane+64, lane+96, so that a warp's
+//            accesses still fall next to each other, whatever the alignment
+//   kWhole:  as kStrided for a block that ends inside its row: no checks, so
+//            that the loads of several blocks go out together
+enum : int { kStrided = 0, kVector = 1, kWhole = 2 };
+template <int HOW> using How = std::integral_constant<int, HOW>;
+
 // `row` points to the block's first element; `left` columns of the block
 // exist.  Values past the end read as zero.
-template <class T, bool VEC>
+template <class T, int HOW>
 __device__ __forceinline__ void load4(const T *row, int lane, int left, float (&v)[4]) {
-    if (VEC) {
-        if (4 * lane < left) {            // left % 4 == 0 whenever VEC
+    if constexpr (HOW == kVector) {
+        if (4 * lane < left) {            // left % 4 == 0 whenever kVector
             const Vec4<T> x = *reinterpret_cast<const Vec4<T> *>(row + 4 * lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = Elem<T>::to_float(x.v[j]);
@@ -136,7 +143,7 @@ __device__ __forceinline__ void load4(const T *row, int lane, int left, float (&
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[j] = lane + 32 * j < left ? Elem<T>::to_float(row[lane + 32 * j]) : 0.f;
+            v[j] = HOW == kWhole || lane + 32 * j < left ? Elem<T>::to_float(row[lane + 32 * j]) : 0.f;
     }
 }
 
@@ -156,9 +163,9 @@ template <int N> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <class T, bool VEC>
+template <class T, int HOW>
 __device__ __forceinline__ void store4(T *row, int lane, int left, const float (&v)[4]) {
-    if (VEC) {
+    if constexpr (HOW == kVector) {
         if (4 * lane < left) {
             Vec4<T> x;
 #pragma unroll
@@ -168,7 +175,7 @@ __device__ __forceinline__ void store4(T *row, int lane, int left, const float (
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (lane + 32 * j < left) row[lane + 32 * j] = Elem<T>::from_float(v[j]);
+            if (HOW == kWhole || lane + 32 * j < left) row[lane + 32 * j] = Elem<T>::from_float(v[j]);
     }
 }
 
@@ -246,14 +253,14 @@ __device__ __forceinline__ uint32_t row_scale(float (&v)[4]) {
     return scale_byte(m);
 }
 
-template <bool VEC>
+template <int HOW>
 __device__ __forceinline__ void store4_e4m3(uint8_t *row, int lane, int left, uint32_t q) {
-    if (VEC) {
+    if constexpr (HOW == kVector) {
         if (4 * lane < left) *reinterpret_cast<uint32_t *>(row + 4 * lane) = q;
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (lane + 32 * j < left) row[lane + 32 * j] = uint8_t(q >> (8 * j));
+            if (HOW == kWhole || lane + 32 * j < left) row[lane + 32 * j] = uint8_t(q >> (8 * j));
     }
 }
 
