@@ -44,6 +44,7 @@
 #include <atomic>
 
 #include "fp8_common.cuh"
+#include "matvec.cuh"
 #include "tcgen05.cuh"
 
 namespace basp_fp8 {
@@ -790,6 +791,32 @@ extern "C" basp_status basp_matmul_fp8(const basp_fp8_matrix *a, const basp_fp8_
     args.matrix(c, a->rows, b->rows, c_stride, esz, true);
     st = args.status();
     if (st != BASP_OK || a->rows == 0 || b->rows == 0) return st;
+
+    if (takes_matvec(a->rows, b->rows, a->cols)) {
+        MatvecArgs v = {};
+        v.x = static_cast<const uint8_t *>(a->data);
+        v.w = static_cast<const uint8_t *>(b->data);
+        v.sx = static_cast<const uint8_t *>(a->scales);
+        v.sw = static_cast<const uint8_t *>(b->scales);
+        v.x_pitch = a->pitch;
+        v.w_pitch = b->pitch;
+        v.sx_pitch = a->scale_pitch;
+        v.sw_pitch = b->scale_pitch;
+        v.sx_shift = a->block_rows == 1 ? 0 : 7;
+        v.sw_shift = b->block_rows == 1 ? 0 : 7;
+        v.c = c;
+        v.bias = bias;
+        v.c_stride = c_stride;
+        v.M = int(a->rows);
+        v.N = int(b->rows);
+        v.K = int(a->cols);
+        v.accumulate = accumulate != 0;
+        switch (dtype) {
+            case BASP_DTYPE_BF16: return launch_matvec<__nv_bfloat16>(v, stream);
+            case BASP_DTYPE_FP16: return launch_matvec<__half>(v, stream);
+            default: return launch_matvec<float>(v, stream);
+        }
+    }
 
     MatmulArgs m = {};
     m.sp = static_cast<const uint8_t *>(b->scales);

@@ -323,6 +323,54 @@ def test_matmul_bias_accumulate_and_stride(M, N, K, out):
     check_product(fp8.matmul(a, b, bias=bias, out_dtype=t), a64, b64, K, f64(bias))
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (2, 17, 128), (3, 33, 1543), (8, 16, 16), (7, 1, 100), (5, 2432, 4100), (8, 130, 8192), (4, 2433, 4224),
+    (8, 8191, 300), (1, 8191, 2040), (2, 8193, 1100), (9, 200, 700), (1, 40, 20000)])
+@pytest.mark.parametrize("out", sorted(DTYPES))
+@pytest.mark.parametrize("blocks", [1, 128])
+def test_matmul_of_few_tokens(M, N, K, out, blocks):
+    """Both kernels that take few tokens, with blocks of either side's rows."""
+    t = DTYPES[out]
+    a, a64 = quantized(M, K, blocks, 1)
+    b, b64 = quantized(N, K, 129 - blocks, 2)
+    if out == "fp16":                                          # fp16 ends at 65504
+        a64, b64 = a64 * 2.0 ** -12, b64 * 2.0 ** -8
+        a.scales.view(torch.uint8).sub_(12)
+        b.scales.view(torch.uint8).sub_(8)
+    bias, base = random(1, N, t, 5)[0], random(M, N, t, 6)
+    store = torch.full((M, N + 5), 7.0, dtype=t, device="cuda")
+    c = store[:, :N]
+    c.copy_(base)
+    fp8.matmul(a, b, bias=bias, out=c, accumulate=True)
+    check_product(c, a64, b64, K, f64(bias), f64(base))
+    assert bool((store[:, N:] == 7).all())
+    first = fp8.matmul(a, b, out_dtype=t)
+    check_product(first, a64, b64, K)
+    assert torch.equal(fp8.matmul(a, b, out_dtype=t), first)
+
+
+@pytest.mark.parametrize("M", [1, 8])
+def test_matmul_of_few_tokens_scales_and_nan(M):
+    """Scales whose product leaves a float's range, that come back into it, and
+    that are NaN; NaN and zeros in the values."""
+    a, a64 = quantized(M, 512, 1, 1)
+    b, b64 = quantized(5, 512, 1, 2)
+    ea, eb = (torch.tensor(e) for e in ([-127, 127, 60, -60], [127, -127, -60, 60]))
+    a.scales.view(torch.uint8).copy_((ea + 127).to(torch.uint8).expand(M, 4))
+    b.scales.view(torch.uint8).copy_((eb + 127).to(torch.uint8).expand(5, 4))
+    av, bv = f64(a.data), f64(b.data)
+    check_product(fp8.matmul(a, b, out_dtype=torch.float32), av, bv, 512)
+    a.scales.view(torch.uint8).fill_(1)                        # 2^-252 in all: nothing is left
+    b.scales.view(torch.uint8).fill_(1)
+    assert bool((fp8.matmul(a, b, out_dtype=torch.float32) == 0).all())
+    b.scales.view(torch.uint8).fill_(253)                      # 2^0 again
+    check_product(fp8.matmul(a, b, out_dtype=torch.float32), av, bv, 512)
+    b.scales.view(torch.uint8)[2, 1] = 255
+    b.data.view(torch.uint8)[3, 500] = 0x7f
+    got = torch.isnan(fp8.matmul(a, b, out_dtype=torch.float32)).cpu()
+    assert got[:, 2:4].all() and not got[:, :2].any() and not got[:, 4].any()
+
+
 def test_matmul_of_128_row_blocks_on_both_sides():
     a, a64 = quantized(300, 400, 128, 1)
     b, b64 = quantized(200, 400, 128, 2)
