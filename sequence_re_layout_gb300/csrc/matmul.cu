@@ -689,8 +689,8 @@ struct Shape {
 // hides.  The figures are fits to GPU times on 152 SMs: one tile of K = 2048
 // takes 5.0 us at 16 wide, 6.8 at 128, 8.7 in a pair 192 wide, and 0.15, 0.19
 // and 0.20 us for each further block; beside other CTAs an SM gets 57 to 68
-// bytes a cycle from L2; a split into 4 saves 5.5 us at one token and K =
-// 8192 (6.6 instead of 12.1) and loses 1.2 at K = 2048.
+// bytes a cycle from L2; a split into 4 takes 6.9 us instead of 11.9 at 16 x
+// 1024 x 8192, and 5.2 instead of 5.0 at 16 x 2048 x 2048.
 Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
     Shape best = {128, 0, 1};
     double best_cost = 1e300;
@@ -703,7 +703,7 @@ Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
         const double rounds = double(ceil_div(tiles * split * cg, sms));
         const double start = pair ? 9000 + 8.0 * bn : 5000 + 15.0 * bn;
         const double cost = start + rounds * double(ceil_div(nk, split)) * block +
-                            (split > 1 ? 2000 + 70.0 * bn : 0);
+                            (split > 1 ? 3000 + 70.0 * bn : 0);
         if (cost < best_cost) {
             best_cost = cost;
             best = {bn, pair, split};

@@ -128,7 +128,9 @@ struct Fp8 {
 
 Fp8 new_fp8(int64_t rows, int64_t cols, int64_t block_rows, const c10::Device &device) {
     const int64_t blocks = ceil_div(cols, kBlock), srows = ceil_div(rows, block_rows);
-    const int64_t pitch = round_up(cols, 16), spitch = round_up(blocks, 4);
+    // A product reads rows in pieces of 128 bytes: 1021 x 2999 x 1543 takes 10.6
+    // us where those are whole cache lines, 11.0 where they are not.
+    const int64_t pitch = round_up(cols, cols > 128 ? 128 : 16), spitch = round_up(blocks, 4);
     const auto options = at::TensorOptions().device(device);
     Fp8 f;
     f.data = at::empty_strided({rows, cols}, {pitch, 1}, options.dtype(at::kFloat8_e4m3fn));

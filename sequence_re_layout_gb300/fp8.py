@@ -39,7 +39,7 @@ class Quantized:
     (r, c) stands for ``data[r, c] * scales[r // block_rows, c // 128]``.
 
     Rows of ``data`` start at multiples of 16 bytes and rows of ``scales`` at
-    multiples of 4, as :meth:`empty` lays them out.  The call that uses a matrix
+    multiples of 4; :meth:`empty` lays them out.  The call that uses a matrix
     checks it."""
 
     __slots__ = ("data", "scales", "block_rows")
@@ -49,12 +49,13 @@ class Quantized:
 
     @classmethod
     def empty(cls, rows, cols, block_rows=1, device="cuda"):
-        """Uninitialised, with rows of ``data`` padded to 16 bytes and rows of
-        ``scales`` to 4."""
+        """Uninitialised, with rows of ``data`` padded to 16 bytes (longer ones
+        than 128 to that, the cache line a product reads) and rows of ``scales``
+        to 4."""
         if block_rows not in (1, BLOCK):
             raise ValueError("Quantized: block_rows must be 1 or %d" % BLOCK)
-        blocks = -(-cols // BLOCK)
-        return cls(torch.empty_strided((rows, cols), (-(-cols // 16) * 16, 1), dtype=torch.float8_e4m3fn,
+        blocks, step = -(-cols // BLOCK), 128 if cols > 128 else 16
+        return cls(torch.empty_strided((rows, cols), (-(-cols // step) * step, 1), dtype=torch.float8_e4m3fn,
                                        device=device),
                    torch.empty_strided((-(-rows // block_rows), blocks), (-(-blocks // 4) * 4, 1),
                                        dtype=torch.float8_e8m0fnu, device=device), block_rows)
