@@ -84,7 +84,7 @@ template <int BN, int CG, class T> struct Sizes {
     static constexpr int kScale = 512 + (BN > 128 ? 1024 : 512);
     static constexpr int kScaleColumns = kScale / 128;
     // results on their way out, one or two buffers for each of four drain warps
-    static constexpr int kOutBuffers = CG == 2 ? 1 : 2;
+    static constexpr int kOutBuffers = BN > 192 ? 1 : 2;   // a seventh stage is worth more
     static constexpr int kOut = sizeof(T) == 4 ? 0 : 4 * kOutBuffers * kOutBytes;
     static constexpr int kFixed = 1024 + kOut + kScaleSlots * kScale + kBarrierBytes;
     static constexpr int kStages = (kSmemLimit - kFixed) / kStage;
@@ -486,6 +486,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         if (ok) {
                             tmem_load16(acc + j0 + 16 * i, v);
                             tmem_load_wait();
+                            tmem_loaded(v);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
@@ -539,6 +540,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         tmem_load_fragments(acc + 32 * ch, v[0]);
                         tmem_load_fragments(acc + 32 * ch + (16u << 16), v[1]);
                         tmem_load_wait();
+                        tmem_loaded(v[0]);
+                        tmem_loaded(v[1]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0x7fffffffu;
@@ -575,6 +578,7 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     if (ok) {
                         tmem_load16(acc + j0, v);
                         tmem_load_wait();
+                        tmem_loaded(v);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
