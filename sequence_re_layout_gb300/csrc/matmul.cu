@@ -16,13 +16,26 @@
 // coalesced whatever the row stride, the bias is one value a thread, and one
 // token costs a 16-wide instruction instead of a padded 128-row one.
 //
-// A CTA has a warp that issues TMA loads (128 bytes of K a stage, in the
-// 128-byte swizzle), one that issues the products, one that brings scales,
-// and four or eight that drain accumulators.  Large products run a persistent
-// CTA per SM whose accumulator is double-buffered, so a tile's drain overlaps
-// the next tile's products.  With few tiles, a cluster of CTAs splits K; the
-// parts meet in shared memory and are added in rank order, so results do not
-// depend on timing.
+// Up to eight tokens against a B of ordinary size have a kernel of their own
+// (matvec.cuh).
+//
+// A CTA's warps.  0 issues TMA loads (in the 128-byte swizzle; a stage is 256
+// values of K, 128 in a pair).  One thread of 1 issues the products, all of its
+// loop inside one election.  2 copies scales to shared memory, 3 passes them on
+// to the products: a fence waits for its own warp's copies, so one warp for both
+// cost 3000 cycles for each four blocks.  Four or eight more drain accumulators.
+// Large products run a persistent CTA per SM, or a pair of CTAs (cta_group::2, each
+// loading half of A's rows), whose accumulator is double-buffered, so a tile's
+// drain overlaps the next tile's products.  With few tiles, a cluster of CTAs
+// splits K; the parts meet in shared memory and are added in rank order, so
+// results do not depend on timing.
+//
+// What bounds it.  32768 x 6144 x 2048 takes 255 to 265 us (3.1 to 3.2 PFLOP/s),
+// 211 at twice the measured bf16 rate: loads from L2 (57 to 68 bytes a cycle and
+// SM, each operand byte read once a tile) and, over seconds, the power limit (300
+// us).  A pair reads a third less of L2 than CTAs 128 wide do, which took 298 us.
+// Small products take 5 us (64 x 2048 x 2048, 0.7 of it the bytes): a launch,
+// barriers, one trip to memory, a drain.
 //
 // Drain.  16-bit results leave tensor memory as matrix fragments, which
 // stmatrix transposes into 64-byte rows of C in shared memory, and TMA stores
