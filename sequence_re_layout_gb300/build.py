@@ -64,7 +64,7 @@ def _torch_command(out):
             "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             "-I", os.path.join(cuda or "/usr/local/cuda", "include"),
             TORCH_OPS_SOURCE, "-o", out, "-L", libs, "-Wl,-rpath," + libs,
-            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:

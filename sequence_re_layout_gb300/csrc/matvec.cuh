@@ -8,10 +8,10 @@
 // values of K; the sum over a block of 128 is scaled in 32 bits.
 //
 // What bounds it: latency (a launch, one trip to memory, one join: 2.4 us at
-// 2048 x 2048), then mma.sync itself, which turns e4m3 operands into 16-bit ones
-// in the conversion units; past some 16 million values of B that takes longer
-// than reading them (131072 x 2048: 50 us, 42 on tcgen05).  In registers of 80
-// a thread 24 warps fit an SM (64: 1 us more at 6144 x 2048).
+// 2048 x 2048), then mma.sync, which the counters show on the half-precision pipe,
+// so that e4m3 operands are converted first; past some 16 million values of B it
+// takes longer than reading them (131072 x 2048: 50 us, 42 on tcgen05).  In 80
+// registers a thread 24 warps fit an SM (64 registers: 1 us more at 6144 x 2048).
 #pragma once
 
 #include "fp8_common.cuh"
