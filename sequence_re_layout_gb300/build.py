@@ -18,7 +18,7 @@ TORCH_OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "quantize.cu", "matmul.cu"]
 HEADERS = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h")] + \
     [os.path.join(CSRC, h) for h in ("layout_internal.h", "relayout_kernel.cuh", "scratch_cache.h",
-                                     "fp8_common.cuh", "matvec.cuh", "tcgen05.cuh")]
+                                     "fp8_common.cuh", "matmul_plan.h", "matvec.cuh", "tcgen05.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

@@ -57,6 +57,7 @@
 #include <atomic>
 
 #include "fp8_common.cuh"
+#include "matmul_plan.h"
 #include "matvec.cuh"
 #include "tcgen05.cuh"
 
@@ -460,6 +461,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         float *part = reinterpret_cast<float *>(smem);     // [BN][128], split only
         Ring<2> accs;
+        using Out = OutRing<S::kOutBuffers>;
+        Out out;                                           // goes on from tile to tile
         bool ok = true;
         auto next_accumulator = [&]() {
             ok = __all_sync(0xffffffffu, ok && wait(acc_full + 8 * accs.at, accs.turn));
@@ -560,8 +563,8 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0x7fffffffu;
                     }
                     if (ch + 1 == CH) release();
-                    const uint32_t buf = out0 + (ch % S::kOutBuffers) * kOutBytes;
-                    if (lane == 0) tma_store_wait_read<S::kOutBuffers - 1>();
+                    const uint32_t buf = out0 + out.next() * kOutBytes;
+                    if (lane == 0) tma_store_wait_read<Out::kUnread>();
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
