@@ -40,8 +40,10 @@
 // Drain.  16-bit results leave tensor memory as matrix fragments, which
 // stmatrix transposes into 64-byte rows of C in shared memory, and TMA stores
 // them: about two instructions a value, where one store a value kept the
-// products waiting (2.2 PFLOP/s at 32768 x 6144 x 2048).  Rows of C that TMA
-// cannot address, and accumulation into C, take one store a value.
+// products waiting (2.2 PFLOP/s at 32768 x 6144 x 2048).  TMA gets whole 16 bytes
+// of a row only: a store clipped at an odd column wrote the element past it.  Up
+// to seven columns at a row's end, rows of C that TMA cannot address, and
+// accumulation into C take one store a value.
 //
 // Long sums.  The tensor cores' 32-bit accumulator truncates: after 1024
 // instructions (K = 32768) a sum is off by 8e-6 of its size, systematically.
@@ -82,6 +84,7 @@ constexpr int kSegment = 16;
 template <class T> __host__ __device__ constexpr int drain_warps() { return sizeof(T) == 4 ? 8 : 4; }
 template <class T> __host__ __device__ constexpr int cta_threads() { return 128 + 32 * drain_warps<T>(); }
 constexpr int kOutBytes = 32 * 64;       // 32 rows of 32 16-bit results
+constexpr int kOutAlign = 8;             // 16-bit results of the 16 bytes that TMA stores are made of
 
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarrierBytes = 512;
@@ -548,6 +551,9 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 const uint32_t acc = next_accumulator();
                 constexpr int CH = BN < 32 ? 1 : BN / 32;  // chunks of 32 columns (a narrow tile: 16 used)
                 const uint32_t out0 = smem_addr(out_smem) + quarter * S::kOutBuffers * kOutBytes;
+                // the columns past the last whole 16 bytes of a row, from the fragments
+                const int64_t tma_end = a.N / kOutAlign * kOutAlign;
+                const bool tail = tma_end < a.N && n0 + quarter * 32 + 32 > tma_end;
                 // row lane % 8 of matrix lane / 8: 16 bytes in the 64-byte swizzle
                 const int r8 = lane % 8, piece = lane / 8;
                 for (int ch = 0; ch < CH; ++ch) {
@@ -579,10 +585,24 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         store_matrix_transposed(buf + r * 64 + 16 * (piece ^ ((r >> 1) & 3)), p[0][0], p[0][1],
                                                 p[1][0], p[1][1]);
                     }
+                    if (tail) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const int q = j / 2 % 2;
+                                const int64_t k = n0 + quarter * 32 + 16 * h + 8 * q + lane / 4;
+                                const int64_t m = m0 + 32 * ch + j / 4 * 8 + lane % 4 * 2 + j % 2;
+                                const bool in_tile = BN >= 32 || j / 4 * 8 < BN;   // a narrow tile: 16 used
+                                if (in_tile && k >= tma_end && k < a.N && m < a.M)
+                                    static_cast<T *>(a.c)[m * a.c_stride + k] =
+                                        Elem<T>::from_float(__uint_as_float(v[h][j]) + fb[h][q]);
+                            }
+                    }
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        if (n0 + quarter * 32 < a.N && m0 + 32 * ch < a.M)
+                        if (n0 + quarter * 32 < tma_end && m0 + 32 * ch < a.M)
                             tma_store_2d(&map_c, buf, int(n0) + quarter * 32, int(m0) + 32 * ch);
                         tma_store_commit();               // also of nothing: buffers are counted in groups
                     }
@@ -686,11 +706,12 @@ bool encode(const basp_fp8_matrix *m, int box_rows, CUtensorMap *out) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Boxes of 32 x 32 16-bit results of C (16 rows where tiles are that narrow).
+// Boxes of 32 x 32 16-bit results of C (16 rows where tiles are that narrow), up
+// to the last whole 16 bytes of its rows.
 bool encode_out(const MatmulArgs &a, int box_rows, CUtensorMap *out) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(a.N), cuuint64_t(a.M)};
+    const cuuint64_t dims[2] = {cuuint64_t(a.N / kOutAlign * kOutAlign), cuuint64_t(a.M)};
     const cuuint64_t strides[1] = {cuuint64_t(a.c_stride) * 2};
     const cuuint32_t box[2] = {32, cuuint32_t(box_rows)};
     const cuuint32_t elem[2] = {1, 1};
@@ -743,8 +764,9 @@ basp_status launch_matmul(MatmulArgs a, const basp_fp8_matrix *p, const basp_fp8
                           cudaStream_t stream) {
     CUtensorMap map_p, map_q, map_c = {};
     // one row of C: its stride is free
-    if (a.M == 1) a.c_stride = ceil_div(a.N, 8) * 8;
-    a.tma_out = sizeof(T) == 2 && a.split == 1 && !a.accumulate && uintptr_t(a.c) % 16 == 0 && a.c_stride % 8 == 0;
+    if (a.M == 1) a.c_stride = ceil_div(a.N, kOutAlign) * kOutAlign;
+    a.tma_out = sizeof(T) == 2 && a.split == 1 && !a.accumulate && a.N >= kOutAlign &&
+                uintptr_t(a.c) % 16 == 0 && a.c_stride % kOutAlign == 0;
     if (!encode(p, kTileP, &map_p) || !encode(q, BN / CG, &map_q) ||
         (a.tma_out && !encode_out(a, BN < 32 ? BN : 32, &map_c)))
         return BASP_ERR_CUDA;
