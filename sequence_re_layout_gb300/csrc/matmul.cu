@@ -70,11 +70,6 @@ __device__ unsigned long long g_timeouts;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-constexpr int kTileP = 128;              // rows of B a tile: the instruction's M
-// Blocks of 128 along K of a stage.  A pair, which waits for loads more than
-// for anything else, has as many stages on their way as fit; a CTA alone
-// spends more on a stage's bookkeeping.
-template <int CG> __host__ __device__ constexpr int stage_blocks() { return CG == 2 ? 1 : 2; }
 constexpr int kScaleSlots = 4;           // scale words on their way, of four blocks each
 
 // Blocks of K of a segment of a 32-bit result.
@@ -115,8 +110,6 @@ template <int BN, int CG, class T> struct Sizes {
     static_assert(8 * kBarriers + 8 <= kBarrierBytes, "barriers");
     static_assert(kBlockQ % 1024 == 0, "swizzle");
 };
-
-constexpr int kMaxSplit = 4;             // CTAs that share K: eight rarely fit a GPC at once
 
 struct MatmulArgs {
     const uint8_t *sp, *sq;              // scales of B (P side) and A (Q side)
@@ -718,45 +711,6 @@ bool encode_out(const MatmulArgs &a, int box_rows, CUtensorMap *out) {
     return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.c, dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Shape {
-    int bn, pair, split;
-};
-
-// The tile (its width along A's rows, one CTA or a pair) and the number of
-// CTAs that split K with the least estimated time, in SM cycles: rounds of
-// tiles over the SMs, each paying for its blocks of K, and what no round
-// hides.  The figures are fits to GPU times on 152 SMs: one tile of K = 2048
-// takes 5.0 us at 16 wide, 6.8 at 128, 8.7 in a pair 192 wide, and 0.15, 0.19
-// and 0.20 us for each further block; beside other CTAs an SM gets 57 to 68
-// bytes a cycle from L2; a split into 4 takes 6.9 us instead of 11.9 at 16 x
-// 1024 x 8192, and 5.2 instead of 5.0 at 16 x 2048 x 2048.
-Shape pick_shape(int64_t M, int64_t N, int64_t nk, int sms) {
-    Shape best = {128, 0, 1};
-    double best_cost = 1e300;
-    auto consider = [&](int bn, int pair, int split) {
-        const int cg = 1 + pair;
-        const int64_t tiles = ceil_div(M, bn) * ceil_div(N, kTileP * cg);
-        if (split > 1 && (split > ceil_div(nk, stage_blocks<1>()) || tiles * split > sms)) return;
-        // a block's products, its loads, or what issuing them takes
-        const double block = std::max({2.0 * bn, (kTileP + bn / cg) * kBlock / (pair ? 57.0 : 68.0), 280.0});
-        const double rounds = double(ceil_div(tiles * split * cg, sms));
-        const double start = pair ? 9000 + 8.0 * bn : 5000 + 15.0 * bn;
-        const double cost = start + rounds * double(ceil_div(nk, split)) * block +
-                            (split > 1 ? 3000 + 70.0 * bn : 0);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = {bn, pair, split};
-        }
-    };
-    for (int bn = 16; bn <= 128; bn *= 2) {
-        if (bn > 16 && bn / 2 >= M) break;
-        for (int split = 1; split <= kMaxSplit; split *= 2) consider(bn, 0, split);
-    }
-    if (M > 128)
-        for (int bn : {224, 192}) consider(bn, 1, 1);
-    return best;
 }
 
 template <int BN, int CG, class T>

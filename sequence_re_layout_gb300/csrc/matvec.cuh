@@ -15,20 +15,12 @@
 #pragma once
 
 #include "fp8_common.cuh"
+#include "matmul_plan.h"
 
 namespace basp_fp8 {
 
-constexpr int kVecTokens = 8;
 constexpr int kVecRows = 16;              // rows of B a warp
 constexpr int kVecBlocks = 2;             // blocks of 128 along K that a warp is worth
-
-// Whether this kernel takes the product.  GPU times in us, one token, here and
-// on matmul.cu's tiles: 128 x 128 1.5, 2.8; 2048 x 2048 2.5, 4.9; 6144 x 2048
-// 3.5, 5.0; 8192 x 1024 3.4, 3.9; 4096 x 4096 5.0, 6.0; 512 x 16384 6.3, 8.8;
-// but 16384 x 1024 5.4, 4.2; 8192 x 2048 5.3, 5.1; 16384 x 2048 10.6, 7.9.
-inline bool takes_matvec(int64_t M, int64_t N, int64_t K) {
-    return M <= kVecTokens && K > 0 && N * K <= (N < 8192 ? int64_t(1) << 24 : int64_t(1) << 23);
-}
 
 struct MatvecArgs {
     const uint8_t *x, *w, *sx, *sw;       // A and B, and their scales

@@ -1,6 +1,10 @@
 // matmul_plan_test.cpp -- host test of sequence_re_layout_gb300/csrc/
 // matmul_plan.h.  Test program.
 //   matmul_plan_test         checks; exit status 0 and "matmul_plan ok" on success
+//   matmul_plan_test SMS M N K [M N K ...]
+//                            for each product: the tile's width (0: matvec.cuh),
+//                            whether by pairs, the CTAs that share K, the most
+//                            tiles of a CTA, and the blocks of K of one CTA
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
@@ -52,7 +56,22 @@ template <int BUFFERS> static void check_ring() {
     }
 }
 
-int main() {
+static void print_plan(int sms, int64_t M, int64_t N, int64_t K) {
+    using namespace basp_fp8;
+    if (takes_matvec(M, N, K)) {
+        std::printf("0 0 0 0 0\n");
+        return;
+    }
+    const int64_t nk = parts_of(K, BASP_FP8_BLOCK);
+    const Shape s = pick_shape(M, N, nk, sms);
+    const int64_t tiles = parts_of(M, s.bn) * parts_of(N, kTileP * (1 + s.pair)), places = sms / (1 + s.pair) / s.split;
+    std::printf("%d %d %d %d %d\n", s.bn, s.pair, s.split, int(parts_of(tiles, places)), int(nk / s.split));
+}
+
+int main(int argc, char **argv) {
+    for (int i = 2; i + 2 < argc; i += 3)
+        print_plan(std::atoi(argv[1]), std::atoll(argv[i]), std::atoll(argv[i + 1]), std::atoll(argv[i + 2]));
+    if (argc > 1) return 0;
     check_ring<1>();
     check_ring<2>();
     check_ring<3>();
