@@ -544,9 +544,10 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 const uint32_t acc = next_accumulator();
                 constexpr int CH = BN < 32 ? 1 : BN / 32;  // chunks of 32 columns (a narrow tile: 16 used)
                 const uint32_t out0 = smem_addr(out_smem) + quarter * S::kOutBuffers * kOutBytes;
-                // the columns past the last whole 16 bytes of a row, from the fragments
-                const int64_t tma_end = a.N / kOutAlign * kOutAlign;
-                const bool tail = tma_end < a.N && n0 + quarter * 32 + 32 > tma_end;
+                // TMA takes the warp's columns up to tma_end; up to seven more follow
+                const int64_t w0 = n0 + quarter * 32, tma_end = a.N / kOutAlign * kOutAlign;
+                const int tail_end = int(min(int64_t(32), a.N - w0));
+                const int tail0 = int(max(int64_t(0), min(int64_t(32), tma_end - w0)));
                 // row lane % 8 of matrix lane / 8: 16 bytes in the 64-byte swizzle
                 const int r8 = lane % 8, piece = lane / 8;
                 for (int ch = 0; ch < CH; ++ch) {
@@ -578,26 +579,20 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                         store_matrix_transposed(buf + r * 64 + 16 * (piece ^ ((r >> 1) & 3)), p[0][0], p[0][1],
                                                 p[1][0], p[1][1]);
                     }
-                    if (tail) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const int q = j / 2 % 2;
-                                const int64_t k = n0 + quarter * 32 + 16 * h + 8 * q + lane / 4;
-                                const int64_t m = m0 + 32 * ch + j / 4 * 8 + lane % 4 * 2 + j % 2;
-                                const bool in_tile = BN >= 32 || j / 4 * 8 < BN;   // a narrow tile: 16 used
-                                if (in_tile && k >= tma_end && k < a.N && m < a.M)
-                                    static_cast<T *>(a.c)[m * a.c_stride + k] =
-                                        Elem<T>::from_float(__uint_as_float(v[h][j]) + fb[h][q]);
-                            }
-                    }
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        if (n0 + quarter * 32 < tma_end && m0 + 32 * ch < a.M)
-                            tma_store_2d(&map_c, buf, int(n0) + quarter * 32, int(m0) + 32 * ch);
+                        if (w0 < tma_end && m0 + 32 * ch < a.M)
+                            tma_store_2d(&map_c, buf, int(w0), int(m0) + 32 * ch);
                         tma_store_commit();               // also of nothing: buffers are counted in groups
+                    }
+                    // a lane has a row of C; the buffer is written again after the next __syncwarp
+                    if (tail0 < tail_end && lane < BN && m0 + 32 * ch + lane < a.M) {
+                        T *to = static_cast<T *>(a.c) + (m0 + 32 * ch + lane) * a.c_stride + w0;
+#pragma unroll 1
+                        for (int k = tail0; k < tail_end; ++k)
+                            to[k] = *reinterpret_cast<const T *>(
+                                smem + (buf - stage0) + lane * 64 + 16 * (k / 8 ^ ((lane >> 1) & 3)) + k % 8 * 2);
                     }
                 }
             } else {
