@@ -307,15 +307,20 @@ struct NvtxRange {
 // SMs of the current device (152 on GB300); 1 if it cannot be read.
 int sm_count();
 
-// CTAs of `kernel` that fit on the current device at once; also lets the
-// kernel have `smem` bytes of dynamic shared memory (48 KB less its static
-// ones come unasked).
+// Lets KERNEL have up to MOST bytes of dynamic shared memory.  The limit belongs
+// to the function, for all host threads: each call sets the same one, whatever
+// its own launch needs, so none lowers it between another's setting and launch.
+template <auto KERNEL, size_t MOST> bool allow_shared_memory() {
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, int(MOST)) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
+// CTAs of `kernel` that fit on the current device at once.
 template <class K>
 int64_t resident_ctas(K kernel, int threads, size_t smem) {
     int per_sm = 0;
-    if ((smem > 16 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  int(smem)) != cudaSuccess) ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         per_sm = 1;
     }

@@ -371,11 +371,15 @@ basp_status launch_tiles(const QuantArgs &a, bool per_row, bool vec16, cudaStrea
         auto kernel = per_row ? quantize_any_tile_kernel<T, true> : quantize_any_tile_kernel<T, false>;
         return launch(kernel, dim3(unsigned(tiles)), dim3(kTileThreads), 0, 1, stream, a, int(blocks));
     }
-    auto kernel = per_row ? quantize_tile_kernel<T, true> : quantize_tile_kernel<T, false>;
-    const size_t smem = size_t(kTileAhead + 1) * kBlock * kBlock * sizeof(T);
-    const int64_t ctas = std::min(tiles, resident_ctas(kernel, kTileThreads, smem));
-    return launch(kernel, dim3(unsigned(ctas)), dim3(kTileThreads), smem, 1, stream, a, int(blocks),
-                  int(ceil_div(a.rows, kBlock)));
+    constexpr size_t smem = size_t(kTileAhead + 1) * kBlock * kBlock * sizeof(T);
+    auto tiles_of = [&](auto each_row) {
+        constexpr auto kernel = quantize_tile_kernel<T, decltype(each_row)::value>;
+        if (!allow_shared_memory<kernel, smem>()) return BASP_ERR_CUDA;
+        const int64_t ctas = std::min(tiles, resident_ctas(kernel, kTileThreads, smem));
+        return launch(kernel, dim3(unsigned(ctas)), dim3(kTileThreads), smem, 1, stream, a, int(blocks),
+                      int(ceil_div(a.rows, kBlock)));
+    };
+    return per_row ? tiles_of(std::true_type()) : tiles_of(std::false_type());
 }
 
 template <class T, bool VEC>

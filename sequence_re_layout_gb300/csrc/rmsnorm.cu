@@ -358,15 +358,19 @@ basp_status launch_norm(const NormArgs &a, cudaStream_t stream) {
     const bool few = a.rows <= 2 * sm_count();
     if (a.vec16 && !few) {
         const int vectors = int(a.cols / Pack<T>::N);
-        auto walk = [&](auto kernel, int nv) {
-            const int threads = int(ceil_div(vectors, nv * 32)) * 32;
-            const size_t smem = size_t(kAhead + 1) * 2 * nv * threads * 16;
+        auto walk = [&](auto vectors_each) {
+            constexpr int NV = decltype(vectors_each)::value;
+            constexpr auto kernel = norm_walk_kernel<T, W, NV>;
+            constexpr size_t per_thread = size_t(kAhead + 1) * 2 * NV * 16;
+            if (!allow_shared_memory<kernel, per_thread * kWalkThreads>()) return BASP_ERR_CUDA;
+            const int threads = int(ceil_div(vectors, NV * 32)) * 32;
+            const size_t smem = per_thread * threads;
             const int64_t ctas = std::min(a.rows, resident_ctas(kernel, threads, smem));
             return launch(kernel, dim3(unsigned(ctas)), dim3(threads), smem, 1, stream, a);
         };
-        if (vectors <= kWalkThreads) return walk(norm_walk_kernel<T, W, 1>, 1);
-        if (vectors <= 2 * kWalkThreads) return walk(norm_walk_kernel<T, W, 2>, 2);
-        if (vectors <= 4 * kWalkThreads) return walk(norm_walk_kernel<T, W, 4>, 4);
+        if (vectors <= kWalkThreads) return walk(std::integral_constant<int, 1>());
+        if (vectors <= 2 * kWalkThreads) return walk(std::integral_constant<int, 2>());
+        if (vectors <= 4 * kWalkThreads) return walk(std::integral_constant<int, 4>());
     }
     if (blocks <= 4 && !few) {            // one warp a row, four rows a CTA
         return launch(norm_kernel<T, W, 4, VEC>, dim3(unsigned(ceil_div(a.rows, 4))), dim3(32, 4), 0, 1,
@@ -617,14 +621,16 @@ basp_status launch_norm_back(const NormBackArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(back_parts(a.rows)));
     if (a.vec16) {
         const int vectors = int(a.cols / Pack<T>::N);
-        auto walk = [&](auto kernel, int nv) {
-            const int threads = int(ceil_div(vectors, nv * 32)) * 32;
-            const size_t smem = size_t(kAhead + 1) * 3 * nv * threads * 16;
-            resident_ctas(kernel, threads, smem);
-            return launch(kernel, grid, dim3(threads), smem, 1, stream, a);
+        auto walk = [&](auto vectors_each) {
+            constexpr int NV = decltype(vectors_each)::value;
+            constexpr auto kernel = norm_back_walk_kernel<T, W, NV>;
+            constexpr size_t per_thread = size_t(kAhead + 1) * 3 * NV * 16;
+            if (!allow_shared_memory<kernel, per_thread * kWalkThreads>()) return BASP_ERR_CUDA;
+            const int threads = int(ceil_div(vectors, NV * 32)) * 32;
+            return launch(kernel, grid, dim3(threads), per_thread * threads, 1, stream, a);
         };
-        if (vectors <= kWalkThreads) return walk(norm_back_walk_kernel<T, W, 1>, 1);
-        if (vectors <= 2 * kWalkThreads) return walk(norm_back_walk_kernel<T, W, 2>, 2);
+        if (vectors <= kWalkThreads) return walk(std::integral_constant<int, 1>());
+        if (vectors <= 2 * kWalkThreads) return walk(std::integral_constant<int, 2>());
     }
     if (blocks <= 32)
         return launch(norm_back_kernel<T, W, 2, VEC>, grid, dim3(unsigned(ceil_div(blocks, 2)) * 32), 0, 1,
