@@ -1,7 +1,8 @@
 """Compile the C-ABI library in-tree with nvcc for sm_103a: ``libbasp.so``
 (release) and ``libbasp_debug.so`` (every access of the re-layout kernel
-bounds-checked); and ``_torch_ops.so``, the 8-bit operators' calls on torch
-tensors (host code only, against the installed torch)."""
+bounds-checked).  They need nvcc alone.  Where torch is installed, also
+``_torch_ops.so``, the 8-bit operators' calls on torch tensors (host code only,
+against that torch)."""
 from __future__ import annotations
 
 import os
@@ -14,6 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libbasp.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "libbasp_debug.so")
 TORCH_OPS_PATH = os.path.join(PKG, "_torch_ops.so")
+TORCH_VERSION_PATH = os.path.join(PKG, "_torch_ops.built_with")
 TORCH_OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "quantize.cu", "matmul.cu"]
 HEADERS = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h")] + \
@@ -52,11 +54,34 @@ def _command(out, extra, verbose):
     return cmd
 
 
-def _torch_command(out):
-    # found without importing torch, which takes longer than the compilation
+def _torch_dir():
+    """The installed torch with CUDA, or None.  Found without importing it, which
+    takes longer than the compilation."""
     import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    torch = os.path.dirname(spec.origin)
+    return torch if os.path.exists(os.path.join(torch, "lib", "libtorch_cuda.so")) else None
+
+
+def _torch_version(torch) -> str:
+    """What _torch_ops.so was built against: it uses torch's C++ interface, which
+    changes from one version to the next."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return torch + "\n" + f.read()
+
+
+def _torch_is_other(torch) -> bool:
+    try:
+        with open(TORCH_VERSION_PATH) as f:
+            return f.read() != _torch_version(torch)
+    except OSError:
+        return True
+
+
+def _torch_command(out, torch):
     import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     libs = os.path.join(torch, "lib")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -68,26 +93,35 @@ def _torch_command(out):
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Build ``libbasp.so``, ``libbasp_debug.so`` and ``_torch_ops.so`` next to
-    this file (side by side) if missing or out of date; return the release
-    library's path."""
-    jobs = []
+    """Build ``libbasp.so``, ``libbasp_debug.so`` and, where torch is installed,
+    ``_torch_ops.so`` next to this file (side by side) if missing or out of date;
+    return the release library's path.  What compiles is put in place also where
+    something else does not; that is an error afterwards."""
     sources = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS
-    for path, deps, command in (
-            (LIB_PATH, sources, lambda tmp: _command(tmp, [], verbose)),
-            (DEBUG_LIB_PATH, sources, lambda tmp: _command(tmp, ["-DBASP_CHECK_BOUNDS=1"], verbose)),
-            (TORCH_OPS_PATH, [TORCH_OPS_SOURCE] + HEADERS[:3], _torch_command)):
-        if force or _stale(path, deps):
-            tmp = path + ".tmp%d" % os.getpid()
-            jobs.append((subprocess.Popen(command(tmp)), tmp, path))
-    failed = None
-    for proc, tmp, path in jobs:
+    commands = []
+    for path, extra in ((LIB_PATH, []), (DEBUG_LIB_PATH, ["-DBASP_CHECK_BOUNDS=1"])):
+        if force or _stale(path, sources):
+            commands.append((path, _command(path + ".tmp%d" % os.getpid(), extra, verbose)))
+    torch = _torch_dir()
+    if torch is not None and (force or _stale(TORCH_OPS_PATH, [TORCH_OPS_SOURCE] + HEADERS[:3]) or
+                              _torch_is_other(torch)):
+        commands.append((TORCH_OPS_PATH, _torch_command(TORCH_OPS_PATH + ".tmp%d" % os.getpid(), torch)))
+    jobs, failed = [], None
+    for path, command in commands:
+        try:
+            jobs.append((path, command, subprocess.Popen(command)))
+        except OSError as e:                    # no such compiler
+            failed = e
+    for path, command, proc in jobs:
         if proc.wait() != 0:
-            failed = proc
-        elif failed is None:
-            os.replace(tmp, path)
+            failed = subprocess.CalledProcessError(proc.returncode, command[0])
+            continue
+        os.replace(path + ".tmp%d" % os.getpid(), path)
+        if path == TORCH_OPS_PATH:
+            with open(TORCH_VERSION_PATH, "w") as f:
+                f.write(_torch_version(torch))
     if failed is not None:
-        raise subprocess.CalledProcessError(failed.returncode, failed.args[0])
+        raise failed
     return LIB_PATH
 
 
