@@ -75,7 +75,7 @@ typedef struct basp_fp8_matrix {
  *                 x or residual (same address and stride)
  *   y             [rows][cols] of `dtype`, or NULL
  *   q             8-bit y (rows x cols, block_rows = 1), or NULL
- *   rstd          [rows] fp32, or NULL
+ *   rstd          [rows] fp32, or NULL (rows without columns: not written)
  * At least one of y and q is given.
  */
 basp_status basp_rmsnorm(basp_dtype dtype, int64_t rows, int64_t cols,

@@ -18,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <limits>
 #include <optional>
 #include <sstream>
 #include <string>
@@ -255,7 +256,9 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
         y = new_tensor(x.sizes(), type, x.device());
         ry = rows_of(&y, rows, cols, type, call.device, where, "y");
     }
-    // the C call wants one of y and q even where there is nothing to write
+    // the C call wants one of y and q even where there is nothing to write; the
+    // mean of no columns is 0 / 0
+    if (cols == 0) rstd.fill_(std::numeric_limits<double>::quiet_NaN());
     if (rows > 0 && cols > 0 &&
         !check(g_lib.rmsnorm(code, rows, cols, rx.p, rx.stride, rr.p, rr.stride, w, wcode, float(eps), rh.p, rh.stride,
                             ry.p, ry.stride, quantized ? &q.c : nullptr, rstd.data_ptr<float>(), call.stream),
