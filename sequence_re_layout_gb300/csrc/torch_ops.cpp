@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -80,6 +81,18 @@ void on_device(const Tensor &x, int device, const char *where, const char *name)
 // 7.4 now).
 Tensor new_tensor(c10::IntArrayRef sizes, at::ScalarType type, c10::Device device) {
     return Tensor(at::detail::empty_cuda(sizes, type, device, std::nullopt));
+}
+
+// A caller's tensor that a call will write to.  The calls are no operations of
+// autograd, so one whose gradient autograd would follow is refused, as torch
+// refuses it for an out=; `written` tells autograd of the write, so that a tensor
+// that was saved for a backward pass and overwritten is noticed there.
+void may_write(const Tensor *t, const char *where, const char *name) {
+    if (t != nullptr && c10::GradMode::is_enabled() && t->requires_grad())
+        refuse(where, text(name, " is written to and must not require a gradient (outside of no_grad)"));
+}
+void written(const Tensor *t) {
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 // A matrix of [rows][cols] as the C calls take it.
@@ -234,6 +247,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     const bool quantized = args[4] == Py_True;
     const Tensor *given = tensor(args[5], where, "h", true);
+    may_write(given, where, "h");
     const auto type = x.scalar_type();
     const basp_dtype code = dtype_code(type, where, "x"), wcode = dtype_code(weight.scalar_type(), where, "weight");
     int64_t rows, cols;
@@ -264,6 +278,7 @@ PyObject *rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n) {
                             ry.p, ry.stride, quantized ? &q.c : nullptr, rstd.data_ptr<float>(), call.stream),
                "basp_rmsnorm"))
         return nullptr;
+    written(given);
     return tuple(wrap(quantized ? q.data : y), wrap_or_none(q.scales), wrap_or_none(h), wrap(rstd));
     END_HANDLE_TH_ERRORS
 }
@@ -344,6 +359,7 @@ PyObject *matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const basp_fp8_matrix b = fp8_of(args[3], args[4], bb, call.device, where, "b");
     if (a.cols != b.cols) refuse(where, text("a has ", a.cols, " columns and b ", b.cols));
     const Tensor *bias = tensor(args[6], where, "bias", true), *given = tensor(args[7], where, "out", true);
+    may_write(given, where, "out");
     const bool accumulate = args[9] == Py_True;
     if (accumulate && given == nullptr) refuse(where, "accumulate needs out");
     if (given == nullptr && !THPDtype_Check(args[8])) refuse(where, "out_dtype must be a torch.dtype");
@@ -359,6 +375,7 @@ PyObject *matmul(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const void *bp = vector_of(bias, b.rows, type, call.device, where, "bias");
     if (!check(g_lib.matmul(&a, &b, bp, accumulate, code, c.p, c.stride, call.stream), "basp_matmul_fp8"))
         return nullptr;
+    written(given);
     return wrap(out);
     END_HANDLE_TH_ERRORS
 }

@@ -7,7 +7,9 @@ projection) and after ``head2seq`` (output projection).
     qkv = fp8.matmul(x8, w8, bias=bias)                 # -> seq2head_qkv
 
 These functions allocate their outputs and run on the current stream; nothing
-synchronises.  ``autograd`` has the differentiable forms.
+synchronises.  They are no operations of autograd: their results carry no gradient
+and no tangent (``autograd`` has the differentiable forms), and a tensor given to
+write to (``h``, ``out``) may not require a gradient outside of ``torch.no_grad()``.
 """
 from __future__ import annotations
 

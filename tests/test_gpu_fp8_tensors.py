@@ -22,3 +22,50 @@ def test_norm_of_no_columns(quantized, dtype):
     assert bool(torch.isnan(rstd).all())
     y, _, rstd = fp8.rmsnorm(x[:0], w, quantized=quantized)
     assert y.shape == (0, 0) and rstd.shape == (0,)
+
+
+def norm_into(t):
+    x, w = torch.ones(t.shape, dtype=t.dtype, device="cuda"), torch.ones(t.shape[1], dtype=t.dtype, device="cuda")
+    return fp8.rmsnorm(x, w, residual=t.detach(), h=t)[1]
+
+
+def product_into(t, accumulate=False):
+    a, b = (fp8.quantize(torch.ones(n, 128, device="cuda")) for n in t.shape)
+    return fp8.matmul(a, b, out=t, accumulate=accumulate)
+
+
+WRITES = {"norm": norm_into, "product": product_into, "accumulate": lambda t: product_into(t, True)}
+
+
+@pytest.mark.parametrize("write", sorted(WRITES))
+def test_a_saved_tensor_that_was_overwritten_is_noticed(write):
+    a = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = torch.exp(a)                                         # saves its result
+    WRITES[write](y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    y = torch.exp(a)
+    y.sum().backward()
+    assert bool((a.grad == 1).all())
+
+
+@pytest.mark.parametrize("write", sorted(WRITES))
+def test_a_write_raises_the_version(write):
+    t = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    part = t[1:3, 16:144]
+    assert WRITES[write](part) is part and t._version == part._version == 1
+    with torch.inference_mode():                             # has no versions
+        i = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+        assert WRITES[write](i) is i and bool((i != 0).all())
+
+
+@pytest.mark.parametrize("write", sorted(WRITES))
+def test_a_tensor_whose_gradient_is_followed_is_not_written_to(write):
+    leaf = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    for t in (leaf, leaf * 2, leaf[:, :128]):
+        with pytest.raises(ValueError, match="must not require a gradient"):
+            WRITES[write](t)
+    assert leaf._version == 0 and bool((leaf == 0).all())
+    with torch.no_grad():
+        WRITES[write](leaf)
+    assert leaf._version == 1 and bool((leaf != 0).all())
