@@ -139,6 +139,12 @@ def _rows(t):
     return t.flatten(0, -2) if t.dim() > 1 else t.unsqueeze(0)
 
 
+def _shaped(grad, shape):
+    """The gradient of the residual, which may have x's rows under other leading
+    dimensions."""
+    return grad if grad is None or grad.shape == shape else grad.reshape(shape)
+
+
 def _saved(q):
     return (None, None) if q is None else (q.data, q.scales)
 
@@ -171,6 +177,7 @@ class _RmsNorm(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         y, h, rstd = fp8.rmsnorm(x, weight, residual, eps, quantized=False)
         ctx.save_for_backward(h, rstd, weight)
+        ctx.residual_shape = None if residual is None else residual.shape
         ctx.set_materialize_grads(False)
         return y, h.view_as(h) if residual is None else h       # an input comes back as a view of it
 
@@ -183,13 +190,14 @@ class _RmsNorm(torch.autograd.Function):
         if dy is not None:
             dx, dw = fp8.rmsnorm_backward(dy.contiguous(), h, rstd, weight, _contig(dh), need_w)
         return (dx if need_x else None, None if dw is None else dw.to(weight.dtype),
-                dx if need_residual else None, None)
+                _shaped(dx, ctx.residual_shape) if need_residual else None, None)
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6):
     """``(y, h)`` with h = x + residual and y = h / sqrt(mean(h^2) + eps) *
     weight over the last dimension, differentiable.  h carries the residual
-    stream on: its gradient joins the norm's in one kernel."""
+    stream on: its gradient joins the norm's in one kernel.  y and h have x's shape;
+    the residual has x's rows, in order, under any leading dimensions."""
     return _RmsNorm.apply(x, weight, residual, eps)
 
 
@@ -235,6 +243,7 @@ class _RmsNormLinearFp8(torch.autograd.Function):
         q, h, rstd = fp8.rmsnorm(x, norm_weight, residual, eps)
         ctx.save_for_backward(h, rstd, norm_weight, *_saved(w_t))
         ctx.eps, ctx.weight_dtype = eps, weight.dtype
+        ctx.residual_shape = None if residual is None else residual.shape
         ctx.set_materialize_grads(False)
         y = fp8.matmul(q, w, bias=bias, out_dtype=x.dtype).view(*x.shape[:-1], weight.shape[0])
         return y, h.view_as(h) if residual is None else h
@@ -259,7 +268,7 @@ class _RmsNormLinearFp8(torch.autograd.Function):
             if dn is not None:
                 dx, dnw = fp8.rmsnorm_backward(dn.view(h.shape), h, rstd, norm_weight, _contig(dh), need_nw)
         return (dx if need_x else None, None if dnw is None else dnw.to(norm_weight.dtype), dw, db,
-                dx if need_residual else None, None)
+                _shaped(dx, ctx.residual_shape) if need_residual else None, None)
 
 
 def rmsnorm_linear_fp8(x, norm_weight, weight, bias=None, residual=None, eps=1e-6):

@@ -86,7 +86,8 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, quantized=True, h=None):
     ``quantized=False`` as a tensor like x; h like x (x itself without a
     residual); rstd float32 [rows], which the backward takes.  ``h`` may be
     given: a buffer to write to, also that of x or of the residual.  ``weight``
-    has x's element type or float32."""
+    has x's element type or float32.  The residual and a given ``h`` have x's rows,
+    in order, under any leading dimensions."""
     y, scales, new_h, rstd = (_ops or _load()).rmsnorm(x, weight, residual, eps, bool(quantized), h)
     return Quantized(y, scales) if quantized else y, x if new_h is None else new_h, rstd
 

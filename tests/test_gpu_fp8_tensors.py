@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sequence_re_layout_gb300 as basp                     # noqa: F401
-from sequence_re_layout_gb300 import fp8
+from sequence_re_layout_gb300 import autograd, fp8
 from test_gpu_fp8 import _built                             # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +69,25 @@ def test_a_tensor_whose_gradient_is_followed_is_not_written_to(write):
     with torch.no_grad():
         WRITES[write](leaf)
     assert leaf._version == 1 and bool((leaf != 0).all())
+
+
+@pytest.mark.parametrize("shapes", [((6, 256), (2, 3, 256)), ((2, 3, 256), (6, 256)), ((256,), (1, 256))])
+@pytest.mark.parametrize("through", ["y", "h", "both"])
+@pytest.mark.parametrize("projected", [False, True])
+def test_a_residual_under_other_leading_dimensions(shapes, through, projected):
+    """The rows are the same, so are the results; the gradient has the residual's shape."""
+    def run(residual_shape):
+        g = torch.Generator().manual_seed(1)
+        x, r = (torch.randn(s, generator=g).bfloat16().cuda().requires_grad_() for s in shapes)
+        w = torch.randn(256, generator=g).bfloat16().cuda().requires_grad_()
+        p = torch.randn(48, 256, generator=g).cuda().requires_grad_()
+        leaf, r = r, r.view(residual_shape)
+        y, h = autograd.rmsnorm_linear_fp8(x, w, p, residual=r) if projected else autograd.rmsnorm(x, w, r)
+        dy, dh = torch.randn(y.shape, generator=g).bfloat16().cuda(), torch.randn(h.shape, generator=g).bfloat16().cuda()
+        outs = {"y": [(y, dy)], "h": [(h, dh)], "both": [(y, dy), (h, dh)]}[through]
+        torch.autograd.backward([o for o, _ in outs], [d for _, d in outs])
+        assert h.shape == x.shape and leaf.grad.shape == leaf.shape
+        return y, h, x.grad, leaf.grad
+
+    for a, b in zip(run(shapes[1]), run(shapes[0])):
+        assert torch.equal(a, b)
