@@ -319,11 +319,12 @@ matmul_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             }
         }
         // A CTA ends after the last arrival at its barriers, and after its
-        // copies in flight (a pair's count at the leader).
+        // copies in flight (a pair's count at the leader): also where another
+        // warp gave up on them after this one had issued them all.
         const uint32_t open = issued < uint32_t(ST) ? issued : ST;
         for (uint32_t j = issued - open; j < issued; ++j) {
             if (CG == 2 && ok) wait(empty + 8 * (j % ST), (j / ST) & 1);
-            if (!ok && peer == 0) wait(full + 8 * (j % ST), (j / ST) & 1, false);
+            if (peer == 0) wait(full + 8 * (j % ST), (j / ST) & 1, false);
         }
     } else if (warp == 1) {
         if (peer == 0 && elect_one()) {                   // products
