@@ -67,7 +67,10 @@ typedef struct basp_fp8_matrix {
 /*
  * h = x + residual (rounded to `dtype`; h = x without a residual),
  * rstd = (mean(h^2) + eps)^-1/2 over each row, y = h * rstd * weight.
- * Sums are in 32 bits; y is rounded once, to `dtype` or to 8 bits.
+ * Sums are in 32 bits; h * rstd and its product with the weight are rounded to
+ * 32 bits each, and y once, to `dtype` or to 8 bits.  Results repeat bit for bit;
+ * the order of a row's sum, and so the last bit of rstd, depends on the number of
+ * rows and columns and on their alignment.
  *   x, residual   [rows][cols] of `dtype` (BF16, FP16 or FP32); residual may
  *                 be NULL
  *   weight        [cols] of `weight_dtype`: `dtype` or FP32

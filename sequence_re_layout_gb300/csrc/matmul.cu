@@ -43,14 +43,18 @@
 // products waiting (2.2 PFLOP/s at 32768 x 6144 x 2048).  TMA gets whole 16 bytes
 // of a row only: a store clipped at an odd column wrote the element past it.  Up
 // to seven columns at a row's end, rows of C that TMA cannot address, and
-// accumulation into C take one store a value.
+// accumulation into C take one store a value (32768 x 6143 x 2048: 291 us, 275 with
+// rows at multiples of 16 bytes).  Accumulation into 16-bit C reads it value by
+// value between the stores and is far from what it could be: 4.9 ms at 32768 x 6144
+// x 2048, 444 us at 6144 x 2048 x 32768 (270 into 32-bit C).
 //
 // Long sums.  The tensor cores' 32-bit accumulator truncates: after 1024
-// instructions (K = 32768) a sum is off by 8e-6 of its size, systematically.
+// instructions (K = 32768) results are off by 8e-6 of themselves (in norm),
+// systematically.
 // For 32-bit results the accumulator therefore starts afresh every 2048
 // values of K, and the drain adds the segments in registers, rounding to
-// nearest; a 16-bit result's own rounding is a hundred times larger, so
-// there one accumulator takes all of K.
+// nearest (2.5e-7).  A 16-bit result's own rounding, up to 2^-11 of it in fp16, is
+// sixty times larger, so there one accumulator takes all of K.
 //
 // Waits.  Every wait on an mbarrier has a time limit.  When one runs out the
 // CTA's roles leave their loops, wait (with the limit again) for copies and

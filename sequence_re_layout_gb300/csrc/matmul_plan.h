@@ -20,10 +20,12 @@ namespace basp_fp8 {
 
 constexpr int kVecTokens = 8;
 
-// Whether matvec.cuh's kernel takes the product.  GPU times in us, one token, there and
-// on matmul.cu's tiles: 128 x 128 1.5, 2.8; 2048 x 2048 2.5, 4.9; 6144 x 2048
-// 3.5, 5.0; 8192 x 1024 3.4, 3.9; 4096 x 4096 5.0, 6.0; 512 x 16384 6.3, 8.8;
-// but 16384 x 1024 5.4, 4.2; 8192 x 2048 5.3, 5.1; 16384 x 2048 10.6, 7.9.
+// Whether matvec.cuh's kernel takes the product.  GPU times in us of one and of
+// eight tokens there, and of either on matmul.cu's tiles: 128 x 128 1.4, 1.4, 2.7;
+// 2048 x 2048 2.5, 2.6, 5.0; 6144 x 2048 3.4, 3.6, 5.0; 8192 x 1024 3.4, 3.7, 3.9;
+// 16384 x 512 3.4, 3.5, 3.5; 4096 x 4096 5.0, 5.4, 6.1; 512 x 16384 6.2, 6.5, 8.8; at
+// the bounds 8191 x 2048 5.1, 5.4, 5.0 to 5.3; but past them, one token: 16384 x 1024
+// 5.4, tiles 4.2; 8192 x 2048 5.3, 5.1; 16384 x 2048 10.6, 7.9.
 inline bool takes_matvec(int64_t M, int64_t N, int64_t K) {
     return M <= kVecTokens && K > 0 && N * K <= (N < 8192 ? int64_t(1) << 24 : int64_t(1) << 23);
 }

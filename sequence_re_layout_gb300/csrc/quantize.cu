@@ -30,7 +30,9 @@ struct QuantArgs {
 constexpr int kRowWarps = 8;       // warps a CTA
 constexpr int kRowBlocks = 4;      // 128-blocks a warp: loads in flight
 
-// Warp units are groups of kRowBlocks neighbouring blocks of one row.
+// Warp units are groups of kRowBlocks neighbouring blocks of one row.  32768 x 2048
+// bf16: 63 us, 30 memory's time: a warp ends after four blocks, and nothing is on
+// its way while they are rounded.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kRowWarps * 32)
 quantize_rows_kernel(const __grid_constant__ QuantArgs a, int groups) {
@@ -291,7 +293,8 @@ quantize_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n, int tiles
 }
 
 // Rows of any alignment: a tile a CTA, its values in registers, columns lane,
-// lane + 32, ... of a row to a lane.
+// lane + 32, ... of a row to a lane.  4099 x 5003 fp16 with 1 x 128 scales: 77 us, 12
+// memory's time: single elements, no tile ahead of another.
 template <class T, bool PER_ROW>
 __global__ void __launch_bounds__(kTileThreads, 2)
 quantize_any_tile_kernel(const __grid_constant__ QuantArgs a, int tiles_n) {
