@@ -10,6 +10,7 @@
  *   basp_rmsnorm            residual addition + root-mean-square norm, with an
  *                           8-bit output, a 16/32-bit output, or both
  *   basp_rmsnorm_backward   its gradient
+ *   basp_layernorm, basp_layernorm_backward   the same for a norm with a mean
  *   basp_quantize_fp8       a 16/32-bit matrix (and its transpose) to 8 bits
  *   basp_matmul_fp8         C = A B^T of two 8-bit matrices
  * The gradients of a projection Y = X W^T are two more products:
@@ -116,6 +117,46 @@ basp_status basp_rmsnorm_backward(basp_dtype dtype, int64_t rows, int64_t cols,
 
 /* Workspace of basp_rmsnorm_backward with dweight, in bytes.  Host only. */
 int64_t basp_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Layer norm: h = x + residual as above, mean and rstd = (mean((h - mean)^2) +
+ * eps)^-1/2 over each row, y = (h - mean) * rstd * weight + bias.  Sums are in 32
+ * bits, the second one about the mean; y is rounded as above.
+ *   bias          [cols] of `weight_dtype`, or NULL
+ *   mean          [rows] fp32, or NULL (as rstd)
+ * All other arguments as for basp_rmsnorm.
+ */
+basp_status basp_layernorm(basp_dtype dtype, int64_t rows, int64_t cols,
+                           const void *x, int64_t x_stride,
+                           const void *residual, int64_t residual_stride,
+                           const void *weight, const void *bias, basp_dtype weight_dtype,
+                           float eps, void *h, int64_t h_stride, void *y, int64_t y_stride,
+                           const basp_fp8_matrix *q, float *mean, float *rstd,
+                           cudaStream_t stream);
+
+/*
+ * Gradient of basp_layernorm (the rounding of y is passed through):
+ *   g = dy * weight, n = (h - mean) * rstd,
+ *   dx = rstd * (g - mean(g) - n * mean(g * n)) + dh, the gradient of x and of the
+ *        residual alike;
+ *   dweight = sum over rows of dy * n, dbias = sum over rows of dy.
+ *   dweight, dbias  [cols] fp32, each may be NULL
+ *   workspace     device scratch of basp_layernorm_backward_workspace(rows, cols)
+ *                 bytes (16-byte aligned); may be NULL without dweight and dbias
+ * All other arguments as for basp_rmsnorm_backward.  Results repeat bit for bit.
+ */
+basp_status basp_layernorm_backward(basp_dtype dtype, int64_t rows, int64_t cols,
+                                    const void *dy, int64_t dy_stride,
+                                    const void *h, int64_t h_stride,
+                                    const float *mean, const float *rstd,
+                                    const void *weight, basp_dtype weight_dtype,
+                                    const void *dh, int64_t dh_stride,
+                                    void *dx, int64_t dx_stride, float *dweight, float *dbias,
+                                    void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/* Workspace of basp_layernorm_backward with dweight or dbias, in bytes.  Host only. */
+int64_t basp_layernorm_backward_workspace(int64_t rows, int64_t cols);
 
 /*
  * x [rows][cols] of `dtype` -> 8 bits.

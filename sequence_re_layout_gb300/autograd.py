@@ -20,7 +20,12 @@ operators they are made of):
     qkv, h = rmsnorm_linear_fp8(x, norm_weight, wqkv, bqkv, residual=r)
     out = linear_fp8(o, wo)
 
-Their gradients treat the rounding to 8 bits as the identity, and round the
+The same with a norm that has a mean (``layernorm``, ``layernorm_linear_fp8``), and
+the attention between the two directions:
+
+    o = attention(q, k, v, window=4096, sinks=4)       # [batch, tokens, heads, d]
+
+The gradients of the 8-bit forms treat the rounding to 8 bits as the identity, and round the
 operands of the gradients' products the same way: with dY in 8 bits along its
 rows, dX = dY W; with dY and X in 8 bits along the tokens, dW = dY^T X.
 
@@ -32,6 +37,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
+from . import attention as _attention
 from . import binding, fp8
 
 
@@ -281,6 +287,119 @@ def rmsnorm_linear_fp8(x, norm_weight, weight, bias=None, residual=None, eps=1e-
         return fp8.matmul(q, w, bias=bias, out_dtype=x.dtype).view(*x.shape[:-1], w.shape[0]), h
     _refuse_quantized(weight)
     return _RmsNormLinearFp8.apply(x, norm_weight, weight, bias, residual, eps)
+
+
+# ---- the norm with a mean ----------------------------------------------------------
+
+def _norm_grads(ctx, dy, dh, need_w, need_b):
+    """(dx, dweight, dbias) of the layer norm whose h, mean, rstd and weight ctx saved."""
+    h, mean, rstd, weight = ctx.saved_tensors[:4]
+    dx, dw, db = fp8.layernorm_backward(dy, h, mean, rstd, weight, _contig(dh), need_w, need_b)
+    return dx, None if dw is None else dw.to(weight.dtype), None if db is None else db.to(weight.dtype)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        y, h, mean, rstd = fp8.layernorm(x, weight, bias, residual, eps, quantized=False)
+        ctx.save_for_backward(h, mean, rstd, weight)
+        ctx.residual_shape = None if residual is None else residual.shape
+        ctx.set_materialize_grads(False)
+        return y, h.view_as(h) if residual is None else h       # an input comes back as a view of it
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        need_x, need_w, need_b, need_residual, _ = ctx.needs_input_grad
+        dx, dw, db = dh, None, None
+        if dy is not None:
+            dx, dw, db = _norm_grads(ctx, dy.contiguous(), dh, need_w, need_b)
+        return (dx if need_x else None, dw, db, _shaped(dx, ctx.residual_shape) if need_residual else None, None)
+
+
+def layernorm(x, weight, bias=None, residual=None, eps=1e-5):
+    """``(y, h)`` with h = x + residual and y = (h - mean) / sqrt(var + eps) *
+    weight + bias over the last dimension, differentiable; otherwise as
+    :func:`rmsnorm`.  weight and bias have one type."""
+    return _LayerNorm.apply(x, weight, bias, residual, eps)
+
+
+class _LayerNormLinearFp8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, norm_weight, norm_bias, weight, bias, residual, eps):
+        need = ctx.needs_input_grad
+        w, w_t = _quantized_weight(weight, need[0] or need[1] or need[2] or need[5])
+        q, h, mean, rstd = fp8.layernorm(x, norm_weight, norm_bias, residual, eps)
+        ctx.save_for_backward(h, mean, rstd, norm_weight, norm_bias, *_saved(w_t))
+        ctx.eps, ctx.weight_dtype = eps, weight.dtype
+        ctx.residual_shape = None if residual is None else residual.shape
+        ctx.set_materialize_grads(False)
+        y = fp8.matmul(q, w, bias=bias, out_dtype=x.dtype).view(*x.shape[:-1], weight.shape[0])
+        return y, h.view_as(h) if residual is None else h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, _, _, norm_weight, norm_bias, wd, ws = ctx.saved_tensors
+        need_x, need_nw, need_nb, need_w, need_b, need_residual, _ = ctx.needs_input_grad
+        dx, dnw, dnb, dw, db = dh, None, None, None, None
+        if dy is not None:
+            x_t = None
+            if need_w:
+                # the norm again, with scales along the tokens (see _RmsNormLinearFp8)
+                y = fp8.layernorm(h, norm_weight, norm_bias, None, ctx.eps, quantized=False)[0]
+                x_t = fp8.quantize(_rows(y), rows=False, transposed=True)
+            dn, dw, db = _product_grads(_rows(dy).contiguous(),
+                                        None if wd is None else fp8.Quantized(wd, ws, fp8.BLOCK), x_t,
+                                        ctx.weight_dtype, need_b)
+            if dn is not None:
+                dx, dnw, dnb = _norm_grads(ctx, dn.view(h.shape), dh, need_nw, need_nb)
+        return (dx if need_x else None, dnw, dnb, dw, db,
+                _shaped(dx, ctx.residual_shape) if need_residual else None, None)
+
+
+def layernorm_linear_fp8(x, norm_weight, norm_bias, weight, bias=None, residual=None, eps=1e-5):
+    """``(y, h)``: :func:`layernorm` and :func:`linear_fp8` of its result, as
+    :func:`rmsnorm_linear_fp8`."""
+    if not torch.is_grad_enabled():
+        q, h, _, _ = fp8.layernorm(x, norm_weight, norm_bias, residual, eps)
+        w = weight if isinstance(weight, fp8.Quantized) else _quantized_weight(weight, False)[0]
+        return fp8.matmul(q, w, bias=bias, out_dtype=x.dtype).view(*x.shape[:-1], w.shape[0]), h
+    _refuse_quantized(weight)
+    return _LayerNormLinearFp8.apply(x, norm_weight, norm_bias, weight, bias, residual, eps)
+
+
+# ---- attention ---------------------------------------------------------------------
+
+def _aligned(t):
+    """t where a kernel can read its heads in place, else a copy: gradients come in
+    any form (one value spread over the result, for instance)."""
+    if t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]):
+        return t
+    return t.contiguous()
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks, scale):
+        o, lse = _attention.forward(q, k, v, window, sinks, scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.mask = window, sinks, scale
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        grads = _attention.backward(_aligned(do), q, k, v, o, lse, *ctx.mask)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None)
+
+
+def attention(q, k, v, window=None, sinks=0, scale=None):
+    """Causal attention of q [batch, Sq, heads, d] over k, v [batch, Sk, key heads, d]
+    with a sliding window and sinks (``attention.py`` in this package says what a
+    query sees), differentiable.  The result is like q."""
+    return _Attention.apply(q, k, v, window, sinks, scale)
 
 
 def _refuse_quantized(weight):

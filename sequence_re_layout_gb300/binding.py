@@ -1,5 +1,5 @@
-"""ctypes binding of ``libbasp.so`` (declared in ``include/basp.h`` and
-``include/basp_fp8.h``).
+"""ctypes binding of ``libbasp.so`` (declared in ``include/basp.h``,
+``include/basp_fp8.h``, ``include/basp_attention.h`` and ``include/basp_optim.h``).
 
 Argument marshalling only: every function here takes Python ints or torch
 tensors, turns them into the C-ABI's pointers and sizes, calls the library and
@@ -39,7 +39,15 @@ EXPORTS = ("basp_layout_create", "basp_layout_create_ex", "basp_layout_query",
 
 # every symbol include/basp_fp8.h declares
 FP8_EXPORTS = ("basp_rmsnorm", "basp_rmsnorm_backward", "basp_rmsnorm_backward_workspace",
-               "basp_quantize_fp8", "basp_matmul_fp8", "basp_matmul_fp8_timeouts")
+               "basp_quantize_fp8", "basp_matmul_fp8", "basp_matmul_fp8_timeouts",
+               "basp_layernorm", "basp_layernorm_backward", "basp_layernorm_backward_workspace")
+
+# every symbol include/basp_attention.h declares
+ATTENTION_EXPORTS = ("basp_attention", "basp_attention_backward", "basp_attention_backward_workspace",
+                     "basp_attention_decode", "basp_attention_decode_workspace", "basp_attention_timeouts")
+
+# every symbol include/basp_optim.h declares
+OPTIM_EXPORTS = ("basp_adamw",)
 
 # values that share a scale along a row of an 8-bit matrix
 BASP_FP8_BLOCK = 128
@@ -68,6 +76,26 @@ class basp_layout_desc(ctypes.Structure):
 class basp_fp8_matrix(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + \
         [(n, ctypes.c_int64) for n in ("rows", "cols", "pitch", "scale_pitch", "block_rows")]
+
+
+class basp_attention_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "q_len", "k_len", "q_heads", "k_heads", "head_dim", "window",
+                                              "sinks")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class basp_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int64) for n in ("stride_batch", "stride_seq", "stride_head")]
+
+
+class basp_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scales", "v_scales")] + \
+        [("n", ctypes.c_int64), ("dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int)]
+
+
+class basp_adamw_options(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", ctypes.c_int64), ("step_at", ctypes.c_void_p), ("seed", ctypes.c_uint32)]
 
 
 class BaspError(RuntimeError):
@@ -129,6 +157,28 @@ def load_library():
     lib.basp_matmul_fp8.restype = ci
     lib.basp_matmul_fp8_timeouts.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
     lib.basp_matmul_fp8_timeouts.restype = ci
+    lib.basp_layernorm.argtypes = [ci, i64, i64, vp, i64, vp, i64, vp, vp, ci, ctypes.c_float,
+                                   vp, i64, vp, i64, mp, vp, vp, vp]
+    lib.basp_layernorm.restype = ci
+    lib.basp_layernorm_backward.argtypes = [ci, i64, i64, vp, i64, vp, i64, vp, vp, vp, ci, vp, i64,
+                                            vp, i64, vp, vp, vp, sz, vp]
+    lib.basp_layernorm_backward.restype = ci
+    lib.basp_layernorm_backward_workspace.argtypes = [i64, i64]
+    lib.basp_layernorm_backward_workspace.restype = i64
+    dp, hp = ctypes.POINTER(basp_attention_desc), ctypes.POINTER(basp_heads)
+    lib.basp_attention.argtypes = [dp] + [hp] * 4 + [vp, vp]
+    lib.basp_attention.restype = ci
+    lib.basp_attention_backward.argtypes = [dp] + [hp] * 4 + [vp] + [hp] * 4 + [vp, sz, vp]
+    lib.basp_attention_backward.restype = ci
+    lib.basp_attention_decode.argtypes = [dp] + [hp] * 3 + [vp, hp, vp, sz, vp]
+    lib.basp_attention_decode.restype = ci
+    for name in ("basp_attention_backward_workspace", "basp_attention_decode_workspace"):
+        getattr(lib, name).argtypes = [dp]
+        getattr(lib, name).restype = i64
+    lib.basp_attention_timeouts.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
+    lib.basp_attention_timeouts.restype = ci
+    lib.basp_adamw.argtypes = [ctypes.POINTER(basp_adamw_tensor), i64, ctypes.POINTER(basp_adamw_options), vp]
+    lib.basp_adamw.restype = ci
     if hasattr(lib, "basp_debug_bounds_violations"):
         lib.basp_debug_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
         lib.basp_debug_bounds_violations.restype = ctypes.c_int
@@ -474,6 +524,43 @@ def basp_rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight=None, workspace=N
         _check(st, w)
 
 
+def basp_layernorm(x, residual, weight, bias, eps, h=None, y=None, q=None, mean=None, rstd=None, stream=None):
+    """Residual addition + layer norm; see ``basp_fp8.h``."""
+    w = "basp_layernorm"
+    shape, t = _2d(x, w, "x"), x.dtype
+    code, wcode, cur = fp8_dtype_code(t), fp8_dtype_code(weight.dtype), _current_device()
+    xp, xs = _rows(x, w, "x", shape, t, cur)
+    rp, rs = _rows(residual, w, "residual", shape, t, cur)
+    hp, hs = _rows(h, w, "h", shape, t, cur)
+    yp, ys = _rows(y, w, "y", shape, t, cur)
+    _check(load_library().basp_layernorm(
+        code, shape[0], shape[1], xp, xs, rp, rs, _vector(weight, w, "weight", shape[1], weight.dtype, cur),
+        _vector(bias, w, "bias", shape[1], weight.dtype, cur), wcode, eps, hp, hs, yp, ys, q,
+        _vector(mean, w, "mean", shape[0], _F32, cur), _vector(rstd, w, "rstd", shape[0], _F32, cur),
+        _stream(stream)), w)
+
+
+def basp_layernorm_backward_workspace(rows: int, cols: int) -> int:
+    return load_library().basp_layernorm_backward_workspace(rows, cols)
+
+
+def basp_layernorm_backward(dy, h, mean, rstd, weight, dh, dx, dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradient of :func:`basp_layernorm`; see ``basp_fp8.h``."""
+    w = "basp_layernorm_backward"
+    shape, t = _2d(dy, w, "dy"), dy.dtype
+    code, wcode, cur = fp8_dtype_code(t), fp8_dtype_code(weight.dtype), _current_device()
+    yp, ys = _rows(dy, w, "dy", shape, t, cur)
+    hp, hs = _rows(h, w, "h", shape, t, cur)
+    dp, ds = _rows(dh, w, "dh", shape, t, cur)
+    xp, xs = _rows(dx, w, "dx", shape, t, cur)
+    _check(load_library().basp_layernorm_backward(
+        code, shape[0], shape[1], yp, ys, hp, hs, _vector(mean, w, "mean", shape[0], _F32, cur),
+        _vector(rstd, w, "rstd", shape[0], _F32, cur), _vector(weight, w, "weight", shape[1], weight.dtype, cur),
+        wcode, dp, ds, xp, xs, _vector(dweight, w, "dweight", shape[1], _F32, cur),
+        _vector(dbias, w, "dbias", shape[1], _F32, cur), _tptr(workspace, None, w, "workspace", "device", cur),
+        _nbytes(workspace), _stream(stream)), w)
+
+
 def basp_quantize_fp8(x, q=None, qt=None, stream=None):
     """A matrix, and its transpose, to 8 bits; see ``basp_fp8.h``.  ``q`` and
     ``qt`` are :class:`basp_fp8_matrix` or None."""
@@ -506,12 +593,68 @@ def fp8_entry_points():
     return tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in FP8_EXPORTS[:5])
 
 
+def layer_entry_points():
+    """Addresses of the loaded library's other entry points that the torch module
+    takes, in its order."""
+    lib = load_library()
+    return tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                 for n in FP8_EXPORTS[6:] + ATTENTION_EXPORTS[:5] + OPTIM_EXPORTS)
+
+
 def basp_matmul_fp8_timeouts() -> int:
     """Read and clear the count of waits that ran out in the product's kernel
     on the current device (synchronises it)."""
     n = ctypes.c_ulonglong()
     _check(load_library().basp_matmul_fp8_timeouts(ctypes.byref(n)), "basp_matmul_fp8_timeouts")
     return n.value
+
+
+# ---- attention and the optimiser (include/basp_attention.h, include/basp_optim.h) ----
+
+# Their structures (basp_attention_desc, basp_heads, basp_adamw_tensor,
+# basp_adamw_options) are filled by the caller; ``attention`` and ``optim`` have the
+# calls on torch tensors.
+
+def basp_attention(desc, q, k, v, o, lse=None, stream=None):
+    """Attention with a window and sinks; see ``basp_attention.h``."""
+    _check(load_library().basp_attention(desc, q, k, v, o, _ptr(lse), _stream(stream)), "basp_attention")
+
+
+def basp_attention_backward_workspace(desc) -> int:
+    return load_library().basp_attention_backward_workspace(desc)
+
+
+def basp_attention_backward(desc, q, k, v, o, lse, d_o, dq, dk, dv, workspace, workspace_bytes=None, stream=None):
+    """Gradients of :func:`basp_attention`; see ``basp_attention.h``."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(load_library().basp_attention_backward(desc, q, k, v, o, _ptr(lse), d_o, dq, dk, dv, _ptr(workspace), wb,
+                                                  _stream(stream)), "basp_attention_backward")
+
+
+def basp_attention_decode_workspace(desc) -> int:
+    return load_library().basp_attention_decode_workspace(desc)
+
+
+def basp_attention_decode(desc, q, k, v, lengths, o, workspace=None, workspace_bytes=None, stream=None):
+    """One new token of each sequence over a cache; see ``basp_attention.h``."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(load_library().basp_attention_decode(desc, q, k, v, _ptr(lengths), o, _ptr(workspace), wb,
+                                                _stream(stream)), "basp_attention_decode")
+
+
+def basp_attention_timeouts() -> int:
+    """Read and clear the count of waits that ran out in the attention kernels on
+    the current device (synchronises it)."""
+    n = ctypes.c_ulonglong()
+    _check(load_library().basp_attention_timeouts(ctypes.byref(n)), "basp_attention_timeouts")
+    return n.value
+
+
+def basp_adamw(tensors, options, stream=None):
+    """A step of AdamW over a sequence of :class:`basp_adamw_tensor`; see
+    ``basp_optim.h``."""
+    table = (basp_adamw_tensor * len(tensors))(*tensors)
+    _check(load_library().basp_adamw(table, len(tensors), options, _stream(stream)), "basp_adamw")
 
 
 class Layout:

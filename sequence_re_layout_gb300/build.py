@@ -1,7 +1,7 @@
 """Compile the C-ABI library in-tree with nvcc for sm_103a: ``libbasp.so``
 (release) and ``libbasp_debug.so`` (every access of the re-layout kernel
 bounds-checked).  They need nvcc alone.  Where torch is installed, also
-``_torch_ops.so``, the 8-bit operators' calls on torch tensors (host code only,
+``_torch_ops.so``, the layer's operators' calls on torch tensors (host code only,
 against that torch)."""
 from __future__ import annotations
 
@@ -17,10 +17,14 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libbasp_debug.so")
 TORCH_OPS_PATH = os.path.join(PKG, "_torch_ops.so")
 TORCH_VERSION_PATH = os.path.join(PKG, "_torch_ops.built_with")
 TORCH_OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
-SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "quantize.cu", "matmul.cu"]
-HEADERS = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h")] + \
+SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "layernorm.cu", "quantize.cu", "matmul.cu", "attention.cu",
+           "adamw.cu"]
+INCLUDES = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h", "basp_attention.h",
+                                               "basp_optim.h")]
+HEADERS = INCLUDES + \
     [os.path.join(CSRC, h) for h in ("layout_internal.h", "relayout_kernel.cuh", "scratch_cache.h",
-                                     "fp8_common.cuh", "matmul_plan.h", "matvec.cuh", "tcgen05.cuh")]
+                                     "fp8_common.cuh", "norm_common.cuh", "matmul_plan.h", "matvec.cuh",
+                                     "tcgen05.cuh", "attention_common.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -103,7 +107,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(path, sources):
             commands.append((path, _command(path + ".tmp%d" % os.getpid(), extra, verbose)))
     torch = _torch_dir()
-    if torch is not None and (force or _stale(TORCH_OPS_PATH, [TORCH_OPS_SOURCE] + HEADERS[:3]) or
+    if torch is not None and (force or _stale(TORCH_OPS_PATH, [TORCH_OPS_SOURCE] + INCLUDES) or
                               _torch_is_other(torch)):
         commands.append((TORCH_OPS_PATH, _torch_command(TORCH_OPS_PATH + ".tmp%d" % os.getpid(), torch)))
     jobs, failed = [], None

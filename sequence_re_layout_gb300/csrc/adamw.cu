@@ -1,0 +1,304 @@
+// adamw.cu -- one step of Adam with decoupled weight decay over many tensors
+// (basp_adamw).
+//
+// The bound is memory: with 32-bit weights and gradients 28 bytes an element with
+// 32-bit states, 16 with 8-bit ones.  One launch takes a table of tensors as its
+// parameter (up to 32 KB, copied with the launch, so there is nothing to keep or to
+// upload) and a grid of chunks; a CTA finds its chunk's tensor by bisection.
+//
+// 8-bit states have a scale for each 128 elements, which one warp holds, four a
+// lane, so the largest magnitude is one warp reduction and nothing is read twice.
+#include <algorithm>
+#include <cmath>
+
+#include "basp_optim.h"
+#include "fp8_common.cuh"
+
+namespace basp_fp8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlocksEach = 4;                       // blocks of 128 that a warp has on their way at once
+constexpr int kChunk = 128 * (kThreads / 32) * kBlocksEach * 4;   // elements of a CTA
+
+struct Entry {
+    void *p;
+    const void *g;
+    void *m, *v, *ms, *vs;
+    int64_t n;
+    int32_t chunk0;                                  // its first chunk in the launch
+    uint8_t type, grad_type, vec, pad;
+};
+static_assert(sizeof(Entry) == 64, "table");
+
+struct Options {
+    float beta1, beta2, one_beta1, one_beta2, eps, decay, lr;   // decay: 1 - lr * weight_decay
+    float c1, c2;                                    // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    float log_beta1, log_beta2;                      // for a t that is known on the GPU only
+    const int32_t *step_at;
+    uint32_t step, seed;
+};
+
+template <int CAP> struct Table {
+    Options o;
+    int32_t count, first;                            // entries; the first one's place in the caller's list
+    Entry e[CAP];
+};
+
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+// |y| <= 448 to the e4m3 grid, up with probability of the fraction: the 16 bits r
+// (and a half) are added below the last of the three mantissa bits.  Values below
+// 2^-6, whose steps are 2^-9, get there by an addition of 2^-6, exact to 2^-29.
+__device__ __forceinline__ float round_at_random(float y, uint32_t r) {
+    const float a = fabsf(y);
+    const bool small = a < 0x1p-6f;
+    uint32_t u = __float_as_uint(small ? a + 0x1p-6f : a);
+    u = (u + (r << 4) + 8u) & 0xfff00000u;
+    const float t = __uint_as_float(u);
+    return copysignf(small ? t - 0x1p-6f : t, y);
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) {           // 2^(byte - 127)
+    return byte != 0 ? __uint_as_float(byte << 23) : 0x1p-127f;
+}
+// e4m3 -> float, by way of fp16, which holds every e4m3 value
+__device__ __forceinline__ void from_e4m3x4(uint32_t q, float (&v)[4]) {
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(uint16_t(q)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(uint16_t(q >> 16)));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+
+// What a step does to one element; m and v become m' and v'.
+__device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v) {
+    m = o.beta1 * m + o.one_beta1 * g;
+    v = o.beta2 * v + o.one_beta2 * g * g;
+    return fmaf(p, o.decay, -c1 * __fdividef(m, fmaf(sqrtf(v), c2, o.eps)));
+}
+
+// Four elements of a 128-block (load4 of fp8_common.cuh), or their state bytes.
+template <int HOW> __device__ __forceinline__ uint32_t load4_bytes(const uint8_t *row, int lane, int left) {
+    if constexpr (HOW == kVector) return 4 * lane < left ? *reinterpret_cast<const uint32_t *>(row + 4 * lane) : 0u;
+    uint32_t q = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < left) q |= uint32_t(row[lane + 32 * j]) << (8 * j);
+    return q;
+}
+
+template <class P, class G, bool EIGHT, int HOW>
+__device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float c1, float c2, uint32_t key, int64_t begin) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = kThreads / 32;
+    const int64_t end = min(e.n, begin + kChunk);
+    for (int64_t b0 = begin + int64_t(warp) * kBlocksEach * kBlock; b0 < end; b0 += int64_t(warps) * kBlocksEach * kBlock) {
+        float p[kBlocksEach][4], g[kBlocksEach][4], m[kBlocksEach][4], v[kBlocksEach][4];
+        uint32_t qm[kBlocksEach], qv[kBlocksEach], em[kBlocksEach], ev[kBlocksEach];
+#pragma unroll
+        for (int i = 0; i < kBlocksEach; ++i) {
+            const int64_t at = b0 + i * kBlock;
+            const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
+            load4<P, HOW>(static_cast<const P *>(e.p) + at, lane, left, p[i]);
+            load4<G, HOW>(static_cast<const G *>(e.g) + at, lane, left, g[i]);
+            if constexpr (EIGHT) {
+                qm[i] = load4_bytes<HOW>(static_cast<const uint8_t *>(e.m) + at, lane, left);
+                qv[i] = load4_bytes<HOW>(static_cast<const uint8_t *>(e.v) + at, lane, left);
+                em[i] = left > 0 ? static_cast<const uint8_t *>(e.ms)[at / kBlock] : 0;
+                ev[i] = left > 0 ? static_cast<const uint8_t *>(e.vs)[at / kBlock] : 0;
+            } else {
+                load4<float, HOW>(static_cast<const float *>(e.m) + at, lane, left, m[i]);
+                load4<float, HOW>(static_cast<const float *>(e.v) + at, lane, left, v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBlocksEach; ++i) {
+            const int64_t at = b0 + i * kBlock;
+            const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
+            if (left == 0) break;
+            if constexpr (EIGHT) {
+                from_e4m3x4(qm[i], m[i]);
+                from_e4m3x4(qv[i], v[i]);
+                const float sm = scale_of(em[i]), sv = scale_of(ev[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m[i][j] *= sm;
+                    v[i][j] *= sv;
+                    v[i][j] *= v[i][j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j]);
+            store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
+            if constexpr (EIGHT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = sqrtf(v[i][j]);
+                const uint32_t bm = row_scale(m[i]), bv = row_scale(v[i]);       // infinities are NaN now
+                const float im = inverse_scale(bm), iv = inverse_scale(bv);
+                float a[4], b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t r = mix(uint32_t(at + (HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
+                    a[j] = m[i][j] == m[i][j] ? round_at_random(m[i][j] * im, r & 0xffffu) : m[i][j];
+                    const float y = v[i][j] * iv;
+                    b[j] = y == y ? round_at_random(y, r >> 16) : y;
+                    if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
+                }
+                store4_e4m3<HOW>(static_cast<uint8_t *>(e.m) + at, lane, left, to_e4m3x4(a, 1.f));
+                store4_e4m3<HOW>(static_cast<uint8_t *>(e.v) + at, lane, left, to_e4m3x4(b, 1.f));
+                if (lane == 0) {
+                    static_cast<uint8_t *>(e.ms)[at / kBlock] = uint8_t(bm);
+                    static_cast<uint8_t *>(e.vs)[at / kBlock] = uint8_t(bv);
+                }
+            } else {
+                store4<float, HOW>(static_cast<float *>(e.m) + at, lane, left, m[i]);
+                store4<float, HOW>(static_cast<float *>(e.v) + at, lane, left, v[i]);
+            }
+        }
+    }
+}
+
+template <int CAP, bool EIGHT>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t) {
+    grid_dependency();
+    int lo = 0, hi = t.count;                        // e[lo].chunk0 <= chunk < e[hi].chunk0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (t.e[mid].chunk0 <= int(blockIdx.x)) lo = mid;
+        else hi = mid;
+    }
+    const Entry &e = t.e[lo];
+    const int64_t begin = int64_t(int(blockIdx.x) - e.chunk0) * kChunk;
+    float c1 = t.o.c1, c2 = t.o.c2;
+    uint32_t step = t.o.step;
+    if (t.o.step_at != nullptr) {
+        const int s = max(1, *t.o.step_at);
+        step = uint32_t(s);
+        c1 = t.o.lr / -expm1f(float(s) * t.o.log_beta1);
+        c2 = rsqrtf(-expm1f(float(s) * t.o.log_beta2));
+    }
+    const uint32_t key = EIGHT ? mix(mix(mix(t.o.seed) ^ step) ^ uint32_t(t.first + lo)) : 0u;
+    auto go = [&](auto pe, auto ge) {
+        using P = decltype(pe);
+        using G = decltype(ge);
+        if (e.vec) do_chunk<P, G, EIGHT, kVector>(e, t.o, c1, c2, key, begin);
+        else do_chunk<P, G, EIGHT, kStrided>(e, t.o, c1, c2, key, begin);
+    };
+    if (e.type == BASP_DTYPE_FP32) return go(float(), float());
+    if (e.type == BASP_DTYPE_BF16)
+        return e.grad_type == BASP_DTYPE_FP32 ? go(__nv_bfloat16(), float()) : go(__nv_bfloat16(), __nv_bfloat16());
+    return e.grad_type == BASP_DTYPE_FP32 ? go(__half(), float()) : go(__half(), __half());
+}
+
+int64_t chunks_of(int64_t n) { return ceil_div(n, kChunk); }
+
+// One launch of entries [i0, i1) of the caller's list.
+template <int CAP>
+basp_status launch_adamw(const basp_adamw_tensor *list, int64_t i0, int64_t i1, bool eight, const Options &o,
+                         int64_t *next, cudaStream_t stream) {
+    Table<CAP> t;
+    t.o = o;
+    t.count = 0;
+    t.first = int32_t(i0);
+    int64_t chunks = 0, i = i0;
+    for (; i < i1 && t.count < CAP; ++i) {
+        const basp_adamw_tensor &x = list[i];
+        const int64_t c = chunks_of(x.n);
+        if (chunks + c > kMaxSide) break;            // the next launch
+        Entry &e = t.e[t.count++];
+        e.p = x.p; e.g = x.g; e.m = x.m; e.v = x.v; e.ms = x.m_scales; e.vs = x.v_scales;
+        e.n = x.n;
+        e.chunk0 = int32_t(chunks);
+        e.type = uint8_t(x.dtype);
+        e.grad_type = uint8_t(x.grad_dtype);
+        // the last block's four elements of a lane may be past the end
+        const int64_t state = eight ? 1 : 4;
+        e.vec = x.n % 4 == 0 && vec4_ok(x.p, 0, x.n, elem_size(x.dtype)) && vec4_ok(x.g, 0, x.n, elem_size(x.grad_dtype)) &&
+                vec4_ok(x.m, 0, x.n, state) && vec4_ok(x.v, 0, x.n, state);
+        e.pad = 0;
+        chunks += c;
+    }
+    *next = i;
+    if (chunks == 0) return BASP_OK;
+    return eight ? launch(adamw_kernel<CAP, true>, dim3(unsigned(chunks)), dim3(kThreads), 0, 1, stream, t)
+                 : launch(adamw_kernel<CAP, false>, dim3(unsigned(chunks)), dim3(kThreads), 0, 1, stream, t);
+}
+
+basp_status check_tensor(const basp_adamw_tensor &x, bool eight) {
+    const int64_t ps = elem_size(x.dtype), gs = elem_size(x.grad_dtype);
+    if (ps == 0 || gs == 0 || (x.grad_dtype != x.dtype && x.grad_dtype != BASP_DTYPE_FP32) || x.n < 0)
+        return BASP_ERR_INVALID_ARG;
+    if (x.n == 0) return BASP_OK;
+    if ((x.m_scales != nullptr) != eight || (x.v_scales != nullptr) != eight) return BASP_ERR_INVALID_ARG;
+    if (chunks_of(x.n) > kMaxSide) return BASP_ERR_TOO_LARGE;
+    const int64_t ss = eight ? 1 : 4;
+    Args args;
+    args.matrix(x.p, 1, x.n, x.n, ps, true);
+    args.matrix(x.g, 1, x.n, x.n, gs, false);
+    args.matrix(x.m, 1, x.n, x.n, ss, true);
+    args.matrix(x.v, 1, x.n, x.n, ss, true);
+    if (eight) {
+        args.matrix(x.m_scales, 1, ceil_div(x.n, kBlock), x.n, 1, true);
+        args.matrix(x.v_scales, 1, ceil_div(x.n, kBlock), x.n, 1, true);
+    }
+    return args.status();
+}
+
+}  // namespace
+}  // namespace basp_fp8
+
+using namespace basp_fp8;
+
+extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_adamw_options *options,
+                                  cudaStream_t stream) {
+    NvtxRange range("basp_adamw");
+    if (count < 0 || options == nullptr || (tensors == nullptr && count > 0)) return BASP_ERR_INVALID_ARG;
+    const basp_adamw_options &p = *options;
+    // a comparison that a NaN fails
+    if (!(p.lr >= 0 && p.lr < INFINITY && p.beta1 >= 0 && p.beta1 < 1 && p.beta2 >= 0 && p.beta2 < 1 && p.eps >= 0 &&
+          p.eps < INFINITY && p.weight_decay >= 0 && p.weight_decay < INFINITY))
+        return BASP_ERR_INVALID_ARG;
+    if (p.step_at == nullptr && (p.step < 1 || p.step > kMaxSide)) return BASP_ERR_INVALID_ARG;
+    if (uintptr_t(p.step_at) % 4) return BASP_ERR_ALIGNMENT;
+    if (count > kMaxSide) return BASP_ERR_TOO_LARGE;
+    bool eight = false;
+    for (int64_t i = 0; i < count; ++i)
+        if (tensors[i].n > 0) {
+            eight = tensors[i].m_scales != nullptr;
+            break;
+        }
+    for (int64_t i = 0; i < count; ++i) {
+        const basp_status st = check_tensor(tensors[i], eight);
+        if (st != BASP_OK) return st;
+    }
+
+    Options o = {};
+    o.beta1 = float(p.beta1); o.beta2 = float(p.beta2);
+    o.one_beta1 = float(1 - p.beta1); o.one_beta2 = float(1 - p.beta2);
+    o.eps = float(p.eps); o.decay = float(1 - p.lr * p.weight_decay); o.lr = float(p.lr);
+    o.seed = p.seed;
+    o.step_at = p.step_at;
+    if (p.step_at == nullptr) {
+        o.step = uint32_t(p.step);
+        o.c1 = float(p.lr / (1 - std::pow(p.beta1, double(p.step))));
+        o.c2 = float(1 / std::sqrt(1 - std::pow(p.beta2, double(p.step))));
+    } else {
+        o.log_beta1 = float(std::log(p.beta1));      // of 0: minus infinity, and beta^t = 0
+        o.log_beta2 = float(std::log(p.beta2));
+    }
+    // Tables of three sizes: a launch copies all of its parameters.
+    basp_status st = BASP_OK;
+    for (int64_t i = 0; i < count && st == BASP_OK;) {
+        if (count - i <= 12) st = launch_adamw<12>(tensors, i, count, eight, o, &i, stream);
+        else if (count - i <= 60) st = launch_adamw<60>(tensors, i, count, eight, o, &i, stream);
+        else st = launch_adamw<500>(tensors, i, count, eight, o, &i, stream);
+    }
+    return st;
+}

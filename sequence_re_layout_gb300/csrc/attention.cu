@@ -1,0 +1,269 @@
+// attention.cu -- causal attention with a sliding window and sinks: forward,
+// backward and one token over a cache (include/basp_attention.h).
+#include <algorithm>
+
+#include "attention_common.cuh"
+
+namespace basp_fp8 {
+namespace {
+
+__device__ unsigned long long g_timeouts;
+
+constexpr int kRowWarps = 4;
+
+enum { kForward, kDelta, kDq, kDkv };
+
+// A warp a row.
+template <class T, int WHAT>
+__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ AttentionArgs a) {
+    __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
+    grid_dependency();
+    const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : a.sq;
+    const int64_t rows = int64_t(a.batch) * heads * len;
+    for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
+        const int i = int(r % len), h = int(r / len % heads), b = int(r / len / heads);
+        float *m = mine[threadIdx.x / 32];
+        if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i, m);
+        if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i, m);
+        if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i, m);
+        if constexpr (WHAT == kDelta) {
+            const float s = delta_row<T>(a, b, h, i);
+            if (threadIdx.x % 32 == 0) a.delta[r] = s;
+        }
+    }
+}
+
+template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cudaStream_t stream) {
+    const int64_t rows = int64_t(a.batch) * (WHAT == kDkv ? int64_t(a.hkv) * a.sk : int64_t(a.hq) * a.sq);
+    if (rows == 0) return BASP_OK;
+    const int64_t ctas = std::min<int64_t>(ceil_div(rows, kRowWarps), 1 << 20);
+    return launch(rows_kernel<T, WHAT>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a);
+}
+
+// One token: the row's keys are those of a query at position lengths[b] - 1.
+template <class T>
+__global__ void __launch_bounds__(kRowWarps * 32) decode_rows_kernel(const __grid_constant__ AttentionArgs a,
+                                                                     const int32_t *lengths) {
+    __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
+    grid_dependency();
+    const int64_t rows = int64_t(a.batch) * a.hq;
+    for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
+        const int b = int(r / a.hq);
+        AttentionArgs s = a;
+        s.sk = max(0, min(a.sk, lengths[b]));
+        forward_row<T>(s, b, int(r % a.hq), 0, mine[threadIdx.x / 32]);
+    }
+}
+
+// ---- host -----------------------------------------------------------------------
+
+bool sizes_ok(const basp_attention_desc *d, basp_status *st) {
+    *st = BASP_ERR_INVALID_ARG;
+    if (d == nullptr || d->batch < 0 || d->q_len < 0 || d->k_len < 0 || d->q_heads < 0 || d->k_heads < 0 ||
+        d->window < 0 || d->sinks < 0 || !(d->scale > -INFINITY && d->scale < INFINITY))
+        return false;
+    if (d->dtype != BASP_DTYPE_BF16 && d->dtype != BASP_DTYPE_FP16) return false;
+    if (d->head_dim < 8 || d->head_dim > kMaxHeadDim || d->head_dim % 8) return false;
+    if (d->k_heads == 0 ? d->q_heads != 0 : d->q_heads % d->k_heads != 0) {
+        *st = BASP_ERR_DIVISIBILITY;
+        return false;
+    }
+    *st = BASP_ERR_TOO_LARGE;
+    for (int64_t n : {d->batch, d->q_len, d->k_len, d->q_heads, d->k_heads})
+        if (n > kMaxSide) return false;
+    *st = BASP_OK;
+    return true;
+}
+
+// Rows of all heads and sequences: a counter of 64 bits holds their elements.
+bool rows_ok(const basp_attention_desc *d) {
+    const __int128 q = __int128(d->batch) * d->q_heads * d->q_len, k = __int128(d->batch) * d->k_heads * d->k_len;
+    return q <= (int64_t(1) << 48) && k <= (int64_t(1) << 48);
+}
+
+// Checks of a call's tensors: each has len x heads rows of head_dim in each sequence.
+class HeadArgs {
+  public:
+    explicit HeadArgs(const basp_attention_desc *d) : d_(d) {}
+    void heads(const basp_heads *t, int64_t len, int64_t heads, bool out) {
+        if (d_->batch == 0 || len == 0 || heads == 0) return;
+        if (t == nullptr || t->data == nullptr || t->stride_batch < 0 || t->stride_seq < 0 || t->stride_head < 0)
+            return fail(BASP_ERR_INVALID_ARG);
+        if (uintptr_t(t->data) % 16 || t->stride_batch % 8 || t->stride_seq % 8 || t->stride_head % 8)
+            return fail(BASP_ERR_ALIGNMENT);
+        const int64_t n[3] = {d_->batch, len, heads};
+        int64_t s[3] = {t->stride_batch, t->stride_seq, t->stride_head};
+        __int128 last = 0;
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] == 1) s[i] = 0;             // says nothing
+            last += __int128(n[i] - 1) * s[i];
+        }
+        if (last > (int64_t(1) << 56)) return fail(BASP_ERR_TOO_LARGE);
+        if (out && !apart(n, s)) return fail(BASP_ERR_ALIASING);
+        args_.matrix(t->data, 1, int64_t(last) + d_->head_dim, 0, 2, out);
+    }
+    void vector(const void *p, int64_t n, int64_t esz, bool out, bool need = true) {
+        args_.matrix(p, n > 0 ? 1 : 0, n, n, esz, out, need);
+    }
+    void fail(basp_status s) { args_.fail(s); }
+    basp_status status() const { return args_.status(); }
+
+  private:
+    // Whether no two elements of an output share an address: from the smallest stride
+    // outwards, each steps over all that the smaller ones reach.
+    bool apart(const int64_t (&n)[3], const int64_t (&s)[3]) const {
+        int order[3] = {0, 1, 2};
+        std::sort(order, order + 3, [&](int x, int y) { return s[x] < s[y]; });
+        __int128 reach = d_->head_dim;
+        for (int i : order) {
+            if (n[i] == 1) continue;
+            if (s[i] < reach) return false;
+            reach += __int128(n[i] - 1) * s[i];
+        }
+        return true;
+    }
+    const basp_attention_desc *d_;
+    Args args_;
+};
+
+Heads heads_of(const basp_heads *t) {
+    if (t == nullptr) return {};
+    return {t->data, t->stride_batch, t->stride_seq, t->stride_head};
+}
+
+AttentionArgs args_of(const basp_attention_desc *d) {
+    AttentionArgs a = {};
+    a.batch = int(d->batch); a.sq = int(d->q_len); a.sk = int(d->k_len);
+    a.hq = int(d->q_heads); a.hkv = int(d->k_heads); a.d = int(d->head_dim);
+    a.group = d->k_heads > 0 ? int(d->q_heads / d->k_heads) : 1;
+    a.window = d->window == 0 ? int(std::max<int64_t>(1, d->k_len)) : int(std::min<int64_t>(d->window, kMaxSide));
+    a.sinks = int(std::min<int64_t>(d->sinks, kMaxSide));
+    a.scale = d->scale;
+    return a;
+}
+
+template <class F> basp_status with_type(basp_dtype t, F &&f) {
+    return t == BASP_DTYPE_BF16 ? f(__nv_bfloat16()) : f(__half());
+}
+
+}  // namespace
+}  // namespace basp_fp8
+
+using namespace basp_fp8;
+
+extern "C" basp_status basp_attention(const basp_attention_desc *desc, const basp_heads *q, const basp_heads *k,
+                                      const basp_heads *v, const basp_heads *o, float *lse, cudaStream_t stream) {
+    NvtxRange range("basp_attention");
+    basp_status st;
+    if (!sizes_ok(desc, &st)) return st;
+    if (!rows_ok(desc)) return BASP_ERR_TOO_LARGE;
+    HeadArgs args(desc);
+    args.heads(q, desc->q_len, desc->q_heads, false);
+    args.heads(k, desc->k_len, desc->k_heads, false);
+    args.heads(v, desc->k_len, desc->k_heads, false);
+    args.heads(o, desc->q_len, desc->q_heads, true);
+    args.vector(lse, desc->batch * desc->q_heads * desc->q_len, 4, true, false);
+    st = args.status();
+    if (st != BASP_OK) return st;
+    AttentionArgs a = args_of(desc);
+    a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o);
+    a.lse = lse;
+    return with_type(desc->dtype, [&](auto t) { return launch_rows<decltype(t), kForward>(a, stream); });
+}
+
+extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
+    basp_status st;
+    if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
+    return desc->batch * desc->q_heads * desc->q_len * int64_t(sizeof(float));
+}
+
+extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
+                                               const basp_heads *k, const basp_heads *v, const basp_heads *o,
+                                               const float *lse, const basp_heads *d_o, const basp_heads *dq,
+                                               const basp_heads *dk, const basp_heads *dv, void *workspace,
+                                               size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange range("basp_attention_backward");
+    basp_status st;
+    if (!sizes_ok(desc, &st)) return st;
+    if (!rows_ok(desc)) return BASP_ERR_TOO_LARGE;
+    HeadArgs args(desc);
+    args.heads(q, desc->q_len, desc->q_heads, false);
+    args.heads(k, desc->k_len, desc->k_heads, false);
+    args.heads(v, desc->k_len, desc->k_heads, false);
+    args.heads(o, desc->q_len, desc->q_heads, false);
+    args.heads(d_o, desc->q_len, desc->q_heads, false);
+    args.heads(dq, desc->q_len, desc->q_heads, true);
+    args.heads(dk, desc->k_len, desc->k_heads, true);
+    args.heads(dv, desc->k_len, desc->k_heads, true);
+    args.vector(lse, desc->batch * desc->q_heads * desc->q_len, 4, false);
+    const int64_t need = basp_attention_backward_workspace(desc);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < size_t(need)) args.fail(BASP_ERR_WORKSPACE);
+        else if (uintptr_t(workspace) % 16) args.fail(BASP_ERR_ALIGNMENT);
+        else args.vector(workspace, need, 1, true);
+    }
+    st = args.status();
+    if (st != BASP_OK) return st;
+    AttentionArgs a = args_of(desc);
+    a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o); a.d_o = heads_of(d_o);
+    a.dq = heads_of(dq); a.dk = heads_of(dk); a.dv = heads_of(dv);
+    a.lse = const_cast<float *>(lse);
+    a.delta = static_cast<float *>(workspace);
+    return with_type(desc->dtype, [&](auto t) {
+        using T = decltype(t);
+        basp_status s = launch_rows<T, kDelta>(a, stream);
+        if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);
+        if (s == BASP_OK) s = launch_rows<T, kDkv>(a, stream);
+        return s;
+    });
+}
+
+extern "C" int64_t basp_attention_decode_workspace(const basp_attention_desc *desc) {
+    basp_status st;
+    if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
+    return 0;
+}
+
+extern "C" basp_status basp_attention_decode(const basp_attention_desc *desc, const basp_heads *q,
+                                             const basp_heads *k, const basp_heads *v, const int32_t *lengths,
+                                             const basp_heads *o, void *workspace, size_t workspace_bytes,
+                                             cudaStream_t stream) {
+    NvtxRange range("basp_attention_decode");
+    basp_status st;
+    if (!sizes_ok(desc, &st)) return st;
+    if (desc->q_len != 1) return BASP_ERR_INVALID_ARG;
+    if (!rows_ok(desc)) return BASP_ERR_TOO_LARGE;
+    HeadArgs args(desc);
+    args.heads(q, 1, desc->q_heads, false);
+    args.heads(k, desc->k_len, desc->k_heads, false);
+    args.heads(v, desc->k_len, desc->k_heads, false);
+    args.heads(o, 1, desc->q_heads, true);
+    args.vector(lengths, desc->batch, 4, false);
+    const int64_t need = basp_attention_decode_workspace(desc);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < size_t(need)) args.fail(BASP_ERR_WORKSPACE);
+        else if (uintptr_t(workspace) % 16) args.fail(BASP_ERR_ALIGNMENT);
+        else args.vector(workspace, need, 1, true);
+    }
+    st = args.status();
+    if (st != BASP_OK || desc->batch == 0 || desc->q_heads == 0) return st;
+    AttentionArgs a = args_of(desc);
+    a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o);
+    return with_type(desc->dtype, [&](auto t) {
+        using T = decltype(t);
+        const int64_t ctas = std::min<int64_t>(ceil_div(int64_t(a.batch) * a.hq, kRowWarps), 1 << 20);
+        return launch(decode_rows_kernel<T>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a, lengths);
+    });
+}
+
+extern "C" basp_status basp_attention_timeouts(unsigned long long *count) {
+    if (count == nullptr) return BASP_ERR_INVALID_ARG;
+    const unsigned long long zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpyFromSymbol(count, g_timeouts, sizeof(*count)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_timeouts, &zero, sizeof(zero)) != cudaSuccess) {
+        cudaGetLastError();
+        return BASP_ERR_CUDA;
+    }
+    return BASP_OK;
+}

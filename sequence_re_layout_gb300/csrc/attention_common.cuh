@@ -1,0 +1,194 @@
+// attention_common.cuh -- what the attention kernels share: which keys a query
+// sees, the tensors as kernels take them, and the plain form, row by row.
+#pragma once
+
+#include "basp_attention.h"
+#include "fp8_common.cuh"
+
+namespace basp_fp8 {
+
+constexpr int kMaxHeadDim = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Heads {
+    void *p;
+    int64_t sb, ss, sh;
+};
+
+template <class T> __device__ __forceinline__ T *row_of(const Heads &t, int64_t b, int64_t s, int64_t h) {
+    return static_cast<T *>(t.p) + b * t.sb + s * t.ss + h * t.sh;
+}
+
+struct AttentionArgs {
+    Heads q, k, v, o, d_o, dq, dk, dv;
+    float *lse, *delta;                  // [batch][Hq][Sq]
+    int batch, sq, sk, hq, hkv, d, group;
+    int window, sinks;                   // window: sk where all is visible
+    float scale;
+};
+
+// The query at position p sees keys [0, first_end) and [last, p].
+struct Sees {
+    int first_end, last;
+};
+__device__ __forceinline__ Sees keys_of(const AttentionArgs &a, int p) {
+    const int low = max(0, p - a.window + 1);
+    return {min(a.sinks, low), low};
+}
+// Key j is seen by the positions [j, last position].
+__device__ __forceinline__ int last_position(const AttentionArgs &a, int j) {
+    return j < a.sinks ? a.sk - 1 : min(int64_t(a.sk) - 1, int64_t(j) + a.window - 1);
+}
+
+// ---- the plain form -----------------------------------------------------------------
+//
+// A warp computes one row from its definition, reading nothing but what the row
+// sees: lanes hold a key (or a query) each for the products, then four elements of
+// the row each for the sums.  `mine` is 2 x 128 floats of shared memory of the warp.
+
+template <class T> __device__ __forceinline__ float row_dot(const float *x, const T *y, int d) {
+    float s = 0.f;
+    for (int e = 0; e < d; e += 8) {
+        float f[8];
+        Pack<T>::unpack(*reinterpret_cast<const uint4 *>(y + e), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(x[e + j], f[j], s);
+    }
+    return s;
+}
+
+template <class T> __device__ __forceinline__ void row_to_shared(float *mine, const T *row, int d, int lane) {
+    for (int e = lane; e < d; e += 32) mine[e] = Elem<T>::to_float(row[e]);
+    __syncwarp();
+}
+
+template <class T> __device__ __forceinline__ void row_add(float (&sum)[4], float p, const T *row, int d, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < d) sum[j] = fmaf(p, Elem<T>::to_float(row[lane + 32 * j]), sum[j]);
+}
+
+template <class T> __device__ __forceinline__ void row_store(T *row, const float (&v)[4], int d, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < d) row[lane + 32 * j] = Elem<T>::from_float(v[j]);
+}
+
+// Calls f(j) for 32 keys at a time of [0, first_end) and [low, end): `have` says
+// whether this lane's exists.
+template <class F> __device__ __forceinline__ void each_keys(int first_end, int low, int end, int lane, F &&f) {
+    for (int j0 = 0; j0 < first_end; j0 += 32) f(j0 + lane, j0 + lane < first_end);
+    for (int j0 = low; j0 < end; j0 += 32) f(j0 + lane, j0 + lane < end);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = v > w || v != v ? v : w;                 // a NaN stays
+    }
+    return v;
+}
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// o and lse of query i.
+template <class T>
+__device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, int i, float *mine) {
+    const int lane = threadIdx.x % 32, p = i + a.sk - a.sq, kh = h / a.group;
+    const Sees see = keys_of(a, p);
+    __syncwarp();
+    row_to_shared(mine, row_of<const T>(a.q, b, i, h), a.d, lane);
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
+        const float s = have ? a.scale * row_dot(mine, row_of<const T>(a.k, b, j, kh), a.d) : -INFINITY;
+        const float top = warp_max(s), next = m > top || m != m ? m : top;
+        const float w = have ? expf(s - next) : 0.f, old = m == -INFINITY && l == 0.f ? 0.f : expf(m - next);
+        l = l * old + warp_add(w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= old;
+        m = next;
+        for (int x = 0; x < 32; ++x) {
+            const int jx = __shfl_sync(0xffffffffu, j, x);
+            const float wx = __shfl_sync(0xffffffffu, w, x);
+            if (__shfl_sync(0xffffffffu, int(have), x)) row_add(o, wx, row_of<const T>(a.v, b, jx, kh), a.d, lane);
+        }
+    });
+    const bool any = p >= 0;                         // whoever sees anything sees itself
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = any ? o[e] / l : 0.f;
+    row_store(row_of<T>(a.o, b, i, h), o, a.d, lane);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[(int64_t(b) * a.hq + h) * a.sq + i] = any ? m + logf(l) : -INFINITY;
+}
+
+// D of query i: do . o.
+template <class T> __device__ __forceinline__ float delta_row(const AttentionArgs &a, int b, int h, int i) {
+    const int lane = threadIdx.x % 32;
+    const T *o = row_of<const T>(a.o, b, i, h), *d_o = row_of<const T>(a.d_o, b, i, h);
+    float s = 0.f;
+    for (int e = lane; e < a.d; e += 32) s = fmaf(Elem<T>::to_float(o[e]), Elem<T>::to_float(d_o[e]), s);
+    return warp_add(s);
+}
+
+// dq of query i.
+template <class T>
+__device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i, float *mine) {
+    const int lane = threadIdx.x % 32, p = i + a.sk - a.sq, kh = h / a.group;
+    const Sees see = keys_of(a, p);
+    __syncwarp();
+    row_to_shared(mine, row_of<const T>(a.q, b, i, h), a.d, lane);
+    row_to_shared(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d, lane);
+    const int64_t at = (int64_t(b) * a.hq + h) * a.sq + i;
+    const float lse = a.lse[at], delta = a.delta[at];
+    float dq[4] = {0.f, 0.f, 0.f, 0.f};
+    each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
+        float ds = 0.f;
+        if (have) {
+            const float w = expf(a.scale * row_dot(mine, row_of<const T>(a.k, b, j, kh), a.d) - lse);
+            ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.v, b, j, kh), a.d) - delta) * a.scale;
+        }
+        for (int x = 0; x < 32; ++x) {
+            const int jx = __shfl_sync(0xffffffffu, j, x);
+            const float dx = __shfl_sync(0xffffffffu, ds, x);
+            if (__shfl_sync(0xffffffffu, int(have), x)) row_add(dq, dx, row_of<const T>(a.k, b, jx, kh), a.d, lane);
+        }
+    });
+    row_store(row_of<T>(a.dq, b, i, h), dq, a.d, lane);
+}
+
+// dk and dv of key j, over all query heads that share it.
+template <class T>
+__device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int j, float *mine) {
+    const int lane = threadIdx.x % 32, shift = a.sk - a.sq;
+    __syncwarp();
+    row_to_shared(mine, row_of<const T>(a.k, b, j, kh), a.d, lane);
+    row_to_shared(mine + kMaxHeadDim, row_of<const T>(a.v, b, j, kh), a.d, lane);
+    const int i0 = max(0, j - shift), i1 = last_position(a, j) - shift + 1;
+    float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int h = kh * a.group; h < (kh + 1) * a.group; ++h) {
+        const int64_t at = (int64_t(b) * a.hq + h) * a.sq;
+        each_keys(0, i0, i1, lane, [&](int i, bool have) {
+            float w = 0.f, ds = 0.f;
+            if (have) {
+                w = expf(a.scale * row_dot(mine, row_of<const T>(a.q, b, i, h), a.d) - a.lse[at + i]);
+                ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d) - a.delta[at + i]) * a.scale;
+            }
+            for (int x = 0; x < 32; ++x) {
+                const int ix = __shfl_sync(0xffffffffu, i, x);
+                const float wx = __shfl_sync(0xffffffffu, w, x), dx = __shfl_sync(0xffffffffu, ds, x);
+                if (__shfl_sync(0xffffffffu, int(have), x)) {
+                    row_add(dv, wx, row_of<const T>(a.d_o, b, ix, h), a.d, lane);
+                    row_add(dk, dx, row_of<const T>(a.q, b, ix, h), a.d, lane);
+                }
+            }
+        });
+    }
+    row_store(row_of<T>(a.dk, b, j, kh), dk, a.d, lane);
+    row_store(row_of<T>(a.dv, b, j, kh), dv, a.d, lane);
+}
+
+}  // namespace basp_fp8

@@ -99,6 +99,24 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, need_dweight=True):
     return (_ops or _load()).rmsnorm_backward(dy, h, rstd, weight, dh, bool(need_dweight))
 
 
+def layernorm(x, weight, bias=None, residual=None, eps=1e-5, quantized=True, h=None):
+    """Residual addition and layer norm over the last dimension: ``h = x +
+    residual``, ``y = (h - mean) / sqrt(var + eps) * weight + bias``.
+
+    Returns ``(y, h, mean, rstd)``: y and h as :func:`rmsnorm` gives them, mean and
+    rstd float32 [rows], which the backward takes.  ``weight`` and ``bias`` have one
+    type, x's or float32."""
+    y, scales, new_h, mean, rstd = (_ops or _load()).layernorm(x, weight, bias, residual, eps, bool(quantized), h)
+    return Quantized(y, scales) if quantized else y, x if new_h is None else new_h, mean, rstd
+
+
+def layernorm_backward(dy, h, mean, rstd, weight, dh=None, need_dweight=True, need_dbias=True):
+    """``(dx, dweight, dbias)`` of :func:`layernorm`: dx is the gradient of x and of
+    the residual alike, with ``dh`` (the gradient that reaches h past the norm)
+    added; dweight and dbias are float32, or None if not needed."""
+    return (_ops or _load()).layernorm_backward(dy, h, mean, rstd, weight, dh, bool(need_dweight), bool(need_dbias))
+
+
 def quantize(x, block_rows=1, rows=True, transposed=False):
     """x [..., cols] to 8 bits with a scale for each ``block_rows`` x 128
     values.  ``transposed`` adds the transpose [cols, rows] with scales along

@@ -1,0 +1,129 @@
+"""AdamW over many tensors at once, over the C ABI of ``include/basp_optim.h``: one
+launch for a few hundred tensors, states in 32 bits or in 8.
+
+    optimizer = optim.AdamW(layer.parameters(), lr=3e-4, weight_decay=0.1, state_bits=8)
+    loss.backward()
+    optimizer.step()
+
+8-bit states hold m and the root of v in e4m3 with a power-of-two scale for each 128
+elements, rounded at random (2 bytes and a 64th an element instead of 8).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import fp8
+
+
+@torch.no_grad()
+def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, seed=0):
+    """One step over lists of tensors, in place: params (bfloat16, float16 or
+    float32), grads (their type or float32), and the states m and v: float32 tensors,
+    or :class:`fp8.Quantized` of one row ([1, n]), v then the root of v.
+
+    ``step`` counts from 1; as an int32 tensor of one element on the GPU it is read
+    when the kernel runs, so that a captured step can be replayed.  The random
+    rounding of 8-bit states depends on ``seed``, the step and each element's place
+    alone.  Every tensor is dense, and none overlaps another."""
+    m, v = list(m), list(v)
+    m_scales = v_scales = None
+    if m and isinstance(m[0], fp8.Quantized):
+        m, m_scales = _parts(m)
+        v, v_scales = _parts(v)
+    (fp8._ops or fp8._load()).adamw(list(params), list(grads), m, v, m_scales, v_scales, step, lr, betas[0], betas[1],
+                                    eps, weight_decay, seed)
+
+
+def _parts(states):
+    if not all(isinstance(s, fp8.Quantized) and s.block_rows == 1 for s in states):
+        raise ValueError("adamw: states must all be float32 tensors, or all fp8.Quantized with a scale for each row's 128")
+    return [s.data for s in states], [s.scales for s in states]
+
+
+class AdamW(torch.optim.Optimizer):
+    """Adam with decoupled weight decay; parameters on the current GPU, dense.
+
+    ``state_bits`` 32 or 8.  ``seed`` is that of the 8-bit states' rounding.  With
+    ``capturable`` the step's number lives on the GPU, so ``step()`` can be captured
+    in a CUDA graph and replayed; without, a capture is refused."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, seed=0,
+                 capturable=False):
+        if state_bits not in (8, 32):
+            raise ValueError("AdamW: state_bits must be 8 or 32, got %r" % (state_bits,))
+        if not (lr >= 0 and eps >= 0 and weight_decay >= 0 and all(0 <= b < 1 for b in betas)):
+            raise ValueError("AdamW: lr, eps and weight_decay must not be negative, betas in [0, 1)")
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
+                                      state_bits=state_bits, seed=seed, capturable=capturable))
+
+    def _init(self, p, group, step):
+        state = self.state[p]
+        state["step"] = step
+        for name in ("exp_avg", "exp_avg_sq" if group["state_bits"] == 32 else "exp_avg_sq_root"):
+            if group["state_bits"] == 32:
+                state[name] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                continue
+            state[name] = torch.zeros(1, p.numel(), dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
+            state[name + "_scales"] = torch.full((1, -(-p.numel() // fp8.BLOCK)), 127, dtype=torch.uint8,
+                                                 device=p.device).view(torch.float8_e8m0fnu)
+        return state
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        """One step over every parameter that has a gradient.  Parameters that joined
+        in the same step share its number; those that joined later count their own."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            if not group["capturable"] and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("AdamW: a captured step would keep its number: pass capturable=True")
+            together, first = {}, None
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if not self.state[p]:
+                    if first is None:
+                        first = torch.zeros(1, dtype=torch.int32, device=p.device) if group["capturable"] else 0
+                    self._init(p, group, first)
+                step = self.state[p]["step"]
+                together.setdefault(id(step) if group["capturable"] else step, []).append(p)
+            for params in together.values():
+                self._take(params, group)
+        return loss
+
+    def _take(self, params, group):
+        states = [self.state[p] for p in params]
+        if group["capturable"]:
+            states[0]["step"].add_(1)
+        else:
+            for s in states:
+                s["step"] += 1
+        if group["state_bits"] == 32:
+            m, v = [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states]
+        else:
+            m, v = ([fp8.Quantized(s[n], s[n + "_scales"]) for s in states] for n in ("exp_avg", "exp_avg_sq_root"))
+        adamw(params, [p.grad.contiguous() for p in params], m, v, step=states[0]["step"], lr=group["lr"],
+              betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"])
+
+    def load_state_dict(self, state_dict):
+        """As torch's, but states keep the types they were saved in."""
+        super().load_state_dict(state_dict)
+        numbers = [i for g in state_dict["param_groups"] for i in g["params"]]
+        places = [(p, g) for g in self.param_groups for p in g["params"]]
+        shared = {}
+        for i, (p, group) in zip(numbers, places):
+            if i not in state_dict["state"]:
+                continue
+            state = {n: x.detach().to(p.device, copy=True) if torch.is_tensor(x) else x
+                     for n, x in state_dict["state"][i].items()}
+            count = int(state["step"])
+            if group["capturable"]:                   # one number on the GPU for those that count together
+                key = id(group), count
+                if key not in shared:
+                    shared[key] = torch.full((1,), count, dtype=torch.int32, device=p.device)
+                state["step"] = shared[key]
+            else:
+                state["step"] = count
+            self.state[p] = state

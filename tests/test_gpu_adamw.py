@@ -1,0 +1,317 @@
+"""AdamW over many tensors (include/basp_optim.h) against its 64-bit form.
+
+Tolerances.  A rounding of m' is 3 * 2^-24 of the magnitudes it adds, of v' 4 * 2^-24 of
+itself; the quotient has the root's half of that, c1's and c2's 2^-24 each and a
+division good to 2^-22: 2^-20 of the step in all, and p's own roundings (the decay's
+factor, the sum, and its type's)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_reference as ref8
+import layer_reference as ref
+from sequence_re_layout_gb300 import fp8, optim
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+F32, TINY = ref.F32, ref.TINY
+BETAS, EPS = (0.9, 0.999), 1e-8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sequence_re_layout_gb300.build import build_library
+    build_library()
+
+
+def u(t):
+    return torch.finfo(t).eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def random(n, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(n, generator=g) * scale).to(dtype).cuda()
+
+
+def spread(n, seed):
+    """Magnitudes over several powers of ten."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.exp(2 * torch.randn(n, generator=g) - 6).cuda()
+
+
+def check(p, g, m, v, got, step, lr, wd):
+    """(p', m', v') of 64 bits, the kernel's against them; m and v as the kernel had them."""
+    p1, m1, v1 = ref.adamw(f64(p), f64(g), m, v, step, lr, *BETAS, EPS, wd)
+    up = np.abs(p1 - f64(p) * (1 - lr * wd))
+    em = 4 * F32 * (np.abs(m) + np.abs(f64(g)))
+    room = lr / (1 - BETAS[0] ** step) * em / (np.sqrt(v1) / np.sqrt(1 - BETAS[1] ** step) + EPS)
+    bound = 2.0 ** -20 * up + 2 * room + 3 * F32 * np.abs(f64(p)) + TINY
+    assert (np.abs(f64(got) - p1) <= bound + u(got.dtype) * (np.abs(p1) + bound)).all()
+    return m1, v1, em
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("grad32", [False, True])
+@pytest.mark.parametrize("step", [1, 2, 1000, 2 ** 31 - 1])
+def test_32_bits(dtype, grad32, step):
+    t = DTYPES[dtype]
+    sizes = [1, 3, 4, 127, 128, 129, 512, 1000, 4096, 16384, 16385, 50000, 0]
+    p = [random(n, t, 3 * i) for i, n in enumerate(sizes)]
+    g = [(random(n, torch.float32, 3 * i + 1) * spread(n, i)).to(torch.float32 if grad32 else t) for i, n in enumerate(sizes)]
+    m = [random(n, torch.float32, 3 * i + 2) * spread(n, i) for i, n in enumerate(sizes)]
+    v = [(spread(n, i + 50)) ** 2 for i, n in enumerate(sizes)]
+    old = [[x.clone() for x in xs] for xs in (p, m, v)]
+    optim.adamw(p, g, m, v, step, lr=0.01, weight_decay=0.1)
+    for i in range(len(sizes)):
+        m1, v1, em = check(old[0][i], g[i], f64(old[1][i]), f64(old[2][i]), p[i], step, 0.01, 0.1)
+        assert (np.abs(f64(m[i]) - m1) <= em + TINY * 2.0 ** -100).all()
+        assert (np.abs(f64(v[i]) - v1) <= 6 * F32 * v1 + 2.0 ** -148).all()
+
+
+def quantized(values):
+    """[1, n] in 8 bits, as a state."""
+    return fp8.quantize(values.view(1, -1).float())
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("step,seed", [(1, 0), (7, 123456789), (2 ** 31 - 1, 2 ** 32 - 1)])
+def test_8_bits(dtype, step, seed):
+    t = DTYPES[dtype]
+    sizes = [1, 3, 127, 128, 129, 130, 1000, 4096, 16384, 16390, 50000]
+    p = [random(n, t, 3 * i) for i, n in enumerate(sizes)]
+    g = [(random(n, torch.float32, 3 * i + 1) * spread(n, i)).to(t) for i, n in enumerate(sizes)]
+    m = [quantized(random(n, torch.float32, 3 * i + 2) * spread(n, i)) for i, n in enumerate(sizes)]
+    v = [quantized(spread(n, i + 50)) for i, n in enumerate(sizes)]
+    old_p, old_m, old_r = [x.clone() for x in p], [f64(x.dequantize())[0] for x in m], [f64(x.dequantize())[0] for x in v]
+    optim.adamw(p, g, m, v, step, lr=0.01, weight_decay=0.1, seed=seed)
+    flips = total = 0
+    for i, n in enumerate(sizes):
+        m1, v1, em = check(old_p[i], g[i], old_m[i], old_r[i] ** 2, p[i], step, 0.01, 0.1)
+        for q, want, error, r in ((m[i], m1, em, 0), (v[i], np.sqrt(v1), 4 * F32 * np.sqrt(v1), 1)):
+            e = q.scales.cpu().view(torch.uint8).numpy().astype(np.int64)[0] - 127
+            exps = ref8.quantize(want[None], 1)[1][0]
+            blocks = np.arange(n) // 128
+            same = (e == exps)[blocks]                     # a block's maximum next to a power's end may go either way
+            assert (np.abs(e - exps) <= 1).all() and (e != exps).mean() <= 0.02
+            scale = 2.0 ** e[blocks].astype(np.float64)
+            y, room = ref.round_at_random(want / scale, ref.random_bits(n, seed, step, i)[r])
+            got = f64(q.data.float())[0]
+            if r:
+                y = np.where((want > 0) & (y == 0), 2.0 ** -9, y)
+            steps = error / scale / 2.0 ** (np.maximum(np.frexp(np.abs(want / scale))[1] - 1, -6) - 3)
+            sure = same & (room > steps + 2.0 ** -18)      # 32 bits decide as 64 do
+            assert np.array_equal(got[sure], y[sure])
+            assert sure[same].mean() > 0.9 or n < 200
+            step_up = 2.0 ** -3 * np.abs(want) + 2.0 ** -9 * scale + 2 * error
+            assert (np.abs(got * scale - want) <= step_up).all()
+
+
+def test_the_rounding_is_fair():
+    """The mean over many elements is the value: each is up with the fraction's
+    probability.  2^20 draws: six standard deviations of sqrt(1/4 / 2^20) steps."""
+    n = 1 << 20
+    p, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    for value in (0.3, 1.0, 2.0 ** -9 * 0.4, 100.0):
+        m = quantized(torch.full((n,), 448.0, device="cuda"))
+        v = quantized(torch.full((n,), 448.0, device="cuda"))
+        g.fill_(0.0)
+        # m' = 0.9 * 448 in a block whose largest is 448: the block's first keeps the scale
+        g[:] = (value - 0.9 * 448) / 0.1
+        g[::128] = 448.0
+        optim.adamw([p], [g], [m], [v], 5, lr=0.0, weight_decay=0.0, seed=7)
+        rest = torch.ones(n, dtype=torch.bool, device="cuda")
+        rest[::128] = False
+        want = 0.9 * 448 + 0.1 * float(g[1])
+        got = m.dequantize()[0][rest].double()
+        step = float(2.0 ** (max(np.floor(np.log2(value)), -6) - 3))
+        assert abs(float(got.mean()) - want) <= 6 * 0.5 * step / np.sqrt(n * 127 / 128) + 2.0 ** -16 * 448 * 2.0 ** -6
+        # m' is off by roundings of 0.9 * 448: next to a power of two it may be below it, where steps are half as wide
+        grid = step / 2 if np.log2(value) == np.floor(np.log2(value)) else step
+        assert set(np.unique(f64(got) / grid % 1)) == {0.0}
+
+
+def test_small_changes_of_v_are_not_lost():
+    """A gradient of zero for 700 steps: v falls by 0.999^700, its root by half of that
+    in the logarithm.  The mean of 2^16 roots, each a walk whose steps have a spread of at
+    most 2^-4 of the value: six standard deviations."""
+    n = 1 << 16
+    p, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    m, v = quantized(torch.zeros(n, device="cuda")), quantized(torch.full((n,), 1.0, device="cuda"))
+    g[::128] = 1.0                                          # keeps the blocks' scale
+    for step in range(1, 701):
+        optim.adamw([p], [g], [m], [v], step, lr=0.0)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[::128] = False
+    got = float(v.dequantize()[0][rest].double().mean())
+    want = 0.999 ** 350
+    assert abs(got / want - 1) <= 6 * 2.0 ** -4 * np.sqrt(700 * 0.01) / np.sqrt(n) + 0.01
+
+
+def test_many_tensors_and_types_in_one_call():
+    """More tensors than a launch's table has; mixed types; the result is that of one call each."""
+    n_of = lambda i: 1 + i * 37 % 999                       # noqa: E731
+    types = [torch.float32, torch.bfloat16, torch.float16]
+    make = lambda: ([random(n_of(i), types[i % 3], i) for i in range(1100)],            # noqa: E731
+                    [random(n_of(i), types[i % 3] if i % 2 else torch.float32, i + 5000) for i in range(1100)],
+                    [random(n_of(i), torch.float32, i + 9000) for i in range(1100)],
+                    [random(n_of(i), torch.float32, i + 7000).square() for i in range(1100)])
+    a, b = make(), make()
+    optim.adamw(*a, step=3)
+    for i in range(1100):
+        optim.adamw(*([x[i]] for x in b), step=3)
+    for x, y in zip(a, b):
+        assert all(torch.equal(s, t) for s, t in zip(x, y))
+
+
+def test_places():
+    """Pieces of one buffer that begin anywhere; nothing beside them is written."""
+    store = torch.zeros(4000, device="cuda")
+    p, g, m, v = (random(4000, torch.float32, s) for s in range(4))
+    v = v.square()
+    whole = [x.clone() for x in (p, m, v)]
+    optim.adamw([whole[0]], [g], [whole[1]], [whole[2]], 4)
+    cuts = [0, 1, 6, 131, 132, 517, 1544, 3999]
+    parts = [[x[i:j] for i, j in zip(cuts, cuts[1:])] for x in (p, g, m, v)]
+    last = [x[3999:].clone() for x in (p, m, v)]
+    optim.adamw(*parts, step=4)
+    for x, y, z in zip((p, m, v), whole, last):
+        assert torch.equal(x[:3999], y[:3999]) and torch.equal(x[3999:], z)
+    assert bool((store == 0).all())
+
+
+def test_step_on_the_gpu_and_captured():
+    p, g, m, v = (random(5000, torch.float32, s) for s in range(4))
+    v = v.square()
+    q = [x.clone() for x in (p, m, v)]
+    step = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for t in range(1, 4):
+        optim.adamw([p], [g], [m], [v], t)
+        step += 1
+        optim.adamw([q[0]], [g], [q[1]], [q[2]], step)
+        for a, b in zip((p, m, v), q):
+            assert bool(((a - b).abs() <= 2.0 ** -20 * a.abs() + 1e-9).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step += 1
+        optim.adamw([q[0]], [g], [q[1]], [q[2]], step)
+    for t in range(4, 7):
+        optim.adamw([p], [g], [m], [v], t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(step) == t
+        for a, b in zip((p, m, v), q):
+            assert bool(((a - b).abs() <= 2.0 ** -20 * a.abs() + 1e-9).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_gradient_that_is_no_number(bits, bad):
+    """It stays in its element (and with 8 bits, does not touch the block's scale)."""
+    def make():
+        p, g = random(300, torch.float32, 1), random(300, torch.float32, 2)
+        m, v = random(300, torch.float32, 3), random(300, torch.float32, 4).square()
+        return p, g, m if bits == 32 else quantized(m), v if bits == 32 else quantized(v.sqrt())
+    values = lambda s: (s if bits == 32 else s.dequantize()).view(-1)         # noqa: E731
+    p, g, m, v = make()
+    optim.adamw([p], [g], [m], [v], 3)
+    p2, g2, m2, v2 = make()
+    g2[130] = bad
+    optim.adamw([p2], [g2], [m2], [v2], 3)
+    rest = torch.arange(300, device="cuda") != 130
+    for a, b in ((p, p2), (values(m), values(m2)), (values(v), values(v2))):
+        assert torch.equal(a[rest], b[rest])
+    assert not bool(torch.isfinite(values(m2)[130])) and (bad == bad or bool(torch.isnan(p2[130])))
+
+
+def test_zeros_stay_zero():
+    for bits in (32, 8):
+        z = torch.zeros(200, device="cuda")
+        m, v = (z.clone(), z.clone()) if bits == 32 else (quantized(z), quantized(z))
+        p = random(200, torch.float32, 1)
+        old = p.clone()
+        optim.adamw([p], [z], [m], [v], 1, lr=0.1, weight_decay=0.0)
+        assert torch.equal(p, old)
+
+
+def layer(seed):
+    torch.manual_seed(seed)
+    return torch.nn.Sequential(torch.nn.Linear(40, 70), torch.nn.Linear(70, 9)).cuda()
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_optimizer_against_torch(capturable):
+    """torch.optim.AdamW in 64 bits; 20 steps of rounding 2^-20 of a step's size."""
+    a, b = layer(1), layer(1).double()
+    mine = optim.AdamW(a.parameters(), lr=0.01, weight_decay=0.2, capturable=capturable)
+    theirs = torch.optim.AdamW(b.parameters(), lr=0.01, weight_decay=0.2)
+    for i in range(20):
+        for x, y in zip(a.parameters(), b.parameters()):
+            x.grad = random(x.numel(), torch.float32, 100 * i + x.numel() % 97).view_as(x)
+            y.grad = x.grad.double()
+        mine.step()
+        theirs.step()
+    for x, y in zip(a.parameters(), b.parameters()):
+        assert bool(((x.double() - y).abs() <= 20 * (0.02 * 2.0 ** -18 + 2.0 ** -23 * y.abs())).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capturable", [False, True])
+def test_optimizer_resumes(bits, capturable):
+    """Ten steps are five, a saved state, and five more: bit for bit; also parameters that join later."""
+    def run(resume):
+        net = layer(2).bfloat16()
+        opt = optim.AdamW(net.parameters(), lr=0.01, state_bits=bits, capturable=capturable, seed=3)
+        for i in range(10):
+            for j, p in enumerate(net.parameters()):
+                p.grad = random(p.numel(), torch.bfloat16, 10 * i + j).view_as(p) if j < 2 or i > 2 else None
+            opt.step()
+            if resume and i == 4:
+                saved = opt.state_dict()
+                opt = optim.AdamW(net.parameters(), lr=0.5, state_bits=bits, capturable=capturable, seed=9)
+                opt.load_state_dict(saved)
+        return net, opt
+    (a, oa), (b, ob) = run(False), run(True)
+    assert all(torch.equal(x, y) for x, y in zip(a.parameters(), b.parameters()))
+    steps = [int(oa.state[p]["step"]) for p in a.parameters()]
+    assert steps == [10, 10, 7, 7] == [int(ob.state[p]["step"]) for p in b.parameters()]
+
+
+def test_optimizer_captured():
+    nets = [layer(3), layer(3)]
+    opts = [optim.AdamW(n.parameters(), lr=0.01, state_bits=8, capturable=True) for n in nets]
+    grads = [random(p.numel(), torch.float32, i).view_as(p) for i, p in enumerate(nets[0].parameters())]
+    for n, o in zip(nets, opts):
+        for p, g in zip(n.parameters(), grads):
+            p.grad = g.clone()
+        o.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opts[1].step()
+    for _ in range(3):
+        opts[0].step()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(nets[0].parameters(), nets[1].parameters()))
+    plain = optim.AdamW(nets[0].parameters())
+    plain.step()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="capturable"):
+        with torch.cuda.graph(graph):
+            plain.step()
+
+
+def test_autograd_is_told():
+    w = torch.randn(64, device="cuda", requires_grad=True)
+    y = torch.exp(w)
+    w.grad = torch.ones_like(w)
+    opt = optim.AdamW([w])
+    z = w * w
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.sum().backward()
+    del y

@@ -1,0 +1,347 @@
+"""Attention with a window and sinks (include/basp_attention.h) against its 64-bit
+form; tests/layer_reference.py derives the bounds."""
+import numpy as np
+import pytest
+import torch
+
+import sequence_re_layout_gb300 as basp
+from layer_reference import Attention
+from sequence_re_layout_gb300 import attention, autograd
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sequence_re_layout_gb300.build import build_library
+    build_library()
+
+
+def u(t):
+    return torch.finfo(t).eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def random(*shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def close(got, want, bound):
+    got = f64(got)
+    assert got.shape == want.shape and np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound).all(), np.abs((got - want) / bound).max()
+
+
+def check(q, k, v, do=None, window=None, sinks=0, scale=None):
+    """Forward, and with `do` backward, of every sequence against 64 bits."""
+    t, d = q.dtype, q.shape[3]
+    o, lse = attention.forward(q, k, v, window, sinks, scale)
+    grads = None if do is None else attention.backward(do, q, k, v, o, lse, window, sinks, scale)
+    assert o.shape == q.shape and o.dtype == t and lse.shape == (q.shape[0], q.shape[2], q.shape[1])
+    for b in range(q.shape[0]):
+        r = Attention(f64(q[b]), f64(k[b]), f64(v[b]), window, sinks, d ** -0.5 if scale is None else scale, u(t))
+        close(o[b], r.o, r.o_bound)
+        some = np.isfinite(r.lse)
+        got = f64(lse[b])
+        assert np.array_equal(np.isneginf(got), ~some)
+        assert (np.abs(got - r.lse)[some] <= r.lse_bound[some]).all()
+        if do is not None:
+            want, bound = r.backward(f64(do[b]), r.o_bound)
+            for name, g in zip(("dq", "dk", "dv"), grads):
+                close(g[b], want[name], bound[name])
+    return o, lse, grads
+
+
+def tensors(B, Sq, Sk, Hq, Hkv, d, t):
+    return (random(B, Sq, Hq, d, dtype=t, seed=1), random(B, Sk, Hkv, d, dtype=t, seed=2),
+            random(B, Sk, Hkv, d, dtype=t, seed=3), random(B, Sq, Hq, d, dtype=t, seed=4))
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("Sq,Sk", [(1, 1), (2, 2), (64, 64), (127, 127), (128, 128), (129, 129), (257, 257), (300, 300),
+                                   (1, 200), (77, 333), (130, 513), (5, 3), (200, 64), (3, 0)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1, 0), (64, 4), (130, 0), (200, 150), (1000, 3), (33, 1000)])
+def test_lengths_and_masks(Sq, Sk, window, sinks, dtype):
+    q, k, v, do = tensors(1, Sq, Sk, 2, 1, 64, DTYPES[dtype])
+    check(q, k, v, do, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("d", [8, 16, 24, 40, 56, 64, 72, 80, 96, 104, 120, 128])
+@pytest.mark.parametrize("S", [70, 200, 400])
+def test_head_sizes(S, d, dtype):
+    q, k, v, do = tensors(1, S, S, 2, 2, d, DTYPES[dtype])
+    check(q, k, v, do, 150, 4)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (3, 1), (4, 2), (6, 2), (8, 1), (5, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_heads(Hq, Hkv, d):
+    q, k, v, do = tensors(2, 261, 261, Hq, Hkv, d, torch.bfloat16)
+    check(q, k, v, do, 140, 5)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 4.0])
+def test_scales(scale):
+    q, k, v, do = tensors(1, 190, 190, 2, 2, 64, torch.float16)
+    check(q, k, v, do, 100, 2, scale)
+
+
+def test_growing_scores():
+    """A row's largest score grows from tile to tile by far more than 8 in the exponent of 2."""
+    t, S, d = torch.bfloat16, 640, 64
+    q, k, v, do = tensors(1, S, S, 1, 1, d, t)
+    k = (k.float() * torch.linspace(0, 12, S, device="cuda").view(1, S, 1, 1)).to(t)
+    check(q, k, v, do)
+    check(q, k.flip(1), v, do, 300, 7)
+
+
+def test_strides():
+    """Packed projections, sequence-first orders, spread-out gradients: read in place."""
+    t, B, S, Hq, Hkv, d = torch.bfloat16, 2, 150, 4, 2, 64
+    packed = random(B, S, (Hq + 2 * Hkv), d, dtype=t, seed=1)
+    q, k, v = packed[:, :, :Hq], packed[:, :, Hq:Hq + Hkv], packed[:, :, Hq + Hkv:]
+    first = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
+    heads = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in (q, k, v)]
+    do = random(B, S, Hq, d, dtype=t, seed=2)
+    want = check(q, k, v, do, 70, 4)
+    for x in (first, heads, [y.contiguous() for y in (q, k, v)]):
+        got = check(*x, do, 70, 4)
+        for a, b in zip((got[0], *got[2]), (want[0], *want[2])):
+            assert torch.equal(a, b)
+    spread = [x[:1].expand(B, S, -1, d) for x in (q, k, v)]
+    got = check(*spread, do, 70, 4)
+    assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1], want[0][0])
+    one = [x[:, :, :1].expand(B, S, 2, d) for x in (q, k, v)]
+    check(*one, do[:, :, :2], 70, 4)
+    out = torch.full((B, S, Hq + 1, d), 7.0, dtype=t, device="cuda")
+    o, _ = attention.forward(q, k, v, 70, 4, out=out[:, :, 1:])
+    assert torch.equal(o, want[0]) and bool((out[:, :, 0] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["k", "v", "q", "do"])
+@pytest.mark.parametrize("at", [0, 5, 60, 130, 299])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_is_not_seen_has_no_part(where, bad, at, d):
+    """One value of one token that is no number: rows that do not see it, or that it does not see, are as before."""
+    S, window, sinks = 300, 90, 3
+    x = dict(zip(("q", "k", "v", "do"), tensors(1, S, S, 2, 1, d, torch.bfloat16)))
+    r = Attention(*(f64(x[n])[0] for n in ("q", "k", "v")), window, sinks, d ** -0.5, u(torch.bfloat16))
+    want, bound = r.backward(f64(x["do"])[0], r.o_bound)
+    x[where][0, at, 0, 7] = bad
+    o, lse = attention.forward(x["q"], x["k"], x["v"], window, sinks)
+    dq, dk, dv = attention.backward(x["do"], x["q"], x["k"], x["v"], o, lse, window, sinks)
+    sees = r.sees
+    if where in ("k", "v"):
+        touched = sees[:, at]                                   # queries
+        keys = sees[touched].any(0)                             # keys that share a query with it
+    else:
+        touched, keys = np.arange(S) == at, sees[at]
+    every = np.ones(S, dtype=bool)
+    for got, w, e, rows in ((o, r.o, r.o_bound, every if where == "do" else ~touched),
+                            (dq, want["dq"], bound["dq"], ~touched), (dk, want["dk"], bound["dk"], ~keys),
+                            (dv, want["dv"], bound["dv"], ~keys)):
+        close(got[0][torch.from_numpy(rows).cuda()], w[rows], e[rows])
+    if bad != bad and where != "do":
+        heads = slice(None) if where in ("k", "v") else 0
+        assert bool(torch.isnan(o[0][torch.from_numpy(touched).cuda()][:, heads].float()).any(-1).all())
+
+
+def test_a_whole_tensor_of_nan():
+    q, k, v, do = tensors(1, 260, 260, 2, 1, 64, torch.bfloat16)
+    o, lse = attention.forward(torch.full_like(q, float("nan")), k, v, 100, 2)
+    assert bool(torch.isnan(o).all())
+    for g in attention.backward(do, torch.full_like(q, float("nan")), k, v, o, lse, 100, 2):
+        assert bool(torch.isnan(g).all())
+
+
+def test_results_repeat():
+    q, k, v, do = tensors(2, 700, 700, 4, 2, 128, torch.bfloat16)
+    o, lse = attention.forward(q, k, v, 300, 4)
+    g = attention.backward(do, q, k, v, o, lse, 300, 4)
+    for _ in range(3):
+        o2, lse2 = attention.forward(q, k, v, 300, 4)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert all(torch.equal(a, b) for a, b in zip(g, attention.backward(do, q, k, v, o, lse, 300, 4)))
+
+
+def test_nothing_is_written_outside():
+    t, S, H, d = torch.bfloat16, 133, 3, 40
+    q, k, v, do = tensors(2, S, S, H, H, d, t)
+    store = torch.full((2, S + 2, H + 1, d + 8), 7.0, dtype=t, device="cuda")
+    out = store[:, 1:S + 1, :H, :d]
+    o, _ = attention.forward(q, k, v, 50, 1, out=out)
+    assert o is out and torch.equal(out, attention.forward(q, k, v, 50, 1)[0])
+    store[:, 1:S + 1, :H, :d] = 7.0
+    assert bool((store == 7).all())
+
+
+def test_sizes_of_zero():
+    t = torch.bfloat16
+    for B, Sq, Sk, Hq, Hkv in [(0, 5, 5, 2, 1), (2, 0, 5, 2, 1), (2, 5, 0, 2, 1), (2, 0, 0, 2, 1), (2, 5, 5, 0, 1), (2, 5, 5, 0, 0)]:
+        q, k, v, do = tensors(B, Sq, Sk, Hq, Hkv, 64, t)
+        o, lse = attention.forward(q, k, v, 3, 1)
+        assert o.shape == q.shape and bool((o == 0).all() if Sk == 0 else True) and bool(torch.isneginf(lse).all() if Sk == 0 else True)
+        dq, dk, dv = attention.backward(do, q, k, v, o, lse, 3, 1)
+        assert dq.shape == q.shape and dk.shape == k.shape and dv.shape == v.shape
+        if Sk == 0:
+            assert bool((dq == 0).all())
+        if Sq == 0 or Hq == 0:
+            assert bool((dk == 0).all()) and bool((dv == 0).all())
+
+
+def test_autograd():
+    q, k, v, do = tensors(2, 200, 200, 4, 2, 64, torch.bfloat16)
+    o, lse = attention.forward(q, k, v, 64, 4)
+    want = attention.backward(do, q, k, v, o, lse, 64, 4)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    got = autograd.attention(*leaves, window=64, sinks=4)
+    got.backward(do)
+    assert torch.equal(got, o)
+    for a, b in zip(leaves, want):
+        assert torch.equal(a.grad, b)
+    for need in range(1, 8):
+        leaves = [x.clone().requires_grad_(bool(need >> i & 1)) for i, x in enumerate((q, k, v))]
+        autograd.attention(*leaves, window=64, sinks=4).backward(do)
+        for i, (a, b) in enumerate(zip(leaves, want)):
+            assert torch.equal(a.grad, b) if need >> i & 1 else a.grad is None
+    one = [x.clone().requires_grad_() for x in (q, k, v)]
+    autograd.attention(*one, window=64, sinks=4).sum().backward()            # a gradient spread from one value
+    ones = attention.backward(torch.ones_like(do), q, k, v, o, lse, 64, 4)
+    assert all(torch.equal(a.grad, b) for a, b in zip(one, ones))
+
+
+def test_gradient_against_differences():
+    """Of the 64-bit form (step 2^-12: off by its square times a third derivative of order one)."""
+    S, d, step, window, sinks = 40, 16, 2.0 ** -12, 11, 2
+    q, k, v, do = tensors(1, S, S, 2, 1, d, torch.float16)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    autograd.attention(*leaves, window=window, sinks=sinks).backward(do)
+    ways = [np.random.default_rng(s).standard_normal(x.shape[1:]) for s, x in enumerate((q, k, v))]
+
+    def value(s):
+        a = Attention(*(f64(x)[0] + s * w for x, w in zip((q, k, v), ways)), window, sinks, d ** -0.5, 0)
+        return (a.o * f64(do)[0]).sum()
+
+    want = (value(step) - value(-step)) / (2 * step)
+    a = Attention(*(f64(x)[0] for x in (q, k, v)), window, sinks, d ** -0.5, u(torch.float16))
+    bounds = a.backward(f64(do)[0], a.o_bound)[1]
+    got = sum((f64(x.grad)[0] * w).sum() for x, w in zip(leaves, ways))
+    room = sum((bounds[n] * np.abs(w)).sum() for n, w in zip(("dq", "dk", "dv"), ways))
+    size = sum((np.abs(f64(x.grad)[0]) * np.abs(w)).sum() for x, w in zip(leaves, ways))
+    assert abs(got - want) <= room + 2.0 ** -18 * size
+
+
+# ---- one token over a cache ----------------------------------------------------------
+
+def check_decode(q, k, v, lengths, window=None, sinks=0, scale=None):
+    t, d = q.dtype, q.shape[2]
+    o = attention.decode(q, k, v, torch.tensor(lengths, dtype=torch.int32, device="cuda"), window, sinks, scale)
+    assert o.shape == q.shape and o.dtype == t
+    for b, n in enumerate(lengths):
+        n = max(0, min(n, k.shape[1]))
+        if n == 0:
+            assert bool((o[b] == 0).all())
+            continue
+        r = Attention(f64(q[b])[None], f64(k[b, :n]), f64(v[b, :n]), window, sinks, d ** -0.5 if scale is None else scale, u(t))
+        close(o[b], r.o[0], r.o_bound[0])
+    return o
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (4, 2), (8, 2), (3, 1), (16, 1), (17, 1), (40, 2)])
+@pytest.mark.parametrize("d", [64, 128, 8, 40, 80, 120])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (100, 4)])
+def test_decode(Hq, Hkv, d, window, sinks, dtype):
+    t = DTYPES[dtype]
+    lengths = [0, 1, 2, 31, 64, 65, 300, 513, 700, -3, 900]
+    B, cap = len(lengths), 700
+    q, k, v = (random(B, *s, dtype=t, seed=i) for i, s in enumerate(((Hq, d), (cap, Hkv, d), (cap, Hkv, d))))
+    check_decode(q, k, v, lengths, window, sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1, 0), (1, 1), (64, 64), (5000, 3), (700, 150), (1, 5000), (4096, 4)])
+@pytest.mark.parametrize("length", [1, 4097, 9000])
+def test_decode_long(window, sinks, length):
+    cap = 9001
+    q, k, v = (random(1, *s, dtype=torch.bfloat16, seed=i) for i, s in enumerate(((8, 64), (cap, 2, 64), (cap, 2, 64))))
+    check_decode(q, k, v, [length], window, sinks)
+
+
+def test_decode_reads_nothing_else():
+    """NaN in every place that the token does not see."""
+    lengths, window, sinks, cap = [1, 50, 400, 777, 1000], 130, 5, 1000
+    q, k, v = (random(5, *s, dtype=torch.bfloat16, seed=i) for i, s in enumerate(((4, 128), (cap, 2, 128), (cap, 2, 128))))
+    want = check_decode(q, k, v, lengths, window, sinks)
+    for b, n in enumerate(lengths):
+        for t in (k, v):
+            t[b, n:] = float("nan")
+            t[b, min(sinks, max(0, n - window)):max(0, n - window)] = float("inf")
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    assert torch.equal(attention.decode(q, k, v, n, window, sinks), want)
+
+
+def test_decode_strides_and_forward():
+    """A cache in any order; and a piece of one query is the same function."""
+    cap, Hq, Hkv, d = 333, 4, 2, 64
+    q, k, v = (random(3, *s, dtype=torch.float16, seed=i) for i, s in enumerate(((Hq, d), (cap, Hkv, d), (cap, Hkv, d))))
+    lengths = [333, 100, 7]
+    want = check_decode(q, k, v, lengths, 90, 2)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    k2, v2 = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (k, v))
+    assert torch.equal(attention.decode(q, k2, v2, n, 90, 2), want)
+    out = torch.full((3, Hq + 1, d), 7.0, dtype=torch.float16, device="cuda")
+    assert torch.equal(attention.decode(q, k, v, n, 90, 2, out=out[:, 1:]), want) and bool((out[:, 0] == 7).all())
+    whole = attention.forward(q[:1, None], k[:1], v[:1], 90, 2)[0]
+    r = Attention(f64(q[:1]), f64(k[0]), f64(v[0]), 90, 2, d ** -0.5, u(torch.float16))
+    close(whole[0], r.o, r.o_bound)
+
+
+def test_decode_captured():
+    """Lengths are read when the kernel runs: a replay follows them."""
+    cap = 600
+    q, k, v = (random(2, *s, dtype=torch.bfloat16, seed=i) for i, s in enumerate(((4, 64), (cap, 2, 64), (cap, 2, 64))))
+    n = torch.tensor([5, 600], dtype=torch.int32, device="cuda")
+    attention.decode(q, k, v, n, 100, 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = attention.decode(q, k, v, n, 100, 4)
+    for lengths in ([5, 600], [0, 1], [600, 37]):
+        n.copy_(torch.tensor(lengths, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, attention.decode(q, k, v, n, 100, 4))
+
+
+def test_step_captured_and_on_another_stream():
+    q, k, v, do = tensors(1, 300, 300, 2, 1, 64, torch.bfloat16)
+    o, lse = attention.forward(q, k, v, 100, 4)
+    want = (o, *attention.backward(do, q, k, v, o, lse, 100, 4))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, lse2 = attention.forward(q, k, v, 100, 4)
+        got = (o2, *attention.backward(do, q, k, v, o2, lse2, 100, 4))
+    for _ in range(2):
+        for g in got:
+            g.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o3, lse3 = attention.forward(q, k, v, 100, 4)
+        got = (o3, *attention.backward(do, q, k, v, o3, lse3, 100, 4))
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_zz_no_wait_ran_out():
+    assert basp.basp_attention_timeouts() == 0
