@@ -18,13 +18,13 @@ TORCH_OPS_PATH = os.path.join(PKG, "_torch_ops.so")
 TORCH_VERSION_PATH = os.path.join(PKG, "_torch_ops.built_with")
 TORCH_OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "layernorm.cu", "quantize.cu", "matmul.cu", "attention.cu",
-           "adamw.cu"]
+           "attention_forward.cu", "adamw.cu"]
 INCLUDES = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h", "basp_attention.h",
                                                "basp_optim.h")]
 HEADERS = INCLUDES + \
     [os.path.join(CSRC, h) for h in ("layout_internal.h", "relayout_kernel.cuh", "scratch_cache.h",
                                      "fp8_common.cuh", "norm_common.cuh", "matmul_plan.h", "matvec.cuh",
-                                     "tcgen05.cuh", "attention_common.cuh")]
+                                     "tcgen05.cuh", "attention_common.cuh", "attention.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

@@ -1,8 +1,12 @@
 // attention.cu -- causal attention with a sliding window and sinks: forward,
 // backward and one token over a cache (include/basp_attention.h).
+//
+// The calls' checks, what TMA needs to know of the tensors, and the plain form of a
+// warp a row, for tensors that TMA cannot address (a sequence stride of 0 or below a
+// head's length, strides of 2^40 bytes).
 #include <algorithm>
 
-#include "attention_common.cuh"
+#include "attention.cuh"
 
 namespace basp_fp8 {
 namespace {
@@ -75,10 +79,11 @@ bool sizes_ok(const basp_attention_desc *d, basp_status *st) {
     return true;
 }
 
-// Rows of all heads and sequences: a counter of 64 bits holds their elements.
+// Heads of all sequences fit a grid, and their rows the GPU's memory.
 bool rows_ok(const basp_attention_desc *d) {
     const __int128 q = __int128(d->batch) * d->q_heads * d->q_len, k = __int128(d->batch) * d->k_heads * d->k_len;
-    return q <= (int64_t(1) << 48) && k <= (int64_t(1) << 48);
+    return q <= (int64_t(1) << 38) && k <= (int64_t(1) << 38) &&          // 2^38 rows are 4 TB
+           d->batch * d->q_heads <= kMaxSide / 2 && d->batch * d->k_heads <= kMaxSide / 2;
 }
 
 // Checks of a call's tensors: each has len x heads rows of head_dim in each sequence.
@@ -142,6 +147,68 @@ AttentionArgs args_of(const basp_attention_desc *d) {
     return a;
 }
 
+// ---- TMA ------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) !=
+                cudaSuccess || qr != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return EncodeFn(nullptr);
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Whether TMA can address the rows of a tensor of `len` x `heads` a sequence.
+bool tma_ok(const AttentionArgs &a, const Heads &t, int len, int heads) {
+    const int64_t most = (int64_t(1) << 39) - 1;          // 2^40 bytes
+    return (len == 1 || (t.ss >= a.d && t.ss <= most)) && (heads == 1 || t.sh <= most) && (a.batch == 1 || t.sb <= most);
+}
+
+// Boxes of 64 values x `rows` rows; what is past a tensor's end reads zero.
+bool encode(const AttentionArgs &a, const Heads &t, int len, int heads, int rows, CUtensorMap *out, int *head, int *batch) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    *head = heads > 1 && t.sh > 0;
+    *batch = a.batch > 1 && t.sb > 0;
+    const cuuint64_t dims[4] = {cuuint64_t(a.d), cuuint64_t(len), cuuint64_t(*head ? heads : 1), cuuint64_t(*batch ? a.batch : 1)};
+    const cuuint64_t strides[3] = {cuuint64_t(len > 1 ? t.ss * 2 : kMaxHeadDim * 2), cuuint64_t(*head ? t.sh * 2 : kMaxHeadDim * 2),
+                                   cuuint64_t(*batch ? t.sb * 2 : kMaxHeadDim * 2)};
+    const cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, t.p, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The count of waits that ran out, on the current device.
+unsigned long long *timeouts_at() {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_timeouts) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return static_cast<unsigned long long *>(p);
+}
+
+bool encode_qkv(const AttentionArgs &a, HeadMaps *m) {
+    m->timeouts = timeouts_at();
+    return m->timeouts != nullptr && encode(a, a.q, a.sq, a.hq, kTile, &m->q, &m->q_head, &m->q_batch) &&
+           encode(a, a.k, a.sk, a.hkv, kTile, &m->k, &m->k_head, &m->k_batch) &&
+           encode(a, a.v, a.sk, a.hkv, kTile, &m->v, &m->v_head, &m->v_batch);
+}
+
+bool tiled(const AttentionArgs &a) {
+    return a.sk > 0 && tma_ok(a, a.q, a.sq, a.hq) && tma_ok(a, a.k, a.sk, a.hkv) && tma_ok(a, a.v, a.sk, a.hkv);
+}
+
 template <class F> basp_status with_type(basp_dtype t, F &&f) {
     return t == BASP_DTYPE_BF16 ? f(__nv_bfloat16()) : f(__half());
 }
@@ -168,6 +235,12 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
     AttentionArgs a = args_of(desc);
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o);
     a.lse = lse;
+    if (a.batch == 0 || a.hq == 0 || a.sq == 0) return BASP_OK;
+    if (tiled(a)) {
+        HeadMaps m = {};
+        if (!encode_qkv(a, &m)) return BASP_ERR_CUDA;
+        return launch_attention_forward(a, m, desc->dtype == BASP_DTYPE_BF16, stream);
+    }
     return with_type(desc->dtype, [&](auto t) { return launch_rows<decltype(t), kForward>(a, stream); });
 }
 

@@ -1,0 +1,20 @@
+// attention.cuh -- the attention's kernels as attention.cu calls them.
+#pragma once
+
+#include <cuda.h>
+
+#include "attention_common.cuh"
+
+namespace basp_fp8 {
+
+// Tensors as TMA sees them: boxes of 64 values x 128 rows of one head of one sequence.
+// A head's or a sequence's number counts as it is (1) or not at all (0, a stride of 0).
+struct HeadMaps {
+    CUtensorMap q, k, v, d_o;
+    int q_head, q_batch, k_head, k_batch, v_head, v_batch, do_head, do_batch;
+    unsigned long long *timeouts;
+};
+
+basp_status launch_attention_forward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream);
+
+}  // namespace basp_fp8

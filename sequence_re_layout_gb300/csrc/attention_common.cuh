@@ -4,6 +4,7 @@
 
 #include "basp_attention.h"
 #include "fp8_common.cuh"
+#include "tcgen05.cuh"
 
 namespace basp_fp8 {
 
@@ -27,12 +28,101 @@ struct AttentionArgs {
     float scale;
 };
 
+// ---- tiles of 128 queries and keys ---------------------------------------------------
+
+constexpr int kTile = 128;
+constexpr int kBox = kTile * 128;        // bytes of a box of 128 rows x 64 values
+
+// Key tiles that any of the queries [r0, r0 + 128) sees: [0, first) and [low, high).
+struct KeyTiles {
+    int first, low, high;
+    __device__ __forceinline__ bool has(int j) const { return j < first || (j >= low && j < high); }
+    __device__ __forceinline__ int count() const { return first + high - low; }
+    __device__ __forceinline__ int begin() const { return first > 0 ? 0 : low; }
+    // the one after j; `high` where there is none
+    __device__ __forceinline__ int next(int j) const { return j + 1 == first ? low : j + 1; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const AttentionArgs &a, int r0) {
+    const int p1 = min(r0 + kTile, a.sq) - 1 + a.sk - a.sq;
+    if (r0 >= a.sq || p1 < 0) return {0, 0, 0};
+    const int low = max(0, max(0, r0 + a.sk - a.sq) - a.window + 1) / kTile;
+    const int first_end = min(a.sinks, max(0, p1 - a.window + 1));
+    return {min((first_end + kTile - 1) / kTile, low), low, p1 / kTile + 1};
+}
+
+// A wait on one of the CTA's barriers, with a limit.
+constexpr uint64_t kAttentionWaitNs = 2000000000ull;
+struct AttentionWaiter {
+    volatile int *abort;                 // shared by the CTA
+    unsigned long long *timeouts;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, bool give_up_early = true) const {
+        if (mbar_try_wait<false>(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait<false>(bar, parity)) {
+            if (give_up_early && *abort) return false;
+            if (global_ns() - t0 > kAttentionWaitNs) {
+                if (!*abort) atomicAdd(timeouts, 1ull);
+                *abort = 1;
+                return false;
+            }
+        }
+        return true;
+    }
+};
+
+// A ring's place and the parity of its turn.
+template <int N> struct Turn {
+    uint32_t at = 0, turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            turn ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <class T> __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    } else {
+        const __half2 p = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
+}
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
 // The query at position p sees keys [0, first_end) and [last, p].
 struct Sees {
     int first_end, last;
 };
 __device__ __forceinline__ Sees keys_of(const AttentionArgs &a, int p) {
-    const int low = max(0, p - a.window + 1);
+    const int low = p < 0 ? 0 : max(0, p - a.window + 1);
     return {min(a.sinks, low), low};
 }
 // Key j is seen by the positions [j, last position].

@@ -1,5 +1,6 @@
-// tcgen05.cuh -- thin wrappers over the PTX instructions of the matrix
-// product: mbarriers, TMA loads, tensor memory, and block-scaled tcgen05.mma.
+// tcgen05.cuh -- thin wrappers over the PTX instructions of the matrix product
+// and the attention: mbarriers, TMA loads, tensor memory, and tcgen05.mma of
+// block-scaled 8-bit and of 16-bit operands.
 #pragma once
 
 #include <cuda.h>
@@ -98,6 +99,13 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         " [%0], [%1, {%2, %3}], [%4];"
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
 // Shared memory -> global, the box clipped to the matrix.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
@@ -173,6 +181,28 @@ __device__ __forceinline__ void tmem_load_fragments(uint32_t addr, uint32_t (&v)
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr) : "memory");
 }
+// 32 lanes x 32 columns of 32 bits, and back.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13,"
+        " %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13,"
+        " %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+          "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+          "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // All loads before this have arrived.  What reads a load's registers must come
 // after `tmem_loaded` of them, which says so to the compiler: to it they are
 // written when the load is issued.
@@ -182,6 +212,18 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&v)[16]) {
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
                    "+r"(v[15])::"memory");
+}
+
+// As tmem_loaded, of 32 registers.
+__device__ __forceinline__ void tmem_loaded32(uint32_t *v) {
+    asm volatile(""
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15])::"memory");
+    asm volatile(""
+                 : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
 // ---- the product ----------------------------------------------------------------
@@ -239,6 +281,42 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint32_t a, uint32_t b, uin
             ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(accumulate)),
               "n"(kOperandDescHigh) : "memory");
 }
+// ---- products of 16-bit operands ----------------------------------------------------
+
+// Operands lie in shared memory as boxes of 128-byte rows (64 values) in the 128-byte
+// swizzle that TMA writes, 8 rows every 1024 bytes.  K along the rows ("K-major"): 16
+// values of K are 32 bytes further on.  K across the rows: the other side is 64 wide
+// a box, boxes are `box_bytes` apart, and 16 values of K are 16 rows.
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+    return (uint64_t(kOperandDescHigh) << 32) | operand_desc_low(addr);
+}
+__device__ __forceinline__ uint64_t desc_k_across(uint32_t addr, uint32_t box_bytes) {
+    return (uint64_t(kOperandDescHigh) << 32) | ((addr & 0x3ffff) >> 4) | ((box_bytes >> 4) << 16);
+}
+
+// Instruction descriptor of kind::f16: M x N, both operands bf16 or both fp16, a
+// 32-bit result; A negated; B's K across its rows.
+__host__ __device__ constexpr uint32_t mma_f16_desc(int M, int N, bool bf16, bool negate_a, bool b_across) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (negate_a ? 1u << 13 : 0u) |
+           (b_across ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+// D (tensor memory) = A B (+ D): A from shared memory, or from tensor memory (two
+// values of K a column).
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
+}
+__device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
+}
+
 // The barrier (in a pair: of both CTAs, at the same place) gets one arrival
 // when everything this thread issued so far is done.
 template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -249,6 +327,17 @@ template <int CG> __device__ __forceinline__ void mma_commit(uint32_t bar) {
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
             ::"r"(bar), "h"(uint16_t(3)) : "memory");
+}
+
+// ---- registers ------------------------------------------------------------------
+
+// By all warps of a warpgroup; what the groups have together may not exceed what the
+// block was launched with.
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---- clusters -------------------------------------------------------------------
