@@ -15,14 +15,14 @@ __device__ unsigned long long g_timeouts;
 
 constexpr int kRowWarps = 4;
 
-enum { kForward, kDelta, kDq, kDkv };
+enum { kForward, kStats, kDq, kDkv };
 
 // A warp a row.
 template <class T, int WHAT>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ AttentionArgs a) {
     __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
     grid_dependency();
-    const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : a.sq;
+    const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : WHAT == kStats ? a.sq_pad : a.sq;
     const int64_t rows = int64_t(a.batch) * heads * len;
     for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
         const int i = int(r % len), h = int(r / len % heads), b = int(r / len / heads);
@@ -30,15 +30,16 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i, m);
         if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i, m);
         if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i, m);
-        if constexpr (WHAT == kDelta) {
-            const float s = delta_row<T>(a, b, h, i);
-            if (threadIdx.x % 32 == 0) a.delta[r] = s;
+        if constexpr (WHAT == kStats) {
+            const float2 s = stats_row<T>(a, b, h, i);
+            if (threadIdx.x % 32 == 0) a.stats[r] = s;
         }
     }
 }
 
 template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cudaStream_t stream) {
-    const int64_t rows = int64_t(a.batch) * (WHAT == kDkv ? int64_t(a.hkv) * a.sk : int64_t(a.hq) * a.sq);
+    const int64_t rows = int64_t(a.batch) * (WHAT == kDkv   ? int64_t(a.hkv) * a.sk
+                                             : int64_t(a.hq) * (WHAT == kStats ? a.sq_pad : a.sq));
     if (rows == 0) return BASP_OK;
     const int64_t ctas = std::min<int64_t>(ceil_div(rows, kRowWarps), 1 << 20);
     return launch(rows_kernel<T, WHAT>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a);
@@ -247,7 +248,7 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
 extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
     basp_status st;
     if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
-    return desc->batch * desc->q_heads * desc->q_len * int64_t(sizeof(float));
+    return desc->batch * desc->q_heads * ceil_div(desc->q_len, kTile) * kTile * int64_t(sizeof(float2));
 }
 
 extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
@@ -281,10 +282,16 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o); a.d_o = heads_of(d_o);
     a.dq = heads_of(dq); a.dk = heads_of(dk); a.dv = heads_of(dv);
     a.lse = const_cast<float *>(lse);
-    a.delta = static_cast<float *>(workspace);
+    a.stats = static_cast<float2 *>(workspace);
+    a.sq_pad = int(ceil_div(a.sq, kTile) * kTile);
+    const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq);
+    HeadMaps m = {};
+    if (tiles && (!encode_qkv(a, &m) || !encode(a, a.d_o, a.sq, a.hq, kTile, &m.d_o, &m.do_head, &m.do_batch)))
+        return BASP_ERR_CUDA;
     return with_type(desc->dtype, [&](auto t) {
         using T = decltype(t);
-        basp_status s = launch_rows<T, kDelta>(a, stream);
+        basp_status s = launch_rows<T, kStats>(a, stream);
+        if (s == BASP_OK && tiles) return launch_attention_backward(a, m, desc->dtype == BASP_DTYPE_BF16, stream);
         if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);
         if (s == BASP_OK) s = launch_rows<T, kDkv>(a, stream);
         return s;

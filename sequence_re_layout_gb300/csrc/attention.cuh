@@ -15,6 +15,7 @@ struct HeadMaps {
     unsigned long long *timeouts;
 };
 
+basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream);
 basp_status launch_attention_forward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream);
 
 }  // namespace basp_fp8

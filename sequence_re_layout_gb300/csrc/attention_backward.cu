@@ -1,0 +1,582 @@
+// attention_backward.cu -- the gradients of attention with a window and sinks, on the
+// tensor cores.
+//
+// Two kernels, each with its sum in tensor memory from the first tile to the last, so
+// that nothing is added by atomics and results repeat:
+//   dk, dv   128 keys a CTA, over the tiles of queries that see them, of every query
+//            head that shares the key head.  Scores are taken transposed, keys along
+//            tensor memory's lanes, so that P^T and dS^T lie there as the products dv +=
+//            P^T dO and dk += dS^T Q want them:
+//                S^T = K Q^T,   P^T = 2^(c S^T - lse),   dP^T = V dO^T,
+//                dS^T = P^T (dP^T - D)
+//   dq       128 queries a CTA, over the tiles of keys that they see:
+//                S = Q K^T,   dP = dO V^T,   dq += dS K
+// That is seven products of a pair of tiles where one kernel with atomics needs five.
+//
+// In both, two warpgroups share a tile's columns, 64 each, a row a thread.  S^T and P^T
+// take turns in one place of tensor memory, dP^T and dS^T in another; the products are
+// issued so that one pair's run while the other's values are made:
+//     dv P^T(i), S^T(i + 1) under dS^T(i),   dk dS^T(i), dP^T(i + 1) under P^T(i + 1).
+// The dq kernel's S and dP are free as soon as they have been read (dS has two places of
+// its own), so S(j + 1) and dP(j + 1) run under dS(j).
+//
+// As in the forward, a row that comes out infinite or NaN is computed again from the
+// definition.
+#include <cuda.h>
+
+#include "attention.cuh"
+#include "attention_common.cuh"
+
+namespace basp_fp8 {
+namespace {
+
+constexpr int kBackThreads = 384;                             // 8 warps of values, one that loads, one that issues
+
+// DKV: of the kernel of dk and dv, which keeps queries' statistics too.
+template <int HD, bool DKV> struct BackSizes {
+    static constexpr int kBoxes = HD / 64;
+    static constexpr int kOperand = kBoxes * kBox;            // bytes of a tile of Q, K, V or dO
+    static constexpr int kStages = HD == 128 ? (DKV ? 4 : 5) : 8;
+    static constexpr int kPlaces = DKV ? kStages / 2 + 1 : 0; // of statistics
+    static constexpr int kStats = kTile * 8;                  // bytes of a tile of queries' statistics
+    static constexpr int kBarriers = 1 + 2 * kStages + 7;
+    static constexpr int kSmem =
+        1024 + (2 + kStages) * kOperand + kPlaces * kStats + 8 * kBarriers + 16 + 32;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// A warp's 16-bit P or dS of 64 columns to tensor memory, and 64 columns from it.
+__device__ __forceinline__ void load64(uint32_t addr, uint32_t (&v)[64]) {
+    tmem_load32(addr, v);
+    tmem_load32(addr + 32, v + 32);
+    tmem_load_wait();
+    tmem_loaded32(v);
+    tmem_loaded32(v + 32);
+}
+template <class T> __device__ __forceinline__ void store64(uint32_t addr, const float (&v)[64]) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
+    tmem_store32(addr, w);
+    tmem_store_wait();
+}
+
+template <class T, int HD>
+__global__ void __launch_bounds__(kBackThreads, 1)
+attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m) {
+    using Z = BackSizes<HD, true>;
+    constexpr int ST = Z::kStages, SS = Z::kPlaces;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    const uint32_t k_at = smem_addr(smem), v_at = k_at + Z::kOperand, ring0 = k_at + 2 * Z::kOperand;
+    uint8_t *stats = smem + (2 + ST) * Z::kOperand;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(stats + SS * Z::kStats);
+    const uint32_t kv_full = smem_addr(bars), full = kv_full + 8, empty = full + 8 * ST;
+    const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8;
+    const uint32_t done = ds_ready + 8, drained = done + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint32_t *bad_rows = tmem_slot + 4;                       // [8 warps]
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (warp == 8 && lane == 0) {
+        mbar_init(kv_full, 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_ready, 8);
+        mbar_init(ds_ready, 8);
+        mbar_init(done, 1);
+        mbar_init(drained, 1);
+        *abort = 0;
+        fence_mbar_init();
+        fence_async_shared();
+    }
+    if (warp == 10) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+    const AttentionWaiter wait{abort, m.timeouts};
+
+    const int heads = a.batch * a.hkv;
+    const int kh = int(blockIdx.x) % heads % a.hkv, b = int(blockIdx.x) % heads / a.hkv;
+    const int k0 = int(blockIdx.x) / heads * kTile, shift = a.sk - a.sq;
+    const QueryTiles tiles = query_tiles(a, k0);
+    const int count = tiles.high - tiles.low, total = count * a.group;
+    const uint32_t dv_acc = tmem + 256, dk_acc = tmem + 256 + HD;
+
+    if (warp == 8) {                                          // loads
+        if (total > 0) {
+            if (elect_one()) {
+                mbar_expect_tx(kv_full, 2 * Z::kOperand);
+                for (int x = 0; x < Z::kBoxes; ++x) {
+                    tma_load_4d(k_at + x * kBox, &m.k, 64 * x, k0, kh * m.k_head, b * m.k_batch, kv_full);
+                    tma_load_4d(v_at + x * kBox, &m.v, 64 * x, k0, kh * m.v_head, b * m.v_batch, kv_full);
+                }
+            }
+            __syncwarp();
+            bool ok = true;
+            uint32_t issued = 0;
+            Turn<ST> ring;
+            Turn<SS> place;
+            for (int i = 0; i < total && ok; ++i) {
+                const int h = kh * a.group + i / count, q = (tiles.low + i % count) * kTile;
+                for (int x = 0; x < 2 && ok; ++x) {           // Q and its statistics, dO
+                    ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t to = ring0 + ring.at * Z::kOperand, bar = full + 8 * ring.at;
+                        mbar_expect_tx(bar, Z::kOperand + (x == 0 ? Z::kStats : 0));
+                        for (int y = 0; y < Z::kBoxes; ++y)
+                            tma_load_4d(to + y * kBox, x == 0 ? &m.q : &m.d_o, 64 * y, q, h * (x == 0 ? m.q_head : m.do_head),
+                                        b * (x == 0 ? m.q_batch : m.do_batch), bar);
+                        if (x == 0)
+                            bulk_load(smem_addr(stats) + place.at * Z::kStats,
+                                      a.stats + (int64_t(b) * a.hq + h) * a.sq_pad + q, Z::kStats, bar);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    ++issued;
+                }
+                place.next();
+            }
+            // a CTA ends after its copies in flight, also where another warp gave up on them
+            const uint32_t open = issued < uint32_t(ST) ? issued : ST;
+            for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
+            wait(kv_full, 0, false);
+        }
+    } else if (warp == 9) {                                   // products
+        if (total > 0 && elect_one()) {
+            const bool bf16 = std::is_same_v<T, __nv_bfloat16>;
+            const int ksteps = (a.d + 15) / 16;
+            const uint32_t is = mma_f16_desc(kTile, kTile, bf16, a.scale < 0.f, false);
+            const uint32_t idp = mma_f16_desc(kTile, kTile, bf16, false, false);
+            const uint32_t io = mma_f16_desc(kTile, ksteps * 16, bf16, false, true);
+            Turn<ST> ring;
+            bool ok = wait(kv_full, 0);
+            // a 128 x 128 product over the head: S^T or dP^T
+            auto across_head = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t desc, uint32_t bar) {
+                const uint64_t dx = desc_k_major(x), dy = desc_k_major(y);
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t at = (k / 4) * (kBox / 16) + (k % 4) * 2;
+                    mma_f16(d, dx + at, dy + at, desc, k > 0);
+                }
+                mma_commit<1>(bar);
+            };
+            // a product over the queries: P^T dO or dS^T Q, each warpgroup's 64 in its own place
+            auto across_queries = [&](uint32_t d, uint32_t x, uint32_t y, bool add) {
+                const uint64_t dy = desc_k_across(y, kBox);
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_f16_tmem(d, x + (k / 4) * 64 + (k % 4) * 8, dy + k * (16 * 128 / 16), io, add || k > 0);
+            };
+            auto take = [&]() {
+                ok = ok && wait(full + 8 * ring.at, ring.turn);
+                const uint32_t at = ring.at;
+                ring.next();
+                return at;
+            };
+            uint32_t q = take(), o = take();
+            if (ok) {
+                tcgen05_after_sync();
+                across_head(tmem, k_at, ring0 + q * Z::kOperand, is, s_full);
+                across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, idp, dp_full);
+            }
+            for (int i = 0; i < total && ok; ++i) {
+                const bool more = i + 1 < total;
+                ok = wait(p_ready, i & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                across_queries(dv_acc, tmem, ring0 + o * Z::kOperand, i > 0);
+                mma_commit<1>(empty + 8 * o);
+                const uint32_t q_now = q;
+                if (more) {
+                    q = take();
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    across_head(tmem, k_at, ring0 + q * Z::kOperand, is, s_full);
+                }
+                ok = wait(ds_ready, i & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                across_queries(dk_acc, tmem + kTile, ring0 + q_now * Z::kOperand, i > 0);
+                mma_commit<1>(empty + 8 * q_now);
+                if (more) {
+                    o = take();
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, idp, dp_full);
+                }
+            }
+            if (ok) mma_commit<1>(done);
+            // nothing is in flight at the end
+            mma_commit<1>(drained);
+            wait(drained, 0, false);
+        }
+    } else if (warp < 8) {                                    // values
+        const int half = warp / 4, quarter = warp % 4, key = k0 + quarter * 32 + lane;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kTile;
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
+        const int k1 = k0 + kTile - 1;
+        bool ok = true;
+        Turn<SS> place;
+        Turn<ST> ring;
+        for (int i = 0; i < total; ++i, place.next(), ring.next(), ring.next()) {
+            // the statistics came with Q
+            ok = __all_sync(0xffffffffu, wait(full + 8 * ring.at, ring.turn) && wait(s_full, i & 1));
+            if (!ok) break;
+            tcgen05_after_sync();
+            const int q0 = (tiles.low + i % count) * kTile, p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
+            const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
+            // columns of this warpgroup that see the key: [first, last]
+            const int at0 = q0 + 64 * half;
+            const int first = key - shift - at0, last = last_position(a, key) - shift - at0;
+            const float4 *st = reinterpret_cast<const float4 *>(stats + place.at * Z::kStats) + 32 * half;
+            uint32_t x[64];
+            float p[64];
+            load64(ts, x);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                const float4 f = st[e / 2];                   // (lse, D) of two queries
+                p[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -f.x));
+                p[e + 1] = exp2_fast(fmaf(__uint_as_float(x[e + 1]), c, -f.z));
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e < first || e > last) p[e] = 0.f;
+            }
+            store64<T>(ts, p);
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready);
+            ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
+            if (!ok) break;
+            tcgen05_after_sync();
+            load64(tp, x);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                const float4 f = st[e / 2];
+                p[e] *= __uint_as_float(x[e]) - f.y;
+                p[e + 1] *= __uint_as_float(x[e + 1]) - f.w;
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e < first || e > last) p[e] = 0.f;    // 0 times an infinity
+            }
+            store64<T>(tp, p);
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ds_ready);
+        }
+        if (total > 0) {
+            ok = __all_sync(0xffffffffu, ok && wait(done, 0));
+            tcgen05_after_sync();
+        }
+        // one warpgroup stores dv, the other dk
+        const bool exists = key < a.sk;
+        const float f = half == 0 ? 1.f : a.scale;
+        const uint32_t acc = (half == 0 ? dv_acc : dk_acc) + lanes;
+        T *row = row_of<T>(half == 0 ? a.dv : a.dk, b, exists ? key : 0, kh);
+        bool finite = true;
+        for (int i = 0; i < (a.d + 31) / 32; ++i) {
+            uint32_t v[32];
+            if (total == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0u;
+            } else if (ok) {
+                tmem_load32(acc + 32 * i, v);
+                tmem_load_wait();
+                tmem_loaded32(v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float u = __uint_as_float(v[e + 2 * y]) * f, z = __uint_as_float(v[e + 2 * y + 1]) * f;
+                    if (32 * i + e < a.d) finite = finite && fabsf(u) < INFINITY && fabsf(z) < INFINITY;
+                    w[y] = pack_pair<T>(u, z);
+                }
+                if (exists && 32 * i + e < a.d)
+                    *reinterpret_cast<uint4 *>(row + 32 * i + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        // rows that are no numbers, again from the definition: dk and dv of a row together
+        const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
+        if (lane == 0) bad_rows[warp] = bad;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
+        if (half == 0)
+            for (; again != 0; again &= again - 1)            // K's tile has been read
+                dkv_row<T>(a, b, kh, k0 + quarter * 32 + __ffs(int(again)) - 1,
+                           reinterpret_cast<float *>(smem) + quarter * 2 * kMaxHeadDim);
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 10) tmem_free<1>(tmem, 512);
+}
+
+template <class T, int HD>
+__global__ void __launch_bounds__(kBackThreads, 1)
+attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m) {
+    using Z = BackSizes<HD, false>;
+    constexpr int ST = Z::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    const uint32_t q_at = smem_addr(smem), o_at = q_at + Z::kOperand, ring0 = q_at + 2 * Z::kOperand;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + ST) * Z::kOperand);
+    const uint32_t qo_full = smem_addr(bars), full = qo_full + 8, empty = full + 8 * ST;
+    const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, taken = dp_full + 8, ds_ready = taken + 8;
+    const uint32_t done = ds_ready + 16, drained = done + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint32_t *bad_rows = tmem_slot + 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (warp == 8 && lane == 0) {
+        mbar_init(qo_full, 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(taken, 8);
+        // one for each place of dS: the next pair's can be complete before this one's is
+        // asked for, and a barrier tells only two phases in a row apart
+        mbar_init(ds_ready, 8);
+        mbar_init(ds_ready + 8, 8);
+        mbar_init(done, 1);
+        mbar_init(drained, 1);
+        *abort = 0;
+        fence_mbar_init();
+        fence_async_shared();
+    }
+    if (warp == 10) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency();
+    const AttentionWaiter wait{abort, m.timeouts};
+
+    // The last queries, which have the most keys, first.
+    const int heads = a.batch * a.hq, block = int(gridDim.x) / heads - 1 - int(blockIdx.x) / heads;
+    const int h = int(blockIdx.x) % heads % a.hq, b = int(blockIdx.x) % heads / a.hq, kh = h / a.group;
+    const int q0 = block * kTile, shift = a.sk - a.sq;
+    const KeyTiles tiles = key_tiles(a, q0);
+    const int total = tiles.count();
+    // S, dP, two places of dS (64 columns each), dq
+    const uint32_t dq_acc = tmem + 384, ds_at = tmem + 256;
+
+    if (warp == 8) {                                          // loads
+        if (total > 0) {
+            if (elect_one()) {
+                mbar_expect_tx(qo_full, 2 * Z::kOperand);
+                for (int x = 0; x < Z::kBoxes; ++x) {
+                    tma_load_4d(q_at + x * kBox, &m.q, 64 * x, q0, h * m.q_head, b * m.q_batch, qo_full);
+                    tma_load_4d(o_at + x * kBox, &m.d_o, 64 * x, q0, h * m.do_head, b * m.do_batch, qo_full);
+                }
+            }
+            __syncwarp();
+            bool ok = true;
+            uint32_t issued = 0;
+            Turn<ST> ring;
+            for (int j = tiles.begin(); j < tiles.high && ok; j = tiles.next(j))
+                for (int x = 0; x < 2 && ok; ++x) {           // K, V
+                    ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t to = ring0 + ring.at * Z::kOperand, bar = full + 8 * ring.at;
+                        mbar_expect_tx(bar, Z::kOperand);
+                        for (int y = 0; y < Z::kBoxes; ++y)
+                            tma_load_4d(to + y * kBox, x == 0 ? &m.k : &m.v, 64 * y, j * kTile,
+                                        kh * (x == 0 ? m.k_head : m.v_head), b * (x == 0 ? m.k_batch : m.v_batch), bar);
+                    }
+                    __syncwarp();
+                    ring.next();
+                    ++issued;
+                }
+            const uint32_t open = issued < uint32_t(ST) ? issued : ST;
+            for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
+            wait(qo_full, 0, false);
+        }
+    } else if (warp == 9) {                                   // products
+        if (total > 0 && elect_one()) {
+            const bool bf16 = std::is_same_v<T, __nv_bfloat16>;
+            const int ksteps = (a.d + 15) / 16;
+            const uint32_t is = mma_f16_desc(kTile, kTile, bf16, a.scale < 0.f, false);
+            const uint32_t idp = mma_f16_desc(kTile, kTile, bf16, false, false);
+            const uint32_t io = mma_f16_desc(kTile, ksteps * 16, bf16, false, true);
+            Turn<ST> ring;
+            bool ok = wait(qo_full, 0);
+            auto take = [&]() {
+                ok = ok && wait(full + 8 * ring.at, ring.turn);
+                const uint32_t at = ring.at;
+                ring.next();
+                return at;
+            };
+            auto across_head = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t desc, uint32_t bar) {
+                const uint64_t dx = desc_k_major(x), dy = desc_k_major(y);
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t at = (k / 4) * (kBox / 16) + (k % 4) * 2;
+                    mma_f16(d, dx + at, dy + at, desc, k > 0);
+                }
+                mma_commit<1>(bar);
+            };
+            uint32_t k_now = 0;
+            // S and dP of a pair of tiles; V's place is free then
+            auto scores = [&]() {
+                k_now = take();
+                if (!ok) return;
+                tcgen05_after_sync();
+                across_head(tmem, q_at, ring0 + k_now * Z::kOperand, is, s_full);
+                const uint32_t v_now = take();
+                if (!ok) return;
+                tcgen05_after_sync();
+                across_head(tmem + kTile, o_at, ring0 + v_now * Z::kOperand, idp, dp_full);
+                mma_commit<1>(empty + 8 * v_now);
+            };
+            scores();
+            for (int i = 0; i < total && ok; ++i) {
+                const uint32_t k_place = k_now;
+                if (i + 1 < total) {
+                    ok = wait(taken, i & 1);                  // S and dP of this pair have been read
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    scores();
+                    if (!ok) break;
+                }
+                ok = wait(ds_ready + 8 * (i & 1), (i >> 1) & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                const uint64_t dk = desc_k_across(ring0 + k_place * Z::kOperand, kBox);
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_f16_tmem(dq_acc, ds_at + (i & 1) * 64 + 8 * k, dk + k * (16 * 128 / 16), io, i > 0 || k > 0);
+                mma_commit<1>(empty + 8 * k_place);
+            }
+            if (ok) mma_commit<1>(done);
+            mma_commit<1>(drained);
+            wait(drained, 0, false);
+        }
+    } else if (warp < 8) {                                    // values
+        const int half = warp / 4, quarter = warp % 4, row = q0 + quarter * 32 + lane, p = row + shift;
+        const int p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kTile;
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
+        const bool exists = row < a.sq;
+        const float2 st = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + row];     // row < sq_pad
+        bool ok = true;
+        int i = 0;
+        for (int j = tiles.begin(); j < tiles.high; j = tiles.next(j), ++i) {
+            ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
+            if (!ok) break;
+            tcgen05_after_sync();
+            const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + 64 * half;
+            const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
+            const int last = p - at0, after = p - a.window - at0, sink = a.sinks - at0;
+            uint32_t x[64];
+            float ds[64];
+            load64(ts, x);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) ds[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -st.x));
+            ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
+            if (!ok) break;
+            tcgen05_after_sync();
+            load64(tp, x);
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(taken);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) ds[e] *= __uint_as_float(x[e]) - st.y;
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e > last || (e <= after && e >= sink)) ds[e] = 0.f;
+            }
+            // the place's last product is done: S(j) was issued after it
+            store64<T>(ds_at + lanes + (i & 1) * 64 + 32 * half, ds);
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ds_ready + 8 * (i & 1));
+        }
+        if (total > 0) {
+            ok = __all_sync(0xffffffffu, ok && wait(done, 0));
+            tcgen05_after_sync();
+        }
+        // the warpgroups store the halves of each row
+        T *to = row_of<T>(a.dq, b, exists ? row : 0, h);
+        bool finite = true;
+        const int chunks = (a.d + 31) / 32;
+        for (int y = half; y < chunks; y += 2) {
+            uint32_t v[32];
+            if (total == 0) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0u;
+            } else if (ok) {
+                tmem_load32(dq_acc + lanes + 32 * y, v);
+                tmem_load_wait();
+                tmem_loaded32(v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float u = __uint_as_float(v[e + 2 * z]) * a.scale, g = __uint_as_float(v[e + 2 * z + 1]) * a.scale;
+                    if (32 * y + e < a.d) finite = finite && fabsf(u) < INFINITY && fabsf(g) < INFINITY;
+                    w[z] = pack_pair<T>(u, g);
+                }
+                if (exists && 32 * y + e < a.d)
+                    *reinterpret_cast<uint4 *>(to + 32 * y + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
+        if (lane == 0) bad_rows[warp] = bad;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
+        if (half == 0)
+            for (; again != 0; again &= again - 1)            // Q's tile has been read
+                dq_row<T>(a, b, h, q0 + quarter * 32 + __ffs(int(again)) - 1,
+                          reinterpret_cast<float *>(smem) + quarter * 2 * kMaxHeadDim);
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 10) tmem_free<1>(tmem, 512);
+}
+
+template <class T, int HD> basp_status go(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
+    constexpr auto dq = attention_dq_kernel<T, HD>, dkv = attention_dkv_kernel<T, HD>;
+    constexpr size_t dq_smem = BackSizes<HD, false>::kSmem, dkv_smem = BackSizes<HD, true>::kSmem;
+    if (!allow_shared_memory<dq, dq_smem>() || !allow_shared_memory<dkv, dkv_smem>()) return BASP_ERR_CUDA;
+    const int64_t q = ceil_div(a.sq, kTile) * a.batch * a.hq, k = ceil_div(a.sk, kTile) * a.batch * a.hkv;
+    if (q > kMaxSide || k > kMaxSide) return BASP_ERR_TOO_LARGE;
+    const basp_status st = launch(dkv, dim3(unsigned(k)), dim3(kBackThreads), dkv_smem, 1, stream, a, m);
+    if (st != BASP_OK) return st;
+    return launch(dq, dim3(unsigned(q)), dim3(kBackThreads), dq_smem, 1, stream, a, m);
+}
+
+}  // namespace
+
+basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream) {
+    if (bf16) return a.d <= 64 ? go<__nv_bfloat16, 64>(a, m, stream) : go<__nv_bfloat16, 128>(a, m, stream);
+    return a.d <= 64 ? go<__half, 64>(a, m, stream) : go<__half, 128>(a, m, stream);
+}
+
+}  // namespace basp_fp8

@@ -22,8 +22,11 @@ template <class T> __device__ __forceinline__ T *row_of(const Heads &t, int64_t 
 
 struct AttentionArgs {
     Heads q, k, v, o, d_o, dq, dk, dv;
-    float *lse, *delta;                  // [batch][Hq][Sq]
-    int batch, sq, sk, hq, hkv, d, group;
+    float *lse;                          // [batch][Hq][Sq]
+    // for the backward: (lse log2(e), D) of each query, [batch][Hq][sq_pad]; what a pair
+    // of a query that does not exist, or sees nothing, is: (infinity, 0)
+    float2 *stats;
+    int batch, sq, sk, sq_pad, hq, hkv, d, group;
     int window, sinks;                   // window: sk where all is visible
     float scale;
 };
@@ -48,6 +51,18 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttentionArgs &a, int r0) {
     const int low = max(0, max(0, r0 + a.sk - a.sq) - a.window + 1) / kTile;
     const int first_end = min(a.sinks, max(0, p1 - a.window + 1));
     return {min((first_end + kTile - 1) / kTile, low), low, p1 / kTile + 1};
+}
+
+// Query tiles that see any of the keys [k0, k0 + 128): [low, high).
+struct QueryTiles {
+    int low, high;
+};
+__device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &a, int k0) {
+    const int shift = a.sk - a.sq, k1 = min(k0 + kTile, a.sk) - 1;
+    const int last = (k0 < a.sinks ? a.sk - 1 : int(min(int64_t(a.sk) - 1, int64_t(k1) + a.window - 1))) - shift;
+    const int first = max(0, k0 - shift);
+    if (last < first) return {0, 0};
+    return {first / kTile, last / kTile + 1};
 }
 
 // A wait on one of the CTA's barriers, with a limit.
@@ -215,13 +230,16 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
         a.lse[(int64_t(b) * a.hq + h) * a.sq + i] = any ? m + logf(l) : -INFINITY;
 }
 
-// D of query i: do . o.
-template <class T> __device__ __forceinline__ float delta_row(const AttentionArgs &a, int b, int h, int i) {
+// The statistics of query i.
+template <class T> __device__ __forceinline__ float2 stats_row(const AttentionArgs &a, int b, int h, int i) {
+    if (i >= a.sq) return make_float2(INFINITY, 0.f);
     const int lane = threadIdx.x % 32;
     const T *o = row_of<const T>(a.o, b, i, h), *d_o = row_of<const T>(a.d_o, b, i, h);
     float s = 0.f;
     for (int e = lane; e < a.d; e += 32) s = fmaf(Elem<T>::to_float(o[e]), Elem<T>::to_float(d_o[e]), s);
-    return warp_add(s);
+    s = warp_add(s);
+    if (i + a.sk - a.sq < 0) return make_float2(INFINITY, 0.f);
+    return make_float2(a.lse[(int64_t(b) * a.hq + h) * a.sq + i] * kLog2e, s);
 }
 
 // dq of query i.
@@ -232,8 +250,8 @@ __device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i,
     __syncwarp();
     row_to_shared(mine, row_of<const T>(a.q, b, i, h), a.d, lane);
     row_to_shared(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d, lane);
-    const int64_t at = (int64_t(b) * a.hq + h) * a.sq + i;
-    const float lse = a.lse[at], delta = a.delta[at];
+    const float lse = a.lse[(int64_t(b) * a.hq + h) * a.sq + i];
+    const float delta = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + i].y;
     float dq[4] = {0.f, 0.f, 0.f, 0.f};
     each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
         float ds = 0.f;
@@ -260,12 +278,13 @@ __device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int 
     const int i0 = max(0, j - shift), i1 = last_position(a, j) - shift + 1;
     float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
     for (int h = kh * a.group; h < (kh + 1) * a.group; ++h) {
-        const int64_t at = (int64_t(b) * a.hq + h) * a.sq;
+        const float *lse = a.lse + (int64_t(b) * a.hq + h) * a.sq;
+        const float2 *stats = a.stats + (int64_t(b) * a.hq + h) * a.sq_pad;
         each_keys(0, i0, i1, lane, [&](int i, bool have) {
             float w = 0.f, ds = 0.f;
             if (have) {
-                w = expf(a.scale * row_dot(mine, row_of<const T>(a.q, b, i, h), a.d) - a.lse[at + i]);
-                ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d) - a.delta[at + i]) * a.scale;
+                w = expf(a.scale * row_dot(mine, row_of<const T>(a.q, b, i, h), a.d) - lse[i]);
+                ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d) - stats[i].y) * a.scale;
             }
             for (int x = 0; x < 32; ++x) {
                 const int ix = __shfl_sync(0xffffffffu, i, x);
