@@ -18,7 +18,8 @@ TORCH_OPS_PATH = os.path.join(PKG, "_torch_ops.so")
 TORCH_VERSION_PATH = os.path.join(PKG, "_torch_ops.built_with")
 TORCH_OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
 SOURCES = ["layout.cpp", "relayout.cu", "rmsnorm.cu", "layernorm.cu", "quantize.cu", "matmul.cu", "attention.cu",
-           "attention_forward.cu", "attention_backward.cu", "adamw.cu"]
+           "attention_forward.cu", "attention_backward.cu", "attention_decode.cu",
+           "adamw.cu"]
 INCLUDES = [os.path.join(INCLUDE, h) for h in ("basp.h", "basp_debug.h", "basp_fp8.h", "basp_attention.h",
                                                "basp_optim.h")]
 HEADERS = INCLUDES + \

@@ -78,11 +78,21 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t q, float (&v)[4]) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// What a step does to one element; m and v become m' and v'.
-__device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v) {
+// The root to one unit in the last place: what is divided by it, or rounded to 8 bits
+// afterwards, needs no more.
+__device__ __forceinline__ float root_of(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a step does to one element; m and v become m' and v', `root` the root of v'.
+__device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v,
+                                         float &root) {
     m = o.beta1 * m + o.one_beta1 * g;
     v = o.beta2 * v + o.one_beta2 * g * g;
-    return fmaf(p, o.decay, -c1 * __fdividef(m, fmaf(sqrtf(v), c2, o.eps)));
+    root = root_of(v);
+    return fmaf(p, o.decay, -c1 * __fdividef(m, fmaf(root, c2, o.eps)));
 }
 
 // Four elements of a 128-block (load4 of fp8_common.cuh), or their state bytes.
@@ -123,6 +133,7 @@ __device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float
             const int64_t at = b0 + i * kBlock;
             const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
             if (left == 0) break;
+            float root[4];
             if constexpr (EIGHT) {
                 from_e4m3x4(qm[i], m[i]);
                 from_e4m3x4(qv[i], v[i]);
@@ -135,19 +146,17 @@ __device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j]);
+            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root[j]);
             store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
             if constexpr (EIGHT) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = sqrtf(v[i][j]);
-                const uint32_t bm = row_scale(m[i]), bv = row_scale(v[i]);       // infinities are NaN now
+                const uint32_t bm = row_scale(m[i]), bv = row_scale(root);       // infinities are NaN now
                 const float im = inverse_scale(bm), iv = inverse_scale(bv);
                 float a[4], b[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t r = mix(uint32_t(at + (HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
                     a[j] = m[i][j] == m[i][j] ? round_at_random(m[i][j] * im, r & 0xffffu) : m[i][j];
-                    const float y = v[i][j] * iv;
+                    const float y = root[j] * iv;
                     b[j] = y == y ? round_at_random(y, r >> 16) : y;
                     if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
                 }

@@ -15,14 +15,14 @@ __device__ unsigned long long g_timeouts;
 
 constexpr int kRowWarps = 4;
 
-enum { kForward, kStats, kDq, kDkv };
+enum { kForward, kDq, kDkv };
 
 // A warp a row.
 template <class T, int WHAT>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ AttentionArgs a) {
     __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
     grid_dependency();
-    const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : WHAT == kStats ? a.sq_pad : a.sq;
+    const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : a.sq;
     const int64_t rows = int64_t(a.batch) * heads * len;
     for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
         const int i = int(r % len), h = int(r / len % heads), b = int(r / len / heads);
@@ -30,34 +30,55 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i, m);
         if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i, m);
         if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i, m);
-        if constexpr (WHAT == kStats) {
-            const float2 s = stats_row<T>(a, b, h, i);
-            if (threadIdx.x % 32 == 0) a.stats[r] = s;
-        }
     }
 }
 
 template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cudaStream_t stream) {
-    const int64_t rows = int64_t(a.batch) * (WHAT == kDkv   ? int64_t(a.hkv) * a.sk
-                                             : int64_t(a.hq) * (WHAT == kStats ? a.sq_pad : a.sq));
+    const int64_t rows = int64_t(a.batch) * (WHAT == kDkv ? int64_t(a.hkv) * a.sk : int64_t(a.hq) * a.sq);
     if (rows == 0) return BASP_OK;
     const int64_t ctas = std::min<int64_t>(ceil_div(rows, kRowWarps), 1 << 20);
     return launch(rows_kernel<T, WHAT>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a);
 }
 
-// One token: the row's keys are those of a query at position lengths[b] - 1.
-template <class T>
-__global__ void __launch_bounds__(kRowWarps * 32) decode_rows_kernel(const __grid_constant__ AttentionArgs a,
-                                                                     const int32_t *lengths) {
-    __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
+// The statistics that the backward takes, of a tile of 128 queries a CTA: LANES lanes a
+// row, 16 bytes each.
+template <class T, int LANES>
+__global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionArgs a) {
+    constexpr int ROWS = 256 / LANES, PASSES = kTile / ROWS;
     grid_dependency();
-    const int64_t rows = int64_t(a.batch) * a.hq;
-    for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
-        const int b = int(r / a.hq);
-        AttentionArgs s = a;
-        s.sk = max(0, min(a.sk, lengths[b]));
-        forward_row<T>(s, b, int(r % a.hq), 0, mine[threadIdx.x / 32]);
+    const int tiles = a.sq_pad / kTile, tile = int(blockIdx.x % unsigned(tiles)), head = int(blockIdx.x / unsigned(tiles));
+    const int h = head % a.hq, b = head / a.hq, e = int(threadIdx.x % LANES) * 8;
+    uint4 o[PASSES], g[PASSES];
+#pragma unroll
+    for (int x = 0; x < PASSES; ++x) {
+        const int i = tile * kTile + x * ROWS + int(threadIdx.x) / LANES;
+        const bool in = i < a.sq && e < a.d;
+        o[x] = in ? *reinterpret_cast<const uint4 *>(row_of<const T>(a.o, b, i, h) + e) : make_uint4(0, 0, 0, 0);
+        g[x] = in ? *reinterpret_cast<const uint4 *>(row_of<const T>(a.d_o, b, i, h) + e) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int x = 0; x < PASSES; ++x) {
+        const int i = tile * kTile + x * ROWS + int(threadIdx.x) / LANES;
+        float u[8], v[8], s = 0.f;
+        Pack<T>::unpack(o[x], u);
+        Pack<T>::unpack(g[x], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(u[j], v[j], s);
+#pragma unroll
+        for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        if (threadIdx.x % LANES == 0) {
+            const bool sees = i < a.sq && i + a.sk - a.sq >= 0;
+            a.stats[int64_t(head) * a.sq_pad + i] =
+                sees ? make_float2(a.lse[int64_t(head) * a.sq + i] * kLog2e, s) : make_float2(INFINITY, 0.f);
+        }
+    }
+}
+template <class T> basp_status launch_stats(const AttentionArgs &a, cudaStream_t stream) {
+    const int64_t ctas = int64_t(a.sq_pad / kTile) * a.batch * a.hq;
+    if (ctas == 0) return BASP_OK;
+    if (ctas > kMaxSide) return BASP_ERR_TOO_LARGE;
+    return a.d <= 64 ? launch(stats_kernel<T, 8>, dim3(unsigned(ctas)), dim3(256), 0, 1, stream, a)
+                     : launch(stats_kernel<T, 16>, dim3(unsigned(ctas)), dim3(256), 0, 1, stream, a);
 }
 
 // ---- host -----------------------------------------------------------------------
@@ -290,7 +311,7 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
         return BASP_ERR_CUDA;
     return with_type(desc->dtype, [&](auto t) {
         using T = decltype(t);
-        basp_status s = launch_rows<T, kStats>(a, stream);
+        basp_status s = launch_stats<T>(a, stream);
         if (s == BASP_OK && tiles) return launch_attention_backward(a, m, desc->dtype == BASP_DTYPE_BF16, stream);
         if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);
         if (s == BASP_OK) s = launch_rows<T, kDkv>(a, stream);
@@ -300,8 +321,8 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
 
 extern "C" int64_t basp_attention_decode_workspace(const basp_attention_desc *desc) {
     basp_status st;
-    if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
-    return 0;
+    if (!sizes_ok(desc, &st) || !rows_ok(desc) || desc->batch == 0 || desc->q_heads == 0) return 0;
+    return decode_workspace(args_of(desc));
 }
 
 extern "C" basp_status basp_attention_decode(const basp_attention_desc *desc, const basp_heads *q,
@@ -312,7 +333,7 @@ extern "C" basp_status basp_attention_decode(const basp_attention_desc *desc, co
     basp_status st;
     if (!sizes_ok(desc, &st)) return st;
     if (desc->q_len != 1) return BASP_ERR_INVALID_ARG;
-    if (!rows_ok(desc)) return BASP_ERR_TOO_LARGE;
+    if (!rows_ok(desc) || !decode_fits(args_of(desc))) return BASP_ERR_TOO_LARGE;
     HeadArgs args(desc);
     args.heads(q, 1, desc->q_heads, false);
     args.heads(k, desc->k_len, desc->k_heads, false);
@@ -329,11 +350,7 @@ extern "C" basp_status basp_attention_decode(const basp_attention_desc *desc, co
     if (st != BASP_OK || desc->batch == 0 || desc->q_heads == 0) return st;
     AttentionArgs a = args_of(desc);
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o);
-    return with_type(desc->dtype, [&](auto t) {
-        using T = decltype(t);
-        const int64_t ctas = std::min<int64_t>(ceil_div(int64_t(a.batch) * a.hq, kRowWarps), 1 << 20);
-        return launch(decode_rows_kernel<T>, dim3(unsigned(ctas)), dim3(kRowWarps * 32), 0, 1, stream, a, lengths);
-    });
+    return launch_attention_decode(a, lengths, workspace, desc->dtype == BASP_DTYPE_BF16, stream);
 }
 
 extern "C" basp_status basp_attention_timeouts(unsigned long long *count) {

@@ -15,6 +15,11 @@ struct HeadMaps {
     unsigned long long *timeouts;
 };
 
+// One token over a cache: the bytes of its workspace, and whether a grid holds its key heads.
+int64_t decode_workspace(const AttentionArgs &a);
+bool decode_fits(const AttentionArgs &a);
+basp_status launch_attention_decode(const AttentionArgs &a, const int32_t *lengths, void *workspace, bool bf16,
+                                    cudaStream_t stream);
 basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream);
 basp_status launch_attention_forward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream);
 

@@ -230,18 +230,6 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
         a.lse[(int64_t(b) * a.hq + h) * a.sq + i] = any ? m + logf(l) : -INFINITY;
 }
 
-// The statistics of query i.
-template <class T> __device__ __forceinline__ float2 stats_row(const AttentionArgs &a, int b, int h, int i) {
-    if (i >= a.sq) return make_float2(INFINITY, 0.f);
-    const int lane = threadIdx.x % 32;
-    const T *o = row_of<const T>(a.o, b, i, h), *d_o = row_of<const T>(a.d_o, b, i, h);
-    float s = 0.f;
-    for (int e = lane; e < a.d; e += 32) s = fmaf(Elem<T>::to_float(o[e]), Elem<T>::to_float(d_o[e]), s);
-    s = warp_add(s);
-    if (i + a.sk - a.sq < 0) return make_float2(INFINITY, 0.f);
-    return make_float2(a.lse[(int64_t(b) * a.hq + h) * a.sq + i] * kLog2e, s);
-}
-
 // dq of query i.
 template <class T>
 __device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i, float *mine) {
