@@ -18,8 +18,7 @@ namespace basp_fp8 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksEach = 4;                       // blocks of 128 that a warp has on their way at once
-constexpr int kChunk = 128 * (kThreads / 32) * kBlocksEach * 4;   // elements of a CTA
+constexpr int kChunk = 128 * (kThreads / 32) * 16;   // elements of a CTA
 
 struct Entry {
     void *p;
@@ -54,15 +53,29 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 // |y| <= 448 to the e4m3 grid, up with probability of the fraction: the 16 bits r
-// (and a half) are added below the last of the three mantissa bits.  Values below
-// 2^-6, whose steps are 2^-9, get there by an addition of 2^-6, exact to 2^-29.
-__device__ __forceinline__ float round_at_random(float y, uint32_t r) {
+// (and a half, `r` is 16 times that: 16 r + 8) are added below the last of the three
+// mantissa bits, which does not reach the sign.
+__device__ __forceinline__ float round_normal(float y, uint32_t r) {
+    return __uint_as_float((__float_as_uint(y) + r) & 0xfff00000u);
+}
+// The same for any y: values below 2^-6, whose steps are 2^-9, get there by an addition of
+// 2^-6, exact to 2^-29; a NaN stays.
+__device__ __forceinline__ float round_any(float y, uint32_t r) {
     const float a = fabsf(y);
+    if (!(a <= 448.f)) return y;
     const bool small = a < 0x1p-6f;
-    uint32_t u = __float_as_uint(small ? a + 0x1p-6f : a);
-    u = (u + (r << 4) + 8u) & 0xfff00000u;
-    const float t = __uint_as_float(u);
+    const float t = round_normal(small ? a + 0x1p-6f : a, r);
     return copysignf(small ? t - 0x1p-6f : t, y);
+}
+
+// The scale byte of a block from its largest magnitude's bits, or where those say that
+// there are infinities or NaN, of what is finite; infinities become NaN.
+__device__ __forceinline__ uint32_t state_scale(uint32_t top, float (&v)[4]) {
+    if (top >= kInfBits) {
+        top = __reduce_max_sync(0xffffffffu, max_finite_bits4(v));
+        infinite_to_nan(v);
+    }
+    return scale_byte(top);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t byte) {           // 2^(byte - 127)
@@ -78,21 +91,27 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t q, float (&v)[4]) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// The root to one unit in the last place: what is divided by it, or rounded to 8 bits
-// afterwards, needs no more.
+// The root to one unit in the last place (what is divided by it, or rounded to 8 bits
+// afterwards, needs no more), of a v below 2^-126 zero; and a quotient.
 __device__ __forceinline__ float root_of(float x) {
     float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float over(float x, float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return x * r;
 }
 
 // What a step does to one element; m and v become m' and v', `root` the root of v'.
 __device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v,
                                          float &root) {
-    m = o.beta1 * m + o.one_beta1 * g;
-    v = o.beta2 * v + o.one_beta2 * g * g;
+    m = fmaf(o.one_beta1, g, o.beta1 * m);
+    v = fmaf(o.one_beta2 * g, g, o.beta2 * v);
     root = root_of(v);
-    return fmaf(p, o.decay, -c1 * __fdividef(m, fmaf(root, c2, o.eps)));
+    return fmaf(p, o.decay, -c1 * over(m, fmaf(root, c2, o.eps)));
 }
 
 // Four elements of a 128-block (load4 of fp8_common.cuh), or their state bytes.
@@ -107,6 +126,7 @@ template <int HOW> __device__ __forceinline__ uint32_t load4_bytes(const uint8_t
 
 template <class P, class G, bool EIGHT, int HOW>
 __device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float c1, float c2, uint32_t key, int64_t begin) {
+    constexpr int kBlocksEach = EIGHT ? 2 : 4;       // blocks of 128 that a warp has on their way at once
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = kThreads / 32;
     const int64_t end = min(e.n, begin + kChunk);
     for (int64_t b0 = begin + int64_t(warp) * kBlocksEach * kBlock; b0 < end; b0 += int64_t(warps) * kBlocksEach * kBlock) {
@@ -149,16 +169,42 @@ __device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float
             for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root[j]);
             store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
             if constexpr (EIGHT) {
-                const uint32_t bm = row_scale(m[i]), bv = row_scale(root);       // infinities are NaN now
-                const float im = inverse_scale(bm), iv = inverse_scale(bv);
-                float a[4], b[4];
+                uint32_t bits[4], tm = 0, tv = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t r = mix(uint32_t(at + (HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
-                    a[j] = m[i][j] == m[i][j] ? round_at_random(m[i][j] * im, r & 0xffffu) : m[i][j];
-                    const float y = root[j] * iv;
-                    b[j] = y == y ? round_at_random(y, r >> 16) : y;
-                    if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
+                    bits[j] = __float_as_uint(m[i][j]) & 0x7fffffffu;
+                    tm = max(tm, bits[j]);
+                    tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
+                }
+                tm = __reduce_max_sync(0xffffffffu, tm);
+                tv = __reduce_max_sync(0xffffffffu, tv);
+                const uint32_t bm = state_scale(tm, m[i]), bv = state_scale(tv, root);
+                const float im = inverse_scale(bm), iv = inverse_scale(bv);
+                float a[4], b[4];
+                uint32_t r[4];
+                bool plain = max(tm, tv) < kInfBits;          // and no value but 0 below the 8 bits' normal range
+                const uint32_t lm = __float_as_uint(0x1p-6f * scale_of(bm)) - 1, lv = __float_as_uint(0x1p-6f * scale_of(bv)) - 1;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[j] = mix((uint32_t(at) + uint32_t(HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
+                    a[j] = m[i][j] * im;
+                    b[j] = root[j] * iv;
+                    plain = plain && bits[j] - 1 >= lm && __float_as_uint(root[j]) - 1 >= lv;
+                }
+                if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a[j] = round_normal(a[j], (r[j] << 4 & 0xffff0u) | 8u);
+                        b[j] = round_normal(b[j], (r[j] >> 12 & 0xffff0u) | 8u);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a[j] = round_any(a[j], (r[j] << 4 & 0xffff0u) | 8u);
+                        const float y = b[j];
+                        b[j] = round_any(y, (r[j] >> 12 & 0xffff0u) | 8u);
+                        if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
+                    }
                 }
                 store4_e4m3<HOW>(static_cast<uint8_t *>(e.m) + at, lane, left, to_e4m3x4(a, 1.f));
                 store4_e4m3<HOW>(static_cast<uint8_t *>(e.v) + at, lane, left, to_e4m3x4(b, 1.f));
@@ -175,7 +221,7 @@ __device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float
 }
 
 template <int CAP, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t) {
+__global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __grid_constant__ Table<CAP> t) {
     grid_dependency();
     int lo = 0, hi = t.count;                        // e[lo].chunk0 <= chunk < e[hi].chunk0
     while (hi - lo > 1) {

@@ -7,9 +7,10 @@
 // end.  Where there is more than one chunk, a second kernel joins the chunks' parts in
 // their order.
 //
-// Keys and values go from memory to registers, 16 bytes a lane, and straight into
-// mma.sync (16 query rows x 8 keys or columns x 16): a tcgen05 product would want 128
-// rows.  The sum over a head's values may be taken in any order, so lane t of four
+// Keys and values go through mma.sync (16 query rows x 8 keys or columns x 16): a
+// tcgen05 product would want 128 rows.  Each lane copies the 16-byte pieces that it will
+// read itself to shared memory, some turns ahead, so that no register holds what is on its
+// way and no barrier is needed: what bounds such a kernel is the number of bytes in flight.  The sum over a head's values may be taken in any order, so lane t of four
 // takes the values 8 t + 32 c .. + 7 of a key for both operands, as they lie; for the
 // product with V, lane g of eight takes the columns 8 g + 64 c .. + 7 of its four keys, and
 // pairs of keys are put together by byte permutations.
@@ -25,8 +26,20 @@ constexpr int kWarps = 4, kKeys = 16, kRows = 16;
 struct DecodeArgs {
     AttentionArgs a;
     const int32_t *lengths;
-    float *part;                         // [batch][Hq][chunks][d + 2]: sum, maximum, O
+    float *part;                         // [batch][Hq][chunks][d]: O
+    float2 *part_stats;                  // [batch][Hq][chunks]: maximum, sum
     int chunk, chunks, row_blocks;
+};
+
+// Turns on their way, and shared memory: 128 KB or more are in flight on an SM, with two
+// CTAs of heads of 128, or three of 64.
+template <int HD> struct DecodeSizes {
+    static constexpr int kStages = HD == 128 ? 3 : 4;
+    static constexpr int kPieces = 2 * (HD / 32) + 4 * (HD / 64);      // of K and of V, a lane and turn
+    static constexpr int kRing = kStages * kPieces * 32 * 16;          // bytes of a warp
+    static constexpr int kSmem = kWarps * kRing;
+    static_assert(kSmem >= kWarps * kRows * (HD + 4) * 4, "the parts of the warps");
+    static constexpr int kCtas = HD == 128 ? 2 : 3;
 };
 
 template <class T> __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -40,18 +53,12 @@ template <class T> __device__ __forceinline__ void mma_16x8x16(float (&c)[4], co
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The cache is read once: past L1, and first to go from L2.
-__device__ __forceinline__ uint4 load_once(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 template <class T, int HD>
-__global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(const __grid_constant__ DecodeArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, DecodeSizes<HD>::kCtas) decode_kernel(const __grid_constant__ DecodeArgs p) {
     constexpr int KC = HD / 32, VC = HD / 64;                 // 16-byte pieces of a key, of a value row, a lane
-    __shared__ float so[kWarps][kRows][HD + 4];
+    constexpr int ST = DecodeSizes<HD>::kStages, PIECES = DecodeSizes<HD>::kPieces;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float(*so)[kRows][HD + 4] = reinterpret_cast<float(*)[kRows][HD + 4]>(smem);        // at the end
     __shared__ float sm[kWarps][kRows], sl[kWarps][kRows];
     const AttentionArgs &a = p.a;
     grid_dependency();
@@ -79,26 +86,32 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
             }
         }
         const T *kp = row_of<const T>(a.k, b, 0, kh), *vp = row_of<const T>(a.v, b, 0, kh);
-        uint4 kr[2][KC], vr[4][VC];
-        auto load_k = [&](int n) {                            // key g of each eight
+        uint4 *mine = reinterpret_cast<uint4 *>(smem + warp * DecodeSizes<HD>::kRing) + lane;
+        auto fetch = [&](int n, int stage) {
+            uint4 *to = mine + stage * PIECES * 32;
+            if (n < n1) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = n + 8 * x + g;
-                const T *r = kp + int64_t(i < see.first_end ? i : i + skip) * a.k.ss;
+                for (int x = 0; x < 2; ++x) {                 // key g of each eight
+                    const int i = n + 8 * x + g;
+                    const T *r = kp + int64_t(i < see.first_end ? i : i + skip) * a.k.ss + 8 * t;
 #pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    kr[x][c] = i < n1 && 8 * t + 32 * c < a.d ? load_once(r + 8 * t + 32 * c) : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < KC; ++c) {
+                        const bool in = i < n1 && 8 * t + 32 * c < a.d;
+                        copy16_async(to + (x * KC + c) * 32, in ? r + 32 * c : kp, in);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {                 // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                    const int i = n + 8 * (x / 2) + 2 * t + x % 2;
+                    const T *r = vp + int64_t(i < see.first_end ? i : i + skip) * a.v.ss + 8 * g;
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) {
+                        const bool in = i < n1 && 8 * g + 64 * c < a.d;
+                        copy16_async(to + (2 * KC + x * VC + c) * 32, in ? r + 64 * c : vp, in);
+                    }
+                }
             }
-        };
-        auto load_v = [&](int n) {                            // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int i = n + 8 * (x / 2) + 2 * t + x % 2;
-                const T *r = vp + int64_t(i < see.first_end ? i : i + skip) * a.v.ss;
-#pragma unroll
-                for (int c = 0; c < VC; ++c)
-                    vr[x][c] = i < n1 && 8 * g + 64 * c < a.d ? load_once(r + 8 * g + 64 * c) : make_uint4(0, 0, 0, 0);
-            }
+            copy_commit();                                    // an empty group past the end keeps the count
         };
         float o[HD / 8][4], top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -106,10 +119,14 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         const float c = a.scale * kLog2e;
-        int n = n0 + warp * kKeys;
-        load_k(n);
-        load_v(n);
+        int n = n0 + warp * kKeys, stage = 0;
+#pragma unroll
+        for (int x = 0; x < ST - 1; ++x) fetch(n + x * kWarps * kKeys, x);
         for (; n < n1; n += kWarps * kKeys) {
+            fetch(n + (ST - 1) * kWarps * kKeys, stage == 0 ? ST - 1 : stage - 1);
+            copy_wait<ST - 1>();
+            const uint4 *from = mine + stage * PIECES * 32;
+            stage = stage + 1 < ST ? stage + 1 : 0;
             float s[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -117,11 +134,11 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
                 for (int j = 0; j < 4; ++j) s[x][j] = 0.f;
 #pragma unroll
                 for (int y = 0; y < KC; ++y) {
-                    mma_16x8x16<T>(s[x], q[2 * y], kr[x][y].x, kr[x][y].y);
-                    mma_16x8x16<T>(s[x], q[2 * y + 1], kr[x][y].z, kr[x][y].w);
+                    const uint4 k = from[(x * KC + y) * 32];
+                    mma_16x8x16<T>(s[x], q[2 * y], k.x, k.y);
+                    mma_16x8x16<T>(s[x], q[2 * y + 1], k.z, k.w);
                 }
             }
-            load_k(n + kWarps * kKeys);
             // rows g and g + 8: columns 2 t, 2 t + 1 of each eight keys
             float high[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -162,15 +179,21 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
                                    pack_pair<T>(s[1][0], s[1][1]), pack_pair<T>(s[1][2], s[1][3])};
 #pragma unroll
             for (int y = 0; y < VC; ++y) {
-                const uint32_t *v0 = &vr[0][y].x, *v1 = &vr[1][y].x, *v2 = &vr[2][y].x, *v3 = &vr[3][y].x;
+                uint32_t v[4][4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint4 u = from[(2 * KC + x * VC + y) * 32];
+                    v[x][0] = u.x; v[x][1] = u.y; v[x][2] = u.z; v[x][3] = u.w;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    mma_16x8x16<T>(o[8 * y + 2 * e], w, __byte_perm(v0[e], v1[e], 0x5410), __byte_perm(v2[e], v3[e], 0x5410));
-                    mma_16x8x16<T>(o[8 * y + 2 * e + 1], w, __byte_perm(v0[e], v1[e], 0x7632), __byte_perm(v2[e], v3[e], 0x7632));
+                    mma_16x8x16<T>(o[8 * y + 2 * e], w, __byte_perm(v[0][e], v[1][e], 0x5410), __byte_perm(v[2][e], v[3][e], 0x5410));
+                    mma_16x8x16<T>(o[8 * y + 2 * e + 1], w, __byte_perm(v[0][e], v[1][e], 0x7632), __byte_perm(v[2][e], v[3][e], 0x7632));
                 }
             }
-            load_v(n + kWarps * kKeys);
         }
+        copy_wait<0>();
+        __syncthreads();                                      // the rings are free
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -184,7 +207,8 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) so[warp][g + 8 * (j / 2)][8 * (2 * t + j % 2) + 64 * (i / 8) + i % 8] = o[i][j];
+            for (int j = 0; j < 4; ++j)
+                if (g + 8 * (j / 2) < rows) so[warp][g + 8 * (j / 2)][8 * (2 * t + j % 2) + 64 * (i / 8) + i % 8] = o[i][j];
         __syncthreads();
         for (int i = threadIdx.x; i < rows * HD; i += kWarps * 32) {
             const int r = i / HD, e = i % HD;
@@ -203,69 +227,111 @@ __global__ void __launch_bounds__(kWarps * 32, HD == 64 ? 4 : 3) decode_kernel(c
             if (p.chunks == 1) {
                 row_of<T>(a.o, b, 0, h)[e] = Elem<T>::from_float(len > 0 ? v / sum : 0.f);
             } else {
-                float *to = p.part + ((int64_t(b) * a.hq + h) * p.chunks + chunk) * (a.d + 2);
-                to[2 + e] = v;
-                if (e == 0) {
-                    to[0] = sum;
-                    to[1] = m;
-                }
+                const int64_t at = (int64_t(b) * a.hq + h) * p.chunks + chunk;
+                p.part[at * a.d + e] = v;
+                if (e == 0) p.part_stats[at] = make_float2(m, sum);
             }
         }
         __syncthreads();
     }
 }
 
-// The chunks' parts of one query head, in their order.
-template <class T> __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecodeArgs p) {
+// The chunks' parts of one query head: lanes of 16 bytes of O, several parts at a time,
+// each lane's in their order and then the lanes' in theirs.
+constexpr int kJoinThreads = 128;
+template <class T> __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs p) {
+    __shared__ float4 so[kJoinThreads];
+    __shared__ float ssum[kJoinThreads / 32], smax[kJoinThreads / 32];
     const AttentionArgs &a = p.a;
     grid_dependency();
-    const int h = int(blockIdx.x) % a.hq, b = int(blockIdx.x) / a.hq, e = threadIdx.x;
+    const int h = int(blockIdx.x) % a.hq, b = int(blockIdx.x) / a.hq, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int len = max(0, min(a.sk, p.lengths[b]));
     const Sees see = keys_of(a, len - 1);
     const int seen = see.first_end + len - see.last, parts = (seen + p.chunk - 1) / p.chunk;
-    const float *from = p.part + int64_t(blockIdx.x) * p.chunks * (a.d + 2);
+    const float2 *stats = p.part_stats + int64_t(blockIdx.x) * p.chunks;
+    const float4 *part = reinterpret_cast<const float4 *>(p.part + int64_t(blockIdx.x) * p.chunks * a.d);
     float m = -INFINITY;
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, from[int64_t(i) * (a.d + 2) + 1]);
-    float sum = 0.f, v = 0.f;
-    for (int i = 0; i < parts; ++i) {
-        const float *x = from + int64_t(i) * (a.d + 2);
-        const float f = x[1] == -INFINITY ? 0.f : exp2_fast(x[1] - m);
-        sum += x[0] * f;
-        if (e < a.d) v += x[2 + e] * f;
+    for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, stats[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) smax[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    // a part of nothing but minus infinities has a sum of 0, or of NaN
+    auto weight = [&](float2 x) { return x.x == -INFINITY ? 1.f : exp2_fast(x.x - m); };
+    float sum = 0.f;
+    for (int i = tid; i < parts; i += kJoinThreads) {
+        const float2 x = stats[i];
+        sum += x.y * weight(x);
     }
-    if (e < a.d) row_of<T>(a.o, b, 0, h)[e] = Elem<T>::from_float(len > 0 ? v / sum : 0.f);
+    sum = warp_add(sum);
+    if (lane == 0) ssum[warp] = sum;
+    const int quads = a.d / 4, slices = kJoinThreads / quads, slice = tid / quads, e = tid % quads;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (slice < slices) {
+#pragma unroll 4
+        for (int i = slice; i < parts; i += slices) {
+            const float f = weight(stats[i]);
+            const float4 x = part[int64_t(i) * quads + e];
+            v.x = fmaf(x.x, f, v.x);
+            v.y = fmaf(x.y, f, v.y);
+            v.z = fmaf(x.z, f, v.z);
+            v.w = fmaf(x.w, f, v.w);
+        }
+    }
+    so[tid] = v;
+    __syncthreads();
+    if (tid >= quads) return;
+    sum = (ssum[0] + ssum[1]) + (ssum[2] + ssum[3]);
+    for (int i = 1; i < slices; ++i) {
+        const float4 x = so[i * quads + tid];
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    const float inv = 1.f / sum;
+    const bool any = len > 0;
+    *reinterpret_cast<uint2 *>(row_of<T>(a.o, b, 0, h) + 4 * tid) =
+        make_uint2(pack_pair<T>(any ? v.x * inv : 0.f, any ? v.y * inv : 0.f),
+                   pack_pair<T>(any ? v.z * inv : 0.f, any ? v.w * inv : 0.f));
 }
 
-// Keys of a chunk: enough CTAs to fill the GPU a few times over, since sequences differ
-// in length, and 128 at least, which is two turns of a CTA's warps.
+// Keys of a chunk: as many CTAs as fit at once for one sequence, four times that for
+// several, which differ in length; 128 at least (two turns of a CTA's warps), 1024 at most.
 DecodeArgs plan(const AttentionArgs &a) {
     DecodeArgs p = {};
     p.a = a;
     p.row_blocks = int(ceil_div(a.group, kRows));
-    const int64_t most = std::min<int64_t>(a.sk, int64_t(a.window) + a.sinks);       // keys that a token can see
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.sk, int64_t(a.window) + a.sinks));   // that a token can see
     const int64_t heads = std::max<int64_t>(1, int64_t(a.batch) * a.hkv * p.row_blocks);
-    const int64_t want = ceil_div(152 * 8, heads);
-    int64_t chunk = ceil_div(std::max<int64_t>(1, ceil_div(most, want)), kWarps * kKeys) * kWarps * kKeys;
-    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), 512);
+    const int64_t ctas = 152 * (a.d <= 64 ? DecodeSizes<64>::kCtas : DecodeSizes<128>::kCtas) * (a.batch == 1 ? 1 : 4);
+    const int64_t turn = kWarps * kKeys;
+    int64_t chunk = ceil_div(ceil_div(most, std::max<int64_t>(1, ctas / heads)), turn) * turn;
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), 1024);
     p.chunk = int(chunk);
-    p.chunks = int(std::max<int64_t>(1, ceil_div(most, chunk)));
+    p.chunks = int(ceil_div(most, chunk));
     return p;
 }
 
-template <class T> basp_status go(const DecodeArgs &p, cudaStream_t stream) {
+template <class T, int HD> basp_status go(const DecodeArgs &p, cudaStream_t stream) {
+    constexpr auto kernel = decode_kernel<T, HD>;
+    constexpr size_t smem = DecodeSizes<HD>::kSmem;
+    if (!allow_shared_memory<kernel, smem>()) return BASP_ERR_CUDA;
     const AttentionArgs &a = p.a;
     const dim3 grid(unsigned(p.chunks), unsigned(a.hkv * p.row_blocks), unsigned(std::min(a.batch, 65535)));
-    const basp_status st = a.d <= 64 ? launch(decode_kernel<T, 64>, grid, dim3(kWarps * 32), 0, 1, stream, p)
-                                     : launch(decode_kernel<T, 128>, grid, dim3(kWarps * 32), 0, 1, stream, p);
+    const basp_status st = launch(kernel, grid, dim3(kWarps * 32), smem, 1, stream, p);
     if (st != BASP_OK || p.chunks == 1) return st;
-    return launch(decode_join_kernel<T>, dim3(unsigned(a.batch * a.hq)), dim3(128), 0, 1, stream, p);
+    return launch(decode_join_kernel<T>, dim3(unsigned(a.batch * a.hq)), dim3(kJoinThreads), 0, 1, stream, p);
+}
+
+// The parts' statistics, then O, which begins at a multiple of 16 bytes.
+int64_t stats_bytes(const DecodeArgs &p) {
+    return ceil_div(int64_t(p.a.batch) * p.a.hq * p.chunks * int64_t(sizeof(float2)), 16) * 16;
 }
 
 }  // namespace
 
 int64_t decode_workspace(const AttentionArgs &a) {
     const DecodeArgs p = plan(a);
-    return p.chunks == 1 ? 0 : int64_t(a.batch) * a.hq * p.chunks * (a.d + 2) * int64_t(sizeof(float));
+    return p.chunks == 1 ? 0 : stats_bytes(p) + int64_t(a.batch) * a.hq * p.chunks * a.d * int64_t(sizeof(float));
 }
 
 bool decode_fits(const AttentionArgs &a) { return int64_t(a.hkv) * ceil_div(a.group, kRows) <= 65535; }
@@ -274,8 +340,10 @@ basp_status launch_attention_decode(const AttentionArgs &a, const int32_t *lengt
                                     cudaStream_t stream) {
     DecodeArgs p = plan(a);
     p.lengths = lengths;
-    p.part = static_cast<float *>(workspace);
-    return bf16 ? go<__nv_bfloat16>(p, stream) : go<__half>(p, stream);
+    p.part_stats = static_cast<float2 *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + stats_bytes(p));
+    if (bf16) return a.d <= 64 ? go<__nv_bfloat16, 64>(p, stream) : go<__nv_bfloat16, 128>(p, stream);
+    return a.d <= 64 ? go<__half, 64>(p, stream) : go<__half, 128>(p, stream);
 }
 
 }  // namespace basp_fp8

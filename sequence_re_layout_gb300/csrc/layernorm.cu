@@ -340,7 +340,7 @@ basp_status launch_layer(const LayerArgs &a, cudaStream_t stream) {
             const int64_t ctas = std::min(a.rows, resident_ctas(kernel, threads, smem));
             return launch(kernel, dim3(unsigned(ctas)), dim3(threads), smem, 1, stream, a);
         };
-        if (vectors <= kWalkThreads) return walk(std::integral_constant<int, 1>());
+        if (vectors <= 32) return walk(std::integral_constant<int, 1>());
         if (vectors <= 2 * kWalkThreads) return walk(std::integral_constant<int, 2>());
         if (vectors <= 4 * kWalkThreads) return walk(std::integral_constant<int, 4>());
     }
