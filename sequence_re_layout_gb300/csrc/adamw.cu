@@ -18,7 +18,7 @@ namespace basp_fp8 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 128 * (kThreads / 32) * 16;   // elements of a CTA
+constexpr int kChunk = 128 * (kThreads / 32) * 16;       // elements of a CTA
 
 struct Entry {
     void *p;
@@ -124,104 +124,174 @@ template <int HOW> __device__ __forceinline__ uint32_t load4_bytes(const uint8_t
     return q;
 }
 
-template <class P, class G, bool EIGHT, int HOW>
-__device__ __forceinline__ void do_chunk(const Entry &e, const Options &o, float c1, float c2, uint32_t key, int64_t begin) {
-    constexpr int kBlocksEach = EIGHT ? 2 : 4;       // blocks of 128 that a warp has on their way at once
+// One block of 128 with 8-bit states: p, g and the state bytes (four a lane) as they were,
+// p and the state bytes as they will be, and the scale bytes.  `at`: the block's first
+// element's place in its tensor.
+template <int HOW>
+__device__ __forceinline__ void step_block(const Options &o, float c1, float c2, uint32_t key, uint32_t at, float (&p)[4],
+                                           const float (&g)[4], uint32_t &qm, uint32_t &qv, uint32_t &em, uint32_t &ev) {
+    const int lane = threadIdx.x % 32;
+    float m[4], v[4], root[4];
+    from_e4m3x4(qm, m);
+    from_e4m3x4(qv, v);
+    const float sm = scale_of(em), sv = scale_of(ev);
+    uint32_t bits[4], tm = 0, tv = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[j] *= sm;
+        v[j] *= sv;
+        v[j] *= v[j];
+        p[j] = step_of(o, c1, c2, p[j], g[j], m[j], v[j], root[j]);
+        bits[j] = __float_as_uint(m[j]) & 0x7fffffffu;
+        tm = max(tm, bits[j]);
+        tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
+    }
+    tm = __reduce_max_sync(0xffffffffu, tm);
+    tv = __reduce_max_sync(0xffffffffu, tv);
+    em = state_scale(tm, m);                              // infinities are NaN now
+    ev = state_scale(tv, root);
+    const float im = inverse_scale(em), iv = inverse_scale(ev);
+    float a[4], b[4];
+    uint32_t r[4];
+    bool plain = max(tm, tv) < kInfBits;                  // and no value but 0 below the 8 bits' normal range
+    const uint32_t lm = __float_as_uint(0x1p-6f * scale_of(em)) - 1, lv = __float_as_uint(0x1p-6f * scale_of(ev)) - 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r[j] = mix((at + uint32_t(HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
+        a[j] = m[j] * im;
+        b[j] = root[j] * iv;
+        plain = plain && bits[j] - 1 >= lm && __float_as_uint(root[j]) - 1 >= lv;
+    }
+    if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = round_normal(a[j], (r[j] << 4 & 0xffff0u) | 8u);
+            b[j] = round_normal(b[j], (r[j] >> 12 & 0xffff0u) | 8u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = round_any(a[j], (r[j] << 4 & 0xffff0u) | 8u);
+            const float y = b[j];
+            b[j] = round_any(y, (r[j] >> 12 & 0xffff0u) | 8u);
+            if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
+        }
+    }
+    qm = to_e4m3x4(a, 1.f);
+    qv = to_e4m3x4(b, 1.f);
+}
+
+// A chunk with 32-bit states.
+template <class P, class G, int HOW>
+__device__ __forceinline__ void do_chunk32(const Entry &e, const Options &o, float c1, float c2, int64_t begin) {
+    constexpr int kBlocksEach = 4;                        // blocks of 128 that a warp has on their way at once
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = kThreads / 32;
     const int64_t end = min(e.n, begin + kChunk);
     for (int64_t b0 = begin + int64_t(warp) * kBlocksEach * kBlock; b0 < end; b0 += int64_t(warps) * kBlocksEach * kBlock) {
-        float p[kBlocksEach][4], g[kBlocksEach][4], m[kBlocksEach][4], v[kBlocksEach][4];
-        uint32_t qm[kBlocksEach], qv[kBlocksEach], em[kBlocksEach], ev[kBlocksEach];
+        float p[kBlocksEach][4], g[kBlocksEach][4], m[kBlocksEach][4], v[kBlocksEach][4], root;
 #pragma unroll
         for (int i = 0; i < kBlocksEach; ++i) {
             const int64_t at = b0 + i * kBlock;
             const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
             load4<P, HOW>(static_cast<const P *>(e.p) + at, lane, left, p[i]);
             load4<G, HOW>(static_cast<const G *>(e.g) + at, lane, left, g[i]);
-            if constexpr (EIGHT) {
-                qm[i] = load4_bytes<HOW>(static_cast<const uint8_t *>(e.m) + at, lane, left);
-                qv[i] = load4_bytes<HOW>(static_cast<const uint8_t *>(e.v) + at, lane, left);
-                em[i] = left > 0 ? static_cast<const uint8_t *>(e.ms)[at / kBlock] : 0;
-                ev[i] = left > 0 ? static_cast<const uint8_t *>(e.vs)[at / kBlock] : 0;
-            } else {
-                load4<float, HOW>(static_cast<const float *>(e.m) + at, lane, left, m[i]);
-                load4<float, HOW>(static_cast<const float *>(e.v) + at, lane, left, v[i]);
-            }
+            load4<float, HOW>(static_cast<const float *>(e.m) + at, lane, left, m[i]);
+            load4<float, HOW>(static_cast<const float *>(e.v) + at, lane, left, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < kBlocksEach; ++i) {
             const int64_t at = b0 + i * kBlock;
             const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
-            if (left == 0) break;
-            float root[4];
-            if constexpr (EIGHT) {
-                from_e4m3x4(qm[i], m[i]);
-                from_e4m3x4(qv[i], v[i]);
-                const float sm = scale_of(em[i]), sv = scale_of(ev[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    m[i][j] *= sm;
-                    v[i][j] *= sv;
-                    v[i][j] *= v[i][j];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root[j]);
+            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root);
             store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
-            if constexpr (EIGHT) {
-                uint32_t bits[4], tm = 0, tv = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    bits[j] = __float_as_uint(m[i][j]) & 0x7fffffffu;
-                    tm = max(tm, bits[j]);
-                    tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
-                }
-                tm = __reduce_max_sync(0xffffffffu, tm);
-                tv = __reduce_max_sync(0xffffffffu, tv);
-                const uint32_t bm = state_scale(tm, m[i]), bv = state_scale(tv, root);
-                const float im = inverse_scale(bm), iv = inverse_scale(bv);
-                float a[4], b[4];
-                uint32_t r[4];
-                bool plain = max(tm, tv) < kInfBits;          // and no value but 0 below the 8 bits' normal range
-                const uint32_t lm = __float_as_uint(0x1p-6f * scale_of(bm)) - 1, lv = __float_as_uint(0x1p-6f * scale_of(bv)) - 1;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    r[j] = mix((uint32_t(at) + uint32_t(HOW == kVector ? 4 * lane + j : lane + 32 * j)) * 0x9E3779B9u + key);
-                    a[j] = m[i][j] * im;
-                    b[j] = root[j] * iv;
-                    plain = plain && bits[j] - 1 >= lm && __float_as_uint(root[j]) - 1 >= lv;
-                }
-                if (__all_sync(0xffffffffu, plain)) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[j] = round_normal(a[j], (r[j] << 4 & 0xffff0u) | 8u);
-                        b[j] = round_normal(b[j], (r[j] >> 12 & 0xffff0u) | 8u);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[j] = round_any(a[j], (r[j] << 4 & 0xffff0u) | 8u);
-                        const float y = b[j];
-                        b[j] = round_any(y, (r[j] >> 12 & 0xffff0u) | 8u);
-                        if (y > 0.f) b[j] = fmaxf(b[j], 0x1p-9f);
-                    }
-                }
-                store4_e4m3<HOW>(static_cast<uint8_t *>(e.m) + at, lane, left, to_e4m3x4(a, 1.f));
-                store4_e4m3<HOW>(static_cast<uint8_t *>(e.v) + at, lane, left, to_e4m3x4(b, 1.f));
-                if (lane == 0) {
-                    static_cast<uint8_t *>(e.ms)[at / kBlock] = uint8_t(bm);
-                    static_cast<uint8_t *>(e.vs)[at / kBlock] = uint8_t(bv);
-                }
-            } else {
-                store4<float, HOW>(static_cast<float *>(e.m) + at, lane, left, m[i]);
-                store4<float, HOW>(static_cast<float *>(e.v) + at, lane, left, v[i]);
-            }
+            store4<float, HOW>(static_cast<float *>(e.m) + at, lane, left, m[i]);
+            store4<float, HOW>(static_cast<float *>(e.v) + at, lane, left, v[i]);
         }
     }
 }
 
+// A chunk with 8-bit states, whose warps have 16 neighbouring blocks each: the scale
+// bytes of those are one load, and one store at the end.
+constexpr int kRun = kChunk / kBlock / (kThreads / 32);
+static_assert(kRun == 16, "a lane for each scale of a run, of m and of v");
+
+// The buffers allow four elements at a time: each lane copies what it will read itself
+// to shared memory, kStages - 1 blocks ahead.  What bounds this kernel otherwise is the
+// number of bytes in flight: 1165 us for four layers of 50 million elements with the loads
+// of two blocks in registers.
+constexpr int kStages = 4, kStageBytes = 32 * (16 + 16 + 4 + 4);
+
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool have) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
+                     ::"r"(dst), "l"(src), "n"(BYTES), "r"(have ? BYTES : 0) : "memory");
+}
+
+template <class P, class G, int HOW>
+__device__ __forceinline__ void do_chunk8(const Entry &e, const Options &o, float c1, float c2, uint32_t key, int64_t begin,
+                                          uint8_t *ring) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t first = begin + int64_t(warp) * kRun * kBlock;
+    if (first >= e.n) return;
+    const int blocks = int(min(int64_t(kRun), (e.n - first + kBlock - 1) / kBlock));
+    uint8_t *const scales = static_cast<uint8_t *>(lane < kRun ? e.ms : e.vs) + first / kBlock + lane % kRun;
+    const uint32_t old = lane % kRun < blocks ? *scales : 0u;
+    uint32_t made = 0;
+    uint8_t *mine = ring + warp * (kStages * kStageBytes);
+    const P *ep = static_cast<const P *>(e.p) + first;
+    const G *eg = static_cast<const G *>(e.g) + first;
+    const uint8_t *m8 = static_cast<const uint8_t *>(e.m) + first, *v8 = static_cast<const uint8_t *>(e.v) + first;
+    auto left_of = [&](int i) { return int(min(e.n - first - int64_t(i) * kBlock, int64_t(kBlock))); };
+    auto fetch = [&](int i) {
+        if constexpr (HOW == kVector) {
+            if (i < blocks) {
+                const uint32_t to = uint32_t(__cvta_generic_to_shared(mine + (i % kStages) * kStageBytes));
+                const bool have = 4 * lane < left_of(i);
+                const int at = have ? i * kBlock + 4 * lane : 0;
+                copy_async<4 * sizeof(P)>(to + lane * 16, ep + at, have);
+                copy_async<4 * sizeof(G)>(to + 512 + lane * 16, eg + at, have);
+                copy_async<4>(to + 1024 + lane * 4, m8 + at, have);
+                copy_async<4>(to + 1152 + lane * 4, v8 + at, have);
+            }
+            copy_commit();                                // an empty group past the end keeps the count
+        }
+    };
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+#pragma unroll 1
+    for (int i = 0; i < blocks; ++i) {
+        const int left = left_of(i);
+        float p[4], g[4];
+        uint32_t qm, qv;
+        fetch(i + kStages - 1);
+        if constexpr (HOW == kVector) {
+            copy_wait<kStages - 1>();
+            const uint8_t *from = mine + (i % kStages) * kStageBytes;
+            load4<P, kVector>(reinterpret_cast<const P *>(from + lane * 16), 0, 4, p);
+            load4<G, kVector>(reinterpret_cast<const G *>(from + 512 + lane * 16), 0, 4, g);
+            qm = *reinterpret_cast<const uint32_t *>(from + 1024 + lane * 4);
+            qv = *reinterpret_cast<const uint32_t *>(from + 1152 + lane * 4);
+        } else {
+            load4<P, HOW>(ep + i * kBlock, lane, left, p);
+            load4<G, HOW>(eg + i * kBlock, lane, left, g);
+            qm = load4_bytes<HOW>(m8 + i * kBlock, lane, left);
+            qv = load4_bytes<HOW>(v8 + i * kBlock, lane, left);
+        }
+        uint32_t em = __shfl_sync(0xffffffffu, old, i), ev = __shfl_sync(0xffffffffu, old, i + kRun);
+        step_block<HOW>(o, c1, c2, key, uint32_t(first + i * kBlock), p, g, qm, qv, em, ev);
+        store4<P, HOW>(static_cast<P *>(e.p) + first + i * kBlock, lane, left, p);
+        store4_e4m3<HOW>(static_cast<uint8_t *>(e.m) + first + i * kBlock, lane, left, qm);
+        store4_e4m3<HOW>(static_cast<uint8_t *>(e.v) + first + i * kBlock, lane, left, qv);
+        if (lane % kRun == i) made = lane < kRun ? em : ev;
+    }
+    if (lane % kRun < blocks) *scales = uint8_t(made);
+}
+
 template <int CAP, bool EIGHT>
 __global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __grid_constant__ Table<CAP> t) {
+    __shared__ __align__(16) uint8_t ring[EIGHT ? (kThreads / 32) * kStages * kStageBytes : 16];
     grid_dependency();
     int lo = 0, hi = t.count;                        // e[lo].chunk0 <= chunk < e[hi].chunk0
     while (hi - lo > 1) {
@@ -243,8 +313,13 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __
     auto go = [&](auto pe, auto ge) {
         using P = decltype(pe);
         using G = decltype(ge);
-        if (e.vec) do_chunk<P, G, EIGHT, kVector>(e, t.o, c1, c2, key, begin);
-        else do_chunk<P, G, EIGHT, kStrided>(e, t.o, c1, c2, key, begin);
+        if constexpr (EIGHT) {
+            if (e.vec) do_chunk8<P, G, kVector>(e, t.o, c1, c2, key, begin, ring);
+            else do_chunk8<P, G, kStrided>(e, t.o, c1, c2, key, begin, ring);
+        } else {
+            if (e.vec) do_chunk32<P, G, kVector>(e, t.o, c1, c2, begin);
+            else do_chunk32<P, G, kStrided>(e, t.o, c1, c2, begin);
+        }
     };
     if (e.type == BASP_DTYPE_FP32) return go(float(), float());
     if (e.type == BASP_DTYPE_BF16)

@@ -20,16 +20,14 @@ enum { kForward, kDq, kDkv };
 // A warp a row.
 template <class T, int WHAT>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ AttentionArgs a) {
-    __shared__ float mine[kRowWarps][2 * kMaxHeadDim];
     grid_dependency();
     const int heads = WHAT == kDkv ? a.hkv : a.hq, len = WHAT == kDkv ? a.sk : a.sq;
     const int64_t rows = int64_t(a.batch) * heads * len;
     for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
         const int i = int(r % len), h = int(r / len % heads), b = int(r / len / heads);
-        float *m = mine[threadIdx.x / 32];
-        if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i, m);
-        if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i, m);
-        if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i, m);
+        if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i);
+        if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i);
+        if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i);
     }
 }
 

@@ -61,6 +61,13 @@ template <class T> __device__ __forceinline__ void store64(uint32_t addr, const 
     tmem_store_wait();
 }
 
+// 0 in the places whose bit is not set.
+__device__ __forceinline__ void keep(float (&v)[64], const uint32_t (&seen)[2]) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        if (!(seen[i / 32] >> (i % 32) & 1u)) v[i] = 0.f;
+}
+
 template <class T, int HD>
 __global__ void __launch_bounds__(kBackThreads, 1)
 attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m) {
@@ -236,6 +243,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             // columns of this warpgroup that see the key: [first, last]
             const int at0 = q0 + 64 * half;
             const int first = key - shift - at0, last = last_position(a, key) - shift - at0;
+            const uint32_t seen[2] = {bits_to(last) & ~bits_to(first - 1), bits_to(last - 32) & ~bits_to(first - 33)};
             const float4 *st = reinterpret_cast<const float4 *>(stats + place.at * Z::kStats) + 32 * half;
             uint32_t x[64];
             float p[64];
@@ -246,11 +254,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 p[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -f.x));
                 p[e + 1] = exp2_fast(fmaf(__uint_as_float(x[e + 1]), c, -f.z));
             }
-            if (masked) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e < first || e > last) p[e] = 0.f;
-            }
+            if (masked) keep(p, seen);
             store64<T>(ts, p);
             tcgen05_before_sync();
             __syncwarp();
@@ -265,11 +269,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 p[e] *= __uint_as_float(x[e]) - f.y;
                 p[e + 1] *= __uint_as_float(x[e + 1]) - f.w;
             }
-            if (masked) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e < first || e > last) p[e] = 0.f;    // 0 times an infinity
-            }
+            if (masked) keep(p, seen);                        // 0 times an infinity
             store64<T>(tp, p);
             tcgen05_before_sync();
             __syncwarp();
@@ -317,9 +317,8 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         asm volatile("bar.sync 1, 256;" ::: "memory");
         uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
         if (half == 0)
-            for (; again != 0; again &= again - 1)            // K's tile has been read
-                dkv_row<T>(a, b, kh, k0 + quarter * 32 + __ffs(int(again)) - 1,
-                           reinterpret_cast<float *>(smem) + quarter * 2 * kMaxHeadDim);
+            for (; again != 0; again &= again - 1)
+                dkv_row<T>(a, b, kh, k0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -502,9 +501,9 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
 #pragma unroll
             for (int e = 0; e < 64; ++e) ds[e] *= __uint_as_float(x[e]) - st.y;
             if (masked) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e > last || (e <= after && e >= sink)) ds[e] = 0.f;
+                const uint32_t seen[2] = {bits_to(last) & (~bits_to(after) | bits_to(sink - 1)),
+                                          bits_to(last - 32) & (~bits_to(after - 32) | bits_to(sink - 33))};
+                keep(ds, seen);
             }
             // the place's last product is done: S(j) was issued after it
             store64<T>(ds_at + lanes + (i & 1) * 64 + 32 * half, ds);
@@ -551,9 +550,8 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         asm volatile("bar.sync 1, 256;" ::: "memory");
         uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
         if (half == 0)
-            for (; again != 0; again &= again - 1)            // Q's tile has been read
-                dq_row<T>(a, b, h, q0 + quarter * 32 + __ffs(int(again)) - 1,
-                          reinterpret_cast<float *>(smem) + quarter * 2 * kMaxHeadDim);
+            for (; again != 0; again &= again - 1)
+                dq_row<T>(a, b, h, q0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();

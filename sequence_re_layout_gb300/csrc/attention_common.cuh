@@ -65,6 +65,9 @@ __device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &a, int k0
     return {first / kTile, last / kTile + 1};
 }
 
+// Bits 0 to n of a word.
+__device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u; }
+
 // A wait on one of the CTA's barriers, with a limit.
 constexpr uint64_t kAttentionWaitNs = 2000000000ull;
 struct AttentionWaiter {
@@ -149,22 +152,18 @@ __device__ __forceinline__ int last_position(const AttentionArgs &a, int j) {
 //
 // A warp computes one row from its definition, reading nothing but what the row
 // sees: lanes hold a key (or a query) each for the products, then four elements of
-// the row each for the sums.  `mine` is 2 x 128 floats of shared memory of the warp.
+// the row each for the sums.
 
-template <class T> __device__ __forceinline__ float row_dot(const float *x, const T *y, int d) {
+template <class T> __device__ __forceinline__ float row_dot(const T *x, const T *y, int d) {
     float s = 0.f;
     for (int e = 0; e < d; e += 8) {
-        float f[8];
-        Pack<T>::unpack(*reinterpret_cast<const uint4 *>(y + e), f);
+        float f[8], g[8];
+        Pack<T>::unpack(*reinterpret_cast<const uint4 *>(x + e), f);
+        Pack<T>::unpack(*reinterpret_cast<const uint4 *>(y + e), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(x[e + j], f[j], s);
+        for (int j = 0; j < 8; ++j) s = fmaf(f[j], g[j], s);
     }
     return s;
-}
-
-template <class T> __device__ __forceinline__ void row_to_shared(float *mine, const T *row, int d, int lane) {
-    for (int e = lane; e < d; e += 32) mine[e] = Elem<T>::to_float(row[e]);
-    __syncwarp();
 }
 
 template <class T> __device__ __forceinline__ void row_add(float (&sum)[4], float p, const T *row, int d, int lane) {
@@ -202,14 +201,13 @@ __device__ __forceinline__ float warp_add(float v) {
 
 // o and lse of query i.
 template <class T>
-__device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, int i, float *mine) {
+__device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, int i) {
     const int lane = threadIdx.x % 32, p = i + a.sk - a.sq, kh = h / a.group;
     const Sees see = keys_of(a, p);
-    __syncwarp();
-    row_to_shared(mine, row_of<const T>(a.q, b, i, h), a.d, lane);
+    const T *q = row_of<const T>(a.q, b, i, h);
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
-        const float s = have ? a.scale * row_dot(mine, row_of<const T>(a.k, b, j, kh), a.d) : -INFINITY;
+        const float s = have ? a.scale * row_dot(q, row_of<const T>(a.k, b, j, kh), a.d) : -INFINITY;
         const float top = warp_max(s), next = m > top || m != m ? m : top;
         const float w = have ? expf(s - next) : 0.f, old = m == -INFINITY && l == 0.f ? 0.f : expf(m - next);
         l = l * old + warp_add(w);
@@ -232,20 +230,18 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
 
 // dq of query i.
 template <class T>
-__device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i, float *mine) {
+__device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i) {
     const int lane = threadIdx.x % 32, p = i + a.sk - a.sq, kh = h / a.group;
     const Sees see = keys_of(a, p);
-    __syncwarp();
-    row_to_shared(mine, row_of<const T>(a.q, b, i, h), a.d, lane);
-    row_to_shared(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d, lane);
+    const T *q = row_of<const T>(a.q, b, i, h), *d_o = row_of<const T>(a.d_o, b, i, h);
     const float lse = a.lse[(int64_t(b) * a.hq + h) * a.sq + i];
     const float delta = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + i].y;
     float dq[4] = {0.f, 0.f, 0.f, 0.f};
     each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
         float ds = 0.f;
         if (have) {
-            const float w = expf(a.scale * row_dot(mine, row_of<const T>(a.k, b, j, kh), a.d) - lse);
-            ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.v, b, j, kh), a.d) - delta) * a.scale;
+            const float w = expf(a.scale * row_dot(q, row_of<const T>(a.k, b, j, kh), a.d) - lse);
+            ds = w * (row_dot(d_o, row_of<const T>(a.v, b, j, kh), a.d) - delta) * a.scale;
         }
         for (int x = 0; x < 32; ++x) {
             const int jx = __shfl_sync(0xffffffffu, j, x);
@@ -258,11 +254,9 @@ __device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i,
 
 // dk and dv of key j, over all query heads that share it.
 template <class T>
-__device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int j, float *mine) {
+__device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int j) {
     const int lane = threadIdx.x % 32, shift = a.sk - a.sq;
-    __syncwarp();
-    row_to_shared(mine, row_of<const T>(a.k, b, j, kh), a.d, lane);
-    row_to_shared(mine + kMaxHeadDim, row_of<const T>(a.v, b, j, kh), a.d, lane);
+    const T *k = row_of<const T>(a.k, b, j, kh), *v = row_of<const T>(a.v, b, j, kh);
     const int i0 = max(0, j - shift), i1 = last_position(a, j) - shift + 1;
     float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
     for (int h = kh * a.group; h < (kh + 1) * a.group; ++h) {
@@ -271,8 +265,8 @@ __device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int 
         each_keys(0, i0, i1, lane, [&](int i, bool have) {
             float w = 0.f, ds = 0.f;
             if (have) {
-                w = expf(a.scale * row_dot(mine, row_of<const T>(a.q, b, i, h), a.d) - lse[i]);
-                ds = w * (row_dot(mine + kMaxHeadDim, row_of<const T>(a.d_o, b, i, h), a.d) - stats[i].y) * a.scale;
+                w = expf(a.scale * row_dot(k, row_of<const T>(a.q, b, i, h), a.d) - lse[i]);
+                ds = w * (row_dot(v, row_of<const T>(a.d_o, b, i, h), a.d) - stats[i].y) * a.scale;
             }
             for (int x = 0; x < 32; ++x) {
                 const int ix = __shfl_sync(0xffffffffu, i, x);
