@@ -13,12 +13,14 @@
 //                S = Q K^T,   dP = dO V^T,   dq += dS K
 // That is seven products of a pair of tiles where one kernel with atomics needs five.
 //
-// In both, two warpgroups share a tile's columns, 64 each, a row a thread.  S^T and P^T
-// take turns in one place of tensor memory, dP^T and dS^T in another; the products are
-// issued so that one pair's run while the other's values are made:
-//     dv P^T(i), S^T(i + 1) under dS^T(i),   dk dS^T(i), dP^T(i + 1) under P^T(i + 1).
-// The dq kernel's S and dP are free as soon as they have been read (dS has two places of
-// its own), so S(j + 1) and dP(j + 1) run under dS(j).
+// In both, four warpgroups share a tile's columns, 32 each, a row a thread.  What bounds
+// them is the chain of waits, loads, exponentials and stores of a pair of tiles, so the
+// products of the next pair are issued as early as tensor memory allows:
+//   - the dq kernel's S and dP are free as soon as they have been read (dS has two places of
+//     its own);
+//   - so are S^T and dP^T for heads of 64, where P^T and dS^T have places of their own (2 x
+//     128 + 2 x 64 columns beside dk and dv);
+//   - for heads of 128, P^T and dS^T take the places of S^T and dP^T.
 //
 // As in the forward, a row that comes out infinite or NaN is computed again from the
 // definition.
@@ -30,7 +32,12 @@
 namespace basp_fp8 {
 namespace {
 
-constexpr int kBackThreads = 384;                             // 8 warps of values, one that loads, one that issues
+constexpr int kWays = 4, kCols = kTile / kWays;               // warpgroups of values, columns of each
+constexpr int kValueWarps = 4 * kWays, kLoadWarp = kValueWarps, kIssueWarp = kLoadWarp + 1, kTmemWarp = kLoadWarp + 2;
+constexpr int kBackThreads = 32 * kValueWarps + 128;
+
+// Whether P^T and dS^T have places of their own.
+template <int HD> constexpr bool kEarly = HD == 64;
 
 // DKV: of the kernel of dk and dv, which keeps queries' statistics too.
 template <int HD, bool DKV> struct BackSizes {
@@ -39,33 +46,36 @@ template <int HD, bool DKV> struct BackSizes {
     static constexpr int kStages = HD == 128 ? (DKV ? 4 : 5) : 8;
     static constexpr int kPlaces = DKV ? kStages / 2 + 1 : 0; // of statistics
     static constexpr int kStats = kTile * 8;                  // bytes of a tile of queries' statistics
-    static constexpr int kBarriers = 1 + 2 * kStages + 7;
+    static constexpr int kBarriers = 1 + 2 * kStages + 9;
     static constexpr int kSmem =
-        1024 + (2 + kStages) * kOperand + kPlaces * kStats + 8 * kBarriers + 16 + 32;
+        1024 + (2 + kStages) * kOperand + kPlaces * kStats + 8 * kBarriers + 16 + 4 * kValueWarps;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// A warp's 16-bit P or dS of 64 columns to tensor memory, and 64 columns from it.
-__device__ __forceinline__ void load64(uint32_t addr, uint32_t (&v)[64]) {
+// A warp's columns from tensor memory, and its 16-bit P or dS to it.
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[kCols]) {
     tmem_load32(addr, v);
-    tmem_load32(addr + 32, v + 32);
     tmem_load_wait();
     tmem_loaded32(v);
-    tmem_loaded32(v + 32);
 }
-template <class T> __device__ __forceinline__ void store64(uint32_t addr, const float (&v)[64]) {
-    uint32_t w[32];
+template <class T> __device__ __forceinline__ void store_columns(uint32_t addr, const float (&v)[kCols]) {
+    uint32_t w[kCols / 2];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
-    tmem_store32(addr, w);
+    for (int i = 0; i < kCols / 2; ++i) w[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
+    tmem_store16(addr, w);
     tmem_store_wait();
 }
-
 // 0 in the places whose bit is not set.
-__device__ __forceinline__ void keep(float (&v)[64], const uint32_t (&seen)[2]) {
+__device__ __forceinline__ void keep(float (&v)[kCols], uint32_t seen) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-        if (!(seen[i / 32] >> (i % 32) & 1u)) v[i] = 0.f;
+    for (int i = 0; i < kCols; ++i)
+        if (!(seen >> i & 1u)) v[i] = 0.f;
+}
+// What this warp read of tensor memory, or wrote to it, is behind it.
+__device__ __forceinline__ void pass_on(uint32_t bar) {
+    tcgen05_before_sync();
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
 template <class T, int HD>
@@ -80,13 +90,15 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     uint64_t *bars = reinterpret_cast<uint64_t *>(stats + SS * Z::kStats);
     const uint32_t kv_full = smem_addr(bars), full = kv_full + 8, empty = full + 8 * ST;
     const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8;
-    const uint32_t done = ds_ready + 8, drained = done + 8;
+    // where products are early: S and dP have been read, dS has been used
+    const uint32_t s_taken = ds_ready + 8, dp_taken = s_taken + 8, ds_used = dp_taken + 8;
+    const uint32_t done = ds_used + 8, drained = done + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    uint32_t *bad_rows = tmem_slot + 4;                       // [8 warps]
+    uint32_t *bad_rows = tmem_slot + 4;                       // [warps of values]
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    if (warp == 8 && lane == 0) {
+    if (warp == kLoadWarp && lane == 0) {
         mbar_init(kv_full, 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(full + 8 * s, 1);
@@ -94,15 +106,18 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(p_ready, 8);
-        mbar_init(ds_ready, 8);
+        mbar_init(p_ready, kValueWarps);
+        mbar_init(ds_ready, kValueWarps);
+        mbar_init(s_taken, kValueWarps);
+        mbar_init(dp_taken, kValueWarps);
+        mbar_init(ds_used, 1);
         mbar_init(done, 1);
         mbar_init(drained, 1);
         *abort = 0;
         fence_mbar_init();
         fence_async_shared();
     }
-    if (warp == 10) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    if (warp == kTmemWarp) tmem_alloc<1>(smem_addr(tmem_slot), 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -115,9 +130,12 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     const int k0 = int(blockIdx.x) / heads * kTile, shift = a.sk - a.sq;
     const QueryTiles tiles = query_tiles(a, k0);
     const int count = tiles.high - tiles.low, total = count * a.group;
-    const uint32_t dv_acc = tmem + 256, dk_acc = tmem + 256 + HD;
+    // S^T, dP^T, P^T and dS^T, dv and dk; each warpgroup's P and dS at a step of its own
+    const uint32_t p_at = kEarly<HD> ? tmem + 256 : tmem, ds_at = kEarly<HD> ? tmem + 320 : tmem + kTile;
+    constexpr int kStep = kEarly<HD> ? kCols / 2 : kCols;
+    const uint32_t dv_acc = tmem + 512 - 2 * HD, dk_acc = tmem + 512 - HD;
 
-    if (warp == 8) {                                          // loads
+    if (warp == kLoadWarp) {                                  // loads
         if (total > 0) {
             if (elect_one()) {
                 mbar_expect_tx(kv_full, 2 * Z::kOperand);
@@ -157,7 +175,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
             wait(kv_full, 0, false);
         }
-    } else if (warp == 9) {                                   // products
+    } else if (warp == kIssueWarp) {                          // products
         if (total > 0 && elect_one()) {
             const bool bf16 = std::is_same_v<T, __nv_bfloat16>;
             const int ksteps = (a.d + 15) / 16;
@@ -175,11 +193,11 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 }
                 mma_commit<1>(bar);
             };
-            // a product over the queries: P^T dO or dS^T Q, each warpgroup's 64 in its own place
+            // a product over the queries: P^T dO or dS^T Q
             auto across_queries = [&](uint32_t d, uint32_t x, uint32_t y, bool add) {
                 const uint64_t dy = desc_k_across(y, kBox);
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_f16_tmem(d, x + (k / 4) * 64 + (k % 4) * 8, dy + k * (16 * 128 / 16), io, add || k > 0);
+                    mma_f16_tmem(d, x + (k / 2) * kStep + (k % 2) * 8, dy + k * (16 * 128 / 16), io, add || k > 0);
             };
             auto take = [&]() {
                 ok = ok && wait(full + 8 * ring.at, ring.turn);
@@ -195,39 +213,42 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             }
             for (int i = 0; i < total && ok; ++i) {
                 const bool more = i + 1 < total;
-                ok = wait(p_ready, i & 1);
-                if (!ok) break;
-                tcgen05_after_sync();
-                across_queries(dv_acc, tmem, ring0 + o * Z::kOperand, i > 0);
-                mma_commit<1>(empty + 8 * o);
-                const uint32_t q_now = q;
-                if (more) {
-                    q = take();
-                    if (!ok) break;
+                const uint32_t q_now = q, o_now = o;
+                // the next pair's product, once its place is free
+                auto next = [&](uint32_t &at, uint32_t d, uint32_t x, uint32_t desc, uint32_t bar, uint32_t taken) {
+                    if (!more) return;
+                    at = take();
+                    if (kEarly<HD>) ok = ok && wait(taken, i & 1);
+                    if (!ok) return;
                     tcgen05_after_sync();
-                    across_head(tmem, k_at, ring0 + q * Z::kOperand, is, s_full);
-                }
-                ok = wait(ds_ready, i & 1);
+                    across_head(d, x, ring0 + at * Z::kOperand, desc, bar);
+                };
+                if (kEarly<HD>) next(q, tmem, k_at, is, s_full, s_taken);
+                ok = ok && wait(p_ready, i & 1);
                 if (!ok) break;
                 tcgen05_after_sync();
-                across_queries(dk_acc, tmem + kTile, ring0 + q_now * Z::kOperand, i > 0);
+                across_queries(dv_acc, p_at, ring0 + o_now * Z::kOperand, i > 0);
+                if (!kEarly<HD>) next(q, tmem, k_at, is, s_full, s_taken);
+                if (kEarly<HD>) next(o, tmem + kTile, v_at, idp, dp_full, dp_taken);
+                mma_commit<1>(empty + 8 * o_now);
+                ok = ok && wait(ds_ready, i & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                across_queries(dk_acc, ds_at, ring0 + q_now * Z::kOperand, i > 0);
+                if (kEarly<HD>) mma_commit<1>(ds_used);
                 mma_commit<1>(empty + 8 * q_now);
-                if (more) {
-                    o = take();
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, idp, dp_full);
-                }
+                if (!kEarly<HD>) next(o, tmem + kTile, v_at, idp, dp_full, dp_taken);
             }
             if (ok) mma_commit<1>(done);
             // nothing is in flight at the end
             mma_commit<1>(drained);
             wait(drained, 0, false);
         }
-    } else if (warp < 8) {                                    // values
-        const int half = warp / 4, quarter = warp % 4, key = k0 + quarter * 32 + lane;
+    } else if (warp < kValueWarps) {                          // values
+        const int way = warp / 4, quarter = warp % 4, key = k0 + quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kTile;
+        const uint32_t ts = tmem + lanes + kCols * way, tp = ts + kTile;
+        const uint32_t to_p = p_at + lanes + kStep * way, to_ds = ds_at + lanes + kStep * way;
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
         const int k1 = k0 + kTile - 1;
         bool ok = true;
@@ -241,51 +262,62 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             const int q0 = (tiles.low + i % count) * kTile, p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
             const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
             // columns of this warpgroup that see the key: [first, last]
-            const int at0 = q0 + 64 * half;
+            const int at0 = q0 + kCols * way;
             const int first = key - shift - at0, last = last_position(a, key) - shift - at0;
-            const uint32_t seen[2] = {bits_to(last) & ~bits_to(first - 1), bits_to(last - 32) & ~bits_to(first - 33)};
-            const float4 *st = reinterpret_cast<const float4 *>(stats + place.at * Z::kStats) + 32 * half;
-            uint32_t x[64];
-            float p[64];
-            load64(ts, x);
+            const uint32_t seen = bits_to(last) & ~bits_to(first - 1);
+            const float4 *st = reinterpret_cast<const float4 *>(stats + place.at * Z::kStats) + kCols / 2 * way;
+            uint32_t x[kCols];
+            float p[kCols];
+            load_columns(ts, x);
+            if (kEarly<HD>) pass_on(s_taken);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < kCols; e += 2) {
                 const float4 f = st[e / 2];                   // (lse, D) of two queries
                 p[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -f.x));
                 p[e + 1] = exp2_fast(fmaf(__uint_as_float(x[e + 1]), c, -f.z));
             }
             if (masked) keep(p, seen);
-            store64<T>(ts, p);
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready);
-            ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
-            if (!ok) break;
-            tcgen05_after_sync();
-            load64(tp, x);
+            if (kEarly<HD>) {
+                // dP(i) is made after dv P(i - 1): P's place is free then
+                ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
+                if (!ok) break;
+                tcgen05_after_sync();
+            }
+            store_columns<T>(to_p, p);
+            pass_on(p_ready);
+            if (!kEarly<HD>) {
+                ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
+                if (!ok) break;
+                tcgen05_after_sync();
+            }
+            load_columns(tp, x);
+            if (kEarly<HD>) pass_on(dp_taken);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < kCols; e += 2) {
                 const float4 f = st[e / 2];
                 p[e] *= __uint_as_float(x[e]) - f.y;
                 p[e + 1] *= __uint_as_float(x[e + 1]) - f.w;
             }
             if (masked) keep(p, seen);                        // 0 times an infinity
-            store64<T>(tp, p);
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_ready);
+            if (kEarly<HD> && i > 0) {
+                ok = __all_sync(0xffffffffu, wait(ds_used, (i - 1) & 1));
+                if (!ok) break;
+                tcgen05_after_sync();
+            }
+            store_columns<T>(to_ds, p);
+            pass_on(ds_ready);
         }
         if (total > 0) {
             ok = __all_sync(0xffffffffu, ok && wait(done, 0));
             tcgen05_after_sync();
         }
-        // one warpgroup stores dv, the other dk
+        // two warpgroups store dv, the others dk, every other 32 values of a row each
         const bool exists = key < a.sk;
-        const float f = half == 0 ? 1.f : a.scale;
-        const uint32_t acc = (half == 0 ? dv_acc : dk_acc) + lanes;
-        T *row = row_of<T>(half == 0 ? a.dv : a.dk, b, exists ? key : 0, kh);
+        const float f = way < 2 ? 1.f : a.scale;
+        const uint32_t acc = (way < 2 ? dv_acc : dk_acc) + lanes;
+        T *row = row_of<T>(way < 2 ? a.dv : a.dk, b, exists ? key : 0, kh);
         bool finite = true;
-        for (int i = 0; i < (a.d + 31) / 32; ++i) {
+        for (int i = way % 2; i < (a.d + 31) / 32; i += 2) {
             uint32_t v[32];
             if (total == 0) {
 #pragma unroll
@@ -314,16 +346,16 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         // rows that are no numbers, again from the definition: dk and dv of a row together
         const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
         if (lane == 0) bad_rows[warp] = bad;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
-        if (half == 0)
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps) : "memory");
+        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
+        if (way == 0)
             for (; again != 0; again &= again - 1)
                 dkv_row<T>(a, b, kh, k0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 10) tmem_free<1>(tmem, 512);
+    if (warp == kTmemWarp) tmem_free<1>(tmem, 512);
 }
 
 template <class T, int HD>
@@ -336,14 +368,14 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
     const uint32_t q_at = smem_addr(smem), o_at = q_at + Z::kOperand, ring0 = q_at + 2 * Z::kOperand;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + ST) * Z::kOperand);
     const uint32_t qo_full = smem_addr(bars), full = qo_full + 8, empty = full + 8 * ST;
-    const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, taken = dp_full + 8, ds_ready = taken + 8;
-    const uint32_t done = ds_ready + 16, drained = done + 8;
+    const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, s_taken = dp_full + 8, dp_taken = s_taken + 8;
+    const uint32_t ds_ready = dp_taken + 8, done = ds_ready + 16, drained = done + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     uint32_t *bad_rows = tmem_slot + 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    if (warp == 8 && lane == 0) {
+    if (warp == kLoadWarp && lane == 0) {
         mbar_init(qo_full, 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(full + 8 * s, 1);
@@ -351,18 +383,19 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(taken, 8);
+        mbar_init(s_taken, kValueWarps);
+        mbar_init(dp_taken, kValueWarps);
         // one for each place of dS: the next pair's can be complete before this one's is
         // asked for, and a barrier tells only two phases in a row apart
-        mbar_init(ds_ready, 8);
-        mbar_init(ds_ready + 8, 8);
+        mbar_init(ds_ready, kValueWarps);
+        mbar_init(ds_ready + 8, kValueWarps);
         mbar_init(done, 1);
         mbar_init(drained, 1);
         *abort = 0;
         fence_mbar_init();
         fence_async_shared();
     }
-    if (warp == 10) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    if (warp == kTmemWarp) tmem_alloc<1>(smem_addr(tmem_slot), 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -379,7 +412,7 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
     // S, dP, two places of dS (64 columns each), dq
     const uint32_t dq_acc = tmem + 384, ds_at = tmem + 256;
 
-    if (warp == 8) {                                          // loads
+    if (warp == kLoadWarp) {                                  // loads
         if (total > 0) {
             if (elect_one()) {
                 mbar_expect_tx(qo_full, 2 * Z::kOperand);
@@ -411,7 +444,7 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
             wait(qo_full, 0, false);
         }
-    } else if (warp == 9) {                                   // products
+    } else if (warp == kIssueWarp) {                          // products
         if (total > 0 && elect_one()) {
             const bool bf16 = std::is_same_v<T, __nv_bfloat16>;
             const int ksteps = (a.d + 15) / 16;
@@ -435,29 +468,26 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
                 mma_commit<1>(bar);
             };
             uint32_t k_now = 0;
-            // S and dP of a pair of tiles; V's place is free then
-            auto scores = [&]() {
+            // S and dP of a pair of tiles, each once its place has been read; V's place is
+            // free then
+            auto scores = [&](int i) {
                 k_now = take();
+                if (i > 0) ok = ok && wait(s_taken, (i - 1) & 1);
                 if (!ok) return;
                 tcgen05_after_sync();
                 across_head(tmem, q_at, ring0 + k_now * Z::kOperand, is, s_full);
                 const uint32_t v_now = take();
+                if (i > 0) ok = ok && wait(dp_taken, (i - 1) & 1);
                 if (!ok) return;
                 tcgen05_after_sync();
                 across_head(tmem + kTile, o_at, ring0 + v_now * Z::kOperand, idp, dp_full);
                 mma_commit<1>(empty + 8 * v_now);
             };
-            scores();
+            scores(0);
             for (int i = 0; i < total && ok; ++i) {
                 const uint32_t k_place = k_now;
-                if (i + 1 < total) {
-                    ok = wait(taken, i & 1);                  // S and dP of this pair have been read
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    scores();
-                    if (!ok) break;
-                }
-                ok = wait(ds_ready + 8 * (i & 1), (i >> 1) & 1);
+                if (i + 1 < total) scores(i + 1);
+                ok = ok && wait(ds_ready + 8 * (i & 1), (i >> 1) & 1);
                 if (!ok) break;
                 tcgen05_after_sync();
                 const uint64_t dk = desc_k_across(ring0 + k_place * Z::kOperand, kBox);
@@ -469,11 +499,11 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             mma_commit<1>(drained);
             wait(drained, 0, false);
         }
-    } else if (warp < 8) {                                    // values
-        const int half = warp / 4, quarter = warp % 4, row = q0 + quarter * 32 + lane, p = row + shift;
+    } else if (warp < kValueWarps) {                          // values
+        const int way = warp / 4, quarter = warp % 4, row = q0 + quarter * 32 + lane, p = row + shift;
         const int p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kTile;
+        const uint32_t ts = tmem + lanes + kCols * way, tp = ts + kTile;
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
         const bool exists = row < a.sq;
         const float2 st = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + row];     // row < sq_pad
@@ -483,43 +513,39 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
             if (!ok) break;
             tcgen05_after_sync();
-            const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + 64 * half;
+            const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + kCols * way;
             const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
             const int last = p - at0, after = p - a.window - at0, sink = a.sinks - at0;
-            uint32_t x[64];
-            float ds[64];
-            load64(ts, x);
+            uint32_t x[kCols];
+            float ds[kCols];
+            load_columns(ts, x);
+            pass_on(s_taken);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) ds[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -st.x));
+            for (int e = 0; e < kCols; ++e) ds[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -st.x));
             ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
             if (!ok) break;
             tcgen05_after_sync();
-            load64(tp, x);
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(taken);
+            load_columns(tp, x);
+            pass_on(dp_taken);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) ds[e] *= __uint_as_float(x[e]) - st.y;
+            for (int e = 0; e < kCols; ++e) ds[e] *= __uint_as_float(x[e]) - st.y;
             if (masked) {
-                const uint32_t seen[2] = {bits_to(last) & (~bits_to(after) | bits_to(sink - 1)),
-                                          bits_to(last - 32) & (~bits_to(after - 32) | bits_to(sink - 33))};
+                const uint32_t seen = bits_to(last) & (~bits_to(after) | bits_to(sink - 1));
                 keep(ds, seen);
             }
-            // the place's last product is done: S(j) was issued after it
-            store64<T>(ds_at + lanes + (i & 1) * 64 + 32 * half, ds);
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_ready + 8 * (i & 1));
+            // the place's last product is done: dP(i) was issued after it
+            store_columns<T>(ds_at + lanes + (i & 1) * 64 + kCols / 2 * way, ds);
+            pass_on(ds_ready + 8 * (i & 1));
         }
         if (total > 0) {
             ok = __all_sync(0xffffffffu, ok && wait(done, 0));
             tcgen05_after_sync();
         }
-        // the warpgroups store the halves of each row
+        // each warpgroup stores 32 values of a row
         T *to = row_of<T>(a.dq, b, exists ? row : 0, h);
         bool finite = true;
         const int chunks = (a.d + 31) / 32;
-        for (int y = half; y < chunks; y += 2) {
+        for (int y = way; y < chunks; y += kWays) {
             uint32_t v[32];
             if (total == 0) {
 #pragma unroll
@@ -547,16 +573,16 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         }
         const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
         if (lane == 0) bad_rows[warp] = bad;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4];
-        if (half == 0)
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps) : "memory");
+        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
+        if (way == 0)
             for (; again != 0; again &= again - 1)
                 dq_row<T>(a, b, h, q0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 10) tmem_free<1>(tmem, 512);
+    if (warp == kTmemWarp) tmem_free<1>(tmem, 512);
 }
 
 template <class T, int HD> basp_status go(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
