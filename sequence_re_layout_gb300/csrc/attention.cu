@@ -66,8 +66,22 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
         for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
         if (threadIdx.x % LANES == 0) {
             const bool sees = i < a.sq && i + a.sk - a.sq >= 0;
-            a.stats[int64_t(head) * a.sq_pad + i] =
-                sees ? make_float2(a.lse[int64_t(head) * a.sq + i] * kLog2e, s) : make_float2(INFINITY, 0.f);
+            const float lse = sees ? a.lse[int64_t(head) * a.sq + i] * kLog2e : 0.f;
+            a.stats[int64_t(head) * a.sq_pad + i] = sees ? make_float2(lse, s) : make_float2(INFINITY, 0.f);
+            // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that
+            // the rows that meet it are made from the definition
+            const float sign = a.scale < 0.f ? 1.f : -1.f;        // the other side of the product is negated
+            float part[8], rest = sees ? sign * lse / score_scale(a.scale) / kFoldLse<T> : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j == 4) rest = sees ? -s : 0.f;
+                part[j] = Elem<T>::to_float(Elem<T>::from_float(rest));
+                if (!(fabsf(part[j]) < INFINITY)) part[j] = __uint_as_float(0x7fffffffu);
+                rest -= part[j];
+            }
+            uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32;
+            *reinterpret_cast<uint4 *>(to + fold_offset(i - tile * kTile, 0)) = Pack<T>::pack(part);
+            *reinterpret_cast<uint4 *>(to + fold_offset(i - tile * kTile, 1)) = make_uint4(0, 0, 0, 0);
         }
     }
 }
@@ -267,7 +281,7 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
 extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
     basp_status st;
     if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
-    return desc->batch * desc->q_heads * ceil_div(desc->q_len, kTile) * kTile * int64_t(sizeof(float2));
+    return desc->batch * desc->q_heads * ceil_div(desc->q_len, kTile) * kTile * (int64_t(sizeof(float2)) + 32);
 }
 
 extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
@@ -301,8 +315,9 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o); a.d_o = heads_of(d_o);
     a.dq = heads_of(dq); a.dk = heads_of(dk); a.dv = heads_of(dv);
     a.lse = const_cast<float *>(lse);
-    a.stats = static_cast<float2 *>(workspace);
     a.sq_pad = int(ceil_div(a.sq, kTile) * kTile);
+    a.stats = static_cast<float2 *>(workspace);
+    a.fold = reinterpret_cast<uint16_t *>(a.stats + int64_t(a.batch) * a.hq * a.sq_pad);
     const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq);
     HeadMaps m = {};
     if (tiles && (!encode_qkv(a, &m) || !encode(a, a.d_o, a.sq, a.hq, kTile, &m.d_o, &m.do_head, &m.do_batch)))

@@ -22,6 +22,11 @@
 //     128 + 2 x 64 columns beside dk and dv);
 //   - for heads of 128, P^T and dS^T take the places of S^T and dP^T.
 //
+// In the dkv kernel lse and D vary along a row.  They are taken off inside the products,
+// by 16 more of K: each query's row has -lse / c and -D there, in four 16-bit parts each,
+// and the keys' side has ones (64 for fp16's lse, whose range is small) where they belong.
+// As loads from shared memory, a value each, they took 1200 of 3000 cycles a pair of tiles.
+//
 // As in the forward, a row that comes out infinite or NaN is computed again from the
 // definition.
 #include <cuda.h>
@@ -44,11 +49,11 @@ template <int HD, bool DKV> struct BackSizes {
     static constexpr int kBoxes = HD / 64;
     static constexpr int kOperand = kBoxes * kBox;            // bytes of a tile of Q, K, V or dO
     static constexpr int kStages = HD == 128 ? (DKV ? 4 : 5) : 8;
-    static constexpr int kPlaces = DKV ? kStages / 2 + 1 : 0; // of statistics
-    static constexpr int kStats = kTile * 8;                  // bytes of a tile of queries' statistics
+    static constexpr int kPlaces = DKV ? kStages / 2 + 1 : 0; // of the queries' lse and D
+    static constexpr int kFold = kFoldBytes;                  // of a tile's 16 more of K
     static constexpr int kBarriers = 1 + 2 * kStages + 9;
     static constexpr int kSmem =
-        1024 + (2 + kStages) * kOperand + kPlaces * kStats + 8 * kBarriers + 16 + 4 * kValueWarps;
+        1024 + (2 + kStages) * kOperand + (kPlaces + (DKV ? 2 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -86,8 +91,9 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     const uint32_t k_at = smem_addr(smem), v_at = k_at + Z::kOperand, ring0 = k_at + 2 * Z::kOperand;
-    uint8_t *stats = smem + (2 + ST) * Z::kOperand;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(stats + SS * Z::kStats);
+    uint8_t *ones = smem + (2 + ST) * Z::kOperand;            // the keys' side of lse, of D
+    const uint32_t ones_at = smem_addr(ones), fold0 = ones_at + 2 * Z::kFold;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + (2 + SS) * Z::kFold);
     const uint32_t kv_full = smem_addr(bars), full = kv_full + 8, empty = full + 8 * ST;
     const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8;
     // where products are early: S and dP have been read, dS has been used
@@ -118,6 +124,14 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         fence_async_shared();
     }
     if (warp == kTmemWarp) tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    if (threadIdx.x < 2 * kTile) {
+        const int row = threadIdx.x % kTile, of_d = threadIdx.x / kTile;
+        const uint32_t w = pack_pair<T>(of_d ? 1.f : kFoldLse<T>, of_d ? 1.f : kFoldLse<T>);
+        uint4 *to = reinterpret_cast<uint4 *>(ones + of_d * Z::kFold + fold_offset(row, 0));
+        to[0] = of_d ? make_uint4(0, 0, w, w) : make_uint4(w, w, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + of_d * Z::kFold + fold_offset(row, 1)) = make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+    }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -151,18 +165,18 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             Turn<SS> place;
             for (int i = 0; i < total && ok; ++i) {
                 const int h = kh * a.group + i / count, q = (tiles.low + i % count) * kTile;
-                for (int x = 0; x < 2 && ok; ++x) {           // Q and its statistics, dO
+                for (int x = 0; x < 2 && ok; ++x) {           // Q and its lse and D, dO
                     ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
                     if (!ok) break;
                     if (elect_one()) {
                         const uint32_t to = ring0 + ring.at * Z::kOperand, bar = full + 8 * ring.at;
-                        mbar_expect_tx(bar, Z::kOperand + (x == 0 ? Z::kStats : 0));
+                        mbar_expect_tx(bar, Z::kOperand + (x == 0 ? Z::kFold : 0));
                         for (int y = 0; y < Z::kBoxes; ++y)
                             tma_load_4d(to + y * kBox, x == 0 ? &m.q : &m.d_o, 64 * y, q, h * (x == 0 ? m.q_head : m.do_head),
                                         b * (x == 0 ? m.q_batch : m.do_batch), bar);
                         if (x == 0)
-                            bulk_load(smem_addr(stats) + place.at * Z::kStats,
-                                      a.stats + (int64_t(b) * a.hq + h) * a.sq_pad + q, Z::kStats, bar);
+                            bulk_load(fold0 + place.at * Z::kFold,
+                                      a.fold + ((int64_t(b) * a.hq + h) * a.sq_pad + q) * 16, Z::kFold, bar);
                     }
                     __syncwarp();
                     ring.next();
@@ -184,13 +198,14 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             const uint32_t io = mma_f16_desc(kTile, ksteps * 16, bf16, false, true);
             Turn<ST> ring;
             bool ok = wait(kv_full, 0);
-            // a 128 x 128 product over the head: S^T or dP^T
-            auto across_head = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t desc, uint32_t bar) {
+            // a 128 x 128 product over the head, S^T or dP^T, and over the 16 more of K
+            auto across_head = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ones, uint32_t fold, uint32_t desc, uint32_t bar) {
                 const uint64_t dx = desc_k_major(x), dy = desc_k_major(y);
                 for (int k = 0; k < ksteps; ++k) {
                     const uint32_t at = (k / 4) * (kBox / 16) + (k % 4) * 2;
                     mma_f16(d, dx + at, dy + at, desc, k > 0);
                 }
+                mma_f16(d, desc_plain(ones, 128, 256), desc_plain(fold, 128, 256), desc, true);
                 mma_commit<1>(bar);
             };
             // a product over the queries: P^T dO or dS^T Q
@@ -206,30 +221,33 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 return at;
             };
             uint32_t q = take(), o = take();
+            Turn<SS> of_s, of_dp;                             // places of lse and D
             if (ok) {
                 tcgen05_after_sync();
-                across_head(tmem, k_at, ring0 + q * Z::kOperand, is, s_full);
-                across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, idp, dp_full);
+                across_head(tmem, k_at, ring0 + q * Z::kOperand, ones_at, fold0, is, s_full);
+                across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, ones_at + Z::kFold, fold0, idp, dp_full);
             }
             for (int i = 0; i < total && ok; ++i) {
                 const bool more = i + 1 < total;
                 const uint32_t q_now = q, o_now = o;
                 // the next pair's product, once its place is free
-                auto next = [&](uint32_t &at, uint32_t d, uint32_t x, uint32_t desc, uint32_t bar, uint32_t taken) {
+                auto next = [&](uint32_t &at, Turn<SS> &place, uint32_t d, uint32_t x, uint32_t ones, uint32_t desc, uint32_t bar,
+                                uint32_t taken) {
                     if (!more) return;
                     at = take();
+                    place.next();
                     if (kEarly<HD>) ok = ok && wait(taken, i & 1);
                     if (!ok) return;
                     tcgen05_after_sync();
-                    across_head(d, x, ring0 + at * Z::kOperand, desc, bar);
+                    across_head(d, x, ring0 + at * Z::kOperand, ones, fold0 + place.at * Z::kFold, desc, bar);
                 };
-                if (kEarly<HD>) next(q, tmem, k_at, is, s_full, s_taken);
+                if (kEarly<HD>) next(q, of_s, tmem, k_at, ones_at, is, s_full, s_taken);
                 ok = ok && wait(p_ready, i & 1);
                 if (!ok) break;
                 tcgen05_after_sync();
                 across_queries(dv_acc, p_at, ring0 + o_now * Z::kOperand, i > 0);
-                if (!kEarly<HD>) next(q, tmem, k_at, is, s_full, s_taken);
-                if (kEarly<HD>) next(o, tmem + kTile, v_at, idp, dp_full, dp_taken);
+                if (!kEarly<HD>) next(q, of_s, tmem, k_at, ones_at, is, s_full, s_taken);
+                if (kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, ones_at + Z::kFold, idp, dp_full, dp_taken);
                 mma_commit<1>(empty + 8 * o_now);
                 ok = ok && wait(ds_ready, i & 1);
                 if (!ok) break;
@@ -237,7 +255,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 across_queries(dk_acc, ds_at, ring0 + q_now * Z::kOperand, i > 0);
                 if (kEarly<HD>) mma_commit<1>(ds_used);
                 mma_commit<1>(empty + 8 * q_now);
-                if (!kEarly<HD>) next(o, tmem + kTile, v_at, idp, dp_full, dp_taken);
+                if (!kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, ones_at + Z::kFold, idp, dp_full, dp_taken);
             }
             if (ok) mma_commit<1>(done);
             // nothing is in flight at the end
@@ -249,32 +267,30 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + kCols * way, tp = ts + kTile;
         const uint32_t to_p = p_at + lanes + kStep * way, to_ds = ds_at + lanes + kStep * way;
-        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
-        const int k1 = k0 + kTile - 1;
+        const float c = score_scale(a.scale);
+        const float2 c2 = make_float2(c, c);
+        const int k1 = k0 + kTile - 1, seen_by = last_position(a, key) - shift;
         bool ok = true;
-        Turn<SS> place;
-        Turn<ST> ring;
-        for (int i = 0; i < total; ++i, place.next(), ring.next(), ring.next()) {
-            // the statistics came with Q
-            ok = __all_sync(0xffffffffu, wait(full + 8 * ring.at, ring.turn) && wait(s_full, i & 1));
+        int q0 = tiles.low * kTile;
+        for (int i = 0; i < total; ++i, q0 = q0 + kTile < tiles.high * kTile ? q0 + kTile : tiles.low * kTile) {
+            ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
             if (!ok) break;
             tcgen05_after_sync();
-            const int q0 = (tiles.low + i % count) * kTile, p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
-            const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
-            // columns of this warpgroup that see the key: [first, last]
-            const int at0 = q0 + kCols * way;
-            const int first = key - shift - at0, last = last_position(a, key) - shift - at0;
-            const uint32_t seen = bits_to(last) & ~bits_to(first - 1);
-            const float4 *st = reinterpret_cast<const float4 *>(stats + place.at * Z::kStats) + kCols / 2 * way;
-            uint32_t x[kCols];
+            // not all keys are seen by all queries, or some queries do not exist
+            const bool masked = !(k1 <= q0 + shift && (k0 > q0 + kTile - 1 + shift - a.window || k1 < a.sinks)) || q0 + kTile > a.sq;
+            uint32_t x[kCols], seen = 0xffffffffu;
             float p[kCols];
             load_columns(ts, x);
             if (kEarly<HD>) pass_on(s_taken);
 #pragma unroll
             for (int e = 0; e < kCols; e += 2) {
-                const float4 f = st[e / 2];                   // (lse, D) of two queries
-                p[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -f.x));
-                p[e + 1] = exp2_fast(fmaf(__uint_as_float(x[e + 1]), c, -f.z));
+                const float2 f = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2);
+                p[e] = exp2_fast(f.x);
+                p[e + 1] = exp2_fast(f.y);
+            }
+            if (masked) {                                     // this warpgroup's columns that see the key
+                const int at0 = q0 + kCols * way;
+                seen = bits_to(seen_by - at0) & ~bits_to(key - shift - at0 - 1);
             }
             if (masked) keep(p, seen);
             if (kEarly<HD>) {
@@ -294,9 +310,9 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             if (kEarly<HD>) pass_on(dp_taken);
 #pragma unroll
             for (int e = 0; e < kCols; e += 2) {
-                const float4 f = st[e / 2];
-                p[e] *= __uint_as_float(x[e]) - f.y;
-                p[e + 1] *= __uint_as_float(x[e + 1]) - f.w;
+                const float2 f = mul2(make_float2(p[e], p[e + 1]), make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                p[e] = f.x;
+                p[e + 1] = f.y;
             }
             if (masked) keep(p, seen);                        // 0 times an infinity
             if (kEarly<HD> && i > 0) {
@@ -504,9 +520,10 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         const int p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + kCols * way, tp = ts + kTile;
-        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);
+        const float c = score_scale(a.scale);
         const bool exists = row < a.sq;
         const float2 st = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + row];     // row < sq_pad
+        const float2 c2 = make_float2(c, c), lse2 = make_float2(-st.x, -st.x), d2 = make_float2(-st.y, -st.y);
         bool ok = true;
         int i = 0;
         for (int j = tiles.begin(); j < tiles.high; j = tiles.next(j), ++i) {
@@ -515,22 +532,30 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             tcgen05_after_sync();
             const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + kCols * way;
             const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
-            const int last = p - at0, after = p - a.window - at0, sink = a.sinks - at0;
             uint32_t x[kCols];
             float ds[kCols];
             load_columns(ts, x);
             pass_on(s_taken);
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) ds[e] = exp2_fast(fmaf(__uint_as_float(x[e]), c, -st.x));
+            for (int e = 0; e < kCols; e += 2) {
+                const float2 f = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, lse2);
+                ds[e] = exp2_fast(f.x);
+                ds[e + 1] = exp2_fast(f.y);
+            }
             ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
             if (!ok) break;
             tcgen05_after_sync();
             load_columns(tp, x);
             pass_on(dp_taken);
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) ds[e] *= __uint_as_float(x[e]) - st.y;
+            for (int e = 0; e < kCols; e += 2) {
+                const float2 f = mul2(make_float2(ds[e], ds[e + 1]),
+                                      add2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), d2));
+                ds[e] = f.x;
+                ds[e + 1] = f.y;
+            }
             if (masked) {
-                const uint32_t seen = bits_to(last) & (~bits_to(after) | bits_to(sink - 1));
+                const uint32_t seen = bits_to(p - at0) & (~bits_to(p - a.window - at0) | bits_to(a.sinks - 1 - at0));
                 keep(ds, seen);
             }
             // the place's last product is done: dP(i) was issued after it

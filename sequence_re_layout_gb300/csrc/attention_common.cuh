@@ -23,9 +23,10 @@ template <class T> __device__ __forceinline__ T *row_of(const Heads &t, int64_t 
 struct AttentionArgs {
     Heads q, k, v, o, d_o, dq, dk, dv;
     float *lse;                          // [batch][Hq][Sq]
-    // for the backward: (lse log2(e), D) of each query, [batch][Hq][sq_pad]; what a pair
-    // of a query that does not exist, or sees nothing, is: (infinity, 0)
+    // for the backward: (lse log2(e), D) of each query, [batch][Hq][sq_pad]; of one that
+    // does not exist, or sees nothing: (infinity, 0)
     float2 *stats;
+    uint16_t *fold;                      // the same as parts of a product, [batch][Hq][sq_pad][16]
     int batch, sq, sk, sq_pad, hq, hkv, d, group;
     int window, sinks;                   // window: sk where all is visible
     float scale;
@@ -67,6 +68,18 @@ __device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &a, int k0
 
 // Bits 0 to n of a word.
 __device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u; }
+
+// What scores are multiplied by before 2^x (a negative scale negates one operand); a scale
+// of 0 leaves all scores alike.
+__device__ __forceinline__ float score_scale(float scale) { return fmaxf(fabsf(scale) * kLog2e, 0x1p-64f); }
+
+// 16 values of K for each of 128 rows, as 16 bytes x 8 rows next to each other: the 8
+// values of half k of a row begin at this byte.
+constexpr int kFoldBytes = kTile * 32;
+__host__ __device__ __forceinline__ constexpr int fold_offset(int row, int k) { return row / 8 * 256 + k * 128 + row % 8 * 16; }
+// lse / c can be beyond fp16's range: its parts are divided by this, which the other side
+// of the product has instead of ones.
+template <class T> constexpr float kFoldLse = std::is_same_v<T, __half> ? 64.f : 1.f;
 
 // A wait on one of the CTA's barriers, with a limit.
 constexpr uint64_t kAttentionWaitNs = 2000000000ull;

@@ -308,6 +308,12 @@ __device__ __forceinline__ uint64_t desc_k_across(uint32_t addr, uint32_t box_by
     return (uint64_t(kOperandDescHigh) << 32) | ((addr & 0x3ffff) >> 4) | ((box_bytes >> 4) << 16);
 }
 
+// Without a swizzle: pieces of 8 rows x 16 bytes, `k_bytes` apart along K and `row_bytes`
+// across.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr, uint32_t k_bytes, uint32_t row_bytes) {
+    return (uint64_t((row_bytes >> 4) | (1u << 14)) << 32) | ((addr & 0x3ffff) >> 4) | ((k_bytes >> 4) << 16);
+}
+
 // Instruction descriptor of kind::f16: M x N, both operands bf16 or both fp16, a
 // 32-bit result; A negated; B's K across its rows.
 __host__ __device__ constexpr uint32_t mma_f16_desc(int M, int N, bool bf16, bool negate_a, bool b_across) {
