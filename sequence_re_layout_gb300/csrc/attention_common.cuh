@@ -117,6 +117,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The largest of three, a NaN not counted.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 template <class T> __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     if constexpr (std::is_same_v<T, __nv_bfloat16>) {
         const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);

@@ -326,51 +326,44 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
                 for (int i = 0; i < kTile; i += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        high[e] = fmaxf(fmaxf(high[e], __uint_as_float(s[i + 2 * e])), __uint_as_float(s[i + 2 * e + 1]));
+                        high[e] = max3(high[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
                 high[0] = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+                const bool grown = !begun || (high[0] - top) * c > 8.f;
+                const bool again = __any_sync(0xffffffffu, begun && grown);      // O is multiplied
+                const float f = grown ? exp2_fast((top - high[0]) * c) : 1.f;
+                if (grown) top = high[0];
+                if (again) l *= f;
+                begun = true;
+                const float shift = top == -INFINITY ? 0.f : -top * c;
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                // P takes the place of S in registers too, until its place in tensor memory is free
+#pragma unroll
+                for (int i = 0; i < kTile / 2; ++i) {
+                    float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, shift2);
+                    x.x = exp2_fast(x.x);
+                    x.y = exp2_fast(x.y);
+                    if (i % 2) sum1 = add2(sum1, x);
+                    else sum0 = add2(sum0, x);
+                    s[i] = pack_pair<T>(x.x, x.y);
+                }
                 if constexpr (EARLY) {                        // P's place and O are free
                     if (n > 0) ok = __all_sync(0xffffffffu, wait(pv_done + 8 * t, (n - 1) & 1));
                     if (!ok) break;
                     tcgen05_after_sync();
                 }
-                if (!begun) {
-                    top = high[0];
-                    begun = true;
-                } else {
-                    const bool grown = (high[0] - top) * c > 8.f;
-                    if (__any_sync(0xffffffffu, grown)) {
-                        const float f = grown ? exp2_fast((top - high[0]) * c) : 1.f;
-                        if (grown) top = high[0];
-                        l *= f;
-                        for (int i = 0; i < ochunks; ++i) {
-                            uint32_t o[32];
-                            tmem_load32(to + 32 * i, o);
-                            tmem_load_wait();
-                            tmem_loaded32(o);
+                if (again)
+                    for (int i = 0; i < ochunks; ++i) {
+                        uint32_t o[32];
+                        tmem_load32(to + 32 * i, o);
+                        tmem_load_wait();
+                        tmem_loaded32(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_store32(to + 32 * i, o);
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_store32(to + 32 * i, o);
                     }
-                }
-                const float shift = top == -INFINITY ? 0.f : -top * c;
-                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int e = 64 * half + 2 * i;
-                        float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, shift2);
-                        x.x = exp2_fast(x.x);
-                        x.y = exp2_fast(x.y);
-                        if (i % 2) sum1 = add2(sum1, x);
-                        else sum0 = add2(sum0, x);
-                        v[i] = pack_pair<T>(x.x, x.y);
-                    }
-                    tmem_store32(tp + 32 * half, v);
-                }
+                tmem_store32(tp, s);
+                tmem_store32(tp + 32, s + 32);
                 l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                 tmem_store_wait();
                 tcgen05_before_sync();
