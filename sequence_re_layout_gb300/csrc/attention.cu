@@ -278,10 +278,17 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
     return with_type(desc->dtype, [&](auto t) { return launch_rows<decltype(t), kForward>(a, stream); });
 }
 
+// The statistics and their parts for the products, a multiple of 1024 bytes.
+static int64_t fold_bytes(const AttentionArgs &a) {
+    return int64_t(a.batch) * a.hq * ceil_div(a.sq, kTile) * kTile * (int64_t(sizeof(float2)) + 32);
+}
+
 extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
     basp_status st;
     if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
-    return desc->batch * desc->q_heads * ceil_div(desc->q_len, kTile) * kTile * (int64_t(sizeof(float2)) + 32);
+    if (desc->batch == 0 || desc->q_heads == 0) return 0;
+    const AttentionArgs a = args_of(desc);
+    return fold_bytes(a) + key_split_bytes(a, key_split(a));
 }
 
 extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
@@ -325,7 +332,11 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     return with_type(desc->dtype, [&](auto t) {
         using T = decltype(t);
         basp_status s = launch_stats<T>(a, stream);
-        if (s == BASP_OK && tiles) return launch_attention_backward(a, m, desc->dtype == BASP_DTYPE_BF16, stream);
+        if (s == BASP_OK && tiles) {
+            KeySplit split = key_split(a);
+            split.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + fold_bytes(a));
+            return launch_attention_backward(a, m, split, desc->dtype == BASP_DTYPE_BF16, stream);
+        }
         if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);
         if (s == BASP_OK) s = launch_rows<T, kDkv>(a, stream);
         return s;

@@ -27,9 +27,15 @@
 // and the keys' side has ones (64 for fp16's lse, whose range is small) where they belong.
 // As loads from shared memory, a value each, they took 1200 of 3000 cycles a pair of tiles.
 //
+// Where key tiles differ much in work (the sinks' keys are seen by every query, a causal
+// mask's first ones by most), or there are few, several CTAs share the longest ones: their
+// sums go to memory and another kernel adds them in order.
+//
 // As in the forward, a row that comes out infinite or NaN is computed again from the
 // definition.
 #include <cuda.h>
+
+#include <algorithm>
 
 #include "attention.cuh"
 #include "attention_common.cuh"
@@ -85,7 +91,8 @@ __device__ __forceinline__ void pass_on(uint32_t bar) {
 
 template <class T, int HD>
 __global__ void __launch_bounds__(kBackThreads, 1)
-attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m) {
+attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m,
+                     const __grid_constant__ KeySplit split) {
     using Z = BackSizes<HD, true>;
     constexpr int ST = Z::kStages, SS = Z::kPlaces;
     extern __shared__ uint8_t smem_raw[];
@@ -141,9 +148,15 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
 
     const int heads = a.batch * a.hkv;
     const int kh = int(blockIdx.x) % heads % a.hkv, b = int(blockIdx.x) % heads / a.hkv;
-    const int k0 = int(blockIdx.x) / heads * kTile, shift = a.sk - a.sq;
+    const int unit = int(blockIdx.x) / heads, shared = split.first[split.tiles], shift = a.sk - a.sq;
+    int tile = split.tiles + unit - shared;
+    if (unit < shared)
+        for (tile = 0; split.first[tile + 1] <= unit;) ++tile;
+    const int k0 = tile * kTile;
     const QueryTiles tiles = query_tiles(a, k0);
-    const int count = tiles.high - tiles.low, total = count * a.group;
+    // pairs [begin, begin + total) of the tile's with each query tile of each head
+    const int count = tiles.high - tiles.low, begin = unit < shared ? (unit - split.first[tile]) * split.chunk : 0;
+    const int total = unit < shared ? min(split.chunk, count * a.group - begin) : count * a.group;
     // S^T, dP^T, P^T and dS^T, dv and dk; each warpgroup's P and dS at a step of its own
     const uint32_t p_at = kEarly<HD> ? tmem + 256 : tmem, ds_at = kEarly<HD> ? tmem + 320 : tmem + kTile;
     constexpr int kStep = kEarly<HD> ? kCols / 2 : kCols;
@@ -164,7 +177,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             Turn<ST> ring;
             Turn<SS> place;
             for (int i = 0; i < total && ok; ++i) {
-                const int h = kh * a.group + i / count, q = (tiles.low + i % count) * kTile;
+                const int h = kh * a.group + (begin + i) / count, q = (tiles.low + (begin + i) % count) * kTile;
                 for (int x = 0; x < 2 && ok; ++x) {           // Q and its lse and D, dO
                     ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
                     if (!ok) break;
@@ -271,7 +284,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         const float2 c2 = make_float2(c, c);
         const int k1 = k0 + kTile - 1, seen_by = last_position(a, key) - shift;
         bool ok = true;
-        int q0 = tiles.low * kTile;
+        int q0 = (tiles.low + (total > 0 ? begin % count : 0)) * kTile;
         for (int i = 0; i < total; ++i, q0 = q0 + kTile < tiles.high * kTile ? q0 + kTile : tiles.low * kTile) {
             ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
             if (!ok) break;
@@ -328,6 +341,9 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             tcgen05_after_sync();
         }
         // two warpgroups store dv, the others dk, every other 32 values of a row each
+        float *part = nullptr;
+        if (unit < shared)
+            part = split.partial + ((int64_t(blockIdx.x) * 2 + way / 2) * kTile + quarter * 32 + lane) * HD;
         const bool exists = key < a.sk;
         const float f = way < 2 ? 1.f : a.scale;
         const uint32_t acc = (way < 2 ? dv_acc : dk_acc) + lanes;
@@ -345,6 +361,12 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+            }
+            if (part != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(part + 32 * i + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                continue;
             }
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -610,22 +632,93 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
     if (warp == kTmemWarp) tmem_free<1>(tmem, 512);
 }
 
-template <class T, int HD> basp_status go(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
-    constexpr auto dq = attention_dq_kernel<T, HD>, dkv = attention_dkv_kernel<T, HD>;
+// dv and dk of the shared tiles: a warp a row, four values a lane, the parts in their order.
+template <class T, int HD>
+__global__ void __launch_bounds__(256) key_join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ KeySplit split) {
+    grid_dependency();
+    const int heads = a.batch * a.hkv, lane = threadIdx.x % 32;
+    const int64_t row = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int at = int(row % kTile), head = int(row / kTile % heads), tile = int(row / kTile / heads), key = tile * kTile + at;
+    if (key >= a.sk) return;
+    const int kh = head % a.hkv, b = head / a.hkv;
+    float g[2][4] = {};
+    const bool mine = 4 * lane < HD;
+    for (int p = split.first[tile]; p < split.first[tile + 1]; ++p)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (mine) {
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    split.partial + (((int64_t(p) * heads + head) * 2 + x) * kTile + at) * HD + 4 * lane);
+                g[x][0] += v.x; g[x][1] += v.y; g[x][2] += v.z; g[x][3] += v.w;
+            }
+    bool finite = true;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const float f = x == 0 ? 1.f : a.scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            g[x][j] *= f;
+            if (4 * lane < a.d) finite = finite && fabsf(g[x][j]) < INFINITY;
+        }
+        if (4 * lane < a.d)
+            *reinterpret_cast<uint2 *>(row_of<T>(x == 0 ? a.dv : a.dk, b, key, kh) + 4 * lane) =
+                make_uint2(pack_pair<T>(g[x][0], g[x][1]), pack_pair<T>(g[x][2], g[x][3]));
+    }
+    if (!__all_sync(0xffffffffu, finite)) dkv_row<T>(a, b, kh, key);
+}
+
+template <class T, int HD>
+basp_status go(const AttentionArgs &a, const HeadMaps &m, const KeySplit &s, cudaStream_t stream) {
+    constexpr auto dq = attention_dq_kernel<T, HD>;
+    constexpr auto dkv = attention_dkv_kernel<T, HD>;
     constexpr size_t dq_smem = BackSizes<HD, false>::kSmem, dkv_smem = BackSizes<HD, true>::kSmem;
     if (!allow_shared_memory<dq, dq_smem>() || !allow_shared_memory<dkv, dkv_smem>()) return BASP_ERR_CUDA;
-    const int64_t q = ceil_div(a.sq, kTile) * a.batch * a.hq, k = ceil_div(a.sk, kTile) * a.batch * a.hkv;
+    const int64_t heads = int64_t(a.batch) * a.hkv, q = ceil_div(a.sq, kTile) * a.batch * a.hq;
+    const int64_t k = (ceil_div(a.sk, kTile) - s.tiles + s.first[s.tiles]) * heads;
     if (q > kMaxSide || k > kMaxSide) return BASP_ERR_TOO_LARGE;
-    const basp_status st = launch(dkv, dim3(unsigned(k)), dim3(kBackThreads), dkv_smem, 1, stream, a, m);
+    basp_status st = launch(dkv, dim3(unsigned(k)), dim3(kBackThreads), dkv_smem, 1, stream, a, m, s);
+    if (st == BASP_OK && s.tiles > 0)
+        st = launch(key_join_kernel<T, HD>, dim3(unsigned(s.tiles * heads * (kTile / 8))), dim3(256), 0, 1, stream, a, s);
     if (st != BASP_OK) return st;
     return launch(dq, dim3(unsigned(q)), dim3(kBackThreads), dq_smem, 1, stream, a, m);
 }
 
 }  // namespace
 
-basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, bool bf16, cudaStream_t stream) {
-    if (bf16) return a.d <= 64 ? go<__nv_bfloat16, 64>(a, m, stream) : go<__nv_bfloat16, 128>(a, m, stream);
-    return a.d <= 64 ? go<__half, 64>(a, m, stream) : go<__half, 128>(a, m, stream);
+// A tile with more work than an SM has to do altogether (and than 64 pairs of tiles) is
+// shared by CTAs of a quarter of that.  A shorter one is hidden behind the others, since the
+// longest begin first: shared, those of 2 x 8192 x 32 heads of 64 with a window of 1024 took
+// 641 us, not 630.
+KeySplit key_split(const AttentionArgs &a) {
+    KeySplit s = {};
+    const int64_t tiles = ceil_div(a.sk, kTile), heads = int64_t(a.batch) * a.hkv;
+    if (tiles > 65536) return s;                              // plenty of tiles, and a loop over them
+    int64_t sum = 0;
+    auto pairs = [&](int64_t t) {
+        const QueryTiles q = query_tiles(a, int(t * kTile));
+        return int64_t(q.high - q.low) * a.group;
+    };
+    for (int64_t t = 0; t < tiles; ++t) sum += pairs(t);
+    const int64_t chunk = std::max<int64_t>(16, ceil_div(sum * heads, 152 * 4));
+    if (chunk > (1 << 30)) return s;
+    s.chunk = int(chunk);
+    for (int64_t t = 0; t < tiles && s.tiles < kMostSplit; ++t) {
+        const int64_t n = pairs(t);
+        if (n <= 4 * chunk || s.first[s.tiles] + ceil_div(n, chunk) > 4096) break;
+        s.first[s.tiles + 1] = s.first[s.tiles] + int(ceil_div(n, chunk));
+        ++s.tiles;
+    }
+    return s;
+}
+
+int64_t key_split_bytes(const AttentionArgs &a, const KeySplit &s) {
+    return int64_t(s.first[s.tiles]) * a.batch * a.hkv * 2 * kTile * (a.d <= 64 ? 64 : 128) * int64_t(sizeof(float));
+}
+
+basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, const KeySplit &s, bool bf16,
+                                      cudaStream_t stream) {
+    if (bf16) return a.d <= 64 ? go<__nv_bfloat16, 64>(a, m, s, stream) : go<__nv_bfloat16, 128>(a, m, s, stream);
+    return a.d <= 64 ? go<__half, 64>(a, m, s, stream) : go<__half, 128>(a, m, s, stream);
 }
 
 }  // namespace basp_fp8

@@ -54,14 +54,19 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttentionArgs &a, int r0) {
     return {min((first_end + kTile - 1) / kTile, low), low, p1 / kTile + 1};
 }
 
+// Key j is seen by the positions [j, last position].
+__host__ __device__ __forceinline__ int last_position(const AttentionArgs &a, int j) {
+    const int64_t last = int64_t(j) + a.window - 1;
+    return j < a.sinks || last >= a.sk ? a.sk - 1 : int(last);
+}
+
 // Query tiles that see any of the keys [k0, k0 + 128): [low, high).
 struct QueryTiles {
     int low, high;
 };
-__device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &a, int k0) {
-    const int shift = a.sk - a.sq, k1 = min(k0 + kTile, a.sk) - 1;
-    const int last = (k0 < a.sinks ? a.sk - 1 : int(min(int64_t(a.sk) - 1, int64_t(k1) + a.window - 1))) - shift;
-    const int first = max(0, k0 - shift);
+__host__ __device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &a, int k0) {
+    const int shift = a.sk - a.sq, k1 = (a.sk - k0 < kTile ? a.sk : k0 + kTile) - 1;
+    const int last = (k0 < a.sinks ? a.sk - 1 : last_position(a, k1)) - shift, first = k0 > shift ? k0 - shift : 0;
     if (last < first) return {0, 0};
     return {first / kTile, last / kTile + 1};
 }
@@ -162,11 +167,6 @@ __device__ __forceinline__ Sees keys_of(const AttentionArgs &a, int p) {
     const int low = p < 0 ? 0 : max(0, p - a.window + 1);
     return {min(a.sinks, low), low};
 }
-// Key j is seen by the positions [j, last position].
-__device__ __forceinline__ int last_position(const AttentionArgs &a, int j) {
-    return j < a.sinks ? a.sk - 1 : min(int64_t(a.sk) - 1, int64_t(j) + a.window - 1);
-}
-
 // ---- the plain form -----------------------------------------------------------------
 //
 // A warp computes one row from its definition, reading nothing but what the row

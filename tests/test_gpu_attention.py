@@ -93,6 +93,23 @@ def test_scales(scale):
     check(q, k, v, do, 100, 2, scale)
 
 
+@pytest.mark.parametrize("Sq,Sk,Hq,Hkv,d,window,sinks", [(4000, 4000, 2, 1, 64, 100, 3), (4000, 4000, 1, 1, 128, 300, 200),
+                                                         (3001, 3001, 4, 2, 40, None, 0), (2500, 3000, 3, 1, 72, 64, 700)])
+def test_long_key_tiles_are_shared(Sq, Sk, Hq, Hkv, d, window, sinks):
+    """Few heads and many queries of the first keys: several CTAs share a tile of keys."""
+    q, k, v, do = tensors(1, Sq, Sk, Hq, Hkv, d, torch.bfloat16)
+    o, lse, g = check(q, k, v, do, window, sinks)
+    assert all(torch.equal(a, b) for a, b in zip(g, attention.backward(do, q, k, v, o, lse, window, sinks)))
+    bad = do.clone()
+    bad[0, Sq - 1, 0, 3] = float("nan")
+    r = Attention(*(f64(x)[0] for x in (q, k, v)), window, sinks, d ** -0.5, u(torch.bfloat16))
+    want, bound = r.backward(f64(do)[0], r.o_bound)
+    rows = ~r.sees[Sq - 1]
+    got = attention.backward(bad, q, k, v, o, lse, window, sinks)
+    for name, x in zip(("dk", "dv"), got[1:]):
+        close(x[0][torch.from_numpy(rows).cuda()], want[name][rows], bound[name][rows])
+
+
 def test_growing_scores():
     """A row's largest score grows from tile to tile by far more than 8 in the exponent of 2."""
     t, S, d = torch.bfloat16, 640, 64
