@@ -250,39 +250,54 @@ template <class T> __global__ void __launch_bounds__(kJoinThreads) decode_join_k
     const int seen = see.first_end + len - see.last, parts = (seen + p.chunk - 1) / p.chunk;
     const float2 *stats = p.part_stats + int64_t(blockIdx.x) * p.chunks;
     const float4 *part = reinterpret_cast<const float4 *>(p.part + int64_t(blockIdx.x) * p.chunks * a.d);
-    float m = -INFINITY;
-    for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, stats[i].x);
+    // what a lane needs first, all on its way before anything is waited for
+    constexpr int kFirst = 8;
+    const int quads = a.d / 4, slices = kJoinThreads / quads, slice = tid / quads, e = tid % quads;
+    float2 ahead_stats[kFirst];
+    float4 ahead[kFirst];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) smax[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
-    // a part of nothing but minus infinities has a sum of 0, or of NaN
-    auto weight = [&](float2 x) { return x.x == -INFINITY ? 1.f : exp2_fast(x.x - m); };
-    float sum = 0.f;
+    for (int x = 0; x < kFirst; ++x) {
+        const int i = slice + x * slices;
+        const bool in = slice < slices && i < parts;
+        ahead_stats[x] = in ? stats[i] : make_float2(-INFINITY, 0.f);
+        ahead[x] = in ? part[int64_t(i) * quads + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m = -INFINITY, sum = 0.f;
     for (int i = tid; i < parts; i += kJoinThreads) {
         const float2 x = stats[i];
-        sum += x.y * weight(x);
+        const float top = fmaxf(m, x.x);
+        // a part of nothing but minus infinities has a sum of 0, or of NaN
+        sum = sum * (m == -INFINITY ? 1.f : exp2_fast(m - top)) + x.y * (x.x == -INFINITY ? 1.f : exp2_fast(x.x - top));
+        m = top;
     }
-    sum = warp_add(sum);
-    if (lane == 0) ssum[warp] = sum;
-    const int quads = a.d / 4, slices = kJoinThreads / quads, slice = tid / quads, e = tid % quads;
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    sum = warp_add(sum * (m == -INFINITY ? 1.f : exp2_fast(m - top)));
+    if (lane == 0) {
+        smax[warp] = top;
+        ssum[warp] = sum;
+    }
+    __syncthreads();
+    m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) sum += ssum[w] * (smax[w] == -INFINITY ? 1.f : exp2_fast(smax[w] - m));
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (slice < slices) {
-#pragma unroll 4
-        for (int i = slice; i < parts; i += slices) {
-            const float f = weight(stats[i]);
-            const float4 x = part[int64_t(i) * quads + e];
-            v.x = fmaf(x.x, f, v.x);
-            v.y = fmaf(x.y, f, v.y);
-            v.z = fmaf(x.z, f, v.z);
-            v.w = fmaf(x.w, f, v.w);
-        }
-    }
+    auto add = [&](float2 s, float4 x) {
+        const float f = s.x == -INFINITY ? 1.f : exp2_fast(s.x - m);
+        v.x = fmaf(x.x, f, v.x);
+        v.y = fmaf(x.y, f, v.y);
+        v.z = fmaf(x.z, f, v.z);
+        v.w = fmaf(x.w, f, v.w);
+    };
+#pragma unroll
+    for (int x = 0; x < kFirst; ++x) add(ahead_stats[x], ahead[x]);
+    if (slice < slices)
+        for (int i = slice + kFirst * slices; i < parts; i += slices) add(stats[i], part[int64_t(i) * quads + e]);
     so[tid] = v;
     __syncthreads();
     if (tid >= quads) return;
-    sum = (ssum[0] + ssum[1]) + (ssum[2] + ssum[3]);
     for (int i = 1; i < slices; ++i) {
         const float4 x = so[i * quads + tid];
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
