@@ -357,8 +357,24 @@ basp_status launch_adamw(const basp_adamw_tensor *list, int64_t i0, int64_t i1, 
     }
     *next = i;
     if (chunks == 0) return BASP_OK;
-    return eight ? launch(adamw_kernel<CAP, true>, dim3(unsigned(chunks)), dim3(kThreads), 0, 1, stream, t)
-                 : launch(adamw_kernel<CAP, false>, dim3(unsigned(chunks)), dim3(kThreads), 0, 1, stream, t);
+    // launch() of fp8_common.cuh would copy the table twice more
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(chunks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&t};
+    const void *kernel = eight ? reinterpret_cast<const void *>(adamw_kernel<CAP, true>)
+                               : reinterpret_cast<const void *>(adamw_kernel<CAP, false>);
+    if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
+        cudaGetLastError();
+        return BASP_ERR_CUDA;
+    }
+    return BASP_OK;
 }
 
 basp_status check_tensor(const basp_adamw_tensor &x, bool eight) {
@@ -368,17 +384,22 @@ basp_status check_tensor(const basp_adamw_tensor &x, bool eight) {
     if (x.n == 0) return BASP_OK;
     if ((x.m_scales != nullptr) != eight || (x.v_scales != nullptr) != eight) return BASP_ERR_INVALID_ARG;
     if (chunks_of(x.n) > kMaxSide) return BASP_ERR_TOO_LARGE;
-    const int64_t ss = eight ? 1 : 4;
-    Args args;
-    args.matrix(x.p, 1, x.n, x.n, ps, true);
-    args.matrix(x.g, 1, x.n, x.n, gs, false);
-    args.matrix(x.m, 1, x.n, x.n, ss, true);
-    args.matrix(x.v, 1, x.n, x.n, ss, true);
-    if (eight) {
-        args.matrix(x.m_scales, 1, ceil_div(x.n, kBlock), x.n, 1, true);
-        args.matrix(x.v_scales, 1, ceil_div(x.n, kBlock), x.n, 1, true);
+    const int64_t ss = eight ? 1 : 4, scales = eight ? ceil_div(x.n, kBlock) : 0;
+    if (x.n > (int64_t(1) << 56)) return BASP_ERR_TOO_LARGE;
+    // p, g, m, v and the scales: there, aligned, and apart
+    const struct { const void *p; int64_t bytes, size; } s[6] = {
+        {x.p, x.n * ps, ps}, {x.g, x.n * gs, gs}, {x.m, x.n * ss, ss}, {x.v, x.n * ss, ss},
+        {x.m_scales, scales, 1}, {x.v_scales, scales, 1}};
+    for (int i = 0; i < (eight ? 6 : 4); ++i) {
+        const uintptr_t at = uintptr_t(s[i].p);
+        if (at == 0) return BASP_ERR_INVALID_ARG;
+        if (at % uintptr_t(s[i].size)) return BASP_ERR_ALIGNMENT;
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t other = uintptr_t(s[j].p);
+            if (at < other + uintptr_t(s[j].bytes) && other < at + uintptr_t(s[i].bytes)) return BASP_ERR_ALIASING;
+        }
     }
-    return args.status();
+    return BASP_OK;
 }
 
 }  // namespace

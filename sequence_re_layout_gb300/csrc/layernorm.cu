@@ -389,11 +389,10 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *part, int w
 }
 
 // NB blocks a warp, as above; the CTA walks rows blockIdx.x, + gridDim.x, ...
-template <class T, class W, int NB, bool VEC>
-__global__ void __launch_bounds__(512) layer_back_kernel(const __grid_constant__ LayerBackArgs a) {
+template <class T, class W, int NB, bool VEC, int THREADS = 512>
+__global__ void __launch_bounds__(THREADS) layer_back_kernel(const __grid_constant__ LayerBackArgs a) {
     __shared__ __align__(16) float2 part[2][32];
-    if (threadIdx.x < 64) part[threadIdx.x / 32][threadIdx.x % 32] = make_float2(0.f, 0.f);
-    if (blockDim.x < 64 && threadIdx.x < 32) part[1][threadIdx.x] = make_float2(0.f, 0.f);
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) part[i / 32][i % 32] = make_float2(0.f, 0.f);
     __syncthreads();
     grid_dependency();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -408,44 +407,50 @@ __global__ void __launch_bounds__(512) layer_back_kernel(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0.f;
         }
-        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-            const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
-            const T *h = static_cast<const T *>(a.h) + row * a.hs;
-            const float mean = a.mean[row], rstd = a.rstd[row];
-            float g[NB][4], n[NB][4];
+        auto walk = [&](auto how) {
+            constexpr int H = decltype(how)::value;
+            for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+                const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
+                const T *h = static_cast<const T *>(a.h) + row * a.hs;
+                const T *dh = static_cast<const T *>(a.dh) + row * a.dhs;
+                const float mean = a.mean[row], rstd = a.rstd[row];
+                float g[NB][4], n[NB][4];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int c = (warp + i * warps) * kBlock;
-                load4<T, VEC>(dy + c, lane, a.cols - c, g[i]);
-                load4<T, VEC>(h + c, lane, a.cols - c, n[i]);
-            }
-            float dot = 0.f, all = 0.f;
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = inside<VEC>(lane, j, a.cols - (warp + i * warps) * kBlock);
-                    n[i][j] = in ? (n[i][j] - mean) * rstd : 0.f;
-                    dw[i][j] += g[i][j] * n[i][j];
-                    db[i][j] += g[i][j];
-                    g[i][j] *= wv[i][j];
-                    all += g[i][j];
-                    dot += g[i][j] * n[i][j];
+                for (int i = 0; i < NB; ++i) {
+                    const int c = (warp + i * warps) * kBlock;
+                    load4<T, H>(dy + c, lane, a.cols - c, g[i]);
+                    load4<T, H>(h + c, lane, a.cols - c, n[i]);
                 }
-            // two buffers in turn: a warp can be one row ahead of another
-            const float2 s = row_sum2(all, dot, part[turn], warps);
-            const float mg = s.x * a.inv_cols, mn = s.y * a.inv_cols;
+                float dot = 0.f, all = 0.f;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int c = (warp + i * warps) * kBlock;
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                if (a.dh != nullptr)
-                    load4<T, VEC>(static_cast<const T *>(a.dh) + row * a.dhs + c, lane, a.cols - c, d);
+                for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] += rstd * (g[i][j] - mg - n[i][j] * mn);
-                store4<T, VEC>(static_cast<T *>(a.dx) + row * a.dxs + c, lane, a.cols - c, d);
+                    for (int j = 0; j < 4; ++j) {
+                        const bool in = inside<H>(lane, j, a.cols - (warp + i * warps) * kBlock);
+                        n[i][j] = in ? (n[i][j] - mean) * rstd : 0.f;
+                        dw[i][j] += g[i][j] * n[i][j];
+                        db[i][j] += g[i][j];
+                        g[i][j] *= wv[i][j];
+                        all += g[i][j];
+                        dot += g[i][j] * n[i][j];
+                    }
+                // two buffers in turn: a warp can be one row ahead of another
+                const float2 s = row_sum2(all, dot, part[turn], warps);
+                const float mg = s.x * a.inv_cols, mn = s.y * a.inv_cols;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int c = (warp + i * warps) * kBlock;
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (a.dh != nullptr) load4<T, H>(dh + c, lane, a.cols - c, d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[j] += rstd * (g[i][j] - mg - n[i][j] * mn);
+                    store4<T, H>(static_cast<T *>(a.dx) + row * a.dxs + c, lane, a.cols - c, d);
+                }
             }
-        }
+        };
+        // a warp whose blocks all end inside the row needs no checks
+        if (!VEC && (warp + (NB - 1) * warps + 1) * kBlock <= a.cols) walk(How<kWhole>());
+        else walk(How<VEC>());
         if (a.part != nullptr) {
             float *to = a.part + int64_t(blockIdx.x) * 2 * a.cols;
 #pragma unroll
@@ -514,10 +519,10 @@ __global__ void __launch_bounds__(512) layer_back_kernel(const __grid_constant__
 }
 
 // The same for rows that allow accesses of 16 bytes, with the loads of the
-// next kAhead rows on their way to shared memory.
-template <class T, class W, int NV>
+// next AHEAD rows on their way to shared memory.
+template <class T, class W, int NV, int AHEAD>
 __global__ void __launch_bounds__(kWalkThreads) layer_back_walk_kernel(const __grid_constant__ LayerBackArgs a) {
-    constexpr int ST = kAhead + 1, N = Pack<T>::N;
+    constexpr int ST = AHEAD + 1, N = Pack<T>::N;
     extern __shared__ __align__(16) uint8_t smem[];     // [stage][dy, h, dh][vector][thread]
     __shared__ __align__(16) float2 part[2][32];
     const int threads = blockDim.x, warps = threads / 32;
@@ -554,14 +559,14 @@ __global__ void __launch_bounds__(kWalkThreads) layer_back_walk_kernel(const __g
         copy_commit();                    // an empty group past the end keeps the count
     };
     const int64_t step = gridDim.x;
-    for (int i = 0; i < kAhead; ++i) fetch(blockIdx.x + i * step, i);
+    for (int i = 0; i < AHEAD; ++i) fetch(blockIdx.x + i * step, i);
     __syncthreads();                      // part is zero
 
     int stage = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += step, turn ^= 1) {
-        fetch(row + kAhead * step, stage >= 1 ? stage - 1 : ST - 1);
+        fetch(row + AHEAD * step, stage >= 1 ? stage - 1 : ST - 1);
         const float mean = a.mean[row], rstd = a.rstd[row];
-        copy_wait<kAhead>();
+        copy_wait<AHEAD>();
         const uint4 *at = mine + stage * 3 * NV * threads;
         float g[NV][N], n[NV][N], dot = 0.f, all = 0.f;
         uint4 rest[NV];
@@ -626,34 +631,40 @@ __global__ void __launch_bounds__(1024) layer_column_sum_kernel(const float *par
     if (lane == 0 && o >= cols && o < width && db != nullptr) db[o - cols] = v;
 }
 
-// CTAs of the backward kernel: never more than fit at once, than there are rows,
-// or than the workspace has room for.
-constexpr int kBackMaxParts = 152 * 4;
-
-int64_t back_parts(int64_t rows) { return std::min<int64_t>(rows, kBackMaxParts); }
+// CTAs of the backward kernel, and parts of dw and db: never more than fit at once, than
+// there are rows, or than the workspace has room for.  Narrow rows have small CTAs, which
+// are more: 60000 x 512 bf16 took 104 us with four an SM.
+int64_t back_parts(int64_t rows, int64_t cols) {
+    return std::min<int64_t>(rows, 152 * std::min<int64_t>(16, std::max<int64_t>(4, 8192 / cols)));
+}
 
 template <class T, class W, bool VEC>
 basp_status launch_layer_back(const LayerBackArgs &a, int64_t *parts, cudaStream_t stream) {
     const int blocks = int(ceil_div(a.cols, kBlock));
     auto go = [&](auto kernel, int threads, size_t smem) {
-        *parts = std::min(back_parts(a.rows), resident_ctas(kernel, threads, smem));
+        *parts = std::min(back_parts(a.rows, a.cols), resident_ctas(kernel, threads, smem));
         return launch(kernel, dim3(unsigned(*parts)), dim3(threads), smem, 1, stream, a);
     };
     if (a.vec16) {
         const int vectors = int(a.cols / Pack<T>::N);
         auto walk = [&](auto vectors_each) {
-            constexpr int NV = decltype(vectors_each)::value;
-            constexpr auto kernel = layer_back_walk_kernel<T, W, NV>;
-            constexpr size_t per_thread = size_t(kAhead + 1) * 3 * NV * 16;
+            constexpr int NV = decltype(vectors_each)::value, AHEAD = NV == 4 ? 1 : kAhead;
+            constexpr auto kernel = layer_back_walk_kernel<T, W, NV, AHEAD>;
+            constexpr size_t per_thread = size_t(AHEAD + 1) * 3 * NV * 16;
             if (!allow_shared_memory<kernel, per_thread * kWalkThreads>()) return BASP_ERR_CUDA;
             const int threads = int(ceil_div(vectors, NV * 32)) * 32;
             return go(kernel, threads, per_thread * threads);
         };
-        if (vectors <= kWalkThreads) return walk(std::integral_constant<int, 1>());
-        if (vectors <= 2 * kWalkThreads) return walk(std::integral_constant<int, 2>());
+        // 16 values a thread: 8192 x 4096 fp32 takes 115 us with two vectors, 85 with four;
+        // 32768 x 2048 bf16 102 with two, 232 with four, which leave no registers
+        if (vectors <= 32) return walk(std::integral_constant<int, 1>());
+        if (vectors <= (Pack<T>::N == 8 ? 2 * kWalkThreads : 64)) return walk(std::integral_constant<int, 2>());
+        if (vectors <= 4 * kWalkThreads) return walk(std::integral_constant<int, 4>());
     }
-    if (blocks <= 32) return go(layer_back_kernel<T, W, 2, VEC>, int(ceil_div(blocks, 2)) * 32, 0);
-    if (blocks <= 64) return go(layer_back_kernel<T, W, 4, VEC>, int(ceil_div(blocks, 4)) * 32, 0);
+    const int threads = int(ceil_div(blocks, 2)) * 32;
+    if (threads <= 512) return go(layer_back_kernel<T, W, 2, VEC>, threads, 0);
+    if (threads <= 768) return go(layer_back_kernel<T, W, 2, VEC, 768>, threads, 0);
+    if (threads <= 1024) return go(layer_back_kernel<T, W, 2, VEC, 1024>, threads, 0);
     return go(layer_back_kernel<T, W, 0, VEC>, 512, 0);
 }
 
@@ -714,7 +725,7 @@ extern "C" basp_status basp_layernorm(basp_dtype dtype, int64_t rows, int64_t co
 
 extern "C" int64_t basp_layernorm_backward_workspace(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0 || rows > kMaxSide || cols > kMaxSide) return 0;
-    return back_parts(rows) * 2 * cols * int64_t(sizeof(float));
+    return back_parts(rows, cols) * 2 * cols * int64_t(sizeof(float));
 }
 
 extern "C" basp_status basp_layernorm_backward(basp_dtype dtype, int64_t rows, int64_t cols, const void *dy,

@@ -484,7 +484,7 @@ PyObject *layernorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // ---- attention -----------------------------------------------------------------
 
-// x [batch, len, heads, d] as the C calls take it.
+// x [batch, len, heads, d], or without `len` [batch, heads, d], as the C calls take it.
 basp_heads heads_of(const Tensor &x, c10::IntArrayRef shape, at::ScalarType type, int device, const char *where,
                     const char *name) {
     on_device(x, device, where, name);
@@ -492,15 +492,16 @@ basp_heads heads_of(const Tensor &x, c10::IntArrayRef shape, at::ScalarType type
         refuse(where, text(name, " must be ", c10::toString(type), ", got ", c10::toString(x.scalar_type())));
     if (x.sizes() != shape) refuse(where, text(name, " must have shape ", shape, ", got ", x.sizes()));
     if (x.numel() == 0) return {};
-    if (x.size(3) > 1 && x.stride(3) != 1)
+    const int64_t last = x.dim() - 1;
+    if (x.size(last) > 1 && x.stride(last) != 1)
         refuse(where, text(name, " must have a head's values next to each other, got strides ", x.strides()));
     basp_heads h = {x.data_ptr(), 0, 0, 0};
-    int64_t *const to[3] = {&h.stride_batch, &h.stride_seq, &h.stride_head};
-    for (int i = 0; i < 3; ++i)
-        if (x.size(i) > 1) *to[i] = x.stride(i);          // of a single one it says nothing
-    for (int i = 0; i < 3; ++i)
-        if (*to[i] % 8 != 0)
-            refuse(where, text(name, " must have strides of whole 16 bytes, got strides ", x.strides()));
+    // the stride of a single one says nothing
+    if (x.size(0) > 1) h.stride_batch = x.stride(0);
+    if (last == 3 && x.size(1) > 1) h.stride_seq = x.stride(1);
+    if (x.size(last - 1) > 1) h.stride_head = x.stride(last - 1);
+    if ((h.stride_batch | h.stride_seq | h.stride_head) % 8 != 0)
+        refuse(where, text(name, " must have strides of whole 16 bytes, got strides ", x.strides()));
     if (reinterpret_cast<uintptr_t>(h.data) % 16 != 0) refuse(where, text(name, " must begin at a multiple of 16 bytes"));
     return h;
 }
@@ -621,15 +622,13 @@ PyObject *attention_decode(PyObject *, PyObject *const *args, Py_ssize_t n) {
     basp_attention_desc d = desc_of(q, k, 3, where);
     mask_of(&d, args[4], args[5], args[6], where);
     const Call call(q, where, "q");
-    const int64_t one[4] = {d.batch, 1, d.q_heads, d.head_dim}, kv[4] = {d.batch, d.k_len, d.k_heads, d.head_dim};
+    const int64_t kv[4] = {d.batch, d.k_len, d.k_heads, d.head_dim};
     const auto type = q.scalar_type();
-    const basp_heads hq = heads_of(q.unsqueeze(1), one, type, call.device, where, "q");
+    const basp_heads hq = heads_of(q, q.sizes(), type, call.device, where, "q");
     const basp_heads hk = heads_of(k, kv, type, call.device, where, "k"), hv = heads_of(v, kv, type, call.device, where, "v");
     const void *len = vector_of(&lengths, d.batch, at::kInt, call.device, where, "lengths");
-    if (given != nullptr && given->sizes() != q.sizes())
-        refuse(where, text("out must have shape ", q.sizes(), ", got ", given->sizes()));
     const Tensor o = given != nullptr ? *given : new_tensor(q.sizes(), type, q.device());
-    const basp_heads ho = heads_of(o.unsqueeze(1), one, type, call.device, where, "out");
+    const basp_heads ho = heads_of(o, q.sizes(), type, call.device, where, "out");
     const int64_t bytes = g_lib.attention_decode_workspace(&d);
     Tensor workspace;
     if (bytes > 0) workspace = new_tensor({bytes}, at::kByte, q.device());
