@@ -12,7 +12,9 @@
 #include <utility>
 
 #include "basp.h"
+#include "basp_attention.h"
 #include "basp_fp8.h"
+#include "basp_optim.h"
 
 namespace basp {
 
@@ -130,6 +132,48 @@ inline void matmul_fp8(const basp_fp8_matrix &a, const basp_fp8_matrix &b, const
                        bool accumulate, basp_dtype dtype, void *c, int64_t c_stride,
                        cudaStream_t stream) {
     check(basp_matmul_fp8(&a, &b, bias, accumulate, dtype, c, c_stride, stream), "basp_matmul_fp8");
+}
+
+inline void layernorm(basp_dtype dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                      const void *residual, int64_t residual_stride, const void *weight, const void *bias,
+                      basp_dtype weight_dtype, float eps, void *h, int64_t h_stride, void *y, int64_t y_stride,
+                      const basp_fp8_matrix *q, float *mean, float *rstd, cudaStream_t stream) {
+    check(basp_layernorm(dtype, rows, cols, x, x_stride, residual, residual_stride, weight, bias, weight_dtype,
+                         eps, h, h_stride, y, y_stride, q, mean, rstd, stream), "basp_layernorm");
+}
+inline void layernorm_backward(basp_dtype dtype, int64_t rows, int64_t cols, const void *dy, int64_t dy_stride,
+                               const void *h, int64_t h_stride, const float *mean, const float *rstd,
+                               const void *weight, basp_dtype weight_dtype, const void *dh, int64_t dh_stride,
+                               void *dx, int64_t dx_stride, float *dweight, float *dbias, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+    check(basp_layernorm_backward(dtype, rows, cols, dy, dy_stride, h, h_stride, mean, rstd, weight,
+                                  weight_dtype, dh, dh_stride, dx, dx_stride, dweight, dbias, workspace,
+                                  workspace_bytes, stream), "basp_layernorm_backward");
+}
+
+// ---- attention (basp_attention.h) and the optimiser's step (basp_optim.h) ------
+
+inline void attention(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,
+                      const basp_heads &v, const basp_heads &o, float *lse, cudaStream_t stream) {
+    check(basp_attention(&desc, &q, &k, &v, &o, lse, stream), "basp_attention");
+}
+inline void attention_backward(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,
+                               const basp_heads &v, const basp_heads &o, const float *lse,
+                               const basp_heads &d_o, const basp_heads &dq, const basp_heads &dk,
+                               const basp_heads &dv, void *workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+    check(basp_attention_backward(&desc, &q, &k, &v, &o, lse, &d_o, &dq, &dk, &dv, workspace, workspace_bytes,
+                                  stream), "basp_attention_backward");
+}
+inline void attention_decode(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,
+                             const basp_heads &v, const int32_t *lengths, const basp_heads &o, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+    check(basp_attention_decode(&desc, &q, &k, &v, lengths, &o, workspace, workspace_bytes, stream),
+          "basp_attention_decode");
+}
+inline void adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_adamw_options &options,
+                  cudaStream_t stream) {
+    check(basp_adamw(tensors, count, &options, stream), "basp_adamw");
 }
 
 }  // namespace basp
