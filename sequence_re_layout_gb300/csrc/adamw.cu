@@ -91,14 +91,13 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t q, float (&v)[4]) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// The root to one unit in the last place (what is divided by it, or rounded to 8 bits
-// afterwards, needs no more), of a v below 2^-126 zero; and a quotient.
+// The root to one unit in the last place, which is enough for what is divided by it, of a
+// v below 2^-126 zero; and a quotient.
 __device__ __forceinline__ float root_of(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
 __device__ __forceinline__ float over(float x, float y) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
@@ -106,11 +105,15 @@ __device__ __forceinline__ float over(float x, float y) {
 }
 
 // What a step does to one element; m and v become m' and v', `root` the root of v'.
+template <bool EXACT_ROOT>
 __device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v,
                                          float &root) {
-    m = fmaf(o.one_beta1, g, o.beta1 * m);
-    v = fmaf(o.one_beta2 * g, g, o.beta2 * v);
-    root = root_of(v);
+    // The states' operations are rounded one by one, as 32-bit arithmetic has them and not
+    // fused: a state is then the same, down to which way it is rounded at random, as that of
+    // any other program that follows the formula in 32 bits.
+    m = __fadd_rn(__fmul_rn(o.beta1, m), __fmul_rn(o.one_beta1, g));
+    v = __fadd_rn(__fmul_rn(o.beta2, v), __fmul_rn(o.one_beta2, __fmul_rn(g, g)));
+    root = EXACT_ROOT ? __fsqrt_rn(v) : root_of(v);
     return fmaf(p, o.decay, -c1 * over(m, fmaf(root, c2, o.eps)));
 }
 
@@ -141,7 +144,7 @@ __device__ __forceinline__ void step_block(const Options &o, float c1, float c2,
         m[j] *= sm;
         v[j] *= sv;
         v[j] *= v[j];
-        p[j] = step_of(o, c1, c2, p[j], g[j], m[j], v[j], root[j]);
+        p[j] = step_of<true>(o, c1, c2, p[j], g[j], m[j], v[j], root[j]);
         bits[j] = __float_as_uint(m[j]) & 0x7fffffffu;
         tm = max(tm, bits[j]);
         tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
@@ -203,7 +206,7 @@ __device__ __forceinline__ void do_chunk32(const Entry &e, const Options &o, flo
             const int64_t at = b0 + i * kBlock;
             const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root);
+            for (int j = 0; j < 4; ++j) p[i][j] = step_of<false>(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root);
             store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
             store4<float, HOW>(static_cast<float *>(e.m) + at, lane, left, m[i]);
             store4<float, HOW>(static_cast<float *>(e.v) + at, lane, left, v[i]);
@@ -290,7 +293,7 @@ __device__ __forceinline__ void do_chunk8(const Entry &e, const Options &o, floa
 }
 
 template <int CAP, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __grid_constant__ Table<CAP> t) {
+__global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __grid_constant__ Table<CAP> t) {
     __shared__ __align__(16) uint8_t ring[EIGHT ? (kThreads / 32) * kStages * kStageBytes : 16];
     grid_dependency();
     int lo = 0, hi = t.count;                        // e[lo].chunk0 <= chunk < e[hi].chunk0
