@@ -42,7 +42,7 @@ extern "C" {
 #endif
 
 typedef struct basp_attention_desc {
-    int64_t batch, q_len, k_len;   /* sequences, Sq, Sk: each below 2^31              */
+    int64_t batch, q_len, k_len;   /* sequences (below 2^31), Sq, Sk (2^31 - 2^12)    */
     int64_t q_heads, k_heads;      /* Hq, Hkv: Hq a multiple of Hkv                   */
     int64_t head_dim;              /* a multiple of 8, 8 to 128                       */
     int64_t window;                /* keys a query sees with its own, >= 1; 0: all    */

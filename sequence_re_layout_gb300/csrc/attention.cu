@@ -5,6 +5,7 @@
 // warp a row, for tensors that TMA cannot address (a sequence stride of 0 or below a
 // head's length, strides of 2^40 bytes).
 #include <algorithm>
+#include <cmath>
 
 #include "attention.cuh"
 
@@ -17,6 +18,9 @@ constexpr int kRowWarps = 4;
 
 enum { kForward, kDq, kDkv };
 
+// Loops over a sequence step past its end by less than what is left of 32 bits.
+constexpr int64_t kMaxLength = (int64_t(1) << 31) - 4096;
+
 // A warp a row.
 template <class T, int WHAT>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ AttentionArgs a) {
@@ -25,7 +29,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     const int64_t rows = int64_t(a.batch) * heads * len;
     for (int64_t r = int64_t(blockIdx.x) * kRowWarps + threadIdx.x / 32; r < rows; r += int64_t(gridDim.x) * kRowWarps) {
         const int i = int(r % len), h = int(r / len % heads), b = int(r / len / heads);
-        if constexpr (WHAT == kForward) forward_row<T>(a, b, h, i);
+        if constexpr (WHAT == kForward) forward_row<T, true>(a, b, h, i);
         if constexpr (WHAT == kDq) dq_row<T>(a, b, h, i);
         if constexpr (WHAT == kDkv) dkv_row<T>(a, b, h, i);
     }
@@ -71,17 +75,20 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
             // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that
             // the rows that meet it are made from the definition
             const float sign = a.scale < 0.f ? 1.f : -1.f;        // the other side of the product is negated
-            float part[8], rest = sees ? sign * lse / score_scale(a.scale) / kFoldLse<T> : 0.f;
+            float part[8], rest = sees ? sign * lse / score_scale(a.scale) : 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                const float unit = fold_unit<T>(j % 4);
                 if (j == 4) rest = sees ? -s : 0.f;
-                part[j] = Elem<T>::to_float(Elem<T>::from_float(rest));
+                part[j] = unit == 0.f ? 0.f : Elem<T>::to_float(Elem<T>::from_float(rest / unit));
                 if (!(fabsf(part[j]) < INFINITY)) part[j] = __uint_as_float(0x7fffffffu);
-                rest -= part[j];
+                rest -= part[j] * unit;
             }
-            uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32;
-            *reinterpret_cast<uint4 *>(to + fold_offset(i - tile * kTile, 0)) = Pack<T>::pack(part);
-            *reinterpret_cast<uint4 *>(to + fold_offset(i - tile * kTile, 1)) = make_uint4(0, 0, 0, 0);
+            uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32 +
+                          fold_offset(i - tile * kTile);
+            const uint4 w = Pack<T>::pack(part);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(w.x, w.y, 0, 0);
+            *reinterpret_cast<uint4 *>(to + kFoldPlane) = make_uint4(w.z, w.w, 0, 0);
         }
     }
 }
@@ -107,8 +114,10 @@ bool sizes_ok(const basp_attention_desc *d, basp_status *st) {
         return false;
     }
     *st = BASP_ERR_TOO_LARGE;
-    for (int64_t n : {d->batch, d->q_len, d->k_len, d->q_heads, d->k_heads})
+    for (int64_t n : {d->batch, d->q_heads, d->k_heads})
         if (n > kMaxSide) return false;
+    for (int64_t n : {d->q_len, d->k_len})
+        if (n > kMaxLength) return false;
     *st = BASP_OK;
     return true;
 }
@@ -175,8 +184,9 @@ AttentionArgs args_of(const basp_attention_desc *d) {
     a.batch = int(d->batch); a.sq = int(d->q_len); a.sk = int(d->k_len);
     a.hq = int(d->q_heads); a.hkv = int(d->k_heads); a.d = int(d->head_dim);
     a.group = d->k_heads > 0 ? int(d->q_heads / d->k_heads) : 1;
-    a.window = d->window == 0 ? int(std::max<int64_t>(1, d->k_len)) : int(std::min<int64_t>(d->window, kMaxSide));
-    a.sinks = int(std::min<int64_t>(d->sinks, kMaxSide));
+    const int64_t all = std::max<int64_t>(1, d->k_len);
+    a.window = int(d->window == 0 ? all : std::min(d->window, all));
+    a.sinks = int(std::min(d->sinks, d->k_len));
     a.scale = d->scale;
     return a;
 }
@@ -325,7 +335,9 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     a.sq_pad = int(ceil_div(a.sq, kTile) * kTile);
     a.stats = static_cast<float2 *>(workspace);
     a.fold = reinterpret_cast<uint16_t *>(a.stats + int64_t(a.batch) * a.hq * a.sq_pad);
-    const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq);
+    // lse / c of the smallest scales is past 32 bits
+    const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq) &&
+                       (a.scale == 0.f || std::fabs(a.scale) >= 0x1p-64f);
     HeadMaps m = {};
     if (tiles && (!encode_qkv(a, &m) || !encode(a, a.d_o, a.sq, a.hq, kTile, &m.d_o, &m.do_head, &m.do_batch)))
         return BASP_ERR_CUDA;

@@ -24,7 +24,8 @@
 //
 // In the dkv kernel lse and D vary along a row.  They are taken off inside the products,
 // by 16 more of K: each query's row has -lse / c and -D there, in four 16-bit parts each,
-// and the keys' side has ones (64 for fp16's lse, whose range is small) where they belong.
+// and the keys' side has ones (for fp16, whose range is small, other powers of two) where
+// they belong.
 // As loads from shared memory, a value each, they took 1200 of 3000 cycles a pair of tiles.
 //
 // Where key tiles differ much in work (the sinks' keys are seen by every query, a causal
@@ -56,10 +57,12 @@ template <int HD, bool DKV> struct BackSizes {
     static constexpr int kOperand = kBoxes * kBox;            // bytes of a tile of Q, K, V or dO
     static constexpr int kStages = HD == 128 ? (DKV ? 4 : 5) : 8;
     static constexpr int kPlaces = DKV ? kStages / 2 + 1 : 0; // of the queries' lse and D
-    static constexpr int kFold = kFoldBytes;                  // of a tile's 16 more of K
+    // A tile's lse and D: planes of lse, of zeros and of D, of which a product's 16 more of K
+    // are the first or the last two.  An infinite D so does not meet the scores.
+    static constexpr int kFold = 3 * kFoldPlane;
     static constexpr int kBarriers = 1 + 2 * kStages + 9;
     static constexpr int kSmem =
-        1024 + (2 + kStages) * kOperand + (kPlaces + (DKV ? 2 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
+        1024 + (2 + kStages) * kOperand + (kPlaces + (DKV ? 1 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -99,8 +102,8 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     const uint32_t k_at = smem_addr(smem), v_at = k_at + Z::kOperand, ring0 = k_at + 2 * Z::kOperand;
     uint8_t *ones = smem + (2 + ST) * Z::kOperand;            // the keys' side of lse, of D
-    const uint32_t ones_at = smem_addr(ones), fold0 = ones_at + 2 * Z::kFold;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + (2 + SS) * Z::kFold);
+    const uint32_t ones_at = smem_addr(ones), fold0 = ones_at + Z::kFold;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + (1 + SS) * Z::kFold);
     const uint32_t kv_full = smem_addr(bars), full = kv_full + 8, empty = full + 8 * ST;
     const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8;
     // where products are early: S and dP have been read, dS has been used
@@ -133,10 +136,11 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     if (warp == kTmemWarp) tmem_alloc<1>(smem_addr(tmem_slot), 512);
     if (threadIdx.x < 2 * kTile) {
         const int row = threadIdx.x % kTile, of_d = threadIdx.x / kTile;
-        const uint32_t w = pack_pair<T>(of_d ? 1.f : kFoldLse<T>, of_d ? 1.f : kFoldLse<T>);
-        uint4 *to = reinterpret_cast<uint4 *>(ones + of_d * Z::kFold + fold_offset(row, 0));
-        to[0] = of_d ? make_uint4(0, 0, w, w) : make_uint4(w, w, 0, 0);
-        *reinterpret_cast<uint4 *>(ones + of_d * Z::kFold + fold_offset(row, 1)) = make_uint4(0, 0, 0, 0);
+        const uint32_t w0 = pack_pair<T>(fold_unit<T>(0), fold_unit<T>(1)), w1 = pack_pair<T>(fold_unit<T>(2), fold_unit<T>(3));
+        *reinterpret_cast<uint4 *>(ones + 2 * of_d * kFoldPlane + fold_offset(row)) = make_uint4(w0, w1, 0, 0);
+        if (of_d)
+            for (int s = 0; s <= SS; ++s)                     // of the ones too
+                *reinterpret_cast<uint4 *>(ones + s * Z::kFold + kFoldPlane + fold_offset(row)) = make_uint4(0, 0, 0, 0);
         fence_async_shared();
     }
     tcgen05_before_sync();
@@ -183,13 +187,14 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                     if (!ok) break;
                     if (elect_one()) {
                         const uint32_t to = ring0 + ring.at * Z::kOperand, bar = full + 8 * ring.at;
-                        mbar_expect_tx(bar, Z::kOperand + (x == 0 ? Z::kFold : 0));
+                        mbar_expect_tx(bar, Z::kOperand + (x == 0 ? 2 * kFoldPlane : 0));
                         for (int y = 0; y < Z::kBoxes; ++y)
                             tma_load_4d(to + y * kBox, x == 0 ? &m.q : &m.d_o, 64 * y, q, h * (x == 0 ? m.q_head : m.do_head),
                                         b * (x == 0 ? m.q_batch : m.do_batch), bar);
                         if (x == 0)
-                            bulk_load(fold0 + place.at * Z::kFold,
-                                      a.fold + ((int64_t(b) * a.hq + h) * a.sq_pad + q) * 16, Z::kFold, bar);
+                            for (int y = 0; y < 2; ++y)
+                                bulk_load(fold0 + place.at * Z::kFold + 2 * y * kFoldPlane,
+                                          a.fold + ((int64_t(b) * a.hq + h) * a.sq_pad + q) * 16 + y * (kFoldPlane / 2), kFoldPlane, bar);
                     }
                     __syncwarp();
                     ring.next();
@@ -218,7 +223,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                     const uint32_t at = (k / 4) * (kBox / 16) + (k % 4) * 2;
                     mma_f16(d, dx + at, dy + at, desc, k > 0);
                 }
-                mma_f16(d, desc_plain(ones, 128, 256), desc_plain(fold, 128, 256), desc, true);
+                mma_f16(d, desc_plain(ones, kFoldPlane, 128), desc_plain(fold, kFoldPlane, 128), desc, true);
                 mma_commit<1>(bar);
             };
             // a product over the queries: P^T dO or dS^T Q
@@ -238,13 +243,13 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             if (ok) {
                 tcgen05_after_sync();
                 across_head(tmem, k_at, ring0 + q * Z::kOperand, ones_at, fold0, is, s_full);
-                across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, ones_at + Z::kFold, fold0, idp, dp_full);
+                across_head(tmem + kTile, v_at, ring0 + o * Z::kOperand, ones_at + kFoldPlane, fold0 + kFoldPlane, idp, dp_full);
             }
             for (int i = 0; i < total && ok; ++i) {
                 const bool more = i + 1 < total;
                 const uint32_t q_now = q, o_now = o;
                 // the next pair's product, once its place is free
-                auto next = [&](uint32_t &at, Turn<SS> &place, uint32_t d, uint32_t x, uint32_t ones, uint32_t desc, uint32_t bar,
+                auto next = [&](uint32_t &at, Turn<SS> &place, uint32_t d, uint32_t x, uint32_t plane, uint32_t desc, uint32_t bar,
                                 uint32_t taken) {
                     if (!more) return;
                     at = take();
@@ -252,15 +257,15 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                     if (kEarly<HD>) ok = ok && wait(taken, i & 1);
                     if (!ok) return;
                     tcgen05_after_sync();
-                    across_head(d, x, ring0 + at * Z::kOperand, ones, fold0 + place.at * Z::kFold, desc, bar);
+                    across_head(d, x, ring0 + at * Z::kOperand, ones_at + plane, fold0 + place.at * Z::kFold + plane, desc, bar);
                 };
-                if (kEarly<HD>) next(q, of_s, tmem, k_at, ones_at, is, s_full, s_taken);
+                if (kEarly<HD>) next(q, of_s, tmem, k_at, 0, is, s_full, s_taken);
                 ok = ok && wait(p_ready, i & 1);
                 if (!ok) break;
                 tcgen05_after_sync();
                 across_queries(dv_acc, p_at, ring0 + o_now * Z::kOperand, i > 0);
-                if (!kEarly<HD>) next(q, of_s, tmem, k_at, ones_at, is, s_full, s_taken);
-                if (kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, ones_at + Z::kFold, idp, dp_full, dp_taken);
+                if (!kEarly<HD>) next(q, of_s, tmem, k_at, 0, is, s_full, s_taken);
+                if (kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, kFoldPlane, idp, dp_full, dp_taken);
                 mma_commit<1>(empty + 8 * o_now);
                 ok = ok && wait(ds_ready, i & 1);
                 if (!ok) break;
@@ -268,7 +273,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
                 across_queries(dk_acc, ds_at, ring0 + q_now * Z::kOperand, i > 0);
                 if (kEarly<HD>) mma_commit<1>(ds_used);
                 mma_commit<1>(empty + 8 * q_now);
-                if (!kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, ones_at + Z::kFold, idp, dp_full, dp_taken);
+                if (!kEarly<HD>) next(o, of_dp, tmem + kTile, v_at, kFoldPlane, idp, dp_full, dp_taken);
             }
             if (ok) mma_commit<1>(done);
             // nothing is in flight at the end
@@ -388,7 +393,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
         if (way == 0)
             for (; again != 0; again &= again - 1)
-                dkv_row<T>(a, b, kh, k0 + quarter * 32 + __ffs(int(again)) - 1);
+                mend_dkv_row<T>(a, b, kh, k0, k0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -624,7 +629,7 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
         if (way == 0)
             for (; again != 0; again &= again - 1)
-                dq_row<T>(a, b, h, q0 + quarter * 32 + __ffs(int(again)) - 1);
+                mend_dq_row<T>(a, b, h, q0, q0 + quarter * 32 + __ffs(int(again)) - 1);
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -664,7 +669,8 @@ __global__ void __launch_bounds__(256) key_join_kernel(const __grid_constant__ A
             *reinterpret_cast<uint2 *>(row_of<T>(x == 0 ? a.dv : a.dk, b, key, kh) + 4 * lane) =
                 make_uint2(pack_pair<T>(g[x][0], g[x][1]), pack_pair<T>(g[x][2], g[x][3]));
     }
-    if (!__all_sync(0xffffffffu, finite)) dkv_row<T>(a, b, kh, key);
+    __syncwarp();                                             // after the stores above
+    if (!__all_sync(0xffffffffu, finite)) mend_dkv_row<T>(a, b, kh, tile * kTile, key);
 }
 
 template <class T, int HD>

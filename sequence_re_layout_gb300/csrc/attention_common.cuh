@@ -26,7 +26,7 @@ struct AttentionArgs {
     // for the backward: (lse log2(e), D) of each query, [batch][Hq][sq_pad]; of one that
     // does not exist, or sees nothing: (infinity, 0)
     float2 *stats;
-    uint16_t *fold;                      // the same as parts of a product, [batch][Hq][sq_pad][16]
+    uint16_t *fold;                      // the same as parts of a product, two planes a tile of queries
     int batch, sq, sk, sq_pad, hq, hkv, d, group;
     int window, sinks;                   // window: sk where all is visible
     float scale;
@@ -78,13 +78,17 @@ __device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31
 // of 0 leaves all scores alike.
 __device__ __forceinline__ float score_scale(float scale) { return fmaxf(fabsf(scale) * kLog2e, 0x1p-64f); }
 
-// 16 values of K for each of 128 rows, as 16 bytes x 8 rows next to each other: the 8
-// values of half k of a row begin at this byte.
-constexpr int kFoldBytes = kTile * 32;
-__host__ __device__ __forceinline__ constexpr int fold_offset(int row, int k) { return row / 8 * 256 + k * 128 + row % 8 * 16; }
-// lse / c can be beyond fp16's range: its parts are divided by this, which the other side
-// of the product has instead of ones.
-template <class T> constexpr float kFoldLse = std::is_same_v<T, __half> ? 64.f : 1.f;
+// 8 values of K for each of 128 rows, as 16 bytes x 8 rows next to each other: a plane.  A
+// tile of queries has one of its lse and one of its D.
+constexpr int kFoldPlane = kTile * 16;
+__host__ __device__ __forceinline__ constexpr int fold_offset(int row) { return row * 16; }
+// Part j of lse / c, or of D, is multiplied by 1 / fold_unit(j) and the other side of the
+// product has fold_unit(j) instead of one.  fp16's range is small at both ends: the first
+// part may be 64 x 65504, and the third is exact to 2^-41.
+template <class T> __host__ __device__ __forceinline__ constexpr float fold_unit(int j) {
+    if (!std::is_same_v<T, __half>) return 1.f;
+    return j == 0 ? 0x1p6f : j == 1 ? 0x1p-5f : j == 2 ? 0x1p-16f : 0.f;
+}
 
 // A wait on one of the CTA's barriers, with a limit.
 constexpr uint64_t kAttentionWaitNs = 2000000000ull;
@@ -197,11 +201,22 @@ template <class T> __device__ __forceinline__ void row_store(T *row, const float
         if (lane + 32 * j < d) row[lane + 32 * j] = Elem<T>::from_float(v[j]);
 }
 
-// Calls f(j) for 32 keys at a time of [0, first_end) and [low, end): `have` says
-// whether this lane's exists.
-template <class F> __device__ __forceinline__ void each_keys(int first_end, int low, int end, int lane, F &&f) {
-    for (int j0 = 0; j0 < first_end; j0 += 32) f(j0 + lane, j0 + lane < first_end);
-    for (int j0 = low; j0 < end; j0 += 32) f(j0 + lane, j0 + lane < end);
+// Calls f(j, have) for 32 keys at a time of [0, first_end) and [low, end), until it says
+// that the rest makes no difference; `have`: whether this lane's key exists.
+template <class F> __device__ __forceinline__ bool each_keys(int first_end, int low, int end, int lane, F &&f) {
+    for (int j0 = 0; j0 < first_end; j0 += 32)
+        if (!f(j0 + lane, j0 + lane < first_end)) return false;
+    for (int j0 = low; j0 < end; j0 += 32)
+        if (!f(j0 + lane, j0 + lane < end)) return false;
+    return true;
+}
+
+// Whether the warp's whole row is NaN, which no more addition changes.
+__device__ __forceinline__ bool row_lost(const float (&v)[4], int d, int lane) {
+    bool lost = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lost = lost && (lane + 32 * j >= d || v[j] != v[j]);
+    return __all_sync(0xffffffffu, lost);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -218,8 +233,8 @@ __device__ __forceinline__ float warp_add(float v) {
     return v;
 }
 
-// o and lse of query i.
-template <class T>
+// o of query i, and with LSE its lse.
+template <class T, bool LSE>
 __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, int i) {
     const int lane = threadIdx.x % 32, p = i + a.sk - a.sq, kh = h / a.group;
     const Sees see = keys_of(a, p);
@@ -238,12 +253,13 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
             const float wx = __shfl_sync(0xffffffffu, w, x);
             if (__shfl_sync(0xffffffffu, int(have), x)) row_add(o, wx, row_of<const T>(a.v, b, jx, kh), a.d, lane);
         }
+        return (LSE && l == l) || !row_lost(o, a.d, lane);
     });
     const bool any = p >= 0;                         // whoever sees anything sees itself
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = any ? o[e] / l : 0.f;
     row_store(row_of<T>(a.o, b, i, h), o, a.d, lane);
-    if (a.lse != nullptr && lane == 0)
+    if (LSE && a.lse != nullptr && lane == 0)
         a.lse[(int64_t(b) * a.hq + h) * a.sq + i] = any ? m + logf(l) : -INFINITY;
 }
 
@@ -267,6 +283,7 @@ __device__ __noinline__ void dq_row(const AttentionArgs &a, int b, int h, int i)
             const float dx = __shfl_sync(0xffffffffu, ds, x);
             if (__shfl_sync(0xffffffffu, int(have), x)) row_add(dq, dx, row_of<const T>(a.k, b, jx, kh), a.d, lane);
         }
+        return !row_lost(dq, a.d, lane);
     });
     row_store(row_of<T>(a.dq, b, i, h), dq, a.d, lane);
 }
@@ -278,10 +295,11 @@ __device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int 
     const T *k = row_of<const T>(a.k, b, j, kh), *v = row_of<const T>(a.v, b, j, kh);
     const int i0 = max(0, j - shift), i1 = last_position(a, j) - shift + 1;
     float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int h = kh * a.group; h < (kh + 1) * a.group; ++h) {
+    bool go_on = true;
+    for (int h = kh * a.group; h < (kh + 1) * a.group && go_on; ++h) {
         const float *lse = a.lse + (int64_t(b) * a.hq + h) * a.sq;
         const float2 *stats = a.stats + (int64_t(b) * a.hq + h) * a.sq_pad;
-        each_keys(0, i0, i1, lane, [&](int i, bool have) {
+        go_on = each_keys(0, i0, i1, lane, [&](int i, bool have) {
             float w = 0.f, ds = 0.f;
             if (have) {
                 w = expf(a.scale * row_dot(k, row_of<const T>(a.q, b, i, h), a.d) - lse[i]);
@@ -295,10 +313,75 @@ __device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int 
                     row_add(dk, dx, row_of<const T>(a.q, b, ix, h), a.d, lane);
                 }
             }
+            return !(row_lost(dk, a.d, lane) && row_lost(dv, a.d, lane));
         });
     }
     row_store(row_of<T>(a.dk, b, j, kh), dk, a.d, lane);
     row_store(row_of<T>(a.dv, b, j, kh), dv, a.d, lane);
+}
+
+// ---- rows of tiles that came out infinite or NaN -------------------------------------
+//
+// A masked pair has P = 0 and dS = 0, but 0 times an infinite or NaN value is NaN.  Only a
+// row with such a value among what its tiles hold and it does not see is computed again:
+// where what it sees is no number itself, the tiles' answer is the definition's, and a
+// batch that has become NaN costs no more than another.
+
+// Whether a row holds a value that is infinite or NaN.
+template <class T> __device__ __forceinline__ bool any_in_row(const T *row, int d) {
+    bool bad = false;
+    for (int e = 0; e < d; e += 8) {
+        float f[8];
+        Pack<T>::unpack(*reinterpret_cast<const uint4 *>(row + e), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bad = bad || !(fabsf(f[j]) < INFINITY);
+    }
+    return bad;
+}
+// Whether rows [s0, s1) of head h do.
+template <class T>
+__device__ __forceinline__ bool any_not_finite(const Heads &t, int b, int h, int s0, int s1, int d, int lane) {
+    for (int s = s0; s < s1; s += 32)
+        if (__any_sync(0xffffffffu, s + lane < s1 && any_in_row<T>(row_of<const T>(t, b, s + lane, h), d))) return true;
+    return false;
+}
+
+// Of the query at position p in the tile of queries from r0: the keys of `t`.
+template <class T>
+__device__ __noinline__ bool masked_keys_not_finite(const AttentionArgs &a, const Heads &t, int b, int kh, int r0, int p) {
+    const int lane = threadIdx.x % 32;
+    const KeyTiles tiles = key_tiles(a, r0);
+    const Sees see = keys_of(a, p);
+    const int low = tiles.low * kTile, high = min(tiles.high * kTile, a.sk);
+    return any_not_finite<T>(t, b, kh, see.first_end, min(tiles.first * kTile, see.last), a.d, lane) ||
+           any_not_finite<T>(t, b, kh, max(low, see.first_end), min(see.last, high), a.d, lane) ||
+           any_not_finite<T>(t, b, kh, max(max(0, p + 1), low), high, a.d, lane);
+}
+
+// Of key j in the tile of keys from k0: the queries and their gradients.
+template <class T>
+__device__ __noinline__ bool masked_queries_not_finite(const AttentionArgs &a, int b, int kh, int k0, int j) {
+    const int lane = threadIdx.x % 32, shift = a.sk - a.sq;
+    const QueryTiles tiles = query_tiles(a, k0);
+    const int low = tiles.low * kTile, high = min(tiles.high * kTile, a.sq);
+    const int i0 = max(0, j - shift), i1 = max(i0, last_position(a, j) - shift + 1);
+    for (int h = kh * a.group; h < (kh + 1) * a.group; ++h)
+        if (any_not_finite<T>(a.q, b, h, low, min(i0, high), a.d, lane) || any_not_finite<T>(a.d_o, b, h, low, min(i0, high), a.d, lane) ||
+            any_not_finite<T>(a.q, b, h, max(i1, low), high, a.d, lane) || any_not_finite<T>(a.d_o, b, h, max(i1, low), high, a.d, lane))
+            return true;
+    return false;
+}
+
+// fp16 has other reasons: dS, or a part of lse or D, past its range.
+template <class T> constexpr bool kOtherReasons = std::is_same_v<T, __half>;
+
+template <class T>
+__device__ __forceinline__ void mend_dq_row(const AttentionArgs &a, int b, int h, int r0, int i) {
+    if (kOtherReasons<T> || masked_keys_not_finite<T>(a, a.k, b, h / a.group, r0, i + a.sk - a.sq)) dq_row<T>(a, b, h, i);
+}
+template <class T>
+__device__ __forceinline__ void mend_dkv_row(const AttentionArgs &a, int b, int kh, int k0, int j) {
+    if (kOtherReasons<T> || masked_queries_not_finite<T>(a, b, kh, k0, j)) dkv_row<T>(a, b, kh, j);
 }
 
 }  // namespace basp_fp8

@@ -278,6 +278,7 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);   // a scale of 0 leaves all scores alike
         const int ochunks = (a.d + 31) / 32;
         uint32_t n = 0, sums = 0;                             // tiles of keys, pairs of tiles with any
+        int bad_from = rounds;                                // the first round with rows that are no numbers
         bool ok = true;
         for (int r = 0; r < rounds; ++r) {
             const int w = pair_of(r);
@@ -407,11 +408,19 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
             if (exists && a.lse != nullptr)
                 a.lse[(int64_t(b) * a.hq + h) * a.sq + row] =
                     !any ? -INFINITY : ok ? top * fabsf(a.scale) + logf(l) : __uint_as_float(0x7fffffffu);
-            // rows that are no numbers, again from the definition
-            uint32_t again = __ballot_sync(0xffffffffu, ok && exists && !finite);
+            if (bad_from == rounds && __any_sync(0xffffffffu, exists && !finite)) bad_from = r;
+        }
+        // Rows that are no numbers, again from the definition; at the end, since the CTA's
+        // other warps would wait for them.
+        for (int r = ok ? bad_from : rounds; r < rounds; ++r) {
+            const int w = pair_of(r);
+            if (w >= pairs) continue;
+            const Pair p(a, w);
+            const int row0 = p.r0 + t * kTile, row = row0 + quarter * 32 + lane;
+            uint32_t again = __ballot_sync(0xffffffffu, row < a.sq && any_in_row<T>(row_of<const T>(a.o, p.b, row < a.sq ? row : 0, p.h), a.d));
             for (; again != 0; again &= again - 1) {
-                __syncwarp();                                 // after the stores above
-                forward_row<T>(a, b, h, row0 + quarter * 32 + __ffs(int(again)) - 1);
+                const int i = row0 + quarter * 32 + __ffs(int(again)) - 1;
+                if (masked_keys_not_finite<T>(a, a.v, p.b, p.kh, row0, i + a.sk - a.sq)) forward_row<T, false>(a, p.b, p.h, i);
             }
         }
     }

@@ -360,5 +360,59 @@ def test_step_captured_and_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("scale,size", [(1000.0, 0.03), (30000.0, 0.005), (1e-30, 1.0), (-1e-12, 1.0)])
+def test_scales_far_from_one(scale, size, dtype):
+    """Scores of a few units under a large scale: lse / scale is small; and under a tiny one, large."""
+    q, k, v, do = tensors(1, 190, 200, 2, 1, 64, DTYPES[dtype])
+    check(q * size, k * size, v, do, 100, 2, scale)
+
+
+def test_gradients_past_fp16():
+    """dS and D beyond what fp16 holds, the gradients within it."""
+    q, k, v, do = tensors(1, 200, 200, 2, 1, 64, torch.float16)
+    o, lse = attention.forward(q * 0.02, k * 0.02, v * 40)
+    got = attention.backward(do * 400, q * 0.02, k * 0.02, v * 40, o, lse)
+    r = Attention(*(f64(x)[0] for x in (q * 0.02, k * 0.02, v * 40)), None, 0, 0.125, u(torch.float16))
+    want, bound = r.backward(f64(do * 400)[0], r.o_bound)
+    assert np.abs((f64(do * 400)[0] * r.o).sum(-1)).max() > 65504
+    for name, g in zip(("dq", "dk"), got):
+        close(g[0], want[name], bound[name])
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 62, 2 ** 62), (50, 2 ** 31 - 1)])
+def test_masks_past_every_length(window, sinks):
+    q, k, v, do = tensors(1, 150, 200, 2, 1, 64, torch.bfloat16)
+    o, lse, g = check(q, k, v, do, window, sinks)
+    want = attention.forward(q, k, v)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    lengths = torch.tensor([200], dtype=torch.int32, device="cuda")
+    assert torch.equal(attention.decode(q[:, -1], k, v, lengths, window, sinks), attention.decode(q[:, -1], k, v, lengths))
+
+
+@pytest.mark.parametrize("where", ["k", "v", "q", "do"])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_one_token_of_nan_in_a_long_sequence(where, dtype):
+    """Rows that do not see it keep their values, also in later rounds of a CTA."""
+    S, H, d, at = 2000, 40, 64, 1000
+    x = dict(zip(("q", "k", "v", "do"), tensors(1, S, S, H, H, d, DTYPES[dtype])))
+    o0, lse0 = attention.forward(x["q"], x["k"], x["v"])
+    g0 = attention.backward(x["do"], x["q"], x["k"], x["v"], o0, lse0)
+    x[where] = x[where].clone()
+    x[where][:, at] = float("nan")
+    o, lse = attention.forward(x["q"], x["k"], x["v"])
+    dq, dk, dv = attention.backward(x["do"], x["q"], x["k"], x["v"], o, lse)
+    rows = torch.arange(S, device="cuda")
+    seers = rows >= at if where in ("k", "v") else rows == at            # queries
+    seen = rows <= (S - 1 if where in ("k", "v") else at)                 # keys of those
+    some = torch.zeros_like(rows, dtype=torch.bool)
+    room = 64 * u(DTYPES[dtype])          # a row from the definition has P and dS in 32 bits
+    for got, want, lost in ((o, o0, some if where == "do" else seers), (dq, g0[0], seers),
+                            (dk, g0[1], seen), (dv, g0[2], some if where == "v" else seen)):
+        assert bool(torch.isnan(got[0][lost]).any(-1).all())
+        a, b = got[0][~lost].double(), want[0][~lost].double()
+        assert bool(((a - b).abs() <= room * b.abs().amax(-1, keepdim=True)).all())
+
+
 def test_zz_no_wait_ran_out():
     assert basp.basp_attention_timeouts() == 0
