@@ -37,8 +37,8 @@ extern "C" {
 #endif
 
 /* One tensor of n elements, in device memory, each buffer dense.  Buffers of one
- * call may not overlap (not checked between tensors, of which there may be
- * thousands). */
+ * call may not overlap (between tensors, of which there may be thousands, only p is
+ * checked: no parameter may come twice). */
 typedef struct basp_adamw_tensor {
     void *p;               /* n of `dtype` (BF16, FP16 or FP32): updated          */
     const void *g;         /* n of `grad_dtype`: `dtype` or FP32                  */

@@ -10,6 +10,8 @@
 // lane, so the largest magnitude is one warp reduction and nothing is read twice.
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "basp_optim.h"
 #include "fp8_common.cuh"
@@ -91,13 +93,7 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t q, float (&v)[4]) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// The root to one unit in the last place, which is enough for what is divided by it, of a
-// v below 2^-126 zero; and a quotient.
-__device__ __forceinline__ float root_of(float x) {
-    float y;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// A quotient to two units in the last place, of a y from 2^-126 to 2^126.
 __device__ __forceinline__ float over(float x, float y) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
@@ -105,7 +101,6 @@ __device__ __forceinline__ float over(float x, float y) {
 }
 
 // What a step does to one element; m and v become m' and v', `root` the root of v'.
-template <bool EXACT_ROOT>
 __device__ __forceinline__ float step_of(const Options &o, float c1, float c2, float p, float g, float &m, float &v,
                                          float &root) {
     // The states' operations are rounded one by one, as 32-bit arithmetic has them and not
@@ -113,7 +108,7 @@ __device__ __forceinline__ float step_of(const Options &o, float c1, float c2, f
     // any other program that follows the formula in 32 bits.
     m = __fadd_rn(__fmul_rn(o.beta1, m), __fmul_rn(o.one_beta1, g));
     v = __fadd_rn(__fmul_rn(o.beta2, v), __fmul_rn(o.one_beta2, __fmul_rn(g, g)));
-    root = EXACT_ROOT ? __fsqrt_rn(v) : root_of(v);
+    root = __fsqrt_rn(v);
     return fmaf(p, o.decay, -c1 * over(m, fmaf(root, c2, o.eps)));
 }
 
@@ -144,7 +139,7 @@ __device__ __forceinline__ void step_block(const Options &o, float c1, float c2,
         m[j] *= sm;
         v[j] *= sv;
         v[j] *= v[j];
-        p[j] = step_of<true>(o, c1, c2, p[j], g[j], m[j], v[j], root[j]);
+        p[j] = step_of(o, c1, c2, p[j], g[j], m[j], v[j], root[j]);
         bits[j] = __float_as_uint(m[j]) & 0x7fffffffu;
         tm = max(tm, bits[j]);
         tv = max(tv, __float_as_uint(root[j]) & 0x7fffffffu);
@@ -206,7 +201,7 @@ __device__ __forceinline__ void do_chunk32(const Entry &e, const Options &o, flo
             const int64_t at = b0 + i * kBlock;
             const int left = int(max(int64_t(0), min(end - at, int64_t(kBlock))));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[i][j] = step_of<false>(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root);
+            for (int j = 0; j < 4; ++j) p[i][j] = step_of(o, c1, c2, p[i][j], g[i][j], m[i][j], v[i][j], root);
             store4<P, HOW>(static_cast<P *>(e.p) + at, lane, left, p[i]);
             store4<float, HOW>(static_cast<float *>(e.m) + at, lane, left, m[i]);
             store4<float, HOW>(static_cast<float *>(e.v) + at, lane, left, v[i]);
@@ -405,6 +400,31 @@ basp_status check_tensor(const basp_adamw_tensor &x, bool eight) {
     return BASP_OK;
 }
 
+// No parameter comes twice: two CTAs would update it at a time.
+basp_status check_apart(const basp_adamw_tensor *list, int64_t count) {
+    struct Span {
+        uintptr_t begin, end;
+        bool operator<(const Span &o) const { return begin < o.begin; }
+    };
+    constexpr int64_t kFew = 512;
+    Span few[kFew];
+    std::unique_ptr<Span[]> many(count > kFew ? new (std::nothrow) Span[size_t(count)] : nullptr);
+    if (count > kFew && many == nullptr) return BASP_ERR_TOO_LARGE;
+    Span *s = count > kFew ? many.get() : few;
+    int64_t n = 0;
+    bool rising = true;                              // as tensors from one allocator often are
+    for (int64_t i = 0; i < count; ++i) {
+        if (list[i].n == 0) continue;
+        const uintptr_t at = uintptr_t(list[i].p);
+        rising = rising && (n == 0 || s[n - 1].begin <= at);
+        s[n++] = {at, at + uintptr_t(list[i].n * elem_size(list[i].dtype))};
+    }
+    if (!rising) std::sort(s, s + n);
+    for (int64_t i = 1; i < n; ++i)
+        if (s[i].begin < s[i - 1].end) return BASP_ERR_ALIASING;
+    return BASP_OK;
+}
+
 }  // namespace
 }  // namespace basp_fp8
 
@@ -432,6 +452,7 @@ extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t coun
         const basp_status st = check_tensor(tensors[i], eight);
         if (st != BASP_OK) return st;
     }
+    if (const basp_status apart = check_apart(tensors, count); apart != BASP_OK) return apart;
 
     Options o = {};
     o.beta1 = float(p.beta1); o.beta2 = float(p.beta2);

@@ -24,7 +24,8 @@ def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weig
     ``step`` counts from 1; as an int32 tensor of one element on the GPU it is read
     when the kernel runs, so that a captured step can be replayed.  The random
     rounding of 8-bit states depends on ``seed``, the step and each element's place
-    alone.  Every tensor is dense, and none overlaps another."""
+    alone.  Every tensor is dense, and none overlaps another: the same parameter
+    twice is refused."""
     m, v = list(m), list(v)
     m_scales = v_scales = None
     if m and isinstance(m[0], fp8.Quantized):
@@ -45,7 +46,8 @@ class AdamW(torch.optim.Optimizer):
 
     ``state_bits`` 32 or 8.  ``seed`` is that of the 8-bit states' rounding.  With
     ``capturable`` the step's number lives on the GPU, so ``step()`` can be captured
-    in a CUDA graph and replayed; without, a capture is refused."""
+    in a CUDA graph and replayed (with the lr and the other options of the capture),
+    once a step has been taken; otherwise a capture is refused."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, seed=0,
                  capturable=False):
@@ -84,6 +86,9 @@ class AdamW(torch.optim.Optimizer):
                 if p.grad is None:
                     continue
                 if not self.state[p]:
+                    if torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError("AdamW: every replay of a captured first step would begin with new states: "
+                                           "take a step before the capture")
                     if first is None:
                         first = torch.zeros(1, dtype=torch.int32, device=p.device) if group["capturable"] else 0
                     self._init(p, group, first)

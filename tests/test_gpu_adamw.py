@@ -315,3 +315,39 @@ def test_autograd_is_told():
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.sum().backward()
     del y
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_tiny_gradients_without_eps(dtype):
+    """v below 2^-126: its root is not, and the step is lr by the first one's definition."""
+    n = 1000
+    g = (random(n, torch.float32, 3).sign() * 2.0 ** -60)
+    p = torch.ones(n, dtype=DTYPES[dtype], device="cuda")
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    optim.adamw([p], [g], [m], [v], 1, lr=0.5, eps=0.0, weight_decay=0.0)
+    # v' = 0.001 * 2^-120 is a multiple of 2^-149: off by 2^-150, 2^-20 of it, its root by half of that
+    want, t = 1 - 0.5 * f64(g.sign()), DTYPES[dtype]
+    assert bool((v > 0).all()) and (np.abs(f64(p) - want) <= 0.5 * 2.0 ** -20 + u(t) * 2).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_first_step_is_not_captured(bits):
+    """Its states would be made anew by every replay."""
+    p = torch.nn.Parameter(torch.ones(300, device="cuda"))
+    p.grad = torch.ones_like(p)
+    o = optim.AdamW([p], state_bits=bits, capturable=True)
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            o.step()
+    torch.cuda.synchronize()
+    assert bool((p == 1).all()) and not o.state.get(p)
+    o.step()
+    torch.cuda.synchronize()
+    assert bool((p < 1).all()) and int(o.state[p]["step"]) == 1
+
+
+def test_a_parameter_does_not_come_twice():
+    p, g, m, v = (torch.ones(200, device="cuda") for _ in range(4))
+    with pytest.raises((ValueError, RuntimeError), match="overlap|alias"):
+        optim.adamw([p, p], [g, g], [m, m.clone()], [v, v.clone()], 1)
+    assert bool((p == 1).all())

@@ -274,3 +274,20 @@ def test_random_bits_are_even():
     for other in (ref.random_bits(n, 6, 17, 2), ref.random_bits(n, 5, 18, 2), ref.random_bits(n, 5, 17, 3)):
         a, b = lo.astype(float) - 32767.5, other[0].astype(float) - 32767.5
         assert abs((a * b).mean() / (65536 ** 2 / 12)) <= 6 / np.sqrt(n)
+
+
+@pytest.mark.parametrize("places,status", [
+    ([1, 10, 1], ALIAS), ([1, 1], ALIAS), ([30, 20, 10, 20], ALIAS), (list(range(10, 10 + 6 * 600, 6)) + [10], ALIAS)])
+def test_a_parameter_does_not_come_twice(lib, places, status):
+    table = (basp.basp_adamw_tensor * len(places))(*(adam(p, g=at(9000), m=at(9001), v=at(9002)) for p in places))
+    assert lib.basp_adamw(table, len(places), basp.basp_adamw_options(**OPTIONS), None) == status
+    part = adam(1, p=at(1) + 396, g=at(9000), m=at(9001), v=at(9002))
+    assert lib.basp_adamw((basp.basp_adamw_tensor * 2)(adam(1), part), 2, basp.basp_adamw_options(**OPTIONS), None) == ALIAS
+
+
+@pytest.mark.parametrize("name", ["q_len", "k_len"])
+def test_the_longest_sequences(lib, name):
+    """A loop over a sequence steps past its end: lengths leave room below 2^31."""
+    assert forward(lib, desc(**{name: 2 ** 31 - 4095})) == LARGE
+    assert basp.basp_attention_decode_workspace(desc(q_len=1, k_len=2 ** 31 - 4095, window=0)) == 0
+    assert basp.basp_attention_decode_workspace(desc(q_len=1, k_len=2 ** 31 - 4096, window=0)) > 0
