@@ -372,9 +372,10 @@ def layernorm_linear_fp8(x, norm_weight, norm_bias, weight, bias=None, residual=
 # ---- attention ---------------------------------------------------------------------
 
 def _aligned(t):
-    """t where a kernel can read its heads in place, else a copy: gradients come in
-    any form (one value spread over the result, for instance)."""
-    if t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]):
+    """t where the kernels of tiles can read its heads in place, else a copy: gradients
+    come in any form (one value, or one token's, spread over the result, for instance)."""
+    if (t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]) and
+            (t.size(1) == 1 or t.stride(1) >= t.size(-1))):
         return t
     return t.contiguous()
 

@@ -139,3 +139,16 @@ def test_example_program(extra):
 
 def test_zz_no_wait_ran_out():
     assert basp.basp_attention_timeouts() == 0 and basp.basp_matmul_fp8_timeouts() == 0
+
+
+@pytest.mark.parametrize("dims", [(0,), (1,), (2,), (0, 1), (0, 1, 2, 3)])
+def test_spread_gradients(dims):
+    """A gradient that is one value, one token's or one head's, spread over the result."""
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(2, 140, h, 64, generator=g).bfloat16().cuda().requires_grad_() for h in (4, 2, 2))
+    shape = [1 if i in dims else n for i, n in enumerate(q.shape)]
+    do = torch.randn(shape, generator=g).bfloat16().cuda()
+    got = torch.autograd.grad(autograd.attention(q, k, v, 60, 3), (q, k, v), do.expand(q.shape))
+    want = torch.autograd.grad(autograd.attention(q, k, v, 60, 3), (q, k, v), do.expand(q.shape).contiguous())
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
