@@ -9,8 +9,12 @@
 //            P^T dO and dk += dS^T Q want them:
 //                S^T = K Q^T,   P^T = 2^(c S^T - lse),   dP^T = V dO^T,
 //                dS^T = P^T (dP^T - D)
-//   dq       128 queries a CTA, over the tiles of keys that they see:
+//   dq       128 queries at a time, over the tiles of keys that they see:
 //                S = Q K^T,   dP = dO V^T,   dq += dS K
+// A window leaves few tiles of keys to one of queries, so the dq kernel's CTAs, one an SM,
+// walk tiles of queries: the next one's loads and first scores run under this one's end (2 x
+// 8192 x 32 heads of 64, window 1024: 271 us; 309 with a CTA for each).
+//
 // That is seven products of a pair of tiles where one kernel with atomics needs five.
 //
 // In both, four warpgroups share a tile's columns, 32 each, a row a thread.  What bounds
@@ -33,7 +37,12 @@
 // sums go to memory and another kernel adds them in order.
 //
 // As in the forward, a row that comes out infinite or NaN is computed again from the
-// definition.
+// definition, where that can differ.
+//
+// Both kernels of 2 x 8192 x 32 heads of 64 over 8 take 570 us with a window of 1024 and 4
+// sinks, 1640 us without a window: 1.19 PFLOP/s of whole tiles' seven products, and as a
+// product of 64 columns takes the tensor cores as long as one of 128, 1.79 of their time.  2 x
+// 16384 x 16 heads of 128, window 4096: 2660 us, 1.34 PFLOP/s.
 #include <cuda.h>
 
 #include <algorithm>
@@ -60,9 +69,10 @@ template <int HD, bool DKV> struct BackSizes {
     // A tile's lse and D: planes of lse, of zeros and of D, of which a product's 16 more of K
     // are the first or the last two.  An infinite D so does not meet the scores.
     static constexpr int kFold = 3 * kFoldPlane;
-    static constexpr int kBarriers = 1 + 2 * kStages + 9;
+    static constexpr int kOwn = !DKV && HD == 64 ? 2 : 1;     // places of the CTA's own Q and dO (or K and V), and of dq
+    static constexpr int kBarriers = (DKV ? 10 : 7 + 4 * kOwn) + 2 * kStages;
     static constexpr int kSmem =
-        1024 + (2 + kStages) * kOperand + (kPlaces + (DKV ? 1 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
+        1024 + (2 * kOwn + kStages) * kOperand + (kPlaces + (DKV ? 1 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -401,25 +411,45 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     if (warp == kTmemWarp) tmem_free<1>(tmem, 512);
 }
 
+// The tile of queries number w, the last queries of every head first.
+struct QueryTile {
+    int b, h, kh, q0;
+    KeyTiles keys;
+    __device__ __forceinline__ QueryTile(const AttentionArgs &a, int w) {
+        const int heads = a.batch * a.hq;
+        h = w % heads % a.hq;
+        b = w % heads / a.hq;
+        kh = h / a.group;
+        q0 = (a.sq_pad / kTile - 1 - w / heads) * kTile;
+        keys = key_tiles(a, q0);
+    }
+};
+
 template <class T, int HD>
 __global__ void __launch_bounds__(kBackThreads, 1)
-attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m) {
+attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m, int items) {
     using Z = BackSizes<HD, false>;
-    constexpr int ST = Z::kStages;
+    constexpr int ST = Z::kStages, OWN = Z::kOwn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    const uint32_t q_at = smem_addr(smem), o_at = q_at + Z::kOperand, ring0 = q_at + 2 * Z::kOperand;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + ST) * Z::kOperand);
-    const uint32_t qo_full = smem_addr(bars), full = qo_full + 8, empty = full + 8 * ST;
+    const uint32_t own0 = smem_addr(smem), ring0 = own0 + 2 * OWN * Z::kOperand;      // [place][Q, dO]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 * OWN + ST) * Z::kOperand);
+    const uint32_t qo_full = smem_addr(bars), qo_empty = qo_full + 8 * OWN, full = qo_empty + 8 * OWN, empty = full + 8 * ST;
     const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, s_taken = dp_full + 8, dp_taken = s_taken + 8;
-    const uint32_t ds_ready = dp_taken + 8, done = ds_ready + 16, drained = done + 8;
+    const uint32_t ds_ready = dp_taken + 8, done = ds_ready + 16, dq_taken = done + 8 * OWN, drained = dq_taken + 8 * OWN;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    uint32_t *bad_rows = tmem_slot + 4;
+    int *bad_from = reinterpret_cast<int *>(tmem_slot + 2);   // the first round with rows that are no numbers
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rounds = (items + int(gridDim.x) - 1) / int(gridDim.x);
 
     if (warp == kLoadWarp && lane == 0) {
-        mbar_init(qo_full, 1);
+        for (int s = 0; s < OWN; ++s) {
+            mbar_init(qo_full + 8 * s, 1);
+            mbar_init(qo_empty + 8 * s, 1);
+            mbar_init(done + 8 * s, 1);
+            mbar_init(dq_taken + 8 * s, kValueWarps);
+        }
         for (int s = 0; s < ST; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
@@ -432,9 +462,9 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         // asked for, and a barrier tells only two phases in a row apart
         mbar_init(ds_ready, kValueWarps);
         mbar_init(ds_ready + 8, kValueWarps);
-        mbar_init(done, 1);
         mbar_init(drained, 1);
         *abort = 0;
+        *bad_from = rounds;
         fence_mbar_init();
         fence_async_shared();
     }
@@ -445,30 +475,35 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     grid_dependency();
     const AttentionWaiter wait{abort, m.timeouts};
-
-    // The last queries, which have the most keys, first.
-    const int heads = a.batch * a.hq, block = int(gridDim.x) / heads - 1 - int(blockIdx.x) / heads;
-    const int h = int(blockIdx.x) % heads % a.hq, b = int(blockIdx.x) % heads / a.hq, kh = h / a.group;
-    const int q0 = block * kTile, shift = a.sk - a.sq;
-    const KeyTiles tiles = key_tiles(a, q0);
-    const int total = tiles.count();
-    // S, dP, two places of dS (64 columns each), dq
+    const int shift = a.sk - a.sq;
+    // S, dP, two places of dS (64 columns each), one of dq or two
     const uint32_t dq_acc = tmem + 384, ds_at = tmem + 256;
 
     if (warp == kLoadWarp) {                                  // loads
-        if (total > 0) {
+        bool ok = true;
+        uint32_t issued = 0;
+        Turn<ST> ring;
+        Turn<OWN> own;
+        uint32_t tiles = 0;
+        for (int r = 0; r < rounds && ok; ++r) {
+            const int w = item_of(r);
+            if (w >= items) continue;
+            const QueryTile t(a, w);
+            if (t.keys.count() == 0) continue;
+            ok = __all_sync(0xffffffffu, wait(qo_empty + 8 * own.at, own.turn ^ 1));
+            if (!ok) break;
             if (elect_one()) {
-                mbar_expect_tx(qo_full, 2 * Z::kOperand);
+                const uint32_t bar = qo_full + 8 * own.at, to = own0 + 2 * own.at * Z::kOperand;
+                mbar_expect_tx(bar, 2 * Z::kOperand);
                 for (int x = 0; x < Z::kBoxes; ++x) {
-                    tma_load_4d(q_at + x * kBox, &m.q, 64 * x, q0, h * m.q_head, b * m.q_batch, qo_full);
-                    tma_load_4d(o_at + x * kBox, &m.d_o, 64 * x, q0, h * m.do_head, b * m.do_batch, qo_full);
+                    tma_load_4d(to + x * kBox, &m.q, 64 * x, t.q0, t.h * m.q_head, t.b * m.q_batch, bar);
+                    tma_load_4d(to + Z::kOperand + x * kBox, &m.d_o, 64 * x, t.q0, t.h * m.do_head, t.b * m.do_batch, bar);
                 }
             }
             __syncwarp();
-            bool ok = true;
-            uint32_t issued = 0;
-            Turn<ST> ring;
-            for (int j = tiles.begin(); j < tiles.high && ok; j = tiles.next(j))
+            own.next();
+            ++tiles;
+            for (int j = t.keys.begin(); j < t.keys.high && ok; j = t.keys.next(j))
                 for (int x = 0; x < 2 && ok; ++x) {           // K, V
                     ok = __all_sync(0xffffffffu, wait(empty + 8 * ring.at, ring.turn ^ 1));
                     if (!ok) break;
@@ -477,25 +512,27 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
                         mbar_expect_tx(bar, Z::kOperand);
                         for (int y = 0; y < Z::kBoxes; ++y)
                             tma_load_4d(to + y * kBox, x == 0 ? &m.k : &m.v, 64 * y, j * kTile,
-                                        kh * (x == 0 ? m.k_head : m.v_head), b * (x == 0 ? m.k_batch : m.v_batch), bar);
+                                        t.kh * (x == 0 ? m.k_head : m.v_head), t.b * (x == 0 ? m.k_batch : m.v_batch), bar);
                     }
                     __syncwarp();
                     ring.next();
                     ++issued;
                 }
-            const uint32_t open = issued < uint32_t(ST) ? issued : ST;
-            for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
-            wait(qo_full, 0, false);
         }
+        // a CTA ends after its copies in flight, also where another warp gave up on them
+        const uint32_t open = issued < uint32_t(ST) ? issued : ST;
+        for (uint32_t i = issued - open; i < issued; ++i) wait(full + 8 * (i % ST), (i / ST) & 1, false);
+        const uint32_t open_own = tiles < uint32_t(OWN) ? tiles : OWN;
+        for (uint32_t i = tiles - open_own; i < tiles; ++i) wait(qo_full + 8 * (i % OWN), (i / OWN) & 1, false);
     } else if (warp == kIssueWarp) {                          // products
-        if (total > 0 && elect_one()) {
+        if (elect_one()) {
             const bool bf16 = std::is_same_v<T, __nv_bfloat16>;
             const int ksteps = (a.d + 15) / 16;
             const uint32_t is = mma_f16_desc(kTile, kTile, bf16, a.scale < 0.f, false);
             const uint32_t idp = mma_f16_desc(kTile, kTile, bf16, false, false);
             const uint32_t io = mma_f16_desc(kTile, ksteps * 16, bf16, false, true);
             Turn<ST> ring;
-            bool ok = wait(qo_full, 0);
+            bool ok = true;
             auto take = [&]() {
                 ok = ok && wait(full + 8 * ring.at, ring.turn);
                 const uint32_t at = ring.at;
@@ -510,126 +547,179 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
                 }
                 mma_commit<1>(bar);
             };
-            uint32_t k_now = 0;
-            // S and dP of a pair of tiles, each once its place has been read; V's place is
-            // free then
-            auto scores = [&](int i) {
-                k_now = take();
-                if (i > 0) ok = ok && wait(s_taken, (i - 1) & 1);
-                if (!ok) return;
-                tcgen05_after_sync();
-                across_head(tmem, q_at, ring0 + k_now * Z::kOperand, is, s_full);
-                const uint32_t v_now = take();
-                if (i > 0) ok = ok && wait(dp_taken, (i - 1) & 1);
-                if (!ok) return;
-                tcgen05_after_sync();
-                across_head(tmem + kTile, o_at, ring0 + v_now * Z::kOperand, idp, dp_full);
-                mma_commit<1>(empty + 8 * v_now);
+            // A pair of tiles; the queries' keys are walked one tile of queries after the other.
+            struct Step {
+                bool there, first, last;
+                uint32_t k_place;
+                Turn<OWN> own;
             };
-            scores(0);
-            for (int i = 0; i < total && ok; ++i) {
-                const uint32_t k_place = k_now;
-                if (i + 1 < total) scores(i + 1);
-                ok = ok && wait(ds_ready + 8 * (i & 1), (i >> 1) & 1);
-                if (!ok) break;
+            int r = -1, j = 0, left = 0;
+            KeyTiles keys = {0, 0, 0};
+            Turn<OWN> own;
+            auto advance = [&]() {
+                Step s = {left > 0, false, false, 0, own};
+                if (left > 0) {
+                    j = keys.next(j);
+                } else {
+                    while (left == 0 && ++r < rounds) {
+                        const int w = item_of(r);
+                        if (w < items) keys = QueryTile(a, w).keys, left = keys.count();
+                    }
+                    if (left == 0) return s;
+                    j = keys.begin();
+                    s.there = s.first = true;
+                }
+                s.last = --left == 0;
+                if (s.last) own.next();
+                return s;
+            };
+            uint32_t made = 0, used = 0;                      // scores, products with dS
+            // S and dP of a pair of tiles, each once its place has been read; V's place is
+            // free then, and after a tile's last pair Q's and dO's
+            auto scores = [&](Step &s) {
+                if (s.first) ok = ok && wait(qo_full + 8 * s.own.at, s.own.turn);
+                const uint32_t q_at = own0 + 2 * s.own.at * Z::kOperand;
+                s.k_place = take();
+                if (made > 0) ok = ok && wait(s_taken, (made - 1) & 1);
+                if (!ok) return;
                 tcgen05_after_sync();
-                const uint64_t dk = desc_k_across(ring0 + k_place * Z::kOperand, kBox);
+                across_head(tmem, q_at, ring0 + s.k_place * Z::kOperand, is, s_full);
+                const uint32_t v_now = take();
+                if (made > 0) ok = ok && wait(dp_taken, (made - 1) & 1);
+                if (!ok) return;
+                tcgen05_after_sync();
+                across_head(tmem + kTile, q_at + Z::kOperand, ring0 + v_now * Z::kOperand, idp, dp_full);
+                mma_commit<1>(empty + 8 * v_now);
+                if (s.last) mma_commit<1>(qo_empty + 8 * s.own.at);
+                ++made;
+            };
+            auto sum = [&](const Step &s) {
+                if (s.first) ok = ok && wait(dq_taken + 8 * s.own.at, s.own.turn ^ 1);
+                ok = ok && wait(ds_ready + 8 * (used & 1), (used >> 1) & 1);
+                if (!ok) return;
+                tcgen05_after_sync();
+                const uint64_t dk = desc_k_across(ring0 + s.k_place * Z::kOperand, kBox);
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_f16_tmem(dq_acc, ds_at + (i & 1) * 64 + 8 * k, dk + k * (16 * 128 / 16), io, i > 0 || k > 0);
-                mma_commit<1>(empty + 8 * k_place);
+                    mma_f16_tmem(dq_acc + s.own.at * HD, ds_at + (used & 1) * 64 + 8 * k, dk + k * (16 * 128 / 16), io, !s.first || k > 0);
+                mma_commit<1>(empty + 8 * s.k_place);
+                if (s.last) mma_commit<1>(done + 8 * s.own.at);
+                ++used;
+            };
+            Step now = advance();
+            if (now.there) scores(now);
+            while (now.there && ok) {
+                Step next = advance();
+                // a tile whose Q and dO come to these ones' place is waited for after this sum
+                const bool early = OWN > 1 || !next.first;
+                if (early && next.there) scores(next);
+                if (ok) sum(now);
+                if (!early && next.there && ok) scores(next);
+                now = next;
             }
-            if (ok) mma_commit<1>(done);
+            // nothing is in flight at the end
             mma_commit<1>(drained);
             wait(drained, 0, false);
         }
     } else if (warp < kValueWarps) {                          // values
-        const int way = warp / 4, quarter = warp % 4, row = q0 + quarter * 32 + lane, p = row + shift;
-        const int p0 = q0 + shift, p1 = min(q0 + kTile, a.sq) - 1 + shift;
+        const int way = warp / 4, quarter = warp % 4;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + kCols * way, tp = ts + kTile;
         const float c = score_scale(a.scale);
-        const bool exists = row < a.sq;
-        const float2 st = a.stats[(int64_t(b) * a.hq + h) * a.sq_pad + row];     // row < sq_pad
-        const float2 c2 = make_float2(c, c), lse2 = make_float2(-st.x, -st.x), d2 = make_float2(-st.y, -st.y);
         bool ok = true;
-        int i = 0;
-        for (int j = tiles.begin(); j < tiles.high; j = tiles.next(j), ++i) {
-            ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
-            if (!ok) break;
-            tcgen05_after_sync();
-            const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + kCols * way;
-            const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
-            uint32_t x[kCols];
-            float ds[kCols];
-            load_columns(ts, x);
-            pass_on(s_taken);
+        uint32_t i = 0;
+        Turn<OWN> own;
+        for (int r = 0; r < rounds; ++r) {
+            const int w = item_of(r);
+            if (w >= items) continue;
+            const QueryTile t(a, w);
+            const int row = t.q0 + quarter * 32 + lane, p = row + shift;
+            const int p0 = t.q0 + shift, p1 = min(t.q0 + kTile, a.sq) - 1 + shift;
+            const bool exists = row < a.sq;
+            const float2 st = a.stats[(int64_t(t.b) * a.hq + t.h) * a.sq_pad + row];     // row < sq_pad
+            const float2 c2 = make_float2(c, c), lse2 = make_float2(-st.x, -st.x), d2 = make_float2(-st.y, -st.y);
+            for (int j = t.keys.begin(); j < t.keys.high && ok; j = t.keys.next(j), ++i) {
+                ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
+                if (!ok) break;
+                tcgen05_after_sync();
+                const int k0 = j * kTile, k1 = k0 + kTile - 1, at0 = k0 + kCols * way;
+                const bool masked = !(k1 <= p0 && (k0 > p1 - a.window || k1 < a.sinks));
+                uint32_t x[kCols];
+                float ds[kCols];
+                load_columns(ts, x);
+                pass_on(s_taken);
 #pragma unroll
-            for (int e = 0; e < kCols; e += 2) {
-                const float2 f = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, lse2);
-                ds[e] = exp2_fast(f.x);
-                ds[e + 1] = exp2_fast(f.y);
-            }
-            ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
-            if (!ok) break;
-            tcgen05_after_sync();
-            load_columns(tp, x);
-            pass_on(dp_taken);
+                for (int e = 0; e < kCols; e += 2) {
+                    const float2 f = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, lse2);
+                    ds[e] = exp2_fast(f.x);
+                    ds[e + 1] = exp2_fast(f.y);
+                }
+                ok = __all_sync(0xffffffffu, wait(dp_full, i & 1));
+                if (!ok) break;
+                tcgen05_after_sync();
+                load_columns(tp, x);
+                pass_on(dp_taken);
 #pragma unroll
-            for (int e = 0; e < kCols; e += 2) {
-                const float2 f = mul2(make_float2(ds[e], ds[e + 1]),
-                                      add2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), d2));
-                ds[e] = f.x;
-                ds[e + 1] = f.y;
+                for (int e = 0; e < kCols; e += 2) {
+                    const float2 f = mul2(make_float2(ds[e], ds[e + 1]),
+                                          add2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), d2));
+                    ds[e] = f.x;
+                    ds[e + 1] = f.y;
+                }
+                if (masked) {
+                    const uint32_t seen = bits_to(p - at0) & (~bits_to(p - a.window - at0) | bits_to(a.sinks - 1 - at0));
+                    keep(ds, seen);
+                }
+                // the place's last product is done: dP(i) was issued after it
+                store_columns<T>(ds_at + lanes + (i & 1) * 64 + kCols / 2 * way, ds);
+                pass_on(ds_ready + 8 * (i & 1));
             }
-            if (masked) {
-                const uint32_t seen = bits_to(p - at0) & (~bits_to(p - a.window - at0) | bits_to(a.sinks - 1 - at0));
-                keep(ds, seen);
+            const bool some = t.keys.count() > 0;
+            if (some) {
+                ok = __all_sync(0xffffffffu, ok && wait(done + 8 * own.at, own.turn));
+                tcgen05_after_sync();
             }
-            // the place's last product is done: dP(i) was issued after it
-            store_columns<T>(ds_at + lanes + (i & 1) * 64 + kCols / 2 * way, ds);
-            pass_on(ds_ready + 8 * (i & 1));
-        }
-        if (total > 0) {
-            ok = __all_sync(0xffffffffu, ok && wait(done, 0));
-            tcgen05_after_sync();
-        }
-        // each warpgroup stores 32 values of a row
-        T *to = row_of<T>(a.dq, b, exists ? row : 0, h);
-        bool finite = true;
-        const int chunks = (a.d + 31) / 32;
-        for (int y = way; y < chunks; y += kWays) {
+            // each warpgroup stores 32 values of a row
+            T *to = row_of<T>(a.dq, t.b, exists ? row : 0, t.h);
+            bool finite = true;
             uint32_t v[32];
-            if (total == 0) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0u;
-            } else if (ok) {
-                tmem_load32(dq_acc + lanes + 32 * y, v);
+            const bool mine = 32 * way < a.d;
+            if (mine && some && ok) {
+                tmem_load32(dq_acc + own.at * HD + lanes + 32 * way, v);
                 tmem_load_wait();
                 tmem_loaded32(v);
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+                for (int e = 0; e < 32; ++e) v[e] = some ? 0x7fffffffu : 0u;
             }
+            if (some) {
+                pass_on(dq_taken + 8 * own.at);
+                own.next();
+            }
+            if (!mine) continue;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
-                uint32_t w[4];
+                uint32_t o[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     const float u = __uint_as_float(v[e + 2 * z]) * a.scale, g = __uint_as_float(v[e + 2 * z + 1]) * a.scale;
-                    if (32 * y + e < a.d) finite = finite && fabsf(u) < INFINITY && fabsf(g) < INFINITY;
-                    w[z] = pack_pair<T>(u, g);
+                    if (32 * way + e < a.d) finite = finite && fabsf(u) < INFINITY && fabsf(g) < INFINITY;
+                    o[z] = pack_pair<T>(u, g);
                 }
-                if (exists && 32 * y + e < a.d)
-                    *reinterpret_cast<uint4 *>(to + 32 * y + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (exists && 32 * way + e < a.d)
+                    *reinterpret_cast<uint4 *>(to + 32 * way + e) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+            if (__any_sync(0xffffffffu, exists && !finite) && lane == 0) atomicMin(bad_from, r);
         }
-        const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
-        if (lane == 0) bad_rows[warp] = bad;
+        // rows that are no numbers, again from the definition
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps) : "memory");
-        uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
-        if (way == 0)
-            for (; again != 0; again &= again - 1)
-                mend_dq_row<T>(a, b, h, q0, q0 + quarter * 32 + __ffs(int(again)) - 1);
+        for (int r = ok ? *bad_from : rounds; r < rounds; ++r) {
+            const int w = item_of(r);
+            if (w >= items || way != r % kWays) continue;
+            const QueryTile t(a, w);
+            const int row0 = t.q0 + quarter * 32, row = row0 + lane;
+            uint32_t again = __ballot_sync(0xffffffffu, row < a.sq && any_in_row<T>(row_of<const T>(a.dq, t.b, row < a.sq ? row : 0, t.h), a.d));
+            for (; again != 0; again &= again - 1) mend_dq_row<T>(a, t.b, t.h, t.q0, row0 + __ffs(int(again)) - 1);
+        }
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -681,12 +771,12 @@ basp_status go(const AttentionArgs &a, const HeadMaps &m, const KeySplit &s, cud
     if (!allow_shared_memory<dq, dq_smem>() || !allow_shared_memory<dkv, dkv_smem>()) return BASP_ERR_CUDA;
     const int64_t heads = int64_t(a.batch) * a.hkv, q = ceil_div(a.sq, kTile) * a.batch * a.hq;
     const int64_t k = (ceil_div(a.sk, kTile) - s.tiles + s.first[s.tiles]) * heads;
-    if (q > kMaxSide || k > kMaxSide) return BASP_ERR_TOO_LARGE;
+    if (q > kMaxSide - 1024 || k > kMaxSide) return BASP_ERR_TOO_LARGE;
     basp_status st = launch(dkv, dim3(unsigned(k)), dim3(kBackThreads), dkv_smem, 1, stream, a, m, s);
     if (st == BASP_OK && s.tiles > 0)
         st = launch(key_join_kernel<T, HD>, dim3(unsigned(s.tiles * heads * (kTile / 8))), dim3(256), 0, 1, stream, a, s);
     if (st != BASP_OK) return st;
-    return launch(dq, dim3(unsigned(q)), dim3(kBackThreads), dq_smem, 1, stream, a, m);
+    return launch(dq, dim3(unsigned(std::min<int64_t>(q, sm_count()))), dim3(kBackThreads), dq_smem, 1, stream, a, m, int(q));
 }
 
 }  // namespace

@@ -71,6 +71,12 @@ __host__ __device__ __forceinline__ QueryTiles query_tiles(const AttentionArgs &
     return {first / kTile, last / kTile + 1};
 }
 
+// A CTA's item in round r of the grid: rounds go to and fro, so that items of falling work
+// come out even.  Past the last one where it is not below their number.
+__device__ __forceinline__ int item_of(int r) {
+    return r * int(gridDim.x) + (r % 2 ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
+}
+
 // Bits 0 to n of a word.
 __device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u; }
 
