@@ -42,7 +42,7 @@
 // Both kernels of 2 x 8192 x 32 heads of 64 over 8 take 570 us with a window of 1024 and 4
 // sinks, 1640 us without a window: 1.19 PFLOP/s of whole tiles' seven products, and as a
 // product of 64 columns takes the tensor cores as long as one of 128, 1.79 of their time.  2 x
-// 16384 x 16 heads of 128, window 4096: 2660 us, 1.34 PFLOP/s.
+// 16384 x 16 heads of 128, window 4096: 2450 us, 1.45 PFLOP/s.
 #include <cuda.h>
 
 #include <algorithm>
@@ -578,17 +578,18 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             // free then, and after a tile's last pair Q's and dO's
             auto scores = [&](Step &s) {
                 if (s.first) ok = ok && wait(qo_full + 8 * s.own.at, s.own.turn);
-                const uint32_t q_at = own0 + 2 * s.own.at * Z::kOperand;
                 s.k_place = take();
                 if (made > 0) ok = ok && wait(s_taken, (made - 1) & 1);
                 if (!ok) return;
                 tcgen05_after_sync();
-                across_head(tmem, q_at, ring0 + s.k_place * Z::kOperand, is, s_full);
+                across_head(tmem, own0 + 2 * s.own.at * Z::kOperand, ring0 + s.k_place * Z::kOperand, is, s_full);
+            };
+            auto gradients = [&](const Step &s) {
                 const uint32_t v_now = take();
                 if (made > 0) ok = ok && wait(dp_taken, (made - 1) & 1);
                 if (!ok) return;
                 tcgen05_after_sync();
-                across_head(tmem + kTile, q_at + Z::kOperand, ring0 + v_now * Z::kOperand, idp, dp_full);
+                across_head(tmem + kTile, own0 + (2 * s.own.at + 1) * Z::kOperand, ring0 + v_now * Z::kOperand, idp, dp_full);
                 mma_commit<1>(empty + 8 * v_now);
                 if (s.last) mma_commit<1>(qo_empty + 8 * s.own.at);
                 ++made;
@@ -605,15 +606,22 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
                 if (s.last) mma_commit<1>(done + 8 * s.own.at);
                 ++used;
             };
+            // The next pair's S before this one's sum; dP as well for heads of 64, whose shorter
+            // sum would wait for it less than it for the sum (all keys 1.69 ms, 1.78 the other
+            // way round), and after it for heads of 128 (16384, window 4096: 2.42 ms for 2.66)
+            constexpr bool BOTH = HD == 64;
             Step now = advance();
             if (now.there) scores(now);
+            if (now.there && ok) gradients(now);
             while (now.there && ok) {
                 Step next = advance();
                 // a tile whose Q and dO come to these ones' place is waited for after this sum
-                const bool early = OWN > 1 || !next.first;
-                if (early && next.there) scores(next);
+                const bool early = next.there && (OWN > 1 || !next.first);
+                if (early) scores(next);
+                if (early && BOTH && ok) gradients(next);
                 if (ok) sum(now);
-                if (!early && next.there && ok) scores(next);
+                if (next.there && !early && ok) scores(next);
+                if (next.there && !(early && BOTH) && ok) gradients(next);
                 now = next;
             }
             // nothing is in flight at the end
