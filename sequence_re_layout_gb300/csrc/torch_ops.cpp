@@ -71,7 +71,8 @@ template <class... A> std::string text(const A &...a) {
 
 const Tensor *tensor(PyObject *o, const char *where, const char *name, bool may_be_none = false) {
     if (o == Py_None && may_be_none) return nullptr;
-    if (!THPVariable_Check(o)) refuse(where, text(name, " must be a tensor"));
+    // the exact types are told without a call
+    if (!THPVariable_CheckTypeExact(Py_TYPE(o)) && !THPVariable_Check(o)) refuse(where, text(name, " must be a tensor"));
     return &THPVariable_Unpack(o);
 }
 
@@ -664,6 +665,8 @@ struct Sequence {                              // a list or tuple, held
     const Tensor &at(Py_ssize_t i, const char *where, const char *name) const {
         return *tensor(PySequence_Fast_GET_ITEM(p, i), where, name);
     }
+    // one that `at` has been asked for
+    const Tensor *seen(Py_ssize_t i) const { return &THPVariable_Unpack(PySequence_Fast_GET_ITEM(p, i)); }
 };
 
 // A dense tensor of n elements in any shape.
@@ -709,12 +712,15 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
     std::vector<basp_adamw_tensor> list(static_cast<size_t>(count));
     const auto state = eight ? at::kFloat8_e4m3fn : at::kFloat;
+    const bool follows = c10::GradMode::is_enabled();
     for (Py_ssize_t i = 0; i < count; ++i) {
         const Tensor &p = params.at(i, where, "a parameter"), &g = grads.at(i, where, "a gradient");
         const Tensor &mi = m.at(i, where, "m"), &vi = v.at(i, where, "v");
-        may_write(&p, where, "a parameter");
-        may_write(&mi, where, "m");
-        may_write(&vi, where, "v");
+        if (follows) {
+            may_write(&p, where, "a parameter");
+            may_write(&mi, where, "m");
+            may_write(&vi, where, "v");
+        }
         basp_adamw_tensor &t = list[size_t(i)];
         t.n = p.numel();
         t.dtype = dtype_code(p.scalar_type(), where, "a parameter");
@@ -735,12 +741,12 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!check(g_lib.adamw(list.data(), count, &o, c10::cuda::getCurrentCUDAStream(device).stream()), "basp_adamw"))
         return nullptr;
     for (Py_ssize_t i = 0; i < count; ++i) {
-        written(&params.at(i, where, "a parameter"));
-        written(&m.at(i, where, "m"));
-        written(&v.at(i, where, "v"));
+        written(params.seen(i));
+        written(m.seen(i));
+        written(v.seen(i));
         if (eight) {
-            written(&ms->at(i, where, "scales of m"));
-            written(&vs->at(i, where, "scales of v"));
+            written(ms->seen(i));
+            written(vs->seen(i));
         }
     }
     Py_RETURN_NONE;

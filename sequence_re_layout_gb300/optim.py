@@ -81,36 +81,45 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             if not group["capturable"] and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("AdamW: a captured step would keep its number: pass capturable=True")
-            together, first = {}, None
+            capturable, first = group["capturable"], None
+            together = {}                             # of each step's number: (parameters, gradients, states)
             for p in group["params"]:
-                if p.grad is None:
+                g = p.grad
+                if g is None:
                     continue
-                if not self.state[p]:
+                s = self.state[p]
+                if not s:
                     if torch.cuda.is_current_stream_capturing():
                         raise RuntimeError("AdamW: every replay of a captured first step would begin with new states: "
                                            "take a step before the capture")
                     if first is None:
-                        first = torch.zeros(1, dtype=torch.int32, device=p.device) if group["capturable"] else 0
-                    self._init(p, group, first)
-                step = self.state[p]["step"]
-                together.setdefault(id(step) if group["capturable"] else step, []).append(p)
-            for params in together.values():
-                self._take(params, group)
+                        first = torch.zeros(1, dtype=torch.int32, device=p.device) if capturable else 0
+                    s = self._init(p, group, first)
+                step = s["step"]
+                number = id(step) if capturable else step
+                lists = together.get(number)
+                if lists is None:
+                    lists = together[number] = [], [], []
+                lists[0].append(p)
+                lists[1].append(g if g.is_contiguous() else g.contiguous())
+                lists[2].append(s)
+            for params, grads, states in together.values():
+                self._take(params, grads, states, group)
         return loss
 
-    def _take(self, params, group):
-        states = [self.state[p] for p in params]
+    def _take(self, params, grads, states, group):
+        step = states[0]["step"]
         if group["capturable"]:
-            states[0]["step"].add_(1)
+            step.add_(1)
         else:
+            step += 1
             for s in states:
-                s["step"] += 1
+                s["step"] = step
         if group["state_bits"] == 32:
             m, v = [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states]
         else:
             m, v = ([fp8.Quantized(s[n], s[n + "_scales"]) for s in states] for n in ("exp_avg", "exp_avg_sq_root"))
-        adamw(params, [p.grad.contiguous() for p in params], m, v, step=states[0]["step"], lr=group["lr"],
-              betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"])
+        adamw(params, grads, m, v, step, group["lr"], group["betas"], group["eps"], group["weight_decay"], group["seed"])
 
     def load_state_dict(self, state_dict):
         """As torch's, but states keep the types they were saved in."""
