@@ -154,15 +154,16 @@ inline void layernorm_backward(basp_dtype dtype, int64_t rows, int64_t cols, con
 // ---- attention (basp_attention.h) and the optimiser's step (basp_optim.h) ------
 
 inline void attention(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,
-                      const basp_heads &v, const basp_heads &o, float *lse, cudaStream_t stream) {
-    check(basp_attention(&desc, &q, &k, &v, &o, lse, stream), "basp_attention");
+                      const basp_heads &v, const basp_heads &o, float *lse, cudaStream_t stream,
+                      const basp_heads *o_rest = nullptr) {
+    check(basp_attention(&desc, &q, &k, &v, &o, o_rest, lse, stream), "basp_attention");
 }
 inline void attention_backward(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,
                                const basp_heads &v, const basp_heads &o, const float *lse,
                                const basp_heads &d_o, const basp_heads &dq, const basp_heads &dk,
                                const basp_heads &dv, void *workspace, size_t workspace_bytes,
-                               cudaStream_t stream) {
-    check(basp_attention_backward(&desc, &q, &k, &v, &o, lse, &d_o, &dq, &dk, &dv, workspace, workspace_bytes,
+                               cudaStream_t stream, const basp_heads *o_rest = nullptr) {
+    check(basp_attention_backward(&desc, &q, &k, &v, &o, o_rest, lse, &d_o, &dq, &dk, &dv, workspace, workspace_bytes,
                                   stream), "basp_attention_backward");
 }
 inline void attention_decode(const basp_attention_desc &desc, const basp_heads &q, const basp_heads &k,

@@ -58,19 +58,23 @@ typedef struct basp_heads {
 
 /*
  * o [batch][Sq][Hq][d] from q (the same), k and v [batch][Sk][Hkv][d].
+ *   o_rest   as o, of 8-bit integers, 8-byte aligned: what o lost when it was rounded, in
+ *            256ths of its last place, or NULL.  The backward's D is then made of both,
+ *            which matters where a query sees few keys
  *   lse      [batch][Hq][Sq] fp32 (the backward takes it), or NULL
  */
 basp_status basp_attention(const basp_attention_desc *desc, const basp_heads *q, const basp_heads *k,
-                           const basp_heads *v, const basp_heads *o, float *lse, cudaStream_t stream);
+                           const basp_heads *v, const basp_heads *o, const basp_heads *o_rest, float *lse,
+                           cudaStream_t stream);
 
 /*
- * Gradients.  o and lse as basp_attention wrote them.
+ * Gradients.  o, o_rest (or NULL) and lse as basp_attention wrote them.
  *   workspace   device scratch of basp_attention_backward_workspace(desc) bytes,
  *               16-byte aligned
  */
 basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q, const basp_heads *k,
-                                    const basp_heads *v, const basp_heads *o, const float *lse,
-                                    const basp_heads *d_o, const basp_heads *dq, const basp_heads *dk,
+                                    const basp_heads *v, const basp_heads *o, const basp_heads *o_rest,
+                                    const float *lse, const basp_heads *d_o, const basp_heads *dq, const basp_heads *dk,
                                     const basp_heads *dv, void *workspace, size_t workspace_bytes,
                                     cudaStream_t stream);
 int64_t basp_attention_backward_workspace(const basp_attention_desc *desc);

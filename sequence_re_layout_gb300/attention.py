@@ -26,16 +26,19 @@ from __future__ import annotations
 from . import fp8
 
 
-def forward(q, k, v, window=None, sinks=0, scale=None, out=None):
+def forward(q, k, v, window=None, sinks=0, scale=None, out=None, rest=None):
     """``(o, lse)``: o like q, or into ``out``; lse float32 [batch, heads, tokens],
     the logarithm of each row's sum of exponentials, which the backward takes.  A
-    query that sees nothing (more queries than keys) has o = 0 and lse = -inf."""
-    return (fp8._ops or fp8._load()).attention(q, k, v, window, sinks, scale, out)
+    query that sees nothing (more queries than keys) has o = 0 and lse = -inf.  An
+    int8 tensor ``rest`` of q's shape gets what o lost when it was rounded."""
+    return (fp8._ops or fp8._load()).attention(q, k, v, window, sinks, scale, out, rest)
 
 
-def backward(do, q, k, v, o, lse, window=None, sinks=0, scale=None):
-    """``(dq, dk, dv)`` of :func:`forward`, contiguous, of the inputs' type."""
-    return (fp8._ops or fp8._load()).attention_backward(do, q, k, v, o, lse, window, sinks, scale)
+def backward(do, q, k, v, o, lse, window=None, sinks=0, scale=None, rest=None):
+    """``(dq, dk, dv)`` of :func:`forward`, contiguous, of the inputs' type.  With the
+    forward's ``rest``, dq and dk are made of an o with 8 bits more: what its rounding
+    adds to their error is most where a query sees few keys."""
+    return (fp8._ops or fp8._load()).attention_backward(do, q, k, v, o, lse, window, sinks, scale, rest)
 
 
 def decode(q, k, v, lengths, window=None, sinks=0, scale=None, out=None):

@@ -383,16 +383,17 @@ def _aligned(t):
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, window, sinks, scale):
-        o, lse = _attention.forward(q, k, v, window, sinks, scale)
-        ctx.save_for_backward(q, k, v, o, lse)
+        rest = torch.empty_like(q, dtype=torch.int8) if ctx.needs_input_grad[0] or ctx.needs_input_grad[1] else None
+        o, lse = _attention.forward(q, k, v, window, sinks, scale, None, rest)
+        ctx.save_for_backward(q, k, v, o, lse, rest)
         ctx.mask = window, sinks, scale
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
-        grads = _attention.backward(_aligned(do), q, k, v, o, lse, *ctx.mask)
+        q, k, v, o, lse, rest = ctx.saved_tensors
+        grads = _attention.backward(_aligned(do), q, k, v, o, lse, *ctx.mask, rest)
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None)
 
 

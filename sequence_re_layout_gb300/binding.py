@@ -166,9 +166,9 @@ def load_library():
     lib.basp_layernorm_backward_workspace.argtypes = [i64, i64]
     lib.basp_layernorm_backward_workspace.restype = i64
     dp, hp = ctypes.POINTER(basp_attention_desc), ctypes.POINTER(basp_heads)
-    lib.basp_attention.argtypes = [dp] + [hp] * 4 + [vp, vp]
+    lib.basp_attention.argtypes = [dp] + [hp] * 5 + [vp, vp]
     lib.basp_attention.restype = ci
-    lib.basp_attention_backward.argtypes = [dp] + [hp] * 4 + [vp] + [hp] * 4 + [vp, sz, vp]
+    lib.basp_attention_backward.argtypes = [dp] + [hp] * 5 + [vp] + [hp] * 4 + [vp, sz, vp]
     lib.basp_attention_backward.restype = ci
     lib.basp_attention_decode.argtypes = [dp] + [hp] * 3 + [vp, hp, vp, sz, vp]
     lib.basp_attention_decode.restype = ci
@@ -615,20 +615,21 @@ def basp_matmul_fp8_timeouts() -> int:
 # basp_adamw_options) are filled by the caller; ``attention`` and ``optim`` have the
 # calls on torch tensors.
 
-def basp_attention(desc, q, k, v, o, lse=None, stream=None):
+def basp_attention(desc, q, k, v, o, lse=None, stream=None, o_rest=None):
     """Attention with a window and sinks; see ``basp_attention.h``."""
-    _check(load_library().basp_attention(desc, q, k, v, o, _ptr(lse), _stream(stream)), "basp_attention")
+    _check(load_library().basp_attention(desc, q, k, v, o, o_rest, _ptr(lse), _stream(stream)), "basp_attention")
 
 
 def basp_attention_backward_workspace(desc) -> int:
     return load_library().basp_attention_backward_workspace(desc)
 
 
-def basp_attention_backward(desc, q, k, v, o, lse, d_o, dq, dk, dv, workspace, workspace_bytes=None, stream=None):
+def basp_attention_backward(desc, q, k, v, o, lse, d_o, dq, dk, dv, workspace, workspace_bytes=None, stream=None,
+                            o_rest=None):
     """Gradients of :func:`basp_attention`; see ``basp_attention.h``."""
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    _check(load_library().basp_attention_backward(desc, q, k, v, o, _ptr(lse), d_o, dq, dk, dv, _ptr(workspace), wb,
-                                                  _stream(stream)), "basp_attention_backward")
+    _check(load_library().basp_attention_backward(desc, q, k, v, o, o_rest, _ptr(lse), d_o, dq, dk, dv, _ptr(workspace),
+                                                  wb, _stream(stream)), "basp_attention_backward")
 
 
 def basp_attention_decode_workspace(desc) -> int:

@@ -43,20 +43,24 @@ template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cud
 }
 
 // The statistics that the backward takes, of a tile of 128 queries a CTA: LANES lanes a
-// row, 16 bytes each.
+// row, 16 bytes each.  Memory is the bound; neighbouring CTAs have neighbouring heads, whose
+// rows lie next to each other.
 template <class T, int LANES>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int ROWS = 256 / LANES, PASSES = kTile / ROWS;
     grid_dependency();
-    const int tiles = a.sq_pad / kTile, tile = int(blockIdx.x % unsigned(tiles)), head = int(blockIdx.x / unsigned(tiles));
-    const int h = head % a.hq, b = head / a.hq, e = int(threadIdx.x % LANES) * 8;
+    const int tiles = a.sq_pad / kTile, h = int(blockIdx.x % unsigned(a.hq)), tile = int(blockIdx.x / unsigned(a.hq) % unsigned(tiles));
+    const int b = int(blockIdx.x / unsigned(a.hq) / unsigned(tiles)), head = b * a.hq + h, e = int(threadIdx.x % LANES) * 8;
     uint4 o[PASSES], g[PASSES];
+    uint2 rest[PASSES];
 #pragma unroll
     for (int x = 0; x < PASSES; ++x) {
         const int i = tile * kTile + x * ROWS + int(threadIdx.x) / LANES;
         const bool in = i < a.sq && e < a.d;
         o[x] = in ? *reinterpret_cast<const uint4 *>(row_of<const T>(a.o, b, i, h) + e) : make_uint4(0, 0, 0, 0);
         g[x] = in ? *reinterpret_cast<const uint4 *>(row_of<const T>(a.d_o, b, i, h) + e) : make_uint4(0, 0, 0, 0);
+        rest[x] = in && a.rest.p != nullptr ? *reinterpret_cast<const uint2 *>(row_of<const int8_t>(a.rest, b, i, h) + e)
+                                            : make_uint2(0, 0);
     }
 #pragma unroll
     for (int x = 0; x < PASSES; ++x) {
@@ -65,7 +69,10 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
         Pack<T>::unpack(o[x], u);
         Pack<T>::unpack(g[x], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(u[j], v[j], s);
+        for (int j = 0; j < 8; ++j) {
+            const int lost = int((j < 4 ? rest[x].x : rest[x].y) << (24 - j % 4 * 8)) >> 24;
+            s = fmaf(with_lost<T>(u[j], lost), v[j], s);
+        }
 #pragma unroll
         for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
         if (threadIdx.x % LANES == 0) {
@@ -133,11 +140,11 @@ bool rows_ok(const basp_attention_desc *d) {
 class HeadArgs {
   public:
     explicit HeadArgs(const basp_attention_desc *d) : d_(d) {}
-    void heads(const basp_heads *t, int64_t len, int64_t heads, bool out) {
+    void heads(const basp_heads *t, int64_t len, int64_t heads, bool out, int64_t esz = 2) {
         if (d_->batch == 0 || len == 0 || heads == 0) return;
         if (t == nullptr || t->data == nullptr || t->stride_batch < 0 || t->stride_seq < 0 || t->stride_head < 0)
             return fail(BASP_ERR_INVALID_ARG);
-        if (uintptr_t(t->data) % 16 || t->stride_batch % 8 || t->stride_seq % 8 || t->stride_head % 8)
+        if (uintptr_t(t->data) % uintptr_t(8 * esz) || t->stride_batch % 8 || t->stride_seq % 8 || t->stride_head % 8)
             return fail(BASP_ERR_ALIGNMENT);
         const int64_t n[3] = {d_->batch, len, heads};
         int64_t s[3] = {t->stride_batch, t->stride_seq, t->stride_head};
@@ -148,7 +155,7 @@ class HeadArgs {
         }
         if (last > (int64_t(1) << 56)) return fail(BASP_ERR_TOO_LARGE);
         if (out && !apart(n, s)) return fail(BASP_ERR_ALIASING);
-        args_.matrix(t->data, 1, int64_t(last) + d_->head_dim, 0, 2, out);
+        args_.matrix(t->data, 1, int64_t(last) + d_->head_dim, 0, esz, out);
     }
     void vector(const void *p, int64_t n, int64_t esz, bool out, bool need = true) {
         args_.matrix(p, n > 0 ? 1 : 0, n, n, esz, out, need);
@@ -263,7 +270,8 @@ template <class F> basp_status with_type(basp_dtype t, F &&f) {
 using namespace basp_fp8;
 
 extern "C" basp_status basp_attention(const basp_attention_desc *desc, const basp_heads *q, const basp_heads *k,
-                                      const basp_heads *v, const basp_heads *o, float *lse, cudaStream_t stream) {
+                                      const basp_heads *v, const basp_heads *o, const basp_heads *o_rest,
+                                      float *lse, cudaStream_t stream) {
     NvtxRange range("basp_attention");
     basp_status st;
     if (!sizes_ok(desc, &st)) return st;
@@ -273,11 +281,13 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
     args.heads(k, desc->k_len, desc->k_heads, false);
     args.heads(v, desc->k_len, desc->k_heads, false);
     args.heads(o, desc->q_len, desc->q_heads, true);
+    if (o_rest != nullptr) args.heads(o_rest, desc->q_len, desc->q_heads, true, 1);
     args.vector(lse, desc->batch * desc->q_heads * desc->q_len, 4, true, false);
     st = args.status();
     if (st != BASP_OK) return st;
     AttentionArgs a = args_of(desc);
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o);
+    a.rest = heads_of(o_rest);
     a.lse = lse;
     if (a.batch == 0 || a.hq == 0 || a.sq == 0) return BASP_OK;
     if (tiled(a)) {
@@ -303,7 +313,7 @@ extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *
 
 extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
                                                const basp_heads *k, const basp_heads *v, const basp_heads *o,
-                                               const float *lse, const basp_heads *d_o, const basp_heads *dq,
+                                               const basp_heads *o_rest, const float *lse, const basp_heads *d_o, const basp_heads *dq,
                                                const basp_heads *dk, const basp_heads *dv, void *workspace,
                                                size_t workspace_bytes, cudaStream_t stream) {
     NvtxRange range("basp_attention_backward");
@@ -315,6 +325,7 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     args.heads(k, desc->k_len, desc->k_heads, false);
     args.heads(v, desc->k_len, desc->k_heads, false);
     args.heads(o, desc->q_len, desc->q_heads, false);
+    if (o_rest != nullptr) args.heads(o_rest, desc->q_len, desc->q_heads, false, 1);
     args.heads(d_o, desc->q_len, desc->q_heads, false);
     args.heads(dq, desc->q_len, desc->q_heads, true);
     args.heads(dk, desc->k_len, desc->k_heads, true);
@@ -331,6 +342,7 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     AttentionArgs a = args_of(desc);
     a.q = heads_of(q); a.k = heads_of(k); a.v = heads_of(v); a.o = heads_of(o); a.d_o = heads_of(d_o);
     a.dq = heads_of(dq); a.dk = heads_of(dk); a.dv = heads_of(dv);
+    a.rest = heads_of(o_rest);
     a.lse = const_cast<float *>(lse);
     a.sq_pad = int(ceil_div(a.sq, kTile) * kTile);
     a.stats = static_cast<float2 *>(workspace);

@@ -21,7 +21,7 @@ template <class T> __device__ __forceinline__ T *row_of(const Heads &t, int64_t 
 }
 
 struct AttentionArgs {
-    Heads q, k, v, o, d_o, dq, dk, dv;
+    Heads q, k, v, o, rest, d_o, dq, dk, dv;     // rest: what o lost in its rounding (lost_of), or none
     float *lse;                          // [batch][Hq][Sq]
     // for the backward: (lse log2(e), D) of each query, [batch][Hq][sq_pad]; of one that
     // does not exist, or sees nothing: (infinity, 0)
@@ -147,6 +147,10 @@ template <class T> __device__ __forceinline__ uint32_t pack_pair(float a, float 
         return *reinterpret_cast<const uint32_t *>(&p);
     }
 }
+template <class T> __device__ __forceinline__ float2 unpack_pair(uint32_t v) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t d;
@@ -182,6 +186,26 @@ __device__ __forceinline__ Sees keys_of(const AttentionArgs &a, int p) {
 // A warp computes one row from its definition, reading nothing but what the row
 // sees: lanes hold a key (or a query) each for the products, then four elements of
 // the row each for the sums.
+
+// What x lost when it was rounded to `rounded` of type T, in 256ths of its last place, cut: the
+// difference of their 32-bit patterns, whose sign is the same, is in the bits that T does not
+// have.  (A value that became 0, or one of fp16's subnormals, has more: as much as fits.)  And x
+// from both, to 2^-17 (fp16: 2^-20) of itself; what is no number stays.
+template <class T> constexpr int kLostShift = std::is_same_v<T, __half> ? 5 : 8;
+template <class T> __device__ __forceinline__ int lost_of(float x, float rounded) {
+    return int(__float_as_uint(x) - __float_as_uint(rounded)) >> kLostShift<T>;
+}
+template <class T> __device__ __forceinline__ float with_lost(float rounded, int lost) {
+    const uint32_t add = (uint32_t(lost) << kLostShift<T>) + (1u << (kLostShift<T> - 1));
+    return fabsf(rounded) < INFINITY ? __uint_as_float(__float_as_uint(rounded) + add) : rounded;
+}
+// Four of them as bytes, each at most 127 and at least -128.
+__device__ __forceinline__ uint32_t lost_bytes(int a, int b, int c, int d) {
+    uint32_t high, all;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(high) : "r"(d), "r"(c), "r"(0));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(all) : "r"(b), "r"(a), "r"(high));
+    return all;
+}
 
 template <class T> __device__ __forceinline__ float row_dot(const T *x, const T *y, int d) {
     float s = 0.f;
@@ -265,6 +289,13 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = any ? o[e] / l : 0.f;
     row_store(row_of<T>(a.o, b, i, h), o, a.d, lane);
+    if (a.rest.p != nullptr) {
+        int8_t *rest = row_of<int8_t>(a.rest, b, i, h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (lane + 32 * e < a.d)
+                rest[lane + 32 * e] = int8_t(max(-128, min(127, lost_of<T>(o[e], Elem<T>::to_float(Elem<T>::from_float(o[e]))))));
+    }
     if (LSE && a.lse != nullptr && lane == 0)
         a.lse[(int64_t(b) * a.hq + h) * a.sq + i] = any ? m + logf(l) : -INFINITY;
 }

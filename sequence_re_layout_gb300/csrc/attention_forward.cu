@@ -53,6 +53,9 @@ template <int HD> struct ForwardSizes {
     static constexpr int kP = kEarly ? 256 : 0, kPStep = kEarly ? 64 : kTile;
     static constexpr int kO = kEarly ? 384 : 256;
 };
+// REST: what o loses in its rounding is stored too.  A kernel of its own, since the branch alone
+// takes 195 us to 202 where it is not (2 x 8192 x 32 heads of 64, window 1024; 212 where it is).
+//
 // Three warpgroups, launched with 168 registers a thread: two softmaxes of 216, and 72
 // for the warps that load and issue (256 x 216 + 128 x 72 = 384 x 168).
 constexpr int kForwardThreads = 384;
@@ -77,7 +80,7 @@ struct Pair {
     }
 };
 
-template <class T, int HD>
+template <class T, int HD, bool REST>
 __global__ void __launch_bounds__(kForwardThreads, 1)
 attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ HeadMaps m, int pairs) {
     using Z = ForwardSizes<HD>;
@@ -381,6 +384,7 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
             const float inv = 1.f / l;
             bool finite = true;
             T *o_row = row_of<T>(a.o, b, exists ? row : 0, h);
+            int8_t *rest_row = REST ? row_of<int8_t>(a.rest, b, exists ? row : 0, h) : nullptr;
             for (int i = 0; i < ochunks; ++i) {
                 uint32_t o[32];
                 if (ok && some) {
@@ -401,8 +405,19 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
                         if (32 * i + e < a.d) finite = finite && fabsf(y) < INFINITY && fabsf(z) < INFINITY;
                         v[x] = pack_pair<T>(y, z);
                     }
-                    if (exists && 32 * i + e < a.d)
+                    if (exists && 32 * i + e < a.d) {
                         *reinterpret_cast<uint4 *>(o_row + 32 * i + e) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if constexpr (REST) {
+                            int lost[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float2 r = unpack_pair<T>(v[x / 2]);
+                                lost[x] = lost_of<T>(any ? __uint_as_float(o[e + x]) * inv : 0.f, x % 2 ? r.y : r.x);
+                            }
+                            *reinterpret_cast<uint2 *>(rest_row + 32 * i + e) =
+                                make_uint2(lost_bytes(lost[0], lost[1], lost[2], lost[3]), lost_bytes(lost[4], lost[5], lost[6], lost[7]));
+                        }
+                    }
                 }
             }
             if (exists && a.lse != nullptr)
@@ -430,13 +445,17 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
     if (warp == 10) tmem_free<1>(tmem, 512);
 }
 
-template <class T, int HD> basp_status go(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
-    constexpr auto kernel = attention_forward_kernel<T, HD>;
+template <class T, int HD, bool REST> basp_status go_for(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
+    constexpr auto kernel = attention_forward_kernel<T, HD, REST>;
     if (!allow_shared_memory<kernel, ForwardSizes<HD>::kSmem>()) return BASP_ERR_CUDA;
     const int64_t pairs = ceil_div(a.sq, 2 * kTile) * a.batch * a.hq;
     if (pairs > kMaxSide - 1024) return BASP_ERR_TOO_LARGE;
     const int64_t ctas = std::min<int64_t>(pairs, sm_count());
     return launch(kernel, dim3(unsigned(ctas)), dim3(kForwardThreads), ForwardSizes<HD>::kSmem, 1, stream, a, m, int(pairs));
+}
+
+template <class T, int HD> basp_status go(const AttentionArgs &a, const HeadMaps &m, cudaStream_t stream) {
+    return a.rest.p != nullptr ? go_for<T, HD, true>(a, m, stream) : go_for<T, HD, false>(a, m, stream);
 }
 
 }  // namespace

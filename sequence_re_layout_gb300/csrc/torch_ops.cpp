@@ -502,8 +502,9 @@ basp_heads heads_of(const Tensor &x, c10::IntArrayRef shape, at::ScalarType type
     if (last == 3 && x.size(1) > 1) h.stride_seq = x.stride(1);
     if (x.size(last - 1) > 1) h.stride_head = x.stride(last - 1);
     if ((h.stride_batch | h.stride_seq | h.stride_head) % 8 != 0)
-        refuse(where, text(name, " must have strides of whole 16 bytes, got strides ", x.strides()));
-    if (reinterpret_cast<uintptr_t>(h.data) % 16 != 0) refuse(where, text(name, " must begin at a multiple of 16 bytes"));
+        refuse(where, text(name, " must have strides of whole ", 8 * x.element_size(), " bytes, got strides ", x.strides()));
+    if (reinterpret_cast<uintptr_t>(h.data) % (8 * x.element_size()) != 0)
+        refuse(where, text(name, " must begin at a multiple of ", 8 * x.element_size(), " bytes"));
     return h;
 }
 
@@ -551,14 +552,15 @@ basp_attention_desc desc_of(const Tensor &q, const Tensor &k, int q_dims, const 
     return d;
 }
 
-// attention(q, k, v, window, sinks, scale, out) -> (o, lse)
+// attention(q, k, v, window, sinks, scale, out, rest) -> (o, lse)
 PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const char *where = "attention";
-    if (!arguments(n, 7, where)) return nullptr;
+    if (!arguments(n, 8, where)) return nullptr;
     const Tensor &q = *tensor(args[0], where, "q"), &k = *tensor(args[1], where, "k"), &v = *tensor(args[2], where, "v");
-    const Tensor *given = tensor(args[6], where, "out", true);
+    const Tensor *given = tensor(args[6], where, "out", true), *rest = tensor(args[7], where, "rest", true);
     may_write(given, where, "out");
+    may_write(rest, where, "rest");
     basp_attention_desc d = desc_of(q, k, 4, where);
     mask_of(&d, args[3], args[4], args[5], where);
     const Call call(q, where, "q");
@@ -569,18 +571,22 @@ PyObject *attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Tensor o = given != nullptr ? *given : new_tensor(q.sizes(), type, q.device());
     const basp_heads ho = heads_of(o, q.sizes(), type, call.device, where, "out");
     const Tensor lse = new_tensor({d.batch, d.q_heads, d.q_len}, at::kFloat, q.device());
-    if (!check(g_lib.attention(&d, &hq, &hk, &hv, &ho, lse.data_ptr<float>(), call.stream), "basp_attention"))
+    basp_heads hr = {};
+    if (rest != nullptr) hr = heads_of(*rest, q.sizes(), at::kChar, call.device, where, "rest");
+    if (!check(g_lib.attention(&d, &hq, &hk, &hv, &ho, rest != nullptr ? &hr : nullptr, lse.data_ptr<float>(), call.stream), "basp_attention"))
         return nullptr;
     written(given);
+    written(rest);
     return tuple(wrap(o), wrap(lse));
     END_HANDLE_TH_ERRORS
 }
 
-// attention_backward(do, q, k, v, o, lse, window, sinks, scale) -> (dq, dk, dv)
+// attention_backward(do, q, k, v, o, lse, window, sinks, scale, rest) -> (dq, dk, dv)
 PyObject *attention_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const char *where = "attention_backward";
-    if (!arguments(n, 9, where)) return nullptr;
+    if (!arguments(n, 10, where)) return nullptr;
+    const Tensor *rest = tensor(args[9], where, "rest", true);
     const Tensor &g = *tensor(args[0], where, "do"), &q = *tensor(args[1], where, "q"), &k = *tensor(args[2], where, "k");
     const Tensor &v = *tensor(args[3], where, "v"), &o = *tensor(args[4], where, "o"), &lse = *tensor(args[5], where, "lse");
     basp_attention_desc d = desc_of(q, k, 4, where);
@@ -592,6 +598,8 @@ PyObject *attention_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const basp_heads hk = heads_of(k, kv, type, call.device, where, "k"), hv = heads_of(v, kv, type, call.device, where, "v");
     const basp_heads ho = heads_of(o, q.sizes(), type, call.device, where, "o");
     const basp_heads hg = heads_of(g, q.sizes(), type, call.device, where, "do");
+    basp_heads hr = {};
+    if (rest != nullptr) hr = heads_of(*rest, q.sizes(), at::kChar, call.device, where, "rest");
     on_device(lse, call.device, where, "lse");
     const int64_t stats[3] = {d.batch, d.q_heads, d.q_len};
     if (lse.scalar_type() != at::kFloat || lse.sizes() != c10::IntArrayRef(stats) || !lse.is_contiguous())
@@ -604,7 +612,7 @@ PyObject *attention_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t bytes = g_lib.attention_backward_workspace(&d);
     Tensor workspace;
     if (bytes > 0) workspace = new_tensor({bytes}, at::kByte, q.device());
-    if (!check(g_lib.attention_backward(&d, &hq, &hk, &hv, &ho, lse.data_ptr<float>(), &hg, &hdq, &hdk, &hdv,
+    if (!check(g_lib.attention_backward(&d, &hq, &hk, &hv, &ho, rest != nullptr ? &hr : nullptr, lse.data_ptr<float>(), &hg, &hdq, &hdk, &hdv,
                                         bytes > 0 ? workspace.data_ptr() : nullptr, size_t(bytes), call.stream),
                "basp_attention_backward"))
         return nullptr;

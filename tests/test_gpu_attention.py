@@ -216,8 +216,9 @@ def test_sizes_of_zero():
 
 def test_autograd():
     q, k, v, do = tensors(2, 200, 200, 4, 2, 64, torch.bfloat16)
-    o, lse = attention.forward(q, k, v, 64, 4)
-    want = attention.backward(do, q, k, v, o, lse, 64, 4)
+    rest = torch.empty_like(q, dtype=torch.int8)
+    o, lse = attention.forward(q, k, v, 64, 4, rest=rest)
+    want = attention.backward(do, q, k, v, o, lse, 64, 4, rest=rest)
     leaves = [x.clone().requires_grad_() for x in (q, k, v)]
     got = autograd.attention(*leaves, window=64, sinks=4)
     got.backward(do)
@@ -231,7 +232,7 @@ def test_autograd():
             assert torch.equal(a.grad, b) if need >> i & 1 else a.grad is None
     one = [x.clone().requires_grad_() for x in (q, k, v)]
     autograd.attention(*one, window=64, sinks=4).sum().backward()            # a gradient spread from one value
-    ones = attention.backward(torch.ones_like(do), q, k, v, o, lse, 64, 4)
+    ones = attention.backward(torch.ones_like(do), q, k, v, o, lse, 64, 4, rest=rest)
     assert all(torch.equal(a.grad, b) for a, b in zip(one, ones))
 
 
@@ -378,6 +379,34 @@ def test_gradients_past_fp16():
     assert np.abs((f64(do * 400)[0] * r.o).sum(-1)).max() > 65504
     for name, g in zip(("dq", "dk"), got):
         close(g[0], want[name], bound[name])
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("Sq,Sk,d,window,sinks", [(300, 300, 64, 4, 0), (300, 300, 128, 2, 1), (130, 400, 40, 17, 3),
+                                                  (400, 150, 72, None, 0), (1, 1, 8, None, 0)])
+def test_what_the_rounding_lost(Sq, Sk, d, window, sinks, dtype):
+    """o and `rest` are o with 8 bits more; D, and with it dq and dk, are of both."""
+    t = DTYPES[dtype]
+    q, k, v, do = tensors(2, Sq, Sk, 4, 2, d, t)
+    rest = torch.full(q.shape, 77, dtype=torch.int8, device="cuda")
+    o, lse = attention.forward(q, k, v, window, sinks, rest=rest)
+    assert torch.equal(o, attention.forward(q, k, v, window, sinks)[0])
+    packed = torch.full((2, Sq, 5, d), 77, dtype=torch.int8, device="cuda")
+    attention.forward(q, k, v, window, sinks, rest=packed[:, :, 1:])
+    assert torch.equal(packed[:, :, 1:], rest) and bool((packed[:, :, 0] == 77).all())
+    grads = attention.backward(do, q, k, v, o, lse, window, sinks, rest=rest)
+    assert all(torch.equal(a, b) for a, b in zip(grads, attention.backward(do, q, k, v, o, lse, window, sinks, rest=packed[:, :, 1:])))
+    # o's bits as a float32, and 256ths of its last place
+    both = (o.float().view(torch.int32) + rest.int() * (256 if t == torch.bfloat16 else 32)).view(torch.float32)
+    for b in range(2):
+        r = Attention(f64(q[b]), f64(k[b]), f64(v[b]), window, sinks, d ** -0.5, u(t))
+        # o's own rounding is replaced by half a 256th of the last place; the largest loss, half of it, is one
+        # 256th too far; subnormals of fp16 (TINY in o_bound) stay
+        less = r.o_bound - u(t) * np.abs(r.o) + u(t) / 64 * (np.abs(r.o) + r.o_bound)
+        assert (np.abs(f64(both[b]) - r.o) <= less).all()
+        want, bound = r.backward(f64(do[b]), less)
+        for name, g in zip(("dq", "dk", "dv"), grads):
+            close(g[b], want[name], bound[name])
 
 
 @pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 62, 2 ** 62), (50, 2 ** 31 - 1)])

@@ -142,3 +142,33 @@ def test_two_streams_at_a_time():
         for a, b in zip(want, got):
             assert all(torch.equal(c, e) for c, e in zip(a, b))
     assert np.isfinite(f64(want[0][0])).all()
+
+
+def test_two_graphs_at_a_time():
+    """Two captured calls of each kind, replayed on two streams at once, share no workspace."""
+    S, H, d = 1200, 4, 128
+    x = [[random(2, S, H, d, dtype=BF16, seed=20 * i + j) for j in range(4)] for i in range(2)]
+    lengths = torch.tensor([S, 321], dtype=torch.int32, device="cuda")
+
+    def work(q, k, v, do):
+        rest = torch.empty(q.shape, dtype=torch.int8, device="cuda")
+        o, lse = attention.forward(q, k, v, None, 0, rest=rest)
+        a, w = q.view(-1, H * d), k.view(-1, H * d)[0]
+        y, _, mean, rstd = fp8.layernorm(a, w, quantized=False)
+        return [o, lse, rest, *attention.backward(do, q, k, v, o, lse, rest=rest),
+                attention.decode(q[:, -1], k, v, lengths), *fp8.layernorm_backward(y, a, mean, rstd, w)]
+
+    want = [work(*i) for i in x]
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, i in zip(graphs, x):
+        with torch.cuda.graph(g):
+            got.append(work(*i))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(c, e) for c, e in zip(a, b))

@@ -86,7 +86,7 @@ def heads(n, length, count, d=64, **change):
 
 
 def forward(lib, d, **change):
-    a = dict(q=heads(1, 100, 6), k=heads(2, 300, 3), v=heads(3, 300, 3), o=heads(4, 100, 6), lse=at(5))
+    a = dict(q=heads(1, 100, 6), k=heads(2, 300, 3), v=heads(3, 300, 3), o=heads(4, 100, 6), rest=None, lse=at(5))
     return lib.basp_attention(d, *{**a, **change}.values(), None)
 
 
@@ -113,6 +113,9 @@ def test_attention_desc_refusals(lib, change, status):
     (dict(k=heads(2, 300, 3, stride_seq=196)), ALIGN), (dict(v=heads(3, 300, 3, stride_head=60)), ALIGN),
     (dict(o=heads(4, 100, 6, stride_head=0)), ALIAS), (dict(o=heads(4, 100, 6, stride_seq=64)), ALIAS),
     (dict(o=heads(4, 100, 6, stride_head=56)), ALIAS), (dict(o=heads(1, 100, 6)), ALIAS), (dict(o=heads(2, 100, 6)), ALIAS),
+    (dict(rest=heads(4, 100, 6)), ALIAS), (dict(rest=heads(1, 100, 6)), ALIAS), (dict(rest=heads(7, 100, 6, stride_head=0)), ALIAS),
+    (dict(rest=heads(7, 100, 6, data=at(7) + 4)), ALIGN), (dict(rest=heads(7, 100, 6, data=None)), INVALID),
+    (dict(rest=heads(7, 100, 6, stride_seq=388)), ALIGN),
     (dict(lse=at(4)), ALIAS), (dict(lse=at(5) + 2), ALIGN), (dict(k=heads(2, 300, 3, stride_batch=1 << 57)), LARGE),
 ])
 def test_attention_refusals(lib, change, status):
@@ -129,11 +132,12 @@ def test_attention_of_nothing(lib):
     (dict(d_o=None), INVALID), (dict(lse=None), INVALID), (dict(dq=None), INVALID), (dict(dk=None), INVALID),
     (dict(dv=heads(3, 300, 3)), ALIAS), (dict(dk=heads(9, 300, 3)), ALIAS), (dict(dq=heads(4, 100, 6)), ALIAS),
     (dict(dv=heads(9, 300, 3, stride_batch=0)), ALIAS), (dict(ws=None), WORKSPACE), (dict(wsb=1), WORKSPACE),
+    (dict(rest=heads(12, 100, 6, data=None)), INVALID), (dict(rest=heads(7, 100, 6)), ALIAS), (dict(rest=heads(11, 100, 6)), ALIAS),
     (dict(ws=at(11) + 8), ALIGN), (dict(ws=at(8)), ALIAS), (dict(dk=heads(8, 300, 3, data=at(8) + 2)), ALIGN),
 ])
 def test_attention_backward_refusals(lib, change, status):
     d = desc()
-    a = dict(q=heads(1, 100, 6), k=heads(2, 300, 3), v=heads(3, 300, 3), o=heads(4, 100, 6), lse=at(5), d_o=heads(6, 100, 6),
+    a = dict(q=heads(1, 100, 6), k=heads(2, 300, 3), v=heads(3, 300, 3), o=heads(4, 100, 6), rest=None, lse=at(5), d_o=heads(6, 100, 6),
              dq=heads(7, 100, 6), dk=heads(8, 300, 3), dv=heads(9, 300, 3), ws=at(11),
              wsb=basp.basp_attention_backward_workspace(d))
     assert lib.basp_attention_backward(d, *{**a, **change}.values(), None) == status
