@@ -43,11 +43,12 @@ template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cud
 }
 
 // The statistics that the backward takes, of a tile of 128 queries a CTA: LANES lanes a
-// row, 16 bytes each.  Memory is the bound; neighbouring CTAs have neighbouring heads, whose
-// rows lie next to each other.
+// row, 16 bytes each, and then a thread a row.  Memory is the bound; neighbouring CTAs have
+// neighbouring heads, whose rows lie next to each other.
 template <class T, int LANES>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int ROWS = 256 / LANES, PASSES = kTile / ROWS;
+    __shared__ float sums[kTile];
     grid_dependency();
     const int tiles = a.sq_pad / kTile, h = int(blockIdx.x % unsigned(a.hq)), tile = int(blockIdx.x / unsigned(a.hq) % unsigned(tiles));
     const int b = int(blockIdx.x / unsigned(a.hq) / unsigned(tiles)), head = b * a.hq + h, e = int(threadIdx.x % LANES) * 8;
@@ -62,42 +63,45 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
         rest[x] = in && a.rest.p != nullptr ? *reinterpret_cast<const uint2 *>(row_of<const int8_t>(a.rest, b, i, h) + e)
                                             : make_uint2(0, 0);
     }
+    const int row = int(threadIdx.x), i = tile * kTile + row;
+    const bool sees = row < kTile && i < a.sq && i + a.sk - a.sq >= 0;
+    const float lse = sees ? a.lse[int64_t(head) * a.sq + i] * kLog2e : 0.f;
 #pragma unroll
     for (int x = 0; x < PASSES; ++x) {
-        const int i = tile * kTile + x * ROWS + int(threadIdx.x) / LANES;
         float u[8], v[8], s = 0.f;
         Pack<T>::unpack(o[x], u);
         Pack<T>::unpack(g[x], v);
+        if (a.rest.p != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int lost = int((j < 4 ? rest[x].x : rest[x].y) << (24 - j % 4 * 8)) >> 24;
-            s = fmaf(with_lost<T>(u[j], lost), v[j], s);
+            for (int j = 0; j < 8; ++j)
+                u[j] = with_lost<T>(u[j], int((j < 4 ? rest[x].x : rest[x].y) << (24 - j % 4 * 8)) >> 24);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(u[j], v[j], s);
 #pragma unroll
         for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        if (threadIdx.x % LANES == 0) {
-            const bool sees = i < a.sq && i + a.sk - a.sq >= 0;
-            const float lse = sees ? a.lse[int64_t(head) * a.sq + i] * kLog2e : 0.f;
-            a.stats[int64_t(head) * a.sq_pad + i] = sees ? make_float2(lse, s) : make_float2(INFINITY, 0.f);
-            // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that
-            // the rows that meet it are made from the definition
-            const float sign = a.scale < 0.f ? 1.f : -1.f;        // the other side of the product is negated
-            float part[8], rest = sees ? sign * lse / score_scale(a.scale) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float unit = fold_unit<T>(j % 4);
-                if (j == 4) rest = sees ? -s : 0.f;
-                part[j] = unit == 0.f ? 0.f : Elem<T>::to_float(Elem<T>::from_float(rest / unit));
-                if (!(fabsf(part[j]) < INFINITY)) part[j] = __uint_as_float(0x7fffffffu);
-                rest -= part[j] * unit;
-            }
-            uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32 +
-                          fold_offset(i - tile * kTile);
-            const uint4 w = Pack<T>::pack(part);
-            *reinterpret_cast<uint4 *>(to) = make_uint4(w.x, w.y, 0, 0);
-            *reinterpret_cast<uint4 *>(to + kFoldPlane) = make_uint4(w.z, w.w, 0, 0);
-        }
+        if (threadIdx.x % LANES == 0) sums[x * ROWS + threadIdx.x / LANES] = s;
     }
+    __syncthreads();
+    if (row >= kTile) return;
+    const float s = sums[row];
+    a.stats[int64_t(head) * a.sq_pad + i] = sees ? make_float2(lse, s) : make_float2(INFINITY, 0.f);
+    // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that the rows
+    // that meet it are made from the definition
+    const float sign = a.scale < 0.f ? 1.f : -1.f;                // the other side of the product is negated
+    float part[8], left = sees ? sign * lse / score_scale(a.scale) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float unit = fold_unit<T>(j % 4);
+        if (j == 4) left = sees ? -s : 0.f;
+        part[j] = unit == 0.f ? 0.f : Elem<T>::to_float(Elem<T>::from_float(left / unit));
+        if (!(fabsf(part[j]) < INFINITY)) part[j] = __uint_as_float(0x7fffffffu);
+        left -= part[j] * unit;
+    }
+    uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32 + fold_offset(row);
+    const uint4 w = Pack<T>::pack(part);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(w.x, w.y, 0, 0);
+    *reinterpret_cast<uint4 *>(to + kFoldPlane) = make_uint4(w.z, w.w, 0, 0);
 }
 template <class T> basp_status launch_stats(const AttentionArgs &a, cudaStream_t stream) {
     const int64_t ctas = int64_t(a.sq_pad / kTile) * a.batch * a.hq;
