@@ -42,7 +42,7 @@
 // Both kernels of 2 x 8192 x 32 heads of 64 over 8 take 570 us with a window of 1024 and 4
 // sinks, 1680 us without a window (1.16 PFLOP/s of whole tiles' seven products): half of the
 // issue slots and of the tensor cores' cycles, so what bounds them is still the chain of a pair
-// of tiles.  2 x 16384 x 16 heads of 128, window 4096: 2450 us, 1.45 PFLOP/s; 73 % (dk, dv) and
+// of tiles.  2 x 16384 x 16 heads of 128, window 4096: 2430 us, 1.47 PFLOP/s; 73 % (dk, dv) and
 // 58 % (dq, before the order of its products changed) of the tensor cores' cycles.
 #include <cuda.h>
 
