@@ -385,8 +385,9 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
             bool finite = true;
             T *o_row = row_of<T>(a.o, b, exists ? row : 0, h);
             int8_t *rest_row = REST ? row_of<int8_t>(a.rest, b, exists ? row : 0, h) : nullptr;
+            const bool rest16 = REST && (uintptr_t(a.rest.p) | uint64_t(a.rest.sb | a.rest.ss | a.rest.sh)) % 16 == 0;
             for (int i = 0; i < ochunks; ++i) {
-                uint32_t o[32];
+                uint32_t o[32], lost[8];
                 if (ok && some) {
                     tmem_load32(to + 32 * i, o);
                     tmem_load_wait();
@@ -405,20 +406,31 @@ attention_forward_kernel(const __grid_constant__ AttentionArgs a, const __grid_c
                         if (32 * i + e < a.d) finite = finite && fabsf(y) < INFINITY && fabsf(z) < INFINITY;
                         v[x] = pack_pair<T>(y, z);
                     }
-                    if (exists && 32 * i + e < a.d) {
+                    if (exists && 32 * i + e < a.d)
                         *reinterpret_cast<uint4 *>(o_row + 32 * i + e) = make_uint4(v[0], v[1], v[2], v[3]);
-                        if constexpr (REST) {
-                            int lost[8];
+                    if constexpr (REST) {
+                        int x[8];
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float2 r = unpack_pair<T>(v[x / 2]);
-                                lost[x] = lost_of<T>(any ? __uint_as_float(o[e + x]) * inv : 0.f, x % 2 ? r.y : r.x);
-                            }
-                            *reinterpret_cast<uint2 *>(rest_row + 32 * i + e) =
-                                make_uint2(lost_bytes(lost[0], lost[1], lost[2], lost[3]), lost_bytes(lost[4], lost[5], lost[6], lost[7]));
+                        for (int y = 0; y < 8; ++y) {
+                            const float2 r = unpack_pair<T>(v[y / 2]);
+                            x[y] = lost_of<T>(any ? __uint_as_float(o[e + y]) * inv : 0.f, y % 2 ? r.y : r.x);
                         }
+                        lost[e / 4] = lost_bytes(x[0], x[1], x[2], x[3]);
+                        lost[e / 4 + 1] = lost_bytes(x[4], x[5], x[6], x[7]);
                     }
                 }
+                if constexpr (REST)                           // 16 bytes at a time where that can be
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int at = 32 * i + 16 * x;
+                        if (!exists) continue;
+                        if (rest16 && at + 16 <= a.d) {
+                            *reinterpret_cast<uint4 *>(rest_row + at) = make_uint4(lost[4 * x], lost[4 * x + 1], lost[4 * x + 2], lost[4 * x + 3]);
+                        } else {
+                            if (at < a.d) *reinterpret_cast<uint2 *>(rest_row + at) = make_uint2(lost[4 * x], lost[4 * x + 1]);
+                            if (at + 8 < a.d) *reinterpret_cast<uint2 *>(rest_row + at + 8) = make_uint2(lost[4 * x + 2], lost[4 * x + 3]);
+                        }
+                    }
             }
             if (exists && a.lse != nullptr)
                 a.lse[(int64_t(b) * a.hq + h) * a.sq + row] =
