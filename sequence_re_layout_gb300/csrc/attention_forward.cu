@@ -54,7 +54,7 @@ template <int HD> struct ForwardSizes {
     static constexpr int kO = kEarly ? 384 : 256;
 };
 // REST: what o loses in its rounding is stored too.  A kernel of its own, since the branch alone
-// takes 195 us to 202 where it is not (2 x 8192 x 32 heads of 64, window 1024; 212 where it is).
+// takes 195 us to 202 where it is not (2 x 8192 x 32 heads of 64, window 1024; 207 where it is).
 //
 // Three warpgroups, launched with 168 registers a thread: two softmaxes of 216, and 72
 // for the warps that load and issue (256 x 216 + 128 x 72 = 384 x 168).
