@@ -6,6 +6,10 @@
 // parameter (up to 32 KB, copied with the launch, so there is nothing to keep or to
 // upload) and a grid of chunks; a CTA finds its chunk's tensor by bisection.
 //
+// 50 million fp32 values: 204 us, at a copy's rate (some of it stays in L2).  Four such with
+// 8-bit states: 560 us, 0.86 of a copy's rate; issue slots bound it (86 % of them), 46 us of it
+// the root to its last bit.
+//
 // 8-bit states have a scale for each 128 elements, which one warp holds, four a
 // lane, so the largest magnitude is one warp reduction and nothing is read twice.
 #include <algorithm>
@@ -216,8 +220,8 @@ static_assert(kRun == 16, "a lane for each scale of a run, of m and of v");
 
 // The buffers allow four elements at a time: each lane copies what it will read itself
 // to shared memory, kStages - 1 blocks ahead.  What bounds this kernel otherwise is the
-// number of bytes in flight: 1165 us for four layers of 50 million elements with the loads
-// of two blocks in registers.
+// number of bytes in flight: 1165 us for four layers of 50 million elements, not 560, with
+// the loads of two blocks in registers.
 constexpr int kStages = 4, kStageBytes = 32 * (16 + 16 + 4 + 4);
 
 template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool have) {

@@ -409,6 +409,37 @@ def test_what_the_rounding_lost(Sq, Sk, d, window, sinks, dtype):
             close(g[b], want[name], bound[name])
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_what_the_rounding_lost_of_spread_tensors(dtype):
+    """Rows from the definition: keys that are one token's, which TMA cannot address; and a NaN that some do not see."""
+    t, S, d = DTYPES[dtype], 150, 64
+    q, k, v, do = tensors(1, S, S, 2, 1, d, t)
+    r = Attention(f64(q[0]), f64(k[:, :1].expand(1, S, 1, d)[0]), f64(v[0]), 40, 2, d ** -0.5, u(t))
+    rest = torch.full(q.shape, 77, dtype=torch.int8, device="cuda")
+    o, _ = attention.forward(q, k[:, :1].expand(1, S, 1, d), v, 40, 2, rest=rest)
+    def both(rows):
+        unit = 256 if t == torch.bfloat16 else 32
+        return (o.float().view(torch.int32) + rest.int() * unit).view(torch.float32)[0, rows]
+    less = r.o_bound - u(t) * np.abs(r.o) + u(t) / 64 * (np.abs(r.o) + r.o_bound)
+    assert (np.abs(f64(both(slice(None))) - r.o) <= less).all()
+    r = Attention(f64(q[0]), f64(k[0]), f64(v[0]), 40, 2, d ** -0.5, u(t))
+    less = r.o_bound - u(t) * np.abs(r.o) + u(t) / 64 * (np.abs(r.o) + r.o_bound)
+    v[0, 70] = float("nan")
+    o, _ = attention.forward(q, k, v, 40, 2, rest=rest)
+    for rows in (slice(0, 70), slice(110, S)):
+        assert (np.abs(f64(both(rows)) - r.o[rows]) <= less[rows]).all()
+
+
+def test_refusals_of_rest():
+    q, k, v, _ = tensors(1, 20, 20, 2, 1, 64, torch.bfloat16)
+    whole = torch.zeros(1, 20, 2, 72, dtype=torch.int8, device="cuda")
+    for rest in (torch.zeros_like(q), whole[..., :56], whole[..., 4:68], whole.cpu()[..., :64],
+                 torch.zeros(1, 20, 2, 68, dtype=torch.int8, device="cuda")[..., :64], 3):
+        with pytest.raises(ValueError, match="rest"):
+            attention.forward(q, k, v, rest=rest)
+    attention.forward(q, k, v, rest=whole[..., 8:])
+
+
 @pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 62, 2 ** 62), (50, 2 ** 31 - 1)])
 def test_masks_past_every_length(window, sinks):
     q, k, v, do = tensors(1, 150, 200, 2, 1, 64, torch.bfloat16)
