@@ -14,9 +14,10 @@
 // One sequence of 16001 keys, 8 key heads of 64: 11.2 us (38 with the loads in registers); 32
 // of up to 16384, 16 of 128, window 4096: 63.6 us, 0.66 of a copy's rate (84).
 //
-// The sum over a head's values may be taken in any order, so lane t of four takes the values 8 t + 32 c .. + 7 of a key for both operands, as they lie; for the
-// product with V, lane g of eight takes the columns 8 g + 64 c .. + 7 of its four keys, and
-// pairs of keys are put together by byte permutations.
+// The sum over a head's values may be taken in any order, so lane t of four takes the values
+// 8 t + 32 c .. + 7 of a key for both operands, as they lie; for the product with V, lane g
+// of eight takes the columns 8 g + 64 c .. + 7 of its four keys, and pairs of keys are put
+// together by byte permutations.
 #include <algorithm>
 
 #include "attention.cuh"
