@@ -408,50 +408,57 @@ __global__ void __launch_bounds__(THREADS) layer_back_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0.f;
         }
-        auto walk = [&](auto how) {
+        // a warp whose blocks all end inside the row needs no checks; the barrier of the row's
+        // sums is for all warps, and so outside of what they do differently
+        const bool whole = !VEC && (warp + (NB - 1) * warps + 1) * kBlock <= a.cols;
+        float g[NB][4], n[NB][4], dot, all;
+        auto read = [&](auto how, const T *dy, const T *h, float mean, float rstd) {
             constexpr int H = decltype(how)::value;
-            for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-                const T *dy = static_cast<const T *>(a.dy) + row * a.dys;
-                const T *h = static_cast<const T *>(a.h) + row * a.hs;
-                const T *dh = static_cast<const T *>(a.dh) + row * a.dhs;
-                const float mean = a.mean[row], rstd = a.rstd[row];
-                float g[NB][4], n[NB][4];
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int c = (warp + i * warps) * kBlock;
-                    load4<T, H>(dy + c, lane, a.cols - c, g[i]);
-                    load4<T, H>(h + c, lane, a.cols - c, n[i]);
+            for (int i = 0; i < NB; ++i) {
+                const int c = (warp + i * warps) * kBlock;
+                load4<T, H>(dy + c, lane, a.cols - c, g[i]);
+                load4<T, H>(h + c, lane, a.cols - c, n[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = inside<H>(lane, j, a.cols - (warp + i * warps) * kBlock);
+                    n[i][j] = in ? (n[i][j] - mean) * rstd : 0.f;
+                    dw[i][j] += g[i][j] * n[i][j];
+                    db[i][j] += g[i][j];
+                    g[i][j] *= wv[i][j];
+                    all += g[i][j];
+                    dot += g[i][j] * n[i][j];
                 }
-                float dot = 0.f, all = 0.f;
+        };
+        auto write = [&](auto how, const T *dh, T *dx, float mg, float mn, float rstd) {
+            constexpr int H = decltype(how)::value;
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < NB; ++i) {
+                const int c = (warp + i * warps) * kBlock;
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                if (a.dh != nullptr) load4<T, H>(dh + c, lane, a.cols - c, d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool in = inside<H>(lane, j, a.cols - (warp + i * warps) * kBlock);
-                        n[i][j] = in ? (n[i][j] - mean) * rstd : 0.f;
-                        dw[i][j] += g[i][j] * n[i][j];
-                        db[i][j] += g[i][j];
-                        g[i][j] *= wv[i][j];
-                        all += g[i][j];
-                        dot += g[i][j] * n[i][j];
-                    }
-                // two buffers in turn: a warp can be one row ahead of another
-                const float2 s = row_sum2(all, dot, part[turn], warps);
-                const float mg = s.x * a.inv_cols, mn = s.y * a.inv_cols;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int c = (warp + i * warps) * kBlock;
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (a.dh != nullptr) load4<T, H>(dh + c, lane, a.cols - c, d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[j] += rstd * (g[i][j] - mg - n[i][j] * mn);
-                    store4<T, H>(static_cast<T *>(a.dx) + row * a.dxs + c, lane, a.cols - c, d);
-                }
+                for (int j = 0; j < 4; ++j) d[j] += rstd * (g[i][j] - mg - n[i][j] * mn);
+                store4<T, H>(dx + c, lane, a.cols - c, d);
             }
         };
-        // a warp whose blocks all end inside the row needs no checks
-        if (!VEC && (warp + (NB - 1) * warps + 1) * kBlock <= a.cols) walk(How<kWhole>());
-        else walk(How<VEC>());
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+            const T *dy = static_cast<const T *>(a.dy) + row * a.dys, *h = static_cast<const T *>(a.h) + row * a.hs;
+            const T *dh = static_cast<const T *>(a.dh) + row * a.dhs;
+            T *dx = static_cast<T *>(a.dx) + row * a.dxs;
+            const float mean = a.mean[row], rstd = a.rstd[row];
+            dot = all = 0.f;
+            if (whole) read(How<kWhole>(), dy, h, mean, rstd);
+            else read(How<VEC>(), dy, h, mean, rstd);
+            // two buffers in turn: a warp can be one row ahead of another
+            const float2 s = row_sum2(all, dot, part[turn], warps);
+            const float mg = s.x * a.inv_cols, mn = s.y * a.inv_cols;
+            if (whole) write(How<kWhole>(), dh, dx, mg, mn, rstd);
+            else write(How<VEC>(), dh, dx, mg, mn, rstd);
+        }
         if (a.part != nullptr) {
             float *to = a.part + int64_t(blockIdx.x) * 2 * a.cols;
 #pragma unroll

@@ -288,3 +288,17 @@ def test_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("cols", [257, 385, 1001, 2047, 4095, 5003, 6143, 8191])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_warps_of_a_row_that_differ(cols, dtype):
+    """Warps whose blocks all end inside the row read without checks, the others with; they
+    meet at one barrier, in each of more rows than there are CTAs."""
+    t, rows = DTYPES[dtype], 1300
+    h, dy, d = (random(rows, cols, dtype=t, seed=s) for s in (1, 2, 3))
+    w = random(cols, dtype=torch.float32, seed=4)
+    _, _, mean, rstd = fp8.layernorm(h, w, quantized=False)
+    got = fp8.layernorm_backward(dy, h, mean, rstd, w, d)
+    check_backward(*got, dy, h, mean, rstd, w, d, t)
+    assert all(torch.equal(a, b) for a, b in zip(got, fp8.layernorm_backward(dy, h, mean, rstd, w, d)))
