@@ -65,6 +65,14 @@ typedef struct basp_adamw_options {
 basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count,
                        const basp_adamw_options *options, cudaStream_t stream);
 
+/*
+ * The same for tensors that have taken different numbers of steps.
+ *   steps_at    [count], in host memory: for each tensor where its own t is in device
+ *               memory, read as step_at is.  The options' step and step_at are not used
+ */
+basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
+                            const basp_adamw_options *options, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

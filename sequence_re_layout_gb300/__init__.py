@@ -20,4 +20,4 @@ from .binding import (  # noqa: F401
     basp_layernorm, basp_layernorm_backward, basp_layernorm_backward_workspace,
     ATTENTION_EXPORTS, basp_attention, basp_attention_backward, basp_attention_backward_workspace,
     basp_attention_decode, basp_attention_decode_workspace, basp_attention_desc, basp_attention_timeouts, basp_heads,
-    OPTIM_EXPORTS, basp_adamw, basp_adamw_options, basp_adamw_tensor)
+    OPTIM_EXPORTS, basp_adamw, basp_adamw_each, basp_adamw_options, basp_adamw_tensor)

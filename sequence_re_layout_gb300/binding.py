@@ -47,7 +47,7 @@ ATTENTION_EXPORTS = ("basp_attention", "basp_attention_backward", "basp_attentio
                      "basp_attention_decode", "basp_attention_decode_workspace", "basp_attention_timeouts")
 
 # every symbol include/basp_optim.h declares
-OPTIM_EXPORTS = ("basp_adamw",)
+OPTIM_EXPORTS = ("basp_adamw", "basp_adamw_each")
 
 # values that share a scale along a row of an 8-bit matrix
 BASP_FP8_BLOCK = 128
@@ -179,6 +179,9 @@ def load_library():
     lib.basp_attention_timeouts.restype = ci
     lib.basp_adamw.argtypes = [ctypes.POINTER(basp_adamw_tensor), i64, ctypes.POINTER(basp_adamw_options), vp]
     lib.basp_adamw.restype = ci
+    lib.basp_adamw_each.argtypes = [ctypes.POINTER(basp_adamw_tensor), ctypes.POINTER(vp), i64,
+                                    ctypes.POINTER(basp_adamw_options), vp]
+    lib.basp_adamw_each.restype = ci
     if hasattr(lib, "basp_debug_bounds_violations"):
         lib.basp_debug_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
         lib.basp_debug_bounds_violations.restype = ctypes.c_int
@@ -656,6 +659,15 @@ def basp_adamw(tensors, options, stream=None):
     ``basp_optim.h``."""
     table = (basp_adamw_tensor * len(tensors))(*tensors)
     _check(load_library().basp_adamw(table, len(tensors), options, _stream(stream)), "basp_adamw")
+
+
+def basp_adamw_each(tensors, steps_at, options, stream=None):
+    """The same with a number of steps for each tensor: int32 tensors or addresses on the GPU."""
+    w, n = "basp_adamw_each", len(tensors)
+    if len(steps_at) != n:
+        raise ValueError("%s: %d numbers of steps for %d tensors" % (w, len(steps_at), n))
+    table, at = (basp_adamw_tensor * n)(*tensors), (ctypes.c_void_p * n)(*(_ptr(s) for s in steps_at))
+    _check(load_library().basp_adamw_each(table, at, n, options, _stream(stream)), w)
 
 
 class Layout:

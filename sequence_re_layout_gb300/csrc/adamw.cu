@@ -30,17 +30,17 @@ struct Entry {
     void *p;
     const void *g;
     void *m, *v, *ms, *vs;
+    const int32_t *step_at;                          // its step's number, or NULL: Options::step
     int64_t n;
     int32_t chunk0;                                  // its first chunk in the launch
     uint8_t type, grad_type, vec, pad;
 };
-static_assert(sizeof(Entry) == 64, "table");
+static_assert(sizeof(Entry) == 72, "table");
 
 struct Options {
     float beta1, beta2, one_beta1, one_beta2, eps, decay, lr;   // decay: 1 - lr * weight_decay
     float c1, c2;                                    // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
     float log_beta1, log_beta2;                      // for a t that is known on the GPU only
-    const int32_t *step_at;
     uint32_t step, seed;
 };
 
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
     const int64_t begin = int64_t(int(blockIdx.x) - e.chunk0) * kChunk;
     float c1 = t.o.c1, c2 = t.o.c2;
     uint32_t step = t.o.step;
-    if (t.o.step_at != nullptr) {
-        const int s = max(1, *t.o.step_at);
+    if (e.step_at != nullptr) {
+        const int s = max(1, *e.step_at);
         step = uint32_t(s);
         c1 = t.o.lr / -expm1f(float(s) * t.o.log_beta1);
         c2 = rsqrtf(-expm1f(float(s) * t.o.log_beta2));
@@ -333,8 +333,8 @@ int64_t chunks_of(int64_t n) { return ceil_div(n, kChunk); }
 
 // One launch of entries [i0, i1) of the caller's list.
 template <int CAP>
-basp_status launch_adamw(const basp_adamw_tensor *list, int64_t i0, int64_t i1, bool eight, const Options &o,
-                         int64_t *next, cudaStream_t stream) {
+basp_status launch_adamw(const basp_adamw_tensor *list, const int32_t *const *steps_at, int64_t i0, int64_t i1, bool eight,
+                         const Options &o, const int32_t *step_at, int64_t *next, cudaStream_t stream) {
     Table<CAP> t;
     t.o = o;
     t.count = 0;
@@ -346,6 +346,7 @@ basp_status launch_adamw(const basp_adamw_tensor *list, int64_t i0, int64_t i1, 
         if (chunks + c > kMaxSide) break;            // the next launch
         Entry &e = t.e[t.count++];
         e.p = x.p; e.g = x.g; e.m = x.m; e.v = x.v; e.ms = x.m_scales; e.vs = x.v_scales;
+        e.step_at = steps_at != nullptr ? steps_at[i] : step_at;
         e.n = x.n;
         e.chunk0 = int32_t(chunks);
         e.type = uint8_t(x.dtype);
@@ -429,22 +430,17 @@ basp_status check_apart(const basp_adamw_tensor *list, int64_t count) {
     return BASP_OK;
 }
 
-}  // namespace
-}  // namespace basp_fp8
-
-using namespace basp_fp8;
-
-extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_adamw_options *options,
-                                  cudaStream_t stream) {
-    NvtxRange range("basp_adamw");
+basp_status adamw(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
+                  const basp_adamw_options *options, cudaStream_t stream) {
     if (count < 0 || options == nullptr || (tensors == nullptr && count > 0)) return BASP_ERR_INVALID_ARG;
     const basp_adamw_options &p = *options;
     // a comparison that a NaN fails
     if (!(p.lr >= 0 && p.lr < INFINITY && p.beta1 >= 0 && p.beta1 < 1 && p.beta2 >= 0 && p.beta2 < 1 && p.eps >= 0 &&
           p.eps < INFINITY && p.weight_decay >= 0 && p.weight_decay < INFINITY))
         return BASP_ERR_INVALID_ARG;
-    if (p.step_at == nullptr && (p.step < 1 || p.step > kMaxSide)) return BASP_ERR_INVALID_ARG;
-    if (uintptr_t(p.step_at) % 4) return BASP_ERR_ALIGNMENT;
+    const bool counted = steps_at == nullptr && p.step_at == nullptr;      // t is the options' step
+    if (counted && (p.step < 1 || p.step > kMaxSide)) return BASP_ERR_INVALID_ARG;
+    if (steps_at == nullptr && uintptr_t(p.step_at) % 4) return BASP_ERR_ALIGNMENT;
     if (count > kMaxSide) return BASP_ERR_TOO_LARGE;
     bool eight = false;
     for (int64_t i = 0; i < count; ++i)
@@ -455,6 +451,8 @@ extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t coun
     for (int64_t i = 0; i < count; ++i) {
         const basp_status st = check_tensor(tensors[i], eight);
         if (st != BASP_OK) return st;
+        if (steps_at != nullptr && tensors[i].n > 0 && steps_at[i] == nullptr) return BASP_ERR_INVALID_ARG;
+        if (steps_at != nullptr && uintptr_t(steps_at[i]) % 4) return BASP_ERR_ALIGNMENT;
     }
     if (const basp_status apart = check_apart(tensors, count); apart != BASP_OK) return apart;
 
@@ -463,8 +461,7 @@ extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t coun
     o.one_beta1 = float(1 - p.beta1); o.one_beta2 = float(1 - p.beta2);
     o.eps = float(p.eps); o.decay = float(1 - p.lr * p.weight_decay); o.lr = float(p.lr);
     o.seed = p.seed;
-    o.step_at = p.step_at;
-    if (p.step_at == nullptr) {
+    if (counted) {
         o.step = uint32_t(p.step);
         o.c1 = float(p.lr / (1 - std::pow(p.beta1, double(p.step))));
         o.c2 = float(1 / std::sqrt(1 - std::pow(p.beta2, double(p.step))));
@@ -475,9 +472,29 @@ extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t coun
     // Tables of three sizes: a launch copies all of its parameters.
     basp_status st = BASP_OK;
     for (int64_t i = 0; i < count && st == BASP_OK;) {
-        if (count - i <= 12) st = launch_adamw<12>(tensors, i, count, eight, o, &i, stream);
-        else if (count - i <= 60) st = launch_adamw<60>(tensors, i, count, eight, o, &i, stream);
-        else st = launch_adamw<500>(tensors, i, count, eight, o, &i, stream);
+        auto go = [&](auto cap) {
+            st = launch_adamw<decltype(cap)::value>(tensors, steps_at, i, count, eight, o, p.step_at, &i, stream);
+        };
+        if (count - i <= 12) go(std::integral_constant<int, 12>());
+        else if (count - i <= 60) go(std::integral_constant<int, 60>());
+        else go(std::integral_constant<int, 440>());
     }
     return st;
+}
+
+}  // namespace
+}  // namespace basp_fp8
+
+extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_adamw_options *options,
+                                  cudaStream_t stream) {
+    basp_fp8::NvtxRange range("basp_adamw");
+    return basp_fp8::adamw(tensors, nullptr, count, options, stream);
+}
+
+extern "C" basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
+                                       const basp_adamw_options *options, cudaStream_t stream) {
+    basp_fp8::NvtxRange range("basp_adamw_each");
+    if (steps_at == nullptr && count > 0) return BASP_ERR_INVALID_ARG;
+    static const int32_t *const none = nullptr;
+    return basp_fp8::adamw(tensors, steps_at != nullptr ? steps_at : &none, count, options, stream);
 }

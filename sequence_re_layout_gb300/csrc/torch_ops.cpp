@@ -57,6 +57,7 @@ struct Library {
     decltype(&basp_attention_decode) attention_decode;
     decltype(&basp_attention_decode_workspace) attention_decode_workspace;
     decltype(&basp_adamw) adamw;
+    decltype(&basp_adamw_each) adamw_each;
 } g_lib;
 
 [[noreturn]] void refuse(const char *where, const std::string &what) {
@@ -688,7 +689,7 @@ void *dense(const Tensor &x, int64_t n, at::ScalarType type, int device, const c
     return n > 0 ? x.data_ptr() : nullptr;
 }
 
-// adamw(params, grads, m, v, m_scales, v_scales (both None with 32-bit states), step, lr, beta1, beta2, eps,
+// adamw(params, grads, m, v, m_scales, v_scales (both None with 32-bit states), step (or a list of them), lr, beta1, beta2, eps,
 //       weight_decay, seed)
 PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -712,7 +713,12 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
     o.seed = uint32_t(PyLong_AsUnsignedLongLongMask(args[12]));
     if (PyErr_Occurred()) return nullptr;
     const int device = c10::cuda::current_device();
-    if (THPVariable_Check(args[6])) {
+    std::optional<Sequence> steps;                // one on the GPU for each tensor
+    std::vector<const int32_t *> steps_at;
+    if (PyList_Check(args[6]) || PyTuple_Check(args[6])) {
+        steps.emplace(args[6], count, where, "step");
+        steps_at.resize(static_cast<size_t>(count));
+    } else if (THPVariable_Check(args[6])) {
         const Tensor &step = THPVariable_Unpack(args[6]);
         o.step_at = static_cast<const int32_t *>(dense(step, 1, at::kInt, device, where, "step"));
     } else {
@@ -741,12 +747,16 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
         t.g = dense(g, t.n, g.scalar_type(), device, where, "a gradient");
         t.m = dense(mi, t.n, state, device, where, "m");
         t.v = dense(vi, t.n, state, device, where, "v");
+        if (steps.has_value())
+            steps_at[size_t(i)] = static_cast<const int32_t *>(dense(steps->at(i, where, "step"), 1, at::kInt, device, where, "step"));
         if (eight) {
             t.m_scales = dense(ms->at(i, where, "scales of m"), ceil_div(t.n, kBlock), at::kFloat8_e8m0fnu, device, where, "scales of m");
             t.v_scales = dense(vs->at(i, where, "scales of v"), ceil_div(t.n, kBlock), at::kFloat8_e8m0fnu, device, where, "scales of v");
         }
     }
-    if (!check(g_lib.adamw(list.data(), count, &o, c10::cuda::getCurrentCUDAStream(device).stream()), "basp_adamw"))
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
+    if (!(steps.has_value() ? check(g_lib.adamw_each(list.data(), steps_at.data(), count, &o, stream), "basp_adamw_each")
+                            : check(g_lib.adamw(list.data(), count, &o, stream), "basp_adamw")))
         return nullptr;
     for (Py_ssize_t i = 0; i < count; ++i) {
         written(params.seen(i));
@@ -789,9 +799,10 @@ PyMODINIT_FUNC PyInit__torch_ops() {
     PyObject *at = g_error != nullptr ? PyObject_CallMethod(binding, "fp8_entry_points", nullptr) : nullptr;
     PyObject *more = at != nullptr ? PyObject_CallMethod(binding, "layer_entry_points", nullptr) : nullptr;
     Py_DECREF(binding);
-    unsigned long long p[5], l[9];
+    unsigned long long p[5], l[10];
     const bool ok = more != nullptr && PyArg_ParseTuple(at, "KKKKK", &p[0], &p[1], &p[2], &p[3], &p[4]) &&
-                    PyArg_ParseTuple(more, "KKKKKKKKK", &l[0], &l[1], &l[2], &l[3], &l[4], &l[5], &l[6], &l[7], &l[8]);
+                    PyArg_ParseTuple(more, "KKKKKKKKKK", &l[0], &l[1], &l[2], &l[3], &l[4], &l[5], &l[6], &l[7], &l[8],
+                                     &l[9]);
     Py_XDECREF(at);
     Py_XDECREF(more);
     if (!ok) return nullptr;
@@ -810,5 +821,6 @@ PyMODINIT_FUNC PyInit__torch_ops() {
     set(g_lib.attention_decode, l[6]);
     set(g_lib.attention_decode_workspace, l[7]);
     set(g_lib.adamw, l[8]);
+    set(g_lib.adamw_each, l[9]);
     return PyModule_Create(&g_module);
 }

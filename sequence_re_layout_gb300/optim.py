@@ -22,10 +22,10 @@ def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weig
     or :class:`fp8.Quantized` of one row ([1, n]), v then the root of v.
 
     ``step`` counts from 1; as an int32 tensor of one element on the GPU it is read
-    when the kernel runs, so that a captured step can be replayed.  The random
-    rounding of 8-bit states depends on ``seed``, the step and each element's place
-    alone.  Every tensor is dense, and none overlaps another: the same parameter
-    twice is refused."""
+    when the kernel runs, so that a captured step can be replayed; a list of those has
+    one for each parameter.  The random rounding of 8-bit states depends on ``seed``,
+    the step and each element's place alone.  Every tensor is dense, and none overlaps
+    another: the same parameter twice is refused."""
     m, v = list(m), list(v)
     m_scales = v_scales = None
     if m and isinstance(m[0], fp8.Quantized):
@@ -45,7 +45,7 @@ class AdamW(torch.optim.Optimizer):
     """Adam with decoupled weight decay; parameters on the current GPU, dense.
 
     ``state_bits`` 32 or 8.  ``seed`` is that of the 8-bit states' rounding.  With
-    ``capturable`` the step's number lives on the GPU, so ``step()`` can be captured
+    ``capturable`` the numbers of the steps live on the GPU, so ``step()`` can be captured
     in a CUDA graph and replayed (with the lr and the other options of the capture),
     once a step has been taken; otherwise a capture is refused."""
 
@@ -58,9 +58,9 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
                                       state_bits=state_bits, seed=seed, capturable=capturable))
 
-    def _init(self, p, group, step):
+    def _init(self, p, group):
         state = self.state[p]
-        state["step"] = step
+        state["step"] = torch.zeros(1, dtype=torch.int32, device=p.device) if group["capturable"] else 0
         for name in ("exp_avg", "exp_avg_sq" if group["state_bits"] == 32 else "exp_avg_sq_root"):
             if group["state_bits"] == 32:
                 state[name] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
@@ -72,8 +72,8 @@ class AdamW(torch.optim.Optimizer):
 
     @torch.no_grad()
     def step(self, closure=None):
-        """One step over every parameter that has a gradient.  Parameters that joined
-        in the same step share its number; those that joined later count their own."""
+        """One step over every parameter that has a gradient.  Each parameter counts the
+        steps that it takes itself, with or without ``capturable``."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -81,8 +81,8 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             if not group["capturable"] and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("AdamW: a captured step would keep its number: pass capturable=True")
-            capturable, first = group["capturable"], None
-            together = {}                             # of each step's number: (parameters, gradients, states)
+            capturable = group["capturable"]
+            together = {}                             # of each step's number, where it is known: (parameters, gradients, states)
             for p in group["params"]:
                 g = p.grad
                 if g is None:
@@ -92,11 +92,8 @@ class AdamW(torch.optim.Optimizer):
                     if torch.cuda.is_current_stream_capturing():
                         raise RuntimeError("AdamW: every replay of a captured first step would begin with new states: "
                                            "take a step before the capture")
-                    if first is None:
-                        first = torch.zeros(1, dtype=torch.int32, device=p.device) if capturable else 0
-                    s = self._init(p, group, first)
-                step = s["step"]
-                number = id(step) if capturable else step
+                    s = self._init(p, group)
+                number = None if capturable else s["step"]
                 lists = together.get(number)
                 if lists is None:
                     lists = together[number] = [], [], []
@@ -108,36 +105,30 @@ class AdamW(torch.optim.Optimizer):
         return loss
 
     def _take(self, params, grads, states, group):
-        step = states[0]["step"]
         if group["capturable"]:
-            step.add_(1)
+            step = [s["step"] for s in states]
+            torch._foreach_add_(step, 1)
         else:
-            step += 1
-            for s in states:
-                s["step"] = step
+            step = states[0]["step"] + 1
         if group["state_bits"] == 32:
             m, v = [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states]
         else:
             m, v = ([fp8.Quantized(s[n], s[n + "_scales"]) for s in states] for n in ("exp_avg", "exp_avg_sq_root"))
         adamw(params, grads, m, v, step, group["lr"], group["betas"], group["eps"], group["weight_decay"], group["seed"])
+        if not group["capturable"]:
+            for s in states:
+                s["step"] = step
 
     def load_state_dict(self, state_dict):
         """As torch's, but states keep the types they were saved in."""
         super().load_state_dict(state_dict)
         numbers = [i for g in state_dict["param_groups"] for i in g["params"]]
         places = [(p, g) for g in self.param_groups for p in g["params"]]
-        shared = {}
         for i, (p, group) in zip(numbers, places):
             if i not in state_dict["state"]:
                 continue
             state = {n: x.detach().to(p.device, copy=True) if torch.is_tensor(x) else x
                      for n, x in state_dict["state"][i].items()}
             count = int(state["step"])
-            if group["capturable"]:                   # one number on the GPU for those that count together
-                key = id(group), count
-                if key not in shared:
-                    shared[key] = torch.full((1,), count, dtype=torch.int32, device=p.device)
-                state["step"] = shared[key]
-            else:
-                state["step"] = count
+            state["step"] = torch.full((1,), count, dtype=torch.int32, device=p.device) if group["capturable"] else count
             self.state[p] = state

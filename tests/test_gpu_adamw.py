@@ -351,3 +351,74 @@ def test_a_parameter_does_not_come_twice():
     with pytest.raises((ValueError, RuntimeError), match="overlap|alias"):
         optim.adamw([p, p], [g, g], [m, m.clone()], [v, v.clone()], 1)
     assert bool((p == 1).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_number_for_each_tensor(bits):
+    """More tensors than a launch's table has: each as with its number for all."""
+    numbers = [1 + i * i % 50 for i in range(900)]
+    def make():
+        p, g = ([random(1 + i % 300, torch.float32, i + s) for i in range(900)] for s in (0, 1000))
+        m, v = ([random(1 + i % 300, torch.float32, i + s).square() for i in range(900)] for s in (2000, 3000))
+        return (p, g, m, v) if bits == 32 else (p, g, [quantized(x) for x in m], [quantized(x.sqrt()) for x in v])
+    values = lambda s: s if bits == 32 else s.dequantize()                    # noqa: E731
+    a = make()
+    steps = list(torch.tensor(numbers, dtype=torch.int32, device="cuda").split(1))
+    optim.adamw(*a, step=steps, seed=5)
+    one = {}
+    for n in sorted(set(numbers)):                          # the whole list with that number
+        b = make()
+        optim.adamw(*b, step=torch.full((1,), n, dtype=torch.int32, device="cuda"), seed=5)
+        one[n] = b
+    for i, n in enumerate(numbers):
+        for x, y in ((a[0][i], one[n][0][i]), (values(a[2][i]), values(one[n][2][i])), (values(a[3][i]), values(one[n][3][i]))):
+            assert torch.equal(x, y)
+    for bad in (steps[:-1], [s.long() for s in steps], [s.cpu() for s in steps], numbers):
+        with pytest.raises(ValueError):
+            optim.adamw(*a, step=bad)
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_parameters_that_miss_steps(capturable):
+    """torch.optim.AdamW in 64 bits, where a parameter has no gradient in some steps."""
+    a, b = layer(1), layer(1).double()
+    mine = optim.AdamW(a.parameters(), lr=0.01, weight_decay=0.2, capturable=capturable)
+    theirs = torch.optim.AdamW(b.parameters(), lr=0.01, weight_decay=0.2)
+    for i in range(20):
+        for j, (x, y) in enumerate(zip(a.parameters(), b.parameters())):
+            x.grad = random(x.numel(), torch.float32, 100 * i + j).view_as(x) if i % (j + 1) == 0 else None
+            y.grad = None if x.grad is None else x.grad.double()
+        mine.step()
+        theirs.step()
+    for x, y in zip(a.parameters(), b.parameters()):
+        assert int(mine.state[x]["step"]) == int(theirs.state[y]["step"])
+        assert bool(((x.double() - y).abs() <= 20 * (0.02 * 2.0 ** -18 + 2.0 ** -23 * y.abs())).all())
+
+
+def test_captured_steps_of_some_and_of_all():
+    """Two graphs, one of whose steps leaves parameters out, and plain steps between them."""
+    nets = [layer(3), layer(3)]
+    opts = [optim.AdamW(n.parameters(), lr=0.01, capturable=c) for n, c in zip(nets, (True, False))]
+    def grads(net, every):
+        for j, p in enumerate(net.parameters()):
+            p.grad = random(p.numel(), torch.float32, j).view_as(p) if every or j % 2 else None
+    graphs = []
+    grads(nets[0], True)
+    opts[0].step()
+    keep = []                                               # the gradients that the graphs read
+    for every in (True, False):
+        grads(nets[0], every)
+        keep.append([p.grad for p in nets[0].parameters()])
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            opts[0].step()
+    for every in (False, False, True, False, True):
+        graphs[0 if every else 1].replay()
+    grads(nets[0], False)
+    opts[0].step()
+    for every in (True, False, False, True, False, True, False):
+        grads(nets[1], every)
+        opts[1].step()
+    for x, y in zip(nets[0].parameters(), nets[1].parameters()):
+        assert int(opts[0].state[x]["step"]) == opts[1].state[y]["step"]
+        assert bool(((x - y).abs() <= 7 * (0.02 * 2.0 ** -18 + 2.0 ** -23 * y.abs())).all())

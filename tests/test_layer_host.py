@@ -295,3 +295,57 @@ def test_the_longest_sequences(lib, name):
     assert forward(lib, desc(**{name: 2 ** 31 - 4095})) == LARGE
     assert basp.basp_attention_decode_workspace(desc(q_len=1, k_len=2 ** 31 - 4095, window=0)) == 0
     assert basp.basp_attention_decode_workspace(desc(q_len=1, k_len=2 ** 31 - 4096, window=0)) > 0
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_parameters_count_the_steps_they_take(capturable, bits, monkeypatch):
+    """As torch.optim.AdamW's; also from a saved state on in which two numbers were equal by chance."""
+    taken = []
+
+    def call(params, grads, m, v, step, *rest):
+        taken.append([int(s) for s in step] if isinstance(step, list) else [step] * len(params))
+
+    monkeypatch.setattr(optim, "adamw", call)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    params = [torch.nn.Parameter(torch.zeros(3)) for _ in range(3)]
+    mine = optim.AdamW(params, capturable=capturable, state_bits=bits)
+    theirs = torch.optim.AdamW(params)
+    # the second misses steps 2 to 5, the third joins in step 4 and misses step 8
+    has = [(1, 1, 0), (1, 0, 0), (1, 0, 0), (1, 0, 1), (1, 0, 1), (1, 1, 1), (1, 1, 1), (1, 1, 0), (1, 1, 1)]
+    for i, h in enumerate(has):
+        if i == 7:
+            old = mine
+            numbers = [int(old.state[p]["step"]) for p in params]
+            assert numbers == [7, 3, 4]
+            for p in params:                              # equal by chance
+                old.state[p]["step"] = torch.full((1,), 4, dtype=torch.int32) if capturable else 4
+            mine = optim.AdamW(params, capturable=capturable, state_bits=bits)
+            mine.load_state_dict(old.state_dict())
+            want = [4, 4, 4]
+        for p, x in zip(params, h):
+            p.grad = torch.ones(3) if x else None
+        taken.clear()
+        mine.step()
+        if i < 7:
+            theirs.step()
+            want = [int(theirs.state[p]["step"]) if p in theirs.state else None for p in params]
+        else:
+            want = [w + x for w, x in zip(want, h)]
+        assert [int(mine.state[p]["step"]) if mine.state.get(p) else None for p in params] == want
+        assert sorted(n for t in taken for n in t) == sorted(w for w, x in zip(want, h) if x)
+
+
+def test_numbers_of_steps_of_their_own(lib):
+    def status(tensors, steps, **change):
+        table, at = (basp.basp_adamw_tensor * len(tensors))(*tensors), (ctypes.c_void_p * len(tensors))(*steps)
+        return lib.basp_adamw_each(table, at, len(tensors), basp.basp_adamw_options(**{**OPTIONS, "step": 0, **change}), None)
+    assert status([adam(1)], [at(90) + 2]) == ALIGN and status([adam(1, n=0)], [at(90) + 2]) == ALIGN
+    assert status([adam(1), adam(10)], [at(90), None]) == INVALID and status([adam(1, p=None)], [at(90)]) == INVALID
+    assert status([adam(1, n=0)], [None]) == OK and status([], []) == OK
+    assert status([adam(1), adam(1)], [at(90), at(91)]) == ALIAS and status([adam(1)], [at(90)], lr=-1.0) == INVALID
+    o = basp.basp_adamw_options(**OPTIONS)
+    assert lib.basp_adamw_each((basp.basp_adamw_tensor * 1)(adam(1)), None, 1, o, None) == INVALID
+    assert lib.basp_adamw_each(None, None, 0, o, None) == OK and lib.basp_adamw_each(None, None, -1, o, None) == INVALID
+    with pytest.raises(ValueError):
+        basp.basp_adamw_each([adam(1)], [], o)
