@@ -373,11 +373,12 @@ def layernorm_linear_fp8(x, norm_weight, norm_bias, weight, bias=None, residual=
 
 def _aligned(t):
     """t where the kernels of tiles can read its heads in place, else a copy: gradients
-    come in any form (one value, or one token's, spread over the result, for instance)."""
+    come in any form (one value, or one token's, spread over the result, or a piece of a
+    buffer that begins anywhere, for instance)."""
     if (t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(s % 8 == 0 for s in t.stride()[:-1]) and
             (t.size(1) == 1 or t.stride(1) >= t.size(-1))):
         return t
-    return t.contiguous()
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class _Attention(torch.autograd.Function):

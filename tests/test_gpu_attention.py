@@ -476,3 +476,19 @@ def test_one_token_of_nan_in_a_long_sequence(where, dtype):
 
 def test_zz_no_wait_ran_out():
     assert basp.basp_attention_timeouts() == 0
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("offset", [1, 3, 4, 8])
+def test_gradients_of_a_piece_of_a_buffer(offset, dtype):
+    """A contiguous gradient that begins anywhere, as the backward of torch.cat hands it on."""
+    q, k, v, _ = tensors(1, 37, 37, 2, 1, 64, DTYPES[dtype])
+    grads = []
+    for before in (offset, 0):
+        leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+        o = autograd.attention(*leaves, window=20, sinks=1)
+        flat = torch.cat([torch.zeros(before, dtype=q.dtype, device="cuda"), o.reshape(-1)])
+        do = random(o.numel(), dtype=q.dtype, seed=5)
+        flat.backward(torch.cat([torch.zeros(before, dtype=q.dtype, device="cuda"), do]))
+        grads.append([x.grad for x in leaves])
+    assert all(torch.equal(a, b) for a, b in zip(*grads))

@@ -11,7 +11,7 @@ import torch
 
 import layer_reference as ref
 import sequence_re_layout_gb300 as basp
-from sequence_re_layout_gb300 import attention, fp8, optim
+from sequence_re_layout_gb300 import attention, autograd, fp8, optim
 from sequence_re_layout_gb300.build import build_library
 from test_fp8_host import ALIAS, ALIGN, BF16, FP16, FP32, FP8, GiB, INVALID, LARGE, OK, WORKSPACE, at, q8
 
@@ -349,3 +349,18 @@ def test_numbers_of_steps_of_their_own(lib):
     assert lib.basp_adamw_each(None, None, 0, o, None) == OK and lib.basp_adamw_each(None, None, -1, o, None) == INVALID
     with pytest.raises(ValueError):
         basp.basp_adamw_each([adam(1)], [], o)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3, 4, 8, 16])
+def test_gradients_that_begin_anywhere(offset):
+    """What the attention's backward gets begins at a multiple of 16 bytes, also of a piece that is contiguous."""
+    flat = torch.arange(2 * 5 * 3 * 8 + 40, dtype=torch.float32).bfloat16()
+    flat = flat[(-flat.data_ptr() // 2) % 8:]
+    t = flat[offset:offset + 240].view(2, 5, 3, 8)
+    got = autograd._aligned(t)
+    assert t.is_contiguous() and got.data_ptr() % 16 == 0 and torch.equal(got, t)
+    assert (got is t) == (offset % 8 == 0)
+    for spread in (t[:, :1].expand(2, 5, 3, 8), t.transpose(0, 1), t[..., :1].expand(2, 5, 3, 8), t[:1, :, :, :4].expand(2, 5, 3, 4)):
+        got = autograd._aligned(spread)
+        assert got.data_ptr() % 16 == 0 and torch.equal(got, spread) and got.stride(-1) == 1
+        assert all(s % 8 == 0 for s, n in zip(got.stride()[:-1], got.shape) if n > 1) or spread.shape[-1] == 4
