@@ -273,7 +273,8 @@ __device__ __noinline__ void forward_row(const AttentionArgs &a, int b, int h, i
     each_keys(see.first_end, see.last, p + 1, lane, [&](int j, bool have) {
         const float s = have ? a.scale * row_dot(q, row_of<const T>(a.k, b, j, kh), a.d) : -INFINITY;
         const float top = warp_max(s), next = m > top || m != m ? m : top;
-        const float w = have ? expf(s - next) : 0.f, old = m == -INFINITY && l == 0.f ? 0.f : expf(m - next);
+        // scores of minus infinity weigh nothing, also before the first that is more
+        const float w = have && next != -INFINITY ? expf(s - next) : 0.f, old = m == -INFINITY && l == 0.f ? 0.f : expf(m - next);
         l = l * old + warp_add(w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] *= old;

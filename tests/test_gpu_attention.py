@@ -492,3 +492,26 @@ def test_gradients_of_a_piece_of_a_buffer(offset, dtype):
         flat.backward(torch.cat([torch.zeros(before, dtype=q.dtype, device="cuda"), do]))
         grads.append([x.grad for x in leaves])
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("path", ["tiles", "rows", "again"])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_scores_of_minus_infinity(path, dtype):
+    """The first key's, alone among the sinks: it weighs nothing, in the tiles, in the form for
+    tensors that TMA cannot address, and in rows that are computed again beside a NaN."""
+    t, S, d, window = DTYPES[dtype], 150, 64, 40
+    q, k, v, _ = tensors(1, S, S, 2, 1, d, t)
+    if path == "rows":
+        q = q[:, :1].clone().expand(1, S, 2, d)
+    q[..., 7] = 1.0
+    k[0, 0, 0, 7] = float("-inf")
+    rows = np.arange(1, S)
+    if path == "again":
+        v[0, 100] = float("nan")
+        rows = rows[(rows < 100) | (rows >= 100 + window)]
+    o, lse = attention.forward(q, k, v, window, 1)
+    # without the first key; rows that see the NaN are left out
+    r = Attention(f64(q[0, 1:]), f64(k[0, 1:]), f64(v[0, 1:].nan_to_num()), window, 0, d ** -0.5, u(t))
+    close(o[0][torch.from_numpy(rows).cuda()], r.o[rows - 1], r.o_bound[rows - 1])
+    close(lse[0, :, 1:], r.lse, r.lse_bound)
+    assert bool(torch.isnan(o[0, 0]).all()) and bool(torch.isneginf(lse[0, :, 0]).all())
