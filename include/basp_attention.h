@@ -18,8 +18,9 @@
  * dk and dv summed over the Hq / Hkv query heads that share a key head.
  *
  * Products are of 16-bit values, summed in 32 bits; P and dS are rounded to the
- * tensors' type before their products (as q, k and v are); maxima, sums of
- * exponentials, D and lse are in 32 bits.  Results repeat bit for bit: nothing is
+ * tensors' type before their products (as q, k and v are; in fp16, which small
+ * gradients would leave, as a power of two times them that follows d_o's size); maxima,
+ * sums of exponentials, D and lse are in 32 bits.  Results repeat bit for bit: nothing is
  * added in an order that timing decides.
  *
  * Heads.  Element (b, s, h, e) of a tensor is data[b * stride_batch + s * stride_seq

@@ -48,7 +48,7 @@ template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cud
 template <class T, int LANES>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int ROWS = 256 / LANES, PASSES = kTile / ROWS;
-    __shared__ float sums[kTile];
+    __shared__ float sums[kTile], tops[kUnits<T> ? kTile : 1];
     grid_dependency();
     const int tiles = a.sq_pad / kTile, h = int(blockIdx.x % unsigned(a.hq)), tile = int(blockIdx.x / unsigned(a.hq) % unsigned(tiles));
     const int b = int(blockIdx.x / unsigned(a.hq) / unsigned(tiles)), head = b * a.hq + h, e = int(threadIdx.x % LANES) * 8;
@@ -71,6 +71,14 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
         float u[8], v[8], s = 0.f;
         Pack<T>::unpack(o[x], u);
         Pack<T>::unpack(g[x], v);
+        if constexpr (kUnits<T>) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.f);
+#pragma unroll
+            for (int w = LANES / 2; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            if (threadIdx.x % LANES == 0) tops[x * ROWS + threadIdx.x / LANES] = top;
+        }
         if (a.rest.p != nullptr) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -86,6 +94,12 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
     if (row >= kTile) return;
     const float s = sums[row];
     a.stats[int64_t(head) * a.sq_pad + i] = sees ? make_float2(lse, s) : make_float2(INFINITY, 0.f);
+    if constexpr (kUnits<T>) {
+        float top = sees ? tops[row] : 0.f;
+        a.unit[int64_t(head) * a.sq_pad + i] = unit_of(top);
+        top = warp_max(top);
+        if (row % 32 == 0) a.peak[(int64_t(head) * a.sq_pad + i) / 32] = top;
+    }
     // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that the rows
     // that meet it are made from the definition
     const float sign = a.scale < 0.f ? 1.f : -1.f;                // the other side of the product is negated
@@ -302,9 +316,10 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
     return with_type(desc->dtype, [&](auto t) { return launch_rows<decltype(t), kForward>(a, stream); });
 }
 
-// The statistics and their parts for the products, a multiple of 1024 bytes.
-static int64_t fold_bytes(const AttentionArgs &a) {
-    return int64_t(a.batch) * a.hq * ceil_div(a.sq, kTile) * kTile * (int64_t(sizeof(float2)) + 32);
+// The statistics, their parts for the products and fp16's units: a multiple of 16 bytes.
+static int64_t row_bytes(const AttentionArgs &a, basp_dtype t) {
+    const int64_t rows = int64_t(a.batch) * a.hq * ceil_div(a.sq, kTile) * kTile;
+    return rows * (int64_t(sizeof(float2)) + 32) + (t == BASP_DTYPE_FP16 ? (rows + rows / 32) * int64_t(sizeof(float)) : 0);
 }
 
 extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
@@ -312,7 +327,7 @@ extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *
     if (!sizes_ok(desc, &st) || !rows_ok(desc)) return 0;
     if (desc->batch == 0 || desc->q_heads == 0) return 0;
     const AttentionArgs a = args_of(desc);
-    return fold_bytes(a) + key_split_bytes(a, key_split(a));
+    return row_bytes(a, desc->dtype) + key_split_bytes(a, key_split(a));
 }
 
 extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, const basp_heads *q,
@@ -350,7 +365,10 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     a.lse = const_cast<float *>(lse);
     a.sq_pad = int(ceil_div(a.sq, kTile) * kTile);
     a.stats = static_cast<float2 *>(workspace);
-    a.fold = reinterpret_cast<uint16_t *>(a.stats + int64_t(a.batch) * a.hq * a.sq_pad);
+    const int64_t rows = int64_t(a.batch) * a.hq * a.sq_pad;
+    a.fold = reinterpret_cast<uint16_t *>(a.stats + rows);
+    a.unit = reinterpret_cast<float *>(a.fold + rows * 16);
+    a.peak = a.unit + rows;
     // lse / c of the smallest scales is past 32 bits
     const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq) &&
                        (a.scale == 0.f || std::fabs(a.scale) >= 0x1p-64f);
@@ -362,7 +380,7 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
         basp_status s = launch_stats<T>(a, stream);
         if (s == BASP_OK && tiles) {
             KeySplit split = key_split(a);
-            split.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + fold_bytes(a));
+            split.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + row_bytes(a, desc->dtype));
             return launch_attention_backward(a, m, split, desc->dtype == BASP_DTYPE_BF16, stream);
         }
         if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);

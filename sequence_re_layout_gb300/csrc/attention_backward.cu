@@ -36,6 +36,9 @@
 // mask's first ones by most), or there are few, several CTAs share the longest ones: their
 // sums go to memory and another kernel adds them in order.
 //
+// fp16 has units of its own for P and dS (attention_common.cuh), which are taken off the sums at
+// the end; 2 x 8192 x 32 heads of 64, window 1024: 607 us with them, 595 without.
+//
 // As in the forward, a row that comes out infinite or NaN is computed again from the
 // definition, where that can differ.
 //
@@ -298,6 +301,18 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         const uint32_t to_p = p_at + lanes + kStep * way, to_ds = ds_at + lanes + kStep * way;
         const float c = score_scale(a.scale);
         const float2 c2 = make_float2(c, c);
+        float ds_unit = 1.f;                                  // dS is multiplied by it
+        if constexpr (kUnits<T>) {
+            float top = 0.f;
+            for (int i = lane; i < total; i += 32) {
+                const int h = kh * a.group + (begin + i) / count, q = (tiles.low + (begin + i) % count) * kTile;
+                const float4 x = *reinterpret_cast<const float4 *>(a.peak + ((int64_t(b) * a.hq + h) * a.sq_pad + q) / 32);
+                top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+            }
+            ds_unit = unit_of(warp_max(top));
+        }
+        const float2 p2 = make_float2(kProbabilityUnit, kProbabilityUnit);
+        const float2 unit2 = make_float2(ds_unit * 0x1p-14f, ds_unit * 0x1p-14f);
         const int k1 = k0 + kTile - 1, seen_by = last_position(a, key) - shift;
         bool ok = true;
         int q0 = (tiles.low + (total > 0 ? begin % count : 0)) * kTile;
@@ -313,7 +328,8 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             if (kEarly<HD>) pass_on(s_taken);
 #pragma unroll
             for (int e = 0; e < kCols; e += 2) {
-                const float2 f = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2);
+                const float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                const float2 f = kUnits<T> ? fma2(y, c2, p2) : mul2(y, c2);
                 p[e] = exp2_fast(f.x);
                 p[e + 1] = exp2_fast(f.y);
             }
@@ -339,7 +355,8 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             if (kEarly<HD>) pass_on(dp_taken);
 #pragma unroll
             for (int e = 0; e < kCols; e += 2) {
-                const float2 f = mul2(make_float2(p[e], p[e + 1]), make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                float2 f = mul2(make_float2(p[e], p[e + 1]), make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                if constexpr (kUnits<T>) f = mul2(f, unit2);
                 p[e] = f.x;
                 p[e + 1] = f.y;
             }
@@ -361,7 +378,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         if (unit < shared)
             part = split.partial + ((int64_t(blockIdx.x) * 2 + way / 2) * kTile + quarter * 32 + lane) * HD;
         const bool exists = key < a.sk;
-        const float f = way < 2 ? 1.f : a.scale;
+        const float f = way < 2 ? 1.f : a.scale, back = way < 2 ? 0x1p-14f : over_unit(ds_unit);
         const uint32_t acc = (way < 2 ? dv_acc : dk_acc) + lanes;
         T *row = row_of<T>(way < 2 ? a.dv : a.dk, b, exists ? key : 0, kh);
         bool finite = true;
@@ -378,6 +395,9 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
             }
+            if constexpr (kUnits<T>)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * back);
             if (part != nullptr) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
@@ -645,7 +665,9 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
             const int p0 = t.q0 + shift, p1 = min(t.q0 + kTile, a.sq) - 1 + shift;
             const bool exists = row < a.sq;
             const float2 st = a.stats[(int64_t(t.b) * a.hq + t.h) * a.sq_pad + row];     // row < sq_pad
-            const float2 c2 = make_float2(c, c), lse2 = make_float2(-st.x, -st.x), d2 = make_float2(-st.y, -st.y);
+            const float unit = kUnits<T> ? a.unit[(int64_t(t.b) * a.hq + t.h) * a.sq_pad + row] : 1.f;
+            const float lse = (kUnits<T> ? float(int(__float_as_uint(unit) >> 23) - 127) : 0.f) - st.x;     // of P in the unit
+            const float2 c2 = make_float2(c, c), lse2 = make_float2(lse, lse), d2 = make_float2(-st.y, -st.y);
             for (int j = t.keys.begin(); j < t.keys.high && ok; j = t.keys.next(j), ++i) {
                 ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
                 if (!ok) break;
@@ -710,7 +732,10 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
                 uint32_t o[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    const float u = __uint_as_float(v[e + 2 * z]) * a.scale, g = __uint_as_float(v[e + 2 * z + 1]) * a.scale;
+                    float u = __uint_as_float(v[e + 2 * z]), g = __uint_as_float(v[e + 2 * z + 1]);
+                    if constexpr (kUnits<T>) u *= over_unit(unit), g *= over_unit(unit);
+                    u *= a.scale;
+                    g *= a.scale;
                     if (32 * way + e < a.d) finite = finite && fabsf(u) < INFINITY && fabsf(g) < INFINITY;
                     o[z] = pack_pair<T>(u, g);
                 }

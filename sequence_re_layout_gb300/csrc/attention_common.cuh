@@ -27,6 +27,7 @@ struct AttentionArgs {
     // does not exist, or sees nothing: (infinity, 0)
     float2 *stats;
     uint16_t *fold;                      // the same as parts of a product, two planes a tile of queries
+    float *unit, *peak;                  // fp16: unit_of each query's dO [batch][Hq][sq_pad], and 32 queries' largest |dO|
     int batch, sq, sk, sq_pad, hq, hkv, d, group;
     int window, sinks;                   // window: sk where all is visible
     float scale;
@@ -95,6 +96,18 @@ template <class T> __host__ __device__ __forceinline__ constexpr float fold_unit
     if (!std::is_same_v<T, __half>) return 1.f;
     return j == 0 ? 0x1p6f : j == 1 ? 0x1p-5f : j == 2 ? 0x1p-16f : 0.f;
 }
+
+// fp16 is exact to 2^-11 from 2^-14 on only, and small gradients have dS far below that (16384
+// keys have P = 2^-14 on average).  So P and dS are rounded in units of their own: P of the dkv
+// kernel in 2^-14, and dS in a power of two near the largest |dO| of the query (dq), or of all
+// queries that a CTA visits (dk), which leaves a factor of 2^15 above |dO| to dP = dO V^T.
+template <class T> constexpr bool kUnits = std::is_same_v<T, __half>;
+constexpr float kProbabilityUnit = 14.f;
+// 2^-e of the finite m in [2^e, 2^(e + 1)), 1 of zero; and 1 / unit.
+__device__ __forceinline__ float unit_of(float m) {
+    return m > 0.f ? __uint_as_float((254u << 23) - (__float_as_uint(m) & 0x7f800000u)) : 1.f;
+}
+__device__ __forceinline__ float over_unit(float unit) { return __uint_as_float((254u << 23) - __float_as_uint(unit)); }
 
 // A wait on one of the CTA's barriers, with a limit.
 constexpr uint64_t kAttentionWaitNs = 2000000000ull;

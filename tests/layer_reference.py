@@ -139,3 +139,29 @@ def round_at_random(y, r):
     k = np.floor(np.abs(y) / step)
     t = np.abs(y) / step - k + (r + 0.5) / 65536
     return np.copysign((k + (t >= 1)) * step, y), np.abs(t - 1)
+
+
+def gradients_in_units(a, do, o_rounding, p_unit, q_unit, k_unit):
+    """(dq, dk, dv) of an Attention and their bounds, where P of dv is rounded as p_unit times
+    it, dS of dq as q_unit [hq, sq] times it and dS of dk as k_unit times it: fp16's last step,
+    TINY, is that much smaller.  The rest as in Attention.backward."""
+    got = {n: np.zeros(x.shape) for n, x in (("dq", a.q), ("dk", a.k), ("dv", a.v))}
+    bound = {n: np.zeros(x.shape) for n, x in got.items()}
+    d, u = a.q.shape[2], a.u
+    for h in range(a.q.shape[1]):
+        kv, p, ep, g = h // a.group, a.p[h], a.ep[h], do[:, h]
+        dp = np.where(a.sees, g @ a.v[:, kv].T, 0)
+        size = np.where(a.sees, np.abs(g) @ np.abs(a.v[:, kv]).T, 0)
+        delta = (g * a.o[:, h]).sum(1)[:, None]
+        ed = (np.abs(g) * (o_rounding[:, h] + (d + 8) * F32 * np.abs(a.o[:, h]))).sum(1)[:, None]
+        ds = p * (dp - delta)
+        e = ep * (np.abs(dp) + np.abs(delta)) + (p + ep) * ((d + 8) * 2.0 ** -23 * size + ed + 2 * F32 * (np.abs(dp) + np.abs(delta)))
+        rounded = lambda x, ex, unit: np.where(a.sees, ex + u * (np.abs(x) + ex) + TINY / unit, 0)       # noqa: E731
+        for name, x, ex, y, at, c in (("dv", p.T, rounded(p, ep, p_unit).T, g, kv, 1.0),
+                                      ("dk", ds.T, rounded(ds, e, k_unit).T, a.q[:, h], kv, a.scale),
+                                      ("dq", ds, rounded(ds, e, q_unit[h][:, None]), a.k[:, kv], h, a.scale)):
+            got[name][:, at] += c * (x @ y)
+            bound[name][:, at] += abs(c) * (ex @ np.abs(y) + a.add * a.group * (np.abs(x) @ np.abs(y)))
+    for name in got:
+        bound[name] += u * np.abs(got[name]) + TINY
+    return got, bound

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import sequence_re_layout_gb300 as basp
-from layer_reference import Attention
+from layer_reference import Attention, gradients_in_units
 from sequence_re_layout_gb300 import attention, autograd
 
 pytestmark = pytest.mark.gpu
@@ -515,3 +515,29 @@ def test_scores_of_minus_infinity(path, dtype):
     close(o[0][torch.from_numpy(rows).cuda()], r.o[rows - 1], r.o_bound[rows - 1])
     close(lse[0, :, 1:], r.lse, r.lse_bound)
     assert bool(torch.isnan(o[0, 0]).all()) and bool(torch.isneginf(lse[0, :, 0]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", ["small", "smaller", "subnormal", "rows", "tiles", "large"])
+@pytest.mark.parametrize("S,Hq,Hkv,window,sinks", [(700, 2, 1, None, 0), (700, 4, 2, 130, 5), (2500, 1, 1, None, 0), (2500, 2, 1, 100, 300)])
+def test_small_gradients_in_fp16(S, Hq, Hkv, window, sinks, kind, d):
+    """dS far below what fp16 is exact to: it is rounded as a power of two times it, 1 to 2 over
+    the largest |do| of a query (dq), or of all queries of the heads (dk, at least), and P of dv
+    as 2^14 times it.  So that dq and dk are not subnormal themselves, q and k are 2^-8 as large
+    and the scale of their products 2^16: the same scores, and gradients 2^8 as large."""
+    t = torch.float16
+    q, k, v, do = tensors(1, S, S, Hq, Hkv, d, t)
+    n = torch.arange(S, device="cuda").view(1, S, 1, 1)
+    size = {"small": 2.0 ** -10, "smaller": 2.0 ** -13, "subnormal": 2.0 ** -19, "rows": torch.exp2(-(n * 7 % 20).float()),
+            "tiles": torch.exp2(-(n // 128 % 3 * 6).float()), "large": 2.0 ** 10}[kind]
+    do = (do.float() * size).to(t)
+    scale = d ** -0.5
+    if kind != "large":
+        q, k, scale = q * 2.0 ** -8, k * 2.0 ** -8, scale * 2.0 ** 16
+    o, lse = attention.forward(q, k, v, window, sinks, scale)
+    got = attention.backward(do, q, k, v, o, lse, window, sinks, scale)
+    r = Attention(f64(q[0]), f64(k[0]), f64(v[0]), window, sinks, scale, u(t))
+    top = np.abs(f64(do[0])).max(-1).T                                          # [hq, sq]
+    want, bound = gradients_in_units(r, f64(do[0]), r.o_bound, 2.0 ** 14, 1 / top, 1 / top.max())
+    for name, g in zip(("dq", "dk", "dv"), got):
+        close(g[0], want[name], bound[name])
