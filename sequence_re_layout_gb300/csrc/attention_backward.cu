@@ -311,8 +311,8 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             }
             ds_unit = unit_of(warp_max(top));
         }
-        const float2 p2 = make_float2(kProbabilityUnit, kProbabilityUnit);
-        const float2 unit2 = make_float2(ds_unit * 0x1p-14f, ds_unit * 0x1p-14f);
+        const float2 p2 = make_float2(kProbabilityExponent, kProbabilityExponent);
+        const float2 unit2 = make_float2(ds_unit * kProbabilityUnit, ds_unit * kProbabilityUnit);
         const int k1 = k0 + kTile - 1, seen_by = last_position(a, key) - shift;
         bool ok = true;
         int q0 = (tiles.low + (total > 0 ? begin % count : 0)) * kTile;
@@ -378,7 +378,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         if (unit < shared)
             part = split.partial + ((int64_t(blockIdx.x) * 2 + way / 2) * kTile + quarter * 32 + lane) * HD;
         const bool exists = key < a.sk;
-        const float f = way < 2 ? 1.f : a.scale, back = way < 2 ? 0x1p-14f : over_unit(ds_unit);
+        const float f = way < 2 ? 1.f : a.scale, back = way < 2 ? kProbabilityUnit : over_unit(ds_unit);
         const uint32_t acc = (way < 2 ? dv_acc : dk_acc) + lanes;
         T *row = row_of<T>(way < 2 ? a.dv : a.dk, b, exists ? key : 0, kh);
         bool finite = true;

@@ -99,10 +99,11 @@ template <class T> __host__ __device__ __forceinline__ constexpr float fold_unit
 
 // fp16 is exact to 2^-11 from 2^-14 on only, and small gradients have dS far below that (16384
 // keys have P = 2^-14 on average).  So P and dS are rounded in units of their own: P of the dkv
-// kernel in 2^-14, and dS in a power of two near the largest |dO| of the query (dq), or of all
-// queries that a CTA visits (dk), which leaves a factor of 2^15 above |dO| to dP = dO V^T.
+// kernel in 2^-10 (its scores' errors may make it larger than one), and dS in a power of two near
+// the largest |dO| of the query (dq), or of all queries that a CTA visits (dk), which leaves a
+// factor of 2^15 above |dO| to dP = dO V^T.
 template <class T> constexpr bool kUnits = std::is_same_v<T, __half>;
-constexpr float kProbabilityUnit = 14.f;
+constexpr float kProbabilityExponent = 10.f, kProbabilityUnit = 0x1p-10f;
 // 2^-e of the finite m in [2^e, 2^(e + 1)), 1 of zero; and 1 / unit.
 __device__ __forceinline__ float unit_of(float m) {
     return m > 0.f ? __uint_as_float((254u << 23) - (__float_as_uint(m) & 0x7f800000u)) : 1.f;
