@@ -48,7 +48,8 @@ template <class T, int WHAT> basp_status launch_rows(const AttentionArgs &a, cud
 template <class T, int LANES>
 __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int ROWS = 256 / LANES, PASSES = kTile / ROWS;
-    __shared__ float sums[kTile], tops[kUnits<T> ? kTile : 1];
+    __shared__ float sums[kTile];
+    __shared__ float2 tops[kUnits<T> ? kTile : 1];            // largest |dO|, sum of |dO|
     grid_dependency();
     const int tiles = a.sq_pad / kTile, h = int(blockIdx.x % unsigned(a.hq)), tile = int(blockIdx.x / unsigned(a.hq) % unsigned(tiles));
     const int b = int(blockIdx.x / unsigned(a.hq) / unsigned(tiles)), head = b * a.hq + h, e = int(threadIdx.x % LANES) * 8;
@@ -72,12 +73,19 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
         Pack<T>::unpack(o[x], u);
         Pack<T>::unpack(g[x], v);
         if constexpr (kUnits<T>) {
-            float top = 0.f;
+            float top = 0.f, sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.f);
+            for (int j = 0; j < 8; ++j) {
+                const float y = fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.f;
+                top = fmaxf(top, y);
+                sum += y;
+            }
 #pragma unroll
-            for (int w = LANES / 2; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            if (threadIdx.x % LANES == 0) tops[x * ROWS + threadIdx.x / LANES] = top;
+            for (int w = LANES / 2; w > 0; w >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            }
+            if (threadIdx.x % LANES == 0) tops[x * ROWS + threadIdx.x / LANES] = make_float2(top, sum);
         }
         if (a.rest.p != nullptr) {
 #pragma unroll
@@ -94,23 +102,28 @@ __global__ void __launch_bounds__(256) stats_kernel(const __grid_constant__ Atte
     if (row >= kTile) return;
     const float s = sums[row];
     a.stats[int64_t(head) * a.sq_pad + i] = sees ? make_float2(lse, s) : make_float2(INFINITY, 0.f);
-    if constexpr (kUnits<T>) {
-        float top = sees ? tops[row] : 0.f;
-        a.unit[int64_t(head) * a.sq_pad + i] = unit_of(top);
-        top = warp_max(top);
-        if (row % 32 == 0) a.peak[(int64_t(head) * a.sq_pad + i) / 32] = top;
-    }
     // -lse / c and -D in parts of 16 bits: what is past their range is NaN, so that the rows
     // that meet it are made from the definition
     const float sign = a.scale < 0.f ? 1.f : -1.f;                // the other side of the product is negated
+    bool past = false;
     float part[8], left = sees ? sign * lse / score_scale(a.scale) : 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float unit = fold_unit<T>(j % 4);
         if (j == 4) left = sees ? -s : 0.f;
         part[j] = unit == 0.f ? 0.f : Elem<T>::to_float(Elem<T>::from_float(left / unit));
-        if (!(fabsf(part[j]) < INFINITY)) part[j] = __uint_as_float(0x7fffffffu);
+        if (!(fabsf(part[j]) < INFINITY)) {
+            part[j] = __uint_as_float(0x7fffffffu);
+            past = true;
+        }
         left -= part[j] * unit;
+    }
+    if constexpr (kUnits<T>) {
+        const float2 own = sees ? tops[row] : make_float2(0.f, 0.f);
+        const float top = warp_max(own.x), sum = warp_max(own.y), most = warp_max(sees && fabsf(s) < INFINITY ? fabsf(s) : 0.f);
+        past = __any_sync(0xffffffffu, past && fabsf(lse) < INFINITY && fabsf(s) < INFINITY);
+        a.unit[int64_t(head) * a.sq_pad + i] = unit_of(own.x);
+        if (row % 32 == 0) a.peak[(int64_t(head) * a.sq_pad + i) / 32] = make_float4(top, sum, past ? INFINITY : most, 0.f);
     }
     uint8_t *to = reinterpret_cast<uint8_t *>(a.fold) + (int64_t(head) * a.sq_pad + tile * kTile) * 32 + fold_offset(row);
     const uint4 w = Pack<T>::pack(part);
@@ -319,7 +332,9 @@ extern "C" basp_status basp_attention(const basp_attention_desc *desc, const bas
 // The statistics, their parts for the products and fp16's units: a multiple of 16 bytes.
 static int64_t row_bytes(const AttentionArgs &a, basp_dtype t) {
     const int64_t rows = int64_t(a.batch) * a.hq * ceil_div(a.sq, kTile) * kTile;
-    return rows * (int64_t(sizeof(float2)) + 32) + (t == BASP_DTYPE_FP16 ? (rows + rows / 32) * int64_t(sizeof(float)) : 0);
+    const int64_t tiles = int64_t(a.batch) * a.hkv * ceil_div(a.sk, kTile);
+    return rows * (int64_t(sizeof(float2)) + 32) +
+           (t == BASP_DTYPE_FP16 ? (rows + ceil_div(tiles, 4) * 4) * int64_t(sizeof(float)) + rows / 32 * int64_t(sizeof(float4)) : 0);
 }
 
 extern "C" int64_t basp_attention_backward_workspace(const basp_attention_desc *desc) {
@@ -368,7 +383,8 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
     const int64_t rows = int64_t(a.batch) * a.hq * a.sq_pad;
     a.fold = reinterpret_cast<uint16_t *>(a.stats + rows);
     a.unit = reinterpret_cast<float *>(a.fold + rows * 16);
-    a.peak = a.unit + rows;
+    a.peak = reinterpret_cast<float4 *>(a.unit + rows);
+    a.v_peak = reinterpret_cast<float *>(a.peak + rows / 32);
     // lse / c of the smallest scales is past 32 bits
     const bool tiles = a.batch > 0 && a.hq > 0 && a.sq > 0 && tiled(a) && tma_ok(a, a.d_o, a.sq, a.hq) &&
                        (a.scale == 0.f || std::fabs(a.scale) >= 0x1p-64f);
@@ -380,7 +396,8 @@ extern "C" basp_status basp_attention_backward(const basp_attention_desc *desc, 
         basp_status s = launch_stats<T>(a, stream);
         if (s == BASP_OK && tiles) {
             KeySplit split = key_split(a);
-            split.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + row_bytes(a, desc->dtype));
+            split.past = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + row_bytes(a, desc->dtype));
+            split.partial = reinterpret_cast<float *>(split.past + ceil_div(key_split_parts(a, split), 4) * 4);
             return launch_attention_backward(a, m, split, desc->dtype == BASP_DTYPE_BF16, stream);
         }
         if (s == BASP_OK) s = launch_rows<T, kDq>(a, stream);

@@ -22,13 +22,16 @@ basp_status launch_attention_decode(const AttentionArgs &a, const int32_t *lengt
                                     cudaStream_t stream);
 // Key tiles whose work, for dk and dv, several CTAs share: the first `tiles`, parts first[t]
 // to first[t + 1] of tile t with `chunk` pairs of tiles each.  The parts' sums pass through
-// `partial`, [part][key heads of all sequences][dv, dk][128][64 or 128].
+// `partial`, [part][key heads of all sequences][dv, dk][128][64 or 128], and with them in `past`,
+// [part][key heads of all sequences], whether something can have been past fp16's range.
 constexpr int kMostSplit = 64;
 struct KeySplit {
     int tiles, chunk, first[kMostSplit + 1];
     float *partial;
+    uint32_t *past;
 };
 KeySplit key_split(const AttentionArgs &a);
+int64_t key_split_parts(const AttentionArgs &a, const KeySplit &s);
 int64_t key_split_bytes(const AttentionArgs &a, const KeySplit &s);
 basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, const KeySplit &s, bool bf16,
                                       cudaStream_t stream);

@@ -37,7 +37,9 @@
 // sums go to memory and another kernel adds them in order.
 //
 // fp16 has units of its own for P and dS (attention_common.cuh), which are taken off the sums at
-// the end; 2 x 8192 x 32 heads of 64, window 1024: 607 us with them, 595 without.
+// the end.  The units, and the largest |v|, which says with the largest |dO| whether dS can have been
+// past the range, are made by two warps that do nothing else: 2 x 8192 x 32 heads of 64, window 1024,
+// take 613 us in fp16 and 595 in bf16, or in fp16 without the units.
 //
 // As in the forward, a row that comes out infinite or NaN is computed again from the
 // definition, where that can differ.
@@ -74,9 +76,9 @@ template <int HD, bool DKV> struct BackSizes {
     // are the first or the last two.  An infinite D so does not meet the scores.
     static constexpr int kFold = 3 * kFoldPlane;
     static constexpr int kOwn = !DKV && HD == 64 ? 2 : 1;     // places of the CTA's own Q and dO (or K and V), and of dq
-    static constexpr int kBarriers = (DKV ? 10 : 7 + 4 * kOwn) + 2 * kStages;
+    static constexpr int kBarriers = (DKV ? 11 : 7 + 4 * kOwn) + 2 * kStages;
     static constexpr int kSmem =
-        1024 + (2 * kOwn + kStages) * kOperand + (kPlaces + (DKV ? 1 : 0)) * kFold + 8 * kBarriers + 16 + 4 * kValueWarps;
+        1024 + (2 * kOwn + kStages) * kOperand + (kPlaces + (DKV ? 1 : 0)) * kFold + 8 * kBarriers + 32 + 4 * kValueWarps;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -122,10 +124,12 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
     const uint32_t s_full = empty + 8 * ST, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8;
     // where products are early: S and dP have been read, dS has been used
     const uint32_t s_taken = ds_ready + 8, dp_taken = s_taken + 8, ds_used = dp_taken + 8;
-    const uint32_t done = ds_used + 8, drained = done + 8;
+    const uint32_t done = ds_used + 8, drained = done + 8, unit_ready = drained + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Z::kBarriers);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     uint32_t *bad_rows = tmem_slot + 4;                       // [warps of values]
+    // fp16: dS's unit, the queries' largest sum |dO| and |D|, and the keys' |v|
+    float *units = reinterpret_cast<float *>(bad_rows + kValueWarps);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     if (warp == kLoadWarp && lane == 0) {
@@ -143,6 +147,7 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         mbar_init(ds_used, 1);
         mbar_init(done, 1);
         mbar_init(drained, 1);
+        mbar_init(unit_ready, 1);
         *abort = 0;
         fence_mbar_init();
         fence_async_shared();
@@ -294,6 +299,44 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
             mma_commit<1>(drained);
             wait(drained, 0, false);
         }
+    } else if (kUnits<T> && warp == kTmemWarp) {              // the unit of dS
+        if (total > 0) {
+            float top = 0.f, sum = 0.f, most = 0.f;
+            for (int i = lane; i < total; i += 32) {
+                const int h = kh * a.group + (begin + i) / count, q = (tiles.low + (begin + i) % count) * kTile;
+#pragma unroll
+                for (int y = 0; y < kTile / 32; ++y) {
+                    const float4 x = a.peak[((int64_t(b) * a.hq + h) * a.sq_pad + q) / 32 + y];
+                    top = fmaxf(top, x.x);
+                    sum = fmaxf(sum, x.y);
+                    most = fmaxf(most, x.z);
+                }
+            }
+            top = warp_max(top);
+            sum = warp_max(sum);
+            most = warp_max(most);
+            if (lane == 0) {
+                units[0] = unit_of(top);
+                units[1] = sum;
+                units[2] = most;
+                mbar_arrive(unit_ready);
+            }
+            __syncwarp();
+        }
+    } else if (kUnits<T> && warp == kTmemWarp + 1) {          // the largest |v|
+        if (total > 0) {
+            const bool ok = __all_sync(0xffffffffu, wait(kv_full, 0));
+            float top = 0.f;
+            for (int x = lane; ok && x < Z::kOperand / 16; x += 32)
+                top = fmaxf(top, finite_peak<T>(*reinterpret_cast<const uint4 *>(smem + Z::kOperand + 16 * x)));
+            top = warp_max(top);
+            if (lane == 0) {
+                units[3] = top;
+                a.v_peak[(int64_t(b) * a.hkv + kh) * ((a.sk + kTile - 1) / kTile) + tile] = top;
+            }
+            __syncwarp();
+        }
+        asm volatile("bar.arrive 1, %0;" ::"n"(32 * kValueWarps + 32) : "memory");
     } else if (warp < kValueWarps) {                          // values
         const int way = warp / 4, quarter = warp % 4, key = k0 + quarter * 32 + lane;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
@@ -301,20 +344,15 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         const uint32_t to_p = p_at + lanes + kStep * way, to_ds = ds_at + lanes + kStep * way;
         const float c = score_scale(a.scale);
         const float2 c2 = make_float2(c, c);
+        bool ok = true;
         float ds_unit = 1.f;                                  // dS is multiplied by it
-        if constexpr (kUnits<T>) {
-            float top = 0.f;
-            for (int i = lane; i < total; i += 32) {
-                const int h = kh * a.group + (begin + i) / count, q = (tiles.low + (begin + i) % count) * kTile;
-                const float4 x = *reinterpret_cast<const float4 *>(a.peak + ((int64_t(b) * a.hq + h) * a.sq_pad + q) / 32);
-                top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
-            }
-            ds_unit = unit_of(warp_max(top));
+        if (kUnits<T> && total > 0) {
+            ok = __all_sync(0xffffffffu, wait(unit_ready, 0));
+            ds_unit = units[0];
         }
         const float2 p2 = make_float2(kProbabilityExponent, kProbabilityExponent);
         const float2 unit2 = make_float2(ds_unit * kProbabilityUnit, ds_unit * kProbabilityUnit);
         const int k1 = k0 + kTile - 1, seen_by = last_position(a, key) - shift;
-        bool ok = true;
         int q0 = (tiles.low + (total > 0 ? begin % count : 0)) * kTile;
         for (int i = 0; i < total; ++i, q0 = q0 + kTile < tiles.high * kTile ? q0 + kTile : tiles.low * kTile) {
             ok = __all_sync(0xffffffffu, wait(s_full, i & 1));
@@ -420,11 +458,15 @@ attention_dkv_kernel(const __grid_constant__ AttentionArgs a, const __grid_const
         // rows that are no numbers, again from the definition: dk and dv of a row together
         const uint32_t bad = __ballot_sync(0xffffffffu, ok && exists && !finite);
         if (lane == 0) bad_rows[warp] = bad;
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps + (kUnits<T> ? 32 : 0)) : "memory");
         uint32_t again = bad_rows[quarter] | bad_rows[quarter + 4] | bad_rows[quarter + 8] | bad_rows[quarter + 12];
-        if (way == 0)
-            for (; again != 0; again &= again - 1)
-                mend_dkv_row<T>(a, b, kh, k0, k0 + quarter * 32 + __ffs(int(again)) - 1);
+        if (again != 0 || unit < shared) {
+            const bool past = kUnits<T> && total > 0 && past_half(ds_unit, units[1], units[3], units[2]);
+            if (unit < shared && threadIdx.x == 0) split.past[blockIdx.x] = past;
+            // a quarter's rows go round its warps
+            for (int x = 0; again != 0; again &= again - 1, ++x)
+                if (x % kWays == way) mend_dkv_row<T>(a, b, kh, k0, k0 + quarter * 32 + __ffs(int(again)) - 1, past);
+        }
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -748,10 +790,12 @@ attention_dq_kernel(const __grid_constant__ AttentionArgs a, const __grid_consta
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kValueWarps) : "memory");
         for (int r = ok ? *bad_from : rounds; r < rounds; ++r) {
             const int w = item_of(r);
-            if (w >= items || way != r % kWays) continue;
+            if (w >= items) continue;
             const QueryTile t(a, w);
             const int row0 = t.q0 + quarter * 32, row = row0 + lane;
-            uint32_t again = __ballot_sync(0xffffffffu, row < a.sq && any_in_row<T>(row_of<const T>(a.dq, t.b, row < a.sq ? row : 0, t.h), a.d));
+            // a quarter's rows go round its warps
+            uint32_t again = __ballot_sync(0xffffffffu, lane % kWays == way && row < a.sq &&
+                                                            any_in_row<T>(row_of<const T>(a.dq, t.b, row < a.sq ? row : 0, t.h), a.d));
             for (; again != 0; again &= again - 1) mend_dq_row<T>(a, t.b, t.h, t.q0, row0 + __ffs(int(again)) - 1);
         }
     }
@@ -794,7 +838,11 @@ __global__ void __launch_bounds__(256) key_join_kernel(const __grid_constant__ A
                 make_uint2(pack_pair<T>(g[x][0], g[x][1]), pack_pair<T>(g[x][2], g[x][3]));
     }
     __syncwarp();                                             // after the stores above
-    if (!__all_sync(0xffffffffu, finite)) mend_dkv_row<T>(a, b, kh, tile * kTile, key);
+    if (__all_sync(0xffffffffu, finite)) return;
+    bool past = false;
+    for (int p = split.first[tile]; p < split.first[tile + 1]; ++p)
+        past = past || split.past[int64_t(p) * heads + head] != 0;
+    mend_dkv_row<T>(a, b, kh, tile * kTile, key, past);
 }
 
 template <class T, int HD>
@@ -841,8 +889,10 @@ KeySplit key_split(const AttentionArgs &a) {
     return s;
 }
 
+int64_t key_split_parts(const AttentionArgs &a, const KeySplit &s) { return int64_t(s.first[s.tiles]) * a.batch * a.hkv; }
+
 int64_t key_split_bytes(const AttentionArgs &a, const KeySplit &s) {
-    return int64_t(s.first[s.tiles]) * a.batch * a.hkv * 2 * kTile * (a.d <= 64 ? 64 : 128) * int64_t(sizeof(float));
+    return (ceil_div(key_split_parts(a, s), 4) * 4 + key_split_parts(a, s) * 2 * kTile * (a.d <= 64 ? 64 : 128)) * int64_t(sizeof(float));
 }
 
 basp_status launch_attention_backward(const AttentionArgs &a, const HeadMaps &m, const KeySplit &s, bool bf16,

@@ -27,7 +27,12 @@ struct AttentionArgs {
     // does not exist, or sees nothing: (infinity, 0)
     float2 *stats;
     uint16_t *fold;                      // the same as parts of a product, two planes a tile of queries
-    float *unit, *peak;                  // fp16: unit_of each query's dO [batch][Hq][sq_pad], and 32 queries' largest |dO|
+    // fp16: unit_of each query's dO [batch][Hq][sq_pad]; of 32 queries the largest |dO|, sum of |dO|
+    // and |D| (infinite where a part of lse or D of one is past the type's range); of each tile of
+    // keys the largest |v|
+    float *unit;
+    float4 *peak;
+    float *v_peak;
     int batch, sq, sk, sq_pad, hq, hkv, d, group;
     int window, sinks;                   // window: sk where all is visible
     float scale;
@@ -109,6 +114,19 @@ __device__ __forceinline__ float unit_of(float m) {
     return m > 0.f ? __uint_as_float((254u << 23) - (__float_as_uint(m) & 0x7f800000u)) : 1.f;
 }
 __device__ __forceinline__ float over_unit(float unit) { return __uint_as_float((254u << 23) - __float_as_uint(unit)); }
+
+// |dP - D| is at most sum |dO| max |v| + |D|: whether that is past fp16 in the unit, a factor of four
+// kept for P.  Of finite values: where dS is no number itself, this does not say so.
+__device__ __forceinline__ bool past_half(float unit, float sum, float v, float d) {
+    return unit * fmaf(sum, v, d) > 65504.f / 4;
+}
+template <class T> __device__ __forceinline__ float finite_peak(uint4 x) {
+    float f[8], top = 0.f;
+    Pack<T>::unpack(x, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]) < INFINITY ? fabsf(f[j]) : 0.f);
+    return top;
+}
 
 // A wait on one of the CTA's barriers, with a limit.
 constexpr uint64_t kAttentionWaitNs = 2000000000ull;
@@ -375,9 +393,10 @@ __device__ __noinline__ void dkv_row(const AttentionArgs &a, int b, int kh, int 
 // ---- rows of tiles that came out infinite or NaN -------------------------------------
 //
 // A masked pair has P = 0 and dS = 0, but 0 times an infinite or NaN value is NaN.  Only a
-// row with such a value among what its tiles hold and it does not see is computed again:
-// where what it sees is no number itself, the tiles' answer is the definition's, and a
-// batch that has become NaN costs no more than another.
+// row with such a value among what its tiles hold and it does not see is computed again, and in
+// fp16 one that met a dS, lse or D past the type's range: where what a row sees is no number
+// itself, the tiles' answer is the definition's.  So a batch that has become NaN costs the search
+// through the ends of its tiles, a row at a time, and no walk over all that a row sees.
 
 // Whether a row holds a value that is infinite or NaN.
 template <class T> __device__ __forceinline__ bool any_in_row(const T *row, int d) {
@@ -424,16 +443,34 @@ __device__ __noinline__ bool masked_queries_not_finite(const AttentionArgs &a, i
     return false;
 }
 
-// fp16 has other reasons: dS, or a part of lse or D, past its range.
-template <class T> constexpr bool kOtherReasons = std::is_same_v<T, __half>;
+// Whether dS of query i, of the tile from r0, can have been past fp16.
+template <class T> __device__ __noinline__ bool dq_past_half(const AttentionArgs &a, int b, int h, int r0, int i) {
+    const int lane = threadIdx.x % 32;
+    const KeyTiles tiles = key_tiles(a, r0);
+    const float *tops = a.v_peak + (int64_t(b) * a.hkv + h / a.group) * ((a.sk + kTile - 1) / kTile);
+    float v = 0.f, sum = 0.f;
+    for (int j = lane; j < tiles.first; j += 32) v = fmaxf(v, tops[j]);
+    for (int j = tiles.low + lane; j < tiles.high; j += 32) v = fmaxf(v, tops[j]);
+    const T *row = row_of<const T>(a.d_o, b, i, h);
+    for (int e = lane; e < a.d; e += 32) {
+        const float x = fabsf(Elem<T>::to_float(row[e]));
+        sum += x < INFINITY ? x : 0.f;
+    }
+    const int64_t at = (int64_t(b) * a.hq + h) * a.sq_pad + i;
+    const float d = fabsf(a.stats[at].y);
+    return d < INFINITY && past_half(a.unit[at], warp_add(sum), warp_max(v), d);
+}
 
 template <class T>
 __device__ __forceinline__ void mend_dq_row(const AttentionArgs &a, int b, int h, int r0, int i) {
-    if (kOtherReasons<T> || masked_keys_not_finite<T>(a, a.k, b, h / a.group, r0, i + a.sk - a.sq)) dq_row<T>(a, b, h, i);
+    bool past = false;
+    if constexpr (kUnits<T>) past = dq_past_half<T>(a, b, h, r0, i);
+    if (past || masked_keys_not_finite<T>(a, a.k, b, h / a.group, r0, i + a.sk - a.sq)) dq_row<T>(a, b, h, i);
 }
+// `past`: something can have been past the type's range.
 template <class T>
-__device__ __forceinline__ void mend_dkv_row(const AttentionArgs &a, int b, int kh, int k0, int j) {
-    if (kOtherReasons<T> || masked_queries_not_finite<T>(a, b, kh, k0, j)) dkv_row<T>(a, b, kh, j);
+__device__ __forceinline__ void mend_dkv_row(const AttentionArgs &a, int b, int kh, int k0, int j, bool past) {
+    if (past || masked_queries_not_finite<T>(a, b, kh, k0, j)) dkv_row<T>(a, b, kh, j);
 }
 
 }  // namespace basp_fp8

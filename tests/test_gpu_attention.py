@@ -541,3 +541,72 @@ def test_small_gradients_in_fp16(S, Hq, Hkv, window, sinks, kind, d):
     want, bound = gradients_in_units(r, f64(do[0]), r.o_bound, 2.0 ** 10, 1 / top, 1 / top.max())
     for name, g in zip(("dq", "dk", "dv"), got):
         close(g[0], want[name], bound[name])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 2.0])
+@pytest.mark.parametrize("S,Hq,Hkv,window,sinks", [(300, 2, 1, 2, 0), (2500, 2, 1, 3, 4), (700, 4, 2, 1, 1), (300, 1, 1, None, 0)])
+def test_past_fp16(S, Hq, Hkv, window, sinks, size, d):
+    """dS past what fp16 holds in units of do, in tiles of keys that CTAs share too; with heads
+    of 128 or twice the gradient, D past what its parts hold: such rows are the definition's."""
+    t = torch.float16
+    q, k, v, do = tensors(1, S, S, Hq, Hkv, d, t)
+    v = (v[..., :1].float().sign() * 60000).to(t).expand(1, S, Hkv, d).contiguous()      # one sign a token
+    q, k, do = q * 2.0 ** -12, k * 2.0 ** -12, torch.full_like(do, size)
+    o, lse = attention.forward(q, k, v, window, sinks)
+    got = attention.backward(do, q, k, v, o, lse, window, sinks)
+    r = Attention(f64(q[0]), f64(k[0]), f64(v[0]), window, sinks, d ** -0.5, u(t))
+    want, bound = r.backward(f64(do)[0], r.o_bound)
+    assert max(np.abs(r.p[h] * (f64(do)[0, :, h] @ f64(v)[0, :, h // (Hq // Hkv)].T)).max() for h in range(Hq)) > 2 * 65504 * size
+    for name, g in zip(("dq", "dk", "dv"), got):
+        close(g[0], want[name], bound[name])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["k", "v", "q", "do"])
+@pytest.mark.parametrize("at", [0, 60, 130, 299])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_is_not_seen_has_no_part_in_fp16(where, bad, at, d):
+    """As above; and rows that do see a NaN are NaN by the tiles' answer."""
+    S, window, sinks = 300, 90, 3
+    x = dict(zip(("q", "k", "v", "do"), tensors(1, S, S, 2, 1, d, torch.float16)))
+    r = Attention(*(f64(x[n])[0] for n in ("q", "k", "v")), window, sinks, d ** -0.5, u(torch.float16))
+    want, bound = r.backward(f64(x["do"])[0], r.o_bound)
+    x[where][0, at, 0, 7] = bad
+    o, lse = attention.forward(x["q"], x["k"], x["v"], window, sinks)
+    grads = attention.backward(x["do"], x["q"], x["k"], x["v"], o, lse, window, sinks)
+    sees = r.sees
+    touched = sees[:, at] if where in ("k", "v") else np.arange(S) == at
+    keys = sees[touched].any(0)
+    for name, g, rows in zip(("dq", "dk", "dv"), grads, (touched, keys, keys)):
+        close(g[0][torch.from_numpy(~rows).cuda()], want[name][~rows], bound[name][~rows])
+    if bad != bad:
+        heads = slice(None) if where in ("k", "v") else 0
+        assert bool(torch.isnan(grads[0][0][torch.from_numpy(touched).cuda()][:, heads].float()).any(-1).all())
+        assert bool(torch.isnan(grads[1][0][torch.from_numpy(keys).cuda()].float()).any(-1).all())
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_one_overflow_costs_little(dtype):
+    """An infinity in the last query's gradient makes every key's row no number: that is the
+    tiles' answer, and no row is walked again for it.  (Walked, it was some hundred times as long.)"""
+    S, H, d = 8192, 8, 64
+    q, k, v, do = tensors(1, S, S, H, H, d, DTYPES[dtype])
+    o, lse = attention.forward(q, k, v)
+
+    def best():
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            got = attention.backward(do, q, k, v, o, lse)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times), got
+
+    plain, _ = best()
+    do[0, S - 1, :, 3] = float("inf")
+    bad, (dq, dk, dv) = best()
+    assert bool(torch.isfinite(dq[0, :S - 1]).all()) and not bool(torch.isfinite(dk).any()) and not bool(torch.isfinite(dv[..., 3]).any())
+    assert bad <= 40 * plain
