@@ -176,9 +176,9 @@ inline void adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_ad
                   cudaStream_t stream) {
     check(basp_adamw(tensors, count, &options, stream), "basp_adamw");
 }
-inline void adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
-                       const basp_adamw_options &options, cudaStream_t stream) {
-    check(basp_adamw_each(tensors, steps_at, count, &options, stream), "basp_adamw_each");
+inline void adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, const uint32_t *numbers,
+                       int64_t count, const basp_adamw_options &options, cudaStream_t stream) {
+    check(basp_adamw_each(tensors, steps_at, numbers, count, &options, stream), "basp_adamw_each");
 }
 
 }  // namespace basp

@@ -66,12 +66,15 @@ basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count,
                        const basp_adamw_options *options, cudaStream_t stream);
 
 /*
- * The same for tensors that have taken different numbers of steps.
- *   steps_at    [count], in host memory: for each tensor where its own t is in device
- *               memory, read as step_at is.  The options' step and step_at are not used
+ * The same for tensors that have taken different numbers of steps, or that come in
+ * other lists from step to step.  Both in host memory:
+ *   steps_at    [count]: for each tensor where its own t is in device memory, read as
+ *               step_at is; the options' step and step_at are not used.  Or NULL
+ *   numbers     [count]: the tensors' numbers for the random bits, in place of their
+ *               places in the list; or NULL
  */
-basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
-                            const basp_adamw_options *options, cudaStream_t stream);
+basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, const uint32_t *numbers,
+                            int64_t count, const basp_adamw_options *options, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -179,8 +179,8 @@ def load_library():
     lib.basp_attention_timeouts.restype = ci
     lib.basp_adamw.argtypes = [ctypes.POINTER(basp_adamw_tensor), i64, ctypes.POINTER(basp_adamw_options), vp]
     lib.basp_adamw.restype = ci
-    lib.basp_adamw_each.argtypes = [ctypes.POINTER(basp_adamw_tensor), ctypes.POINTER(vp), i64,
-                                    ctypes.POINTER(basp_adamw_options), vp]
+    lib.basp_adamw_each.argtypes = [ctypes.POINTER(basp_adamw_tensor), ctypes.POINTER(vp),
+                                    ctypes.POINTER(ctypes.c_uint32), i64, ctypes.POINTER(basp_adamw_options), vp]
     lib.basp_adamw_each.restype = ci
     if hasattr(lib, "basp_debug_bounds_violations"):
         lib.basp_debug_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
@@ -661,13 +661,16 @@ def basp_adamw(tensors, options, stream=None):
     _check(load_library().basp_adamw(table, len(tensors), options, _stream(stream)), "basp_adamw")
 
 
-def basp_adamw_each(tensors, steps_at, options, stream=None):
-    """The same with a number of steps for each tensor: int32 tensors or addresses on the GPU."""
+def basp_adamw_each(tensors, steps_at, options, stream=None, numbers=None):
+    """The same with a number of steps for each tensor (int32 tensors or addresses on the
+    GPU, or None), and with the tensors' numbers for the random bits."""
     w, n = "basp_adamw_each", len(tensors)
-    if len(steps_at) != n:
-        raise ValueError("%s: %d numbers of steps for %d tensors" % (w, len(steps_at), n))
-    table, at = (basp_adamw_tensor * n)(*tensors), (ctypes.c_void_p * n)(*(_ptr(s) for s in steps_at))
-    _check(load_library().basp_adamw_each(table, at, n, options, _stream(stream)), w)
+    for name, x in (("steps", steps_at), ("tensors", numbers)):
+        if x is not None and len(x) != n:
+            raise ValueError("%s: %d numbers of %s for %d tensors" % (w, len(x), name, n))
+    at = None if steps_at is None else (ctypes.c_void_p * n)(*(_ptr(s) for s in steps_at))
+    no = None if numbers is None else (ctypes.c_uint32 * n)(*numbers)
+    _check(load_library().basp_adamw_each((basp_adamw_tensor * n)(*tensors), at, no, n, options, _stream(stream)), w)
 
 
 class Layout:

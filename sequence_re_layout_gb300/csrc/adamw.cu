@@ -32,10 +32,11 @@ struct Entry {
     void *m, *v, *ms, *vs;
     const int32_t *step_at;                          // its step's number, or NULL: Options::step
     int64_t n;
+    uint32_t number;                                 // for the random bits
     int32_t chunk0;                                  // its first chunk in the launch
-    uint8_t type, grad_type, vec, pad;
+    uint8_t type, grad_type, vec, pad[5];
 };
-static_assert(sizeof(Entry) == 72, "table");
+static_assert(sizeof(Entry) == 80, "table");
 
 struct Options {
     float beta1, beta2, one_beta1, one_beta2, eps, decay, lr;   // decay: 1 - lr * weight_decay
@@ -46,7 +47,7 @@ struct Options {
 
 template <int CAP> struct Table {
     Options o;
-    int32_t count, first;                            // entries; the first one's place in the caller's list
+    int32_t count, pad;                              // entries
     Entry e[CAP];
 };
 
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
         c1 = t.o.lr / -expm1f(float(s) * t.o.log_beta1);
         c2 = rsqrtf(-expm1f(float(s) * t.o.log_beta2));
     }
-    const uint32_t key = EIGHT ? mix(mix(mix(t.o.seed) ^ step) ^ uint32_t(t.first + lo)) : 0u;
+    const uint32_t key = EIGHT ? mix(mix(mix(t.o.seed) ^ step) ^ e.number) : 0u;
     auto go = [&](auto pe, auto ge) {
         using P = decltype(pe);
         using G = decltype(ge);
@@ -333,12 +334,12 @@ int64_t chunks_of(int64_t n) { return ceil_div(n, kChunk); }
 
 // One launch of entries [i0, i1) of the caller's list.
 template <int CAP>
-basp_status launch_adamw(const basp_adamw_tensor *list, const int32_t *const *steps_at, int64_t i0, int64_t i1, bool eight,
-                         const Options &o, const int32_t *step_at, int64_t *next, cudaStream_t stream) {
+basp_status launch_adamw(const basp_adamw_tensor *list, const int32_t *const *steps_at, const uint32_t *numbers, int64_t i0,
+                         int64_t i1, bool eight, const Options &o, const int32_t *step_at, int64_t *next, cudaStream_t stream) {
     Table<CAP> t;
     t.o = o;
     t.count = 0;
-    t.first = int32_t(i0);
+    t.pad = 0;
     int64_t chunks = 0, i = i0;
     for (; i < i1 && t.count < CAP; ++i) {
         const basp_adamw_tensor &x = list[i];
@@ -348,6 +349,7 @@ basp_status launch_adamw(const basp_adamw_tensor *list, const int32_t *const *st
         e.p = x.p; e.g = x.g; e.m = x.m; e.v = x.v; e.ms = x.m_scales; e.vs = x.v_scales;
         e.step_at = steps_at != nullptr ? steps_at[i] : step_at;
         e.n = x.n;
+        e.number = numbers != nullptr ? numbers[i] : uint32_t(i);
         e.chunk0 = int32_t(chunks);
         e.type = uint8_t(x.dtype);
         e.grad_type = uint8_t(x.grad_dtype);
@@ -355,7 +357,7 @@ basp_status launch_adamw(const basp_adamw_tensor *list, const int32_t *const *st
         const int64_t state = eight ? 1 : 4;
         e.vec = x.n % 4 == 0 && vec4_ok(x.p, 0, x.n, elem_size(x.dtype)) && vec4_ok(x.g, 0, x.n, elem_size(x.grad_dtype)) &&
                 vec4_ok(x.m, 0, x.n, state) && vec4_ok(x.v, 0, x.n, state);
-        e.pad = 0;
+        std::fill(e.pad, e.pad + sizeof(e.pad), uint8_t(0));
         chunks += c;
     }
     *next = i;
@@ -430,7 +432,7 @@ basp_status check_apart(const basp_adamw_tensor *list, int64_t count) {
     return BASP_OK;
 }
 
-basp_status adamw(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
+basp_status adamw(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, const uint32_t *numbers, int64_t count,
                   const basp_adamw_options *options, cudaStream_t stream) {
     if (count < 0 || options == nullptr || (tensors == nullptr && count > 0)) return BASP_ERR_INVALID_ARG;
     const basp_adamw_options &p = *options;
@@ -473,11 +475,11 @@ basp_status adamw(const basp_adamw_tensor *tensors, const int32_t *const *steps_
     basp_status st = BASP_OK;
     for (int64_t i = 0; i < count && st == BASP_OK;) {
         auto go = [&](auto cap) {
-            st = launch_adamw<decltype(cap)::value>(tensors, steps_at, i, count, eight, o, p.step_at, &i, stream);
+            st = launch_adamw<decltype(cap)::value>(tensors, steps_at, numbers, i, count, eight, o, p.step_at, &i, stream);
         };
         if (count - i <= 12) go(std::integral_constant<int, 12>());
         else if (count - i <= 60) go(std::integral_constant<int, 60>());
-        else go(std::integral_constant<int, 440>());
+        else go(std::integral_constant<int, 400>());
     }
     return st;
 }
@@ -488,13 +490,12 @@ basp_status adamw(const basp_adamw_tensor *tensors, const int32_t *const *steps_
 extern "C" basp_status basp_adamw(const basp_adamw_tensor *tensors, int64_t count, const basp_adamw_options *options,
                                   cudaStream_t stream) {
     basp_fp8::NvtxRange range("basp_adamw");
-    return basp_fp8::adamw(tensors, nullptr, count, options, stream);
+    return basp_fp8::adamw(tensors, nullptr, nullptr, count, options, stream);
 }
 
-extern "C" basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at, int64_t count,
-                                       const basp_adamw_options *options, cudaStream_t stream) {
+extern "C" basp_status basp_adamw_each(const basp_adamw_tensor *tensors, const int32_t *const *steps_at,
+                                       const uint32_t *numbers, int64_t count, const basp_adamw_options *options,
+                                       cudaStream_t stream) {
     basp_fp8::NvtxRange range("basp_adamw_each");
-    if (steps_at == nullptr && count > 0) return BASP_ERR_INVALID_ARG;
-    static const int32_t *const none = nullptr;
-    return basp_fp8::adamw(tensors, steps_at != nullptr ? steps_at : &none, count, options, stream);
+    return basp_fp8::adamw(tensors, steps_at, numbers, count, options, stream);
 }

@@ -690,11 +690,11 @@ void *dense(const Tensor &x, int64_t n, at::ScalarType type, int device, const c
 }
 
 // adamw(params, grads, m, v, m_scales, v_scales (both None with 32-bit states), step (or a list of them), lr, beta1, beta2, eps,
-//       weight_decay, seed)
+//       weight_decay, seed, numbers or None)
 PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const char *where = "adamw";
-    if (!arguments(n, 13, where)) return nullptr;
+    if (!arguments(n, 14, where)) return nullptr;
     const Sequence params(args[0], -1, where, "params");
     const Py_ssize_t count = params.size();
     const Sequence grads(args[1], count, where, "grads"), m(args[2], count, where, "m"), v(args[3], count, where, "v");
@@ -723,6 +723,12 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
         o.step_at = static_cast<const int32_t *>(dense(step, 1, at::kInt, device, where, "step"));
     } else {
         o.step = whole(args[6], where, "step", 1);
+    }
+    std::vector<uint32_t> places;                 // the tensors' numbers
+    if (args[13] != Py_None) {
+        const Sequence given(args[13], count, where, "numbers");
+        for (Py_ssize_t i = 0; i < count; ++i)
+            places.push_back(uint32_t(whole(PySequence_Fast_GET_ITEM(given.p, i), where, "a tensor's number", 0)));
     }
     std::vector<basp_adamw_tensor> list(static_cast<size_t>(count));
     const auto state = eight ? at::kFloat8_e4m3fn : at::kFloat;
@@ -755,8 +761,10 @@ PyObject *adamw(PyObject *, PyObject *const *args, Py_ssize_t n) {
         }
     }
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
-    if (!(steps.has_value() ? check(g_lib.adamw_each(list.data(), steps_at.data(), count, &o, stream), "basp_adamw_each")
-                            : check(g_lib.adamw(list.data(), count, &o, stream), "basp_adamw")))
+    const int32_t *const *at = steps.has_value() ? steps_at.data() : nullptr;
+    const uint32_t *no = args[13] != Py_None ? places.data() : nullptr;
+    if (!(at == nullptr && no == nullptr ? check(g_lib.adamw(list.data(), count, &o, stream), "basp_adamw")
+                                         : check(g_lib.adamw_each(list.data(), at, no, count, &o, stream), "basp_adamw_each")))
         return nullptr;
     for (Py_ssize_t i = 0; i < count; ++i) {
         written(params.seen(i));

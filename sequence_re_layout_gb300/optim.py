@@ -16,7 +16,8 @@ from . import fp8
 
 
 @torch.no_grad()
-def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, seed=0):
+def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, seed=0,
+          numbers=None):
     """One step over lists of tensors, in place: params (bfloat16, float16 or
     float32), grads (their type or float32), and the states m and v: float32 tensors,
     or :class:`fp8.Quantized` of one row ([1, n]), v then the root of v.
@@ -24,7 +25,8 @@ def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weig
     ``step`` counts from 1; as an int32 tensor of one element on the GPU it is read
     when the kernel runs, so that a captured step can be replayed; a list of those has
     one for each parameter.  The random rounding of 8-bit states depends on ``seed``,
-    the step and each element's place alone.  Every tensor is dense, and none overlaps
+    the step, the tensor's number (its place in the list, or ``numbers``) and each
+    element's place alone.  Every tensor is dense, and none overlaps
     another: the same parameter twice is refused."""
     m, v = list(m), list(v)
     m_scales = v_scales = None
@@ -32,7 +34,7 @@ def adamw(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weig
         m, m_scales = _parts(m)
         v, v_scales = _parts(v)
     (fp8._ops or fp8._load()).adamw(list(params), list(grads), m, v, m_scales, v_scales, step, lr, betas[0], betas[1],
-                                    eps, weight_decay, seed)
+                                    eps, weight_decay, seed, numbers)
 
 
 def _parts(states):
@@ -78,12 +80,13 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        before = 0                                    # parameters of the groups before
         for group in self.param_groups:
             if not group["capturable"] and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("AdamW: a captured step would keep its number: pass capturable=True")
             capturable = group["capturable"]
-            together = {}                             # of each step's number, where it is known: (parameters, gradients, states)
-            for p in group["params"]:
+            together = {}                             # of each step's number, where it is known: (parameters, gradients, states, their numbers)
+            for i, p in enumerate(group["params"]):
                 g = p.grad
                 if g is None:
                     continue
@@ -96,25 +99,28 @@ class AdamW(torch.optim.Optimizer):
                 number = None if capturable else s["step"]
                 lists = together.get(number)
                 if lists is None:
-                    lists = together[number] = [], [], []
+                    lists = together[number] = [], [], [], []
                 lists[0].append(p)
                 lists[1].append(g if g.is_contiguous() else g.contiguous())
                 lists[2].append(s)
-            for params, grads, states in together.values():
-                self._take(params, grads, states, group)
+                lists[3].append(before + i)
+            for lists in together.values():
+                self._take(*lists, group)
+            before += len(group["params"])
         return loss
 
-    def _take(self, params, grads, states, group):
+    def _take(self, params, grads, states, numbers, group):
         if group["capturable"]:
             step = [s["step"] for s in states]
             torch._foreach_add_(step, 1)
         else:
             step = states[0]["step"] + 1
         if group["state_bits"] == 32:
-            m, v = [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states]
+            m, v, numbers = [s["exp_avg"] for s in states], [s["exp_avg_sq"] for s in states], None
         else:
             m, v = ([fp8.Quantized(s[n], s[n + "_scales"]) for s in states] for n in ("exp_avg", "exp_avg_sq_root"))
-        adamw(params, grads, m, v, step, group["lr"], group["betas"], group["eps"], group["weight_decay"], group["seed"])
+        adamw(params, grads, m, v, step, group["lr"], group["betas"], group["eps"], group["weight_decay"], group["seed"],
+              numbers)
         if not group["capturable"]:
             for s in states:
                 s["step"] = step

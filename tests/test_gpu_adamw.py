@@ -422,3 +422,42 @@ def test_captured_steps_of_some_and_of_all():
     for x, y in zip(nets[0].parameters(), nets[1].parameters()):
         assert int(opts[0].state[x]["step"]) == opts[1].state[y]["step"]
         assert bool(((x - y).abs() <= 7 * (0.02 * 2.0 ** -18 + 2.0 ** -23 * y.abs())).all())
+
+
+def test_numbers_of_the_tensors():
+    """The bits follow a tensor's number, not its place in the list."""
+    def make():
+        p, g = ([random(777, torch.float32, i + s) for i in range(5)] for s in (0, 10))
+        m, v = ([quantized(random(777, torch.float32, i + s).abs()) for i in range(5)] for s in (20, 30))
+        return p, g, m, v
+    a, b, c = make(), make(), make()
+    optim.adamw(*a, step=3, seed=2)
+    order = [3, 0, 4, 2, 1]
+    optim.adamw(*([x[i] for i in order] for x in b), step=3, seed=2, numbers=order)
+    for x, y in zip(a[2] + a[3], b[2] + b[3]):
+        assert torch.equal(x.dequantize(), y.dequantize())
+    optim.adamw(*c, step=3, seed=2, numbers=[1000, 2 ** 32 - 1, 7, 6, 5])
+    for x, y, number in ((a, c, 0),):
+        assert all(torch.equal(s, t) for s, t in zip(x[0], y[0]))       # the step is made before the rounding
+        assert not any(torch.equal(s.dequantize(), t.dequantize()) for s, t in zip(x[2] + x[3], y[2] + y[3]))
+    for bad in ([1, 2], [1, 2, 3, 4, "5"], [0, 1, 2, 3, -1], 5):
+        with pytest.raises(ValueError):
+            optim.adamw(*a, step=4, numbers=bad)
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_bits_of_groups_and_of_missing_gradients(capturable):
+    """Equal parameters of two groups are rounded by bits of their own, and a parameter's bits do
+    not depend on whether one before it has a gradient."""
+    def run(first):
+        ps = [torch.nn.Parameter(random(2000, torch.float32, s)) for s in (1, 2, 1, 2)]
+        o = optim.AdamW([{"params": ps[:2]}, {"params": ps[2:]}], state_bits=8, seed=3, capturable=capturable)
+        for i in range(3):
+            for j, p in enumerate(ps):
+                p.grad = random(2000, torch.float32, 10 * i + j % 2) if first or j % 2 else None
+            o.step()
+        return [(o.state[p]["exp_avg"].float(), o.state[p]["exp_avg_sq_root"].float()) if o.state.get(p) else None for p in ps]
+    a, b = run(True), run(False)
+    for i in (0, 1):
+        assert not torch.equal(a[0][i], a[2][i]) and not torch.equal(a[1][i], a[3][i])
+        assert torch.equal(a[1][i], b[1][i]) and torch.equal(a[3][i], b[3][i])

@@ -339,16 +339,19 @@ def test_parameters_count_the_steps_they_take(capturable, bits, monkeypatch):
 def test_numbers_of_steps_of_their_own(lib):
     def status(tensors, steps, **change):
         table, at = (basp.basp_adamw_tensor * len(tensors))(*tensors), (ctypes.c_void_p * len(tensors))(*steps)
-        return lib.basp_adamw_each(table, at, len(tensors), basp.basp_adamw_options(**{**OPTIONS, "step": 0, **change}), None)
+        return lib.basp_adamw_each(table, at, None, len(tensors), basp.basp_adamw_options(**{**OPTIONS, "step": 0, **change}), None)
     assert status([adam(1)], [at(90) + 2]) == ALIGN and status([adam(1, n=0)], [at(90) + 2]) == ALIGN
     assert status([adam(1), adam(10)], [at(90), None]) == INVALID and status([adam(1, p=None)], [at(90)]) == INVALID
     assert status([adam(1, n=0)], [None]) == OK and status([], []) == OK
     assert status([adam(1), adam(1)], [at(90), at(91)]) == ALIAS and status([adam(1)], [at(90)], lr=-1.0) == INVALID
     o = basp.basp_adamw_options(**OPTIONS)
-    assert lib.basp_adamw_each((basp.basp_adamw_tensor * 1)(adam(1)), None, 1, o, None) == INVALID
-    assert lib.basp_adamw_each(None, None, 0, o, None) == OK and lib.basp_adamw_each(None, None, -1, o, None) == INVALID
-    with pytest.raises(ValueError):
-        basp.basp_adamw_each([adam(1)], [], o)
+    assert lib.basp_adamw_each((basp.basp_adamw_tensor * 1)(adam(1, p=None)), None, None, 1, o, None) == INVALID
+    assert lib.basp_adamw_each(None, None, None, 0, o, None) == OK and lib.basp_adamw_each(None, None, None, -1, o, None) == INVALID
+    o.step = 0
+    assert lib.basp_adamw_each(None, None, None, 0, o, None) == INVALID
+    for change in (dict(steps_at=[]), dict(steps_at=None, numbers=[])):
+        with pytest.raises(ValueError):
+            basp.basp_adamw_each([adam(1)], options=o, **change)
 
 
 @pytest.mark.parametrize("offset", [0, 1, 3, 4, 8, 16])
