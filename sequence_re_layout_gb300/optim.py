@@ -53,12 +53,24 @@ class AdamW(torch.optim.Optimizer):
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, seed=0,
                  capturable=False):
-        if state_bits not in (8, 32):
-            raise ValueError("AdamW: state_bits must be 8 or 32, got %r" % (state_bits,))
-        if not (lr >= 0 and eps >= 0 and weight_decay >= 0 and all(0 <= b < 1 for b in betas)):
-            raise ValueError("AdamW: lr, eps and weight_decay must not be negative, betas in [0, 1)")
-        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
-                                      state_bits=state_bits, seed=seed, capturable=capturable))
+        defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay, state_bits=state_bits, seed=seed,
+                        capturable=capturable)
+        self._check(defaults)
+        super().__init__(params, defaults)
+
+    @staticmethod
+    def _check(options):
+        if options["state_bits"] not in (8, 32):
+            raise ValueError("AdamW: state_bits must be 8 or 32, got %r" % (options["state_bits"],))
+        if not (options["lr"] >= 0 and options["eps"] >= 0 and options["weight_decay"] >= 0 and
+                len(options["betas"]) == 2 and all(0 <= b < 1 for b in options["betas"])):
+            raise ValueError("AdamW: lr, eps and weight_decay must not be negative, betas two in [0, 1)")
+
+    def add_param_group(self, param_group):
+        """As torch's; a group's own options are checked as the constructor's are."""
+        if isinstance(param_group, dict):
+            self._check({**self.defaults, **param_group})
+        super().add_param_group(param_group)
 
     def _init(self, p, group):
         state = self.state[p]

@@ -367,3 +367,22 @@ def test_gradients_that_begin_anywhere(offset):
         got = autograd._aligned(spread)
         assert got.data_ptr() % 16 == 0 and torch.equal(got, spread) and got.stride(-1) == 1
         assert all(s % 8 == 0 for s, n in zip(got.stride()[:-1], got.shape) if n > 1) or spread.shape[-1] == 4
+
+
+@pytest.mark.parametrize("bad", [dict(state_bits=16), dict(lr=-1.0), dict(lr=float("nan")), dict(eps=-1e-8), dict(weight_decay=-0.1),
+                                 dict(betas=(0.9, 1.0)), dict(betas=(-0.1, 0.9)), dict(betas=(0.9,))])
+def test_options_of_a_group(bad):
+    """A group's own options are refused as the constructor's are, and the group is not taken."""
+    a, b = (torch.nn.Parameter(torch.zeros(3)) for _ in range(2))
+    with pytest.raises(ValueError):
+        optim.AdamW([a], **bad)
+    with pytest.raises(ValueError):
+        optim.AdamW([{"params": [a], **bad}])
+    o = optim.AdamW([a])
+    with pytest.raises(ValueError):
+        o.add_param_group({"params": [b], **bad})
+    assert len(o.param_groups) == 1
+    o.add_param_group({"params": [b], "state_bits": 8, "lr": 0.0})
+    assert [g["state_bits"] for g in o.param_groups] == [32, 8]
+    with pytest.raises(TypeError):
+        o.add_param_group([b])
