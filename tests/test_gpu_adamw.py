@@ -461,3 +461,39 @@ def test_bits_of_groups_and_of_missing_gradients(capturable):
     for i in (0, 1):
         assert not torch.equal(a[0][i], a[2][i]) and not torch.equal(a[1][i], a[3][i])
         assert torch.equal(a[1][i], b[1][i]) and torch.equal(a[3][i], b[3][i])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("offset", [0, 1, 3, 8])
+def test_nothing_is_written_beside_the_tensors(offset, dtype, bits):
+    """Every buffer lies in a larger one, whose other elements stay as they were."""
+    t, guard = DTYPES[dtype], 40
+    for n in (1, 3, 4, 127, 128, 130, 517, 4096, 16390):
+        def inside(values, fill):
+            whole = torch.full((n_of(values) + 2 * guard,), fill, dtype=values.dtype, device="cuda")
+            at = (guard & ~15) + offset
+            whole[at:at + n_of(values)] = values.view(-1)
+            return whole, whole[at:at + n_of(values)].view(values.shape), at
+        n_of = lambda x: x.numel()                            # noqa: E731
+        p, g = random(n, t, 1), random(n, t, 2)
+        m, v = random(n, torch.float32, 3), random(n, torch.float32, 4).square()
+        if bits == 32:
+            want = [p.clone(), g, m.clone(), v.clone()]
+            optim.adamw(*([x] for x in want), step=3)
+            places = [inside(x, 7.0) for x in (p, g, m, v)]
+            optim.adamw(*([x[1]] for x in places), step=3)
+        else:
+            m, v = quantized(m), quantized(v.sqrt())
+            want = [p.clone(), g, m.data.clone(), m.scales.clone(), v.data.clone(), v.scales.clone()]
+            state = [fp8.Quantized(want[2], want[3]), fp8.Quantized(want[4], want[5])]
+            optim.adamw([want[0]], [g], [state[0]], [state[1]], step=3)
+            want = [x.view(torch.uint8) if x.element_size() == 1 else x for x in want]
+            places = [inside(x, 7.0) for x in (p, g)] + [inside(x.view(torch.uint8), 7) for x in (m.data, m.scales, v.data, v.scales)]
+            as8 = lambda i, ty: places[i][1].view(1, -1).view(ty)          # noqa: E731
+            e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+            optim.adamw([places[0][1]], [places[1][1]], [fp8.Quantized(as8(2, e4m3), as8(3, e8m0))],
+                        [fp8.Quantized(as8(4, e4m3), as8(5, e8m0))], step=3)
+        for x, (whole, part, at) in zip(want, places):
+            assert torch.equal(part.view(-1), x.view(-1))
+            assert bool((whole[:at] == 7).all()) and bool((whole[at + x.numel():] == 7).all())

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import sequence_re_layout_gb300 as basp
 from layer_reference import Attention
 from sequence_re_layout_gb300 import attention, fp8, optim
 from test_gpu_attention import _built, close, f64, random, u         # noqa: F401
@@ -172,3 +173,7 @@ def test_two_graphs_at_a_time():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(c, e) for c, e in zip(a, b))
+
+
+def test_zz_no_wait_ran_out():
+    assert basp.basp_attention_timeouts() == 0

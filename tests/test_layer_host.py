@@ -386,3 +386,13 @@ def test_options_of_a_group(bad):
     assert [g["state_bits"] for g in o.param_groups] == [32, 8]
     with pytest.raises(TypeError):
         o.add_param_group([b])
+
+
+@pytest.mark.parametrize("change,status", DESC_REFUSALS)
+def test_workspaces_of_what_is_refused(lib, change, status):
+    """A call that is refused needs none; only a bad q_len alone is a good decode call without it."""
+    one = basp.basp_attention_decode_workspace(desc(**{"window": 0, "k_len": 100000, **change, "q_len": 1}))
+    assert (one > 0) == (set(change) == {"q_len"})
+    if "q_len" in change:
+        assert basp.basp_attention_decode_workspace(desc(**change)) == 0
+    assert basp.basp_attention_backward_workspace(desc(**change)) == 0
