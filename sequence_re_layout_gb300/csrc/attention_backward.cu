@@ -877,7 +877,7 @@ KeySplit key_split(const AttentionArgs &a) {
         return int64_t(q.high - q.low) * a.group;
     };
     for (int64_t t = 0; t < tiles; ++t) sum += pairs(t);
-    const int64_t chunk = std::max<int64_t>(16, ceil_div(sum * heads, 152 * 4));
+    const int64_t chunk = std::max<int64_t>(16, ceil_div(sum * heads, kSms * 4));
     if (chunk > (1 << 30)) return s;
     s.chunk = int(chunk);
     for (int64_t t = 0; t < tiles && s.tiles < kMostSplit; ++t) {

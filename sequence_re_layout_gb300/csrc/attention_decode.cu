@@ -321,7 +321,7 @@ DecodeArgs plan(const AttentionArgs &a) {
     p.row_blocks = int(ceil_div(a.group, kRows));
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a.sk, int64_t(a.window) + a.sinks));   // that a token can see
     const int64_t heads = std::max<int64_t>(1, int64_t(a.batch) * a.hkv * p.row_blocks);
-    const int64_t ctas = 152 * (a.d <= 64 ? DecodeSizes<64>::kCtas : DecodeSizes<128>::kCtas) * (a.batch == 1 ? 1 : 4);
+    const int64_t ctas = int64_t(kSms) * (a.d <= 64 ? DecodeSizes<64>::kCtas : DecodeSizes<128>::kCtas) * (a.batch == 1 ? 1 : 4);
     const int64_t turn = kWarps * kKeys;
     int64_t chunk = ceil_div(ceil_div(most, std::max<int64_t>(1, ctas / heads)), turn) * turn;
     chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), 1024);

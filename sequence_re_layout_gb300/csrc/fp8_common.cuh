@@ -304,6 +304,9 @@ struct NvtxRange {
     ~NvtxRange() { nvtxRangePop(); }
 };
 
+// SMs of a GB300, for sizes that a host without one has to know too (workspaces).
+constexpr int kSms = 152;
+
 // SMs of the current device (152 on GB300); 1 if it cannot be read.
 int sm_count();
 

@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(1024) layer_column_sum_kernel(const float *par
 // there are rows, or than the workspace has room for.  Narrow rows have small CTAs, which
 // are more: 60000 x 512 bf16 took 104 us with four an SM.
 int64_t back_parts(int64_t rows, int64_t cols) {
-    return std::min<int64_t>(rows, 152 * std::min<int64_t>(16, std::max<int64_t>(4, 8192 / cols)));
+    return std::min<int64_t>(rows, kSms * std::min<int64_t>(16, std::max<int64_t>(4, 8192 / cols)));
 }
 
 template <class T, class W, bool VEC>

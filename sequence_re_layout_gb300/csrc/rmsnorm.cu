@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int
 // CTAs of the backward kernel: enough to fill the GPU four times over with
 // rows of ordinary length, never more than there are rows.
 constexpr int kBackCtasPerSm = 4;
-constexpr int kBackMaxParts = 152 * kBackCtasPerSm;
+constexpr int kBackMaxParts = kSms * kBackCtasPerSm;
 
 int64_t back_parts(int64_t rows) { return std::min<int64_t>(rows, kBackMaxParts); }
 
