@@ -610,3 +610,30 @@ def test_one_overflow_costs_little(dtype):
     bad, (dq, dk, dv) = best()
     assert bool(torch.isfinite(dq[0, :S - 1]).all()) and not bool(torch.isfinite(dk).any()) and not bool(torch.isfinite(dv[..., 3]).any())
     assert bad <= 40 * plain
+
+
+@pytest.mark.parametrize("S,Hq,Hkv,d,window,sinks", [(700, 4, 2, 128, 300, 4), (2500, 2, 1, 64, 100, 300), (130, 6, 2, 96, None, 0)])
+def test_results_repeat_in_fp16(S, Hq, Hkv, d, window, sinks):
+    """Units and bounds are made anew by each call, in a graph and on another stream too, whatever
+    its workspace held before."""
+    x = tensors(2, S, S, Hq, Hkv, d, torch.float16)
+    y = [t * 2.0 ** -8 for t in x]
+    o, lse = attention.forward(*x[:3], window, sinks)
+    want = attention.backward(x[3], *x[:3], o, lse, window, sinks)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = attention.backward(x[3], *x[:3], o, lse, window, sinks)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        attention.backward(y[3] * 2.0 ** -9, *x[:3], o, lse, window, sinks)          # another unit, the same memory
+        for g in got:
+            g.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            beside = attention.backward(x[3], *x[:3], o, lse, window, sinks)
+        again = attention.backward(x[3], *x[:3], o, lse, window, sinks)
+        torch.cuda.synchronize()
+        for grads in (got, beside, again):
+            assert all(torch.equal(a, b) for a, b in zip(grads, want))
