@@ -637,3 +637,88 @@ def test_results_repeat_in_fp16(S, Hq, Hkv, d, window, sinks):
         torch.cuda.synchronize()
         for grads in (got, beside, again):
             assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+def is_shared(Sq, Sk, Hq, Hkv, d, window, sinks, dtype, batch=1):
+    """Whether CTAs share a tile of keys: then the workspace holds their parts' sums beside the
+    rows' statistics (40 bytes a query of whole tiles) and fp16's units (less than 5, and a number a tile of keys)."""
+    desc = basp.basp_attention_desc(batch, Sq, Sk, Hq, Hkv, d, window or 0, sinks, d ** -0.5, basp.DTYPE_CODES[dtype])
+    rows, tiles = batch * Hq * (-(-Sq // 128) * 128), batch * Hkv * -(-Sk // 128)
+    own = rows * 40 + ((rows * 4 + rows // 32 * 16 + -(-tiles // 4) * 16) if dtype == "fp16" else 0)
+    got = basp.basp_attention_backward_workspace(desc)
+    assert got >= own
+    return got > own
+
+
+SHARED = [(2300, 2300, 4, 1, 64, 100, 3), (2300, 2300, 5, 1, 128, None, 0), (2000, 2501, 10, 2, 40, 300, 200),
+          (1500, 2001, 8, 1, 72, 64, 700), (20000, 20000, 1, 1, 64, 50, 2)]
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("Sq,Sk,Hq,Hkv,d,window,sinks", SHARED[:4])
+def test_shared_key_tiles(Sq, Sk, Hq, Hkv, d, window, sinks, dtype):
+    t = DTYPES[dtype]
+    assert is_shared(Sq, Sk, Hq, Hkv, d, window, sinks, dtype)
+    q, k, v, do = tensors(1, Sq, Sk, Hq, Hkv, d, t)
+    o, lse, g = check(q, k, v, do, window, sinks)
+    assert all(torch.equal(a, b) for a, b in zip(g, attention.backward(do, q, k, v, o, lse, window, sinks)))
+    bad = do.clone()
+    bad[0, Sq // 2, 0, 3] = float("nan")
+    r = Attention(*(f64(x)[0] for x in (q, k, v)), window, sinks, d ** -0.5, u(t))
+    want, bound = r.backward(f64(do)[0], r.o_bound)
+    rows = ~r.sees[Sq // 2]
+    got = attention.backward(bad, q, k, v, o, lse, window, sinks)
+    for name, x in zip(("dk", "dv"), got[1:]):
+        close(x[0][torch.from_numpy(rows).cuda()], want[name][rows], bound[name][rows])
+    assert bool(torch.isnan(got[1][0, :, 0][torch.from_numpy(~rows).cuda()]).all())        # the first query head's key head
+    assert bool(torch.isfinite(got[1][0, :, 1:]).all())
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_shared_key_tiles_of_a_long_sequence(dtype):
+    """One head: its first keys' dk and dv in 64 bits, from the lse and o that the backward gets."""
+    Sq, Sk, Hq, Hkv, d, window, sinks = SHARED[4]
+    assert is_shared(Sq, Sk, Hq, Hkv, d, window, sinks, dtype)
+    t = DTYPES[dtype]
+    q, k, v, do = tensors(1, Sq, Sk, Hq, Hkv, d, t)
+    o, lse = attention.forward(q, k, v, window, sinks)
+    dq, dk, dv = attention.backward(do, q, k, v, o, lse, window, sinks)
+    n, s = 4, d ** -0.5
+    qd, kd, vd, dod = (x[0, :, 0].double() for x in (q, k, v, do))
+    first = kd[:n]
+    p = torch.exp(s * qd @ first.T - lse[0, 0].double()[:, None])
+    i, j = torch.arange(Sq, device="cuda")[:, None], torch.arange(n, device="cuda")
+    p = p * ((j <= i) & ((j > i - window) | (j < sinks)))
+    ds = p * (dod @ vd[:n].T - (dod * o[0, :, 0].double()).sum(1, keepdim=True))
+    for got, want, size in ((dv, p.T @ dod, p.T @ dod.abs()), (dk, s * ds.T @ qd, s * ds.abs().T @ qd.abs())):
+        room = 4 * u(t) * size + u(t) * want.abs() + 2.0 ** -24
+        assert bool(((got[0, :n, 0].double() - want).abs() <= room).all())
+    assert bool(torch.isfinite(dq).all())
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_past_fp16_in_shared_tiles(d, size):
+    """As test_past_fp16: the parts of a shared tile say it to the kernel that adds them."""
+    t, S, Hq, window, sinks = torch.float16, 1300, 8, 3, 4
+    assert is_shared(S, S, Hq, 1, d, window, sinks, "fp16")
+    q, k, v, do = tensors(1, S, S, Hq, 1, d, t)
+    v = (v[..., :1].float().sign() * 60000).to(t).expand(1, S, 1, d).contiguous()
+    q, k, do = q * 2.0 ** -14, k * 2.0 ** -14, torch.full_like(do, size)
+    o, lse = attention.forward(q, k, v, window, sinks)
+    got = attention.backward(do, q, k, v, o, lse, window, sinks)
+    r = Attention(f64(q[0]), f64(k[0]), f64(v[0]), window, sinks, d ** -0.5, u(t))
+    want, bound = r.backward(f64(do)[0], r.o_bound)
+    for name, g in zip(("dq", "dk", "dv"), got):
+        close(g[0], want[name], bound[name])
+
+
+@pytest.mark.parametrize("kind", ["smaller", "rows", "tiles"])
+def test_small_gradients_in_shared_tiles(kind):
+    """Each part of a shared tile has a unit of its own."""
+    assert is_shared(1500, 1500, 6, 1, 64, None, 0, "fp16")
+    test_small_gradients_in_fp16(1500, 6, 1, None, 0, kind, 64)
+
+
+def test_zzz_no_wait_ran_out_either():
+    assert basp.basp_attention_timeouts() == 0
